@@ -309,7 +309,10 @@ def _prepare_logprobs(c, seed):
     # a few likely tokens per row; the last columns are padding of the vocabulary and banned
     x.scatter_add_(1, torch.randint(0, v, (n, 12), generator=g, device=DEV), torch.rand((n, 12), generator=g, device=DEV) * 12)
     x[:, v - 7:] = -math.inf
-    return dict(logits=x.to(BF) if c["bf16"] else x, top=c["top"], temp=c["temp"],
+    outs = tuple(torch.empty(shape, dtype=dtype, device=DEV) for shape, dtype in (
+        ((n, c["cands"]), torch.float32), ((n,), torch.float32), ((n,), torch.float32), ((n, c["top"]), torch.int32),
+        ((n, c["top"]), torch.float32)))
+    return dict(logits=x.to(BF) if c["bf16"] else x, top=c["top"], temp=c["temp"], outs=outs,
                 tokens=torch.randint(0, v - 7, (n, c["cands"]), generator=g, device=DEV).int())
 
 
@@ -489,7 +492,7 @@ def _own(s):
     if op == "compact":
         table, refs = tb.cache_compact(s["cache"], s["table"], s["refs"], s["workspace"], s["out_table"], s["out_refs"])
         return table, refs, _as_ints(s["pool"])
-    return tuple(tb.token_logprobs(s["logits"], s["tokens"], s["top"], s["workspace"], s["temp"]))
+    return tuple(tb.token_logprobs(s["logits"], s["tokens"], s["top"], s["workspace"], s["temp"], s["outs"]))
 
 
 def run(state):
