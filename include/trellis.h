@@ -74,10 +74,11 @@ enum trellis_status {
   TRELLIS_EWORKSPACE = -5, /* workspace missing, misaligned or too small */
   TRELLIS_ECUDA = -6,      /* CUDA reported an error at launch */
   TRELLIS_ENULL = -7,      /* a required pointer is NULL */
-  TRELLIS_EDEVICE = -8     /* no usable sm_103 device is current */
+  TRELLIS_EDEVICE = -8,    /* no usable sm_103 device is current */
+  TRELLIS_ESHAPE = -9      /* unsupported or inconsistent sizes, strides or types of a serving call */
 };
 
-/* Version of this interface (major*100 + minor): 101. */
+/* Version of this interface (major*100 + minor): 102. */
 int trellis_abi_version(void);
 
 /* Static description of a status code; never NULL. */
@@ -276,6 +277,223 @@ int trellis_gemm_prefill(const uint32_t *codes, const uint16_t *scales, const ui
                          uint16_t *out, int M, const trellis_geom_t *g, trellis_stream_t stream);
 
 /*
+ * ---- The rest of a decoding step --------------------------------------------
+ *
+ * A step of a served model runs the packed projections over a few tokens: one
+ * per sequence, or a drafted tree of tokens per sequence (speculative
+ * decoding).  The calls below are what such a step needs between and after
+ * its projections.  The pages have no counterpart (their attention and their
+ * sampling are outside the linear layers); these are additions of this
+ * library.  They follow the conventions above (device pointers, 16-byte
+ * aligned unless a call says otherwise; asynchronous on `stream`; nothing
+ * allocated; the same status codes), except that arrays with a stride
+ * argument need not be dense.  A count of zero (n, batch, pairs) is not an
+ * error: the call does nothing.
+ */
+
+enum trellis_dtype { TRELLIS_BF16 = 0, TRELLIS_E4M3 = 1, TRELLIS_F32 = 2 };
+
+/*
+ * A paged key/value cache of all layers:
+ *   pool   [layers][pages][2][heads][page_size][head_dim], keys at index 0 of
+ *          the third axis and values at index 1; bf16, or e4m3 (8 bits: 4 of
+ *          exponent, 3 of mantissa, no infinities, largest value 448)
+ *   scales [layers][2][heads] fp32 for e4m3 (NULL: all 1); must be NULL for
+ *          bf16.  A stored e4m3 number stands for itself times its scale.
+ * A sequence holds the pages of one row of a page table: position p of a
+ * sequence is row p % page_size of page table[p / page_size].
+ */
+typedef struct trellis_cache {
+  void *pool;
+  const float *scales;
+  int64_t pages;     /* pages per layer, 1 .. 2^24 */
+  int32_t layers;    /* 1 .. 65535 */
+  int32_t heads;     /* key/value heads, 1 .. 1024 */
+  int32_t page_size; /* 16, 32, 64 or 128 */
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int32_t dtype;     /* TRELLIS_BF16 or TRELLIS_E4M3 */
+  int32_t reserved;  /* must be 0 */
+} trellis_cache_t;
+
+/* 0 if the calls below support the cache, else a negative status.  Pure host check. */
+int trellis_check_cache(const trellis_cache_t *cache);
+
+/* What trellis_qk_norm_rope_append needs of a layer besides the tokens. */
+typedef struct trellis_norm_rope {
+  const uint16_t *q_weight; /* [head_dim] bf16 */
+  const uint16_t *k_weight; /* [head_dim] bf16 */
+  const float *rope;        /* [max_pos][rotary_dim] fp32: rotary_dim/2 cosines, then as many sines; NULL if rotary_dim is 0 */
+  int64_t max_pos;
+  int32_t q_heads, kv_heads, head_dim;
+  int32_t rotary_dim;       /* 0 .. head_dim, a multiple of 16: the leading dims that are rotated */
+  int32_t interleaved;      /* 0: dim i is paired with i + rotary_dim/2;  1: dim 2i with 2i + 1 */
+  int32_t reserved;         /* must be 0 */
+  float eps;
+  float weight_offset;      /* added to every weight (0, or 1 for weights stored around zero) */
+} trellis_norm_rope_t;
+
+/*
+ * trellis_qk_norm_rope_append -- the norms of queries and keys for each head,
+ * the rotation by position, and the write of keys and values into the cache,
+ * in one launch.  For each token and head, in fp32 with one rounding at the end:
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *   (a, b) of each pair of the first rotary_dim dims -> (a c - b s, b c + a s),
+ *   c and s from row positions[token] of `rope`
+ * q_out gets the queries as bf16.  Keys, and the values as they are, go to
+ * row slots[token] % page_size of page slots[token] / page_size of `layer`:
+ * as bf16, or as e4m3 of the number divided by its scale, clamped to +-448
+ * (nearest, ties to even; NaN stays NaN).
+ *   q [n][q_heads][head_dim]   k, v [n][kv_heads][head_dim] bf16; the strides
+ *   are those from token to token, in elements, multiples of 8.  q_out may be
+ *   q (with the same stride).
+ *   positions [n] int32: a token whose position is outside [0, max_pos) gets
+ *   NaN queries and keys.
+ *   slots [n] int64: a token whose slot is outside the pool (a negative one
+ *   for padding) writes no keys and values.  The others must be distinct.
+ * n <= 2^20.  cache->heads and head_dim must be those of p.
+ */
+int trellis_qk_norm_rope_append(const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                                const uint16_t *v, int64_t v_stride, const int32_t *positions, const int64_t *slots,
+                                uint16_t *q_out, int64_t q_out_stride, int n, const trellis_norm_rope_t *p,
+                                const trellis_cache_t *cache, int layer, trellis_stream_t stream);
+
+/* One step's sequences and drafted tokens, as trellis_tree_attention takes them. */
+typedef struct trellis_drafts {
+  const int32_t *table;   /* [batch][width] page table */
+  const int32_t *prefix;  /* [batch] positions before the drafts */
+  const int32_t *q_start; /* [batch + 1] sequence b's drafts are tokens q_start[b] .. q_start[b+1]-1 */
+  const uint64_t *mask;   /* [n]: bit j set: the token sees draft j of its sequence.  NULL: drafts 0 .. itself */
+  int32_t batch;          /* 1 .. 1024 */
+  int32_t width;          /* pages per row of the table */
+  int32_t n;              /* tokens of all sequences */
+  int32_t max_tokens;     /* most drafts of a sequence, 1 .. 64 */
+} trellis_drafts_t;
+
+/*
+ * trellis_tree_attention -- attention of each sequence's drafted tokens over
+ * its cached prefix and over the drafts that its mask names.  Draft j of
+ * sequence b is at position prefix[b] + j of the cache (written there before,
+ * by trellis_qk_norm_rope_append); a plain decode step has one draft per
+ * sequence.  For token i of sequence b and query head h, over the positions p
+ * it sees, with the key/value head h / (q_heads / heads):
+ *   out = sum_p softmax_p(scale * q.k_p) v_p      lse = log sum_p exp(scale * q.k_p)
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to 16 bits (bf16, or fp16 with an e4m3 cache) for the products with
+ * the values; one rounding to bf16 at the end.  A token that sees nothing (or
+ * only scores of minus infinity) gets zeros and an lse of minus infinity.
+ * What a token does not see (masked drafts, rows past a sequence's end) does
+ * not reach its result, whatever its bits are.
+ *   q, out [n][q_heads][head_dim] bf16, strides from token to token in
+ *   elements, multiples of 8;  lse [n][q_heads] fp32 or NULL
+ *   workspace: as for trellis_matvec_axis0, of at least
+ *   trellis_tree_workspace_bytes bytes.
+ * q_heads must be a multiple of cache->heads.  Lengths are device data and
+ * clamped: prefix to the table's width, drafts to max_tokens and n, table
+ * entries to the pool (entries that a length does not reach are not read).
+ * Tokens outside every sequence's range are left unwritten.
+ */
+int trellis_tree_attention(const uint16_t *q, int64_t q_stride, const trellis_cache_t *cache, int layer,
+                           const trellis_drafts_t *d, int q_heads, float scale, uint16_t *out, int64_t out_stride,
+                           float *lse, void *workspace, size_t workspace_bytes, trellis_stream_t stream);
+
+/* Bytes of workspace trellis_tree_attention needs for (cache, batch,
+ * max_tokens, q_heads) on the current device; 0 if they are unsupported. */
+size_t trellis_tree_workspace_bytes(const trellis_cache_t *cache, int batch, int max_tokens, int q_heads);
+
+/*
+ * trellis_cache_copy -- copies pages src[i] to dst[i] in every layer.
+ *   src, dst [n] int32; a pair with an index outside the pool is skipped.  No
+ *   page may be both a source and a destination, or a destination twice.
+ */
+int trellis_cache_copy(const trellis_cache_t *cache, const int32_t *src, const int32_t *dst, int n,
+                       trellis_stream_t stream);
+
+/*
+ * trellis_cache_fork -- forks, grows and frees rows of a page table, with the
+ * copy of the pages that cannot be shared.  Row r holds the leading entries
+ * >= 0 of table[r]; refs[p] counts the entries of all rows that hold page p
+ * (0: free).  Per pair i:
+ *   parent[i] = r, child[i] = c != r: c gives up what it held and becomes a
+ *     copy of r of the same length.  The pages that r's length fills are
+ *     shared; the partly filled one is copied, in every layer.  Fresh pages
+ *     are added until c has room for lens[r] + room positions.
+ *   parent[i] = child[i] = c: c gets fresh pages until it has that room.
+ *   parent[i] = -1: c gives up its pages (lens 0).
+ * All pairs act at once: parents are read as they were before the call, and
+ * the k-th page handed out, in the order of the pairs, is the k-th lowest page
+ * that was free before the call.
+ *   status [pairs] int32: 0 done; 1 no room (not enough free pages, or more
+ *   pages than the row's width: c is left empty, or as it was if it is its own
+ *   parent); 2 a row, length or page out of range (nothing done).
+ *   table [rows][width], lens [rows], refs [pages] int32, updated in place
+ *   workspace: at least trellis_cache_workspace_bytes bytes, no initial state.
+ * pairs <= 1024; no row may be a child twice.
+ */
+int trellis_cache_fork(const trellis_cache_t *cache, int32_t *table, int32_t *lens, int32_t *refs,
+                       const int32_t *parent, const int32_t *child, int32_t *status, int pairs, int rows, int width,
+                       int room, void *workspace, size_t workspace_bytes, trellis_stream_t stream);
+
+/*
+ * trellis_cache_compact -- moves the live pages (refs > 0) to the front of the
+ * pool, in every layer: with n of them, the k-th live page at an index >= n
+ * moves to the k-th free index < n.  The table's entries and refs follow
+ * (entries outside the pool stay as they are; refs past n become 0).
+ *   table [rows][width], refs [pages]; out_table, out_refs may be the same
+ *   arrays.  workspace: as for trellis_cache_fork.
+ */
+int trellis_cache_compact(const trellis_cache_t *cache, const int32_t *table, const int32_t *refs, int32_t *out_table,
+                          int32_t *out_refs, int rows, int width, void *workspace, size_t workspace_bytes,
+                          trellis_stream_t stream);
+
+/* Bytes of workspace of trellis_cache_fork and trellis_cache_compact; 0 if unsupported. */
+size_t trellis_cache_workspace_bytes(const trellis_cache_t *cache, int pairs, int width);
+
+/*
+ * trellis_cache_commit -- keeps the accepted drafts of each sequence: for
+ * i < accepted[b], position prefix[b] + path[b][i] moves to prefix[b] + i, in
+ * every layer, and lens[b] = prefix[b] + accepted[b].
+ *   table [batch][width], prefix, accepted, lens [batch], path [batch][max_tokens] int32
+ *   path[b] lists the accepted drafts in ascending order, so path[b][i] >= i;
+ *   an entry that does not, or whose pages are out of range, is skipped.
+ *   accepted is clamped to [0, max_tokens].  lens may be prefix.
+ * max_tokens <= 64.
+ */
+int trellis_cache_commit(const trellis_cache_t *cache, const int32_t *table, const int32_t *prefix,
+                         const int32_t *path, const int32_t *accepted, int32_t *lens, int batch, int width,
+                         int max_tokens, trellis_stream_t stream);
+
+/*
+ * trellis_token_logprobs -- log probabilities of given tokens, with the
+ * entropy and the most likely alternatives of each row, in one pass over the
+ * logits.  With z = logits / temperature, in fp32:
+ *   lse = log sum_j exp(z_j)        logprobs[r][c] = z[tokens[r][c]] - lse
+ *   entropy = lse - sum_j p_j z_j   (p = softmax of z)
+ *   top_ids[r][0..top_k), top_logprobs: the columns in descending order of
+ *   the logit, equal ones in ascending order of the index
+ * A token outside [0, vocab) has log probability minus infinity.  Logits of
+ * minus infinity are tokens of probability zero; a row of nothing else has
+ * lse = minus infinity, entropy 0 and only log probabilities of minus
+ * infinity.  NaN, or plus infinity, makes the row's numbers NaN (NaN orders
+ * before every number).
+ *   logits [n] rows of vocab bf16 or fp32 (dtype), row_stride elements apart
+ *   (any stride >= vocab; the base 16-byte aligned)
+ *   tokens [n][cands] int32 (NULL if cands is 0)
+ *   logprobs [n][cands], lse [n], entropy [n], top_logprobs [n][top_k] fp32,
+ *   top_ids [n][top_k] int32
+ *   workspace: as for trellis_matvec_axis0, of at least
+ *   trellis_logprobs_workspace_bytes bytes.
+ * 1 <= vocab <= 2^24, 0 <= cands <= 64, 0 <= top_k <= min(32, vocab),
+ * temperature > 0, n <= 2^20.
+ */
+int trellis_token_logprobs(const void *logits, int dtype, int64_t row_stride, const int32_t *tokens, int n, int vocab,
+                           int cands, int top_k, float temperature, float *logprobs, float *lse, float *entropy,
+                           int32_t *top_ids, float *top_logprobs, void *workspace, size_t workspace_bytes,
+                           trellis_stream_t stream);
+
+/* Bytes of workspace trellis_token_logprobs needs; 0 if the sizes are unsupported. */
+size_t trellis_logprobs_workspace_bytes(int n, int vocab, int top_k);
+
+/*
  * trellis_load_floor -- measurement aid with no counterpart in the pages'
  * operations: reads an axis-1 bitstream with exactly the access pattern of
  * trellis_matvec_axis1 at M = 1 (one lane per stored row, 16-byte loads of
@@ -324,8 +542,8 @@ int trellis_load_floor_rows(const uint32_t *codes, uint32_t *out, const trellis_
 int trellis_prefill_plan(int M, const trellis_geom_t *g, int sms, int *tokens_per_tile, int *launches);
 
 /*
- * trellis_device_error -- diagnostic of the tensor-core kernel.  Every wait on
- * an mbarrier inside trellis_gemm_prefill is bounded (2 s); a wait that gives
+ * trellis_device_error -- diagnostic of the kernels that wait on mbarriers.  Every
+ * such wait inside trellis_gemm_prefill and trellis_tree_attention is bounded (2 s); a wait that gives
  * up records a non-zero code in a device word instead of hanging the GPU.
  * Returns that code (0 = none), reading it synchronously from the current
  * device; reset != 0 clears it.  Negative values are trellis_status errors.
@@ -334,8 +552,8 @@ int trellis_device_error(int reset);
 
 /*
  * trellis_set_wait_limit -- diagnostic with no counterpart in the pages:
- * sets the limit of each bounded wait in the tensor-core kernel
- * (trellis_gemm_prefill) for launches issued after the call, in
+ * sets the limit of each bounded wait in the tensor-core kernels
+ * (trellis_gemm_prefill, trellis_tree_attention) for launches issued after the call, in
  * nanoseconds of the GPU's global timer; 0 restores the default (2 s).
  * It exists so that tests can make the waits run out on an ordinary
  * problem and check the error path: the kernel then records a non-zero

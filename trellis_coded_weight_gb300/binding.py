@@ -16,6 +16,7 @@ import ctypes
 import os
 import threading
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -24,13 +25,17 @@ LIB_PATH = os.path.join(_PKG, "libtrellis.so")
 
 TRELLIS_OK = 0
 STATUS_NAMES = {0: "TRELLIS_OK", -1: "TRELLIS_EGEOM", -2: "TRELLIS_EM", -3: "TRELLIS_EALIGN", -4: "TRELLIS_EAXIS",
-                -5: "TRELLIS_EWORKSPACE", -6: "TRELLIS_ECUDA", -7: "TRELLIS_ENULL", -8: "TRELLIS_EDEVICE"}
+                -5: "TRELLIS_EWORKSPACE", -6: "TRELLIS_ECUDA", -7: "TRELLIS_ENULL", -8: "TRELLIS_EDEVICE",
+                -9: "TRELLIS_ESHAPE"}
 
 EXPORTS = ("trellis_abi_version", "trellis_status_string", "trellis_check_geom", "trellis_expand_bf16",
            "trellis_matvec_axis1", "trellis_matvec_axis0", "trellis_workspace_bytes", "trellis_gateup_swiglu",
            "trellis_gemm_prefill", "trellis_device_error", "trellis_mlp_decode", "trellis_matvec_axis1_bf16w",
            "trellis_matvec_axis0_bf16w", "trellis_load_floor", "trellis_load_floor_rows", "trellis_prefill_plan",
-           "trellis_set_wait_limit", "trellis_matvec_axis1_host")
+           "trellis_set_wait_limit", "trellis_matvec_axis1_host", "trellis_check_cache", "trellis_qk_norm_rope_append",
+           "trellis_tree_attention", "trellis_tree_workspace_bytes", "trellis_cache_copy", "trellis_cache_fork",
+           "trellis_cache_compact", "trellis_cache_workspace_bytes", "trellis_cache_commit", "trellis_token_logprobs",
+           "trellis_logprobs_workspace_bytes")
 
 
 class TrellisGeom(ctypes.Structure):
@@ -372,3 +377,365 @@ class MlpDecodeGraph:
     def replay(self):
         self.graph.replay()
         return self.out
+
+
+# ---- The rest of a decoding step: paged cache, norms with rotation, tree attention, token log probabilities ----
+
+TRELLIS_BF16, TRELLIS_E4M3, TRELLIS_F32 = 0, 1, 2
+
+
+class TrellisCache(ctypes.Structure):
+    """Mirror of trellis_cache_t."""
+    _fields_ = [("pool", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("layers", ctypes.c_int32), ("heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class TrellisNormRope(ctypes.Structure):
+    """Mirror of trellis_norm_rope_t."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class TrellisDrafts(ctypes.Structure):
+    """Mirror of trellis_drafts_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("batch", ctypes.c_int32), ("width", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32)]
+
+
+def _raw_stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _req_tokens(t: torch.Tensor, name: str, n: int, heads: int, dim: int):
+    """A bf16 [n, heads, dim] tensor whose tokens may be apart (a slice of a wider projection): pointer, stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, dim)}")
+    stride, per_head, one = t.stride()
+    if (one != 1 and dim > 1) or (per_head != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), stride
+
+
+def _req_rows(t: torch.Tensor, name: str, dtype, shape):
+    """As _req for one dtype."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _req_workspace(t: torch.Tensor):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+_serving = None
+
+
+def _serving_lib():
+    """The library with the argument types of the serving calls set (once)."""
+    global _serving
+    if _serving is None:
+        lib = load()
+        vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+        cache = ctypes.POINTER(TrellisCache)
+        for name, res, args in (
+                ("trellis_check_cache", i32, [cache]),
+                ("trellis_qk_norm_rope_append", i32, [vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32,
+                                                      ctypes.POINTER(TrellisNormRope), cache, i32, vp]),
+                ("trellis_tree_attention", i32, [vp, i64, cache, i32, ctypes.POINTER(TrellisDrafts), i32, f32, vp, i64,
+                                                 vp, vp, sz, vp]),
+                ("trellis_tree_workspace_bytes", sz, [cache, i32, i32, i32]),
+                ("trellis_cache_copy", i32, [cache, vp, vp, i32, vp]),
+                ("trellis_cache_fork", i32, [cache, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
+                ("trellis_cache_compact", i32, [cache, vp, vp, vp, vp, i32, i32, vp, sz, vp]),
+                ("trellis_cache_workspace_bytes", sz, [cache, i32, i32]),
+                ("trellis_cache_commit", i32, [cache, vp, vp, vp, vp, vp, i32, i32, i32, vp]),
+                ("trellis_token_logprobs", i32, [vp, i32, i64, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, sz,
+                                                 vp]),
+                ("trellis_logprobs_workspace_bytes", sz, [i32, i32, i32])):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = res, args
+        _serving = lib
+    return _serving
+
+
+class PagedCache:
+    """A paged key/value cache of all layers: pool [layers, pages, 2, heads, page_size, head_dim], bf16 or e4m3
+    (torch.float8_e4m3fn, with scales [layers, 2, heads] fp32 or None for ones).  Keeps the tensors it describes."""
+
+    def __init__(self, pool: torch.Tensor, scales: torch.Tensor = None):
+        if not isinstance(pool, torch.Tensor) or not pool.is_cuda:
+            raise ValueError("pool must be a CUDA tensor")
+        if pool.dim() != 6 or pool.shape[2] != 2:
+            raise ValueError(f"pool has shape {tuple(pool.shape)}, expected [layers, pages, 2, heads, page_size, head_dim]")
+        if pool.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError(f"pool has dtype {pool.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
+        if not pool.is_contiguous():
+            raise ValueError("pool must be contiguous")
+        self.pool, self.scales, self.device = pool, scales, pool.device
+        self.layers, self.pages, _, self.heads, self.page_size, self.head_dim = pool.shape
+        if scales is not None:
+            if pool.dtype != torch.float8_e4m3fn:
+                raise ValueError("scales belong to an e4m3 pool")
+            _req_rows(scales, "scales", torch.float32, (self.layers, 2, self.heads))
+            _same_device(self.device, scales=scales)
+        self._c = TrellisCache(pool.data_ptr(), scales.data_ptr() if scales is not None else None, self.pages, self.layers,
+                               self.heads, self.page_size, self.head_dim,
+                               TRELLIS_E4M3 if pool.dtype == torch.float8_e4m3fn else TRELLIS_BF16, 0)
+        self._ref = ctypes.byref(self._c)
+        _check("trellis_check_cache", _serving_lib().trellis_check_cache(self._ref))
+
+    @classmethod
+    def new(cls, layers, pages, heads, page_size, head_dim, device, dtype=torch.bfloat16, scales=None):
+        """A cache over a fresh (zeroed) pool."""
+        return cls(torch.zeros((layers, pages, 2, heads, page_size, head_dim), dtype=dtype, device=device), scales)
+
+
+class NormRope:
+    """The weights, rotation table and constants of a layer's query/key norms (trellis_norm_rope_t).
+
+    rope [max_pos, rotary_dim] fp32: rotary_dim/2 cosines, then as many sines, per position; None: no rotation.
+    interleaved pairs dim 2i with 2i + 1, else i with i + rotary_dim/2."""
+
+    def __init__(self, q_weight, k_weight, rope, q_heads: int, kv_heads: int, interleaved: bool = False, eps: float = 1e-6,
+                 weight_offset: float = 0.0):
+        dim = q_weight.shape[-1]
+        _req_rows(q_weight, "q_weight", torch.bfloat16, (dim,))
+        _req_rows(k_weight, "k_weight", torch.bfloat16, (dim,))
+        _same_device(q_weight.device, k_weight=k_weight)
+        if rope is not None:
+            _req_rows(rope, "rope", torch.float32, (rope.shape[0], rope.shape[-1]))
+            _same_device(q_weight.device, rope=rope)
+        self.q_heads, self.kv_heads, self.head_dim, self.device = q_heads, kv_heads, dim, q_weight.device
+        self._kept = (q_weight, k_weight, rope)
+        # without rotation there is no table, and any position is in range
+        self._c = TrellisNormRope(q_weight.data_ptr(), k_weight.data_ptr(), rope.data_ptr() if rope is not None else None,
+                                  rope.shape[0] if rope is not None else 1 << 31, q_heads, kv_heads, dim,
+                                  rope.shape[1] if rope is not None else 0, int(interleaved), 0, eps, weight_offset)
+        self._ref = ctypes.byref(self._c)
+
+
+def qk_norm_rope_append(q, k, v, positions, slots, norm: NormRope, cache: PagedCache, layer: int, out=None):
+    """Per-head norms of q [n, q_heads, dim] and k [n, kv_heads, dim], the rotation by positions [n] int32, and the
+    write of k and v to slots [n] int64 (page * page_size + row; negative: none) of the cache's layer, in one launch.
+    q, k and v may be slices of one projection.  Returns the queries (out may be q)."""
+    n, dev = q.shape[0], cache.device
+    qp, qs = _req_tokens(q, "q", n, norm.q_heads, norm.head_dim)
+    kp, ks = _req_tokens(k, "k", n, norm.kv_heads, norm.head_dim)
+    vp, vs = _req_tokens(v, "v", n, norm.kv_heads, norm.head_dim)
+    if out is None:
+        out = torch.empty((n, norm.q_heads, norm.head_dim), dtype=torch.bfloat16, device=dev)
+    op, os_ = _req_tokens(out, "out", n, norm.q_heads, norm.head_dim)
+    pp = _req_rows(positions, "positions", torch.int32, (n,))
+    sp = _req_rows(slots, "slots", torch.int64, (n,))
+    if not (q.device == k.device == v.device == out.device == positions.device == slots.device == norm.device == dev):
+        raise ValueError(f"q, k, v, out, positions, slots and norm must be on the cache's device {dev}")
+    with _on(q):
+        st = _serving_lib().trellis_qk_norm_rope_append(qp, qs, kp, ks, vp, vs, pp, sp, op, os_, n, norm._ref, cache._ref,
+                                                        layer, _raw_stream(dev))
+    if st:
+        _check("trellis_qk_norm_rope_append", st)
+    return out
+
+
+class DraftBatch:
+    """One step's sequences and drafted tokens (trellis_drafts_t), shared by the step's layers.
+
+    table [batch, width] int32 pages;  prefix [batch] int32 positions before the drafts;  q_start [batch + 1] int32
+    (sequence b's drafts are tokens q_start[b] .. q_start[b+1] - 1);  max_tokens: most drafts of a sequence (<= 64);
+    mask [n] int64: bit j set where the token sees draft j of its sequence (None: drafts 0 .. itself, then n is
+    needed).  Keeps the tensors; their contents are read by each call."""
+
+    def __init__(self, table, prefix, q_start, max_tokens: int, mask=None, n: int = None):
+        batch, width = table.shape
+        if mask is not None:
+            n = mask.shape[0] if n is None else n
+            _req_rows(mask, "mask", torch.int64, (n,))
+        elif n is None:
+            raise ValueError("n is needed without a mask")
+        _req_rows(table, "table", torch.int32, (batch, width))
+        _req_rows(prefix, "prefix", torch.int32, (batch,))
+        _req_rows(q_start, "q_start", torch.int32, (batch + 1,))
+        _same_device(table.device, prefix=prefix, q_start=q_start, **({} if mask is None else {"mask": mask}))
+        self.table, self.prefix, self.q_start, self.mask = table, prefix, q_start, mask
+        self.batch, self.width, self.n, self.max_tokens, self.device = batch, width, n, max_tokens, table.device
+        self._c = TrellisDrafts(table.data_ptr(), prefix.data_ptr(), q_start.data_ptr(),
+                                mask.data_ptr() if mask is not None else None, batch, width, n, max_tokens)
+        self._ref = ctypes.byref(self._c)
+
+
+def _workspace(nbytes: int, device, what: str) -> torch.Tensor:
+    if nbytes == 0:
+        raise ValueError(f"unsupported sizes for {what}")
+    return torch.zeros((nbytes + 15) // 16 * 4, dtype=torch.int32, device=device)
+
+
+def new_tree_workspace(cache: PagedCache, batch: DraftBatch, q_heads: int) -> torch.Tensor:
+    """A zero-filled workspace for tree_attention (reusable for calls of these sizes, one at a time)."""
+    with _on(cache.pool):
+        return _workspace(int(_serving_lib().trellis_tree_workspace_bytes(cache._ref, max(1, batch.batch), batch.max_tokens,
+                                                                          q_heads)), cache.device, "tree_attention")
+
+
+def tree_attention(q, cache: PagedCache, layer: int, batch: DraftBatch, workspace, scale: float = None, out=None, lse=None):
+    """Attention of the drafted tokens q [n, q_heads, head_dim] over their sequences' cached prefixes and the drafts
+    their masks name (written to the cache before).  scale defaults to head_dim ** -0.5.  Returns (out, lse), lse
+    [n, q_heads] fp32 being the log of each softmax sum; lse=False leaves it out."""
+    n, heads, dim = q.shape
+    dev = cache.device
+    qp, qs = _req_tokens(q, "q", batch.n, heads, cache.head_dim)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=torch.bfloat16, device=dev)
+    op, os_ = _req_tokens(out, "out", n, heads, dim)
+    if lse is None:
+        lse = torch.empty((n, heads), dtype=torch.float32, device=dev)
+    lp = None if lse is False else _req_rows(lse, "lse", torch.float32, (n, heads))
+    wp, wn = _req_workspace(workspace)
+    if not (q.device == out.device == batch.device == workspace.device == dev) or (lp and lse.device != dev):
+        raise ValueError(f"q, out, lse, the batch and the workspace must be on the cache's device {dev}")
+    with _on(q):
+        st = _serving_lib().trellis_tree_attention(qp, qs, cache._ref, layer, batch._ref, heads,
+                                                   dim ** -0.5 if scale is None else scale, op, os_, lp, wp, wn,
+                                                   _raw_stream(dev))
+    if st:
+        _check("trellis_tree_attention", st)
+    return out, (None if lse is False else lse)
+
+
+def new_cache_workspace(cache: PagedCache, table, pairs: int = 0) -> torch.Tensor:
+    """A workspace for cache_fork (of up to `pairs` pairs) and cache_compact over the page table."""
+    return _workspace(int(_serving_lib().trellis_cache_workspace_bytes(cache._ref, pairs, table.shape[1])), cache.device,
+                      "cache_fork")
+
+
+def cache_copy(cache: PagedCache, src, dst):
+    """Copies pages src[i] to dst[i] (int32) in every layer."""
+    n = src.shape[0]
+    sp, dp = _req_rows(src, "src", torch.int32, (n,)), _req_rows(dst, "dst", torch.int32, (n,))
+    _same_device(cache.device, src=src, dst=dst)
+    with _on(cache.pool):
+        _check("trellis_cache_copy", _serving_lib().trellis_cache_copy(cache._ref, sp, dp, n, _raw_stream(cache.device)))
+
+
+def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, workspace, room: int = 0):
+    """Forks, grows and frees rows of the page table in place (all int32): row child[i] becomes a copy of row
+    parent[i], sharing the pages its length fills and copying the partly filled one, with room for `room` more
+    positions; parent[i] = child[i] only adds the room, parent[i] = -1 frees the row.  status[i]: 0 done, 1 no room,
+    2 out of range."""
+    rows, width = table.shape
+    pairs = parent.shape[0]
+    args = (_req_rows(table, "table", torch.int32, (rows, width)), _req_rows(lens, "lens", torch.int32, (rows,)),
+            _req_rows(refs, "refs", torch.int32, (cache.pages,)), _req_rows(parent, "parent", torch.int32, (pairs,)),
+            _req_rows(child, "child", torch.int32, (pairs,)), _req_rows(status, "status", torch.int32, (pairs,)))
+    wp, wn = _req_workspace(workspace)
+    _same_device(cache.device, table=table, lens=lens, refs=refs, parent=parent, child=child, status=status,
+                 workspace=workspace)
+    with _on(table):
+        _check("trellis_cache_fork", _serving_lib().trellis_cache_fork(cache._ref, *args, pairs, rows, width, room, wp, wn,
+                                                                       _raw_stream(cache.device)))
+    return status
+
+
+def cache_compact(cache: PagedCache, table, refs, workspace, out_table=None, out_refs=None):
+    """Moves the live pages (refs > 0) to the front of the pool; returns the renamed table and refs (in place unless
+    out_table and out_refs are given)."""
+    rows, width = table.shape
+    out_table = table if out_table is None else out_table
+    out_refs = refs if out_refs is None else out_refs
+    args = (_req_rows(table, "table", torch.int32, (rows, width)), _req_rows(refs, "refs", torch.int32, (cache.pages,)),
+            _req_rows(out_table, "out_table", torch.int32, (rows, width)),
+            _req_rows(out_refs, "out_refs", torch.int32, (cache.pages,)))
+    wp, wn = _req_workspace(workspace)
+    _same_device(cache.device, table=table, refs=refs, out_table=out_table, out_refs=out_refs, workspace=workspace)
+    with _on(table):
+        _check("trellis_cache_compact", _serving_lib().trellis_cache_compact(cache._ref, *args, rows, width, wp, wn,
+                                                                             _raw_stream(cache.device)))
+    return out_table, out_refs
+
+
+def cache_commit(cache: PagedCache, table, prefix, path, accepted, out_lens=None):
+    """Keeps the accepted drafts of each sequence: position prefix[b] + path[b, i] moves to prefix[b] + i for
+    i < accepted[b], in every layer (all int32; path [batch, max_tokens] ascending).  Returns prefix + accepted
+    (out_lens may be prefix)."""
+    batch, width = table.shape
+    tokens = path.shape[1]
+    if out_lens is None:
+        out_lens = torch.empty_like(prefix)
+    args = (_req_rows(table, "table", torch.int32, (batch, width)), _req_rows(prefix, "prefix", torch.int32, (batch,)),
+            _req_rows(path, "path", torch.int32, (batch, tokens)),
+            _req_rows(accepted, "accepted", torch.int32, (batch,)), _req_rows(out_lens, "out_lens", torch.int32, (batch,)))
+    _same_device(cache.device, table=table, prefix=prefix, path=path, accepted=accepted, out_lens=out_lens)
+    with _on(table):
+        _check("trellis_cache_commit", _serving_lib().trellis_cache_commit(cache._ref, *args, batch, width, tokens,
+                                                                           _raw_stream(cache.device)))
+    return out_lens
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns, per row of logits."""
+    logprobs: torch.Tensor      # [n, cands] fp32, of the given tokens
+    lse: torch.Tensor           # [n] fp32
+    entropy: torch.Tensor       # [n] fp32
+    top_ids: torch.Tensor       # [n, top_k] int32, most likely first
+    top_logprobs: torch.Tensor  # [n, top_k] fp32
+
+
+def new_logprobs_workspace(n: int, vocab: int, top_k: int, device) -> torch.Tensor:
+    """A zero-filled workspace for token_logprobs of up to n rows (reusable, one call at a time)."""
+    with torch.cuda.device(device):
+        return _workspace(int(_serving_lib().trellis_logprobs_workspace_bytes(n, vocab, top_k)), device, "token_logprobs")
+
+
+def token_logprobs(logits, tokens, top_k: int, workspace, temperature: float = 1.0, out=None) -> TokenLogprobs:
+    """Log probabilities of tokens [n, cands] int32 under softmax(logits / temperature), with each row's log of the
+    softmax sum, entropy and top_k most likely tokens (equal logits: lowest index first).  logits [n, vocab] bf16 or
+    fp32, rows may be apart.  out: five tensors to write, as TokenLogprobs."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    n, vocab = logits.shape
+    dev = logits.device
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits has dtype {logits.dtype}, expected torch.bfloat16 or torch.float32")
+    stride, one = logits.stride()
+    if one != 1 and vocab > 1:
+        raise ValueError("the logits of a row must be contiguous")
+    cands = tokens.shape[1]
+    if out is None:
+        f32 = dict(dtype=torch.float32, device=dev)
+        out = (torch.empty((n, cands), **f32), torch.empty((n,), **f32), torch.empty((n,), **f32),
+               torch.empty((n, top_k), dtype=torch.int32, device=dev), torch.empty((n, top_k), **f32))
+    lp, ls, en, ti, tl = out
+    args = (_req_rows(lp, "logprobs", torch.float32, (n, cands)), _req_rows(ls, "lse", torch.float32, (n,)),
+            _req_rows(en, "entropy", torch.float32, (n,)), _req_rows(ti, "top_ids", torch.int32, (n, top_k)),
+            _req_rows(tl, "top_logprobs", torch.float32, (n, top_k)))
+    tp = _req_rows(tokens, "tokens", torch.int32, (n, cands))
+    wp, wn = _req_workspace(workspace)
+    if not (tokens.device == lp.device == ls.device == en.device == ti.device == tl.device == workspace.device == dev):
+        raise ValueError(f"tokens, out and the workspace must be on the logits' device {dev}")
+    with _on(logits):
+        st = _serving_lib().trellis_token_logprobs(logits.data_ptr(), TRELLIS_BF16 if logits.dtype == torch.bfloat16 else TRELLIS_F32,
+                                                   stride, tp, n, vocab, cands, top_k, temperature, *args, wp, wn, _raw_stream(dev))
+    if st:
+        _check("trellis_token_logprobs", st)
+    return out if isinstance(out, TokenLogprobs) else TokenLogprobs(*out)

@@ -10,15 +10,17 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "devcache.h"
+#include "abi_common.h"
 #include "launch.h"
 #include "trellis.h"
 
+using trellis::aligned16;
+using trellis::cuda_status;
+using trellis::device_ok;
+
 namespace {
 
-constexpr int kAbiVersion = 101;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+constexpr int kAbiVersion = 102;
 
 int geom_ok(const trellis_geom_t* g) {
   if (!g) return TRELLIS_ENULL;
@@ -37,28 +39,6 @@ int geom_ok(const trellis_geom_t* g) {
   return TRELLIS_OK;
 }
 
-// The current device must be compute capability 10.3 (the library holds
-// sm_103a code only).  Cached per device.
-int device_ok() {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
-    cudaGetLastError();
-    return TRELLIS_EDEVICE;
-  }
-  static trellis::PerDevice<int> ok_of;
-  const auto probe = [dev] {
-    int major = 0, minor = 0;
-    const bool ok = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) == cudaSuccess &&
-                    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) == cudaSuccess &&
-                    major == 10 && minor == 3;
-    if (!ok) cudaGetLastError();
-    return ok ? TRELLIS_OK : TRELLIS_EDEVICE;
-  };
-  return dev < trellis::kMaxDevices ? ok_of.get(dev, probe, TRELLIS_EDEVICE) : probe();
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? TRELLIS_OK : TRELLIS_ECUDA; }
-
 }  // namespace
 
 extern "C" {
@@ -76,6 +56,7 @@ const char* trellis_status_string(int status) {
     case TRELLIS_ECUDA: return "CUDA error at launch";
     case TRELLIS_ENULL: return "a required pointer is NULL";
     case TRELLIS_EDEVICE: return "no usable sm_103 CUDA device is current";
+    case TRELLIS_ESHAPE: return "unsupported or inconsistent sizes, strides or types";
     default: return "unknown status";
   }
 }
@@ -298,8 +279,8 @@ int trellis_set_wait_limit(uint64_t nanoseconds) {
 int trellis_device_error(int reset) {
   int st = device_ok();
   if (st) return st;
-  const int v = trellis::read_device_error(reset);
-  return v < 0 ? TRELLIS_ECUDA : v;
+  const int v = trellis::read_device_error(reset), w = trellis::read_tree_error(reset);
+  return v < 0 || w < 0 ? TRELLIS_ECUDA : v ? v : w;
 }
 
 }  // extern "C"

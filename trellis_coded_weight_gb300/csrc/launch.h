@@ -4,6 +4,8 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 namespace trellis {
@@ -99,9 +101,15 @@ cudaError_t launch_load_floor(const uint32_t* codes, uint32_t* out, int k, int64
 cudaError_t launch_load_floor_rows(const uint32_t* codes, uint32_t* out, int k, int64_t rows, int64_t cols,
                                    cudaStream_t st);
 
-// Device error word of the tensor-core kernels (bounded waits that gave up).
+// Device error words of the kernels that wait on mbarriers (bounded waits that gave up): the prefill's and the
+// tree attention's.
 int read_device_error(int reset);
-// Limit of each bounded wait of the tensor-core kernels for later launches (ns; 0: the 2 s default).
+int read_tree_error(int reset);
+// Limit of each bounded wait of those kernels for later launches (ns; 0: the 2 s default), and the one in force.
 void set_wait_limit_ns(uint64_t ns);
+uint64_t wait_limit_ns();
+
+// cuTensorMapEncodeTiled of the driver, or nullptr.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 }  // namespace trellis

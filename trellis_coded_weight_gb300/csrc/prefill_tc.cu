@@ -885,6 +885,9 @@ cudaError_t launch_gemm_prefill(const uint32_t* codes, const uint16_t* scales, c
 // Limit of each pipeline wait of the tensor-core kernels (ns); 0 restores the default.
 void set_wait_limit_ns(uint64_t ns) { g_wait_ns.store(ns ? ns : kWaitNs); }
 
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+
 // Read (and optionally clear) the device error word.
 int read_device_error(int reset) {
   int v = 0;

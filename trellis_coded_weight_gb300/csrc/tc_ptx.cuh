@@ -87,6 +87,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// As mbar_wait, for waits that are over in a microsecond or two: with a test limit every try, the first one too, is
+// suspended at most the limit (a plain first try would outlast such a wait).
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+  if (timeout_ns >= kShortWaitNs) return mbar_wait(bar, parity, timeout_ns);
+  const uint64_t deadline = globaltimer() + timeout_ns;
+  for (;;) {
+    if (mbar_try_wait_hint(bar, parity, (uint32_t)timeout_ns)) return true;
+    if (globaltimer() > deadline) return false;
+  }
+}
+
 // ---- thread-block clusters -------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -1,0 +1,674 @@
+// tree_attention.cu -- attention of drafted tokens over a paged cache (trellis_tree_attention).
+//
+// For a query row with scores x_p = scale * q.k_p * log2(e) over the positions it sees:
+//   m = max x_p,  l = sum 2^(x_p - m),  o = sum 2^(x_p - m) v_p;   out = o / l,  lse = ln2 (m + log2 l)
+// computed in one pass over the keys with m, l and o carried along (o and l are scaled by 2^(m_old - m_new) when the
+// maximum moves), and joined over disjoint sets of keys by the same rule.
+//
+// The rows of one key/value head -- its group of query heads times the drafts -- share every key, so a block takes ROWS of them
+// (16, 32 or 64) and its warps split the rows by 16 and the keys of a tile between them: scores and outputs
+// are warp-level matrix products (m16n8k16) whose accumulators, maxima and sums stay in the registers of one warp
+// until the segment ends.  Keys and values arrive as 64-key tiles by tensor copies (TMA, 128-byte swizzle, one box
+// per page) issued by a warp of its own, several tiles ahead.  An e4m3 cache stays 8 bits in shared memory and becomes fp16 in registers;
+// its queries are fp16 too, each row scaled by a power of two.  How the work is divided: tree_sched.cuh.
+//
+// Bound: HBM (the cache is read once per 64 rows; other row blocks of the head find it in L2), down to the latency of
+// a launch and a join for short contexts.
+#include <cstring>
+#include <cuda.h>
+
+#include "common.cuh"
+#include "devcache.h"
+#include "launch.h"
+#include "pdl.cuh"
+#include "serving.h"
+#include "tc_ptx.cuh"
+#include "tree_sched.cuh"
+
+namespace trellis {
+namespace {
+
+__device__ int g_tree_error = 0;  // set when a bounded wait gives up (trellis_device_error)
+
+constexpr uint64_t kDrainNs = 2000000000ull;  // for copies in flight when a block leaves
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// c += a (16 x 16) * b (16 x 8), 16-bit operands (bf16, or fp16), fp32 sums.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// Two e4m3 (low 16 bits) to two fp16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+
+template <int D, bool F8, int ROWS>
+struct Cfg {
+  static constexpr int WR = ROWS / 16;              // warps along the rows
+  static constexpr int WK = ROWS == 64 ? 2 : 4;     // warps along the keys of a tile
+  static constexpr int KW = kTile / WK;             // keys of a warp per tile
+  static constexpr int Consumers = WR * WK;         // warps
+  static constexpr int Threads = (Consumers + 1) * 32;
+  static constexpr int RowBytes = D * (F8 ? 1 : 2);  // a key or value
+  static constexpr int BoxBytes = RowBytes < 128 ? RowBytes : 128;  // of it in one copy: a swizzled row
+  static constexpr int Blocks = RowBytes / BoxBytes;
+  static constexpr int HalfStage = kTile * RowBytes;  // the keys, or the values, of a tile
+  static constexpr int Stage = 2 * HalfStage;
+  static constexpr int QBytes = ROWS * D * 2;
+  static constexpr int Regs = D / 2;                 // output numbers of a lane
+  static constexpr int JoinFloats = (Regs + 4) * 32; // a warp's outputs, maxima and sums
+  static constexpr int JoinTurns = D == 256 ? 2 : 1;  // wide heads join their outputs in two turns, to fit
+  static constexpr int JoinSlot = (Regs / JoinTurns + 4) * 32;
+  static constexpr int Join = WR * (WK / 2) * JoinSlot * 4;
+  static constexpr int Cum = (kTreeMaxBatch + 4) * 4;
+  static constexpr int Fixed = QBytes + Join + ROWS * 8 + ROWS * 4 + Cum + 256;
+  static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Stage;
+  static constexpr int Stages = Fit > 8 ? 8 : Fit;
+  static_assert(Stages >= 2, "two tiles in flight at least");
+  static constexpr int Smem = 1024 + Stages * Stage + Fixed;
+};
+
+// Offset of 16-byte chunk `chunk` of row `row` in a swizzled tile of kTile rows (copied as Blocks boxes side by side).
+template <typename C>
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  if constexpr (C::BoxBytes == 128)
+    return (uint32_t)((chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+  else  // 64-byte rows, 64-byte swizzle
+    return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
+}
+
+template <int D, bool F8, int ROWS>
+__global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
+  using C = Cfg<D, F8, ROWS>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* stages = base;
+  uint8_t* sq = stages + C::Stages * C::Stage;
+  float* join = reinterpret_cast<float*>(sq + C::QBytes);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(join + C::Join / 4);
+  float* row_fac = reinterpret_cast<float*>(row_mask + ROWS);
+  int* cum = reinterpret_cast<int*>(row_fac + ROWS);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cum) + C::Cum);
+  uint64_t* empty = full + C::Stages;
+  volatile int* flags = reinterpret_cast<volatile int*>(empty + C::Stages);  // [0] a wait gave up, [1] last to arrive
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::prefetch_tmap(&map);
+    for (int i = 0; i < C::Stages; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, C::Consumers);
+    }
+    flags[0] = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_enter();
+  if (warp == 0) tree_cumulate<ROWS>(p, cum);
+  __syncthreads();
+  const int total = cum[p.batch];
+  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x;
+  const int cta = blockIdx.x;
+  if (cta >= ctas) return;  // fewer steps than blocks
+
+  TreeWalk walk(total, ctas, cta);
+  TreeSegment g;
+  if (warp == C::Consumers) {
+    // ---- the copying warp: every tile of the range, as many ahead as there are stages
+    int it = 0, issued = 0;
+    bool dead = false;
+    while (walk.next<ROWS>(p, cum, total, ctas, g)) {
+      const int32_t* row = p.table + (int64_t)g.b * p.width;
+      const int len = g.seq.prefix + g.seq.count;
+      const int box = p.page_shift < 6 ? 1 << p.page_shift : kTile;  // rows of one copy
+      for (int t = 0; t < g.tiles; ++t, ++it) {
+        const int s = it % C::Stages;
+        const int pos0 = (g.tile0 + t) * kTile;
+        // lane i fetches box i of the tile; boxes past the sequence's end are not copied
+        const int pos = pos0 + lane * box;
+        const bool mine = lane * box < kTile && pos < len;
+        int y = 0;
+        if (mine) {
+          int page = __ldg(row + (pos >> p.page_shift));
+          page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+          y = (((page * 2) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+        }
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        bool ok = true;
+        if (it >= C::Stages && !dead) ok = tc::mbar_wait_short(empty + s, (uint32_t)((it / C::Stages) & 1) ^ 1u, p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok) && !dead) {
+          dead = true;
+          if (lane == 0) flags[0] = 1;
+        }
+        if (dead) continue;  // the consumers' waits run out too; what is in flight lands below
+        issued = it + 1;
+        uint8_t* st = stages + s * C::Stage;
+        if (lane == 0) tc::mbar_arrive_expect_tx(full + s, (uint32_t)(2 * boxes * box * C::RowBytes));
+        __syncwarp();
+        if (mine) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int blk = 0; blk < C::Blocks; ++blk)
+              tc::tma_load_2d(st + kv * C::HalfStage + blk * (kTile * C::BoxBytes) + lane * box * C::BoxBytes, &map, full + s,
+                              blk * (F8 ? C::BoxBytes : C::BoxBytes / 2), y + kv * (p.hkv << p.page_shift));
+        }
+      }
+    }
+    // no copy may land in a block that has left, also where a consumer's wait gave up: see the last ones through
+    for (int i = issued > C::Stages ? issued - C::Stages : 0; i < issued; ++i)
+      tc::mbar_wait(full + i % C::Stages, (uint32_t)((i / C::Stages) & 1), kDrainNs);
+  } else {
+    const int wr = warp / C::WK, wk = warp % C::WK;
+    const int gq = lane >> 2, c4 = lane & 3;  // fragment row and column pair
+    const int nthr = C::Consumers * 32;
+    int it = 0;
+    bool dead = false;
+    while (walk.next<ROWS>(p, cum, total, ctas, g)) {
+      const int rows = min(ROWS, g.seq.count * p.group - g.row_block * ROWS);  // rows of this block that exist
+      const int row0 = g.row_block * ROWS;
+      named_sync(1, nthr);  // the previous segment's queries are no longer read
+      // ---- queries: row r is draft (row0 + r) / group, head (row0 + r) % group of the key/value head's group
+      {
+        constexpr int LPR = D / 8;  // lanes of a row
+        for (int r = threadIdx.x / LPR; r < ROWS; r += nthr / LPR) {
+          const int l = threadIdx.x % LPR;
+          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            u = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
+                                                     (int64_t)(g.head * p.group + hh) * D + 8 * l));
+          float fac = 1.f;
+          if constexpr (F8) {
+            float x[8] = {bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y),
+                          bf16lo_to_f32(u.z), bf16hi_to_f32(u.z), bf16lo_to_f32(u.w), bf16hi_to_f32(u.w)};
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+            constexpr unsigned kLanes = LPR == 32 ? 0xFFFFFFFFu : (1u << LPR) - 1;
+#pragma unroll
+            for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kLanes << (lane / LPR * LPR), m, o));
+            // the row's largest exponent to 0: fp16 then keeps every bf16 number within 2^-14 of the largest exactly
+            uint32_t e = __float_as_uint(m) >> 23;
+            if (e < 2 || e > 252) e = 127;  // zero, subnormal, infinite or NaN rows as they are
+            fac = __uint_as_float(e << 23);
+            const float inv = __uint_as_float((254u - e) << 23);
+            u = make_uint4(pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv),
+                           pack_f16x2(x[4] * inv, x[5] * inv), pack_f16x2(x[6] * inv, x[7] * inv));
+          }
+          *reinterpret_cast<uint4*>(sq + r * (D * 2) + ((l ^ (r & 7)) << 4)) = u;
+          if (l == 0) {
+            row_fac[r] = fac;
+            row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
+          }
+        }
+      }
+      named_sync(1, nthr);
+      float rc[2];
+      uint64_t seen[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = wr * 16 + gq + 8 * i;
+        rc[i] = p.scale_log2 * row_fac[r] * (F8 && p.scales ? __ldg(p.scales + g.head) : 1.f);
+        seen[i] = row_mask[r];
+      }
+      const uint32_t sq32 = tc::smem_u32(sq);
+      constexpr int KS = D / 16;
+      constexpr bool kHold = D <= 128;  // query fragments stay in registers
+      uint32_t qa[kHold ? KS : 1][4];
+      const auto load_q = [&](uint32_t (&a)[4], int ks) {
+        if constexpr (F8) {
+          // the order of the 16 numbers of a step is the one the 8-bit keys have in registers: lane column c4 has 4 c4 .. 4 c4 + 3
+          const int chunk = 2 * ks + (c4 >> 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = wr * 16 + gq + 8 * i;
+            const uint2 v = *reinterpret_cast<const uint2*>(sq + r * (D * 2) + ((chunk ^ (r & 7)) << 4) + (c4 & 1) * 8);
+            a[i] = v.x;
+            a[2 + i] = v.y;
+          }
+        } else {
+          const int r = wr * 16 + (lane & 15), chunk = 2 * ks + (lane >> 4);
+          ldsm4(a, sq32 + r * (D * 2) + ((chunk ^ (r & 7)) << 4));
+        }
+      };
+      if constexpr (kHold)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) load_q(qa[ks], ks);
+
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      const int len = g.seq.prefix + g.seq.count;
+      // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
+      constexpr float kLift = F8 ? 15.f : 0.f;
+
+      for (int t = 0; t < g.tiles; ++t, ++it) {
+        const int s = it % C::Stages;
+        bool ok = dead || tc::mbar_wait_short(full + s, (uint32_t)((it / C::Stages) & 1), p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok) && !dead) {
+          dead = true;
+          if (lane == 0) flags[0] = 1;
+        }
+        const uint32_t sk = tc::smem_u32(stages + s * C::Stage), sv = sk + C::HalfStage;
+        const int key0 = wk * C::KW;                       // this warp's keys of the tile
+        const int pos0 = (g.tile0 + t) * kTile + key0;      // their positions
+        const bool tail = pos0 + C::KW > g.seq.prefix;      // drafts, or past the end, among them
+
+        // ---- scores
+        float x[C::KW / 8][4];
+#pragma unroll
+        for (int i = 0; i < C::KW / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+        if constexpr (F8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += 2) {
+            uint32_t qb[2][4];
+            if constexpr (!kHold) {
+              load_q(qb[0], ks);
+              load_q(qb[1], ks + 1);
+            }
+#pragma unroll
+            for (int kb = 0; kb < C::KW / 16; ++kb) {
+              uint32_t r[4];
+              const int row = key0 + kb * 16 + (lane & 15);
+              ldsm4(r, sk + tile_at<C>(row, ks + (lane >> 4)));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {  // r[0], r[1]: keys 0..7, 8..15 of step ks;  r[2], r[3]: of step ks + 1
+                const uint32_t b0 = e4m3x2_to_f16x2(r[j]), b1 = e4m3x2_to_f16x2(r[j] >> 16);
+                mma16816<true>(x[kb * 2 + (j & 1)], kHold ? qa[kHold ? ks + (j >> 1) : 0] : qb[j >> 1], b0, b1);
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t qb[4];
+            if constexpr (!kHold) load_q(qb, ks);
+#pragma unroll
+            for (int kb = 0; kb < C::KW / 16; ++kb) {
+              uint32_t r[4];
+              const int row = key0 + kb * 16 + (lane & 7) + ((lane >> 4) << 3);
+              ldsm4(r, sk + tile_at<C>(row, 2 * ks + ((lane >> 3) & 1)));
+              mma16816<false>(x[kb * 2], kHold ? qa[kHold ? ks : 0] : qb, r[0], r[1]);
+              mma16816<false>(x[kb * 2 + 1], kHold ? qa[kHold ? ks : 0] : qb, r[2], r[3]);
+            }
+          }
+        }
+
+        // ---- softmax over this warp's keys
+        float mx[2] = {m[0], m[1]};
+#pragma unroll
+        for (int i = 0; i < C::KW / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v = x[i][j] * rc[j >> 1];
+            if (tail) {
+              const int pos = pos0 + i * 8 + c4 * 2 + (j & 1), jd = pos - g.seq.prefix;
+              const bool vis = jd < 0 || (jd < g.seq.count && ((seen[j >> 1] >> jd) & 1ull));
+              v = vis ? v : -INFINITY;
+            }
+            x[i][j] = v;
+            mx[j >> 1] = fmaxf(mx[j >> 1], v);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
+          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 2));
+        }
+        if (__any_sync(0xFFFFFFFFu, mx[0] != m[0] || mx[1] != m[1])) {
+          float a[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            a[i] = m[i] == mx[i] ? 1.f : ex2(m[i] - mx[i]);
+            l[i] *= a[i];
+            m[i] = mx[i];
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] *= a[j >> 1];
+        }
+        const float ms[2] = {(m[0] == -INFINITY ? 0.f : m[0]) - kLift, (m[1] == -INFINITY ? 0.f : m[1]) - kLift};
+        uint32_t pa[C::KW / 16][4];
+#pragma unroll
+        for (int i = 0; i < C::KW / 8; ++i) {
+          float e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[j] = ex2(x[i][j] - ms[j >> 1]);
+            l[j >> 1] += e[j];
+          }
+          pa[i >> 1][(i & 1) * 2] = F8 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
+          pa[i >> 1][(i & 1) * 2 + 1] = F8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
+        }
+
+        // ---- outputs
+        constexpr uint32_t kExp = F8 ? 0x7C00u : 0x7F80u;  // all ones: infinite or NaN
+        bool odd = false;  // a draft with numbers that are not finite
+#pragma unroll
+        for (int kb = 0; kb < C::KW / 16; ++kb) {
+          const int row = key0 + kb * 16 + (lane & 15);
+          // in a tail tile: rows past the end count as zeros whatever their bits; drafts that are not finite are left
+          // to the rows that see them
+          const auto clean = [&](uint32_t& v, int half) {
+            const int pos = pos0 + kb * 16 + half * 8 + c4 * 2;
+            if (pos >= len) v = 0;
+            else if (pos + 1 >= len) v &= 0xFFFFu;
+            if (pos >= g.seq.prefix && (v & kExp) == kExp) { v &= 0xFFFF0000u; odd = true; }
+            if (pos + 1 >= g.seq.prefix && (v >> 16 & kExp) == kExp) { v &= 0xFFFFu; odd = true; }
+          };
+#pragma unroll
+          for (int dc = 0; dc < C::RowBytes / 16; dc += 2) {
+            uint32_t r[4];
+            ldsm4t(r, sv + tile_at<C>(row, dc + (lane >> 4)));
+            if constexpr (F8) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {  // chunk dc + j: its even columns, then its odd ones
+                uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4420)), e1 = e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4420));
+                uint32_t o0 = e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4431)), o1 = e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4431));
+                if (tail) { clean(e0, 0); clean(e1, 1); clean(o0, 0); clean(o1, 1); }
+                mma16816<true>(o[2 * (dc + j)], pa[kb], e0, e1);
+                mma16816<true>(o[2 * (dc + j) + 1], pa[kb], o0, o1);
+              }
+            } else {
+              if (tail) { clean(r[0], 0); clean(r[1], 1); clean(r[2], 0); clean(r[3], 1); }
+              mma16816<false>(o[dc], pa[kb], r[0], r[1]);
+              mma16816<false>(o[dc + 1], pa[kb], r[2], r[3]);
+            }
+          }
+        }
+        if (tail && __any_sync(0xFFFFFFFFu, odd)) {
+          // infinities and NaN of a draft reach the rows that see it, and no others
+          for (int kk = 0; kk < C::KW; ++kk) {
+            const int jd = pos0 + kk - g.seq.prefix;
+            if (jd < 0 || jd >= g.seq.count) continue;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int d = F8 ? (i >> 1) * 16 + c4 * 4 + (j & 1) * 2 + (i & 1) : i * 8 + c4 * 2 + (j & 1);
+                const int byte = F8 ? d : 2 * d;
+                const uint8_t* at = stages + s * C::Stage + C::HalfStage + tile_at<C>(key0 + kk, byte >> 4) + (byte & 15);
+                const uint32_t v = F8 ? e4m3x2_to_f16x2(*at) & 0xFFFFu : *reinterpret_cast<const uint16_t*>(at);
+                if ((v & kExp) == kExp && ((seen[j >> 1] >> jd) & 1ull)) o[i][j] += F8 ? f16_to_f32((uint16_t)v) : bf16_to_f32((uint16_t)v);
+              }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(empty + s);
+      }
+
+      // ---- the segment's end: sums over the lanes of a row, then over the warps that share rows
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], 2);
+      }
+#pragma unroll
+      for (int step = C::WK / 2; step; step >>= 1) {
+        constexpr int NT = C::Regs / C::JoinTurns;
+        float* mine = join + (wr * (C::WK / 2) + (wk & (step - 1))) * C::JoinSlot + lane;
+        float a[2], b[2];
+#pragma unroll
+        for (int turn = 0; turn < C::JoinTurns; ++turn) {
+          if (wk >= step && wk < 2 * step) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mine[i * 32] = o[(turn * NT + i) >> 2][i & 3];
+            if (turn == 0)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                mine[(NT + i) * 32] = m[i];
+                mine[(NT + 2 + i) * 32] = l[i];
+              }
+          }
+          named_sync(1, nthr);
+          if (wk < step) {
+            if (turn == 0)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float om = mine[(NT + i) * 32], nm = fmaxf(m[i], om), base_m = nm == -INFINITY ? 0.f : nm;
+                a[i] = ex2(m[i] - base_m);
+                b[i] = ex2(om - base_m);
+                l[i] = l[i] * a[i] + mine[(NT + 2 + i) * 32] * b[i];
+                m[i] = nm;
+              }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float& v = o[(turn * NT + i) >> 2][i & 3];
+              v = v * a[(i >> 1) & 1] + mine[i * 32] * b[(i >> 1) & 1];
+            }
+          }
+          named_sync(1, nthr);
+        }
+      }
+
+      // an output fragment, already joined, to the outputs
+      const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
+      const auto store = [&](const float (&v)[4], int i, const float (&fl)[2]) {  // i: output fragment
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = wr * 16 + gq + 8 * half;
+          if (r >= rows) continue;
+          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          uint16_t* at = p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D;
+          if constexpr (F8) {
+            const int col = (i >> 1) * 16 + c4 * 4 + (i & 1);
+            at[col] = f32_to_bf16_rn(v[2 * half] * fl[half]);
+            at[col + 2] = f32_to_bf16_rn(v[2 * half + 1] * fl[half]);
+          } else {
+            *reinterpret_cast<uint32_t*>(at + i * 8 + c4 * 2) = pack_bf16x2(v[2 * half] * fl[half], v[2 * half + 1] * fl[half]);
+          }
+        }
+      };
+      const auto store_lse = [&](const float (&mm)[2], const float (&ll)[2]) {
+        if (!p.lse || c4 != 0) return;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = wr * 16 + gq + 8 * half;
+          if (r >= rows) continue;
+          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] =
+              ll[half] == 0.f ? -INFINITY : kLn2 * (mm[half] + (log2f(ll[half]) - kLift));
+        }
+      };
+      if (g.first == g.last) {
+        if (wk == 0) {
+          const float fl[2] = {l[0] == 0.f ? 0.f : vs / l[0], l[1] == 0.f ? 0.f : vs / l[1]};
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) store(o[i], i, fl);
+          store_lse(m, l);
+        }
+        continue;
+      }
+      // a part: the warps' fragments as they are, [row warp][number][lane]
+      if (wk == 0) {
+        float* at = p.part + ((int64_t)tree_slot(cta, g.tile0 == 0) * C::WR + wr) * C::JoinFloats + lane;
+#pragma unroll
+        for (int i = 0; i < C::Regs; ++i) __stcg(at + i * 32, o[i >> 2][i & 3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          __stcg(at + (C::Regs + i) * 32, m[i]);
+          __stcg(at + (C::Regs + 2 + i) * 32, l[i]);
+        }
+      }
+      named_sync(1, nthr);
+      if (threadIdx.x == 0)
+        flags[1] = tree_arrive(p.counter + g.first, g.last - g.first);
+      named_sync(1, nthr);
+      if (!flags[1]) continue;
+      // the last to arrive: weights of the parts from their maxima, then the weighted sums; each warp takes a share
+      // of the numbers of its rows
+      const int parts = g.last - g.first + 1;
+      const auto part_of = [&](int j) {
+        return p.part + ((int64_t)tree_slot(g.first + j, j == 0) * C::WR + wr) * C::JoinFloats + lane;
+      };
+      float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};
+      for (int j = 0; j < parts; ++j) {
+        const float* at = part_of(j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mm[i] = fmaxf(mm[i], __ldcg(at + (C::Regs + i) * 32));
+      }
+      const float bm[2] = {mm[0] == -INFINITY ? 0.f : mm[0], mm[1] == -INFINITY ? 0.f : mm[1]};
+      constexpr int N = C::Regs / C::WK;  // numbers of this warp
+      float acc[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < parts; ++j) {
+        const float* at = part_of(j);
+        float w[2], v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __ldcg(at + (wk * N + i) * 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          w[i] = ex2(__ldcg(at + (C::Regs + i) * 32) - bm[i]);
+          ll[i] += w[i] * __ldcg(at + (C::Regs + 2 + i) * 32);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += w[(i >> 1) & 1] * v[i];
+      }
+      const float fl[2] = {ll[0] == 0.f ? 0.f : vs / ll[0], ll[1] == 0.f ? 0.f : vs / ll[1]};
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        const float v[4] = {acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+        store(v, wk * (N / 4) + i, fl);
+      }
+      if (wk == 0) store_lse(mm, ll);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && flags[0]) atomicCAS(&g_tree_error, 0, 1);
+}
+
+// ---------------------------------------------------------------- host
+
+int rows_of(int max_tokens, int group) {
+  const int rows = max_tokens * group;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+int tree_ctas() { return device_sm_count() < kTreeMaxCtas ? device_sm_count() : kTreeMaxCtas; }
+
+template <int D, bool F8, int ROWS>
+cudaError_t launch_rows(const CUtensorMap& map, const TreeParams& p, cudaStream_t st) {
+  using C = Cfg<D, F8, ROWS>;
+  auto kern = tree_kernel<D, F8, ROWS>;
+  static PerDevice<cudaError_t> attr_of;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  const cudaError_t e = attr_of.get(dev, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
+  }, cudaErrorInvalidDevice);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)tree_ctas()), dim3(C::Threads), C::Smem, st, map, p);
+}
+
+template <int D, bool F8>
+cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int rows, cudaStream_t st) {
+  if (rows == 16) return launch_rows<D, F8, 16>(map, p, st);
+  if (rows == 32) return launch_rows<D, F8, 32>(map, p, st);
+  return launch_rows<D, F8, 64>(map, p, st);
+}
+
+}  // namespace
+
+size_t tree_workspace_bytes(const trellis_cache_t& c, int batch, int max_tokens, int q_heads) {
+  (void)batch;  // parts belong to thread blocks, whatever the batch
+  const size_t part = (size_t)(rows_of(max_tokens, q_heads / c.heads) / 16) * (c.head_dim / 2 + 4) * 32 * 4;
+  return kTreeMaxCtas * 4 + part * 2 * tree_ctas();
+}
+
+int read_tree_error(int reset) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_tree_error, sizeof(int)) != cudaSuccess) return -1;
+  if (reset && v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_tree_error, &zero, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,
+                                  const trellis_drafts_t& d, int q_heads, float scale, uint16_t* out,
+                                  int64_t out_stride, float* lse, void* workspace, cudaStream_t st) {
+  TreeParams p{};
+  p.q = q; p.out = out; p.lse = lse;
+  p.table = d.table; p.prefix = d.prefix; p.q_start = d.q_start; p.mask = d.mask;
+  p.scales = c.scales ? c.scales + (int64_t)layer * 2 * c.heads : nullptr;
+  p.q_stride = q_stride; p.out_stride = out_stride;
+  p.pages = c.pages;
+  p.wait_ns = wait_limit_ns();
+  p.batch = d.batch; p.width = d.width; p.n = d.n; p.max_tokens = d.max_tokens;
+  p.hq = q_heads; p.hkv = c.heads; p.group = q_heads / c.heads;
+  p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  const int rows = rows_of(d.max_tokens, p.group);
+  p.row_blocks = (d.max_tokens * p.group + rows - 1) / rows;
+  p.scale_log2 = scale * kLog2e;
+  p.counter = static_cast<uint32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kTreeMaxCtas * 4);
+
+  const auto fn = tensor_map_encoder();
+  if (!fn) return cudaErrorNotSupported;
+  const bool f8 = c.dtype == TRELLIS_E4M3;
+  const int elem = (int)cache_elem_bytes(c), row_bytes = c.head_dim * elem, inner = row_bytes < 128 ? row_bytes : 128;
+  uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
+  // the layer's rows of head_dim numbers; a copy takes up to 128 bytes of each of one page's rows (at most a tile)
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.pages * 2 * c.heads * c.page_size)};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)(inner / elem), (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  if (f8) {
+    if (c.head_dim == 64) return launch_d<64, true>(map, p, rows, st);
+    if (c.head_dim == 128) return launch_d<128, true>(map, p, rows, st);
+    return launch_d<256, true>(map, p, rows, st);
+  }
+  if (c.head_dim == 64) return launch_d<64, false>(map, p, rows, st);
+  if (c.head_dim == 128) return launch_d<128, false>(map, p, rows, st);
+  return launch_d<256, false>(map, p, rows, st);
+}
+
+}  // namespace trellis

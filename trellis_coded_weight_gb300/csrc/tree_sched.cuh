@@ -1,0 +1,141 @@
+// tree_sched.cuh -- how the work of a tree attention call is divided over the GPU, shared by its kernels.
+//
+// An item is one key/value head of one sequence and one block of ROWS query rows (row r of a sequence and head:
+// draft r / group, query head r % group of the head's group); it takes one step per kTile keys.  Lengths are device
+// data, so the division is made on the device: all steps of all items, in the order of (sequence, row block, head,
+// tile), are cut into equal contiguous ranges, one per thread block.  An item that falls into one range is finished
+// there.  Otherwise each block writes its part (maximum, sum and unnormalised output of its keys, fp32) to the
+// workspace, and the last one to arrive joins the parts in their order, so results do not depend on timing.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "serving.h"
+
+namespace trellis {
+
+constexpr int kTile = 64;            // keys per step
+constexpr int kTreeMaxCtas = 1024;   // bound on the grid (sizes the counters)
+
+struct TreeParams {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const int32_t *table, *prefix, *q_start;
+  const uint64_t* mask;
+  const float* scales;  // [2][hkv] of the layer, or null
+  uint32_t* counter;    // [kTreeMaxCtas], zero between calls: arrivals for the item that block c was the first to share
+  float* part;          // two slots per thread block
+  int64_t q_stride, out_stride;
+  int64_t pages;
+  uint64_t wait_ns;
+  int batch, width, n, max_tokens, hq, hkv, group, page_shift, row_blocks;
+  float scale_log2;     // scale * log2(e)
+};
+
+// One sequence's lengths, clamped to what the arrays hold.
+struct TreeSeq {
+  int start, count, prefix;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  TreeSeq s;
+  int a = __ldg(p.q_start + b), z = __ldg(p.q_start + b + 1);
+  a = a < 0 ? 0 : a > p.n ? p.n : a;
+  z = z < a ? a : z > p.n ? p.n : z;
+  const int room = p.width << p.page_shift;
+  int c = z - a;
+  c = c > p.max_tokens ? p.max_tokens : c;
+  c = c > room ? room : c;
+  int pre = __ldg(p.prefix + b);
+  pre = pre < 0 ? 0 : pre > room - c ? room - c : pre;
+  s.start = a;
+  s.count = c;
+  s.prefix = pre;
+  return s;
+}
+__device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return s.count ? (s.prefix + s.count + kTile - 1) / kTile : 0; }
+
+// cum[b] = steps of the sequences before b (batch + 1 entries), by one warp.
+template <int ROWS>
+__device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int v = 0;
+    if (b < p.batch) {
+      const TreeSeq s = tree_seq(p, b);
+      v = tree_tiles(s) * ((s.count * p.group + ROWS - 1) / ROWS) * p.hkv;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (b < p.batch) cum[b + 1] = before + v;
+    before += __shfl_sync(0xFFFFFFFFu, v, 31);
+  }
+  if (lane == 0) cum[0] = 0;
+}
+
+// The blocks' ranges: block c of `ctas` takes steps [c * total / ctas, (c + 1) * total / ctas).
+__device__ __forceinline__ int tree_cta_of(int64_t step, int64_t total, int ctas) { return (int)(((step + 1) * ctas - 1) / total); }
+
+// A stretch of one item's steps inside a block's range.
+struct TreeSegment {
+  TreeSeq seq;
+  int b, head, row_block;
+  int tile0, tiles;   // first tile, number of tiles
+  int first, last;    // blocks that share the item
+};
+
+// Walks a block's range segment by segment.
+struct TreeWalk {
+  int at, end, b;
+  __device__ __forceinline__ TreeWalk(int total, int ctas, int cta)
+      : at((int)((int64_t)cta * total / ctas)), end((int)((int64_t)(cta + 1) * total / ctas)), b(-1) {}
+  template <int ROWS>
+  __device__ __forceinline__ bool next(const TreeParams& p, const int* cum, int total, int ctas, TreeSegment& g) {
+    if (at >= end) return false;
+    if (b < 0) {  // the last sequence that starts at or before `at`; empty ones are passed over
+      int lo = 0, hi = p.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= at) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+    } else {
+      while (cum[b + 1] <= at) ++b;
+    }
+    g.b = b;
+    g.seq = tree_seq(p, b);
+    const int nt = tree_tiles(g.seq), r = at - cum[b], item = r / nt;
+    g.tile0 = r - item * nt;
+    g.row_block = item / p.hkv;
+    g.head = item - g.row_block * p.hkv;
+    const int left = nt - g.tile0;
+    g.tiles = left < end - at ? left : end - at;
+    const int64_t start = (int64_t)cum[b] + (int64_t)item * nt;
+    g.first = tree_cta_of(start, total, ctas);
+    g.last = tree_cta_of(start + nt - 1, total, ctas);
+    at += g.tiles;
+    return true;
+  }
+};
+
+// The workspace slot of a block's part: a block has at most one part that starts its item and one that does not.
+__device__ __forceinline__ int tree_slot(int cta, bool starts_item) { return 2 * cta + (starts_item ? 1 : 0); }
+
+// One arrival at the counter of the item's first block (an item that is shared is the last one of the block it starts
+// in, so no two items share a counter, and a workspace serves calls of any sizes); true for the last of the blocks that share the item.  Acquire-release: parts written before (and a
+// barrier) are visible to whoever sees the last count.
+__device__ __forceinline__ bool tree_arrive(uint32_t* counter, int others) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  if (old != (uint32_t)others) return false;
+  *counter = 0u;
+  return true;
+}
+
+}  // namespace trellis
