@@ -8,12 +8,13 @@
 // Sums of different references are joined by 2^(c (R - R')), t by t + s c (R - R').
 //
 // Alternatives: a number's key is its bits made to order like its value, above the complement of its column, so that keys are
-// distinct and the larger key is the earlier alternative.  A block keeps the best top_k so far and their last value as
-// a threshold; what passes it is appended to a list in shared memory, which is cut back to top_k by counting, for
-// each key, the larger ones.  The first chunk's threshold is the top_k-th largest of 64 maxima over 64th parts of the chunk
-// (at least top_k numbers reach it), so few numbers pass.  If more pass than the list holds (rows of equal numbers,
-// rising rows) the chunk is taken again with such a threshold of its own, and if that fails (many equal numbers), by
-// top_k searches for the next key.
+// distinct and the larger key is the earlier alternative.  While the sums run, each thread only keeps the largest
+// number it has met.  The top_k-th largest of 64 maxima (of four threads each) is a threshold that at least top_k
+// numbers reach, so only threads whose own maximum reaches it -- about top_k of 256 -- can hold an alternative:
+// their numbers are read once more (from L2), what reaches the threshold is listed, and the list is put in order by counting
+// larger keys.  Where more numbers reach it than the list holds, many are equal to it: those above it are listed, and
+// the first equal ones from the block's first column on; if those above are too many as well, top_k rounds of a tournament
+// between the threads take the next key each.
 //
 // A row is split over blocks where there are few rows; the last block to arrive joins the parts in their order, so
 // results do not depend on timing.  Bound: HBM for many rows (one read of the logits), latency for one.
@@ -27,11 +28,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 1024;       // candidates held before they are cut back
-constexpr int kCutAt = 192;       // a list longer than this is cut back after its chunk
-constexpr int kVecs = 4;          // 16-byte vectors of a thread per chunk
-constexpr int kCounters = 4096;   // rows that may be split
-constexpr int kGroupThreads = 4;  // threads of one of the 64 parts of a chunk
+constexpr int kPerSM = 5;          // blocks of an SM at a time
+constexpr int kList = 768;         // numbers that may reach the threshold
+constexpr int kBatch = 4;          // 16-byte loads of a thread in flight
+constexpr int kMaxSplits = 64;
+constexpr int kCounters = 4096;    // rows that may be split
+constexpr int kGroupThreads = 4;   // threads of one of the 64 maxima
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kFar = -16384.f;  // 2^kFar is 0: stands in for minus infinity where it would be multiplied
@@ -45,7 +47,7 @@ struct Params {
   float* sums;                  // [n][splits][4]
   unsigned long long* keys;     // [n][splits][top_k]
   int64_t row_stride;
-  int n, vocab, cands, top_k, splits, chunks;
+  int n, vocab, cands, top_k, splits;
   float c, inv_t;               // log2(e) / temperature, 1 / temperature
 };
 
@@ -86,228 +88,295 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
   return Sums{r, a.s * ea + b.s * eb, (a.t + a.s * da) * ea + (b.t + b.s * db) * eb};
 }
 
+// 16 bytes of logits: their numbers, their maximum (NaN if there is one).
 template <typename T>
 struct Vec;
 template <>
 struct Vec<uint16_t> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void get(const uint4& u, float (&x)[8]) {
-    x[0] = bf16lo_to_f32(u.x); x[1] = bf16hi_to_f32(u.x);
-    x[2] = bf16lo_to_f32(u.y); x[3] = bf16hi_to_f32(u.y);
-    x[4] = bf16lo_to_f32(u.z); x[5] = bf16hi_to_f32(u.z);
-    x[6] = bf16lo_to_f32(u.w); x[7] = bf16hi_to_f32(u.w);
+  static __device__ __forceinline__ float2 pair(const uint4& u, int i) {
+    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+    return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float max(const uint4& u) {
+    const uint32_t m = max2(max2(u.x, u.y), max2(u.z, u.w));
+    return max_nan(bf16lo_to_f32(m), bf16hi_to_f32(m));
   }
   static __device__ __forceinline__ float one(const uint16_t* p) { return bf16_to_f32(*p); }
+  static __device__ __forceinline__ uint4 edge(const uint16_t* x, int col, int vocab) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = col + i >= 0 && col + i < vocab ? x[col + i] : 0xFF80u;
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void get(const uint4& u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ float2 pair(const uint4& u, int i) {
+    return i == 0 ? make_float2(__uint_as_float(u.x), __uint_as_float(u.y)) : make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ float max(const uint4& u) {
+    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ uint4 edge(const float* x, int col, int vocab) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = col + i >= 0 && col + i < vocab ? __float_as_uint(x[col + i]) : 0xFF800000u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Vectors of a row begin on 16-byte boundaries: vector v holds columns v * N - skew .., those outside the row read as
+// minus infinity.
+template <typename T>
+struct Row {
+  const T* x;
+  int skew, vocab;
+  __device__ __forceinline__ int col(int v) const { return v * Vec<T>::N - skew; }
+  __device__ __forceinline__ uint4 load(int v) const {
+    const int c = col(v);
+    if (c >= 0 && c + Vec<T>::N <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + c));
+    return Vec<T>::edge(x, c, vocab);
+  }
 };
 
 struct Shared {
-  unsigned long long list[kList];
-  unsigned long long best[kMaxTop];  // cut back: descending
+  alignas(16) unsigned long long list[kList];
+  alignas(16) uint32_t group[64];
+  unsigned long long best[kMaxTop];  // descending
   unsigned long long red[kWarps];
   Sums part[kWarps];
-  float group_max[64];
+  int holders[kThreads];
   float threshold;
-  int count;
+  int count, n_holders;
   uint32_t last;
 };
 
-// The list's `count` keys cut back to the top_k largest, in descending order; the threshold is the last one's value.
+// The list's sh.count keys cut back to the top_k largest, in descending order, in sh.best; sh.count follows.  The
+// caller's barrier precedes it; ends with a barrier.
 __device__ __forceinline__ void cut_back(Shared& sh, int top_k) {
-  const int count = sh.count;  // the caller's barrier precedes this
+  const int count = sh.count;
   for (int i = threadIdx.x; i < count; i += kThreads) {
     const unsigned long long mine = sh.list[i];
     int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < count; ++j) rank += sh.list[j] > mine;
     if (rank < top_k) sh.best[rank] = mine;
   }
   __syncthreads();
-  const int kept = count < top_k ? count : top_k;
-  if (threadIdx.x < kept) sh.list[threadIdx.x] = sh.best[threadIdx.x];
-  if (threadIdx.x == 0) {
-    sh.count = kept;
-    sh.threshold = kept == top_k ? from_order_bits((uint32_t)(sh.best[top_k - 1] >> 32)) : -INFINITY;
-  }
+  if (threadIdx.x == 0) sh.count = count < top_k ? count : top_k;
   __syncthreads();
 }
 
-// A value that at least top_k of the chunk's numbers reach (minus infinity if that needs more than 64 parts):
-// the top_k-th largest of the 64 parts' maxima.  Ends with a barrier.
-__device__ __forceinline__ float chunk_threshold(Shared& sh, float thread_max, int top_k) {
+// A value that at least top_k of the block's numbers reach: the top_k-th largest of the 64 maxima.  Ends with a
+// barrier.
+__device__ __forceinline__ float find_threshold(Shared& sh, float thread_max, int top_k) {
   float g = thread_max;
 #pragma unroll
   for (int o = 1; o < kGroupThreads; o <<= 1) g = max_nan(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
-  if (threadIdx.x % kGroupThreads == 0) sh.group_max[threadIdx.x / kGroupThreads] = g;
+  if (threadIdx.x % kGroupThreads == 0) sh.group[threadIdx.x / kGroupThreads] = order_bits(g);
   __syncthreads();
   if (threadIdx.x < 64) {
-    const uint32_t mine = order_bits(sh.group_max[threadIdx.x]);
+    const uint32_t mine = sh.group[threadIdx.x];
     int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < 64; ++j) {
-      const uint32_t o = order_bits(sh.group_max[j]);
-      rank += o > mine || (o == mine && j < (int)threadIdx.x);
+#pragma unroll
+    for (int j = 0; j < 64; j += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(sh.group + j);
+      rank += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      rank += (o.x == mine && j < (int)threadIdx.x) + (o.y == mine && j + 1 < (int)threadIdx.x) +
+              (o.z == mine && j + 2 < (int)threadIdx.x) + (o.w == mine && j + 3 < (int)threadIdx.x);
     }
     if (rank == top_k - 1) sh.threshold = from_order_bits(mine);
   }
   __syncthreads();
-  const float th = sh.threshold;
-  __syncthreads();
-  return th;
+  return sh.threshold;
+}
+
+// The largest key below `below` among the vectors first + of, first + of + kThreads, .. of thread `of`, by a warp.
+template <typename T>
+__device__ __forceinline__ unsigned long long next_key(const Row<T>& row, int of, int first, int last, unsigned long long below) {
+  constexpr int N = Vec<T>::N;
+  unsigned long long best = 0;
+  for (int v = first + of + (threadIdx.x & 31) * kThreads; v < last; v += 32 * kThreads) {
+    const int c = row.col(v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i >= 0 && c + i < row.vocab) {
+        const unsigned long long key = key_of(Vec<T>::one(row.x + c + i), c + i);
+        if (key < below && key > best) best = key;
+      }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const unsigned long long u = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+    best = u > best ? u : best;
+  }
+  return best;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params p) {
   pdl_enter();
-  constexpr int N = Vec<T>::N, PER = kVecs * N, CHUNK = kThreads * PER;
+  constexpr int N = Vec<T>::N;
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int split = blockIdx.x;
   const int64_t row = blockIdx.y;
-  const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
-  // chunks start on 16-byte boundaries: a row that does not starts `skew` numbers into its first chunk
-  const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int first = (int)((int64_t)split * p.chunks / p.splits), last = (int)((int64_t)(split + 1) * p.chunks / p.splits);
+  Row<T> x;
+  x.x = static_cast<const T*>(p.logits) + row * p.row_stride;
+  x.skew = (int)((reinterpret_cast<uintptr_t>(x.x) & 15) / sizeof(T));
+  x.vocab = p.vocab;
+  const int vecs = (p.vocab + x.skew + N - 1) / N;
+  const int first = (int)((int64_t)split * vecs / p.splits), last = (int)((int64_t)(split + 1) * vecs / p.splits);
   if (tid == 0) {
     sh.count = 0;
-    sh.threshold = -INFINITY;
+    sh.n_holders = 0;
   }
-  __syncthreads();
 
+  // ---- the sums, and each thread's largest number
   Sums acc{-INFINITY, 0.f, 0.f};
-  bool cut = false;  // the list has been cut back to top_k: its threshold holds for later columns
-  for (int ch = first; ch < last; ++ch) {
-    // vector v of the thread: columns col0 + v * kThreads * N ..
-    const int col0 = ch * CHUNK - skew + tid * N;
-    float xs[PER];
-    float vmax[kVecs];
+  const auto add = [&](const uint4 (&u)[kBatch], int n) {
+    float m = acc.r;
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int c0 = col0 + v * kThreads * N;
-      float(&e)[N] = *reinterpret_cast<float(*)[N]>(xs + v * N);
-      if (c0 >= 0 && c0 + N <= p.vocab) {
-        Vec<T>::get(__ldcs(reinterpret_cast<const uint4*>(x + c0)), e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = c0 + i >= 0 && c0 + i < p.vocab ? Vec<T>::one(x + c0 + i) : -INFINITY;
-      }
-    }
-    float tmax = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      float m = xs[v * N];
-#pragma unroll
-      for (int i = 1; i < N; ++i) m = max_nan(m, xs[v * N + i]);
-      vmax[v] = m;
-      tmax = max_nan(tmax, m);
-    }
-    const float r = max_nan(acc.r, tmax);
-    if (r != acc.r && acc.r != -INFINITY) {
-      const float d = max_nan((acc.r - r) * p.c, kFar), e = ex2(d);
+    for (int b = 0; b < kBatch; ++b)
+      if (b < n) m = max_nan(m, Vec<T>::max(u[b]));
+    if (m != acc.r && acc.r != -INFINITY) {  // also where m is NaN
+      const float d = max_nan((acc.r - m) * p.c, kFar), e = ex2(d);
       acc.t = (acc.t + acc.s * d) * e;
       acc.s *= e;
     }
-    acc.r = r;
-    if (r != -INFINITY) {
+    acc.r = m;
+    if (m == -INFINITY) return;
+    const float2 neg = make_float2(-m, -m), cc = make_float2(p.c, p.c);
+    float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float y = max_nan((xs[i] - r) * p.c, kFar);
-        const float e = ex2(y);
-        acc.s += e;
-        acc.t = __fmaf_rn(e, y, acc.t);
+    for (int b = 0; b < kBatch; ++b) {
+      if (b >= n) break;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        float2 y = __fmul2_rn(__fadd2_rn(Vec<T>::pair(u[b], i), neg), cc);
+        y.x = max_nan(y.x, kFar);
+        y.y = max_nan(y.y, kFar);
+        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+        s = __fadd2_rn(s, e);
+        t = __ffma2_rn(e, y, t);
       }
     }
+    acc.s += s.x + s.y;
+    acc.t += t.x + t.y;
+  };
+  {
+    uint4 u[kBatch];
+    int v = first + tid;
+    for (; v + (kBatch - 1) * kThreads < last; v += kBatch * kThreads) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) u[b] = x.load(v + b * kThreads);
+      add(u, kBatch);
+    }
+    int n = 0;
+#pragma unroll
+    for (int b = 0; b < kBatch - 1; ++b)
+      if (v + b * kThreads < last) {
+        u[b] = x.load(v + b * kThreads);
+        n = b + 1;
+      }
+    if (n) add(u, n);
+  }
 
-    if (p.top_k == 0) continue;
-    const float old_th = cut ? sh.threshold : -INFINITY;
-    float th = old_th;
-    bool strict = cut;  // later columns lose to equal earlier ones once top_k are held
-    if (!cut) {
-      th = chunk_threshold(sh, tmax, p.top_k);
-      strict = false;
-    }
-    const int held = sh.count;
+  // ---- the alternatives
+  if (p.top_k) {
+    const float th = find_threshold(sh, acc.r, p.top_k);
+    if (!(acc.r < th) && first + tid < last) sh.holders[atomicAdd(&sh.n_holders, 1)] = tid;
     __syncthreads();
-    for (int attempt = 0;; ++attempt) {
+    const int holders = sh.n_holders;
+    // lists what passes: numbers from the threshold up, or (strict) above it
+    const auto collect = [&](bool strict) {
+      for (int h = warp; h < holders; h += kWarps)
+        for (int v = first + sh.holders[h] + lane * kThreads; v < last; v += 32 * kThreads) {
+          const uint4 u = x.load(v);
+          const float m = Vec<T>::max(u);
+          if (strict ? m <= th : m < th) continue;
+          const int c = x.col(v);
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        if (strict ? vmax[v] <= th : vmax[v] < th) continue;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float e = xs[v * N + i];
-          const int col = col0 + v * kThreads * N + i;
-          if ((strict ? !(e <= th) : !(e < th)) && col >= 0 && col < p.vocab) {
+          for (int i = 0; i < N; ++i) {
+            const float2 q = Vec<T>::pair(u, i >> 1);
+            const float e = i & 1 ? q.y : q.x;
+            if (!(strict ? e <= th : e < th) && c + i >= 0 && c + i < p.vocab) {
+              const int at = atomicAdd(&sh.count, 1);
+              if (at < kList) sh.list[at] = key_of(e, c + i);
+            }
+          }
+        }
+      __syncthreads();
+    };
+    collect(false);
+    bool listed = sh.count <= kList;
+    if (!listed) {
+      // many numbers equal to the threshold (banned tokens, flat rows): those above it, and the first ones equal to it
+      __syncthreads();
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      collect(true);
+      const int above = sh.count;
+      listed = above <= kList - 2 * kThreads;
+      if (listed) {
+        const int end = min(x.col(last), p.vocab);
+        for (int c0 = max(x.col(first), 0); c0 < end; c0 += kThreads) {
+          const int c = c0 + tid;
+          if (c < end && Vec<T>::one(x.x + c) == th) {
             const int at = atomicAdd(&sh.count, 1);
-            if (at < kList) sh.list[at] = key_of(e, col);
+            sh.list[at] = key_of(th, c);
           }
+          __syncthreads();
+          const bool enough = sh.count - above >= p.top_k;
+          __syncthreads();
+          if (enough) break;
         }
       }
+    }
+    if (listed) {
+      cut_back(sh, p.top_k);
+    } else {
+      // a tournament: the threads' best keys, the best of which is taken and replaced by its thread's next
       __syncthreads();
-      if (sh.count <= kList) break;
-      __syncthreads();
-      if (tid == 0) sh.count = held;
-      if (attempt == 0) {
-        // again, with this chunk's own threshold where it is the higher one
-        const float own_th = chunk_threshold(sh, tmax, p.top_k);
-        if (!(own_th < th) || !cut) {
-          if (!(strict && own_th == th)) strict = false;
-          th = own_th;
-        }
-        if (cut && tid == 0) sh.threshold = old_th;
-        __syncthreads();
-        continue;
+      unsigned long long mine = 0;
+      for (int t = warp * 32; t < warp * 32 + 32; ++t) {
+        const unsigned long long k = next_key(x, t, first, last, ~0ull);
+        if (t == tid) mine = k;
       }
-      // top_k searches for the largest key below the last one found, among the list and the chunk
-      unsigned long long below = ~0ull;
-      __syncthreads();
       for (int k = 0; k < p.top_k; ++k) {
-        unsigned long long mine = 0;
-        for (int i = tid; i < held; i += kThreads)
-          if (sh.list[i] < below && sh.list[i] > mine) mine = sh.list[i];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int col = col0 + (i / N) * kThreads * N + i % N;
-          if (col >= 0 && col < p.vocab) {
-            const unsigned long long key = key_of(xs[i], col);
-            if (key < below && key > mine) mine = key;
-          }
-        }
+        unsigned long long b = mine;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
-          const unsigned long long u = __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-          mine = u > mine ? u : mine;
+          const unsigned long long u = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+          b = u > b ? u : b;
         }
-        if (lane == 0) sh.red[warp] = mine;
+        const unsigned long long warp_best = b;
+        if (lane == 0) sh.red[warp] = b;
         __syncthreads();
-        below = sh.red[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) below = sh.red[w] > below ? sh.red[w] : below;
-        if (tid == 0) sh.best[k] = below;
+        for (int w = 0; w < kWarps; ++w) b = sh.red[w] > b ? sh.red[w] : b;
+        if (tid == 0) sh.best[k] = b;
+        if (warp_best == b) {  // this warp's thread holds it: keys are distinct (more than top_k numbers, so none is 0)
+          const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, mine == b)) - 1;
+          const unsigned long long next = next_key(x, warp * 32 + owner, first, last, b);
+          if (lane == owner) mine = next;
+        }
         __syncthreads();
       }
-      if (tid < p.top_k) sh.list[tid] = sh.best[tid];
-      if (tid == 0) sh.count = p.top_k;  // more than kList numbers passed, so there are top_k
+      if (tid == 0) sh.count = p.top_k;
       __syncthreads();
-      break;
     }
-    if (!cut || sh.count > kCutAt) {
-      __syncthreads();
-      cut_back(sh, p.top_k);
-      cut = sh.count == p.top_k;
-    }
-  }
-  if (p.top_k) {
-    __syncthreads();
-    cut_back(sh, p.top_k);
   }
 
-  // the block's sums
+  // ---- the block's sums
 #pragma unroll
   for (int o = 16; o; o >>= 1)
     acc = join(acc, Sums{__shfl_xor_sync(0xFFFFFFFFu, acc.r, o), __shfl_xor_sync(0xFFFFFFFFu, acc.s, o),
@@ -320,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
 
   if (p.splits > 1) {
     const int64_t at = row * p.splits + split;
-    if (tid < p.top_k) p.keys[at * p.top_k + tid] = tid < sh.count ? sh.list[tid] : 0ull;
+    if (tid < p.top_k) p.keys[at * p.top_k + tid] = tid < sh.count ? sh.best[tid] : 0ull;
     if (tid == 0) *reinterpret_cast<float4*>(p.sums + at * 4) = make_float4(acc.r, acc.s, acc.t, 0.f);
     __syncthreads();
     if (tid == 0) {
@@ -337,17 +406,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + (row * p.splits + i) * 4));
       acc = join(acc, Sums{v.x, v.y, v.z}, p.c);
     }
-    if (p.top_k) {
-      const int total = p.splits * p.top_k;
-      for (int base = 0; base < total; base += kList - kMaxTop) {  // as many as fit at a time
-        const int n = total - base < kList - kMaxTop ? total - base : kList - kMaxTop;
-        for (int i = tid; i < n; i += kThreads) {
-          const unsigned long long key = __ldcg(p.keys + row * total + base + i);
-          if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
-        }
-        __syncthreads();
-        cut_back(sh, p.top_k);
+    const int total = p.splits * p.top_k;
+    for (int base = 0; base < total; base += kList - kMaxTop) {  // as many as fit beside the best so far
+      const int held = sh.count;
+      if (tid < held) sh.list[tid] = sh.best[tid];
+      __syncthreads();
+      const int n = total - base < kList - kMaxTop ? total - base : kList - kMaxTop;
+      for (int i = tid; i < n; i += kThreads) {
+        const unsigned long long key = __ldcg(p.keys + row * total + base + i);
+        if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
       }
+      __syncthreads();
+      cut_back(sh, p.top_k);
     }
   }
 
@@ -359,35 +429,42 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
   }
   const auto logprob = [&](float v) { return none ? -INFINITY : __fmaf_rn(v - acc.r, p.inv_t, -lns); };
   if (tid < p.top_k) {
-    const unsigned long long key = sh.list[tid];
+    const unsigned long long key = sh.best[tid];
     p.top_ids[row * p.top_k + tid] = (int32_t)~(uint32_t)key;
     p.top_logprobs[row * p.top_k + tid] = logprob(from_order_bits((uint32_t)(key >> 32)));
   }
   for (int i = tid; i < p.cands; i += kThreads) {
     const int32_t tok = p.tokens[row * p.cands + i];
-    p.logprobs[row * p.cands + i] = tok >= 0 && tok < p.vocab ? logprob(Vec<T>::one(x + tok)) : -INFINITY;
+    p.logprobs[row * p.cands + i] = tok >= 0 && tok < p.vocab ? logprob(Vec<T>::one(x.x + tok)) : -INFINITY;
   }
 }
 
-// Blocks of a row: as many as make six blocks per SM over all rows, at most one per chunk.
-int splits_of(int n, int chunks) {
-  const int64_t want = 6 * (int64_t)device_sm_count();
-  int64_t s = (want + n - 1) / n;
-  if (s > chunks) s = chunks;
-  if (s > 64) s = 64;
+// Blocks of a row: as many as the GPU holds at a time over all rows, each thread with one vector at least.  At 256
+// rows of 151936 bf16 that is two; three do not all fit at a time.
+int splits_of(int n, int vocab, int per_vec) {
+  int64_t s = kPerSM * (int64_t)device_sm_count() / n;
+  const int64_t most = (vocab + per_vec * kThreads - 1) / (per_vec * kThreads);
+  if (s > most) s = most;
+  if (s > kMaxSplits) s = kMaxSplits;
   if (n > kCounters) s = 1;
   return s < 1 ? 1 : (int)s;
 }
-// A row may start up to 15 bytes into its first vector: seven bf16 columns more.
-int chunks_of(int vocab, int per_chunk) { return (vocab + 7 + per_chunk - 1) / per_chunk; }
 
 }  // namespace
 
-// Counters (always as many, so that a workspace serves calls of any sizes), sums [n][splits][4], keys [n][splits][top_k], for the larger split count of the two types.
+// Counters (always as many, so that a workspace serves calls of any sizes), sums [n][splits][4], keys
+// [n][splits][top_k], for the larger split count of the two types.
 size_t logprobs_workspace_bytes(int n, int vocab, int top_k) {
-  const int64_t most = chunks_of(vocab, kThreads * kVecs * 4), splits = most < 64 ? most : 64;
-  const int64_t rows = n < kCounters ? n : kCounters;  // only split rows use it
-  return (size_t)(kCounters * 4 + rows * splits * 16 + (rows * splits * top_k * 8 + 15) / 16 * 16);
+  size_t most = 0;
+  // fewer rows have more splits each: a workspace for n rows serves fewer too
+  for (int per_vec = 4; per_vec <= 8; per_vec += 4) {
+    const int64_t one = splits_of(1, vocab, per_vec);
+    const int64_t all = kPerSM * (int64_t)device_sm_count();  // rows * splits, where rows are split at all
+    const int64_t parts = one * n < all ? one * n : all;
+    const size_t b = (size_t)(kCounters * 4 + parts * 16 + (parts * top_k * 8 + 15) / 16 * 16);
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t row_stride, const int32_t* tokens, int n,
@@ -401,13 +478,12 @@ cudaError_t launch_token_logprobs(const void* logits, int dtype, int64_t row_str
   p.n = n; p.vocab = vocab; p.cands = cands; p.top_k = top_k;
   p.c = kLog2e / temperature;
   p.inv_t = 1.f / temperature;
-  p.chunks = chunks_of(vocab, kThreads * kVecs * (dtype == TRELLIS_BF16 ? 8 : 4));
-  p.splits = splits_of(n, p.chunks);
+  p.splits = splits_of(n, vocab, dtype == TRELLIS_BF16 ? 8 : 4);
   char* w = static_cast<char*>(workspace);
   p.counter = reinterpret_cast<uint32_t*>(w);
   w += kCounters * 4;
   p.sums = reinterpret_cast<float*>(w);
-  w += (int64_t)(n < kCounters ? n : kCounters) * p.splits * 16;
+  w += p.splits > 1 ? (int64_t)n * p.splits * 16 : 0;
   p.keys = reinterpret_cast<unsigned long long*>(w);
   const int64_t kMaxRows = 65535;  // rows of one launch (a grid's y)
   for (int64_t r0 = 0; r0 < n; r0 += kMaxRows) {
