@@ -127,6 +127,20 @@ __device__ __forceinline__ bool bar_and(bool v, int id, int count) {
   return r != 0;
 }
 
+// OR of v, likewise; also a barrier (and memory ordering) among the group.
+__device__ __forceinline__ bool bar_or(bool v, int id, int count) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q, o;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "barrier.red.or.pred o, %2, %3, q;\n\t"
+      "selp.u32 %0, 1, 0, o;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Shared-memory address of the same object in CTA `rank` of the cluster.

@@ -15,6 +15,7 @@
 // Bound: HBM (the cache is read once per 64 rows; other row blocks of the head find it in L2), down to the latency of
 // a launch and a join for short contexts.
 #include <cstring>
+#include <type_traits>
 #include <cuda.h>
 
 #include "common.cuh"
@@ -168,11 +169,14 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           y = (((page * 2) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         }
         const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        bool ok = true;
-        if (it >= C::Stages && !dead) ok = tc::mbar_wait_short(empty + s, (uint32_t)((it / C::Stages) & 1) ^ 1u, p.wait_ns);
-        if (!__all_sync(0xFFFFFFFFu, ok) && !dead) {
-          dead = true;
-          if (lane == 0) flags[0] = 1;
+        if (it >= C::Stages && !dead) {
+          const bool ok = tc::mbar_wait_short(empty + s, (uint32_t)((it / C::Stages) & 1) ^ 1u, p.wait_ns);
+          // A consumer that gave up releases tiles it never saw, perhaps before they landed: its flag, set before its
+          // arrival, ends the copying too, since a barrier must not be armed again while its copies are in flight.
+          if (__any_sync(0xFFFFFFFFu, !ok || flags[0] != 0)) {
+            dead = true;
+            if (lane == 0) flags[0] = 1;
+          }
         }
         if (dead) continue;  // the consumers' waits run out too; what is in flight lands below
         issued = it + 1;
@@ -280,9 +284,11 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
       // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
       constexpr float kLift = F8 ? 15.f : 0.f;
 
-      for (int t = 0; t < g.tiles; ++t, ++it) {
+      // One tile.  TAIL: drafts, or rows past the sequence's end, are among its keys.
+      const auto step = [&](int t, auto tail) {
+        constexpr bool TAIL = decltype(tail)::value;
         const int s = it % C::Stages;
-        bool ok = dead || tc::mbar_wait_short(full + s, (uint32_t)((it / C::Stages) & 1), p.wait_ns);
+        const bool ok = dead || tc::mbar_wait_short(full + s, (uint32_t)((it / C::Stages) & 1), p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, ok) && !dead) {
           dead = true;
           if (lane == 0) flags[0] = 1;
@@ -290,7 +296,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
         const uint32_t sk = tc::smem_u32(stages + s * C::Stage), sv = sk + C::HalfStage;
         const int key0 = wk * C::KW;                       // this warp's keys of the tile
         const int pos0 = (g.tile0 + t) * kTile + key0;      // their positions
-        const bool tail = pos0 + C::KW > g.seq.prefix;      // drafts, or past the end, among them
 
         // ---- scores
         float x[C::KW / 8][4];
@@ -341,8 +346,8 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float v = x[i][j] * rc[j >> 1];
-            if (tail) {
-              const int pos = pos0 + i * 8 + c4 * 2 + (j & 1), jd = pos - g.seq.prefix;
+            if constexpr (TAIL) {
+              const int jd = pos0 + i * 8 + c4 * 2 + (j & 1) - g.seq.prefix;
               const bool vis = jd < 0 || (jd < g.seq.count && ((seen[j >> 1] >> jd) & 1ull));
               v = vis ? v : -INFINITY;
             }
@@ -381,21 +386,57 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           pa[i >> 1][(i & 1) * 2 + 1] = F8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
         }
 
+        if constexpr (TAIL) {
+          // Values that must not reach a product: rows past the end, whatever their bits, become zeros; drafts with
+          // numbers that are not finite (rare) are added to the rows that see them, and become zeros there too.
+          uint8_t* tile = stages + s * C::Stage + C::HalfStage;
+          const int base_pos = (g.tile0 + t) * kTile, from = max(g.seq.prefix - base_pos, 0);
+          constexpr uint32_t kExp = F8 ? 0x7Fu : 0x7F80u;  // bits that are all ones in what is not finite
+          constexpr int Chunks = C::RowBytes / 16;
+          const auto not_finite = [&](uint32_t w) {
+            if constexpr (F8) return (w & 0x7Fu) == 0x7Fu || (w >> 8 & 0x7Fu) == 0x7Fu || (w >> 16 & 0x7Fu) == 0x7Fu || (w >> 24 & 0x7Fu) == 0x7Fu;
+            else return (w & kExp) == kExp || (w >> 16 & kExp) == kExp;
+          };
+          bool odd = false;
+          for (int e = from * Chunks + threadIdx.x; e < kTile * Chunks; e += nthr) {
+            const int row = e / Chunks;
+            uint4* at = reinterpret_cast<uint4*>(tile + tile_at<C>(row, e - row * Chunks));
+            if (base_pos + row >= len) *at = make_uint4(0, 0, 0, 0);
+            else odd |= not_finite(at->x) || not_finite(at->y) || not_finite(at->z) || not_finite(at->w);
+          }
+          if (tc::bar_or(odd, 1, nthr)) {
+            for (int kk = 0; kk < C::KW; ++kk) {
+              const int jd = pos0 + kk - g.seq.prefix;
+              if (jd < 0 || jd >= g.seq.count) continue;
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int d = F8 ? (i >> 1) * 16 + c4 * 4 + (j & 1) * 2 + (i & 1) : i * 8 + c4 * 2 + (j & 1);
+                  const int byte = F8 ? d : 2 * d;
+                  const uint8_t* at = tile + tile_at<C>(key0 + kk, byte >> 4) + (byte & 15);
+                  const uint32_t v = F8 ? *at : *reinterpret_cast<const uint16_t*>(at);
+                  if ((v & kExp) == kExp && ((seen[j >> 1] >> jd) & 1ull))
+                    o[i][j] += F8 ? __int_as_float(0x7FC00000) : bf16_to_f32((uint16_t)v);
+                }
+            }
+            named_sync(1, nthr);
+            for (int e = from * Chunks * 16 + threadIdx.x * 2; e < kTile * Chunks * 16; e += nthr * 2) {
+              const int row = e / (Chunks * 16), byte = e - row * (Chunks * 16);
+              uint16_t* at = reinterpret_cast<uint16_t*>(tile + tile_at<C>(row, byte >> 4) + (byte & 15));
+              const uint32_t v = *at;
+              if constexpr (F8) *at = (uint16_t)(((v & 0x7Fu) == 0x7Fu ? 0 : v & 0xFFu) | ((v >> 8 & 0x7Fu) == 0x7Fu ? 0 : v & 0xFF00u));
+              else if ((v & kExp) == kExp) *at = 0;
+            }
+            named_sync(1, nthr);
+          }
+          tc::fence_proxy_async_smem();  // before the next copy into this tile
+        }
+
         // ---- outputs
-        constexpr uint32_t kExp = F8 ? 0x7C00u : 0x7F80u;  // all ones: infinite or NaN
-        bool odd = false;  // a draft with numbers that are not finite
 #pragma unroll
         for (int kb = 0; kb < C::KW / 16; ++kb) {
           const int row = key0 + kb * 16 + (lane & 15);
-          // in a tail tile: rows past the end count as zeros whatever their bits; drafts that are not finite are left
-          // to the rows that see them
-          const auto clean = [&](uint32_t& v, int half) {
-            const int pos = pos0 + kb * 16 + half * 8 + c4 * 2;
-            if (pos >= len) v = 0;
-            else if (pos + 1 >= len) v &= 0xFFFFu;
-            if (pos >= g.seq.prefix && (v & kExp) == kExp) { v &= 0xFFFF0000u; odd = true; }
-            if (pos + 1 >= g.seq.prefix && (v >> 16 & kExp) == kExp) { v &= 0xFFFFu; odd = true; }
-          };
 #pragma unroll
           for (int dc = 0; dc < C::RowBytes / 16; dc += 2) {
             uint32_t r[4];
@@ -403,39 +444,24 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
             if constexpr (F8) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) {  // chunk dc + j: its even columns, then its odd ones
-                uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4420)), e1 = e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4420));
-                uint32_t o0 = e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4431)), o1 = e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4431));
-                if (tail) { clean(e0, 0); clean(e1, 1); clean(o0, 0); clean(o1, 1); }
-                mma16816<true>(o[2 * (dc + j)], pa[kb], e0, e1);
-                mma16816<true>(o[2 * (dc + j) + 1], pa[kb], o0, o1);
+                mma16816<true>(o[2 * (dc + j)], pa[kb], e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4420)),
+                               e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4420)));
+                mma16816<true>(o[2 * (dc + j) + 1], pa[kb], e4m3x2_to_f16x2(__byte_perm(r[2 * j], 0, 0x4431)),
+                               e4m3x2_to_f16x2(__byte_perm(r[2 * j + 1], 0, 0x4431)));
               }
             } else {
-              if (tail) { clean(r[0], 0); clean(r[1], 1); clean(r[2], 0); clean(r[3], 1); }
               mma16816<false>(o[dc], pa[kb], r[0], r[1]);
               mma16816<false>(o[dc + 1], pa[kb], r[2], r[3]);
             }
           }
         }
-        if (tail && __any_sync(0xFFFFFFFFu, odd)) {
-          // infinities and NaN of a draft reach the rows that see it, and no others
-          for (int kk = 0; kk < C::KW; ++kk) {
-            const int jd = pos0 + kk - g.seq.prefix;
-            if (jd < 0 || jd >= g.seq.count) continue;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int d = F8 ? (i >> 1) * 16 + c4 * 4 + (j & 1) * 2 + (i & 1) : i * 8 + c4 * 2 + (j & 1);
-                const int byte = F8 ? d : 2 * d;
-                const uint8_t* at = stages + s * C::Stage + C::HalfStage + tile_at<C>(key0 + kk, byte >> 4) + (byte & 15);
-                const uint32_t v = F8 ? e4m3x2_to_f16x2(*at) & 0xFFFFu : *reinterpret_cast<const uint16_t*>(at);
-                if ((v & kExp) == kExp && ((seen[j >> 1] >> jd) & 1ull)) o[i][j] += F8 ? f16_to_f32((uint16_t)v) : bf16_to_f32((uint16_t)v);
-              }
-          }
-        }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty + s);
-      }
+        ++it;
+      };
+      const int clear = min(g.tiles, max(0, g.seq.prefix / kTile - g.tile0));  // tiles of prefix alone
+      for (int t = 0; t < clear; ++t) step(t, std::false_type{});
+      for (int t = clear; t < g.tiles; ++t) step(t, std::true_type{});
 
       // ---- the segment's end: sums over the lanes of a row, then over the warps that share rows
 #pragma unroll
