@@ -15,7 +15,6 @@
 // Bound: HBM (the cache is read once per 64 rows; other row blocks of the head find it in L2), down to the latency of
 // a launch and a join for short contexts.
 #include <cstring>
-#include <type_traits>
 #include <cuda.h>
 
 #include "common.cuh"
@@ -284,9 +283,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
       // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
       constexpr float kLift = F8 ? 15.f : 0.f;
 
-      // One tile.  TAIL: drafts, or rows past the sequence's end, are among its keys.
-      const auto step = [&](int t, auto tail) {
-        constexpr bool TAIL = decltype(tail)::value;
+      const int clear = g.seq.prefix / kTile - g.tile0;  // tiles from here on have drafts, or rows past the end, among their keys
+      for (int t = 0; t < g.tiles; ++t, ++it) {
+        const bool tail = t >= clear;
         const int s = it % C::Stages;
         const bool ok = dead || tc::mbar_wait_short(full + s, (uint32_t)((it / C::Stages) & 1), p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, ok) && !dead) {
@@ -344,16 +343,20 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
 #pragma unroll
         for (int i = 0; i < C::KW / 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float v = x[i][j] * rc[j >> 1];
-            if constexpr (TAIL) {
+          for (int j = 0; j < 4; ++j) x[i][j] *= rc[j >> 1];
+        if (tail)
+#pragma unroll
+          for (int i = 0; i < C::KW / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
               const int jd = pos0 + i * 8 + c4 * 2 + (j & 1) - g.seq.prefix;
               const bool vis = jd < 0 || (jd < g.seq.count && ((seen[j >> 1] >> jd) & 1ull));
-              v = vis ? v : -INFINITY;
+              x[i][j] = vis ? x[i][j] : -INFINITY;
             }
-            x[i][j] = v;
-            mx[j >> 1] = fmaxf(mx[j >> 1], v);
-          }
+#pragma unroll
+        for (int i = 0; i < C::KW / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j >> 1] = fmaxf(mx[j >> 1], x[i][j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], 1));
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           pa[i >> 1][(i & 1) * 2 + 1] = F8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
         }
 
-        if constexpr (TAIL) {
+        if (tail) {
           // Values that must not reach a product: rows past the end, whatever their bits, become zeros; drafts with
           // numbers that are not finite (rare) are added to the rows that see them, and become zeros there too.
           uint8_t* tile = stages + s * C::Stage + C::HalfStage;
@@ -457,11 +460,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty + s);
-        ++it;
-      };
-      const int clear = min(g.tiles, max(0, g.seq.prefix / kTile - g.tile0));  // tiles of prefix alone
-      for (int t = 0; t < clear; ++t) step(t, std::false_type{});
-      for (int t = clear; t < g.tiles; ++t) step(t, std::true_type{});
+      }
 
       // ---- the segment's end: sums over the lanes of a row, then over the warps that share rows
 #pragma unroll
@@ -509,32 +508,32 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
 
       // an output fragment, already joined, to the outputs
       const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
+      uint16_t* to[2];     // this lane's rows in the outputs
+      int64_t to_lse[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = wr * 16 + gq + 8 * half, d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+        to[half] = r < rows ? p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D : nullptr;
+        to_lse[half] = (int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh;
+      }
       const auto store = [&](const float (&v)[4], int i, const float (&fl)[2]) {  // i: output fragment
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int r = wr * 16 + gq + 8 * half;
-          if (r >= rows) continue;
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
-          uint16_t* at = p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D;
+          if (!to[half]) continue;
           if constexpr (F8) {
             const int col = (i >> 1) * 16 + c4 * 4 + (i & 1);
-            at[col] = f32_to_bf16_rn(v[2 * half] * fl[half]);
-            at[col + 2] = f32_to_bf16_rn(v[2 * half + 1] * fl[half]);
+            to[half][col] = f32_to_bf16_rn(v[2 * half] * fl[half]);
+            to[half][col + 2] = f32_to_bf16_rn(v[2 * half + 1] * fl[half]);
           } else {
-            *reinterpret_cast<uint32_t*>(at + i * 8 + c4 * 2) = pack_bf16x2(v[2 * half] * fl[half], v[2 * half + 1] * fl[half]);
+            *reinterpret_cast<uint32_t*>(to[half] + i * 8 + c4 * 2) = pack_bf16x2(v[2 * half] * fl[half], v[2 * half + 1] * fl[half]);
           }
         }
       };
       const auto store_lse = [&](const float (&mm)[2], const float (&ll)[2]) {
         if (!p.lse || c4 != 0) return;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = wr * 16 + gq + 8 * half;
-          if (r >= rows) continue;
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
-          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] =
-              ll[half] == 0.f ? -INFINITY : kLn2 * (mm[half] + (log2f(ll[half]) - kLift));
-        }
+        for (int half = 0; half < 2; ++half)
+          if (to[half]) p.lse[to_lse[half]] = ll[half] == 0.f ? -INFINITY : kLn2 * (mm[half] + (log2f(ll[half]) - kLift));
       };
       if (g.first == g.last) {
         if (wk == 0) {
