@@ -31,6 +31,7 @@ namespace {
 __device__ int g_tree_error = 0;  // set when a bounded wait gives up (trellis_device_error)
 
 constexpr uint64_t kDrainNs = 2000000000ull;  // for copies in flight when a block leaves
+constexpr int kTile = 64;  // keys per step
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     tc::fence_mbar_init();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<ROWS>(p, cum);
+  if (warp == 0) tree_cumulate<ROWS, kTile>(p, cum);
   __syncthreads();
   const int total = cum[p.batch];
   const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     // ---- the copying warp: every tile of the range, as many ahead as there are stages
     int it = 0, issued = 0;
     bool dead = false;
-    while (walk.next<ROWS>(p, cum, total, ctas, g)) {
+    while (walk.next<kTile>(p, cum, total, ctas, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const int box = p.page_shift < 6 ? 1 << p.page_shift : kTile;  // rows of one copy
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     const int nthr = C::Consumers * 32;
     int it = 0;
     bool dead = false;
-    while (walk.next<ROWS>(p, cum, total, ctas, g)) {
+    while (walk.next<kTile>(p, cum, total, ctas, g)) {
       const int rows = min(ROWS, g.seq.count * p.group - g.row_block * ROWS);  // rows of this block that exist
       const int row0 = g.row_block * ROWS;
       named_sync(1, nthr);  // the previous segment's queries are no longer read
@@ -638,7 +639,9 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int rows, cuda
 
 size_t tree_workspace_bytes(const trellis_cache_t& c, int batch, int max_tokens, int q_heads) {
   (void)batch;  // parts belong to thread blocks, whatever the batch
-  const size_t part = (size_t)(rows_of(max_tokens, q_heads / c.heads) / 16) * (c.head_dim / 2 + 4) * 32 * 4;
+  const int group = q_heads / c.heads;
+  const size_t part = tree_tc_fits(c, max_tokens * group) ? tree_tc_part_bytes(c)
+                                                          : (size_t)(rows_of(max_tokens, group) / 16) * (c.head_dim / 2 + 4) * 32 * 4;
   return kTreeMaxCtas * 4 + part * 2 * tree_ctas();
 }
 
@@ -649,7 +652,8 @@ int read_tree_error(int reset) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_tree_error, &zero, sizeof(int)) != cudaSuccess) return -1;
   }
-  return v;
+  const int w = read_tree_tc_error(reset);
+  return v ? v : w;
 }
 
 cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,
@@ -666,26 +670,27 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   p.hq = q_heads; p.hkv = c.heads; p.group = q_heads / c.heads;
   p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   const int rows = rows_of(d.max_tokens, p.group);
-  p.row_blocks = (d.max_tokens * p.group + rows - 1) / rows;
   p.scale_log2 = scale * kLog2e;
   p.counter = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kTreeMaxCtas * 4);
 
   const auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
-  const bool f8 = c.dtype == TRELLIS_E4M3;
+  const bool f8 = c.dtype == TRELLIS_E4M3, tc = tree_tc_fits(c, d.max_tokens * p.group);
   const int elem = (int)cache_elem_bytes(c), row_bytes = c.head_dim * elem, inner = row_bytes < 128 ? row_bytes : 128;
   uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
   // the layer's rows of head_dim numbers; a copy takes up to 128 bytes of each of one page's rows (at most a tile)
   CUtensorMap map;
   const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.pages * 2 * c.heads * c.page_size)};
   const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)(inner / elem), (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile)};
+  const cuuint32_t box[2] = {(cuuint32_t)(inner / elem), (cuuint32_t)(tc ? tree_tc_box_rows(c) : c.page_size < kTile ? c.page_size : kTile)};
   const cuuint32_t estr[2] = {1, 1};
   if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
+  p.pool = reinterpret_cast<const uint16_t*>(pool);
+  if (tc) return launch_tree_tc(map, p, c.head_dim, tree_ctas(), st);
   if (f8) {
     if (c.head_dim == 64) return launch_d<64, true>(map, p, rows, st);
     if (c.head_dim == 128) return launch_d<128, true>(map, p, rows, st);

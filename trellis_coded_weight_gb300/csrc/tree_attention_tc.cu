@@ -1,0 +1,656 @@
+// tree_attention_tc.cu -- tree attention with the 5th-generation tensor cores, for more rows per key/value head than
+// tree_attention.cu handles at the rate of HBM.
+//
+// The mathematics is that of tree_attention.cu.  A block takes up to 256 rows of one key/value head and 128 keys per
+// step; both products are 128 x N tcgen05 MMAs of one issuing thread with accumulators in tensor memory:
+//   S = Q K^T    Q and K in shared memory (128-byte swizzle, along the head dim)
+//   O += P V     P in tensor memory over the scores it was made of, V in shared memory (swizzled, along the head dim too)
+// Two softmax warpgroups, one thread per row, each own a stream of steps with its own S, O, maximum and sum:
+//   up to 128 rows     both streams have the same rows and alternate between the tiles of keys, and are joined at the end
+//   up to 256 rows     each has 128 of the rows, and both take every tile
+// so that one stream's products run while the other's softmax does.  A stream's maximum is only moved when it has grown by
+// more than 2^8: the weights then stay below 2^8, well inside bf16 and fp32, and O is rarely rescaled.
+// Keys and values arrive by TMA in a ring of tiles in the order of their use.
+#include <cstring>
+#include <cuda.h>
+
+#include "common.cuh"
+#include "devcache.h"
+#include "launch.h"
+#include "pdl.cuh"
+#include "serving.h"
+#include "tc_ptx.cuh"
+#include "tree_sched.cuh"
+
+namespace trellis {
+namespace {
+
+__device__ int g_tree_tc_error = 0;  // set when a bounded wait gives up (trellis_device_error)
+
+constexpr uint64_t kDrainNs = 2000000000ull;  // for copies and products in flight when a block leaves
+constexpr int kTile = 128;                    // keys per step
+constexpr int kRows = 256;                    // rows of a block
+constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 320;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kMove = 8.f;                  // log2 of the growth that moves a row's maximum
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// This warp's 32 lanes x 16 (32) consecutive columns from registers.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Operand whose rows are the reduction index (values: [key][head dim]) in the 128-byte swizzle: 64 numbers of a row
+// are contiguous; `lbo` bytes from one such block of columns to the next, 1024 bytes from 8 rows to the next 8.
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kBMnMajor = 1u << 16;  // instruction descriptor: B's rows are the reduction index
+
+template <int D>
+struct Cfg {
+  static constexpr int Blocks = D / 64;                     // 128-byte blocks of a row
+  static constexpr int Slot = kTile * D * 2;                // the keys, or the values, of a tile
+  static constexpr int QTile = 128 * D * 2;
+  static constexpr int Fixed = 2 * QTile + kRows * 8 + 4 * 128 * 4 + (kTreeMaxBatch + 4) * 4 + 512;
+  static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Slot;
+  static constexpr int Slots = Fit > 8 ? 8 : Fit;
+  static_assert(Slots >= 4, "keys and values of two tiles");
+  static constexpr int Smem = 1024 + Slots * Slot + Fixed;
+  static constexpr int PartFloats = kRows * (D + 2);        // a part: [D/4][256 rows][4], maxima, sums
+  // tensor memory columns
+  static constexpr int S(int s) { return s * 128; }
+  static constexpr int O(int s) { return 256 + s * 128; }
+};
+
+// Ring positions of tile i's keys and values among a segment's 2n entries, in the order in which they are used.
+struct Order {
+  int n;
+  bool split_keys;
+  __device__ __forceinline__ int key(int i) const { return !split_keys ? 2 * i : i < 2 ? i : 2 * i - 1; }
+  __device__ __forceinline__ int value(int i) const { return !split_keys ? 2 * i + 1 : i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
+  // entry e: tile and kind
+  __device__ __forceinline__ int at(int e, bool* is_value) const {
+    if (!split_keys) {
+      *is_value = e & 1;
+      return e >> 1;
+    }
+    if (e < 2 && e < n) { *is_value = false; return e; }
+    if (e == 2 * n - 1) { *is_value = true; return n - 1; }
+    *is_value = !(e & 1);
+    return e & 1 ? (e + 1) / 2 : (e - 2) / 2;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = base;
+  uint8_t* sq = ring + C::Slots * C::Slot;
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(sq + 2 * C::QTile);
+  float* row_stat = reinterpret_cast<float*>(row_mask + kRows);  // [stream][maximum, sum][128]
+  int* cum = reinterpret_cast<int*>(row_stat + 4 * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(cum + kTreeMaxBatch + 4);
+  uint64_t* empty = full + C::Slots;
+  uint64_t* q_ready = empty + C::Slots;
+  uint64_t* s_full = q_ready + 1;  // [2] scores there; also: the stream's products before them are complete
+  uint64_t* p_ready = s_full + 2;  // [2] weights written, values clean
+  uint64_t* o_full = p_ready + 2;  // [2] the segment's last product complete
+  uint64_t* drained = o_full + 2;
+  volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] a wait gave up, [1] last to arrive, [2] segment with odd values
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::prefetch_tmap(&map);
+    for (int i = 0; i < C::Slots; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, 1);
+    }
+    tc::mbar_init(q_ready, kSoftmaxWarps);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(s_full + s, 1);
+      tc::mbar_init(p_ready + s, kSoftmaxWarps / 2);
+      tc::mbar_init(o_full + s, 1);
+    }
+    tc::mbar_init(drained, 1);
+    flags[0] = 0;
+    flags[2] = -1;
+    tc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  pdl_enter();
+  if (warp == 0) tree_cumulate<kRows, kTile>(p, cum);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int total = cum[p.batch];
+  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x;
+  const int cta = blockIdx.x;
+  TreeWalk walk(total, ctas < 1 ? 1 : ctas, cta);
+  if (cta >= ctas) walk.at = walk.end = 0;  // fewer steps than blocks
+  TreeSegment g;
+  const auto rows_of = [&](const TreeSegment& x) { return min(kRows, x.seq.count * p.group - x.row_block * kRows); };
+
+  if (warp == kCopyWarp) {
+    // ---- the copying warp
+    int it = 0;
+    bool dead = false;
+    const int box = min(1 << p.page_shift, kTile);  // rows of one copy
+    while (!dead && walk.next<kTile>(p, cum, total, ctas, g)) {
+      const int32_t* row = p.table + (int64_t)g.b * p.width;
+      const int len = g.seq.prefix + g.seq.count;
+      const Order order{g.tiles, rows_of(g) <= 128};
+      for (int e = 0; e < 2 * g.tiles && !dead; ++e, ++it) {
+        bool value;
+        const int t = order.at(e, &value);
+        const int s = it % C::Slots;
+        const int pos = (g.tile0 + t) * kTile + lane * box;  // lane i copies box i of the tile, none past the end
+        const bool mine = lane * box < kTile && pos < len;
+        int y = 0;
+        if (mine) {
+          int page = __ldg(row + (pos >> p.page_shift));
+          page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+          y = (((page * 2 + (value ? 1 : 0)) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+        }
+        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        if (it >= C::Slots) {
+          const bool ok = tc::mbar_wait_short(empty + s, (uint32_t)((it / C::Slots) & 1) ^ 1u, p.wait_ns);
+          if (__any_sync(0xFFFFFFFFu, !ok)) {
+            dead = true;
+            if (lane == 0) flags[0] = 1;
+            break;
+          }
+        }
+        if (lane == 0) tc::mbar_arrive_expect_tx(full + s, (uint32_t)(boxes * box * D * 2));
+        __syncwarp();
+        if (mine)
+#pragma unroll
+          for (int blk = 0; blk < C::Blocks; ++blk)
+            tc::tma_load_2d(ring + s * C::Slot + blk * (kTile * 128) + lane * box * 128, &map, full + s, blk * 64, y);
+      }
+    }
+    // no copy may land in a block that has left
+    for (int i = it > C::Slots ? it - C::Slots : 0; i < it; ++i) tc::mbar_wait(full + i % C::Slots, (uint32_t)((i / C::Slots) & 1), kDrainNs);
+  } else if (warp == kMmaWarp) {
+    // ---- the thread that issues the products
+    if (lane == 0) {
+      bool dead = false;
+      bool issued = false;
+      int it0 = 0, seg = 0, ns[2] = {0, 0};
+      const auto wait = [&](uint64_t* bar, int count) {  // the count-th completion (from 0)
+        if (!dead && !tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns)) {
+          dead = true;
+          flags[0] = 1;
+        }
+        return !dead;
+      };
+      const uint32_t ring32 = tc::smem_u32(ring), q32 = tc::smem_u32(sq);
+      const uint32_t id_s = tc::idesc_bf16_f32(128, kTile), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
+      const auto slot_of = [&](int e) { return (it0 + e) % C::Slots; };
+      const auto wait_entry = [&](int e) { return wait(full + slot_of(e), (it0 + e) / C::Slots); };
+      const auto release = [&](int e) { tc::mma_commit(empty + slot_of(e)); };
+      const auto scores = [&](int s, int qtile, int e) {
+        const uint64_t a = tc::desc_kmajor(q32 + qtile * C::QTile, 1024, 2), b = tc::desc_kmajor(ring32 + slot_of(e) * C::Slot, 1024, 2);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
+          tc::mma_bf16(tmem + C::S(s), a + step, b + step, id_s, k > 0);
+        }
+        tc::mma_commit(s_full + s);
+        issued = true;
+      };
+      const auto outputs = [&](int s, int e, bool fresh) {
+        const uint64_t b = desc_mnmajor(ring32 + slot_of(e) * C::Slot, kTile * 128);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint64_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
+      };
+      while (!dead && walk.next<kTile>(p, cum, total, ctas, g)) {
+        const int n = g.tiles;
+        const Order order{n, rows_of(g) <= 128};
+        if (!wait(q_ready, seg)) break;
+        tc::fence_after_sync();
+        if (order.split_keys) {
+          for (int i = 0; i < 2 && i < n; ++i) {
+            if (!wait_entry(order.key(i))) break;
+            scores(i, 0, order.key(i));
+            release(order.key(i));
+          }
+          for (int i = 0; i < n && !dead; ++i) {
+            const int s = i & 1;
+            if (!wait_entry(order.value(i)) || !wait(p_ready + s, ns[s]++)) break;
+            tc::fence_after_sync();
+            outputs(s, order.value(i), i < 2);
+            release(order.value(i));
+            if (i + 2 >= n) tc::mma_commit(o_full + s);
+            if (i + 2 < n) {
+              if (!wait_entry(order.key(i + 2))) break;
+              scores(s, 0, order.key(i + 2));
+              release(order.key(i + 2));
+            }
+          }
+        } else {
+          if (!wait_entry(order.key(0))) break;
+          scores(0, 0, order.key(0));
+          scores(1, 1, order.key(0));
+          release(order.key(0));
+          for (int i = 0; i < n && !dead; ++i) {
+            if (!wait_entry(order.value(i)) || (i + 1 < n && !wait_entry(order.key(i + 1)))) break;
+            for (int s = 0; s < 2; ++s) {
+              if (!wait(p_ready + s, ns[s]++)) break;
+              tc::fence_after_sync();
+              outputs(s, order.value(i), i == 0);
+              if (s == 1) release(order.value(i));
+              if (i + 1 == n) tc::mma_commit(o_full + s);
+              if (i + 1 < n) {
+                scores(s, s, order.key(i + 1));
+                if (s == 1) release(order.key(i + 1));
+              }
+            }
+          }
+        }
+        it0 += 2 * n;
+        ++seg;
+      }
+      // tensor memory is given back once every product issued has completed, also where a wait gave up
+      if (issued) {
+        tc::mma_commit(drained);
+        tc::mbar_wait(drained, 0, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: stream s, one thread per row; warp w of a group reaches tensor memory lanes 32 w ..
+    const int s = warp >> 2, lrow = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + C::S(s) + lanes, t_o = tmem + C::O(s) + lanes;
+    const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // a scale of 0 too leaves minus infinity where it is
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
+    int it0 = 0, seg = 0, ns = 0, no = 0;
+    bool dead = false;
+    const auto wait = [&](uint64_t* bar, int count) {
+      const bool ok = dead || tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns);
+      if (__any_sync(0xFFFFFFFFu, !ok)) {
+        dead = true;
+        if (lane == 0) flags[0] = 1;
+      }
+    };
+    while (walk.next<kTile>(p, cum, total, ctas, g)) {
+      const int rows = rows_of(g), row0 = g.row_block * kRows, n = g.tiles;
+      const Order order{n, rows <= 128};
+      const int len = g.seq.prefix + g.seq.count;
+      named_sync(1, 256);  // the segment before is finished: its queries, statistics and outputs are no longer read
+      // ---- queries
+      {
+        constexpr int LPR = D / 8;
+        const int qrows = order.split_keys ? 128 : 256;
+        for (int r = threadIdx.x / LPR; r < qrows; r += 256 / LPR) {
+          const int l = threadIdx.x % LPR;
+          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            u = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
+                                                     (int64_t)(g.head * p.group + hh) * D + 8 * l));
+            u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QTile + (l >> 3) * (128 * 128) + (r & 127) * 128 + (((l & 7) ^ (r & 7)) << 4)) = u;
+          if (l == 0) row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
+        }
+        tc::fence_proxy_async_smem();
+        named_sync(1, 256);  // masks
+        if (lane == 0) tc::mbar_arrive(q_ready);
+      }
+      const int r = order.split_keys ? lrow : s * 128 + lrow;  // this thread's row of the block
+      const uint64_t seen = row_mask[r];
+      float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
+      const int first_tile = order.split_keys ? s : 0, tile_step = order.split_keys ? 2 : 1;
+      bool any = false;
+      for (int i = first_tile; i < n; i += tile_step) {
+        wait(s_full + s, ns++);
+        tc::fence_after_sync();
+        const int pos0 = (g.tile0 + i) * kTile;
+        const bool tail = pos0 + kTile > g.seq.prefix;
+        // bit j of word w: column 32 w + j is seen
+        uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (tail) {
+          // columns before `from` are prefix; drafts come after, then nothing
+          const int from = g.seq.prefix - pos0;
+          const uint64_t drafts = g.seq.count >= 64 ? seen : seen & ((1ull << g.seq.count) - 1);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int at = from - 32 * w;  // the first draft's place relative to this word
+            uint32_t bits = at >= 32 ? 0xFFFFFFFFu : at > 0 ? (1u << at) - 1 : 0u;
+            if (at >= 0 && at < 32) bits |= (uint32_t)(drafts << at);
+            else if (at < 0 && at > -64) bits |= (uint32_t)(drafts >> -at);
+            vis[w] = bits;
+          }
+        }
+        // ---- the row's maximum
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t x[32];
+          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+          tc::tmem_ld_wait();
+          if (tail)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = vis[w] >> j & 1 ? x[j] : 0xFF800000u;
+          float a = mx, b = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            a = fmaxf(a, __uint_as_float(x[j]));
+            b = fmaxf(b, __uint_as_float(x[j + 1]));
+          }
+          mx = fmaxf(a, b);
+        }
+        mx *= c;
+        const bool move = mx > m + kMove || (m == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float to = move ? mx : m, a = m == to ? 1.f : ex2(m - to);
+          l *= a;
+          m = to;
+          if (any) {
+#pragma unroll 1
+            for (int col = 0; col < D; col += 32) {
+              uint32_t x[32];
+              tc::tmem_ld_32x32b_x32(t_o + col, x);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * a);
+              tmem_st_x32(t_o + col, x);
+            }
+          }
+        }
+        any = true;
+        // ---- weights, over the scores
+        const float ms = m == -INFINITY ? 0.f : -m;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t x[32], e[16];
+          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+          tc::tmem_ld_wait();
+          if (tail)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = vis[w] >> j & 1 ? x[j] : 0xFF800000u;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(c, c), make_float2(ms, ms));
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum = __fadd2_rn(sum, y);
+            e[j >> 1] = pack_bf16x2(y.x, y.y);
+          }
+          tmem_st_x16(t_s + 16 * w, e);
+        }
+        l += sum.x + sum.y;
+        tmem_st_wait();
+        if (tail) {
+          // Values that must not reach a product: rows past the end become zeros, whatever their bits; so do numbers of
+          // drafts that are not finite (rare), which are added at the end to the rows that see them.
+          wait(full + (it0 + order.value(i)) % C::Slots, (it0 + order.value(i)) / C::Slots);
+          uint8_t* tile = ring + ((it0 + order.value(i)) % C::Slots) * C::Slot;
+          const int from = max(g.seq.prefix - pos0, 0);
+          constexpr int Chunks = D / 8;
+          for (int e = from * Chunks + (threadIdx.x & 127); e < kTile * Chunks; e += 128) {
+            const int row = e / Chunks, ch = e - row * Chunks;
+            uint4* at = reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+            if (pos0 + row >= len) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 v = *at;
+            bool odd = false;
+            const auto clean = [&](uint32_t& w) {
+              if ((w & 0x7F80u) == 0x7F80u) { w &= 0xFFFF0000u; odd = true; }
+              if ((w >> 16 & 0x7F80u) == 0x7F80u) { w &= 0xFFFFu; odd = true; }
+            };
+            clean(v.x); clean(v.y); clean(v.z); clean(v.w);
+            if (odd) {
+              flags[2] = seg;
+              __threadfence_block();
+              *at = v;
+            }
+          }
+          tc::fence_proxy_async_smem();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_ready + s);
+      }
+      // ---- the segment's end
+      if (any) wait(o_full + s, no++);
+      tc::fence_after_sync();
+      it0 += 2 * n;
+      const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+      const bool valid = r < rows;
+      float wa = 1.f, wb = 0.f;  // weights of the own stream's and the other's outputs
+      bool other = false;
+      int col0 = 0, cols = D;
+      if (order.split_keys) {
+        // both streams have the same rows: each finishes half of the columns
+        row_stat[(s * 2) * 128 + lrow] = m;
+        row_stat[(s * 2 + 1) * 128 + lrow] = l;
+        tc::fence_before_sync();
+        named_sync(1, 256);
+        tc::fence_after_sync();
+        const float om = row_stat[((1 - s) * 2) * 128 + lrow], ol = row_stat[((1 - s) * 2 + 1) * 128 + lrow];
+        const float nm = fmaxf(m, om), bm = nm == -INFINITY ? 0.f : nm;
+        wa = ex2(m - bm);
+        wb = ex2(om - bm);
+        l = l * wa + ol * wb;
+        m = nm;
+        other = s == 0 ? n > 1 : true;  // a single tile is stream 0's
+        col0 = s * (D / 2);
+        cols = D / 2;
+      } else {
+        named_sync(1, 256);
+      }
+      const bool own = any;
+      const bool odd = flags[2] == seg;
+      const uint32_t t_other = tmem + C::O(1 - s) + lanes;
+      const auto fetch = [&](int col, float (&v)[32]) {  // 32 columns of the row, joined
+        uint32_t x[32];
+        if (own) {
+          tc::tmem_ld_32x32b_x32(t_o + col, x);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(x[j]) * wa;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        if (other) {
+          tc::tmem_ld_32x32b_x32(t_other + col, x);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(x[j]) * wb;
+        }
+        if (odd && valid)
+          for (int j = 0; j < g.seq.count; ++j) {
+            const int pos = g.seq.prefix + j, at = pos - g.tile0 * kTile;
+            if (!(seen >> j & 1) || at < 0 || at >= n * kTile) continue;
+            int page = __ldg(p.table + (int64_t)g.b * p.width + (pos >> p.page_shift));
+            page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+            const uint16_t* vr = p.pool + (((int64_t)((page * 2 + 1) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint16_t b = vr[k];
+              if ((b & 0x7F80u) == 0x7F80u) v[k] += bf16_to_f32(b);
+            }
+          }
+      };
+      const auto store = [&](int col, const float (&v)[32], float f) {
+        uint4* at = reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + col);
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+          at[j / 8] = make_uint4(pack_bf16x2(v[j] * f, v[j + 1] * f), pack_bf16x2(v[j + 2] * f, v[j + 3] * f),
+                                 pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
+      };
+      const auto store_lse = [&](float mm, float ll) {
+        if (p.lse && col0 == 0)
+          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = ll == 0.f ? -INFINITY : kLn2 * (mm + log2f(ll));
+      };
+      if (g.first == g.last) {
+        const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int col = col0; col < col0 + cols; col += 32) {
+          float v[32];
+          fetch(col, v);
+          if (valid) store(col, v, f);
+        }
+        if (valid) store_lse(m, l);
+        tc::fence_before_sync();
+        ++seg;
+        continue;
+      }
+      // a part: [D/4][256 rows][4] sums, then maxima and sums of weights
+      {
+        float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * C::PartFloats;
+#pragma unroll 1
+        for (int col = col0; col < col0 + cols; col += 32) {
+          float v[32];
+          fetch(col, v);
+          if (valid)
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              __stcg(reinterpret_cast<float4*>(part + ((int64_t)(col + j) / 4 * kRows + r) * 4), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+        }
+        if (valid && col0 == 0) {
+          __stcg(part + (int64_t)kRows * D + r, m);
+          __stcg(part + (int64_t)kRows * D + kRows + r, l);
+        }
+        tc::fence_before_sync();
+      }
+      named_sync(1, 256);
+      if (threadIdx.x == 0) flags[1] = tree_arrive(p.counter + g.first, g.last - g.first);
+      named_sync(1, 256);
+      ++seg;
+      if (!flags[1]) continue;
+      // the last to arrive joins the parts in their order; a thread has one row, and with few rows half of its columns
+      const int parts = g.last - g.first + 1;
+      const auto part_of = [&](int j) { return p.part + (int64_t)tree_slot(g.first + j, j == 0) * C::PartFloats; };
+      float mm = -INFINITY, ll = 0.f;
+      if (valid) {
+        for (int j = 0; j < parts; ++j) mm = fmaxf(mm, __ldcg(part_of(j) + (int64_t)kRows * D + r));
+        const float bm = mm == -INFINITY ? 0.f : mm;
+        for (int j = 0; j < parts; ++j)
+          ll += ex2(__ldcg(part_of(j) + (int64_t)kRows * D + r) - bm) * __ldcg(part_of(j) + (int64_t)kRows * D + kRows + r);
+        const float f = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll 1
+        for (int col = col0; col < col0 + cols; col += 32) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          for (int j = 0; j < parts; ++j) {
+            const float* part = part_of(j);
+            const float w = ex2(__ldcg(part + (int64_t)kRows * D + r) - bm);
+            float4 u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[k] = __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)col / 4 + k) * kRows * 4 + r * 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              v[4 * k] += w * u[k].x;
+              v[4 * k + 1] += w * u[k].y;
+              v[4 * k + 2] += w * u[k].z;
+              v[4 * k + 3] += w * u[k].w;
+            }
+          }
+          store(col, v, f);
+        }
+        store_lse(mm, ll);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && flags[0]) atomicCAS(&g_tree_tc_error, 0, 2);
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cudaStream_t st) {
+  auto kern = tree_tc_kernel<D>;
+  static PerDevice<cudaError_t> attr_of;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  const cudaError_t e = attr_of.get(dev, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Smem);
+  }, cudaErrorInvalidDevice);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
+}
+
+}  // namespace
+
+bool tree_tc_fits(const trellis_cache_t& c, int rows) { return c.dtype == TRELLIS_BF16 && c.head_dim <= 128 && rows > 16; }
+
+int tree_tc_box_rows(const trellis_cache_t& c) { return c.page_size < kTile ? c.page_size : kTile; }
+
+size_t tree_tc_part_bytes(const trellis_cache_t& c) { return (size_t)kRows * (c.head_dim + 2) * 4; }
+
+cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st) {
+  return head_dim == 64 ? launch_d<64>(map, p, ctas, st) : launch_d<128>(map, p, ctas, st);
+}
+
+int read_tree_tc_error(int reset) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_tree_tc_error, sizeof(int)) != cudaSuccess) return -1;
+  if (reset && v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_tree_tc_error, &zero, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
+}
+
+}  // namespace trellis

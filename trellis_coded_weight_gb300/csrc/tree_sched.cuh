@@ -1,20 +1,20 @@
 // tree_sched.cuh -- how the work of a tree attention call is divided over the GPU, shared by its kernels.
 //
 // An item is one key/value head of one sequence and one block of ROWS query rows (row r of a sequence and head:
-// draft r / group, query head r % group of the head's group); it takes one step per kTile keys.  Lengths are device
+// draft r / group, query head r % group of the head's group); it takes one step per TILE keys.  Lengths are device
 // data, so the division is made on the device: all steps of all items, in the order of (sequence, row block, head,
 // tile), are cut into equal contiguous ranges, one per thread block.  An item that falls into one range is finished
 // there.  Otherwise each block writes its part (maximum, sum and unnormalised output of its keys, fp32) to the
 // workspace, and the last one to arrive joins the parts in their order, so results do not depend on timing.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "serving.h"
 
 namespace trellis {
 
-constexpr int kTile = 64;            // keys per step
 constexpr int kTreeMaxCtas = 1024;   // bound on the grid (sizes the counters)
 
 struct TreeParams {
@@ -24,12 +24,13 @@ struct TreeParams {
   const int32_t *table, *prefix, *q_start;
   const uint64_t* mask;
   const float* scales;  // [2][hkv] of the layer, or null
+  const uint16_t* pool; // the layer's pages (bf16 ones)
   uint32_t* counter;    // [kTreeMaxCtas], zero between calls: arrivals for the item that block c was the first to share
   float* part;          // two slots per thread block
   int64_t q_stride, out_stride;
   int64_t pages;
   uint64_t wait_ns;
-  int batch, width, n, max_tokens, hq, hkv, group, page_shift, row_blocks;
+  int batch, width, n, max_tokens, hq, hkv, group, page_shift;
   float scale_log2;     // scale * log2(e)
 };
 
@@ -53,10 +54,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.prefix = pre;
   return s;
 }
-__device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return s.count ? (s.prefix + s.count + kTile - 1) / kTile : 0; }
+template <int TILE>
+__device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return s.count ? (s.prefix + s.count + TILE - 1) / TILE : 0; }
 
 // cum[b] = steps of the sequences before b (batch + 1 entries), by one warp.
-template <int ROWS>
+template <int ROWS, int TILE>
 __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
   const int lane = threadIdx.x & 31;
   int before = 0;
@@ -65,7 +67,7 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
     int v = 0;
     if (b < p.batch) {
       const TreeSeq s = tree_seq(p, b);
-      v = tree_tiles(s) * ((s.count * p.group + ROWS - 1) / ROWS) * p.hkv;
+      v = tree_tiles<TILE>(s) * ((s.count * p.group + ROWS - 1) / ROWS) * p.hkv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -94,7 +96,7 @@ struct TreeWalk {
   int at, end, b;
   __device__ __forceinline__ TreeWalk(int total, int ctas, int cta)
       : at((int)((int64_t)cta * total / ctas)), end((int)((int64_t)(cta + 1) * total / ctas)), b(-1) {}
-  template <int ROWS>
+  template <int TILE>
   __device__ __forceinline__ bool next(const TreeParams& p, const int* cum, int total, int ctas, TreeSegment& g) {
     if (at >= end) return false;
     if (b < 0) {  // the last sequence that starts at or before `at`; empty ones are passed over
@@ -110,7 +112,7 @@ struct TreeWalk {
     }
     g.b = b;
     g.seq = tree_seq(p, b);
-    const int nt = tree_tiles(g.seq), r = at - cum[b], item = r / nt;
+    const int nt = tree_tiles<TILE>(g.seq), r = at - cum[b], item = r / nt;
     g.tile0 = r - item * nt;
     g.row_block = item / p.hkv;
     g.head = item - g.row_block * p.hkv;
@@ -137,5 +139,12 @@ __device__ __forceinline__ bool tree_arrive(uint32_t* counter, int others) {
   *counter = 0u;
   return true;
 }
+
+// The tensor-core kernel (tree_attention_tc.cu) and what it takes of the caller.
+bool tree_tc_fits(const trellis_cache_t& c, int rows);
+int tree_tc_box_rows(const trellis_cache_t& c);
+size_t tree_tc_part_bytes(const trellis_cache_t& c);
+cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st);
+int read_tree_tc_error(int reset);
 
 }  // namespace trellis
