@@ -139,20 +139,20 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     tc::fence_mbar_init();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<ROWS, kTile>(p, cum);
+  if (warp == 0) tree_cumulate<ROWS, kTile, false>(p, cum);
   __syncthreads();
   const int total = cum[p.batch];
-  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x;
+  const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
   const int cta = blockIdx.x;
   if (cta >= ctas) return;  // fewer steps than blocks
 
-  TreeWalk walk(total, ctas, cta);
+  TreeWalk<ROWS, kTile, false> walk(total, ctas, cta);
   TreeSegment g;
   if (warp == C::Consumers) {
     // ---- the copying warp: every tile of the range, as many ahead as there are stages
     int it = 0, issued = 0;
     bool dead = false;
-    while (walk.next<kTile>(p, cum, total, ctas, g)) {
+    while (walk.next(p, cum, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const int box = p.page_shift < 6 ? 1 << p.page_shift : kTile;  // rows of one copy
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     const int nthr = C::Consumers * 32;
     int it = 0;
     bool dead = false;
-    while (walk.next<kTile>(p, cum, total, ctas, g)) {
+    while (walk.next(p, cum, g)) {
       const int rows = min(ROWS, g.seq.count * p.group - g.row_block * ROWS);  // rows of this block that exist
       const int row0 = g.row_block * ROWS;
       named_sync(1, nthr);  // the previous segment's queries are no longer read

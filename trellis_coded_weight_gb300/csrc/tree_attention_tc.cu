@@ -31,7 +31,7 @@ constexpr uint64_t kDrainNs = 2000000000ull;  // for copies and products in flig
 constexpr int kTile = 128;                    // keys per step
 constexpr int kRows = 256;                    // rows of a block
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // two softmax warpgroups; one for the copying and the issuing warp, and two that idle
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kMove = 8.f;                  // log2 of the growth that moves a row's maximum
 
@@ -165,25 +165,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<kRows, kTile>(p, cum);
+  if (warp == 0) tree_cumulate<kRows, kTile, true>(p, cum);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int total = cum[p.batch];
-  const int ctas = total < (int)gridDim.x ? total : (int)gridDim.x;
   const int cta = blockIdx.x;
-  TreeWalk walk(total, ctas < 1 ? 1 : ctas, cta);
-  if (cta >= ctas) walk.at = walk.end = 0;  // fewer steps than blocks
+  TreeWalk<kRows, kTile, true> walk(total, tree_ctas_used<true>(total, (int)gridDim.x), cta);
   TreeSegment g;
   const auto rows_of = [&](const TreeSegment& x) { return min(kRows, x.seq.count * p.group - x.row_block * kRows); };
 
+  if (warp >= kSoftmaxWarps) {
+  // 384 threads x 168 registers at launch = 256 x 200 + 128 x 104
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kCopyWarp) {
     // ---- the copying warp
     int it = 0;
     bool dead = false;
     const int box = min(1 << p.page_shift, kTile);  // rows of one copy
-    while (!dead && walk.next<kTile>(p, cum, total, ctas, g)) {
+    while (!dead && walk.next(p, cum, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const Order order{g.tiles, rows_of(g) <= 128};
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < kTile / 16; ++k)
           mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint64_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
       };
-      while (!dead && walk.next<kTile>(p, cum, total, ctas, g)) {
+      while (!dead && walk.next(p, cum, g)) {
         const int n = g.tiles;
         const Order order{n, rows_of(g) <= 128};
         if (!wait(q_ready, seg)) break;
@@ -306,7 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax: stream s, one thread per row; warp w of a group reaches tensor memory lanes 32 w ..
     const int s = warp >> 2, lrow = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) flags[0] = 1;
       }
     };
-    while (walk.next<kTile>(p, cum, total, ctas, g)) {
+    while (walk.next(p, cum, g)) {
       const int rows = rows_of(g), row0 = g.row_block * kRows, n = g.tiles;
       const Order order{n, rows <= 128};
       const int len = g.seq.prefix + g.seq.count;
@@ -357,39 +360,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         const int pos0 = (g.tile0 + i) * kTile;
         const bool tail = pos0 + kTile > g.seq.prefix;
-        // bit j of word w: column 32 w + j is seen
-        uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
         if (tail) {
-          // columns before `from` are prefix; drafts come after, then nothing
+          // scores that the row does not see become minus infinity, in place: columns before `from` are prefix, drafts
+          // come after, then nothing
           const int from = g.seq.prefix - pos0;
           const uint64_t drafts = g.seq.count >= 64 ? seen : seen & ((1ull << g.seq.count) - 1);
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < 4; ++w) {
-            const int at = from - 32 * w;  // the first draft's place relative to this word
+            const int at = from - 32 * w;  // the first draft's place relative to this word of 32 columns
             uint32_t bits = at >= 32 ? 0xFFFFFFFFu : at > 0 ? (1u << at) - 1 : 0u;
             if (at >= 0 && at < 32) bits |= (uint32_t)(drafts << at);
             else if (at < 0 && at > -64) bits |= (uint32_t)(drafts >> -at);
-            vis[w] = bits;
+            uint32_t y[32];
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = bits >> j & 1 ? y[j] : 0xFF800000u;
+            tmem_st_x32(t_s + 32 * w, y);
           }
+          tmem_st_wait();
         }
-        // ---- the row's maximum
-        float mx = -INFINITY;
+        // ---- the row's maximum; the scores stay in registers
+        uint32_t x[4][32];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) tc::tmem_ld_32x32b_x32(t_s + 32 * w, x[w]);
+        tc::tmem_ld_wait();
+        float mw[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          uint32_t x[32];
-          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
-          tc::tmem_ld_wait();
-          if (tail)
+          float a = __uint_as_float(x[w][0]);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = vis[w] >> j & 1 ? x[j] : 0xFF800000u;
-          float a = mx, b = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            a = fmaxf(a, __uint_as_float(x[j]));
-            b = fmaxf(b, __uint_as_float(x[j + 1]));
-          }
-          mx = fmaxf(a, b);
+          for (int j = 1; j < 31; j += 2) a = fmaxf(fmaxf(a, __uint_as_float(x[w][j])), __uint_as_float(x[w][j + 1]));
+          mw[w] = fmaxf(a, __uint_as_float(x[w][31]));
         }
+        float mx = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
         mx *= c;
         const bool move = mx > m + kMove || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, move)) {
@@ -399,12 +403,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (any) {
 #pragma unroll 1
             for (int col = 0; col < D; col += 32) {
-              uint32_t x[32];
-              tc::tmem_ld_32x32b_x32(t_o + col, x);
+              uint32_t y[32];
+              tc::tmem_ld_32x32b_x32(t_o + col, y);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * a);
-              tmem_st_x32(t_o + col, x);
+              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * a);
+              tmem_st_x32(t_o + col, y);
             }
           }
         }
@@ -414,15 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          uint32_t x[32], e[16];
-          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
-          tc::tmem_ld_wait();
-          if (tail)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = vis[w] >> j & 1 ? x[j] : 0xFF800000u;
+          uint32_t e[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(c, c), make_float2(ms, ms));
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[w][j]), __uint_as_float(x[w][j + 1])), make_float2(c, c), make_float2(ms, ms));
             y.x = ex2(y.x);
             y.y = ex2(y.y);
             sum = __fadd2_rn(sum, y);

@@ -2,10 +2,12 @@
 //
 // An item is one key/value head of one sequence and one block of ROWS query rows (row r of a sequence and head:
 // draft r / group, query head r % group of the head's group); it takes one step per TILE keys.  Lengths are device
-// data, so the division is made on the device: all steps of all items, in the order of (sequence, row block, head,
-// tile), are cut into equal contiguous ranges, one per thread block.  An item that falls into one range is finished
-// there.  Otherwise each block writes its part (maximum, sum and unnormalised output of its keys, fp32) to the
-// workspace, and the last one to arrive joins the parts in their order, so results do not depend on timing.
+// data, so the division is made on the device: the steps of all items, in the order of (sequence, row block, head,
+// tile), are laid end to end and cut into equal contiguous ranges, one per thread block; a step belongs to the range that
+// holds its beginning.  A step has length 1, or (HALVES) 2 where its rows fill more than half a block, since it then
+// takes that kernel twice as long.  An item that falls into one range is finished there.  Otherwise each block
+// writes its part (maximum, sum and unnormalised output of its keys, fp32) to the workspace, and the last one to arrive
+// joins the parts in their order, so results do not depend on timing.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -57,8 +59,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 template <int TILE>
 __device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return s.count ? (s.prefix + s.count + TILE - 1) / TILE : 0; }
 
-// cum[b] = steps of the sequences before b (batch + 1 entries), by one warp.
-template <int ROWS, int TILE>
+// cum[b] = length of the sequences before b (batch + 1 entries), by one warp.
+template <int ROWS, int TILE, bool HALVES>
 __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
   const int lane = threadIdx.x & 31;
   int before = 0;
@@ -67,7 +69,8 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
     int v = 0;
     if (b < p.batch) {
       const TreeSeq s = tree_seq(p, b);
-      v = tree_tiles<TILE>(s) * ((s.count * p.group + ROWS - 1) / ROWS) * p.hkv;
+      constexpr int kUnit = HALVES ? ROWS / 2 : ROWS;
+      v = tree_tiles<TILE>(s) * ((s.count * p.group + kUnit - 1) / kUnit) * p.hkv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -80,8 +83,14 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
   if (lane == 0) cum[0] = 0;
 }
 
-// The blocks' ranges: block c of `ctas` takes steps [c * total / ctas, (c + 1) * total / ctas).
-__device__ __forceinline__ int tree_cta_of(int64_t step, int64_t total, int ctas) { return (int)(((step + 1) * ctas - 1) / total); }
+// The blocks' ranges: block c of `ctas` takes [c * total / ctas, (c + 1) * total / ctas).
+__device__ __forceinline__ int tree_cta_of(int64_t at, int64_t total, int ctas) { return (int)(((at + 1) * ctas - 1) / total); }
+// Blocks in use: none is left without a step.
+template <bool HALVES>
+__device__ __forceinline__ int tree_ctas_used(int total, int grid) {
+  const int most = HALVES ? (total + 1) / 2 : total;
+  return most < grid ? most : grid;
+}
 
 // A stretch of one item's steps inside a block's range.
 struct TreeSegment {
@@ -92,37 +101,46 @@ struct TreeSegment {
 };
 
 // Walks a block's range segment by segment.
+template <int ROWS, int TILE, bool HALVES>
 struct TreeWalk {
-  int at, end, b;
-  __device__ __forceinline__ TreeWalk(int total, int ctas, int cta)
-      : at((int)((int64_t)cta * total / ctas)), end((int)((int64_t)(cta + 1) * total / ctas)), b(-1) {}
-  template <int TILE>
-  __device__ __forceinline__ bool next(const TreeParams& p, const int* cum, int total, int ctas, TreeSegment& g) {
-    if (at >= end) return false;
-    if (b < 0) {  // the last sequence that starts at or before `at`; empty ones are passed over
-      int lo = 0, hi = p.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= at) lo = mid;
-        else hi = mid;
-      }
-      b = lo;
-    } else {
-      while (cum[b + 1] <= at) ++b;
+  int at, end, b, total, ctas;
+  __device__ __forceinline__ TreeWalk(int total_, int ctas_, int cta) : at(0), end(0), b(-1), total(total_), ctas(ctas_) {
+    if (cta < ctas) {
+      at = (int)((int64_t)cta * total / ctas);
+      end = (int)((int64_t)(cta + 1) * total / ctas);
     }
-    g.b = b;
-    g.seq = tree_seq(p, b);
-    const int nt = tree_tiles<TILE>(g.seq), r = at - cum[b], item = r / nt;
-    g.tile0 = r - item * nt;
-    g.row_block = item / p.hkv;
-    g.head = item - g.row_block * p.hkv;
-    const int left = nt - g.tile0;
-    g.tiles = left < end - at ? left : end - at;
-    const int64_t start = (int64_t)cum[b] + (int64_t)item * nt;
-    g.first = tree_cta_of(start, total, ctas);
-    g.last = tree_cta_of(start + nt - 1, total, ctas);
-    at += g.tiles;
-    return true;
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, const int* cum, TreeSegment& g) {
+    while (at < end) {
+      if (b < 0) {  // the last sequence that starts at or before `at`; empty ones are passed over
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (cum[mid] <= at) lo = mid;
+          else hi = mid;
+        }
+        b = lo;
+      } else {
+        while (cum[b + 1] <= at) ++b;
+      }
+      g.b = b;
+      g.seq = tree_seq(p, b);
+      const int nt = tree_tiles<TILE>(g.seq), r = at - cum[b], block = (HALVES ? 2 : 1) * nt * p.hkv;
+      g.row_block = r / block;
+      const int w = HALVES && g.seq.count * p.group - g.row_block * ROWS > ROWS / 2 ? 2 : 1;
+      const int q = r - g.row_block * block;
+      g.head = q / (nt * w);
+      const int off = q - g.head * nt * w;             // into the item
+      const int stop = off + (end - at) < nt * w ? off + (end - at) : nt * w;
+      g.tile0 = (off + w - 1) / w;
+      g.tiles = (stop + w - 1) / w - g.tile0;
+      const int64_t start = (int64_t)at - off;
+      g.first = tree_cta_of(start, total, ctas);
+      g.last = tree_cta_of(start + (int64_t)(nt - 1) * w, total, ctas);
+      at += stop - off;
+      if (g.tiles > 0) return true;
+    }
+    return false;
   }
 };
 
