@@ -91,7 +91,8 @@ struct Cfg {
   static constexpr int Stage = 2 * HalfStage;
   static constexpr int QBytes = ROWS * D * 2;
   static constexpr int Regs = D / 2;                 // output numbers of a lane
-  static constexpr int JoinFloats = (Regs + 4) * 32; // a warp's outputs, maxima and sums
+  // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
+  static constexpr float Lift = F8 ? 15.f : 0.f;
   static constexpr int JoinTurns = D == 256 ? 2 : 1;  // wide heads join their outputs in two turns, to fit
   static constexpr int JoinSlot = (Regs / JoinTurns + 4) * 32;
   static constexpr int Join = WR * (WK / 2) * JoinSlot * 4;
@@ -126,8 +127,9 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
   int* cum = reinterpret_cast<int*>(row_fac + ROWS);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cum) + C::Cum);
   uint64_t* empty = full + C::Stages;
-  volatile int* flags = reinterpret_cast<volatile int*>(empty + C::Stages);  // [0] a wait gave up, [1] last to arrive
+  volatile int* flags = reinterpret_cast<volatile int*>(empty + C::Stages);  // [0] a wait gave up
 
+  constexpr float kLift = C::Lift;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&map);
@@ -144,7 +146,10 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
   const int total = cum[p.batch];
   const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;  // fewer steps than blocks
+  if (cta >= ctas) {  // fewer steps than blocks
+    if (threadIdx.x == 0) p.items[cta] = make_int4(-1, 0, 0, 0);
+    return;
+  }
 
   TreeWalk<ROWS, kTile, false> walk(total, ctas, cta);
   TreeSegment g;
@@ -200,6 +205,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     const int wr = warp / C::WK, wk = warp % C::WK;
     const int gq = lane >> 2, c4 = lane & 3;  // fragment row and column pair
     const int nthr = C::Consumers * 32;
+    int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
     int it = 0;
     bool dead = false;
     while (walk.next(p, cum, g)) {
@@ -281,8 +287,6 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       const int len = g.seq.prefix + g.seq.count;
-      // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
-      constexpr float kLift = F8 ? 15.f : 0.f;
 
       const int clear = g.seq.prefix / kTile - g.tile0;  // tiles from here on have drafts, or rows past the end, among their keys
       for (int t = 0; t < g.tiles; ++t, ++it) {
@@ -507,99 +511,59 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
         }
       }
 
-      // an output fragment, already joined, to the outputs
-      const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
-      uint16_t* to[2];     // this lane's rows in the outputs
-      int64_t to_lse[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = wr * 16 + gq + 8 * half, d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
-        to[half] = r < rows ? p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D : nullptr;
-        to_lse[half] = (int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh;
-      }
-      const auto store = [&](const float (&v)[4], int i, const float (&fl)[2]) {  // i: output fragment
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!to[half]) continue;
-          if constexpr (F8) {
-            const int col = (i >> 1) * 16 + c4 * 4 + (i & 1);
-            to[half][col] = f32_to_bf16_rn(v[2 * half] * fl[half]);
-            to[half][col + 2] = f32_to_bf16_rn(v[2 * half + 1] * fl[half]);
-          } else {
-            *reinterpret_cast<uint32_t*>(to[half] + i * 8 + c4 * 2) = pack_bf16x2(v[2 * half] * fl[half], v[2 * half + 1] * fl[half]);
-          }
-        }
-      };
-      const auto store_lse = [&](const float (&mm)[2], const float (&ll)[2]) {
-        if (!p.lse || c4 != 0) return;
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-          if (to[half]) p.lse[to_lse[half]] = ll[half] == 0.f ? -INFINITY : kLn2 * (mm[half] + (log2f(ll[half]) - kLift));
-      };
       if (g.first == g.last) {
         if (wk == 0) {
-          const float fl[2] = {l[0] == 0.f ? 0.f : vs / l[0], l[1] == 0.f ? 0.f : vs / l[1]};
+          const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) store(o[i], i, fl);
-          store_lse(m, l);
+          for (int half = 0; half < 2; ++half) {
+            const int r = wr * 16 + gq + 8 * half;
+            if (r >= rows) continue;
+            const float f = l[half] == 0.f ? 0.f : vs / l[half];
+            const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+            uint16_t* to = p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D;
+            if constexpr (F8) {
+#pragma unroll
+              for (int i = 0; i < D / 8; i += 2)
+                *reinterpret_cast<uint2*>(to + (i >> 1) * 16 + c4 * 4) =
+                    make_uint2(pack_bf16x2(o[i][2 * half] * f, o[i + 1][2 * half] * f), pack_bf16x2(o[i][2 * half + 1] * f, o[i + 1][2 * half + 1] * f));
+            } else {
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint32_t*>(to + i * 8 + c4 * 2) = pack_bf16x2(o[i][2 * half] * f, o[i][2 * half + 1] * f);
+            }
+            if (p.lse && c4 == 0)
+              p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] =
+                  l[half] == 0.f ? -INFINITY : kLn2 * (m[half] + (log2f(l[half]) - kLift));
+          }
         }
         continue;
       }
-      // a part: the warps' fragments as they are, [row warp][number][lane]
+      // a part, for the joining kernel
       if (wk == 0) {
-        float* at = p.part + ((int64_t)tree_slot(cta, g.tile0 == 0) * C::WR + wr) * C::JoinFloats + lane;
+        float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * tree_part_floats(ROWS, D);
 #pragma unroll
-        for (int i = 0; i < C::Regs; ++i) __stcg(at + i * 32, o[i >> 2][i & 3]);
+        for (int half = 0; half < 2; ++half) {
+          const int r = wr * 16 + gq + 8 * half;
+          if (r >= rows) continue;
+          if constexpr (F8) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          __stcg(at + (C::Regs + i) * 32, m[i]);
-          __stcg(at + (C::Regs + 2 + i) * 32, l[i]);
+            for (int i = 0; i < D / 8; i += 2)
+              *reinterpret_cast<float4*>(part + r * D + (i >> 1) * 16 + c4 * 4) =
+                  make_float4(o[i][2 * half], o[i + 1][2 * half], o[i][2 * half + 1], o[i + 1][2 * half + 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+              *reinterpret_cast<float2*>(part + r * D + i * 8 + c4 * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+          }
+          if (c4 == 0) {
+            part[ROWS * D + r] = m[half];
+            part[ROWS * D + ROWS + r] = l[half];
+          }
         }
       }
-      named_sync(1, nthr);
-      if (threadIdx.x == 0)
-        flags[1] = tree_arrive(p.counter + g.first, g.last - g.first);
-      named_sync(1, nthr);
-      if (!flags[1]) continue;
-      // the last to arrive: weights of the parts from their maxima, then the weighted sums; each warp takes a share
-      // of the numbers of its rows
-      const int parts = g.last - g.first + 1;
-      const auto part_of = [&](int j) {
-        return p.part + ((int64_t)tree_slot(g.first + j, j == 0) * C::WR + wr) * C::JoinFloats + lane;
-      };
-      float mm[2] = {-INFINITY, -INFINITY}, ll[2] = {0.f, 0.f};
-      for (int j = 0; j < parts; ++j) {
-        const float* at = part_of(j);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) mm[i] = fmaxf(mm[i], __ldcg(at + (C::Regs + i) * 32));
-      }
-      const float bm[2] = {mm[0] == -INFINITY ? 0.f : mm[0], mm[1] == -INFINITY ? 0.f : mm[1]};
-      constexpr int N = C::Regs / C::WK;  // numbers of this warp
-      float acc[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll 2
-      for (int j = 0; j < parts; ++j) {
-        const float* at = part_of(j);
-        float w[2], v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __ldcg(at + (wk * N + i) * 32);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          w[i] = ex2(__ldcg(at + (C::Regs + i) * 32) - bm[i]);
-          ll[i] += w[i] * __ldcg(at + (C::Regs + 2 + i) * 32);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] += w[(i >> 1) & 1] * v[i];
-      }
-      const float fl[2] = {ll[0] == 0.f ? 0.f : vs / ll[0], ll[1] == 0.f ? 0.f : vs / ll[1]};
-#pragma unroll
-      for (int i = 0; i < N / 4; ++i) {
-        const float v[4] = {acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
-        store(v, wk * (N / 4) + i, fl);
-      }
-      if (wk == 0) store_lse(mm, ll);
+      if (threadIdx.x == 0 && g.first == cta) shared_item = make_int4(g.b, g.head, g.row_block, g.last);
     }
+    if (threadIdx.x == 0) p.items[cta] = shared_item;
   }
   __syncthreads();
   if (threadIdx.x == 0 && flags[0]) atomicCAS(&g_tree_error, 0, 1);
@@ -625,7 +589,8 @@ cudaError_t launch_rows(const CUtensorMap& map, const TreeParams& p, cudaStream_
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
   }, cudaErrorInvalidDevice);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)tree_ctas()), dim3(C::Threads), C::Smem, st, map, p);
+  const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)tree_ctas()), dim3(C::Threads), C::Smem, st, map, p);
+  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, ROWS, C::Lift, tree_ctas(), st);
 }
 
 template <int D, bool F8>
@@ -640,9 +605,8 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int rows, cuda
 size_t tree_workspace_bytes(const trellis_cache_t& c, int batch, int max_tokens, int q_heads) {
   (void)batch;  // parts belong to thread blocks, whatever the batch
   const int group = q_heads / c.heads;
-  const size_t part = tree_tc_fits(c, max_tokens * group) ? tree_tc_part_bytes(c)
-                                                          : (size_t)(rows_of(max_tokens, group) / 16) * (c.head_dim / 2 + 4) * 32 * 4;
-  return kTreeMaxCtas * 4 + part * 2 * tree_ctas();
+  const int rows = tree_tc_fits(c, max_tokens * group) ? tree_tc_rows() : rows_of(max_tokens, group);
+  return kTreeMaxCtas * sizeof(int4) + (size_t)tree_part_floats(rows, c.head_dim) * 4 * 2 * tree_ctas();
 }
 
 int read_tree_error(int reset) {
@@ -671,8 +635,8 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   const int rows = rows_of(d.max_tokens, p.group);
   p.scale_log2 = scale * kLog2e;
-  p.counter = static_cast<uint32_t*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kTreeMaxCtas * 4);
+  p.items = static_cast<int4*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kTreeMaxCtas * sizeof(int4));
 
   const auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;

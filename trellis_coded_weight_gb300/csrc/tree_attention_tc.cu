@@ -96,7 +96,6 @@ struct Cfg {
   static constexpr int Slots = Fit > 8 ? 8 : Fit;
   static_assert(Slots >= 4, "keys and values of two tiles");
   static constexpr int Smem = 1024 + Slots * Slot + Fixed;
-  static constexpr int PartFloats = kRows * (D + 2);        // a part: [D/4][256 rows][4], maxima, sums
   // tensor memory columns
   static constexpr int S(int s) { return s * 128; }
   static constexpr int O(int s) { return 256 + s * 128; }
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_ready = s_full + 2;  // [2] weights written, values clean
   uint64_t* o_full = p_ready + 2;  // [2] the segment's last product complete
   uint64_t* drained = o_full + 2;
-  volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] a wait gave up, [1] last to arrive, [2] segment with odd values
+  volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] a wait gave up, [2] segment with odd values
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,82 +221,88 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ---- the thread that issues the products
     if (lane == 0) {
-      bool dead = false;
-      bool issued = false;
-      int it0 = 0, seg = 0, ns[2] = {0, 0};
-      const auto wait = [&](uint64_t* bar, int count) {  // the count-th completion (from 0)
-        if (!dead && !tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns)) {
+      // The tensor cores queue little ahead, so what this thread does between products is kept short: ring places
+      // advance by counting, and most freed tiles are announced by the softmax warps.
+      bool dead = false, issued = false;
+      int seg = 0;
+      uint32_t slot = 0, use = 0;  // the next ring entry
+      uint32_t ns[2] = {0, 0};
+      const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !tc::mbar_wait_short(bar, parity, p.wait_ns)) {
           dead = true;
           flags[0] = 1;
         }
         return !dead;
       };
-      const uint32_t ring32 = tc::smem_u32(ring), q32 = tc::smem_u32(sq);
       const uint32_t id_s = tc::idesc_bf16_f32(128, kTile), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
-      const auto slot_of = [&](int e) { return (it0 + e) % C::Slots; };
-      const auto wait_entry = [&](int e) { return wait(full + slot_of(e), (it0 + e) / C::Slots); };
-      const auto release = [&](int e) { tc::mma_commit(empty + slot_of(e)); };
-      const auto scores = [&](int s, int qtile, int e) {
-        const uint64_t a = tc::desc_kmajor(q32 + qtile * C::QTile, 1024, 2), b = tc::desc_kmajor(ring32 + slot_of(e) * C::Slot, 1024, 2);
+      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
+                     v_desc = desc_mnmajor(tc::smem_u32(ring), kTile * 128);
+      // waits for the next ring entry and steps past it; its place in the descriptors' units
+      const auto take = [&](uint32_t& at) {
+        at = slot * (C::Slot >> 4);
+        const bool ok = wait(full + slot, use & 1u);
+        if (++slot == C::Slots) {
+          slot = 0;
+          ++use;
+        }
+        return ok;
+      };
+      const auto scores = [&](int s, int qtile, uint32_t at) {
+        const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4)), b = k_desc + at;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint64_t step = (uint64_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
+          const uint32_t step = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
           tc::mma_bf16(tmem + C::S(s), a + step, b + step, id_s, k > 0);
         }
         tc::mma_commit(s_full + s);
         issued = true;
       };
-      const auto outputs = [&](int s, int e, bool fresh) {
-        const uint64_t b = desc_mnmajor(ring32 + slot_of(e) * C::Slot, kTile * 128);
+      const auto outputs = [&](int s, uint32_t at, bool fresh) {
+        const uint64_t b = v_desc + at;
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint64_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
+          mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
       };
       while (!dead && walk.next(p, cum, g)) {
         const int n = g.tiles;
-        const Order order{n, rows_of(g) <= 128};
-        if (!wait(q_ready, seg)) break;
+        uint32_t k_at, v_at;
+        if (!wait(q_ready, (uint32_t)(seg & 1))) break;
         tc::fence_after_sync();
-        if (order.split_keys) {
+        if (rows_of(g) <= 128) {
           for (int i = 0; i < 2 && i < n; ++i) {
-            if (!wait_entry(order.key(i))) break;
-            scores(i, 0, order.key(i));
-            release(order.key(i));
+            if (!take(k_at)) break;
+            scores(i, 0, k_at);
           }
           for (int i = 0; i < n && !dead; ++i) {
             const int s = i & 1;
-            if (!wait_entry(order.value(i)) || !wait(p_ready + s, ns[s]++)) break;
+            const bool more = i + 2 < n;
+            const uint32_t v_slot = slot;
+            if (!take(v_at) || !wait(p_ready + s, ns[s] & 1u)) break;
+            ++ns[s];
             tc::fence_after_sync();
-            outputs(s, order.value(i), i < 2);
-            release(order.value(i));
-            if (i + 2 >= n) tc::mma_commit(o_full + s);
-            if (i + 2 < n) {
-              if (!wait_entry(order.key(i + 2))) break;
-              scores(s, 0, order.key(i + 2));
-              release(order.key(i + 2));
-            }
+            outputs(s, v_at, i < 2);
+            tc::mma_commit(empty + v_slot);
+            if (!more) tc::mma_commit(o_full + s);
+            else if (take(k_at)) scores(s, 0, k_at);
           }
         } else {
-          if (!wait_entry(order.key(0))) break;
-          scores(0, 0, order.key(0));
-          scores(1, 1, order.key(0));
-          release(order.key(0));
+          if (!take(k_at)) break;
+          scores(0, 0, k_at);
+          scores(1, 1, k_at);
           for (int i = 0; i < n && !dead; ++i) {
-            if (!wait_entry(order.value(i)) || (i + 1 < n && !wait_entry(order.key(i + 1)))) break;
+            const bool more = i + 1 < n;
+            if (!take(v_at) || (more && !take(k_at))) break;
+#pragma unroll
             for (int s = 0; s < 2; ++s) {
-              if (!wait(p_ready + s, ns[s]++)) break;
+              if (!wait(p_ready + s, ns[s] & 1u)) break;
+              ++ns[s];
               tc::fence_after_sync();
-              outputs(s, order.value(i), i == 0);
-              if (s == 1) release(order.value(i));
-              if (i + 1 == n) tc::mma_commit(o_full + s);
-              if (i + 1 < n) {
-                scores(s, s, order.key(i + 1));
-                if (s == 1) release(order.key(i + 1));
-              }
+              outputs(s, v_at, i == 0);
+              if (more) scores(s, s, k_at);
+              else tc::mma_commit(o_full + s);
             }
           }
         }
-        it0 += 2 * n;
         ++seg;
       }
       // tensor memory is given back once every product issued has completed, also where a wait gave up
@@ -317,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // a scale of 0 too leaves minus infinity where it is
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
     int it0 = 0, seg = 0, ns = 0, no = 0;
+    int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
     bool dead = false;
     const auto wait = [&](uint64_t* bar, int count) {
       const bool ok = dead || tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns);
@@ -354,10 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t seen = row_mask[r];
       float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
       const int first_tile = order.split_keys ? s : 0, tile_step = order.split_keys ? 2 : 1;
+      const auto release = [&](int e) { tc::mbar_arrive(empty + (it0 + e) % C::Slots); };
       bool any = false;
       for (int i = first_tile; i < n; i += tile_step) {
         wait(s_full + s, ns++);
         tc::fence_after_sync();
+        // Scores that are complete free their keys.  Where both streams take every tile, stream 1's products are the
+        // later ones, and complete scores mean that the step before is complete too: its values are free.
+        if (threadIdx.x % 128 == 0 && !dead && (order.split_keys || s == 1)) {
+          release(order.key(i));
+          if (!order.split_keys && i > 0) release(order.value(i - 1));
+        }
         const int pos0 = (g.tile0 + i) * kTile;
         const bool tail = pos0 + kTile > g.seq.prefix;
         if (tail) {
@@ -465,7 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) tc::mbar_arrive(p_ready + s);
       }
       // ---- the segment's end
-      if (any) wait(o_full + s, no++);
+      if (any) {
+        wait(o_full + s, no++);
+        if (threadIdx.x % 128 == 0 && !dead && !order.split_keys && s == 1) release(order.value(n - 1));
+      }
       tc::fence_after_sync();
       it0 += 2 * n;
       const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
@@ -550,63 +566,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
         continue;
       }
-      // a part: [D/4][256 rows][4] sums, then maxima and sums of weights
-      {
-        float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * C::PartFloats;
+      // a part, for the joining kernel
+      float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * tree_part_floats(kRows, D);
 #pragma unroll 1
-        for (int col = col0; col < col0 + cols; col += 32) {
-          float v[32];
-          fetch(col, v);
-          if (valid)
+      for (int col = col0; col < col0 + cols; col += 32) {
+        float v[32];
+        fetch(col, v);
+        if (valid)
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              __stcg(reinterpret_cast<float4*>(part + ((int64_t)(col + j) / 4 * kRows + r) * 4), make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
-        }
-        if (valid && col0 == 0) {
-          __stcg(part + (int64_t)kRows * D + r, m);
-          __stcg(part + (int64_t)kRows * D + kRows + r, l);
-        }
-        tc::fence_before_sync();
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(part + (int64_t)r * D + col + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       }
-      named_sync(1, 256);
-      if (threadIdx.x == 0) flags[1] = tree_arrive(p.counter + g.first, g.last - g.first);
-      named_sync(1, 256);
+      if (valid && col0 == 0) {
+        part[(int64_t)kRows * D + r] = m;
+        part[(int64_t)kRows * D + kRows + r] = l;
+      }
+      tc::fence_before_sync();
+      if (threadIdx.x == 0 && g.first == cta) shared_item = make_int4(g.b, g.head, g.row_block, g.last);
       ++seg;
-      if (!flags[1]) continue;
-      // the last to arrive joins the parts in their order; a thread has one row, and with few rows half of its columns
-      const int parts = g.last - g.first + 1;
-      const auto part_of = [&](int j) { return p.part + (int64_t)tree_slot(g.first + j, j == 0) * C::PartFloats; };
-      float mm = -INFINITY, ll = 0.f;
-      if (valid) {
-        for (int j = 0; j < parts; ++j) mm = fmaxf(mm, __ldcg(part_of(j) + (int64_t)kRows * D + r));
-        const float bm = mm == -INFINITY ? 0.f : mm;
-        for (int j = 0; j < parts; ++j)
-          ll += ex2(__ldcg(part_of(j) + (int64_t)kRows * D + r) - bm) * __ldcg(part_of(j) + (int64_t)kRows * D + kRows + r);
-        const float f = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll 1
-        for (int col = col0; col < col0 + cols; col += 32) {
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
-          for (int j = 0; j < parts; ++j) {
-            const float* part = part_of(j);
-            const float w = ex2(__ldcg(part + (int64_t)kRows * D + r) - bm);
-            float4 u[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)col / 4 + k) * kRows * 4 + r * 4));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              v[4 * k] += w * u[k].x;
-              v[4 * k + 1] += w * u[k].y;
-              v[4 * k + 2] += w * u[k].z;
-              v[4 * k + 3] += w * u[k].w;
-            }
-          }
-          store(col, v, f);
-        }
-        store_lse(mm, ll);
-      }
     }
+    if (threadIdx.x == 0) p.items[cta] = shared_item;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -627,7 +606,8 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cuda
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Smem);
   }, cudaErrorInvalidDevice);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
+  const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
+  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, kRows, 0.f, ctas, st);
 }
 
 }  // namespace
@@ -636,7 +616,7 @@ bool tree_tc_fits(const trellis_cache_t& c, int rows) { return c.dtype == TRELLI
 
 int tree_tc_box_rows(const trellis_cache_t& c) { return c.page_size < kTile ? c.page_size : kTile; }
 
-size_t tree_tc_part_bytes(const trellis_cache_t& c) { return (size_t)kRows * (c.head_dim + 2) * 4; }
+int tree_tc_rows() { return kRows; }
 
 cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st) {
   return head_dim == 64 ? launch_d<64>(map, p, ctas, st) : launch_d<128>(map, p, ctas, st);

@@ -6,8 +6,9 @@
 // tile), are laid end to end and cut into equal contiguous ranges, one per thread block; a step belongs to the range that
 // holds its beginning.  A step has length 1, or (HALVES) 2 where its rows fill more than half a block, since it then
 // takes that kernel twice as long.  An item that falls into one range is finished there.  Otherwise each block
-// writes its part (maximum, sum and unnormalised output of its keys, fp32) to the workspace, and the last one to arrive
-// joins the parts in their order, so results do not depend on timing.
+// writes its part (maximum, sum and unnormalised output of its keys, fp32) to the workspace, and a second launch
+// (tree_join.cu) joins the parts in their order over the whole GPU: results do not depend on timing, and no block has the
+// joining of a long item to itself.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -27,7 +28,7 @@ struct TreeParams {
   const uint64_t* mask;
   const float* scales;  // [2][hkv] of the layer, or null
   const uint16_t* pool; // the layer's pages (bf16 ones)
-  uint32_t* counter;    // [kTreeMaxCtas], zero between calls: arrivals for the item that block c was the first to share
+  int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (sequence or -1, head, row block, last block)
   float* part;          // two slots per thread block
   int64_t q_stride, out_stride;
   int64_t pages;
@@ -146,22 +147,17 @@ struct TreeWalk {
 
 // The workspace slot of a block's part: a block has at most one part that starts its item and one that does not.
 __device__ __forceinline__ int tree_slot(int cta, bool starts_item) { return 2 * cta + (starts_item ? 1 : 0); }
+// A part: unnormalised outputs [rows][dim], maxima [rows] (log2), sums of weights [rows].
+__host__ __device__ constexpr int64_t tree_part_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
 
-// One arrival at the counter of the item's first block (an item that is shared is the last one of the block it starts
-// in, so no two items share a counter, and a workspace serves calls of any sizes); true for the last of the blocks that share the item.  Acquire-release: parts written before (and a
-// barrier) are visible to whoever sees the last count.
-__device__ __forceinline__ bool tree_arrive(uint32_t* counter, int others) {
-  uint32_t old;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
-  if (old != (uint32_t)others) return false;
-  *counter = 0u;
-  return true;
-}
+// Joins the parts of shared items, after a kernel over `ctas` blocks of `rows` rows on the stream (tree_join.cu).  lift: log2 of a
+// factor that the weights carry.
+cudaError_t launch_tree_join(const TreeParams& p, int dim, int rows, float lift, int ctas, cudaStream_t st);
 
 // The tensor-core kernel (tree_attention_tc.cu) and what it takes of the caller.
 bool tree_tc_fits(const trellis_cache_t& c, int rows);
 int tree_tc_box_rows(const trellis_cache_t& c);
-size_t tree_tc_part_bytes(const trellis_cache_t& c);
+int tree_tc_rows();
 cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st);
 int read_tree_tc_error(int reset);
 
