@@ -299,3 +299,33 @@ def test_bounded_waits_run_out_and_the_next_call_is_right():
         tb.set_wait_limit(0)
     got = s.run()
     assert tb.device_error(reset=True) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("hq,hkv,d,toks", [(32, 8, 128, 8), (16, 4, 64, 12), (40, 2, 128, 12)])
+def test_many_items_per_block_in_repeated_calls(hq, hkv, d, toks):
+    """Rings of tiles that go through many items, of one and of two streams' rows, in both orders."""
+    rng = np.random.default_rng(d + toks)
+    lens = [int(x) for x in rng.integers(0, 1500, 70)]
+    counts = [int(x) for x in rng.integers(1, toks + 1, 70)]
+    s = Step(lens, counts, hq, hkv, d, 64, seed=22)
+    first = [t.clone() for t in s.run()]
+    s.check(*first, sequences=range(0, 70, 3))
+    for _ in range(20):
+        got = s.run()
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    assert tb.device_error() == 0
+
+
+def test_bounded_waits_run_out_with_many_rows():
+    s = Step([60000, 300], [16, 4], 32, 8, 128, 64, seed=23)
+    want = [t.clone() for t in s.run()]
+    assert tb.device_error(reset=True) == 0
+    tb.set_wait_limit(200)
+    try:
+        s.run()
+        torch.cuda.synchronize()
+        assert tb.device_error(reset=True) != 0
+    finally:
+        tb.set_wait_limit(0)
+    got = s.run()
+    assert tb.device_error(reset=True) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))

@@ -548,12 +548,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           if constexpr (F8) {
 #pragma unroll
             for (int i = 0; i < D / 8; i += 2)
-              *reinterpret_cast<float4*>(part + r * D + (i >> 1) * 16 + c4 * 4) =
+              *reinterpret_cast<float4*>(part + (((i >> 1) * 4 + c4) * ROWS + r) * 4) =
                   make_float4(o[i][2 * half], o[i + 1][2 * half], o[i][2 * half + 1], o[i + 1][2 * half + 1]);
           } else {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<float2*>(part + r * D + i * 8 + c4 * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+              *reinterpret_cast<float2*>(part + ((i * 2 + (c4 >> 1)) * ROWS + r) * 4 + (c4 & 1) * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
           }
           if (c4 == 0) {
             part[ROWS * D + r] = m[half];

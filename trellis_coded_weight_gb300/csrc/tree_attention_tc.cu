@@ -93,21 +93,23 @@ struct Cfg {
   static constexpr int QTile = 128 * D * 2;
   static constexpr int Fixed = 2 * QTile + kRows * 8 + 4 * 128 * 4 + (kTreeMaxBatch + 4) * 4 + 512;
   static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Slot;
-  static constexpr int Slots = Fit > 8 ? 8 : Fit;
-  static_assert(Slots >= 4, "keys and values of two tiles");
+  static constexpr int Pairs = Fit >= 8 ? 4 : 2;            // tiles in flight, each in a slot for its keys and one for its values
+  static constexpr int Slots = 2 * Pairs;
+  static_assert(Fit >= Slots, "keys and values of two tiles");
   static constexpr int Smem = 1024 + Slots * Slot + Fixed;
   // tensor memory columns
   static constexpr int S(int s) { return s * 128; }
   static constexpr int O(int s) { return 256 + s * 128; }
 };
 
-// Ring positions of tile i's keys and values among a segment's 2n entries, in the order in which they are used.
+// The order in which a segment's 2n entries are copied, which is that of their use: entry e is tile at(e)'s keys or values.
+//
+// Tile i of a segment that begins at the block's tile t0 is in pair (t0 + i) % Pairs, as that pair's use (t0 + i) / Pairs.
+// The number of pairs is even, so the use of a slot before a stream's tile is the same stream's, or of a finished segment:
+// a thread that waits for a phase has seen the one before complete, as waits by parity need.
 struct Order {
   int n;
   bool split_keys;
-  __device__ __forceinline__ int key(int i) const { return !split_keys ? 2 * i : i < 2 ? i : 2 * i - 1; }
-  __device__ __forceinline__ int value(int i) const { return !split_keys ? 2 * i + 1 : i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
-  // entry e: tile and kind
   __device__ __forceinline__ int at(int e, bool* is_value) const {
     if (!split_keys) {
       *is_value = e & 1;
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tmap(&map);
     for (int i = 0; i < C::Slots; ++i) {
       tc::mbar_init(full + i, 1);
-      tc::mbar_init(empty + i, 1);
+      tc::mbar_init(empty + i, 2);  // both streams, or one twice
     }
     tc::mbar_init(q_ready, kSoftmaxWarps);
     for (int s = 0; s < 2; ++s) {
@@ -180,17 +182,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kCopyWarp) {
     // ---- the copying warp
-    int it = 0;
+    int t0 = 0, copied[2] = {0, 0};  // keys, values
     bool dead = false;
     const int box = min(1 << p.page_shift, kTile);  // rows of one copy
     while (!dead && walk.next(p, cum, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const Order order{g.tiles, rows_of(g) <= 128};
-      for (int e = 0; e < 2 * g.tiles && !dead; ++e, ++it) {
+      for (int e = 0; e < 2 * g.tiles; ++e) {
         bool value;
         const int t = order.at(e, &value);
-        const int s = it % C::Slots;
+        const int s = (t0 + t) % C::Pairs * 2 + (value ? 1 : 0), use = (t0 + t) / C::Pairs;
         const int pos = (g.tile0 + t) * kTile + lane * box;  // lane i copies box i of the tile, none past the end
         const bool mine = lane * box < kTile && pos < len;
         int y = 0;
@@ -200,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           y = (((page * 2 + (value ? 1 : 0)) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         }
         const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        if (it >= C::Slots) {
-          const bool ok = tc::mbar_wait_short(empty + s, (uint32_t)((it / C::Slots) & 1) ^ 1u, p.wait_ns);
+        if (use > 0) {
+          const bool ok = tc::mbar_wait_short(empty + s, (uint32_t)(use & 1) ^ 1u, p.wait_ns);
           if (__any_sync(0xFFFFFFFFu, !ok)) {
             dead = true;
             if (lane == 0) flags[0] = 1;
@@ -210,22 +212,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) tc::mbar_arrive_expect_tx(full + s, (uint32_t)(boxes * box * D * 2));
         __syncwarp();
+        copied[value ? 1 : 0] = t0 + t + 1;
         if (mine)
 #pragma unroll
           for (int blk = 0; blk < C::Blocks; ++blk)
             tc::tma_load_2d(ring + s * C::Slot + blk * (kTile * 128) + lane * box * 128, &map, full + s, blk * 64, y);
       }
+      t0 += g.tiles;
     }
     // no copy may land in a block that has left
-    for (int i = it > C::Slots ? it - C::Slots : 0; i < it; ++i) tc::mbar_wait(full + i % C::Slots, (uint32_t)((i / C::Slots) & 1), kDrainNs);
+    for (int kv = 0; kv < 2; ++kv)
+      for (int t = max(0, copied[kv] - C::Pairs); t < copied[kv]; ++t)
+        tc::mbar_wait(full + t % C::Pairs * 2 + kv, (uint32_t)(t / C::Pairs & 1), kDrainNs);
   } else if (warp == kMmaWarp) {
-    // ---- the thread that issues the products
+    // ---- the thread that issues the products.  One thread for both streams: with one each, products of 256 rows measured
+    // 153 us against 135 (1 x 64 drafts, 131072 keys).  The tensor cores queue only a few products ahead, so waits sit behind
+    // products that are still queued where they can.
     if (lane == 0) {
-      // The tensor cores queue little ahead, so what this thread does between products is kept short: ring places
-      // advance by counting, and most freed tiles are announced by the softmax warps.
       bool dead = false, issued = false;
-      int seg = 0;
-      uint32_t slot = 0, use = 0;  // the next ring entry
+      int t0 = 0, seg = 0;
       uint32_t ns[2] = {0, 0};
       const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !tc::mbar_wait_short(bar, parity, p.wait_ns)) {
@@ -237,18 +242,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = tc::idesc_bf16_f32(128, kTile), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
       const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
                      v_desc = desc_mnmajor(tc::smem_u32(ring), kTile * 128);
-      // waits for the next ring entry and steps past it; its place in the descriptors' units
-      const auto take = [&](uint32_t& at) {
-        at = slot * (C::Slot >> 4);
-        const bool ok = wait(full + slot, use & 1u);
-        if (++slot == C::Slots) {
-          slot = 0;
-          ++use;
-        }
-        return ok;
-      };
-      const auto scores = [&](int s, int qtile, uint32_t at) {
-        const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4)), b = k_desc + at;
+      // tile i's slot for keys (0) or values (1), and the wait for it
+      const auto slot_of = [&](int i, uint32_t kv) { return (uint32_t)(t0 + i) % C::Pairs * 2 + kv; };
+      const auto take = [&](int i, uint32_t kv) { return wait(full + slot_of(i, kv), (uint32_t)(t0 + i) / C::Pairs & 1u); };
+      const auto scores = [&](int s, int qtile, int i) {
+        const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4)), b = k_desc + slot_of(i, 0) * (C::Slot >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t step = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
@@ -257,52 +255,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mma_commit(s_full + s);
         issued = true;
       };
-      const auto outputs = [&](int s, uint32_t at, bool fresh) {
-        const uint64_t b = v_desc + at;
+      const auto outputs = [&](int s, int i, bool fresh) {
+        const uint64_t b = v_desc + slot_of(i, 1) * (C::Slot >> 4);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
       };
+      const auto weights = [&](int s) {  // waits for the stream's
+        if (!wait(p_ready + s, ns[s] & 1u)) return false;
+        ++ns[s];
+        tc::fence_after_sync();
+        return true;
+      };
       while (!dead && walk.next(p, cum, g)) {
         const int n = g.tiles;
-        uint32_t k_at, v_at;
         if (!wait(q_ready, (uint32_t)(seg & 1))) break;
         tc::fence_after_sync();
         if (rows_of(g) <= 128) {
-          for (int i = 0; i < 2 && i < n; ++i) {
-            if (!take(k_at)) break;
-            scores(i, 0, k_at);
-          }
-          for (int i = 0; i < n && !dead; ++i) {
+          for (int i = 0; i < 2 && i < n; ++i)
+            if (take(i, 0)) scores(i, 0, i);
+          for (int i = 0; i < n; ++i) {
             const int s = i & 1;
-            const bool more = i + 2 < n;
-            const uint32_t v_slot = slot;
-            if (!take(v_at) || !wait(p_ready + s, ns[s] & 1u)) break;
-            ++ns[s];
-            tc::fence_after_sync();
-            outputs(s, v_at, i < 2);
-            tc::mma_commit(empty + v_slot);
-            if (!more) tc::mma_commit(o_full + s);
-            else if (take(k_at)) scores(s, 0, k_at);
+            if (!take(i, 1) || !weights(s)) break;
+            outputs(s, i, i < 2);
+            tc::mma_commit(empty + slot_of(i, 1));  // its tile alone: free at once, for both counts
+            tc::mma_commit(empty + slot_of(i, 1));
+            if (i + 2 >= n) tc::mma_commit(o_full + s);
+            else if (take(i + 2, 0)) scores(s, 0, i + 2);
           }
         } else {
-          if (!take(k_at)) break;
-          scores(0, 0, k_at);
-          scores(1, 1, k_at);
-          for (int i = 0; i < n && !dead; ++i) {
+          if (!take(0, 0)) break;
+          scores(0, 0, 0);
+          scores(1, 1, 0);
+          if (!take(0, 1)) break;
+          for (int i = 0; i < n; ++i) {
             const bool more = i + 1 < n;
-            if (!take(v_at) || (more && !take(k_at))) break;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (!wait(p_ready + s, ns[s] & 1u)) break;
-              ++ns[s];
-              tc::fence_after_sync();
-              outputs(s, v_at, i == 0);
-              if (more) scores(s, s, k_at);
-              else tc::mma_commit(o_full + s);
+            if (!weights(0)) break;
+            outputs(0, i, i == 0);
+            if (more) {
+              if (!take(i + 1, 0)) break;
+              scores(0, 0, i + 1);
+            } else {
+              tc::mma_commit(o_full);
+            }
+            if (!weights(1)) break;
+            outputs(1, i, i == 0);
+            if (more) {
+              scores(1, 1, i + 1);
+              if (!take(i + 1, 1)) break;
+            } else {
+              tc::mma_commit(o_full + 1);
             }
           }
         }
+        t0 += n;
         ++seg;
       }
       // tensor memory is given back once every product issued has completed, also where a wait gave up
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + C::S(s) + lanes, t_o = tmem + C::O(s) + lanes;
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // a scale of 0 too leaves minus infinity where it is
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
-    int it0 = 0, seg = 0, ns = 0, no = 0;
+    int t0 = 0, seg = 0, ns = 0, no = 0;
     int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
     bool dead = false;
     const auto wait = [&](uint64_t* bar, int count) {
@@ -338,19 +344,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_sync(1, 256);  // the segment before is finished: its queries, statistics and outputs are no longer read
       // ---- queries
       {
-        constexpr int LPR = D / 8;
-        const int qrows = order.split_keys ? 128 : 256;
-        for (int r = threadIdx.x / LPR; r < qrows; r += 256 / LPR) {
-          const int l = threadIdx.x % LPR;
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            u = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
-                                                     (int64_t)(g.head * p.group + hh) * D + 8 * l));
-            u.x ^= flip; u.y ^= flip; u.z ^= flip; u.w ^= flip;
+        constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = D == 128 ? 8 : 4;  // lanes of a row, rows at a time, loads in flight
+        const int qrows = order.split_keys ? 128 : 256, l = threadIdx.x % LPR;
+        for (int r0 = threadIdx.x / LPR; r0 < qrows; r0 += kStep * kMost) {
+          uint4 u[kMost];
+#pragma unroll
+          for (int k = 0; k < kMost; ++k) {
+            const int r = r0 + k * kStep, d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+            u[k] = make_uint4(0, 0, 0, 0);
+            if (r < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
           }
-          *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QTile + (l >> 3) * (128 * 128) + (r & 127) * 128 + (((l & 7) ^ (r & 7)) << 4)) = u;
-          if (l == 0) row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
+#pragma unroll
+          for (int k = 0; k < kMost; ++k) {
+            const int r = r0 + k * kStep;
+            *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QTile + (l >> 3) * (128 * 128) + (r & 127) * 128 + (((l & 7) ^ (r & 7)) << 4)) =
+                make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
+          }
+        }
+        if (threadIdx.x < qrows) {
+          const int r = threadIdx.x, d = (row0 + r) / p.group;
+          row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
         }
         tc::fence_proxy_async_smem();
         named_sync(1, 256);  // masks
@@ -360,16 +373,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t seen = row_mask[r];
       float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
       const int first_tile = order.split_keys ? s : 0, tile_step = order.split_keys ? 2 : 1;
-      const auto release = [&](int e) { tc::mbar_arrive(empty + (it0 + e) % C::Slots); };
+      const auto release = [&](int i, int kv) { tc::mbar_arrive(empty + (t0 + i) % C::Pairs * 2 + kv); };
       bool any = false;
       for (int i = first_tile; i < n; i += tile_step) {
         wait(s_full + s, ns++);
         tc::fence_after_sync();
-        // Scores that are complete free their keys.  Where both streams take every tile, stream 1's products are the
-        // later ones, and complete scores mean that the step before is complete too: its values are free.
-        if (threadIdx.x % 128 == 0 && !dead && (order.split_keys || s == 1)) {
-          release(order.key(i));
-          if (!order.split_keys && i > 0) release(order.value(i - 1));
+        // Scores that are complete free their keys, and, as a stream's products complete in order, the values of its step before.
+        if (threadIdx.x % 128 == 0 && !dead) {
+          release(i, 0);
+          if (order.split_keys) release(i, 0);
+          else if (i > 0) release(i - 1, 1);
         }
         const int pos0 = (g.tile0 + i) * kTile;
         const bool tail = pos0 + kTile > g.seq.prefix;
@@ -447,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tail) {
           // Values that must not reach a product: rows past the end become zeros, whatever their bits; so do numbers of
           // drafts that are not finite (rare), which are added at the end to the rows that see them.
-          wait(full + (it0 + order.value(i)) % C::Slots, (it0 + order.value(i)) / C::Slots);
-          uint8_t* tile = ring + ((it0 + order.value(i)) % C::Slots) * C::Slot;
+          const int slot = (t0 + i) % C::Pairs * 2 + 1;
+          wait(full + slot, (t0 + i) / C::Pairs);
+          uint8_t* tile = ring + slot * C::Slot;
           const int from = max(g.seq.prefix - pos0, 0);
           constexpr int Chunks = D / 8;
           for (int e = from * Chunks + (threadIdx.x & 127); e < kTile * Chunks; e += 128) {
@@ -480,11 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the segment's end
       if (any) {
         wait(o_full + s, no++);
-        if (threadIdx.x % 128 == 0 && !dead && !order.split_keys && s == 1) release(order.value(n - 1));
+        if (threadIdx.x % 128 == 0 && !dead && !order.split_keys) release(n - 1, 1);
       }
       tc::fence_after_sync();
-      it0 += 2 * n;
-      const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+      t0 += n;
       const bool valid = r < rows;
       float wa = 1.f, wb = 0.f;  // weights of the own stream's and the other's outputs
       bool other = false;
@@ -542,27 +555,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       };
-      const auto store = [&](int col, const float (&v)[32], float f) {
-        uint4* at = reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + col);
-#pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          at[j / 8] = make_uint4(pack_bf16x2(v[j] * f, v[j + 1] * f), pack_bf16x2(v[j + 2] * f, v[j + 3] * f),
-                                 pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
-      };
-      const auto store_lse = [&](float mm, float ll) {
-        if (p.lse && col0 == 0)
-          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = ll == 0.f ? -INFINITY : kLn2 * (mm + log2f(ll));
-      };
       if (g.first == g.last) {
+        // finished here: rows go through the queries' place (no longer read) so that a row's numbers are stored together
         const float f = l == 0.f ? 0.f : 1.f / l;
+        uint8_t* stage = sq + (order.split_keys ? 0 : s * C::QTile) + lrow * (D * 2);
 #pragma unroll 1
         for (int col = col0; col < col0 + cols; col += 32) {
           float v[32];
           fetch(col, v);
-          if (valid) store(col, v, f);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8)
+            *reinterpret_cast<uint4*>(stage + ((((col + j) / 8) ^ (lrow & 7)) << 4)) =
+                make_uint4(pack_bf16x2(v[j] * f, v[j + 1] * f), pack_bf16x2(v[j + 2] * f, v[j + 3] * f),
+                           pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
         }
-        if (valid) store_lse(m, l);
+        if (valid && col0 == 0 && p.lse) {
+          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        }
         tc::fence_before_sync();
+        named_sync(1, 256);
+        constexpr int LPR = D / 8;
+        const int ch = threadIdx.x % LPR;
+#pragma unroll 1
+        for (int q = threadIdx.x / LPR; q < rows; q += 256 / LPR) {
+          const int d = (row0 + q) / p.group, hh = (row0 + q) - d * p.group;
+          *reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + 8 * ch) =
+              *reinterpret_cast<const uint4*>(sq + (q >> 7) * C::QTile + (q & 127) * (D * 2) + ((ch ^ (q & 7)) << 4));
+        }
         ++seg;
         continue;
       }
@@ -575,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid)
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(part + (int64_t)r * D + col + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            *reinterpret_cast<float4*>(part + ((int64_t)(col + j) / 4 * kRows + r) * 4) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
       }
       if (valid && col0 == 0) {
         part[(int64_t)kRows * D + r] = m;

@@ -48,11 +48,11 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int 
   const int64_t part_floats = tree_part_floats(prows, D);
   constexpr int LPR = D / 4;  // threads of a row
   const int sharers = parts >= kManyParts ? 4 : 1;
-  const int elems = kThreads / sharers, mine = threadIdx.x / elems, e = threadIdx.x % elems, col = e % LPR * 4;
+  const int elems = kThreads / sharers, step = elems / LPR;  // rows at a time
+  const int mine = threadIdx.x / elems, e = threadIdx.x % elems, row_in = e % step, col = e / step * 4;
   const float vs = p.scales ? __ldg(p.scales + p.hkv + head) : 1.f;
-  const int step = elems / LPR;
   for (int r0 = blockIdx.y * step; r0 < rows; r0 += gridDim.y * step) {
-    const int r = r0 + e / LPR;
+    const int r = r0 + row_in;
     State s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (r < rows)
       for (int j0 = mine; j0 < parts; j0 += sharers * kBatch) {
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int 
             const float* part = p.part + (int64_t)tree_slot(first + j, j == 0) * part_floats;
             m[b] = __ldcg(part + (int64_t)prows * D + r);
             l[b] = __ldcg(part + (int64_t)prows * D + prows + r);
-            o[b] = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)r * D + col));
+            o[b] = __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)(col / 4) * prows + r) * 4));
           }
         }
         float mx = s.m;

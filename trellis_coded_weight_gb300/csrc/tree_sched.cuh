@@ -147,7 +147,7 @@ struct TreeWalk {
 
 // The workspace slot of a block's part: a block has at most one part that starts its item and one that does not.
 __device__ __forceinline__ int tree_slot(int cta, bool starts_item) { return 2 * cta + (starts_item ? 1 : 0); }
-// A part: unnormalised outputs [rows][dim], maxima [rows] (log2), sums of weights [rows].
+// A part: unnormalised outputs [dim / 4][rows][4], maxima [rows] (log2), sums of weights [rows].
 __host__ __device__ constexpr int64_t tree_part_floats(int rows, int dim) { return (int64_t)rows * (dim + 2); }
 
 // Joins the parts of shared items, after a kernel over `ctas` blocks of `rows` rows on the stream (tree_join.cu).  lift: log2 of a
