@@ -301,13 +301,14 @@ def test_bounded_waits_run_out_and_the_next_call_is_right():
     assert tb.device_error(reset=True) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-@pytest.mark.parametrize("hq,hkv,d,toks", [(32, 8, 128, 8), (16, 4, 64, 12), (40, 2, 128, 12)])
-def test_many_items_per_block_in_repeated_calls(hq, hkv, d, toks):
+@pytest.mark.parametrize("hq,hkv,d,toks,f8", [(32, 8, 128, 8, False), (16, 4, 64, 12, False), (40, 2, 128, 12, False),
+                                               (16, 2, 256, 4, True), (16, 2, 256, 9, False), (40, 4, 128, 12, True), (16, 2, 64, 20, True)])
+def test_many_items_per_block_in_repeated_calls(hq, hkv, d, toks, f8):
     """Rings of tiles that go through many items, of one and of two streams' rows, in both orders."""
     rng = np.random.default_rng(d + toks)
     lens = [int(x) for x in rng.integers(0, 1500, 70)]
     counts = [int(x) for x in rng.integers(1, toks + 1, 70)]
-    s = Step(lens, counts, hq, hkv, d, 64, seed=22)
+    s = Step(lens, counts, hq, hkv, d, 64, f8, seed=22)
     first = [t.clone() for t in s.run()]
     s.check(*first, sequences=range(0, 70, 3))
     for _ in range(20):
@@ -316,8 +317,9 @@ def test_many_items_per_block_in_repeated_calls(hq, hkv, d, toks):
     assert tb.device_error() == 0
 
 
-def test_bounded_waits_run_out_with_many_rows():
-    s = Step([60000, 300], [16, 4], 32, 8, 128, 64, seed=23)
+@pytest.mark.parametrize("f8", [False, True])
+def test_bounded_waits_run_out_with_many_rows(f8):
+    s = Step([60000, 300], [16, 4], 32, 8, 128, 64, f8, seed=23)
     want = [t.clone() for t in s.run()]
     assert tb.device_error(reset=True) == 0
     tb.set_wait_limit(200)

@@ -31,6 +31,7 @@ namespace {
 __device__ int g_tree_error = 0;  // set when a bounded wait gives up (trellis_device_error)
 
 constexpr uint64_t kDrainNs = 2000000000ull;  // for copies in flight when a block leaves
+constexpr int kRows = 16;  // rows of a block
 constexpr int kTile = 64;  // keys per step
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -77,27 +78,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 
 __device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 
-template <int D, bool F8, int ROWS>
+template <int D, bool F8>
 struct Cfg {
-  static constexpr int WR = ROWS / 16;              // warps along the rows
-  static constexpr int WK = ROWS == 64 ? 2 : 4;     // warps along the keys of a tile
+  static constexpr int WK = 4;                      // warps, along the keys of a tile
   static constexpr int KW = kTile / WK;             // keys of a warp per tile
-  static constexpr int Consumers = WR * WK;         // warps
+  static constexpr int Consumers = WK;
   static constexpr int Threads = (Consumers + 1) * 32;
   static constexpr int RowBytes = D * (F8 ? 1 : 2);  // a key or value
   static constexpr int BoxBytes = RowBytes < 128 ? RowBytes : 128;  // of it in one copy: a swizzled row
   static constexpr int Blocks = RowBytes / BoxBytes;
   static constexpr int HalfStage = kTile * RowBytes;  // the keys, or the values, of a tile
   static constexpr int Stage = 2 * HalfStage;
-  static constexpr int QBytes = ROWS * D * 2;
+  static constexpr int QBytes = kRows * D * 2;
   static constexpr int Regs = D / 2;                 // output numbers of a lane
   // fp16 weights are lifted to 2^15 at most, so that small ones do not vanish below its smallest numbers
   static constexpr float Lift = F8 ? 15.f : 0.f;
-  static constexpr int JoinTurns = D == 256 ? 2 : 1;  // wide heads join their outputs in two turns, to fit
-  static constexpr int JoinSlot = (Regs / JoinTurns + 4) * 32;
-  static constexpr int Join = WR * (WK / 2) * JoinSlot * 4;
+  static constexpr int JoinSlot = (Regs + 4) * 32;   // a warp's outputs, maxima and sums
+  static constexpr int Join = WK / 2 * JoinSlot * 4;
   static constexpr int Cum = (kTreeMaxBatch + 4) * 4;
-  static constexpr int Fixed = QBytes + Join + ROWS * 8 + ROWS * 4 + Cum + 256;
+  static constexpr int Fixed = QBytes + Join + kRows * 8 + kRows * 4 + Cum + 256;
   static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Stage;
   static constexpr int Stages = Fit > 8 ? 8 : Fit;
   static_assert(Stages >= 2, "two tiles in flight at least");
@@ -113,18 +112,18 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
     return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
 }
 
-template <int D, bool F8, int ROWS>
-__global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
+template <int D, bool F8>
+__global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
-  using C = Cfg<D, F8, ROWS>;
+  using C = Cfg<D, F8>;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* stages = base;
   uint8_t* sq = stages + C::Stages * C::Stage;
   float* join = reinterpret_cast<float*>(sq + C::QBytes);
   uint64_t* row_mask = reinterpret_cast<uint64_t*>(join + C::Join / 4);
-  float* row_fac = reinterpret_cast<float*>(row_mask + ROWS);
-  int* cum = reinterpret_cast<int*>(row_fac + ROWS);
+  float* row_fac = reinterpret_cast<float*>(row_mask + kRows);
+  int* cum = reinterpret_cast<int*>(row_fac + kRows);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cum) + C::Cum);
   uint64_t* empty = full + C::Stages;
   volatile int* flags = reinterpret_cast<volatile int*>(empty + C::Stages);  // [0] a wait gave up
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     tc::fence_mbar_init();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<ROWS, kTile, false>(p, cum);
+  if (warp == 0) tree_cumulate<kRows, kTile, false>(p, cum);
   __syncthreads();
   const int total = cum[p.batch];
   const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
@@ -151,7 +150,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     return;
   }
 
-  TreeWalk<ROWS, kTile, false> walk(total, ctas, cta);
+  TreeWalk<kRows, kTile, false> walk(total, ctas, cta);
   TreeSegment g;
   if (warp == C::Consumers) {
     // ---- the copying warp: every tile of the range, as many ahead as there are stages
@@ -202,20 +201,20 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
     for (int i = issued > C::Stages ? issued - C::Stages : 0; i < issued; ++i)
       tc::mbar_wait(full + i % C::Stages, (uint32_t)((i / C::Stages) & 1), kDrainNs);
   } else {
-    const int wr = warp / C::WK, wk = warp % C::WK;
+    const int wk = warp;
     const int gq = lane >> 2, c4 = lane & 3;  // fragment row and column pair
     const int nthr = C::Consumers * 32;
     int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
     int it = 0;
     bool dead = false;
     while (walk.next(p, cum, g)) {
-      const int rows = min(ROWS, g.seq.count * p.group - g.row_block * ROWS);  // rows of this block that exist
-      const int row0 = g.row_block * ROWS;
+      const int rows = min(kRows, g.seq.count * p.group - g.row_block * kRows);  // rows of this block that exist
+      const int row0 = g.row_block * kRows;
       named_sync(1, nthr);  // the previous segment's queries are no longer read
       // ---- queries: row r is draft (row0 + r) / group, head (row0 + r) % group of the key/value head's group
       {
         constexpr int LPR = D / 8;  // lanes of a row
-        for (int r = threadIdx.x / LPR; r < ROWS; r += nthr / LPR) {
+        for (int r = threadIdx.x / LPR; r < kRows; r += nthr / LPR) {
           const int l = threadIdx.x % LPR;
           const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
           uint4 u = make_uint4(0, 0, 0, 0);
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
       uint64_t seen[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = wr * 16 + gq + 8 * i;
+        const int r = gq + 8 * i;
         rc[i] = p.scale_log2 * row_fac[r] * (F8 && p.scales ? __ldg(p.scales + g.head) : 1.f);
         seen[i] = row_mask[r];
       }
@@ -266,13 +265,13 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           const int chunk = 2 * ks + (c4 >> 1);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = wr * 16 + gq + 8 * i;
+            const int r = gq + 8 * i;
             const uint2 v = *reinterpret_cast<const uint2*>(sq + r * (D * 2) + ((chunk ^ (r & 7)) << 4) + (c4 & 1) * 8);
             a[i] = v.x;
             a[2 + i] = v.y;
           }
         } else {
-          const int r = wr * 16 + (lane & 15), chunk = 2 * ks + (lane >> 4);
+          const int r = (lane & 15), chunk = 2 * ks + (lane >> 4);
           ldsm4(a, sq32 + r * (D * 2) + ((chunk ^ (r & 7)) << 4));
         }
       };
@@ -475,40 +474,34 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
       }
 #pragma unroll
       for (int step = C::WK / 2; step; step >>= 1) {
-        constexpr int NT = C::Regs / C::JoinTurns;
-        float* mine = join + (wr * (C::WK / 2) + (wk & (step - 1))) * C::JoinSlot + lane;
-        float a[2], b[2];
+        float* mine = join + (wk & (step - 1)) * C::JoinSlot + lane;
+        if (wk >= step && wk < 2 * step) {
 #pragma unroll
-        for (int turn = 0; turn < C::JoinTurns; ++turn) {
-          if (wk >= step && wk < 2 * step) {
+          for (int i = 0; i < C::Regs; ++i) mine[i * 32] = o[i >> 2][i & 3];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mine[i * 32] = o[(turn * NT + i) >> 2][i & 3];
-            if (turn == 0)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mine[(NT + i) * 32] = m[i];
-                mine[(NT + 2 + i) * 32] = l[i];
-              }
+          for (int i = 0; i < 2; ++i) {
+            mine[(C::Regs + i) * 32] = m[i];
+            mine[(C::Regs + 2 + i) * 32] = l[i];
           }
-          named_sync(1, nthr);
-          if (wk < step) {
-            if (turn == 0)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float om = mine[(NT + i) * 32], nm = fmaxf(m[i], om), base_m = nm == -INFINITY ? 0.f : nm;
-                a[i] = ex2(m[i] - base_m);
-                b[i] = ex2(om - base_m);
-                l[i] = l[i] * a[i] + mine[(NT + 2 + i) * 32] * b[i];
-                m[i] = nm;
-              }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              float& v = o[(turn * NT + i) >> 2][i & 3];
-              v = v * a[(i >> 1) & 1] + mine[i * 32] * b[(i >> 1) & 1];
-            }
-          }
-          named_sync(1, nthr);
         }
+        named_sync(1, nthr);
+        if (wk < step) {
+          float a[2], b[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float om = mine[(C::Regs + i) * 32], nm = fmaxf(m[i], om), base_m = nm == -INFINITY ? 0.f : nm;
+            a[i] = ex2(m[i] - base_m);
+            b[i] = ex2(om - base_m);
+            l[i] = l[i] * a[i] + mine[(C::Regs + 2 + i) * 32] * b[i];
+            m[i] = nm;
+          }
+#pragma unroll
+          for (int i = 0; i < C::Regs; ++i) {
+            float& v = o[i >> 2][i & 3];
+            v = v * a[(i >> 1) & 1] + mine[i * 32] * b[(i >> 1) & 1];
+          }
+        }
+        named_sync(1, nthr);
       }
 
       if (g.first == g.last) {
@@ -516,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
           const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const int r = wr * 16 + gq + 8 * half;
+            const int r = gq + 8 * half;
             if (r >= rows) continue;
             const float f = l[half] == 0.f ? 0.f : vs / l[half];
             const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
@@ -540,24 +533,24 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
       }
       // a part, for the joining kernel
       if (wk == 0) {
-        float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * tree_part_floats(ROWS, D);
+        float* part = p.part + (int64_t)tree_slot(cta, g.tile0 == 0) * tree_part_floats(kRows, D);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int r = wr * 16 + gq + 8 * half;
+          const int r = gq + 8 * half;
           if (r >= rows) continue;
           if constexpr (F8) {
 #pragma unroll
             for (int i = 0; i < D / 8; i += 2)
-              *reinterpret_cast<float4*>(part + (((i >> 1) * 4 + c4) * ROWS + r) * 4) =
+              *reinterpret_cast<float4*>(part + (((i >> 1) * 4 + c4) * kRows + r) * 4) =
                   make_float4(o[i][2 * half], o[i + 1][2 * half], o[i][2 * half + 1], o[i + 1][2 * half + 1]);
           } else {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-              *reinterpret_cast<float2*>(part + ((i * 2 + (c4 >> 1)) * ROWS + r) * 4 + (c4 & 1) * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
+              *reinterpret_cast<float2*>(part + ((i * 2 + (c4 >> 1)) * kRows + r) * 4 + (c4 & 1) * 2) = make_float2(o[i][2 * half], o[i][2 * half + 1]);
           }
           if (c4 == 0) {
-            part[ROWS * D + r] = m[half];
-            part[ROWS * D + ROWS + r] = l[half];
+            part[kRows * D + r] = m[half];
+            part[kRows * D + kRows + r] = l[half];
           }
         }
       }
@@ -571,17 +564,12 @@ __global__ void __launch_bounds__(Cfg<D, F8, ROWS>::Threads, 1)
 
 // ---------------------------------------------------------------- host
 
-int rows_of(int max_tokens, int group) {
-  const int rows = max_tokens * group;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
 int tree_ctas() { return device_sm_count() < kTreeMaxCtas ? device_sm_count() : kTreeMaxCtas; }
 
-template <int D, bool F8, int ROWS>
-cudaError_t launch_rows(const CUtensorMap& map, const TreeParams& p, cudaStream_t st) {
-  using C = Cfg<D, F8, ROWS>;
-  auto kern = tree_kernel<D, F8, ROWS>;
+template <int D, bool F8>
+cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, cudaStream_t st) {
+  using C = Cfg<D, F8>;
+  auto kern = tree_kernel<D, F8>;
   static PerDevice<cudaError_t> attr_of;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
@@ -590,14 +578,7 @@ cudaError_t launch_rows(const CUtensorMap& map, const TreeParams& p, cudaStream_
   }, cudaErrorInvalidDevice);
   if (e != cudaSuccess) return e;
   const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)tree_ctas()), dim3(C::Threads), C::Smem, st, map, p);
-  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, ROWS, C::Lift, tree_ctas(), st);
-}
-
-template <int D, bool F8>
-cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int rows, cudaStream_t st) {
-  if (rows == 16) return launch_rows<D, F8, 16>(map, p, st);
-  if (rows == 32) return launch_rows<D, F8, 32>(map, p, st);
-  return launch_rows<D, F8, 64>(map, p, st);
+  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, kRows, C::Lift, tree_ctas(), st);
 }
 
 }  // namespace
@@ -605,7 +586,8 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int rows, cuda
 size_t tree_workspace_bytes(const trellis_cache_t& c, int batch, int max_tokens, int q_heads) {
   (void)batch;  // parts belong to thread blocks, whatever the batch
   const int group = q_heads / c.heads;
-  const int rows = tree_tc_fits(c, max_tokens * group) ? tree_tc_rows() : rows_of(max_tokens, group);
+  const int most = max_tokens * group;
+  const int rows = tree_tc_fits(c, most) ? tree_tc_rows() : tree_tc1_fits(c, most) ? tree_tc1_rows() : kRows;
   return kTreeMaxCtas * sizeof(int4) + (size_t)tree_part_floats(rows, c.head_dim) * 4 * 2 * tree_ctas();
 }
 
@@ -616,8 +598,8 @@ int read_tree_error(int reset) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_tree_error, &zero, sizeof(int)) != cudaSuccess) return -1;
   }
-  const int w = read_tree_tc_error(reset);
-  return v ? v : w;
+  const int w = read_tree_tc_error(reset), x = read_tree_tc1_error(reset);
+  return v ? v : w ? w : x;
 }
 
 cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,
@@ -633,36 +615,39 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   p.batch = d.batch; p.width = d.width; p.n = d.n; p.max_tokens = d.max_tokens;
   p.hq = q_heads; p.hkv = c.heads; p.group = q_heads / c.heads;
   p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
-  const int rows = rows_of(d.max_tokens, p.group);
   p.scale_log2 = scale * kLog2e;
   p.items = static_cast<int4*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kTreeMaxCtas * sizeof(int4));
 
   const auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
-  const bool f8 = c.dtype == TRELLIS_E4M3, tc = tree_tc_fits(c, d.max_tokens * p.group);
-  const int elem = (int)cache_elem_bytes(c), row_bytes = c.head_dim * elem, inner = row_bytes < 128 ? row_bytes : 128;
+  const int most = d.max_tokens * p.group, elem = (int)cache_elem_bytes(c), row_bytes = c.head_dim * elem;
+  const bool f8 = c.dtype == TRELLIS_E4M3, tc = tree_tc_fits(c, most), tc1 = tree_tc1_fits(c, most);
+  TreeBox copy{c.page_size < kTile ? c.page_size : kTile, row_bytes < 128 ? row_bytes : 128, true};
+  if (tc) tree_tc_box(c, &copy);
+  if (tc1) tree_tc1_box(c, &copy);
   uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
-  // the layer's rows of head_dim numbers; a copy takes up to 128 bytes of each of one page's rows (at most a tile)
   CUtensorMap map;
   const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.pages * 2 * c.heads * c.page_size)};
   const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)(inner / elem), (cuuint32_t)(tc ? tree_tc_box_rows(c) : c.page_size < kTile ? c.page_size : kTile)};
+  const cuuint32_t box[2] = {(cuuint32_t)(copy.bytes / elem), (cuuint32_t)copy.rows};
   const cuuint32_t estr[2] = {1, 1};
   if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, 
+         !copy.swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : copy.bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   p.pool = reinterpret_cast<const uint16_t*>(pool);
-  if (tc) return launch_tree_tc(map, p, c.head_dim, tree_ctas(), st);
+  if (tc) return launch_tree_tc(map, p, c, tree_ctas(), st);
+  if (tc1) return launch_tree_tc1(map, p, c, tree_ctas(), st);
   if (f8) {
-    if (c.head_dim == 64) return launch_d<64, true>(map, p, rows, st);
-    if (c.head_dim == 128) return launch_d<128, true>(map, p, rows, st);
-    return launch_d<256, true>(map, p, rows, st);
+    if (c.head_dim == 64) return launch_d<64, true>(map, p, st);
+    if (c.head_dim == 128) return launch_d<128, true>(map, p, st);
+    return launch_d<256, true>(map, p, st);
   }
-  if (c.head_dim == 64) return launch_d<64, false>(map, p, rows, st);
-  if (c.head_dim == 128) return launch_d<128, false>(map, p, rows, st);
-  return launch_d<256, false>(map, p, rows, st);
+  if (c.head_dim == 64) return launch_d<64, false>(map, p, st);
+  if (c.head_dim == 128) return launch_d<128, false>(map, p, st);
+  return launch_d<256, false>(map, p, st);
 }
 
 }  // namespace trellis

@@ -21,70 +21,19 @@
 #include "serving.h"
 #include "tc_ptx.cuh"
 #include "tree_sched.cuh"
+#include "tree_tc.cuh"
 
 namespace trellis {
 namespace {
 
+using namespace tree;
+
 __device__ int g_tree_tc_error = 0;  // set when a bounded wait gives up (trellis_device_error)
 
-constexpr uint64_t kDrainNs = 2000000000ull;  // for copies and products in flight when a block leaves
 constexpr int kTile = 128;                    // keys per step
 constexpr int kRows = 256;                    // rows of a block
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;  // two softmax warpgroups; one for the copying and the issuing warp, and two that idle
-constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kMove = 8.f;                  // log2 of the growth that moves a row's maximum
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
-
-// D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulate.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// This warp's 32 lanes x 16 (32) consecutive columns from registers.
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Operand whose rows are the reduction index (values: [key][head dim]) in the 128-byte swizzle: 64 numbers of a row
-// are contiguous; `lbo` bytes from one such block of columns to the next, 1024 bytes from 8 rows to the next 8.
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-constexpr uint32_t kBMnMajor = 1u << 16;  // instruction descriptor: B's rows are the reduction index
 
 template <int D>
 struct Cfg {
@@ -102,26 +51,9 @@ struct Cfg {
   static constexpr int O(int s) { return 256 + s * 128; }
 };
 
-// The order in which a segment's 2n entries are copied, which is that of their use: entry e is tile at(e)'s keys or values.
-//
 // Tile i of a segment that begins at the block's tile t0 is in pair (t0 + i) % Pairs, as that pair's use (t0 + i) / Pairs.
 // The number of pairs is even, so the use of a slot before a stream's tile is the same stream's, or of a finished segment:
 // a thread that waits for a phase has seen the one before complete, as waits by parity need.
-struct Order {
-  int n;
-  bool split_keys;
-  __device__ __forceinline__ int at(int e, bool* is_value) const {
-    if (!split_keys) {
-      *is_value = e & 1;
-      return e >> 1;
-    }
-    if (e < 2 && e < n) { *is_value = false; return e; }
-    if (e == 2 * n - 1) { *is_value = true; return n - 1; }
-    *is_value = !(e & 1);
-    return e & 1 ? (e + 1) / 2 : (e - 2) / 2;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
@@ -259,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t b = v_desc + slot_of(i, 1) * (C::Slot >> 4);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_bf16_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
+          mma_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
       };
       const auto weights = [&](int s) {  // waits for the stream's
         if (!wait(p_ready + s, ns[s] & 1u)) return false;
@@ -634,12 +566,16 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cuda
 
 bool tree_tc_fits(const trellis_cache_t& c, int rows) { return c.dtype == TRELLIS_BF16 && c.head_dim <= 128 && rows > 16; }
 
-int tree_tc_box_rows(const trellis_cache_t& c) { return c.page_size < kTile ? c.page_size : kTile; }
-
 int tree_tc_rows() { return kRows; }
 
-cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st) {
-  return head_dim == 64 ? launch_d<64>(map, p, ctas, st) : launch_d<128>(map, p, ctas, st);
+void tree_tc_box(const trellis_cache_t& c, TreeBox* b) {
+  b->rows = c.page_size < kTile ? c.page_size : kTile;
+  b->bytes = 128;
+  b->swizzled = true;
+}
+
+cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st) {
+  return c.head_dim == 64 ? launch_d<64>(map, p, ctas, st) : launch_d<128>(map, p, ctas, st);
 }
 
 int read_tree_tc_error(int reset) {

@@ -154,11 +154,23 @@ __host__ __device__ constexpr int64_t tree_part_floats(int rows, int dim) { retu
 // factor that the weights carry.
 cudaError_t launch_tree_join(const TreeParams& p, int dim, int rows, float lift, int ctas, cudaStream_t st);
 
-// The tensor-core kernel (tree_attention_tc.cu) and what it takes of the caller.
-bool tree_tc_fits(const trellis_cache_t& c, int rows);
-int tree_tc_box_rows(const trellis_cache_t& c);
+// One copy of a cache's tensor map: rows of head_dim numbers, bytes of each, and the layout in shared memory (128-byte swizzle
+// or rows end to end).
+struct TreeBox {
+  int rows, bytes;
+  bool swizzled;
+};
+
+// The tensor-core kernels: where they take a call, the rows of their blocks, and what they need copied.
+bool tree_tc_fits(const trellis_cache_t& c, int rows);  // tree_attention_tc.cu
 int tree_tc_rows();
-cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, int head_dim, int ctas, cudaStream_t st);
+void tree_tc_box(const trellis_cache_t& c, TreeBox* b);
+cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st);
 int read_tree_tc_error(int reset);
+bool tree_tc1_fits(const trellis_cache_t& c, int rows);  // tree_attention_tc1.cu
+int tree_tc1_rows();
+void tree_tc1_box(const trellis_cache_t& c, TreeBox* b);
+cudaError_t launch_tree_tc1(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st);
+int read_tree_tc1_error(int reset);
 
 }  // namespace trellis

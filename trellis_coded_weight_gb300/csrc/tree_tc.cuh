@@ -1,0 +1,88 @@
+// tree_tc.cuh -- what the tree attention kernels on the 5th-generation tensor cores share (tree_attention_tc.cu,
+// tree_attention_tc1.cu): the forms of the tensor-memory instructions that only they use, and the order of their copies.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "tc_ptx.cuh"
+#include "tree_sched.cuh"
+
+namespace trellis {
+namespace tree {
+
+constexpr uint64_t kDrainNs = 2000000000ull;  // for copies and products in flight when a block leaves
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kMove = 8.f;                  // log2 of the growth that moves a row's maximum
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs (both bf16 or both fp16, as the descriptor says), fp32 accumulate.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// This warp's 32 lanes x 16 (32) consecutive columns from registers.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Operand whose rows are the reduction index (values: [key][head dim]) in the 128-byte swizzle: 64 numbers of a row
+// are contiguous; `lbo` bytes from one such block of columns to the next, 1024 bytes from 8 rows to the next 8.
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kBMnMajor = 1u << 16;  // instruction descriptor: B's rows are the reduction index
+
+
+// The order in which a segment's 2n entries are copied, which is that of their use: entry e is tile at(e)'s keys or
+// values.  split_keys: the keys of two tiles come before the first one's values.
+struct Order {
+  int n;
+  bool split_keys;
+  __device__ __forceinline__ int at(int e, bool* is_value) const {
+    if (!split_keys) {
+      *is_value = e & 1;
+      return e >> 1;
+    }
+    if (e < 2 && e < n) { *is_value = false; return e; }
+    if (e == 2 * n - 1) { *is_value = true; return n - 1; }
+    *is_value = !(e & 1);
+    return e & 1 ? (e + 1) / 2 : (e - 2) / 2;
+  }
+};
+
+
+}  // namespace tree
+}  // namespace trellis
