@@ -623,7 +623,7 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   if (!fn) return cudaErrorNotSupported;
   const int most = d.max_tokens * p.group, elem = (int)cache_elem_bytes(c), row_bytes = c.head_dim * elem;
   const bool f8 = c.dtype == TRELLIS_E4M3, tc = tree_tc_fits(c, most), tc1 = tree_tc1_fits(c, most);
-  TreeBox copy{c.page_size < kTile ? c.page_size : kTile, row_bytes < 128 ? row_bytes : 128, true};
+  TreeBox copy{c.page_size < kTile ? c.page_size : kTile, row_bytes < 128 ? row_bytes : 128};
   if (tc) tree_tc_box(c, &copy);
   if (tc1) tree_tc1_box(c, &copy);
   uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
@@ -633,8 +633,8 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   const cuuint32_t box[2] = {(cuuint32_t)(copy.bytes / elem), (cuuint32_t)copy.rows};
   const cuuint32_t estr[2] = {1, 1};
   if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, 
-         !copy.swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : copy.bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+         CU_TENSOR_MAP_INTERLEAVE_NONE,
+         copy.bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   p.pool = reinterpret_cast<const uint16_t*>(pool);

@@ -110,8 +110,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto rows_of = [&](const TreeSegment& x) { return min(kRows, x.seq.count * p.group - x.row_block * kRows); };
 
   if (warp >= kSoftmaxWarps) {
-  // 384 threads x 168 registers at launch = 256 x 200 + 128 x 104
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == kCopyWarp) {
     // ---- the copying warp
     int t0 = 0, copied[2] = {0, 0};  // keys, values
@@ -252,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax: stream s, one thread per row; warp w of a group reaches tensor memory lanes 32 w ..
     const int s = warp >> 2, lrow = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -338,20 +335,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st_wait();
         }
-        // ---- the row's maximum; the scores stay in registers
-        uint32_t x[4][32];
+        // ---- the row's maximum.  Both passes over the scores are loops over 32 columns: reading tensor memory twice costs
+        // less than the registers and the code of a step held whole
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int w = 0; w < kTile / 32; ++w) {
+          uint32_t x[32];
+          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+          tc::tmem_ld_wait();
+          float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) tc::tmem_ld_32x32b_x32(t_s + 32 * w, x[w]);
-        tc::tmem_ld_wait();
-        float mw[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          float a = __uint_as_float(x[w][0]);
-#pragma unroll
-          for (int j = 1; j < 31; j += 2) a = fmaxf(fmaxf(a, __uint_as_float(x[w][j])), __uint_as_float(x[w][j + 1]));
-          mw[w] = fmaxf(a, __uint_as_float(x[w][31]));
+          for (int j = 2; j < 30; j += 4) {
+            a = fmaxf(fmaxf(a, __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
+            b = fmaxf(fmaxf(b, __uint_as_float(x[j + 2])), __uint_as_float(x[j + 3]));
+          }
+          mx = fmaxf(mx, fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))));
         }
-        float mx = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
         mx *= c;
         const bool move = mx > m + kMove || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, move)) {
@@ -374,12 +373,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- weights, over the scores
         const float ms = m == -INFINITY ? 0.f : -m;
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t e[16];
+#pragma unroll 1
+        for (int w = 0; w < kTile / 32; ++w) {
+          uint32_t x[32], e[16];
+          tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+          tc::tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[w][j]), __uint_as_float(x[w][j + 1])), make_float2(c, c), make_float2(ms, ms));
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(c, c), make_float2(ms, ms));
             y.x = ex2(y.x);
             y.y = ex2(y.y);
             sum = __fadd2_rn(sum, y);
@@ -571,7 +572,6 @@ int tree_tc_rows() { return kRows; }
 void tree_tc_box(const trellis_cache_t& c, TreeBox* b) {
   b->rows = c.page_size < kTile ? c.page_size : kTile;
   b->bytes = 128;
-  b->swizzled = true;
 }
 
 cudaError_t launch_tree_tc(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st) {

@@ -6,11 +6,11 @@
 // maximum in use is one per row: the warp that has tile i hands its rows' maxima to the warp that has tile i + 1 (an mbarrier
 // per warp), before it makes its weights; the groups' sums of weights stay apart until the end.
 //
-// An e4m3 cache is copied as it is, and a warpgroup of its own turns each tile into fp16 in the layout that the MMAs read
-// (exact: 2 bytes of shared memory per number instead of 1, but the products see 16-bit operands and Q keeps its 8
-// significant bits).  Q is fp16 then, each row scaled by a power of two, and P fp16 too.  That group also clears what
-// must not reach a product.
-// Bound: HBM for a cache of 16-bit numbers; the products and the conversion come near it with e4m3.
+// An e4m3 cache is copied as it is.  The scores' MMAs read its keys as they are: Q's 8 significant bits are split exactly into
+// two e4m3 numbers of 4 (each row scaled by a power of two first), S = Qhi K^T + Qlo K^T at twice the 16-bit rate.  The
+// values become fp16 in shared memory, by a warpgroup of its own (exact), since weights of 4 bits would not do; P is fp16
+// then.  That group also clears what must not reach a product.
+// Bound: HBM for a cache of 16-bit numbers; with e4m3 the conversion of the values comes near it.
 #include <cstring>
 #include <cuda.h>
 
@@ -48,22 +48,37 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
 template <int D, bool F8>
 struct Cfg {
   static constexpr int Tile = D == 256 ? 64 : 128;          // keys per step
-  static constexpr int Blocks = D / 64;                     // 128-byte blocks of a row of 16-bit numbers
-  static constexpr int Slot = Tile * D * 2;                 // the keys, or the values, of a tile
-  static constexpr int QTile = kRows * D * 2;
-  static constexpr int RawSlot = Tile * D;
+  static constexpr int KBytes = D * (F8 ? 1 : 2);           // a key
+  static constexpr int KBlock = KBytes < 128 ? KBytes : 128;  // of it in one swizzled row
+  static constexpr int KSlot = Tile * KBytes;
+  static constexpr int VSlot = Tile * D * 2;                // a tile's values, 16 bits
+  static constexpr int RSlot = F8 ? Tile * D : 0;           // as the cache has them
+  static constexpr int QBytes = kRows * D * 2;              // bf16, or two e4m3 halves
   static constexpr int Threads = F8 ? 512 : 384;
-  static constexpr int Fixed = QTile + kRows * 8 + kRows * 4 * 4 + (kTreeMaxBatch + 4) * 4 + 1024;
-  static constexpr int Room = 227 * 1024 - 1024 - Fixed;
-  static constexpr int Slots = D == 256 && F8 ? 3 : D == 64 ? 6 : 4;
-  static constexpr int RawFit = (Room - Slots * Slot) / RawSlot;
-  static constexpr int RawSlots = F8 ? (RawFit > 8 ? 8 : RawFit) : 0;
-  static_assert(Slots * Slot <= Room && (!F8 || RawSlots >= 3), "fits");
-  static constexpr int Smem = 1024 + Slots * Slot + RawSlots * RawSlot + Fixed;
+  static constexpr int KSlots = F8 ? (D == 256 ? 3 : 4) : 2, VSlots = 2, RSlots = F8 ? (D == 256 ? 2 : 3) : 0;
+  static constexpr int Fixed = QBytes + kRows * 8 + kRows * 4 * 4 + (kTreeMaxBatch + 4) * 4 + 1024;
+  static constexpr int Smem = 1024 + KSlots * KSlot + VSlots * VSlot + RSlots * RSlot + Fixed;
+  static_assert(Smem <= 227 * 1024, "fits");
   static constexpr int S(int s) { return s * 128; }         // tensor memory columns
   static constexpr int O = 256;
   static constexpr float Lift = F8 ? 7.f : 0.f;             // fp16 weights reach 2^15: 2^kMove times this
+  static constexpr uint32_t KSwizzle = KBlock == 128 ? 2 : 4;  // descriptor: 128-byte or 64-byte
 };
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, e4m3 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
@@ -72,19 +87,22 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   constexpr int kTile = C::Tile;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* ring = base;
-  uint8_t* sq = ring + C::Slots * C::Slot;
-  uint8_t* raws = sq + C::QTile;
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(raws + C::RawSlots * C::RawSlot);
+  uint8_t* keys = base;
+  uint8_t* values = keys + C::KSlots * C::KSlot;
+  uint8_t* raws = values + C::VSlots * C::VSlot;
+  uint8_t* sq = raws + C::RSlots * C::RSlot;
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(sq + C::QBytes);
   float* row_fac = reinterpret_cast<float*>(row_mask + kRows);
   float* row_max = row_fac + kRows;       // in use
   float* row_sum = row_max + kRows;       // [2][rows]
   int* cum = reinterpret_cast<int*>(row_sum + 2 * kRows);
-  uint64_t* full = reinterpret_cast<uint64_t*>(cum + kTreeMaxBatch + 4);
-  uint64_t* empty = full + C::Slots;
-  uint64_t* raw_full = empty + C::Slots;
-  uint64_t* raw_empty = raw_full + 8;
-  uint64_t* q_ready = raw_empty + 8;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(cum + kTreeMaxBatch + 4);
+  uint64_t* k_empty = k_full + 4;
+  uint64_t* v_full = k_empty + 4;
+  uint64_t* v_empty = v_full + 4;
+  uint64_t* r_full = v_empty + 4;   // e4m3: the values as copied
+  uint64_t* r_empty = r_full + 4;
+  uint64_t* q_ready = r_empty + 4;
   uint64_t* s_full = q_ready + 1;   // [2] a tile's scores; also: the products of the tile two before it are complete
   uint64_t* p_ready = s_full + 2;   // [2] weights written
   uint64_t* o_done = p_ready + 2;   // each tile's product with the values
@@ -97,13 +115,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&map);
-    for (int i = 0; i < C::Slots; ++i) {
-      tc::mbar_init(full + i, F8 ? kConvertThreads / 32 : 1);
-      tc::mbar_init(empty + i, 1);
-    }
-    for (int i = 0; i < C::RawSlots; ++i) {
-      tc::mbar_init(raw_full + i, 1);
-      tc::mbar_init(raw_empty + i, kConvertThreads / 32);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(k_full + i, 1);
+      tc::mbar_init(k_empty + i, 1);
+      tc::mbar_init(v_full + i, F8 ? kConvertThreads / 32 : 1);
+      tc::mbar_init(v_empty + i, 1);
+      tc::mbar_init(r_full + i, 1);
+      tc::mbar_init(r_empty + i, kConvertThreads / 32);
     }
     tc::mbar_init(q_ready, kSoftmaxWarps);
     for (int s = 0; s < 2; ++s) {
@@ -134,24 +152,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   TreeSegment g;
 
   if (warp >= kSoftmaxWarps) {
-    // F8: 512 threads x 128 registers at launch = 256 x 184 + 256 x 72; else 384 x 168 = 256 x 200 + 128 x 104
-    if constexpr (F8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kCopyWarp) {
-      // ---- the copying warp: tiles as the cache has them, into the ring or (e4m3) into the raw ring
-      constexpr int kSlots = F8 ? C::RawSlots : C::Slots;
-      uint64_t* const bar_full = F8 ? raw_full : full;
-      uint64_t* const bar_empty = F8 ? raw_empty : empty;
-      int it = 0;
+      // ---- the copying warp: keys, and values (e4m3: to be converted), tiles in the order of their use
+      int t0 = 0, copied[2] = {0, 0};
       bool dead = false;
       const int box = min(1 << p.page_shift, kTile);  // rows of one copy
       while (!dead && walk.next(p, cum, g)) {
         const int32_t* row = p.table + (int64_t)g.b * p.width;
         const int len = g.seq.prefix + g.seq.count;
         const Order order{g.tiles, true};
-        for (int e = 0; e < 2 * g.tiles; ++e, ++it) {
+        for (int e = 0; e < 2 * g.tiles; ++e) {
           bool value;
-          const int t = order.at(e, &value), s = it % kSlots;
+          const int t = order.at(e, &value), tile = t0 + t;
+          const int slots = !value ? C::KSlots : F8 ? C::RSlots : C::VSlots, s = tile % slots, use = tile / slots;
+          uint64_t* const bar = (!value ? k_full : F8 ? r_full : v_full) + s;
           const int pos = (g.tile0 + t) * kTile + lane * box;  // lane i copies box i of the tile, none past the end
           const bool mine = lane * box < kTile && pos < len;
           int y = 0;
@@ -161,35 +175,38 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             y = (((page * 2 + (value ? 1 : 0)) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
           }
           const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-          if (it >= kSlots) {
-            const bool ok = tc::mbar_wait_short(bar_empty + s, (uint32_t)(it / kSlots & 1) ^ 1u, p.wait_ns);
+          if (use > 0) {
+            const bool ok = tc::mbar_wait_short((!value ? k_empty : F8 ? r_empty : v_empty) + s, (uint32_t)(use & 1) ^ 1u, p.wait_ns);
             if (__any_sync(0xFFFFFFFFu, !ok)) {
               dead = true;
               if (lane == 0) flags[0] = 1;
               break;
             }
           }
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar_full + s, (uint32_t)(boxes * box * D * (F8 ? 1 : 2)));
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * C::KBytes));
           __syncwarp();
+          copied[value ? 1 : 0] = tile + 1;
           if (mine) {
-            if constexpr (F8) {
-              tc::tma_load_2d(raws + s * C::RawSlot + lane * box * D, &map, bar_full + s, 0, y);
-            } else {
+            uint8_t* const to = !value ? keys + s * C::KSlot : F8 ? raws + s * C::RSlot : values + s * C::VSlot;
 #pragma unroll
-              for (int blk = 0; blk < C::Blocks; ++blk)
-                tc::tma_load_2d(ring + s * C::Slot + blk * (kTile * 128) + lane * box * 128, &map, bar_full + s, blk * 64, y);
-            }
+            for (int blk = 0; blk < C::KBytes / C::KBlock; ++blk)
+              tc::tma_load_2d(to + blk * (kTile * C::KBlock) + lane * box * C::KBlock, &map, bar, blk * (F8 ? C::KBlock : C::KBlock / 2), y);
           }
         }
+        t0 += g.tiles;
       }
       // no copy may land in a block that has left
-      for (int i = it > kSlots ? it - kSlots : 0; i < it; ++i) tc::mbar_wait(bar_full + i % kSlots, (uint32_t)(i / kSlots & 1), kDrainNs);
+      for (int kv = 0; kv < 2; ++kv) {
+        const int slots = kv == 0 ? C::KSlots : F8 ? C::RSlots : C::VSlots;
+        for (int t = max(0, copied[kv] - slots); t < copied[kv]; ++t)
+          tc::mbar_wait((kv == 0 ? k_full : F8 ? r_full : v_full) + t % slots, (uint32_t)(t / slots & 1), kDrainNs);
+      }
     } else if (warp == kMmaWarp) {
-      // ---- the thread that issues the products, taking the ring's entries in order
+      // ---- the thread that issues the products
       if (lane == 0) {
         bool dead = false, issued = false;
         int seg = 0;
-        uint32_t slot = 0, use = 0, ns[2] = {0, 0};
+        uint32_t ks = 0, kuse = 0, vs = 0, vuse = 0, ns[2] = {0, 0};  // next slots
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
           if (!dead && !tc::mbar_wait_short(bar, parity, p.wait_ns)) {
             dead = true;
@@ -197,50 +214,55 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
           return !dead;
         };
-        constexpr uint32_t kType = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 operands: type fields 0
+        // type fields: bf16 1, fp16 0 of kind::f16; e4m3 0 of kind::f8f6f4
+        constexpr uint32_t kType = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;
         const uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kType, id_o = (tc::idesc_bf16_f32(128, D) & kType) | kBMnMajor;
-        const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
-                       v_desc = desc_mnmajor(tc::smem_u32(ring), kTile * 128);
-        const auto take = [&] { return wait(full + slot, use & 1u); };
-        const auto release = [&] {
-          tc::mma_commit(empty + slot);
-          if (++slot == C::Slots) {
-            slot = 0;
-            ++use;
-          }
-        };
+        const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 8 * C::KBlock, C::KSwizzle),
+                       k_desc = tc::desc_kmajor(tc::smem_u32(keys), 8 * C::KBlock, C::KSwizzle),
+                       v_desc = desc_mnmajor(tc::smem_u32(values), kTile * 128);
         const auto scores = [&](int s) {
-          const uint64_t b = k_desc + slot * (C::Slot >> 4);
+          if (!wait(k_full + ks, kuse & 1u)) return;
+          const uint64_t b = k_desc + ks * (C::KSlot >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16(tmem + C::S(s), q_desc + (uint32_t)(((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4),
-                         b + (uint32_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4), id_s, k > 0);
+          for (int h = 0; h < (F8 ? 2 : 1); ++h)
+#pragma unroll
+            for (int k = 0; k < C::KBytes / 32; ++k) {
+              constexpr int kPer = C::KBlock / 32;
+              const uint64_t qa = q_desc + (uint32_t)((h * (kRows * D) + k / kPer * (kRows * C::KBlock) + k % kPer * 32) >> 4);
+              const uint64_t ka = b + (uint32_t)((k / kPer * (kTile * C::KBlock) + k % kPer * 32) >> 4);
+              if constexpr (F8) mma_e4m3(tmem + C::S(s), qa, ka, id_s, h > 0 || k > 0);
+              else tc::mma_bf16(tmem + C::S(s), qa, ka, id_s, k > 0);
+            }
           tc::mma_commit(s_full + s);
+          tc::mma_commit(k_empty + ks);
           issued = true;
-          release();
+          if (++ks == C::KSlots) {
+            ks = 0;
+            ++kuse;
+          }
         };
         while (!dead && walk.next(p, cum, g)) {
           const int n = g.tiles;
           if (!wait(q_ready, (uint32_t)(seg & 1))) break;
           tc::fence_after_sync();
-          for (int i = 0; i < 2 && i < n; ++i)
-            if (take()) scores(i);
+          for (int i = 0; i < 2 && i < n; ++i) scores(i);
           for (int i = 0; i < n; ++i) {
             const int s = i & 1;
-            if (!take() || !wait(p_ready + s, ns[s] & 1u)) break;
+            if (!wait(v_full + vs, vuse & 1u) || !wait(p_ready + s, ns[s] & 1u)) break;
             ++ns[s];
             tc::fence_after_sync();
-            const uint64_t b = v_desc + slot * (C::Slot >> 4);
+            const uint64_t b = v_desc + vs * (C::VSlot >> 4);
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
               mma_ts(tmem + C::O, tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, i > 0 || k > 0);
             tc::mma_commit(o_done);
-            release();
-            if (i + 1 == n) tc::mma_commit(o_full);
-            if (i + 2 < n) {
-              if (!take()) break;
-              scores(s);
+            tc::mma_commit(v_empty + vs);
+            if (++vs == C::VSlots) {
+              vs = 0;
+              ++vuse;
             }
+            if (i + 1 == n) tc::mma_commit(o_full);
+            if (i + 2 < n) scores(s);
           }
           ++seg;
         }
@@ -252,9 +274,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       }
       __syncwarp();
     } else if (F8 && warp >= kConvertWarp) {
-      // ---- e4m3 to fp16, tile by tile in the order of the copies
+      // ---- values, e4m3 to fp16, tile by tile
       const int tid = threadIdx.x - kConvertWarp * 32;
-      int it = 0, seg = 0;
+      int tile = 0, seg = 0;
       bool dead = false;
       const auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
@@ -265,70 +287,71 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         return !dead;
       };
       while (!dead && walk.next(p, cum, g)) {
-        const Order order{g.tiles, true};
         const int len = g.seq.prefix + g.seq.count;
-        for (int e = 0; e < 2 * g.tiles; ++e, ++it) {
-          bool value;
-          const int t = order.at(e, &value);
-          const int rs = F8 ? it % (F8 ? C::RawSlots : 1) : 0, s = it % C::Slots;
-          if (!wait(raw_full + rs, (uint32_t)(it / (F8 ? C::RawSlots : 1) & 1))) break;
-          if (it >= C::Slots && !wait(empty + s, (uint32_t)(it / C::Slots & 1) ^ 1u)) break;
-          const uint8_t* from = raws + rs * C::RawSlot;
-          uint8_t* to = ring + s * C::Slot;
+        for (int t = 0; t < g.tiles; ++t, ++tile) {
+          constexpr int kR = F8 ? C::RSlots : 1;
+          const int rs = tile % kR, vs = tile % C::VSlots;
+          if (!wait(r_full + rs, (uint32_t)(tile / kR & 1))) break;
+          if (tile >= C::VSlots && !wait(v_empty + vs, (uint32_t)(tile / C::VSlots & 1) ^ 1u)) break;
+          const uint8_t* from = raws + rs * C::RSlot;
+          uint8_t* to = values + vs * C::VSlot;
           const int pos0 = (g.tile0 + t) * kTile;
-          const bool tail = value && pos0 + kTile > g.seq.prefix;
+          const bool tail = pos0 + kTile > g.seq.prefix;
           constexpr int CPR = D / 16, kPer = kTile * CPR / kConvertThreads;  // 16-byte chunks of a row, of a thread
-          uint4 u[kPer];
+          constexpr int kBlockChunks = C::KBlock / 16;                       // of a swizzled row
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) u[k] = *reinterpret_cast<const uint4*>(from + (tid + k * kConvertThreads) * 16);
-          if (tail) {
-            // values of rows past the end, and those of drafts that are not numbers (the only ones e4m3 has), become zeros
+          for (int k0 = 0; k0 < kPer; k0 += 4) {
+            uint4 u[4];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const int row = (tid + k * kConvertThreads) / CPR;
-              if (pos0 + row >= len) u[k] = make_uint4(0, 0, 0, 0);
-              else if (pos0 + row >= g.seq.prefix) {
-                bool odd = false;
-                const auto clean = [&](uint32_t& w) {
+            for (int k = 0; k < 4; ++k) {
+              const int idx = tid + (k0 + k) * kConvertThreads, row = idx / CPR, c = idx % CPR;
+              const int sw = C::KBlock == 128 ? row & 7 : row >> 1 & 3;
+              u[k] = *reinterpret_cast<const uint4*>(from + c / kBlockChunks * (kTile * C::KBlock) + row * C::KBlock + ((c % kBlockChunks) ^ sw) * 16);
+              if (tail) {
+                // rows past the end, and numbers of drafts that are none (the only ones e4m3 has), become zeros
+                if (pos0 + row >= len) u[k] = make_uint4(0, 0, 0, 0);
+                else if (pos0 + row >= g.seq.prefix) {
+                  uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, odd = 0;
 #pragma unroll
-                  for (int b = 0; b < 32; b += 8)
-                    if ((w >> b & 0x7Fu) == 0x7Fu) { w &= ~(0xFFu << b); odd = true; }
-                };
-                clean(u[k].x); clean(u[k].y); clean(u[k].z); clean(u[k].w);
-                if (odd) flags[2] = seg;
+                  for (int j = 0; j < 4; ++j) {
+                    const uint32_t nan = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of such bytes
+                    odd |= nan;
+                    w[j] &= ~((nan >> 7) * 0xFFu);
+                  }
+                  u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                  if (odd) flags[2] = seg;
+                }
               }
             }
-          }
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int idx = tid + k * kConvertThreads, row = idx / CPR, c = idx % CPR;
-            uint4 h[2];
-            h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
-            h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
-            // eight lanes write eight different places of the banks: half of them their second chunk first
-            const int flip = c >> 2 & 1;
-            uint8_t* at = to + (c >> 2) * (kTile * 128) + row * 128;
-            *reinterpret_cast<uint4*>(at + (((2 * c + flip) & 7) ^ (row & 7)) * 16) = flip ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(at + (((2 * c + (flip ^ 1)) & 7) ^ (row & 7)) * 16) = flip ? h[0] : h[1];
+            for (int k = 0; k < 4; ++k) {
+              const int idx = tid + (k0 + k) * kConvertThreads, row = idx / CPR, c = idx % CPR;
+              uint4 h[2];
+              h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
+              h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
+              // eight lanes write eight different places of the banks: half of them their second chunk first
+              const int flip = c >> 2 & 1;
+              uint8_t* at = to + (c >> 2) * (kTile * 128) + row * 128;
+              *reinterpret_cast<uint4*>(at + (((2 * c + flip) & 7) ^ (row & 7)) * 16) = flip ? h[1] : h[0];
+              *reinterpret_cast<uint4*>(at + (((2 * c + (flip ^ 1)) & 7) ^ (row & 7)) * 16) = flip ? h[0] : h[1];
+            }
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tc::mbar_arrive(raw_empty + rs);
-            tc::mbar_arrive(full + s);
+            tc::mbar_arrive(r_empty + rs);
+            tc::mbar_arrive(v_full + vs);
           }
         }
         ++seg;
       }
     }
   } else {
-    if constexpr (F8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax: group s, one thread per row; warp w of a group reaches tensor memory lanes 32 w ..
     const int s = warp >> 2, w4 = warp & 3, r = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t t_s = tmem + C::S(s) + lanes, t_o = tmem + C::O + lanes;
-    int it0 = 0, done0 = 0, seg = 0, ns = 0, turns = 0;  // turns: the other group's hand-overs of this warp's rows so far
+    int t0 = 0, seg = 0, ns = 0, turns = 0;  // turns: the other group's hand-overs of this warp's rows so far
     int4 shared_item = make_int4(-1, 0, 0, 0);
     bool dead = false;
     const auto wait = [&](uint64_t* bar, int count) {
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
             const int q = r0 + k * kStep;
-            uint4 v = make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
+            const uint4 v = make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
             if constexpr (F8) {
               const float x[8] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y),
                                   bf16lo_to_f32(v.z), bf16hi_to_f32(v.z), bf16lo_to_f32(v.w), bf16hi_to_f32(v.w)};
@@ -368,15 +391,29 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
               for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
 #pragma unroll
               for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-              // the row's largest exponent to 0: fp16 then keeps every bf16 number within 2^-14 of the largest exactly
+              // the row's largest number to [2^7, 2^8): a number is then the sum of two e4m3 ones, exactly down to 2^-9 of
+              // the largest and within 2^-17 of it below
               uint32_t e = __float_as_uint(m) >> 23;
-              if (e < 2 || e > 252) e = 127;  // zero, subnormal, infinite or NaN rows as they are
-              const float inv = __uint_as_float((254u - e) << 23);
-              v = make_uint4(pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv),
-                             pack_f16x2(x[4] * inv, x[5] * inv), pack_f16x2(x[6] * inv, x[7] * inv));
-              if (l == 0) row_fac[q] = __uint_as_float(e << 23);
+              const bool none = e == 255;     // infinite or NaN: so are the row's results
+              if (e < 10 || none) e = 134;    // zero, or too small to matter: as they are
+              const float inv = __uint_as_float((261u - e) << 23);
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+                hi[i] = none ? 0x7F7Fu : e4m3x2(a, b);
+                const uint32_t back = e4m3x2_to_f16x2(hi[i]);
+                lo[i] = e4m3x2(a - f16_to_f32((uint16_t)back), b - f16_to_f32((uint16_t)(back >> 16)));
+              }
+              if (l == 0) row_fac[q] = __uint_as_float((e - 7u) << 23);
+              constexpr int kLanes = C::KBlock / 8;  // of a swizzled row
+              const int sw = C::KBlock == 128 ? q & 7 : q >> 1 & 3, ch = l % kLanes;
+              uint8_t* at = sq + l / kLanes * (kRows * C::KBlock) + q * C::KBlock + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
+              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2*>(at + kRows * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            } else {
+              *reinterpret_cast<uint4*>(sq + (l >> 3) * (kRows * 128) + q * 128 + (((l & 7) ^ (q & 7)) << 4)) = v;
             }
-            *reinterpret_cast<uint4*>(sq + (l >> 3) * (kRows * 128) + q * 128 + (((l & 7) ^ (q & 7)) << 4)) = v;
           }
         }
         if (threadIdx.x < kRows) {
@@ -419,18 +456,21 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             }
             tmem_st_wait();
           }
-          // ---- the row's maximum; the scores stay in registers
-          uint32_t x[W][32];
-#pragma unroll
-          for (int w = 0; w < W; ++w) tc::tmem_ld_32x32b_x32(t_s + 32 * w, x[w]);
-          tc::tmem_ld_wait();
+          // ---- the row's maximum.  Both passes over the scores are loops over 32 columns: reading tensor memory twice costs
+          // less than the registers and the code of a step held whole
           float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < W; ++w) {
-            float a = __uint_as_float(x[w][0]);
+            uint32_t x[32];
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+            tc::tmem_ld_wait();
+            float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
-            for (int j = 1; j < 31; j += 2) a = fmaxf(fmaxf(a, __uint_as_float(x[w][j])), __uint_as_float(x[w][j + 1]));
-            mx = fmaxf(mx, fmaxf(a, __uint_as_float(x[w][31])));
+            for (int j = 2; j < 30; j += 4) {
+              a = fmaxf(fmaxf(a, __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
+              b = fmaxf(fmaxf(b, __uint_as_float(x[j + 2])), __uint_as_float(x[j + 3]));
+            }
+            mx = fmaxf(mx, fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))));
           }
           mx *= c;
           // ---- the maximum in use, from the warp that has the tile before; moved, and handed on
@@ -443,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           if (lane == 0) tc::mbar_arrive(turn + s * 4 + w4);
           if (i > 0 && __any_sync(0xFFFFFFFFu, move)) {
             const float a = move ? ex2(old - m) : 1.f;
-            wait(o_done, done0 + i - 1);  // (the product before that is known to be complete)
+            wait(o_done, t0 + i - 1);  // (the product before that is known to be complete)
             tc::fence_after_sync();
 #pragma unroll 1
             for (int col = 0; col < D; col += 32) {
@@ -462,12 +502,14 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           // ---- weights, over the scores
           const float ms = m == -INFINITY ? C::Lift : C::Lift - m;
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
           for (int w = 0; w < W; ++w) {
-            uint32_t e[16];
+            uint32_t x[32], e[16];
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
+            tc::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[w][j]), __uint_as_float(x[w][j + 1])), make_float2(c, c), make_float2(ms, ms));
+              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(c, c), make_float2(ms, ms));
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum = __fadd2_rn(sum, y);
@@ -483,9 +525,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           if (pos0 + kTile > g.seq.prefix) {
             // Values that must not reach a product: rows past the end become zeros, whatever their bits; so do numbers of
             // drafts that are not finite (rare), which are added at the end to the rows that see them.
-            const int e0 = it0 + (i < n - 1 ? 2 * i + 2 : 2 * n - 1);  // their place in the ring
-            wait(full + e0 % C::Slots, e0 / C::Slots);
-            uint8_t* tile = ring + e0 % C::Slots * C::Slot;
+            const int vs = (t0 + i) % C::VSlots;
+            wait(v_full + vs, (t0 + i) / C::VSlots);
+            uint8_t* tile = values + vs * C::VSlot;
             const int from = max(g.seq.prefix - pos0, 0);
             constexpr int Chunks = D / 8;
             for (int e = from * Chunks + (threadIdx.x & 127); e < kTile * Chunks; e += 128) {
@@ -517,8 +559,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       // ---- the segment's end
       wait(o_full, seg);
       tc::fence_after_sync();
-      it0 += 2 * n;
-      done0 += n;
+      t0 += n;
       if (active) turns += (n + s) >> 1;  // tiles of the other group: of group 0 (n + 1) / 2, of group 1 n / 2
       named_sync(1, 256);
       // the last tile's warp has left the final maxima: both groups bring their sums to them
@@ -639,10 +680,9 @@ bool tree_tc1_fits(const trellis_cache_t& c, int rows) { return rows > 16 && (c.
 int tree_tc1_rows() { return kRows; }
 
 void tree_tc1_box(const trellis_cache_t& c, TreeBox* b) {
-  const int tile = c.head_dim == 256 ? 64 : 128;
+  const int tile = c.head_dim == 256 ? 64 : 128, bytes = (int)(c.head_dim * cache_elem_bytes(c));
   b->rows = c.page_size < tile ? c.page_size : tile;
-  b->bytes = c.dtype == TRELLIS_E4M3 ? c.head_dim : 128;
-  b->swizzled = c.dtype != TRELLIS_E4M3;
+  b->bytes = bytes < 128 ? bytes : 128;
 }
 
 cudaError_t launch_tree_tc1(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st) {

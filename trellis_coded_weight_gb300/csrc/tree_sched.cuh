@@ -154,11 +154,10 @@ __host__ __device__ constexpr int64_t tree_part_floats(int rows, int dim) { retu
 // factor that the weights carry.
 cudaError_t launch_tree_join(const TreeParams& p, int dim, int rows, float lift, int ctas, cudaStream_t st);
 
-// One copy of a cache's tensor map: rows of head_dim numbers, bytes of each, and the layout in shared memory (128-byte swizzle
-// or rows end to end).
+// One copy of a cache's tensor map: rows of head_dim numbers, and bytes of each (128, or 64; also the
+// swizzle).
 struct TreeBox {
   int rows, bytes;
-  bool swizzled;
 };
 
 // The tensor-core kernels: where they take a call, the rows of their blocks, and what they need copied.
