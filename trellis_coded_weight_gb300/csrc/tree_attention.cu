@@ -95,8 +95,7 @@ struct Cfg {
   static constexpr float Lift = F8 ? 15.f : 0.f;
   static constexpr int JoinSlot = (Regs + 4) * 32;   // a warp's outputs, maxima and sums
   static constexpr int Join = WK / 2 * JoinSlot * 4;
-  static constexpr int Cum = (kTreeMaxBatch + 4) * 4;
-  static constexpr int Fixed = QBytes + Join + kRows * 8 + kRows * 4 + Cum + 256;
+  static constexpr int Fixed = QBytes + Join + kRows * 8 + kRows * 4 + (int)sizeof(TreeMap) + 256;
   static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Stage;
   static constexpr int Stages = Fit > 8 ? 8 : Fit;
   static_assert(Stages >= 2, "two tiles in flight at least");
@@ -123,8 +122,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   float* join = reinterpret_cast<float*>(sq + C::QBytes);
   uint64_t* row_mask = reinterpret_cast<uint64_t*>(join + C::Join / 4);
   float* row_fac = reinterpret_cast<float*>(row_mask + kRows);
-  int* cum = reinterpret_cast<int*>(row_fac + kRows);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cum) + C::Cum);
+  TreeMap& seqs = *reinterpret_cast<TreeMap*>(row_fac + kRows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(&seqs + 1);
   uint64_t* empty = full + C::Stages;
   volatile int* flags = reinterpret_cast<volatile int*>(empty + C::Stages);  // [0] a wait gave up
 
@@ -140,9 +139,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     tc::fence_mbar_init();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<kRows, kTile, false>(p, cum);
+  if (warp == 0) tree_cumulate<kRows, kTile, false>(p, seqs);
   __syncthreads();
-  const int total = cum[p.batch];
+  const int total = seqs.cum[p.batch];
   const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
   const int cta = blockIdx.x;
   if (cta >= ctas) {  // fewer steps than blocks
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     // ---- the copying warp: every tile of the range, as many ahead as there are stages
     int it = 0, issued = 0;
     bool dead = false;
-    while (walk.next(p, cum, g)) {
+    while (walk.next(p, seqs, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const int box = p.page_shift < 6 ? 1 << p.page_shift : kTile;  // rows of one copy
@@ -207,7 +206,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
     int it = 0;
     bool dead = false;
-    while (walk.next(p, cum, g)) {
+    while (walk.next(p, seqs, g)) {
       const int rows = min(kRows, g.seq.count * p.group - g.row_block * kRows);  // rows of this block that exist
       const int row0 = g.row_block * kRows;
       named_sync(1, nthr);  // the previous segment's queries are no longer read
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         constexpr int LPR = D / 8;  // lanes of a row
         for (int r = threadIdx.x / LPR; r < kRows; r += nthr / LPR) {
           const int l = threadIdx.x % LPR;
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
           uint4 u = make_uint4(0, 0, 0, 0);
           if (r < rows)
             u = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         named_sync(1, nthr);
       }
 
-      if (g.first == g.last) {
+      if (g.whole) {
         if (wk == 0) {
           const float vs = F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f;
 #pragma unroll
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             const int r = gq + 8 * half;
             if (r >= rows) continue;
             const float f = l[half] == 0.f ? 0.f : vs / l[half];
-            const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+            const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
             uint16_t* to = p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D;
             if constexpr (F8) {
 #pragma unroll
@@ -554,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
         }
       }
-      if (threadIdx.x == 0 && g.first == cta) shared_item = make_int4(g.b, g.head, g.row_block, g.last);
+      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;
   }
@@ -614,6 +613,7 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   p.wait_ns = wait_limit_ns();
   p.batch = d.batch; p.width = d.width; p.n = d.n; p.max_tokens = d.max_tokens;
   p.hq = q_heads; p.hkv = c.heads; p.group = q_heads / c.heads;
+  p.group_inv = (((uint64_t)1 << 32) + p.group - 1) / p.group;
   p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   p.scale_log2 = scale * kLog2e;
   p.items = static_cast<int4*>(workspace);

@@ -40,7 +40,7 @@ struct Cfg {
   static constexpr int Blocks = D / 64;                     // 128-byte blocks of a row
   static constexpr int Slot = kTile * D * 2;                // the keys, or the values, of a tile
   static constexpr int QTile = 128 * D * 2;
-  static constexpr int Fixed = 2 * QTile + kRows * 8 + 4 * 128 * 4 + (kTreeMaxBatch + 4) * 4 + 512;
+  static constexpr int Fixed = 2 * QTile + kRows * 8 + 4 * 128 * 4 + (int)sizeof(TreeMap) + 512;
   static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Slot;
   static constexpr int Pairs = Fit >= 8 ? 4 : 2;            // tiles in flight, each in a slot for its keys and one for its values
   static constexpr int Slots = 2 * Pairs;
@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = ring + C::Slots * C::Slot;
   uint64_t* row_mask = reinterpret_cast<uint64_t*>(sq + 2 * C::QTile);
   float* row_stat = reinterpret_cast<float*>(row_mask + kRows);  // [stream][maximum, sum][128]
-  int* cum = reinterpret_cast<int*>(row_stat + 4 * 128);
-  uint64_t* full = reinterpret_cast<uint64_t*>(cum + kTreeMaxBatch + 4);
+  TreeMap& seqs = *reinterpret_cast<TreeMap*>(row_stat + 4 * 128);
+  uint64_t* full = reinterpret_cast<uint64_t*>(&seqs + 1);
   uint64_t* empty = full + C::Slots;
   uint64_t* q_ready = empty + C::Slots;
   uint64_t* s_full = q_ready + 1;  // [2] scores there; also: the stream's products before them are complete
@@ -98,14 +98,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<kRows, kTile, true>(p, cum);
+  if (warp == 0) tree_cumulate<kRows, kTile, true>(p, seqs);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int total = cum[p.batch];
+  const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
-  TreeWalk<kRows, kTile, true> walk(total, tree_ctas_used<true>(total, (int)gridDim.x), cta);
+  const int ctas = tree_ctas_used<true>(total, (int)gridDim.x);
+  TreeWalk<kRows, kTile, true> walk(total, ctas, cta);
   TreeSegment g;
   const auto rows_of = [&](const TreeSegment& x) { return min(kRows, x.seq.count * p.group - x.row_block * kRows); };
 
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int t0 = 0, copied[2] = {0, 0};  // keys, values
     bool dead = false;
     const int box = min(1 << p.page_shift, kTile);  // rows of one copy
-    while (!dead && walk.next(p, cum, g)) {
+    while (!dead && walk.next(p, seqs, g)) {
       const int32_t* row = p.table + (int64_t)g.b * p.width;
       const int len = g.seq.prefix + g.seq.count;
       const Order order{g.tiles, rows_of(g) <= 128};
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         return true;
       };
-      while (!dead && walk.next(p, cum, g)) {
+      while (!dead && walk.next(p, seqs, g)) {
         const int n = g.tiles;
         if (!wait(q_ready, (uint32_t)(seg & 1))) break;
         tc::fence_after_sync();
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) flags[0] = 1;
       }
     };
-    while (walk.next(p, cum, g)) {
+    while (walk.next(p, seqs, g)) {
       const int rows = rows_of(g), row0 = g.row_block * kRows, n = g.tiles;
       const Order order{n, rows <= 128};
       const int len = g.seq.prefix + g.seq.count;
@@ -274,24 +275,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- queries
       {
         constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = D == 128 ? 8 : 4;  // lanes of a row, rows at a time, loads in flight
-        const int qrows = order.split_keys ? 128 : 256, l = threadIdx.x % LPR;
+        const int qrows = (rows + 31) & ~31, l = threadIdx.x % LPR;  // whole warps' rows; what others hold does not matter
         for (int r0 = threadIdx.x / LPR; r0 < qrows; r0 += kStep * kMost) {
           uint4 u[kMost];
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
-            const int r = r0 + k * kStep, d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+            const int r = r0 + k * kStep, d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
             u[k] = make_uint4(0, 0, 0, 0);
             if (r < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
           }
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
             const int r = r0 + k * kStep;
-            *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QTile + (l >> 3) * (128 * 128) + (r & 127) * 128 + (((l & 7) ^ (r & 7)) << 4)) =
+            if (r < qrows)
+              *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QTile + (l >> 3) * (128 * 128) + (r & 127) * 128 + (((l & 7) ^ (r & 7)) << 4)) =
                 make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
           }
         }
         if (threadIdx.x < qrows) {
-          const int r = threadIdx.x, d = (row0 + r) / p.group;
+          const int r = threadIdx.x, d = tree_draft(p, row0 + r);
           row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
         }
         tc::fence_proxy_async_smem();
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
       };
-      if (g.first == g.last) {
+      if (g.whole) {
         // finished here: rows go through the queries' place (no longer read) so that a row's numbers are stored together
         const float f = l == 0.f ? 0.f : 1.f / l;
         uint8_t* stage = sq + (order.split_keys ? 0 : s * C::QTile) + lrow * (D * 2);
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
         }
         if (valid && col0 == 0 && p.lse) {
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
           p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
         }
         tc::fence_before_sync();
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ch = threadIdx.x % LPR;
 #pragma unroll 1
         for (int q = threadIdx.x / LPR; q < rows; q += 256 / LPR) {
-          const int d = (row0 + q) / p.group, hh = (row0 + q) - d * p.group;
+          const int d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
           *reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + 8 * ch) =
               *reinterpret_cast<const uint4*>(sq + (q >> 7) * C::QTile + (q & 127) * (D * 2) + ((ch ^ (q & 7)) << 4));
         }
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         part[(int64_t)kRows * D + kRows + r] = l;
       }
       tc::fence_before_sync();
-      if (threadIdx.x == 0 && g.first == cta) shared_item = make_int4(g.b, g.head, g.row_block, g.last);
+      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
       ++seg;
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;

@@ -31,8 +31,8 @@ using namespace tree;
 __device__ int g_tree_tc1_error = 0;  // set when a bounded wait gives up (trellis_device_error)
 
 constexpr int kRows = 128;  // rows of a block
-constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 12;
-constexpr int kConvertThreads = 128;
+constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
+constexpr int kConvertThreads = 192;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   uint32_t r;
@@ -55,8 +55,8 @@ struct Cfg {
   static constexpr int RSlot = F8 ? Tile * D : 0;           // as the cache has them
   static constexpr int QBytes = kRows * D * 2;              // bf16, or two e4m3 halves
   static constexpr int Threads = F8 ? 512 : 384;
-  static constexpr int KSlots = F8 ? (D == 256 ? 3 : 4) : 2, VSlots = 2, RSlots = F8 ? (D == 256 ? 2 : 3) : 0;
-  static constexpr int Fixed = QBytes + kRows * 8 + kRows * 4 * 4 + (kTreeMaxBatch + 4) * 4 + 1024;
+  static constexpr int KSlots = F8 ? (D == 256 ? 2 : 4) : 2, VSlots = 2, RSlots = F8 ? 3 : 0;
+  static constexpr int Fixed = QBytes + kRows * 8 + kRows * 4 * 4 + (int)sizeof(TreeMap) + 1024;
   static constexpr int Smem = 1024 + KSlots * KSlot + VSlots * VSlot + RSlots * RSlot + Fixed;
   static_assert(Smem <= 227 * 1024, "fits");
   static constexpr int S(int s) { return s * 128; }         // tensor memory columns
@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   float* row_fac = reinterpret_cast<float*>(row_mask + kRows);
   float* row_max = row_fac + kRows;       // in use
   float* row_sum = row_max + kRows;       // [2][rows]
-  int* cum = reinterpret_cast<int*>(row_sum + 2 * kRows);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(cum + kTreeMaxBatch + 4);
+  TreeMap& seqs = *reinterpret_cast<TreeMap*>(row_sum + 2 * kRows);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(&seqs + 1);
   uint64_t* k_empty = k_full + 4;
   uint64_t* v_full = k_empty + 4;
   uint64_t* v_empty = v_full + 4;
@@ -141,14 +141,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     tc::tmem_relinquish();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<kRows, kTile, false>(p, cum);
+  if (warp == 0) tree_cumulate<kRows, kTile, false>(p, seqs);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int total = cum[p.batch];
+  const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
-  TreeWalk<kRows, kTile, false> walk(total, tree_ctas_used<false>(total, (int)gridDim.x), cta);
+  const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
+  TreeWalk<kRows, kTile, false> walk(total, ctas, cta);
   TreeSegment g;
 
   if (warp >= kSoftmaxWarps) {
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       int t0 = 0, copied[2] = {0, 0};
       bool dead = false;
       const int box = min(1 << p.page_shift, kTile);  // rows of one copy
-      while (!dead && walk.next(p, cum, g)) {
+      while (!dead && walk.next(p, seqs, g)) {
         const int32_t* row = p.table + (int64_t)g.b * p.width;
         const int len = g.seq.prefix + g.seq.count;
         const Order order{g.tiles, true};
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             ++kuse;
           }
         };
-        while (!dead && walk.next(p, cum, g)) {
+        while (!dead && walk.next(p, seqs, g)) {
           const int n = g.tiles;
           if (!wait(q_ready, (uint32_t)(seg & 1))) break;
           tc::fence_after_sync();
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         }
         return !dead;
       };
-      while (!dead && walk.next(p, cum, g)) {
+      while (!dead && walk.next(p, seqs, g)) {
         const int len = g.seq.prefix + g.seq.count;
         for (int t = 0; t < g.tiles; ++t, ++tile) {
           constexpr int kR = F8 ? C::RSlots : 1;
@@ -297,14 +298,15 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           uint8_t* to = values + vs * C::VSlot;
           const int pos0 = (g.tile0 + t) * kTile;
           const bool tail = pos0 + kTile > g.seq.prefix;
-          constexpr int CPR = D / 16, kPer = kTile * CPR / kConvertThreads;  // 16-byte chunks of a row, of a thread
-          constexpr int kBlockChunks = C::KBlock / 16;                       // of a swizzled row
+          constexpr int CPR = D / 16, kChunks = kTile * CPR;  // 16-byte chunks of a row, of the tile
+          constexpr int kBlockChunks = C::KBlock / 16;        // of a swizzled row
 #pragma unroll
-          for (int k0 = 0; k0 < kPer; k0 += 4) {
-            uint4 u[4];
+          for (int i0 = 0; i0 < kChunks; i0 += 2 * kConvertThreads) {
+            uint4 u[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int idx = tid + (k0 + k) * kConvertThreads, row = idx / CPR, c = idx % CPR;
+            for (int k = 0; k < 2; ++k) {
+              const int idx = i0 + k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
+              if (idx >= kChunks) break;
               const int sw = C::KBlock == 128 ? row & 7 : row >> 1 & 3;
               u[k] = *reinterpret_cast<const uint4*>(from + c / kBlockChunks * (kTile * C::KBlock) + row * C::KBlock + ((c % kBlockChunks) ^ sw) * 16);
               if (tail) {
@@ -324,8 +326,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
               }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int idx = tid + (k0 + k) * kConvertThreads, row = idx / CPR, c = idx % CPR;
+            for (int k = 0; k < 2; ++k) {
+              const int idx = i0 + k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
+              if (idx >= kChunks) break;
               uint4 h[2];
               h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
               h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         if (lane == 0) flags[0] = 1;
       }
     };
-    while (walk.next(p, cum, g)) {
+    while (walk.next(p, seqs, g)) {
       const int row0 = g.row_block * kRows, rows = min(kRows, g.seq.count * p.group - row0), n = g.tiles;
       const int len = g.seq.prefix + g.seq.count;
       const float k_scale = F8 && p.scales ? __ldg(p.scales + g.head) : 1.f;
@@ -369,19 +372,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       named_sync(1, 256);  // the segment before is finished: its queries, statistics and outputs are no longer read
       // ---- queries
       {
-        constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = kRows / kStep < 8 ? kRows / kStep : 8;  // lanes of a row, rows at a time, loads in flight
-        const int l = threadIdx.x % LPR;
-        for (int r0 = threadIdx.x / LPR; r0 < kRows; r0 += kStep * kMost) {
+        constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = 4;  // lanes of a row, rows at a time, loads in flight
+        const int l = threadIdx.x % LPR, qrows = (rows + 31) & ~31;  // whole warps' rows; what others hold does not matter
+        for (int r0 = threadIdx.x / LPR; r0 < qrows; r0 += kStep * kMost) {
           uint4 u[kMost];
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
-            const int q = r0 + k * kStep, d = (row0 + q) / p.group, hh = (row0 + q) - d * p.group;
+            const int q = r0 + k * kStep, d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
             u[k] = make_uint4(0, 0, 0, 0);
             if (q < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
           }
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
             const int q = r0 + k * kStep;
+            if (q >= qrows) break;  // of a warp as a whole: its lanes have one row, or rows of one 32
             const uint4 v = make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
             if constexpr (F8) {
               const float x[8] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y),
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
         }
         if (threadIdx.x < kRows) {
-          const int d = (row0 + threadIdx.x) / p.group;
+          const int d = tree_draft(p, row0 + threadIdx.x);
           row_mask[threadIdx.x] = threadIdx.x >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
         }
         tc::fence_proxy_async_smem();
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             }
           }
       };
-      if (g.first == g.last) {
+      if (g.whole) {
         // finished here: rows go through the queries' place (no longer read) so that a row's numbers are stored together
         const float f = l == 0.f ? 0.f : (F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f) / l;
         if (active) {
@@ -611,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
         }
         if (valid && s == 0 && p.lse) {
-          const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+          const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
           p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::Lift));
         }
         tc::fence_before_sync();
@@ -620,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         const int ch = threadIdx.x % LPR;
 #pragma unroll 1
         for (int q = threadIdx.x / LPR; q < rows; q += 256 / LPR) {
-          const int d = (row0 + q) / p.group, hh = (row0 + q) - d * p.group;
+          const int d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
           *reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + 8 * ch) =
               *reinterpret_cast<const uint4*>(sq + q * (D * 2) + ((ch ^ (q & 7)) << 4));
         }
@@ -644,7 +648,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         part[(int64_t)kRows * D + kRows + r] = l;
       }
       tc::fence_before_sync();
-      if (threadIdx.x == 0 && g.first == cta) shared_item = make_int4(g.b, g.head, g.row_block, g.last);
+      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
       ++seg;
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int 
     }
     if (r < rows && mine == 0) {
       const float f = s.l == 0.f ? 0.f : vs / s.l;
-      const int d = (row0 + r) / p.group, hh = (row0 + r) - d * p.group;
+      const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
       *reinterpret_cast<uint2*>(p.out + (seq.start + d) * p.out_stride + (int64_t)(head * p.group + hh) * D + col) =
           make_uint2(pack_bf16x2(s.o.x * f, s.o.y * f), pack_bf16x2(s.o.z * f, s.o.w * f));
       if (p.lse && col == 0)

@@ -33,6 +33,7 @@ struct TreeParams {
   int64_t q_stride, out_stride;
   int64_t pages;
   uint64_t wait_ns;
+  uint64_t group_inv;   // ceil(2^32 / group)
   int batch, width, n, max_tokens, hq, hkv, group, page_shift;
   float scale_log2;     // scale * log2(e)
 };
@@ -60,9 +61,25 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 template <int TILE>
 __device__ __forceinline__ int tree_tiles(const TreeSeq& s) { return s.count ? (s.prefix + s.count + TILE - 1) / TILE : 0; }
 
-// cum[b] = length of the sequences before b (batch + 1 entries), by one warp.
+// Row r of a sequence and head: its draft, without a division (exact: r < 2^16, group <= 2^10).
+__device__ __forceinline__ int tree_draft(const TreeParams& p, int r) { return (int)((uint64_t)(uint32_t)r * p.group_inv >> 32); }
+
+// What every thread of a block knows of the sequences, in shared memory: cum[b], the length of the sequences before b, and
+// the first kCached sequences themselves.
+struct TreeMap {
+  static constexpr int kCached = 256;
+  int cum[kTreeMaxBatch + 4];
+  int4 seq[kCached];  // start, count, prefix
+};
+__device__ __forceinline__ TreeSeq tree_seq_of(const TreeParams& p, const TreeMap& map, int b) {
+  if (b >= TreeMap::kCached) return tree_seq(p, b);
+  const int4 v = map.seq[b];
+  return TreeSeq{v.x, v.y, v.z};
+}
+
+// Fills the map, by one warp.
 template <int ROWS, int TILE, bool HALVES>
-__device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
+__device__ __forceinline__ void tree_cumulate(const TreeParams& p, TreeMap& map) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -70,6 +87,7 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
     int v = 0;
     if (b < p.batch) {
       const TreeSeq s = tree_seq(p, b);
+      if (b < TreeMap::kCached) map.seq[b] = make_int4(s.start, s.count, s.prefix, 0);
       constexpr int kUnit = HALVES ? ROWS / 2 : ROWS;
       v = tree_tiles<TILE>(s) * ((s.count * p.group + kUnit - 1) / kUnit) * p.hkv;
     }
@@ -78,13 +96,13 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, int* cum) {
       const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v += u;
     }
-    if (b < p.batch) cum[b + 1] = before + v;
+    if (b < p.batch) map.cum[b + 1] = before + v;
     before += __shfl_sync(0xFFFFFFFFu, v, 31);
   }
-  if (lane == 0) cum[0] = 0;
+  if (lane == 0) map.cum[0] = 0;
 }
 
-// The blocks' ranges: block c of `ctas` takes [c * total / ctas, (c + 1) * total / ctas).
+// The blocks' ranges: block c of `ctas` takes [c * total / ctas, (c + 1) * total / ctas); the block that holds `at`:
 __device__ __forceinline__ int tree_cta_of(int64_t at, int64_t total, int ctas) { return (int)(((at + 1) * ctas - 1) / total); }
 // Blocks in use: none is left without a step.
 template <bool HALVES>
@@ -98,35 +116,36 @@ struct TreeSegment {
   TreeSeq seq;
   int b, head, row_block;
   int tile0, tiles;   // first tile, number of tiles
-  int first, last;    // blocks that share the item
+  bool starts, whole; // the item's first step is in this range; all of them are
+  int last_at;        // where its last step begins
 };
 
 // Walks a block's range segment by segment.
 template <int ROWS, int TILE, bool HALVES>
 struct TreeWalk {
-  int at, end, b, total, ctas;
-  __device__ __forceinline__ TreeWalk(int total_, int ctas_, int cta) : at(0), end(0), b(-1), total(total_), ctas(ctas_) {
+  int at, begin, end, b;
+  __device__ __forceinline__ TreeWalk(int total, int ctas, int cta) : at(0), begin(0), end(0), b(-1) {
     if (cta < ctas) {
-      at = (int)((int64_t)cta * total / ctas);
+      begin = at = (int)((int64_t)cta * total / ctas);
       end = (int)((int64_t)(cta + 1) * total / ctas);
     }
   }
-  __device__ __forceinline__ bool next(const TreeParams& p, const int* cum, TreeSegment& g) {
+  __device__ __forceinline__ bool next(const TreeParams& p, const TreeMap& map, TreeSegment& g) {
     while (at < end) {
       if (b < 0) {  // the last sequence that starts at or before `at`; empty ones are passed over
         int lo = 0, hi = p.batch;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (cum[mid] <= at) lo = mid;
+          if (map.cum[mid] <= at) lo = mid;
           else hi = mid;
         }
         b = lo;
       } else {
-        while (cum[b + 1] <= at) ++b;
+        while (map.cum[b + 1] <= at) ++b;
       }
       g.b = b;
-      g.seq = tree_seq(p, b);
-      const int nt = tree_tiles<TILE>(g.seq), r = at - cum[b], block = (HALVES ? 2 : 1) * nt * p.hkv;
+      g.seq = tree_seq_of(p, map, b);
+      const int nt = tree_tiles<TILE>(g.seq), r = at - map.cum[b], block = (HALVES ? 2 : 1) * nt * p.hkv;
       g.row_block = r / block;
       const int w = HALVES && g.seq.count * p.group - g.row_block * ROWS > ROWS / 2 ? 2 : 1;
       const int q = r - g.row_block * block;
@@ -135,9 +154,9 @@ struct TreeWalk {
       const int stop = off + (end - at) < nt * w ? off + (end - at) : nt * w;
       g.tile0 = (off + w - 1) / w;
       g.tiles = (stop + w - 1) / w - g.tile0;
-      const int64_t start = (int64_t)at - off;
-      g.first = tree_cta_of(start, total, ctas);
-      g.last = tree_cta_of(start + (int64_t)(nt - 1) * w, total, ctas);
+      g.last_at = at - off + (nt - 1) * w;
+      g.starts = at - off >= begin;
+      g.whole = g.starts && g.last_at < end;
       at += stop - off;
       if (g.tiles > 0) return true;
     }
