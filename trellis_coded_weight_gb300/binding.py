@@ -406,8 +406,28 @@ class TrellisDrafts(ctypes.Structure):
                 ("max_tokens", ctypes.c_int32)]
 
 
+_BF16, _I32, _I64, _FP32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+_current_device = torch._C._cuda_getDevice
+_stream_of_index = torch._C._cuda_getCurrentRawStream
+
+
 def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream_of_index(device.index)
+
+
+def _call(fn: str, index: int, *args):
+    """The C call of that name with device `index` current and its current stream as the last argument.
+
+    The calls of a decoding step are a few microseconds on the GPU, so the functions below test all arguments in one
+    expression first and only go through the messages of _req_tokens and _req_rows when it fails."""
+    f = getattr(_serving_lib(), fn)
+    if _current_device() == index:
+        st = f(*args, _stream_of_index(index))
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, _stream_of_index(index))
+    if st:
+        _check(fn, st)
 
 
 def _same_device(device: torch.device, **tensors):
@@ -493,7 +513,7 @@ class PagedCache:
             raise ValueError(f"pool has dtype {pool.dtype}, expected torch.bfloat16 or torch.float8_e4m3fn")
         if not pool.is_contiguous():
             raise ValueError("pool must be contiguous")
-        self.pool, self.scales, self.device = pool, scales, pool.device
+        self.pool, self.scales, self.device, self.index = pool, scales, pool.device, pool.get_device()
         self.layers, self.pages, _, self.heads, self.page_size, self.head_dim = pool.shape
         if scales is not None:
             if pool.dtype != torch.float8_e4m3fn:
@@ -528,6 +548,7 @@ class NormRope:
             _req_rows(rope, "rope", torch.float32, (rope.shape[0], rope.shape[-1]))
             _same_device(q_weight.device, rope=rope)
         self.q_heads, self.kv_heads, self.head_dim, self.device = q_heads, kv_heads, dim, q_weight.device
+        self.index = q_weight.get_device()
         self._kept = (q_weight, k_weight, rope)
         # without rotation there is no table, and any position is in range
         self._c = TrellisNormRope(q_weight.data_ptr(), k_weight.data_ptr(), rope.data_ptr() if rope is not None else None,
@@ -540,22 +561,24 @@ def qk_norm_rope_append(q, k, v, positions, slots, norm: NormRope, cache: PagedC
     """Per-head norms of q [n, q_heads, dim] and k [n, kv_heads, dim], the rotation by positions [n] int32, and the
     write of k and v to slots [n] int64 (page * page_size + row; negative: none) of the cache's layer, in one launch.
     q, k and v may be slices of one projection.  Returns the queries (out may be q)."""
-    n, dev = q.shape[0], cache.device
-    qp, qs = _req_tokens(q, "q", n, norm.q_heads, norm.head_dim)
-    kp, ks = _req_tokens(k, "k", n, norm.kv_heads, norm.head_dim)
-    vp, vs = _req_tokens(v, "v", n, norm.kv_heads, norm.head_dim)
+    n, dim, index = q.shape[0], norm.head_dim, cache.index
     if out is None:
-        out = torch.empty((n, norm.q_heads, norm.head_dim), dtype=torch.bfloat16, device=dev)
-    op, os_ = _req_tokens(out, "out", n, norm.q_heads, norm.head_dim)
-    pp = _req_rows(positions, "positions", torch.int32, (n,))
-    sp = _req_rows(slots, "slots", torch.int64, (n,))
-    if not (q.device == k.device == v.device == out.device == positions.device == slots.device == norm.device == dev):
-        raise ValueError(f"q, k, v, out, positions, slots and norm must be on the cache's device {dev}")
-    with _on(q):
-        st = _serving_lib().trellis_qk_norm_rope_append(qp, qs, kp, ks, vp, vs, pp, sp, op, os_, n, norm._ref, cache._ref,
-                                                        layer, _raw_stream(dev))
-    if st:
-        _check("trellis_qk_norm_rope_append", st)
+        out = torch.empty((n, norm.q_heads, dim), dtype=_BF16, device=cache.device)
+    wide, narrow, row, inner = (n, norm.q_heads, dim), (n, norm.kv_heads, dim), (n,), (dim, 1)
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), out.stride()
+    if not (q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16 and out.dtype is _BF16 and positions.dtype is _I32 and
+            slots.dtype is _I64 and q.shape == wide and out.shape == wide and k.shape == narrow and v.shape == narrow and
+            positions.shape == row and slots.shape == row and qs[1:] == inner and ks[1:] == inner and vs[1:] == inner and
+            os_[1:] == inner and positions.is_contiguous() and slots.is_contiguous() and
+            q.get_device() == k.get_device() == v.get_device() == out.get_device() == positions.get_device() ==
+            slots.get_device() == norm.index == index):
+        for t, name, shape in ((q, "q", wide), (k, "k", narrow), (v, "v", narrow), (out, "out", wide)):
+            _req_tokens(t, name, *shape)
+        _req_rows(positions, "positions", _I32, row)
+        _req_rows(slots, "slots", _I64, row)
+        _same_device(cache.device, q=q, k=k, v=v, out=out, positions=positions, slots=slots, norm=norm)
+    _call("trellis_qk_norm_rope_append", index, q.data_ptr(), qs[0], k.data_ptr(), ks[0], v.data_ptr(), vs[0],
+          positions.data_ptr(), slots.data_ptr(), out.data_ptr(), os_[0], n, norm._ref, cache._ref, layer)
     return out
 
 
@@ -580,6 +603,7 @@ class DraftBatch:
         _same_device(table.device, prefix=prefix, q_start=q_start, **({} if mask is None else {"mask": mask}))
         self.table, self.prefix, self.q_start, self.mask = table, prefix, q_start, mask
         self.batch, self.width, self.n, self.max_tokens, self.device = batch, width, n, max_tokens, table.device
+        self.index = table.get_device()
         self._c = TrellisDrafts(table.data_ptr(), prefix.data_ptr(), q_start.data_ptr(),
                                 mask.data_ptr() if mask is not None else None, batch, width, n, max_tokens)
         self._ref = ctypes.byref(self._c)
@@ -602,24 +626,29 @@ def tree_attention(q, cache: PagedCache, layer: int, batch: DraftBatch, workspac
     """Attention of the drafted tokens q [n, q_heads, head_dim] over their sequences' cached prefixes and the drafts
     their masks name (written to the cache before).  scale defaults to head_dim ** -0.5.  Returns (out, lse), lse
     [n, q_heads] fp32 being the log of each softmax sum; lse=False leaves it out."""
-    n, heads, dim = q.shape
-    dev = cache.device
-    qp, qs = _req_tokens(q, "q", batch.n, heads, cache.head_dim)
+    n, heads, dim = shape = q.shape
+    index = cache.index
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=torch.bfloat16, device=dev)
-    op, os_ = _req_tokens(out, "out", n, heads, dim)
+        out = torch.empty(shape, dtype=_BF16, device=cache.device)
     if lse is None:
-        lse = torch.empty((n, heads), dtype=torch.float32, device=dev)
-    lp = None if lse is False else _req_rows(lse, "lse", torch.float32, (n, heads))
-    wp, wn = _req_workspace(workspace)
-    if not (q.device == out.device == batch.device == workspace.device == dev) or (lp and lse.device != dev):
-        raise ValueError(f"q, out, lse, the batch and the workspace must be on the cache's device {dev}")
-    with _on(q):
-        st = _serving_lib().trellis_tree_attention(qp, qs, cache._ref, layer, batch._ref, heads,
-                                                   dim ** -0.5 if scale is None else scale, op, os_, lp, wp, wn,
-                                                   _raw_stream(dev))
-    if st:
-        _check("trellis_tree_attention", st)
+        lse = torch.empty((n, heads), dtype=_FP32, device=cache.device)
+    qs, os_ = q.stride(), out.stride()
+    inner = (dim, 1)
+    if not (q.dtype is _BF16 and out.dtype is _BF16 and n == batch.n and dim == cache.head_dim and out.shape == shape and
+            qs[1:] == inner and os_[1:] == inner and workspace.is_contiguous() and
+            (lse is False or (lse.dtype is _FP32 and lse.shape == (n, heads) and lse.is_contiguous() and
+                              lse.get_device() == index)) and
+            q.get_device() == out.get_device() == workspace.get_device() == batch.index == index):
+        _req_tokens(q, "q", batch.n, heads, cache.head_dim)
+        _req_tokens(out, "out", n, heads, dim)
+        if lse is not False:
+            _req_rows(lse, "lse", _FP32, (n, heads))
+            _same_device(cache.device, lse=lse)
+        _req_workspace(workspace)
+        _same_device(cache.device, q=q, out=out, workspace=workspace, batch=batch)
+    _call("trellis_tree_attention", index, q.data_ptr(), qs[0], cache._ref, layer, batch._ref, heads,
+          dim ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], None if lse is False else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, (None if lse is False else lse)
 
 
@@ -634,8 +663,7 @@ def cache_copy(cache: PagedCache, src, dst):
     n = src.shape[0]
     sp, dp = _req_rows(src, "src", torch.int32, (n,)), _req_rows(dst, "dst", torch.int32, (n,))
     _same_device(cache.device, src=src, dst=dst)
-    with _on(cache.pool):
-        _check("trellis_cache_copy", _serving_lib().trellis_cache_copy(cache._ref, sp, dp, n, _raw_stream(cache.device)))
+    _call("trellis_cache_copy", cache.index, cache._ref, sp, dp, n)
 
 
 def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, workspace, room: int = 0):
@@ -651,9 +679,7 @@ def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, work
     wp, wn = _req_workspace(workspace)
     _same_device(cache.device, table=table, lens=lens, refs=refs, parent=parent, child=child, status=status,
                  workspace=workspace)
-    with _on(table):
-        _check("trellis_cache_fork", _serving_lib().trellis_cache_fork(cache._ref, *args, pairs, rows, width, room, wp, wn,
-                                                                       _raw_stream(cache.device)))
+    _call("trellis_cache_fork", cache.index, cache._ref, *args, pairs, rows, width, room, wp, wn)
     return status
 
 
@@ -668,9 +694,7 @@ def cache_compact(cache: PagedCache, table, refs, workspace, out_table=None, out
             _req_rows(out_refs, "out_refs", torch.int32, (cache.pages,)))
     wp, wn = _req_workspace(workspace)
     _same_device(cache.device, table=table, refs=refs, out_table=out_table, out_refs=out_refs, workspace=workspace)
-    with _on(table):
-        _check("trellis_cache_compact", _serving_lib().trellis_cache_compact(cache._ref, *args, rows, width, wp, wn,
-                                                                             _raw_stream(cache.device)))
+    _call("trellis_cache_compact", cache.index, cache._ref, *args, rows, width, wp, wn)
     return out_table, out_refs
 
 
@@ -686,9 +710,7 @@ def cache_commit(cache: PagedCache, table, prefix, path, accepted, out_lens=None
             _req_rows(path, "path", torch.int32, (batch, tokens)),
             _req_rows(accepted, "accepted", torch.int32, (batch,)), _req_rows(out_lens, "out_lens", torch.int32, (batch,)))
     _same_device(cache.device, table=table, prefix=prefix, path=path, accepted=accepted, out_lens=out_lens)
-    with _on(table):
-        _check("trellis_cache_commit", _serving_lib().trellis_cache_commit(cache._ref, *args, batch, width, tokens,
-                                                                           _raw_stream(cache.device)))
+    _call("trellis_cache_commit", cache.index, cache._ref, *args, batch, width, tokens)
     return out_lens
 
 
@@ -711,31 +733,37 @@ def token_logprobs(logits, tokens, top_k: int, workspace, temperature: float = 1
     """Log probabilities of tokens [n, cands] int32 under softmax(logits / temperature), with each row's log of the
     softmax sum, entropy and top_k most likely tokens (equal logits: lowest index first).  logits [n, vocab] bf16 or
     fp32, rows may be apart.  out: five tensors to write, as TokenLogprobs."""
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
-        raise ValueError("logits must be a CUDA tensor")
     n, vocab = logits.shape
-    dev = logits.device
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"logits has dtype {logits.dtype}, expected torch.bfloat16 or torch.float32")
-    stride, one = logits.stride()
-    if one != 1 and vocab > 1:
-        raise ValueError("the logits of a row must be contiguous")
-    cands = tokens.shape[1]
+    index, cands, stride = logits.get_device(), tokens.shape[1], logits.stride()
+    dtype = logits.dtype
     if out is None:
-        f32 = dict(dtype=torch.float32, device=dev)
+        if index < 0:
+            raise ValueError("logits must be a CUDA tensor")
+        f32 = dict(dtype=_FP32, device=logits.device)
         out = (torch.empty((n, cands), **f32), torch.empty((n,), **f32), torch.empty((n,), **f32),
-               torch.empty((n, top_k), dtype=torch.int32, device=dev), torch.empty((n, top_k), **f32))
+               torch.empty((n, top_k), dtype=_I32, device=logits.device), torch.empty((n, top_k), **f32))
     lp, ls, en, ti, tl = out
-    args = (_req_rows(lp, "logprobs", torch.float32, (n, cands)), _req_rows(ls, "lse", torch.float32, (n,)),
-            _req_rows(en, "entropy", torch.float32, (n,)), _req_rows(ti, "top_ids", torch.int32, (n, top_k)),
-            _req_rows(tl, "top_logprobs", torch.float32, (n, top_k)))
-    tp = _req_rows(tokens, "tokens", torch.int32, (n, cands))
-    wp, wn = _req_workspace(workspace)
-    if not (tokens.device == lp.device == ls.device == en.device == ti.device == tl.device == workspace.device == dev):
-        raise ValueError(f"tokens, out and the workspace must be on the logits' device {dev}")
-    with _on(logits):
-        st = _serving_lib().trellis_token_logprobs(logits.data_ptr(), TRELLIS_BF16 if logits.dtype == torch.bfloat16 else TRELLIS_F32,
-                                                   stride, tp, n, vocab, cands, top_k, temperature, *args, wp, wn, _raw_stream(dev))
-    if st:
-        _check("trellis_token_logprobs", st)
+    row, given, top = (n,), (n, cands), (n, top_k)
+    if not (index >= 0 and (dtype is _BF16 or dtype is _FP32) and stride[1] == 1 and tokens.dtype is _I32 and ti.dtype is _I32 and
+            lp.dtype is _FP32 and ls.dtype is _FP32 and en.dtype is _FP32 and tl.dtype is _FP32 and tokens.shape == given and
+            lp.shape == given and ls.shape == row and en.shape == row and ti.shape == top and tl.shape == top and
+            tokens.is_contiguous() and lp.is_contiguous() and ls.is_contiguous() and en.is_contiguous() and
+            ti.is_contiguous() and tl.is_contiguous() and workspace.is_contiguous() and
+            tokens.get_device() == lp.get_device() == ls.get_device() == en.get_device() == ti.get_device() ==
+            tl.get_device() == workspace.get_device() == index):
+        if index < 0:
+            raise ValueError("logits must be a CUDA tensor")
+        if dtype not in (_BF16, _FP32):
+            raise ValueError(f"logits has dtype {dtype}, expected torch.bfloat16 or torch.float32")
+        if stride[1] != 1 and vocab > 1:
+            raise ValueError("the logits of a row must be contiguous")
+        for t, name, dt, shape in ((tokens, "tokens", _I32, given), (lp, "logprobs", _FP32, given), (ls, "lse", _FP32, row),
+                                   (en, "entropy", _FP32, row), (ti, "top_ids", _I32, top), (tl, "top_logprobs", _FP32, top)):
+            _req_rows(t, name, dt, shape)
+        _req_workspace(workspace)
+        _same_device(logits.device, tokens=tokens, logprobs=lp, lse=ls, entropy=en, top_ids=ti, top_logprobs=tl,
+                     workspace=workspace)
+    _call("trellis_token_logprobs", index, logits.data_ptr(), TRELLIS_BF16 if dtype is _BF16 else TRELLIS_F32, stride[0],
+          tokens.data_ptr(), n, vocab, cands, top_k, temperature, lp.data_ptr(), ls.data_ptr(), en.data_ptr(), ti.data_ptr(),
+          tl.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out if isinstance(out, TokenLogprobs) else TokenLogprobs(*out)

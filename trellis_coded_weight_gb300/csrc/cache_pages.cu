@@ -4,7 +4,7 @@
 // Fork and compact are two launches each.  A planning kernel of one thread block works on the integers (page table,
 // reference counts): a running count over the pages gives the k-th lowest free page, so the result does not depend
 // on any order of execution.  It leaves a list of page copies in the workspace.  The copying kernel then moves them in all layers, in
-// units of 16 KB spread over the GPU.  The copies are bound by HBM; the planning by latency.
+// units of 16 KB spread evenly over the GPU.  The copies are bound by HBM; the planning by latency.
 #include "common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyThreads = 256;
+constexpr int kCopyBlocks = 4;  // of an SM
 constexpr int kUnit = 16384;  // bytes of a copying step: four 16-byte loads of each thread in flight
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) { return __ldcs(p); }
@@ -34,31 +35,58 @@ struct CopyParams {
   int64_t entries;
 };
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyParams p) {
+// A block takes a contiguous range of the units (pair major, then layer, then place in the page), stepping through them
+// without divisions; a unit's loads go out before the stores of the one before it.
+__global__ void __launch_bounds__(kCopyThreads, kCopyBlocks) copy_pages_kernel(const CopyParams p) {
   pdl_enter();
   const int n = p.count ? __ldcg(p.count) : p.most;
   const int per_page = (int)((p.page_bytes + kUnit - 1) / kUnit);
   const int64_t units = (int64_t)n * p.layers * per_page;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t pl = u / per_page;
-    const int i = (int)(pl / p.layers);
-    const int64_t layer = pl - (int64_t)i * p.layers, at = (u - pl * per_page) * kUnit;
-    const int64_t src = __ldcg(p.src + i), dst = __ldcg(p.dst + i);
-    if (src < 0 || src >= p.pages || dst < 0 || dst >= p.pages) continue;
-    const uint4* from = reinterpret_cast<const uint4*>(p.pool + layer * p.layer_bytes + src * p.page_bytes + at);
-    uint4* to = reinterpret_cast<uint4*>(p.pool + layer * p.layer_bytes + dst * p.page_bytes + at);
-    const int vecs = (int)((p.page_bytes - at < kUnit ? p.page_bytes - at : kUnit) / 16);
-    uint4 v[4];
+  const int64_t lo = units * blockIdx.x / gridDim.x;
+  int left = (int)(units * (blockIdx.x + 1) / gridDim.x - lo);
+  int chunk = (int)(lo % per_page), layer = (int)(lo / per_page % p.layers), i = (int)(lo / per_page / p.layers);
+  constexpr int kVecs = kUnit / 16 / kCopyThreads;
+  struct Unit {
+    uint4 v[kVecs];
+    uint4* to;
+    int vecs;  // of the unit; 0: nothing to move
+  };
+  const auto fetch = [&](Unit& u) {
+    const int64_t src = __ldcg(p.src + i), dst = __ldcg(p.dst + i), at = (int64_t)chunk * kUnit;
+    u.vecs = 0;
+    if (src >= 0 && src < p.pages && dst >= 0 && dst < p.pages) {
+      const int64_t rest = p.page_bytes - at;
+      u.vecs = (int)((rest < kUnit ? rest : kUnit) / 16);
+      const uint4* from = reinterpret_cast<const uint4*>(p.pool + layer * p.layer_bytes + src * p.page_bytes + at);
+      u.to = reinterpret_cast<uint4*>(p.pool + layer * p.layer_bytes + dst * p.page_bytes + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = threadIdx.x + j * kCopyThreads;
-      if (e < vecs) v[j] = ld_stream(from + e);
+      for (int j = 0; j < kVecs; ++j) {
+        const int e = threadIdx.x + j * kCopyThreads;
+        if (e < u.vecs) u.v[j] = ld_stream(from + e);
+      }
     }
+    if (++chunk == per_page) {
+      chunk = 0;
+      if (++layer == p.layers) {
+        layer = 0;
+        ++i;
+      }
+    }
+  };
+  const auto store = [&](const Unit& u) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kVecs; ++j) {
       const int e = threadIdx.x + j * kCopyThreads;
-      if (e < vecs) to[e] = v[j];
+      if (e < u.vecs) u.to[e] = u.v[j];
     }
+  };
+  Unit a, b;
+  if (left > 0) fetch(a);
+  for (; left > 0; left -= 2) {
+    if (left > 1) fetch(b);
+    store(a);
+    if (left > 2) fetch(a);
+    if (left > 1) store(b);
   }
   for (int64_t e = blockIdx.x * (int64_t)kCopyThreads + threadIdx.x; e < p.entries; e += (int64_t)gridDim.x * kCopyThreads) {
     const int32_t page = p.table[e];
@@ -68,7 +96,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPara
 
 cudaError_t launch_copy(CopyParams p, cudaStream_t st) {
   const int64_t units = (int64_t)p.most * p.layers * ((p.page_bytes + kUnit - 1) / kUnit);
-  const int64_t full = 8 * (int64_t)device_sm_count();  // eight blocks of 256 threads fill an SM
+  const int64_t full = kCopyBlocks * (int64_t)device_sm_count();
   int64_t grid = units < full ? units : full;
   const int64_t table = (p.entries + kCopyThreads - 1) / kCopyThreads;
   if (grid < table) grid = table < full ? table : full;

@@ -18,6 +18,7 @@ namespace trellis {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // rounds of heads whose loads are in flight
 
 struct Params {
   NormRopeTokens t;
@@ -79,65 +80,80 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
   // the lane that holds the other half of this lane's pairs
   const int partner = (lane - l) + (second ? l - half / 8 : l + half / 8);
 
-  // every lane of a warp takes part in each round of heads
-  for (int h0 = blockIdx.y * GROUPS; h0 < heads; h0 += gridDim.y * GROUPS) {
-    const int h = h0 + group;
-    const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, active = h < heads;
-    const int hk = is_q ? 0 : is_k ? h - p.hq : h - p.hq - p.hkv;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (active) {
-      const uint16_t* x = is_q ? p.t.q + tok * p.t.q_stride + (int64_t)h * D
-                               : is_k ? p.t.k + tok * p.t.k_stride + (int64_t)hk * D : p.t.v + tok * p.t.v_stride + (int64_t)hk * D;
-      u = *reinterpret_cast<const uint4*>(x + 8 * l);
+  // Every lane of a warp takes part in each round of heads; the loads of kBatch rounds go out together (one at a time
+  // measured 25.7 us against 16.5 for 4099 tokens of 20 heads of 256, e4m3: too few bytes in flight).
+  for (int h00 = blockIdx.y * GROUPS; h00 < heads; h00 += gridDim.y * GROUPS * kBatch) {
+    uint4 us[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int h = h00 + b * gridDim.y * GROUPS + group;
+      us[b] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        const uint16_t* x = h < p.hq ? p.t.q + tok * p.t.q_stride + (int64_t)h * D
+                            : h < p.hq + p.hkv ? p.t.k + tok * p.t.k_stride + (int64_t)(h - p.hq) * D
+                                               : p.t.v + tok * p.t.v_stride + (int64_t)(h - p.hq - p.hkv) * D;
+        us[b] = *reinterpret_cast<const uint4*>(x + 8 * l);
+      }
     }
-    float x[8];
-    unpack8(u, x);
-    float ss = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < kBatch; ++b) {
+      const int h0 = h00 + b * gridDim.y * GROUPS;
+      if (h0 >= heads) break;
+      const uint4 u = us[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+      for (int i = 1; i < kBatch; ++i) us[i - 1] = us[i];
+      const int h = h0 + group;
+      const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, active = h < heads;
+      const int hk = is_q ? 0 : is_k ? h - p.hq : h - p.hq - p.hkv;
+      float x[8];
+      unpack8(u, x);
+      float ss = 0.f;
 #pragma unroll
-    for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    const bool norm = is_q || is_k;
-    if (norm) {
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      float w[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>((is_q ? p.wq : p.wk) + 8 * l)), w);
+      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (w[i] + p.offset);
-    }
-    if constexpr (INTERLEAVED) {
-      if (norm && turned) {
+      for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      const bool norm = is_q || is_k;
+      if (norm) {
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        float w[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>((is_q ? p.wq : p.wk) + 8 * l)), w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * c[i] - b * s[i];
-          x[2 * i + 1] = b * c[i] + a * s[i];
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (w[i] + p.offset);
+      }
+      if constexpr (INTERLEAVED) {
+        if (norm && turned) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = a * c[i] - b * s[i];
+            x[2 * i + 1] = b * c[i] + a * s[i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = __shfl_sync(0xFFFFFFFFu, x[i], partner & 31);
+          if (norm && turned) x[i] = x[i] * c[i] - o * s[i];
         }
       }
-    } else {
+      if (norm && !pos_ok)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xFFFFFFFFu, x[i], partner & 31);
-        if (norm && turned) x[i] = x[i] * c[i] - o * s[i];
-      }
-    }
-    if (norm && !pos_ok)
+        for (int i = 0; i < 8; ++i) x[i] = __int_as_float(0x7FC00000);
+      if (!active) continue;
+      if (is_q) {
+        *reinterpret_cast<uint4*>(p.t.q_out + tok * p.t.q_out_stride + (int64_t)h * D + 8 * l) = pack8(x);
+      } else if (slot_ok) {
+        const int64_t page = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
+        const int64_t e = ((((page * 2 + (is_k ? 0 : 1)) * p.hkv + hk) << p.page_shift) + off) * D + 8 * l;
+        if constexpr (E4M3) {
+          const float sc = p.scales ? __ldg(p.scales + (is_k ? 0 : p.hkv) + hk) : 1.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __int_as_float(0x7FC00000);
-    if (!active) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(p.t.q_out + tok * p.t.q_out_stride + (int64_t)h * D + 8 * l) = pack8(x);
-    } else if (slot_ok) {
-      const int64_t page = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
-      const int64_t e = ((((page * 2 + (is_k ? 0 : 1)) * p.hkv + hk) << p.page_shift) + off) * D + 8 * l;
-      if constexpr (E4M3) {
-        const float sc = p.scales ? __ldg(p.scales + (is_k ? 0 : p.hkv) + hk) : 1.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], sc);
-        *reinterpret_cast<uint2*>(p.pool + e) = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
-                                                           e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
-      } else {
-        *reinterpret_cast<uint4*>(p.pool + 2 * e) = is_k ? pack8(x) : u;  // values keep their bits
+          for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], sc);
+          *reinterpret_cast<uint2*>(p.pool + e) = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
+                                                             e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+        } else {
+          *reinterpret_cast<uint4*>(p.pool + 2 * e) = is_k ? pack8(x) : u;  // values keep their bits
+        }
       }
     }
   }

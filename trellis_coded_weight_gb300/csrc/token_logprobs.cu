@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerSM = 5;          // blocks of an SM at a time
+constexpr int kPerSM = 4;          // blocks of an SM at a time
 constexpr int kList = 768;         // numbers that may reach the threshold
 constexpr int kBatch = 4;          // 16-byte loads of a thread in flight
 constexpr int kMaxSplits = 64;
@@ -163,12 +163,16 @@ struct Shared {
 // caller's barrier precedes it; ends with a barrier.
 __device__ __forceinline__ void cut_back(Shared& sh, int top_k) {
   const int count = sh.count;
-  for (int i = threadIdx.x; i < count; i += kThreads) {
-    const unsigned long long mine = sh.list[i];
+  // several threads count for one key where there are few
+  const int per = count <= 32 ? 8 : count <= 64 ? 4 : count <= 128 ? 2 : 1;
+  for (int i0 = 0; i0 < count; i0 += kThreads / per) {
+    const int i = i0 + threadIdx.x / per;
+    const unsigned long long mine = i < count ? sh.list[i] : 0ull;
     int rank = 0;
 #pragma unroll 4
-    for (int j = 0; j < count; ++j) rank += sh.list[j] > mine;
-    if (rank < top_k) sh.best[rank] = mine;
+    for (int j = threadIdx.x % per; j < count; j += per) rank += sh.list[j] > mine;
+    for (int o = 1; o < per; o <<= 1) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, o);
+    if (i < count && rank < top_k && threadIdx.x % per == 0) sh.best[rank] = mine;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.count = count < top_k ? count : top_k;
@@ -240,6 +244,15 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
     sh.n_holders = 0;
   }
 
+  // the given tokens' logits are fetched early, by every block of the row: the last one has them when it needs them
+  float cand = 0.f;
+  bool cand_ok = false;
+  if (tid < p.cands) {
+    const int32_t tok = p.tokens[row * p.cands + tid];
+    cand_ok = tok >= 0 && tok < p.vocab;
+    if (cand_ok) cand = Vec<T>::one(x.x + tok);
+  }
+
   // ---- the sums, and each thread's largest number
   Sums acc{-INFINITY, 0.f, 0.f};
   const auto add = [&](const uint4 (&u)[kBatch], int n) {
@@ -273,21 +286,29 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
     acc.t += t.x + t.y;
   };
   {
-    uint4 u[kBatch];
-    int v = first + tid;
-    for (; v + (kBatch - 1) * kThreads < last; v += kBatch * kThreads) {
+    // the next batch's loads are in flight while one is worked on
+    uint4 u[kBatch], next[kBatch];
+    int v = first + tid, n = 0, more = 0;
+    const auto fetch = [&](uint4 (&to)[kBatch], int at) {
+      int k = 0;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) u[b] = x.load(v + b * kThreads);
-      add(u, kBatch);
+      for (int b = 0; b < kBatch; ++b)
+        if (at + b * kThreads < last) {
+          to[b] = x.load(at + b * kThreads);
+          k = b + 1;
+        }
+      return k;
+    };
+    n = fetch(u, v);
+    while (n) {
+      v += kBatch * kThreads;
+      more = fetch(next, v);
+      if (n == kBatch) add(u, kBatch);
+      else add(u, n);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) u[b] = next[b];
+      n = more;
     }
-    int n = 0;
-#pragma unroll
-    for (int b = 0; b < kBatch - 1; ++b)
-      if (v + b * kThreads < last) {
-        u[b] = x.load(v + b * kThreads);
-        n = b + 1;
-      }
-    if (n) add(u, n);
   }
 
   // ---- the alternatives
@@ -401,10 +422,17 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
     }
     __syncthreads();
     if (!sh.last) return;
-    acc = Sums{-INFINITY, 0.f, 0.f};
-    for (int i = 0; i < p.splits; ++i) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + (row * p.splits + i) * 4));
-      acc = join(acc, Sums{v.x, v.y, v.z}, p.c);
+    if (warp == 0) {  // the parts' sums, by a warp, while the others fetch keys
+      Sums a{-INFINITY, 0.f, 0.f};
+      for (int i = lane; i < p.splits; i += 32) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.sums + (row * p.splits + i) * 4));
+        a = join(a, Sums{v.x, v.y, v.z}, p.c);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        a = join(a, Sums{__shfl_xor_sync(0xFFFFFFFFu, a.r, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o),
+                         __shfl_xor_sync(0xFFFFFFFFu, a.t, o)}, p.c);
+      if (lane == 0) sh.part[0] = a;
     }
     const int total = p.splits * p.top_k;
     for (int base = 0; base < total; base += kList - kMaxTop) {  // as many as fit beside the best so far
@@ -419,6 +447,8 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
       __syncthreads();
       cut_back(sh, p.top_k);
     }
+    if (!total) __syncthreads();
+    acc = sh.part[0];
   }
 
   const float lns = logf(acc.s);
@@ -433,10 +463,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
     p.top_ids[row * p.top_k + tid] = (int32_t)~(uint32_t)key;
     p.top_logprobs[row * p.top_k + tid] = logprob(from_order_bits((uint32_t)(key >> 32)));
   }
-  for (int i = tid; i < p.cands; i += kThreads) {
-    const int32_t tok = p.tokens[row * p.cands + i];
-    p.logprobs[row * p.cands + i] = tok >= 0 && tok < p.vocab ? logprob(Vec<T>::one(x.x + tok)) : -INFINITY;
-  }
+  if (tid < p.cands) p.logprobs[row * p.cands + tid] = cand_ok ? logprob(cand) : -INFINITY;
 }
 
 // Blocks of a row: as many as the GPU holds at a time over all rows, each thread with one vector at least.  At 256
