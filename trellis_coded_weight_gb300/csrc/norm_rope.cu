@@ -7,8 +7,10 @@
 //
 // A head lives in D/8 neighbouring lanes, 8 numbers (one 16-byte load) each: the sum of squares is a shuffle over
 // those lanes, a pair that spans half a rotation is one shuffle away, an interleaved pair is in one lane.  Nothing is
-// staged.  A thread block serves one token (and a share of its heads); its lanes keep their 8 cosines and sines,
-// which every head of the token uses.  Bound: launch latency for a few tokens, HBM beyond.
+// staged.  A group of lanes has a share of one token's heads -- queries, then keys, then values, each in a loop of its own
+// with its weights in registers -- and keeps the cosines and sines of its lanes.
+// Bound: launch latency for a few tokens; beyond, HBM and the issue of instructions are close (a general loop over all
+// kinds of heads took three times the instructions, and 25 us where this takes 21 for 4099 tokens of 20 heads of 256, e4m3).
 #include "common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
@@ -18,7 +20,8 @@ namespace trellis {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // rounds of heads whose loads are in flight
+// Blocks of an SM at a time (4096 tokens of 56 heads of 128: 28.1 us with 4, 36 with 5 or 6, whose registers spill).
+constexpr int kPerSM = 4;
 
 struct Params {
   NormRopeTokens t;
@@ -27,19 +30,18 @@ struct Params {
   const float* scales;  // [2][kv_heads] of the layer, or null
   uint8_t* pool;        // the layer's pages
   int64_t max_pos, pages;
-  int hq, hkv, rot, page_shift;
+  int hq, hkv, rot, page_shift, split;
   float eps, offset;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  x[0] = bf16lo_to_f32(u.x); x[1] = bf16hi_to_f32(u.x);
-  x[2] = bf16lo_to_f32(u.y); x[3] = bf16hi_to_f32(u.y);
-  x[4] = bf16lo_to_f32(u.z); x[5] = bf16hi_to_f32(u.z);
-  x[6] = bf16lo_to_f32(u.w); x[7] = bf16hi_to_f32(u.w);
+__device__ __forceinline__ void unpack8(const uint4& u, float2 (&x)[4]) {
+  x[0] = make_float2(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x));
+  x[1] = make_float2(bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
+  x[2] = make_float2(bf16lo_to_f32(u.z), bf16hi_to_f32(u.z));
+  x[3] = make_float2(bf16lo_to_f32(u.w), bf16hi_to_f32(u.w));
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
 }
 
 // Two fp32 to e4m3 (nearest even; beyond the largest value: clamped), a in the low byte.
@@ -50,126 +52,143 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
 }
 
 template <int D, bool E4M3, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kPerSM) norm_rope_kernel(const Params p) {
   pdl_enter();
-  constexpr int LPH = D / 8;               // lanes per head
-  constexpr int GROUPS = kThreads / LPH;   // heads of a block at a time
-  const int lane = threadIdx.x & 31, l = threadIdx.x % LPH, group = threadIdx.x / LPH;
-  const int64_t tok = blockIdx.x;
-  const int heads = p.hq + 2 * p.hkv;
+  constexpr int LPH = D / 8;  // lanes of a head
+  const int lane = threadIdx.x & 31, l = lane % LPH;
+  constexpr uint32_t kGroup = LPH == 32 ? 0xFFFFFFFFu : (1u << LPH) - 1;
+  const uint32_t lanes = kGroup << (lane - l);  // this group's
+  const int heads = p.hq + 2 * p.hkv, split = p.split;
+  // this group: heads h, h + split, .. of a token
+  const uint32_t gid = (blockIdx.x * (uint32_t)kThreads + threadIdx.x) / LPH;
+  const uint32_t tok = gid / (uint32_t)split;
+  if (tok >= (uint32_t)p.t.n) return;
+  int h = (int)(gid - tok * (uint32_t)split);
 
   const int pos = __ldg(p.t.positions + tok);
   const int64_t slot = __ldg(p.t.slots + tok);
+  const uint16_t* const qb = p.t.q + tok * p.t.q_stride + 8 * l;
+  const uint16_t* const kb = p.t.k + tok * p.t.k_stride + 8 * l;
+  const uint16_t* const vb = p.t.v + tok * p.t.v_stride + 8 * l;
+  const auto fetch = [&](int at) {
+    const uint16_t* from = at < p.hq ? qb + at * D : at < p.hq + p.hkv ? kb + (at - p.hq) * D : vb + (at - p.hq - p.hkv) * D;
+    return at < heads ? *reinterpret_cast<const uint4*>(from) : make_uint4(0, 0, 0, 0);
+  };
+  uint4 u = fetch(h), ahead = fetch(h + split);  // two heads in flight, before the position is used
+
   const bool pos_ok = pos >= 0 && pos < p.max_pos;
-  const bool slot_ok = slot >= 0 && slot < p.pages << p.page_shift;
   const bool turned = 8 * l < p.rot;  // rot is a multiple of 16: a lane is rotated as a whole
   const int half = p.rot >> 1;
   const bool second = !INTERLEAVED && 8 * l >= half;  // the b of its pairs
-  float c[INTERLEAVED ? 4 : 8], s[INTERLEAVED ? 4 : 8];
+  // interleaved: cosines and sines of the lane's four pairs; else of its eight numbers, two by two.  No turn: 1 and 0;
+  // positions out of range: NaN.
+  float2 c[INTERLEAVED ? 2 : 4], s[INTERLEAVED ? 2 : 4];
+  const float one = pos_ok ? 1.f : __int_as_float(0x7FC00000);
+#pragma unroll
+  for (int i = 0; i < (INTERLEAVED ? 2 : 4); ++i) {
+    c[i] = make_float2(one, one);
+    s[i] = make_float2(0.f, 0.f);
+  }
   if (turned && pos_ok) {
     const float* row = p.rope + (int64_t)pos * p.rot + (INTERLEAVED ? 4 * l : second ? 8 * l - half : 8 * l);
+    const float sign = INTERLEAVED || second ? 1.f : -1.f;  // y' = y c + partner s for both halves
 #pragma unroll
-    for (int i = 0; i < (INTERLEAVED ? 4 : 8); i += 4) {
-      *reinterpret_cast<float4*>(c + i) = __ldg(reinterpret_cast<const float4*>(row + i));
-      *reinterpret_cast<float4*>(s + i) = __ldg(reinterpret_cast<const float4*>(row + half + i));
+    for (int i = 0; i < (INTERLEAVED ? 2 : 4); i += 2) {
+      const float4 cv = __ldg(reinterpret_cast<const float4*>(row + 2 * i)), sv = __ldg(reinterpret_cast<const float4*>(row + half + 2 * i));
+      c[i] = make_float2(cv.x, cv.y);
+      c[i + 1] = make_float2(cv.z, cv.w);
+      s[i] = make_float2(sign * sv.x, sign * sv.y);
+      s[i + 1] = make_float2(sign * sv.z, sign * sv.w);
     }
-    if (second)
-#pragma unroll
-      for (int i = 0; i < (INTERLEAVED ? 4 : 8); ++i) s[i] = -s[i];  // y' = y c - partner s  for both halves
   }
   // the lane that holds the other half of this lane's pairs
-  const int partner = (lane - l) + (second ? l - half / 8 : l + half / 8);
+  const int partner = turned ? (lane - l) + (second ? l - half / 8 : l + half / 8) : lane;
 
-  // Every lane of a warp takes part in each round of heads; the loads of kBatch rounds go out together (one at a time
-  // measured 25.7 us against 16.5 for 4099 tokens of 20 heads of 256, e4m3: too few bytes in flight).
-  for (int h00 = blockIdx.y * GROUPS; h00 < heads; h00 += gridDim.y * GROUPS * kBatch) {
-    uint4 us[kBatch];
+  float2 w[4];
+  const auto weights = [&](const uint16_t* from) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(from + 8 * l)), w);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int h = h00 + b * gridDim.y * GROUPS + group;
-      us[b] = make_uint4(0, 0, 0, 0);
-      if (h < heads) {
-        const uint16_t* x = h < p.hq ? p.t.q + tok * p.t.q_stride + (int64_t)h * D
-                            : h < p.hq + p.hkv ? p.t.k + tok * p.t.k_stride + (int64_t)(h - p.hq) * D
-                                               : p.t.v + tok * p.t.v_stride + (int64_t)(h - p.hq - p.hkv) * D;
-        us[b] = *reinterpret_cast<const uint4*>(x + 8 * l);
+    for (int i = 0; i < 4; ++i) w[i] = __fadd2_rn(w[i], make_float2(p.offset, p.offset));
+  };
+  const auto advance = [&] {
+    h += split;
+    u = ahead;
+    ahead = fetch(h + split);
+  };
+  // the head in u, normed and rotated
+  const auto normed = [&](float2 (&x)[4]) {
+    unpack8(u, x);
+    float2 sq = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sq = __ffma2_rn(x[i], x[i], sq);
+    float ss = sq.x + sq.y;
+#pragma unroll
+    for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __fmul2_rn(__fmul2_rn(x[i], make_float2(r, r)), w[i]);
+    if constexpr (INTERLEAVED) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float cc = i & 1 ? c[i / 2].y : c[i / 2].x, sc = i & 1 ? s[i / 2].y : s[i / 2].x;
+        x[i] = make_float2(x[i].x * cc - x[i].y * sc, x[i].y * cc + x[i].x * sc);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 o = make_float2(__shfl_sync(lanes, x[i].x, partner), __shfl_sync(lanes, x[i].y, partner));
+        x[i] = __ffma2_rn(o, s[i], __fmul2_rn(x[i], c[i]));
       }
     }
-#pragma unroll 1
-    for (int b = 0; b < kBatch; ++b) {
-      const int h0 = h00 + b * gridDim.y * GROUPS;
-      if (h0 >= heads) break;
-      const uint4 u = us[0];
-#pragma unroll
-      for (int i = 1; i < kBatch; ++i) us[i - 1] = us[i];
-      const int h = h0 + group;
-      const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv, active = h < heads;
-      const int hk = is_q ? 0 : is_k ? h - p.hq : h - p.hq - p.hkv;
-      float x[8];
-      unpack8(u, x);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-#pragma unroll
-      for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const bool norm = is_q || is_k;
-      if (norm) {
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        float w[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>((is_q ? p.wq : p.wk) + 8 * l)), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (w[i] + p.offset);
-      }
-      if constexpr (INTERLEAVED) {
-        if (norm && turned) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = a * c[i] - b * s[i];
-            x[2 * i + 1] = b * c[i] + a * s[i];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xFFFFFFFFu, x[i], partner & 31);
-          if (norm && turned) x[i] = x[i] * c[i] - o * s[i];
-        }
-      }
-      if (norm && !pos_ok)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __int_as_float(0x7FC00000);
-      if (!active) continue;
-      if (is_q) {
-        *reinterpret_cast<uint4*>(p.t.q_out + tok * p.t.q_out_stride + (int64_t)h * D + 8 * l) = pack8(x);
-      } else if (slot_ok) {
-        const int64_t page = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
-        const int64_t e = ((((page * 2 + (is_k ? 0 : 1)) * p.hkv + hk) << p.page_shift) + off) * D + 8 * l;
-        if constexpr (E4M3) {
-          const float sc = p.scales ? __ldg(p.scales + (is_k ? 0 : p.hkv) + hk) : 1.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], sc);
-          *reinterpret_cast<uint2*>(p.pool + e) = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
-                                                             e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
-        } else {
-          *reinterpret_cast<uint4*>(p.pool + 2 * e) = is_k ? pack8(x) : u;  // values keep their bits
-        }
-      }
+  };
+
+  weights(p.wq);
+  uint16_t* const out = p.t.q_out + tok * p.t.q_out_stride + 8 * l;
+  while (h < p.hq) {
+    float2 x[4];
+    normed(x);
+    *reinterpret_cast<uint4*>(out + h * D) = pack8(x);
+    advance();
+  }
+  if (slot < 0 || slot >= p.pages << p.page_shift) return;
+  // the heads of keys, then those of values, are one after the other in a page
+  const int64_t kv_row = ((slot >> p.page_shift) * 2 * p.hkv << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  uint8_t* const to = p.pool + (kv_row * D + 8 * l) * (E4M3 ? 1 : 2);
+  const auto keep = [&](const float2 (&x)[4], int hk, const uint4* same) {
+    uint8_t* at = to + ((int64_t)(hk * D) << p.page_shift) * (E4M3 ? 1 : 2);
+    if constexpr (E4M3) {
+      const float inv = p.scales ? __fdiv_rn(1.f, __ldg(p.scales + hk)) : 1.f;
+      *reinterpret_cast<uint2*>(at) = make_uint2(e4m3x2(x[0].x * inv, x[0].y * inv) | e4m3x2(x[1].x * inv, x[1].y * inv) << 16,
+                                                 e4m3x2(x[2].x * inv, x[2].y * inv) | e4m3x2(x[3].x * inv, x[3].y * inv) << 16);
+    } else {
+      *reinterpret_cast<uint4*>(at) = same ? *same : pack8(x);
     }
+  };
+  weights(p.wk);
+  while (h < p.hq + p.hkv) {
+    float2 x[4];
+    normed(x);
+    keep(x, h - p.hq, nullptr);
+    advance();
+  }
+  while (h < heads) {
+    float2 x[4];
+    unpack8(u, x);
+    keep(x, h - p.hq, &u);  // bf16 values keep their bits
+    advance();
   }
 }
 
 template <int D, bool E4M3>
-cudaError_t launch_d(const Params& p, int interleaved, cudaStream_t st) {
+cudaError_t launch_d(Params p, int interleaved, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D / 8);
   const int heads = p.hq + 2 * p.hkv;
-  // A block per token once tokens alone fill the GPU several times over; below that a token's heads are spread
-  // over blocks until each group of lanes has one head.
-  const int64_t want = 8 * (int64_t)device_sm_count();
-  const int rounds = (heads + GROUPS - 1) / GROUPS;
-  int64_t split = (want + p.t.n - 1) / p.t.n;
-  if (split > rounds) split = rounds;
-  const dim3 grid((unsigned)p.t.n, (unsigned)split);
+  // A token's heads go to as many groups of lanes as fill the GPU once over all tokens: several heads each for many
+  // tokens, one for a few.  (Rounding up instead, into a second wave, measured 35 us against 28.)
+  const int64_t groups = (int64_t)kPerSM * device_sm_count() * GROUPS;
+  const int64_t split = groups / p.t.n;
+  p.split = (int)(split < 1 ? 1 : split > heads ? heads : split);
+  const dim3 grid((unsigned)(((int64_t)p.t.n * p.split + GROUPS - 1) / GROUPS));
   return interleaved ? launch_pdl(norm_rope_kernel<D, E4M3, true>, grid, dim3(kThreads), 0, st, p)
                      : launch_pdl(norm_rope_kernel<D, E4M3, false>, grid, dim3(kThreads), 0, st, p);
 }
