@@ -460,21 +460,26 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             }
             tmem_st_wait();
           }
-          // ---- the row's maximum.  Both passes over the scores are loops over 32 columns: reading tensor memory twice costs
-          // less than the registers and the code of a step held whole
+          // ---- the row's maximum.  Both passes over the scores are loops over 64 columns: reading tensor memory twice costs less
+          // than the registers and the code of a step held whole, and a loop over 32 waits twice as often.
+          uint32_t x[2][32];
           float mx = -INFINITY;
-#pragma unroll 1
-          for (int w = 0; w < W; ++w) {
-            uint32_t x[32];
-            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
-            tc::tmem_ld_wait();
-            float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+          const auto largest = [&](const uint32_t (&v)[32]) {
+            float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
             for (int j = 2; j < 30; j += 4) {
-              a = fmaxf(fmaxf(a, __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
-              b = fmaxf(fmaxf(b, __uint_as_float(x[j + 2])), __uint_as_float(x[j + 3]));
+              a = fmaxf(fmaxf(a, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+              b = fmaxf(fmaxf(b, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
             }
-            mx = fmaxf(mx, fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]))));
+            mx = fmaxf(mx, fmaxf(fmaxf(a, b), fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]))));
+          };
+#pragma unroll 1
+          for (int w = 0; w < W; w += 2) {
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x[0]);
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w + 32, x[1]);
+            tc::tmem_ld_wait();
+            largest(x[0]);
+            largest(x[1]);
           }
           mx *= c;
           // ---- the maximum in use, from the warp that has the tile before; moved, and handed on
@@ -506,20 +511,25 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           // ---- weights, over the scores
           const float ms = m == -INFINITY ? C::Lift : C::Lift - m;
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int w = 0; w < W; ++w) {
-            uint32_t x[32], e[16];
-            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x);
-            tc::tmem_ld_wait();
+          const auto weigh = [&](const uint32_t (&v)[32], int w) {
+            uint32_t e[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), make_float2(c, c), make_float2(ms, ms));
+              float2 y = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), make_float2(c, c), make_float2(ms, ms));
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum = __fadd2_rn(sum, y);
               e[j >> 1] = F8 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
             }
             tmem_st_x16(t_s + 16 * w, e);
+          };
+#pragma unroll 1
+          for (int w = 0; w < W; w += 2) {
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w, x[0]);
+            tc::tmem_ld_32x32b_x32(t_s + 32 * w + 32, x[1]);
+            tc::tmem_ld_wait();
+            weigh(x[0], w);
+            weigh(x[1], w + 1);
           }
           l += sum.x + sum.y;
           tmem_st_wait();
