@@ -171,6 +171,23 @@ def test_what_is_not_seen_does_not_reach_the_result(d, f8):
     assert got[seen][:, :, 5].all() and not got[~seen].any() and int(got[seen].sum()) == int(seen.sum()) * s.hq
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("d,hq", [(64, 16), (128, 8), (256, 10)])
+def test_odd_values_in_short_sequences_one_after_another(d, hq, f8):
+    # every sequence is one short item and has a draft whose values are no numbers: each block has several such items
+    count, t = 700, 5
+    lens = [int(v) for v in np.random.default_rng(5).integers(0, 40, count)]
+    s = Step(lens, [t] * count, hq, 2, d, 16, f8=f8, seed=11)
+    bad = s.pool.view(torch.uint8 if f8 else torch.int16)
+    at = torch.as_tensor([[s.table[b, (lens[b] + b % t) // 16], (lens[b] + b % t) % 16] for b in range(count)]).cuda()
+    bad[0, at[:, 0], 1, :, at[:, 1]] = 0x7F if f8 else 0x7FC0
+    out, _ = s.run()
+    masks = torch.tensor(s.masks).view(count, t)
+    sees = (masks >> (torch.arange(count) % t)[:, None] & 1).bool().view(-1)
+    nan = out.isnan().cpu()
+    assert nan[sees].all() and not nan[~sees].any()
+
+
 @pytest.mark.parametrize("f8,d,hq,hkv,toks", [(False, 128, 8, 2, 1), (True, 128, 8, 1, 4), (False, 64, 16, 2, 8),
                                                (False, 128, 16, 2, 33), (True, 256, 4, 1, 16)])
 def test_long_contexts_split_over_the_gpu(f8, d, hq, hkv, toks):

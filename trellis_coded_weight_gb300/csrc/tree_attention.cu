@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     int it = 0, issued = 0;
     bool dead = false;
     while (walk.next(p, seqs, g)) {
-      const int32_t* row = p.table + (int64_t)g.b * p.width;
+      TreePages<kTile> pages(p, g, lane);
       const int len = g.seq.prefix + g.seq.count;
       const int box = p.page_shift < 6 ? 1 << p.page_shift : kTile;  // rows of one copy
       for (int t = 0; t < g.tiles; ++t, ++it) {
@@ -165,9 +165,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         // lane i fetches box i of the tile; boxes past the sequence's end are not copied
         const int pos = pos0 + lane * box;
         const bool mine = lane * box < kTile && pos < len;
-        int y = 0;
+        int y = 0, page = pages.at(t);
         if (mine) {
-          int page = __ldg(row + (pos >> p.page_shift));
           page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
           y = (((page * 2) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         }

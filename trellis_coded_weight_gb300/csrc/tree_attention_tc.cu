@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] a wait gave up, [2] segment with odd values
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&map);
     for (int i = 0; i < C::Slots; ++i) {
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
   const int ctas = tree_ctas_used<true>(total, (int)gridDim.x);
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool dead = false;
     const int box = min(1 << p.page_shift, kTile);  // rows of one copy
     while (!dead && walk.next(p, seqs, g)) {
-      const int32_t* row = p.table + (int64_t)g.b * p.width;
+      TreePages<kTile> pages(p, g, lane);
       const int len = g.seq.prefix + g.seq.count;
       const Order order{g.tiles, rows_of(g) <= 128};
       for (int e = 0; e < 2 * g.tiles; ++e) {
@@ -126,9 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (t0 + t) % C::Pairs * 2 + (value ? 1 : 0), use = (t0 + t) / C::Pairs;
         const int pos = (g.tile0 + t) * kTile + lane * box;  // lane i copies box i of the tile, none past the end
         const bool mine = lane * box < kTile && pos < len;
-        int y = 0;
+        int y = 0, page = pages.at(t);
         if (mine) {
-          int page = __ldg(row + (pos >> p.page_shift));
           page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
           y = (((page * 2 + (value ? 1 : 0)) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
         }
@@ -156,99 +155,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = max(0, copied[kv] - C::Pairs); t < copied[kv]; ++t)
         tc::mbar_wait(full + t % C::Pairs * 2 + kv, (uint32_t)(t / C::Pairs & 1), kDrainNs);
   } else if (warp == kMmaWarp) {
-    // ---- the thread that issues the products.  One thread for both streams: with one each, products of 256 rows measured
+    // ---- the warp that issues the products.  One for both streams: with one each, products of 256 rows measured
     // 153 us against 135 (1 x 64 drafts, 131072 keys).  The tensor cores queue only a few products ahead, so waits sit behind
     // products that are still queued where they can.
-    if (lane == 0) {
-      bool dead = false, issued = false;
-      int t0 = 0, seg = 0;
-      uint32_t ns[2] = {0, 0};
-      const auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !tc::mbar_wait_short(bar, parity, p.wait_ns)) {
-          dead = true;
-          flags[0] = 1;
-        }
-        return !dead;
-      };
-      const uint32_t id_s = tc::idesc_bf16_f32(128, kTile), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
-      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
-                     v_desc = desc_mnmajor(tc::smem_u32(ring), kTile * 128);
-      // tile i's slot for keys (0) or values (1), and the wait for it
-      const auto slot_of = [&](int i, uint32_t kv) { return (uint32_t)(t0 + i) % C::Pairs * 2 + kv; };
-      const auto take = [&](int i, uint32_t kv) { return wait(full + slot_of(i, kv), (uint32_t)(t0 + i) / C::Pairs & 1u); };
-      const auto scores = [&](int s, int qtile, int i) {
-        const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4)), b = k_desc + slot_of(i, 0) * (C::Slot >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t step = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + C::S(s), a + step, b + step, id_s, k > 0);
-        }
-        tc::mma_commit(s_full + s);
-        issued = true;
-      };
-      const auto outputs = [&](int s, int i, bool fresh) {
-        const uint64_t b = v_desc + slot_of(i, 1) * (C::Slot >> 4);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
-      };
-      const auto weights = [&](int s) {  // waits for the stream's
-        if (!wait(p_ready + s, ns[s] & 1u)) return false;
-        ++ns[s];
-        tc::fence_after_sync();
-        return true;
-      };
-      while (!dead && walk.next(p, seqs, g)) {
-        const int n = g.tiles;
-        if (!wait(q_ready, (uint32_t)(seg & 1))) break;
-        tc::fence_after_sync();
-        if (rows_of(g) <= 128) {
-          for (int i = 0; i < 2 && i < n; ++i)
-            if (take(i, 0)) scores(i, 0, i);
-          for (int i = 0; i < n; ++i) {
-            const int s = i & 1;
-            if (!take(i, 1) || !weights(s)) break;
-            outputs(s, i, i < 2);
-            tc::mma_commit(empty + slot_of(i, 1));  // its tile alone: free at once, for both counts
-            tc::mma_commit(empty + slot_of(i, 1));
-            if (i + 2 >= n) tc::mma_commit(o_full + s);
-            else if (take(i + 2, 0)) scores(s, 0, i + 2);
-          }
-        } else {
-          if (!take(0, 0)) break;
-          scores(0, 0, 0);
-          scores(1, 1, 0);
-          if (!take(0, 1)) break;
-          for (int i = 0; i < n; ++i) {
-            const bool more = i + 1 < n;
-            if (!weights(0)) break;
-            outputs(0, i, i == 0);
-            if (more) {
-              if (!take(i + 1, 0)) break;
-              scores(0, 0, i + 1);
-            } else {
-              tc::mma_commit(o_full);
-            }
-            if (!weights(1)) break;
-            outputs(1, i, i == 0);
-            if (more) {
-              scores(1, 1, i + 1);
-              if (!take(i + 1, 1)) break;
-            } else {
-              tc::mma_commit(o_full + 1);
-            }
-          }
-        }
-        t0 += n;
-        ++seg;
+    bool dead = false, issued = false;
+    int t0 = 0, seg = 0;
+    uint32_t ns[2] = {0, 0};
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
+      if (__any_sync(0xFFFFFFFFu, !ok)) {
+        dead = true;
+        flags[0] = 1;
       }
-      // tensor memory is given back once every product issued has completed, also where a wait gave up
-      if (issued) {
-        tc::mma_commit(drained);
-        tc::mbar_wait(drained, 0, kDrainNs);
+      return !dead;
+    };
+    const uint32_t id_s = tc::idesc_bf16_f32(128, kTile), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
+    const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
+                   v_desc = desc_mnmajor(tc::smem_u32(ring), kTile * 128);
+    // tile i's slot for keys (0) or values (1), and the wait for it
+    const auto slot_of = [&](int i, uint32_t kv) { return (uint32_t)(t0 + i) % C::Pairs * 2 + kv; };
+    const auto take = [&](int i, uint32_t kv) { return wait(full + slot_of(i, kv), (uint32_t)(t0 + i) / C::Pairs & 1u); };
+    const auto scores = [&](int s, int qtile, int i) {
+      const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4)), b = k_desc + slot_of(i, 0) * (C::Slot >> 4);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t step = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+        mma_ss(tmem + C::S(s), a + step, b + step, id_s, k > 0);
       }
+      mma_done(s_full + s);
+      issued = true;
+    };
+    const auto outputs = [&](int s, int i, bool fresh) {
+      const uint64_t b = v_desc + slot_of(i, 1) * (C::Slot >> 4);
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(tmem + C::O(s), tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, !(fresh && k == 0));
+    };
+    const auto weights = [&](int s) {  // waits for the stream's
+      if (!wait(p_ready + s, ns[s] & 1u)) return false;
+      ++ns[s];
+      tc::fence_after_sync();
+      return true;
+    };
+    while (!dead && __any_sync(0xFFFFFFFFu, walk.next(p, seqs, g))) {
+      const int n = uniform(g.tiles);
+      if (!wait(q_ready, (uint32_t)(seg & 1))) break;
+      tc::fence_after_sync();
+      if (uniform(rows_of(g)) <= 128) {
+        for (int i = 0; i < 2 && i < n; ++i)
+          if (take(i, 0)) scores(i, 0, i);
+        for (int i = 0; i < n; ++i) {
+          const int s = i & 1;
+          if (!take(i, 1) || !weights(s)) break;
+          outputs(s, i, i < 2);
+          mma_done(empty + slot_of(i, 1));  // its tile alone: free at once, for both counts
+          mma_done(empty + slot_of(i, 1));
+          if (i + 2 >= n) mma_done(o_full + s);
+          else if (take(i + 2, 0)) scores(s, 0, i + 2);
+        }
+      } else {
+        if (!take(0, 0)) break;
+        scores(0, 0, 0);
+        scores(1, 1, 0);
+        if (!take(0, 1)) break;
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n;
+          if (!weights(0)) break;
+          outputs(0, i, i == 0);
+          if (more) {
+            if (!take(i + 1, 0)) break;
+            scores(0, 0, i + 1);
+          } else {
+            mma_done(o_full);
+          }
+          if (!weights(1)) break;
+          outputs(1, i, i == 0);
+          if (more) {
+            scores(1, 1, i + 1);
+            if (!take(i + 1, 1)) break;
+          } else {
+            mma_done(o_full + 1);
+          }
+        }
+      }
+      t0 += n;
+      ++seg;
     }
-    __syncwarp();
+    // tensor memory is given back once every product issued has completed, also where a wait gave up
+    if (issued) {
+      mma_done(drained);
+      tc::mbar_wait(drained, 0, kDrainNs);
+    }
   }
   } else {
     // ---- softmax: stream s, one thread per row; warp w of a group reaches tensor memory lanes 32 w ..

@@ -1,7 +1,8 @@
 // tree_attention_tc1.cu -- tree attention with the 5th-generation tensor cores for e4m3 caches (any head dim) and heads of
 // 256, where tree_attention_tc.cu's two accumulators do not fit.
 //
-// As there, S = Q K^T and O += P V are tcgen05 MMAs of one issuing thread, P lies in tensor memory over its scores, and two
+// As there, S = Q K^T and O += P V are tcgen05 MMAs of one issuing thread, P lies in tensor memory over its scores (here Q
+// does too, which spares shared memory a read of it per step), and two
 // softmax warpgroups alternate between the tiles, a thread per row.  Here a block has 128 rows and one accumulator O, so the
 // maximum in use is one per row: the warp that has tile i hands its rows' maxima to the warp that has tile i + 1 (an mbarrier
 // per warp), before it makes its weights; the groups' sums of weights stay apart until the end.
@@ -33,6 +34,7 @@ __device__ int g_tree_tc1_error = 0;  // set when a bounded wait gives up (trell
 constexpr int kRows = 128;  // rows of a block
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
 constexpr int kConvertThreads = 192;
+constexpr int kOdd = 8;     // segments whose odd values are known at a time
 
 __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   uint32_t r;
@@ -53,27 +55,21 @@ struct Cfg {
   static constexpr int KSlot = Tile * KBytes;
   static constexpr int VSlot = Tile * D * 2;                // a tile's values, 16 bits
   static constexpr int RSlot = F8 ? Tile * D : 0;           // as the cache has them
-  static constexpr int QBytes = kRows * D * 2;              // bf16, or two e4m3 halves
   static constexpr int Threads = F8 ? 512 : 384;
-  static constexpr int KSlots = F8 ? (D == 256 ? 2 : 4) : 2, VSlots = 2, RSlots = F8 ? 3 : 0;
-  static constexpr int Fixed = QBytes + kRows * 8 + kRows * 4 * 4 + (int)sizeof(TreeMap) + 1024;
+  static constexpr int KSlots = 3, VSlots = 3, RSlots = F8 ? 3 : 0;
+  static constexpr int Stage = 32 * D * 2;                  // 32 rows of queries: bf16, or two e4m3 numbers
+  static_assert(VSlots + 1 < kOdd, "the converting warps are at most the values' slots and a tile ahead");
+  static constexpr int Fixed = Stage + 32 * 4 + kRows * 4 * 3 + (int)sizeof(TreeMap) + 1024;
   static constexpr int Smem = 1024 + KSlots * KSlot + VSlots * VSlot + RSlots * RSlot + Fixed;
   static_assert(Smem <= 227 * 1024, "fits");
-  static constexpr int S(int s) { return s * 128; }         // tensor memory columns
+  // tensor memory columns: scores, outputs, queries
+  static constexpr int S(int s) { return s * Tile; }
   static constexpr int O = 256;
+  static constexpr int Q = D == 256 ? 128 : 384;
   static constexpr float Lift = F8 ? 7.f : 0.f;             // fp16 weights reach 2^15: 2^kMove times this
   static constexpr uint32_t KSwizzle = KBlock == 128 ? 2 : 4;  // descriptor: 128-byte or 64-byte
 };
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, e4m3 inputs, fp32 accumulate.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
@@ -90,10 +86,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   uint8_t* keys = base;
   uint8_t* values = keys + C::KSlots * C::KSlot;
   uint8_t* raws = values + C::VSlots * C::VSlot;
-  uint8_t* sq = raws + C::RSlots * C::RSlot;
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(sq + C::QBytes);
-  float* row_fac = reinterpret_cast<float*>(row_mask + kRows);
-  float* row_max = row_fac + kRows;       // in use
+  uint8_t* stage = raws + C::RSlots * C::RSlot;
+  float* row_fac = reinterpret_cast<float*>(stage + C::Stage);
+  float* row_max = row_fac + 32;          // in use
   float* row_sum = row_max + kRows;       // [2][rows]
   TreeMap& seqs = *reinterpret_cast<TreeMap*>(row_sum + 2 * kRows);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(&seqs + 1);
@@ -109,10 +104,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   uint64_t* o_full = o_done + 1;    // the segment's last one
   uint64_t* drained = o_full + 1;
   uint64_t* turn = drained + 1;     // [2][4] a warp's row maxima of its tile
-  volatile int* flags = reinterpret_cast<volatile int*>(turn + 8);  // [0] a wait gave up, [2] segment with odd values
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4);
+  volatile int* flags = reinterpret_cast<volatile int*>(turn + 8);  // [0] a wait gave up
+  volatile int* odd_of = flags + 4;  // [segment % kOdd] the segment, if it has odd values
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4 + kOdd);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::prefetch_tmap(&map);
     for (int i = 0; i < 4; ++i) {
@@ -133,7 +129,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     tc::mbar_init(drained, 1);
     for (int i = 0; i < 8; ++i) tc::mbar_init(turn + i, 1);
     flags[0] = 0;
-    flags[2] = -1;
+    for (int i = 0; i < kOdd; ++i) odd_of[i] = -1;
     tc::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -145,7 +141,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
   const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
@@ -159,7 +155,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       bool dead = false;
       const int box = min(1 << p.page_shift, kTile);  // rows of one copy
       while (!dead && walk.next(p, seqs, g)) {
-        const int32_t* row = p.table + (int64_t)g.b * p.width;
+        TreePages<kTile> pages(p, g, lane);
         const int len = g.seq.prefix + g.seq.count;
         const Order order{g.tiles, true};
         for (int e = 0; e < 2 * g.tiles; ++e) {
@@ -169,9 +165,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           uint64_t* const bar = (!value ? k_full : F8 ? r_full : v_full) + s;
           const int pos = (g.tile0 + t) * kTile + lane * box;  // lane i copies box i of the tile, none past the end
           const bool mine = lane * box < kTile && pos < len;
-          int y = 0;
+          int y = 0, page = pages.at(t);
           if (mine) {
-            int page = __ldg(row + (pos >> p.page_shift));
             page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
             y = (((page * 2 + (value ? 1 : 0)) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
           }
@@ -203,77 +198,74 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           tc::mbar_wait((kv == 0 ? k_full : F8 ? r_full : v_full) + t % slots, (uint32_t)(t / slots & 1), kDrainNs);
       }
     } else if (warp == kMmaWarp) {
-      // ---- the thread that issues the products
-      if (lane == 0) {
-        bool dead = false, issued = false;
-        int seg = 0;
-        uint32_t ks = 0, kuse = 0, vs = 0, vuse = 0, ns[2] = {0, 0};  // next slots
-        const auto wait = [&](uint64_t* bar, uint32_t parity) {
-          if (!dead && !tc::mbar_wait_short(bar, parity, p.wait_ns)) {
-            dead = true;
-            flags[0] = 1;
-          }
-          return !dead;
-        };
-        // type fields: bf16 1, fp16 0 of kind::f16; e4m3 0 of kind::f8f6f4
-        constexpr uint32_t kType = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;
-        const uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kType, id_o = (tc::idesc_bf16_f32(128, D) & kType) | kBMnMajor;
-        const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 8 * C::KBlock, C::KSwizzle),
-                       k_desc = tc::desc_kmajor(tc::smem_u32(keys), 8 * C::KBlock, C::KSwizzle),
-                       v_desc = desc_mnmajor(tc::smem_u32(values), kTile * 128);
-        const auto scores = [&](int s) {
-          if (!wait(k_full + ks, kuse & 1u)) return;
-          const uint64_t b = k_desc + ks * (C::KSlot >> 4);
+      // ---- the warp that issues the products
+      bool dead = false, issued = false;
+      int seg = 0;
+      uint32_t ks = 0, kuse = 0, vs = 0, vuse = 0, ns[2] = {0, 0};  // next slots
+      const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
+        if (__any_sync(0xFFFFFFFFu, !ok)) {
+          dead = true;
+          flags[0] = 1;
+        }
+        return !dead;
+      };
+      // type fields: bf16 1, fp16 0 of kind::f16; e4m3 0 of kind::f8f6f4
+      constexpr uint32_t kType = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;
+      const uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kType, id_o = (tc::idesc_bf16_f32(128, D) & kType) | kBMnMajor;
+      const uint64_t k_desc = tc::desc_kmajor(tc::smem_u32(keys), 8 * C::KBlock, C::KSwizzle),
+                     v_desc = desc_mnmajor(tc::smem_u32(values), kTile * 128);
+      const auto scores = [&](int s) {
+        if (!wait(k_full + ks, kuse & 1u)) return;
+        const uint64_t b = k_desc + ks * (C::KSlot >> 4);
 #pragma unroll
-          for (int h = 0; h < (F8 ? 2 : 1); ++h)
+        for (int h = 0; h < (F8 ? 2 : 1); ++h)
 #pragma unroll
-            for (int k = 0; k < C::KBytes / 32; ++k) {
-              constexpr int kPer = C::KBlock / 32;
-              const uint64_t qa = q_desc + (uint32_t)((h * (kRows * D) + k / kPer * (kRows * C::KBlock) + k % kPer * 32) >> 4);
-              const uint64_t ka = b + (uint32_t)((k / kPer * (kTile * C::KBlock) + k % kPer * 32) >> 4);
-              if constexpr (F8) mma_e4m3(tmem + C::S(s), qa, ka, id_s, h > 0 || k > 0);
-              else tc::mma_bf16(tmem + C::S(s), qa, ka, id_s, k > 0);
-            }
-          tc::mma_commit(s_full + s);
-          tc::mma_commit(k_empty + ks);
-          issued = true;
-          if (++ks == C::KSlots) {
-            ks = 0;
-            ++kuse;
+          for (int k = 0; k < C::KBytes / 32; ++k) {
+            constexpr int kPer = C::KBlock / 32;
+            const uint32_t qa = tmem + C::Q + h * (D / 4) + 8 * k;
+            const uint64_t ka = b + (uint32_t)((k / kPer * (kTile * C::KBlock) + k % kPer * 32) >> 4);
+            if constexpr (F8) mma_ts_e4m3(tmem + C::S(s), qa, ka, id_s, h > 0 || k > 0);
+            else mma_ts(tmem + C::S(s), qa, ka, id_s, k > 0);
           }
-        };
-        while (!dead && walk.next(p, seqs, g)) {
-          const int n = g.tiles;
-          if (!wait(q_ready, (uint32_t)(seg & 1))) break;
+        mma_done(s_full + s);
+        mma_done(k_empty + ks);
+        issued = true;
+        if (++ks == C::KSlots) {
+          ks = 0;
+          ++kuse;
+        }
+      };
+      while (!dead && __any_sync(0xFFFFFFFFu, walk.next(p, seqs, g))) {
+        const int n = uniform(g.tiles);
+        if (!wait(q_ready, (uint32_t)(seg & 1))) break;
+        tc::fence_after_sync();
+        for (int i = 0; i < 2 && i < n; ++i) scores(i);
+        for (int i = 0; i < n; ++i) {
+          const int s = i & 1;
+          if (!wait(v_full + vs, vuse & 1u) || !wait(p_ready + s, ns[s] & 1u)) break;
+          ++ns[s];
           tc::fence_after_sync();
-          for (int i = 0; i < 2 && i < n; ++i) scores(i);
-          for (int i = 0; i < n; ++i) {
-            const int s = i & 1;
-            if (!wait(v_full + vs, vuse & 1u) || !wait(p_ready + s, ns[s] & 1u)) break;
-            ++ns[s];
-            tc::fence_after_sync();
-            const uint64_t b = v_desc + vs * (C::VSlot >> 4);
+          const uint64_t b = v_desc + vs * (C::VSlot >> 4);
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(tmem + C::O, tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, i > 0 || k > 0);
-            tc::mma_commit(o_done);
-            tc::mma_commit(v_empty + vs);
-            if (++vs == C::VSlots) {
-              vs = 0;
-              ++vuse;
-            }
-            if (i + 1 == n) tc::mma_commit(o_full);
-            if (i + 2 < n) scores(s);
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tmem + C::O, tmem + C::S(s) + 8 * k, b + (uint32_t)((k * 16 * 128) >> 4), id_o, i > 0 || k > 0);
+          mma_done(o_done);
+          mma_done(v_empty + vs);
+          if (++vs == C::VSlots) {
+            vs = 0;
+            ++vuse;
           }
-          ++seg;
+          if (i + 1 == n) mma_done(o_full);
+          if (i + 2 < n) scores(s);
         }
-        // tensor memory is given back once every product issued has completed, also where a wait gave up
-        if (issued) {
-          tc::mma_commit(drained);
-          tc::mbar_wait(drained, 0, kDrainNs);
-        }
+        ++seg;
       }
-      __syncwarp();
+      // tensor memory is given back once every product issued has completed, also where a wait gave up
+      if (issued) {
+        mma_done(drained);
+        tc::mbar_wait(drained, 0, kDrainNs);
+      }
     } else if (F8 && warp >= kConvertWarp) {
       // ---- values, e4m3 to fp16, tile by tile
       const int tid = threadIdx.x - kConvertWarp * 32;
@@ -293,58 +285,60 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           constexpr int kR = F8 ? C::RSlots : 1;
           const int rs = tile % kR, vs = tile % C::VSlots;
           if (!wait(r_full + rs, (uint32_t)(tile / kR & 1))) break;
-          if (tile >= C::VSlots && !wait(v_empty + vs, (uint32_t)(tile / C::VSlots & 1) ^ 1u)) break;
           const uint8_t* from = raws + rs * C::RSlot;
           uint8_t* to = values + vs * C::VSlot;
           const int pos0 = (g.tile0 + t) * kTile;
           const bool tail = pos0 + kTile > g.seq.prefix;
           constexpr int CPR = D / 16, kChunks = kTile * CPR;  // 16-byte chunks of a row, of the tile
           constexpr int kBlockChunks = C::KBlock / 16;        // of a swizzled row
+          constexpr int kMine = (kChunks + kConvertThreads - 1) / kConvertThreads;
+          uint4 u[kMine];
 #pragma unroll
-          for (int i0 = 0; i0 < kChunks; i0 += 2 * kConvertThreads) {
-            uint4 u[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int idx = i0 + k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
-              if (idx >= kChunks) break;
-              const int sw = C::KBlock == 128 ? row & 7 : row >> 1 & 3;
+          for (int k = 0; k < kMine; ++k) {
+            const int idx = k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
+            const int sw = C::KBlock == 128 ? row & 7 : row >> 1 & 3;
+            u[k] = make_uint4(0, 0, 0, 0);
+            if (idx < kChunks)
               u[k] = *reinterpret_cast<const uint4*>(from + c / kBlockChunks * (kTile * C::KBlock) + row * C::KBlock + ((c % kBlockChunks) ^ sw) * 16);
-              if (tail) {
-                // rows past the end, and numbers of drafts that are none (the only ones e4m3 has), become zeros
-                if (pos0 + row >= len) u[k] = make_uint4(0, 0, 0, 0);
-                else if (pos0 + row >= g.seq.prefix) {
-                  uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, odd = 0;
+          }
+          if (tail) {
+            // rows past the end, and numbers of drafts that are none (the only ones e4m3 has), become zeros
 #pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const uint32_t nan = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of such bytes
-                    odd |= nan;
-                    w[j] &= ~((nan >> 7) * 0xFFu);
-                  }
-                  u[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                  if (odd) flags[2] = seg;
+            for (int k = 0; k < kMine; ++k) {
+              const int row = (k * kConvertThreads + tid) / CPR;
+              if (pos0 + row >= len) u[k] = make_uint4(0, 0, 0, 0);
+              else if (pos0 + row >= g.seq.prefix) {
+                uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, odd = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t nan = ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of such bytes
+                  odd |= nan;
+                  w[j] &= ~((nan >> 7) * 0xFFu);
                 }
+                u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (odd) odd_of[seg % kOdd] = seg;
               }
             }
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(r_empty + rs);
+          if (tile >= C::VSlots && !wait(v_empty + vs, (uint32_t)(tile / C::VSlots & 1) ^ 1u)) break;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int idx = i0 + k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
-              if (idx >= kChunks) break;
-              uint4 h[2];
-              h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
-              h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
-              // eight lanes write eight different places of the banks: half of them their second chunk first
-              const int flip = c >> 2 & 1;
-              uint8_t* at = to + (c >> 2) * (kTile * 128) + row * 128;
-              *reinterpret_cast<uint4*>(at + (((2 * c + flip) & 7) ^ (row & 7)) * 16) = flip ? h[1] : h[0];
-              *reinterpret_cast<uint4*>(at + (((2 * c + (flip ^ 1)) & 7) ^ (row & 7)) * 16) = flip ? h[0] : h[1];
-            }
+          for (int k = 0; k < kMine; ++k) {
+            const int idx = k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
+            if (idx >= kChunks) break;
+            uint4 h[2];
+            h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
+            h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
+            // eight lanes write eight different places of the banks: half of them their second chunk first
+            const int flip = c >> 2 & 1;
+            uint8_t* at = to + (c >> 2) * (kTile * 128) + row * 128;
+            *reinterpret_cast<uint4*>(at + (((2 * c + flip) & 7) ^ (row & 7)) * 16) = flip ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(at + (((2 * c + (flip ^ 1)) & 7) ^ (row & 7)) * 16) = flip ? h[0] : h[1];
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive(r_empty + rs);
-            tc::mbar_arrive(v_full + vs);
-          }
+          if (lane == 0) tc::mbar_arrive(v_full + vs);
         }
         ++seg;
       }
@@ -369,69 +363,88 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       const int len = g.seq.prefix + g.seq.count;
       const float k_scale = F8 && p.scales ? __ldg(p.scales + g.head) : 1.f;
       const uint32_t flip = p.scale_log2 * k_scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
-      named_sync(1, 256);  // the segment before is finished: its queries, statistics and outputs are no longer read
-      // ---- queries
+      const bool valid = r < rows, active = w4 * 32 < rows;  // warps without a row only keep the count
+      const int draft = tree_draft(p, row0 + r), qhead = g.head * p.group + row0 + r - draft * p.group;
+      // ---- queries, 32 rows at a time: loaded along the rows, staged, and put into tensor memory by the warps that own the rows,
+      // each of the two with half of what is there (bf16: half of the row; e4m3: one number of each pair)
+      float fac = 1.f;
       {
-        constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = 4;  // lanes of a row, rows at a time, loads in flight
-        const int l = threadIdx.x % LPR, qrows = (rows + 31) & ~31;  // whole warps' rows; what others hold does not matter
-        for (int r0 = threadIdx.x / LPR; r0 < qrows; r0 += kStep * kMost) {
+        constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = 32 / kStep;  // lanes of a row, rows at a time, loads of a thread
+        const int l = threadIdx.x % LPR;
+#pragma unroll 1
+        for (int rb = 0; rb < rows; rb += 32) {
           uint4 u[kMost];
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
-            const int q = r0 + k * kStep, d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
+            const int q = rb + k * kStep + threadIdx.x / LPR, d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
             u[k] = make_uint4(0, 0, 0, 0);
             if (q < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
           }
+          if (rb > 0) named_sync(1, 256);  // the rows before have been taken
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
-            const int q = r0 + k * kStep;
-            if (q >= qrows) break;  // of a warp as a whole: its lanes have one row, or rows of one 32
+            const int q = k * kStep + threadIdx.x / LPR;
             const uint4 v = make_uint4(u[k].x ^ flip, u[k].y ^ flip, u[k].z ^ flip, u[k].w ^ flip);
+            uint8_t* const to = stage + q * (D * 2);
             if constexpr (F8) {
-              const float x[8] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y),
-                                  bf16lo_to_f32(v.z), bf16hi_to_f32(v.z), bf16lo_to_f32(v.w), bf16hi_to_f32(v.w)};
-              float m = 0.f;
+              uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 #pragma unroll
-              for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-#pragma unroll
-              for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+              for (int o = LPR / 2; o; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
               // the row's largest number to [2^7, 2^8): a number is then the sum of two e4m3 ones, exactly down to 2^-9 of
               // the largest and within 2^-17 of it below
-              uint32_t e = __float_as_uint(m) >> 23;
+              uint32_t e = max(m2 & 0xFFFFu, m2 >> 16) >> 7;
               const bool none = e == 255;     // infinite or NaN: so are the row's results
               if (e < 10 || none) e = 134;    // zero, or too small to matter: as they are
               const float inv = __uint_as_float((261u - e) << 23);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+                const float a = bf16lo_to_f32(w[i]) * inv, b = bf16hi_to_f32(w[i]) * inv;
                 hi[i] = none ? 0x7F7Fu : e4m3x2(a, b);
                 const uint32_t back = e4m3x2_to_f16x2(hi[i]);
                 lo[i] = e4m3x2(a - f16_to_f32((uint16_t)back), b - f16_to_f32((uint16_t)(back >> 16)));
               }
               if (l == 0) row_fac[q] = __uint_as_float((e - 7u) << 23);
-              constexpr int kLanes = C::KBlock / 8;  // of a swizzled row
-              const int sw = C::KBlock == 128 ? q & 7 : q >> 1 & 3, ch = l % kLanes;
-              uint8_t* at = sq + l / kLanes * (kRows * C::KBlock) + q * C::KBlock + (((ch >> 1) ^ sw) << 4) + (ch & 1) * 8;
-              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-              *reinterpret_cast<uint2*>(at + kRows * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+              const int ch = l >> 1, at = (l & 1) * 8;
+              *reinterpret_cast<uint2*>(to + ((ch ^ (q & 3)) << 4) + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2*>(to + D + ((ch ^ (q & 3)) << 4) + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             } else {
-              *reinterpret_cast<uint4*>(sq + (l >> 3) * (kRows * 128) + q * 128 + (((l & 7) ^ (q & 7)) << 4)) = v;
+              *reinterpret_cast<uint4*>(to + ((l ^ (q & 7)) << 4)) = v;
             }
           }
+          named_sync(1, 256);
+          if (w4 == rb >> 5) {
+            constexpr int kChunks = D / 16 < 8 ? D / 16 : 8;  // of 16 bytes, at a time
+            const int sw = F8 ? lane & 3 : lane & 7;
+            if constexpr (F8) fac = row_fac[lane];
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 16; c0 += kChunks) {
+              uint32_t y[4 * kChunks];
+#pragma unroll
+              for (int k = 0; k < kChunks; ++k) {
+                const int ch = s * (D / 16) + ((c0 + k) ^ sw);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + lane * (D * 2) + (ch << 4));
+                y[4 * k] = v.x;
+                y[4 * k + 1] = v.y;
+                y[4 * k + 2] = v.z;
+                y[4 * k + 3] = v.w;
+              }
+              const uint32_t to = tmem + C::Q + lanes + s * (D / 4) + 4 * c0;
+              if constexpr (kChunks == 8) tmem_st_x32(to, y);
+              else tmem_st_x16(to, y);
+            }
+            tmem_st_wait();
+          }
         }
-        if (threadIdx.x < kRows) {
-          const int d = tree_draft(p, row0 + threadIdx.x);
-          row_mask[threadIdx.x] = threadIdx.x >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
-        }
-        tc::fence_proxy_async_smem();
-        named_sync(1, 256);  // masks and factors
-        if (lane == 0) tc::mbar_arrive(q_ready);
       }
-      const uint64_t seen = row_mask[r];
+      const uint64_t seen = !valid ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + draft) : draft >= 63 ? ~0ull : (2ull << draft) - 1;
+      // this thread is past the segment before, and so is all that it read of it
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(q_ready);
       // a scale of 0 too leaves minus infinity where it is
-      const float c = fmaxf(fabsf(p.scale_log2 * k_scale) * (F8 ? row_fac[r] : 1.f), 1e-37f);
-      const bool active = w4 * 32 < rows;     // warps without a row only keep the count
+      const float c = fmaxf(fabsf(p.scale_log2 * k_scale) * fac, 1e-37f);
       float used = -INFINITY, l = 0.f;        // the maximum that l is relative to
       for (int i = s; i < n; i += 2) {
         wait(s_full + s, ns++);
@@ -559,7 +572,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
               };
               clean(v.x); clean(v.y); clean(v.z); clean(v.w);
               if (odd) {
-                flags[2] = seg;
+                odd_of[seg % kOdd] = seg;
                 *at = v;
               }
             }
@@ -582,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       row_sum[s * kRows + r] = mine;
       named_sync(1, 256);
       l = mine + row_sum[(1 - s) * kRows + r];
-      const bool odd = flags[2] == seg, valid = r < rows;
+      const bool odd = odd_of[seg % kOdd] == seg;
       const int col0 = s * (D / 2), cols = D / 2;  // each group finishes half of the columns
       const auto fetch = [&](int col, float (&v)[32]) {
         uint32_t x[32];
@@ -609,35 +622,24 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
       };
       if (g.whole) {
-        // finished here: rows go through the queries' place (no longer read) so that a row's numbers are stored together
+        // finished here
         const float f = l == 0.f ? 0.f : (F8 && p.scales ? __ldg(p.scales + p.hkv + g.head) : 1.f) / l;
+        uint16_t* const to = p.out + (int64_t)(g.seq.start + draft) * p.out_stride + (int64_t)qhead * D;
         if (active) {
-          uint8_t* stage = sq + r * (D * 2);
 #pragma unroll 1
           for (int col = col0; col < col0 + cols; col += 32) {
             float v[32];
             fetch(col, v);
+            if (valid)
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              *reinterpret_cast<uint4*>(stage + ((((col + j) / 8) ^ (r & 7)) << 4)) =
-                  make_uint4(pack_bf16x2(v[j] * f, v[j + 1] * f), pack_bf16x2(v[j + 2] * f, v[j + 3] * f),
-                             pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
+              for (int j = 0; j < 32; j += 8)
+                *reinterpret_cast<uint4*>(to + col + j) =
+                    make_uint4(pack_bf16x2(v[j] * f, v[j + 1] * f), pack_bf16x2(v[j + 2] * f, v[j + 3] * f),
+                               pack_bf16x2(v[j + 4] * f, v[j + 5] * f), pack_bf16x2(v[j + 6] * f, v[j + 7] * f));
           }
         }
-        if (valid && s == 0 && p.lse) {
-          const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
-          p.lse[(int64_t)(g.seq.start + d) * p.hq + g.head * p.group + hh] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::Lift));
-        }
-        tc::fence_before_sync();
-        named_sync(1, 256);
-        constexpr int LPR = D / 8;
-        const int ch = threadIdx.x % LPR;
-#pragma unroll 1
-        for (int q = threadIdx.x / LPR; q < rows; q += 256 / LPR) {
-          const int d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
-          *reinterpret_cast<uint4*>(p.out + (g.seq.start + d) * p.out_stride + (int64_t)(g.head * p.group + hh) * D + 8 * ch) =
-              *reinterpret_cast<const uint4*>(sq + q * (D * 2) + ((ch ^ (q & 7)) << 4));
-        }
+        if (valid && s == 0 && p.lse)
+          p.lse[(int64_t)(g.seq.start + draft) * p.hq + qhead] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::Lift));
         ++seg;
         continue;
       }

@@ -164,6 +164,36 @@ struct TreeWalk {
   }
 };
 
+// The pages of a segment's tiles, for the warp that copies them: table entries are read 32 boxes (copies of up to a page) at a
+// time and a window ahead, since a copy that waits for its own entry costs the warp a trip to memory each time (4 sequences of
+// 64 drafts and 16384 keys, 40/8 heads of 128: 132 us so, 122 with the window).
+template <int TILE>
+struct TreePages {
+  const int32_t* row;
+  int first, len, shift, box, per, lane, window, prev, now, next;  // per: boxes of a tile
+  __device__ __forceinline__ TreePages(const TreeParams& p, const TreeSegment& g, int lane_)
+      : row(p.table + (int64_t)g.b * p.width), first(g.tile0 * TILE), len(g.seq.prefix + g.seq.count), shift(p.page_shift),
+        box(min(1 << p.page_shift, TILE)), per(TILE / box), lane(lane_), window(0) {
+    prev = now = load(0);
+    next = load(1);
+  }
+  __device__ __forceinline__ int load(int w) const {
+    const int pos = first + (32 * w + lane) * box;
+    return pos < len ? __ldg(row + (pos >> shift)) : 0;
+  }
+  // Page of this lane's box of tile t (lanes below `per`).  Tiles come in order, or up to two behind the last one.
+  __device__ __forceinline__ int at(int t) {
+    const int i = t * per, w = i >> 5;
+    if (w > window) {
+      prev = now;
+      now = next;
+      next = load(w + 1);
+      window = w;
+    }
+    return __shfl_sync(0xFFFFFFFFu, w == window ? now : prev, (i + lane) & 31);
+  }
+};
+
 // The workspace slot of a block's part: a block has at most one part that starts its item and one that does not.
 __device__ __forceinline__ int tree_slot(int cta, bool starts_item) { return 2 * cta + (starts_item ? 1 : 0); }
 // A part: unnormalised outputs [dim / 4][rows][4], maxima [rows] (log2), sums of weights [rows].

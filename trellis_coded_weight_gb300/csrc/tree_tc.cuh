@@ -21,15 +21,36 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void named_sync(int id, int count) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs (both bf16 or both fp16, as the descriptor says), fp32 accumulate.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The products are issued by a warp as a whole, one thread of which is elected in the instruction's own block: operands that are
+// the warp's then lie in uniform registers.  From a branch of one thread an MMA took no less than 50 cycles to issue, whatever
+// its size; so it takes 11 (A in tensor memory, 128 x 16 x 32 bytes), and 34 at N = 64, which is the MMA itself.
+// Converged warps only.  D[tmem] (+)= A[smem desc or tmem] * B[smem desc], fp32 accumulate.
+#define TRELLIS_TREE_MMA(NAME, KIND, A, ASM_A, REG_A)                                                                     \
+  __device__ __forceinline__ void NAME(uint32_t d, A a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {           \
+    asm volatile(                                                                                                         \
+        "{\n\t.reg .pred p, q;\n\t"                                                                                      \
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"                                                                                \
+        "setp.ne.b32 p, %4, 0;\n\t"                                                                                      \
+        "@q tcgen05.mma.cta_group::1.kind::" KIND " [%0], " ASM_A ", %2, %3, p;\n\t}"                                     \
+        ::"r"(d), REG_A(a), "l"(bdesc), "r"(idesc), "r"(accumulate)                                                       \
+        : "memory");                                                                                                      \
+  }
+TRELLIS_TREE_MMA(mma_ss, "f16", uint64_t, "%1", "l")           // 16-bit inputs, both bf16 or both fp16 as the descriptor says
+TRELLIS_TREE_MMA(mma_ts, "f16", uint32_t, "[%1]", "r")
+TRELLIS_TREE_MMA(mma_ts_e4m3, "f8f6f4", uint32_t, "[%1]", "r")  // e4m3 inputs
+#undef TRELLIS_TREE_MMA
+// The mbarrier receives one arrival once the products issued so far have completed.
+__device__ __forceinline__ void mma_done(uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
       : "memory");
 }
+// A number that is the same in all lanes, to the compiler too.
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // This warp's 32 lanes x 16 (32) consecutive columns from registers.
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
