@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
   const int cta = blockIdx.x;
   if (cta >= ctas) {  // fewer steps than blocks
-    if (threadIdx.x == 0) p.items[cta] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0) p.items[cta] = make_int4(0, 0, 0, 0);
     return;
   }
 
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     const int wk = warp;
     const int gq = lane >> 2, c4 = lane & 3;  // fragment row and column pair
     const int nthr = C::Consumers * 32;
-    int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
+    int4 shared_item = make_int4(0, 0, 0, 0);  // the item that starts here and ends in a later block
     int it = 0;
     bool dead = false;
     while (walk.next(p, seqs, g)) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
         }
       }
-      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
+      if (threadIdx.x == 0 && g.starts) shared_item = tree_item(g, row0, rows, cta, tree_cta_of(g.last_at, total, ctas));
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;
   }

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // a scale of 0 too leaves minus infinity where it is
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
     int t0 = 0, seg = 0, ns = 0, no = 0;
-    int4 shared_item = make_int4(-1, 0, 0, 0);  // the item that starts here and ends in a later block
+    int4 shared_item = make_int4(0, 0, 0, 0);  // the item that starts here and ends in a later block
     bool dead = false;
     const auto wait = [&](uint64_t* bar, int count) {
       const bool ok = dead || tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns);
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         part[(int64_t)kRows * D + kRows + r] = l;
       }
       tc::fence_before_sync();
-      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
+      if (threadIdx.x == 0 && g.starts) shared_item = tree_item(g, row0, rows, cta, tree_cta_of(g.last_at, total, ctas));
       ++seg;
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;

@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t t_s = tmem + C::S(s) + lanes, t_o = tmem + C::O + lanes;
     int t0 = 0, seg = 0, ns = 0, turns = 0;  // turns: the other group's hand-overs of this warp's rows so far
-    int4 shared_item = make_int4(-1, 0, 0, 0);
+    int4 shared_item = make_int4(0, 0, 0, 0);
     bool dead = false;
     const auto wait = [&](uint64_t* bar, int count) {
       const bool ok = dead || tc::mbar_wait_short(bar, (uint32_t)(count & 1), p.wait_ns);
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         part[(int64_t)kRows * D + kRows + r] = l;
       }
       tc::fence_before_sync();
-      if (threadIdx.x == 0 && g.starts) shared_item = make_int4(g.b, g.head, g.row_block, tree_cta_of(g.last_at, total, ctas));
+      if (threadIdx.x == 0 && g.starts) shared_item = tree_item(g, row0, rows, cta, tree_cta_of(g.last_at, total, ctas));
       ++seg;
     }
     if (threadIdx.x == 0) p.items[cta] = shared_item;

@@ -2,10 +2,11 @@
 //
 // With m_j, l_j, o_j of the parts:  m = max m_j,  l = sum 2^(m_j - m) l_j,  o = sum 2^(m_j - m) o_j;
 // out = o / l,  lse = ln2 (m + log2 l).
-// A thread has four columns of a row and goes through the parts in their order, eight at a time, with its own running
-// maximum; where an item has many parts four threads share them and join at the end.  The blocks of a shared item (one
-// per first block of an item and share of its rows) spread over the GPU.  Bound: latency of the launch and of one or
-// two rounds of loads; the parts are still in L2.
+// A thread has four columns of a row and loads eight parts at a time; where an item has more, up to eight threads share them
+// and join at the end.  Eight rows go side by side (128 contiguous bytes of a part).  Where items have
+// many rows every block counts the units of work for itself, from the table that the attention kernel has left, and takes its share.  19 parts of 256 rows by 8 heads of 128:
+// 6.5 us; a grid of a block per possible item and rows, most of which had none, took 11, and warps that each went through the
+// table by themselves 9.  Bound: latency of the launch and of two or three rounds of loads; the parts are still in L2.
 #include "common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
@@ -15,8 +16,9 @@ namespace trellis {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;       // parts whose loads are in flight
-constexpr int kManyParts = 16;  // from here on four threads share them
+constexpr int kPerSM = 3;
+constexpr int kBatch = 8;   // parts whose loads are in flight
+constexpr int kRows = 8;    // rows of a unit
 constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -36,23 +38,27 @@ __device__ __forceinline__ void scale_to(State& s, float m) {
   s.m = m;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int prows, float lift) {
+// direct: block (x, y) takes the item that attention block x was the first to share, and of its units y, y + gridDim.y, ..
+template <int D, bool Direct>
+__global__ void __launch_bounds__(kThreads, kPerSM) join_kernel(const TreeParams p, int prows, int ctas, float lift) {
   pdl_enter();
   __shared__ State sh[kThreads];
-  const int4 item = __ldcg(p.items + blockIdx.x);
-  if (item.x < 0) return;
-  const TreeSeq seq = tree_seq(p, item.x);
-  const int head = item.y, row0 = item.z * prows, first = blockIdx.x, parts = item.w - first + 1;
-  const int rows = min(prows, seq.count * p.group - row0);
+  __shared__ int sums[kThreads / 32];
+  __shared__ int4 s_item;
+  __shared__ int2 s_at;
+  constexpr int LPR = D / 4;  // fours of columns of a row
   const int64_t part_floats = tree_part_floats(prows, D);
-  constexpr int LPR = D / 4;  // threads of a row
-  const int sharers = parts >= kManyParts ? 4 : 1;
-  const int elems = kThreads / sharers, step = elems / LPR;  // rows at a time
-  const int mine = threadIdx.x / elems, e = threadIdx.x % elems, row_in = e % step, col = e / step * 4;
-  const float vs = p.scales ? __ldg(p.scales + p.hkv + head) : 1.f;
-  for (int r0 = blockIdx.y * step; r0 < rows; r0 += gridDim.y * step) {
-    const int r = r0 + row_in;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // of a unit's threads as many share a column's parts as the item says, and two at least where a row has fewer columns than
+  // there would be threads
+  const auto sharers_of = [](int w) { return D == 64 && tree_item_shared(w) == 0 ? 2 : 1 << tree_item_shared(w); };
+  const auto units_of = [&](int w) { return (tree_item_rows(w) + kRows - 1) / kRows * (LPR * kRows * sharers_of(w) / kThreads); };
+  const auto join = [&](const int4 item, int first, int at) {  // unit `at` of an item whose first part is block `first`'s
+    const int head = item.y, row0 = item.z, rows = tree_item_rows(item.w), parts = tree_item_last(item.w) - first + 1;
+    const int sharers = sharers_of(item.w), elems = kThreads / sharers, groups = LPR * kRows / elems;  // of columns
+    const int mine = tid / elems, e = tid % elems, r = at / groups * kRows + e % kRows;
+    const int col = (at % groups * (elems / kRows) + e / kRows) * 4;
+    const float vs = p.scales ? __ldg(p.scales + p.hkv + head) : 1.f;
     State s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (r < rows)
       for (int j0 = mine; j0 < parts; j0 += sharers * kBatch) {
@@ -75,24 +81,23 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int 
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) mx = fmaxf(mx, m[b]);
         if (mx > s.m) scale_to(s, mx);
-        const float base = mx == -INFINITY ? 0.f : mx;
+        const float base_m = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const float w = ex2(m[b] - base);
-          s.l += w * l[b];
-          s.o.x += w * o[b].x;
-          s.o.y += w * o[b].y;
-          s.o.z += w * o[b].z;
-          s.o.w += w * o[b].w;
+          const float a = ex2(m[b] - base_m);
+          s.l += a * l[b];
+          s.o.x += a * o[b].x;
+          s.o.y += a * o[b].y;
+          s.o.z += a * o[b].z;
+          s.o.w += a * o[b].w;
         }
       }
     if (sharers > 1) {
-      __syncthreads();
-      sh[threadIdx.x] = s;
+      sh[tid] = s;
       __syncthreads();
       if (mine == 0)
-        for (int k = 1; k < 4; ++k) {
-          State t = sh[threadIdx.x + k * elems];
+        for (int k = 1; k < sharers; ++k) {
+          State t = sh[tid + k * elems];
           const float mx = fmaxf(s.m, t.m);
           if (mx > -INFINITY) {
             scale_to(s, mx);
@@ -105,26 +110,72 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const TreeParams p, int 
     if (r < rows && mine == 0) {
       const float f = s.l == 0.f ? 0.f : vs / s.l;
       const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
-      *reinterpret_cast<uint2*>(p.out + (seq.start + d) * p.out_stride + (int64_t)(head * p.group + hh) * D + col) =
+      *reinterpret_cast<uint2*>(p.out + (item.x + d) * p.out_stride + (int64_t)(head * p.group + hh) * D + col) =
           make_uint2(pack_bf16x2(s.o.x * f, s.o.y * f), pack_bf16x2(s.o.z * f, s.o.w * f));
       if (p.lse && col == 0)
-        p.lse[(int64_t)(seq.start + d) * p.hq + head * p.group + hh] = s.l == 0.f ? -INFINITY : kLn2 * (s.m + (log2f(s.l) - lift));
+        p.lse[(int64_t)(item.x + d) * p.hq + head * p.group + hh] = s.l == 0.f ? -INFINITY : kLn2 * (s.m + (log2f(s.l) - lift));
+    }
+  };
+  if constexpr (Direct) {
+    const int4 item = __ldcg(p.items + blockIdx.x);
+    const int units = units_of(item.w);
+    for (int at = blockIdx.y; at < units; at += gridDim.y) {
+      join(item, blockIdx.x, at);
+      __syncthreads();
+    }
+    return;
+  }
+  // units: 8 rows of an item and as many columns as fit; block b has units b, b + gridDim.x, ..
+  int unit = blockIdx.x, done = 0;
+  for (int base = 0; base < ctas; base += kThreads) {
+    const int4 mine_item = base + tid < ctas ? __ldcg(p.items + base + tid) : make_int4(0, 0, 0, 0);
+    const int units = units_of(mine_item.w);
+    int upto = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    __syncthreads();
+    if (lane == 31) sums[tid >> 5] = upto;
+    __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < tid >> 5) upto += sums[w];
+      sum += sums[w];
+    }
+    upto += done;
+    done += sum;
+    for (; unit < done; unit += gridDim.x) {
+      __syncthreads();
+      if (unit < upto && unit >= upto - units) {
+        s_item = mine_item;
+        s_at = make_int2(base + tid, unit - (upto - units));
+      }
+      __syncthreads();
+      join(s_item, s_at.x, s_at.y);
     }
   }
 }
 
 }  // namespace
 
+template <int D>
+static cudaError_t launch_one(const TreeParams& p, int rows, float lift, int ctas, cudaStream_t st) {
+  const int most = p.max_tokens * p.group;
+  // Few rows are a few units per item, found without counting: 4 x 1 tokens, 1000 keys, 32/8 heads of 128: 12.2 us for the whole
+  // call, 13.5 with the count; 64 drafts, 131072 keys: 119 and 112.
+  if (rows <= 16)
+    return launch_pdl(join_kernel<D, true>, dim3((unsigned)ctas, (most + kRows - 1) / kRows * 4u), dim3(kThreads), 0, st, p, rows, ctas, lift);
+  // no more blocks than there can be units: of a head's rows an eighth and one per sequence, times shares of the columns
+  const int64_t units = (int64_t)p.hkv * (p.n * p.group / kRows + p.n) * (D / 16), fit = (int64_t)kPerSM * device_sm_count();
+  return launch_pdl(join_kernel<D, false>, dim3((unsigned)(units < fit ? units : fit)), dim3(kThreads), 0, st, p, rows, ctas, lift);
+}
+
 cudaError_t launch_tree_join(const TreeParams& p, int dim, int rows, float lift, int ctas, cudaStream_t st) {
-  const int most = p.max_tokens * p.group < rows ? p.max_tokens * p.group : rows;
-  // shares of an item's rows: as small as a block's rows with many parts, at most 32
-  const int least = kThreads / 4 / (dim / 4) < 1 ? 1 : kThreads / 4 / (dim / 4);
-  int y = (most + least - 1) / least;
-  if (y > 32) y = 32;
-  const dim3 grid((unsigned)ctas, (unsigned)y), block(kThreads);
-  if (dim == 64) return launch_pdl(join_kernel<64>, grid, block, 0, st, p, rows, lift);
-  if (dim == 128) return launch_pdl(join_kernel<128>, grid, block, 0, st, p, rows, lift);
-  return launch_pdl(join_kernel<256>, grid, block, 0, st, p, rows, lift);
+  return dim == 64 ? launch_one<64>(p, rows, lift, ctas, st) : dim == 128 ? launch_one<128>(p, rows, lift, ctas, st)
+                                                                        : launch_one<256>(p, rows, lift, ctas, st);
 }
 
 }  // namespace trellis

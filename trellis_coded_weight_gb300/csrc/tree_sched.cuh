@@ -18,7 +18,7 @@
 
 namespace trellis {
 
-constexpr int kTreeMaxCtas = 1024;   // bound on the grid (sizes the counters)
+constexpr int kTreeMaxCtas = 1024;   // bound on the grid (sizes the table of shared items)
 
 struct TreeParams {
   const uint16_t* q;
@@ -28,7 +28,7 @@ struct TreeParams {
   const uint64_t* mask;
   const float* scales;  // [2][hkv] of the layer, or null
   const uint16_t* pool; // the layer's pages (bf16 ones)
-  int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (sequence or -1, head, row block, last block)
+  int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (tree_item), or none
   float* part;          // two slots per thread block
   int64_t q_stride, out_stride;
   int64_t pages;
@@ -194,6 +194,15 @@ struct TreePages {
   }
 };
 
+// An item for the joining kernel, of parts from block `first` to `last`: its sequence's first draft, head, first row; packed,
+// the last block, rows, and (log2) how many share its parts.  Packed 0: no item.
+__device__ __forceinline__ int4 tree_item(const TreeSegment& g, int row0, int rows, int first, int last) {
+  const int parts = last - first + 1, shared = parts <= 8 ? 0 : parts <= 16 ? 1 : parts <= 32 ? 2 : 3;
+  return make_int4(g.seq.start, g.head, row0, shared << 24 | rows << 12 | last);
+}
+__device__ __forceinline__ int tree_item_last(int w) { return w & 0xFFF; }
+__device__ __forceinline__ int tree_item_rows(int w) { return w >> 12 & 0xFFF; }
+__device__ __forceinline__ int tree_item_shared(int w) { return w >> 24; }
 // The workspace slot of a block's part: a block has at most one part that starts its item and one that does not.
 __device__ __forceinline__ int tree_slot(int cta, bool starts_item) { return 2 * cta + (starts_item ? 1 : 0); }
 // A part: unnormalised outputs [dim / 4][rows][4], maxima [rows] (log2), sums of weights [rows].
