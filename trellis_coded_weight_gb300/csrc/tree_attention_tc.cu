@@ -33,6 +33,8 @@ __device__ int g_tree_tc_error = 0;  // set when a bounded wait gives up (trelli
 constexpr int kTile = 128;                    // keys per step
 constexpr int kRows = 256;                    // rows of a block
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9;
+// an item's start and end, in steps (32 x 8 drafts, ragged to 2048 keys, 32/8 heads of 128: 74 us without, 35, 38 with 12)
+constexpr int kExtra = 6;
 constexpr int kThreads = 384;  // two softmax warpgroups; one for the copying and the issuing warp, and two that idle
 
 template <int D>
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish();
   }
   pdl_enter();
-  if (warp == 0) tree_cumulate<kRows, kTile, true>(p, seqs);
+  if (warp == 0) tree_cumulate<kRows, kTile, true, kExtra>(p, seqs);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

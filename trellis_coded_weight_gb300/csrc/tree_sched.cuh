@@ -5,7 +5,7 @@
 // data, so the division is made on the device: the steps of all items, in the order of (sequence, row block, head,
 // tile), are laid end to end and cut into equal contiguous ranges, one per thread block; a step belongs to the range that
 // holds its beginning.  A step has length 1, or (HALVES) 2 where its rows fill more than half a block, since it then
-// takes that kernel twice as long.  An item that falls into one range is finished there.  Otherwise each block
+// takes that kernel twice as long; an item has some length besides, for what it costs to start and finish it.  An item that falls into one range is finished there.  Otherwise each block
 // writes its part (maximum, sum and unnormalised output of its keys, fp32) to the workspace, and a second launch
 // (tree_join.cu) joins the parts in their order over the whole GPU: results do not depend on timing, and no block has the
 // joining of a long item to itself.
@@ -68,7 +68,8 @@ __device__ __forceinline__ int tree_draft(const TreeParams& p, int r) { return (
 // the first kCached sequences themselves.
 struct TreeMap {
   static constexpr int kCached = 256;
-  int cum[kTreeMaxBatch + 4];
+  int cum[kTreeMaxBatch + 4], items[kTreeMaxBatch + 4];  // items: their number
+  int extra;  // length of an item besides its steps
   int4 seq[kCached];  // start, count, prefix
 };
 __device__ __forceinline__ TreeSeq tree_seq_of(const TreeParams& p, const TreeMap& map, int b) {
@@ -77,29 +78,44 @@ __device__ __forceinline__ TreeSeq tree_seq_of(const TreeParams& p, const TreeMa
   return TreeSeq{v.x, v.y, v.z};
 }
 
-// Fills the map, by one warp.
-template <int ROWS, int TILE, bool HALVES>
+// Fills the map, by one warp.  An item has EXTRA steps before its own (no more than a block's share of the steps): what it costs
+// to start and finish one is then counted, and a block with many short items has fewer steps.
+template <int ROWS, int TILE, bool HALVES, int EXTRA>
 __device__ __forceinline__ void tree_cumulate(const TreeParams& p, TreeMap& map) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
+  int before = 0, items = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    int v = 0;
+    int v = 0, n = 0;
     if (b < p.batch) {
       const TreeSeq s = tree_seq(p, b);
       if (b < TreeMap::kCached) map.seq[b] = make_int4(s.start, s.count, s.prefix, 0);
       constexpr int kUnit = HALVES ? ROWS / 2 : ROWS;
       v = tree_tiles<TILE>(s) * ((s.count * p.group + kUnit - 1) / kUnit) * p.hkv;
+      n = (s.count * p.group + ROWS - 1) / ROWS * p.hkv;
     }
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v += u;
+      const int u = __shfl_up_sync(0xFFFFFFFFu, v, o), k = __shfl_up_sync(0xFFFFFFFFu, n, o);
+      if (lane >= o) {
+        v += u;
+        n += k;
+      }
     }
-    if (b < p.batch) map.cum[b + 1] = before + v;
+    if (b < p.batch) {
+      map.cum[b + 1] = before + v;
+      map.items[b + 1] = items + n;
+    }
     before += __shfl_sync(0xFFFFFFFFu, v, 31);
+    items += __shfl_sync(0xFFFFFFFFu, n, 31);
   }
-  if (lane == 0) map.cum[0] = 0;
+  const int extra = min(EXTRA, before / (int)gridDim.x);
+  __syncwarp();
+  for (int b = lane; b < p.batch; b += 32) map.cum[b + 1] += extra * map.items[b + 1];
+  if (lane == 0) {
+    map.cum[0] = 0;
+    map.extra = extra;
+  }
 }
 
 // The blocks' ranges: block c of `ctas` takes [c * total / ctas, (c + 1) * total / ctas); the block that holds `at`:
@@ -116,7 +132,7 @@ struct TreeSegment {
   TreeSeq seq;
   int b, head, row_block;
   int tile0, tiles;   // first tile, number of tiles
-  bool starts, whole; // the item's first step is in this range; all of them are
+  bool starts, whole; // the item's first tile is in this range; all of them are
   int last_at;        // where its last step begins
 };
 
@@ -145,17 +161,19 @@ struct TreeWalk {
       }
       g.b = b;
       g.seq = tree_seq_of(p, map, b);
-      const int nt = tree_tiles<TILE>(g.seq), r = at - map.cum[b], block = (HALVES ? 2 : 1) * nt * p.hkv;
+      const int nt = tree_tiles<TILE>(g.seq), extra = map.extra, r = at - map.cum[b];
+      const int block = ((HALVES ? 2 : 1) * nt + extra) * p.hkv;
       g.row_block = r / block;
       const int w = HALVES && g.seq.count * p.group - g.row_block * ROWS > ROWS / 2 ? 2 : 1;
       const int q = r - g.row_block * block;
-      g.head = q / (nt * w);
-      const int off = q - g.head * nt * w;             // into the item
-      const int stop = off + (end - at) < nt * w ? off + (end - at) : nt * w;
-      g.tile0 = (off + w - 1) / w;
-      g.tiles = (stop + w - 1) / w - g.tile0;
-      g.last_at = at - off + (nt - 1) * w;
-      g.starts = at - off >= begin;
+      const int length = extra + nt * w;
+      g.head = q / length;
+      const int off = q - g.head * length;             // into the item
+      const int stop = off + (end - at) < length ? off + (end - at) : length;
+      g.tile0 = (max(off - extra, 0) + w - 1) / w;
+      g.tiles = (max(stop - extra, 0) + w - 1) / w - g.tile0;
+      g.last_at = at - off + extra + (nt - 1) * w;
+      g.starts = g.tile0 == 0;
       g.whole = g.starts && g.last_at < end;
       at += stop - off;
       if (g.tiles > 0) return true;
