@@ -33,7 +33,7 @@ __device__ int g_tree_tc1_error = 0;  // set when a bounded wait gives up (trell
 
 constexpr int kRows = 128;  // rows of a block
 constexpr int kSoftmaxWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvertWarp = 10;
-constexpr int kConvertThreads = 192;
+constexpr int kConvertThreads = 128;  // rows of a tile are 8, 16 or 32 apart in a thread's chunks: what it swizzles by stays the same
 // an item's start and end, in steps (32 x 4 drafts, ragged to 8200 e4m3 keys, 16/2 heads of 256: 54 us without, 42)
 constexpr int kExtra = 7;
 constexpr int kOdd = 8;     // segments whose odd values are known at a time
@@ -57,7 +57,7 @@ struct Cfg {
   static constexpr int KSlot = Tile * KBytes;
   static constexpr int VSlot = Tile * D * 2;                // a tile's values, 16 bits
   static constexpr int RSlot = F8 ? Tile * D : 0;           // as the cache has them
-  static constexpr int Threads = F8 ? 512 : 384;
+  static constexpr int Threads = F8 ? 448 : 384;
   static constexpr int KSlots = 3, VSlots = 3, RSlots = F8 ? 3 : 0;
   static constexpr int Stage = 32 * D * 2;                  // 32 rows of queries: bf16, or two e4m3 numbers
   static_assert(VSlots + 1 < kOdd, "the converting warps are at most the values' slots and a tile ahead");
@@ -270,7 +270,13 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       }
     } else if (F8 && warp >= kConvertWarp) {
       // ---- values, e4m3 to fp16, tile by tile
-      const int tid = threadIdx.x - kConvertWarp * 32;
+      const int tid = threadIdx.x - kConvertWarp * 32, row0 = tid / (D / 16), ch = tid % (D / 16);
+      constexpr int kBlockChunks = C::KBlock / 16;  // of a swizzled row
+      const int from_at = ch / kBlockChunks * (kTile * C::KBlock) + row0 * C::KBlock +
+                          ((ch % kBlockChunks) ^ (C::KBlock == 128 ? row0 & 7 : row0 >> 1 & 3)) * 16;
+      // a chunk becomes two; eight lanes write eight different places of the banks: half of them their second one first
+      const int flip = ch >> 2 & 1, to_at = (ch >> 2) * (kTile * 128) + row0 * 128;
+      const int to_first = to_at + (((2 * ch + flip) & 7) ^ (row0 & 7)) * 16, to_second = to_at + (((2 * ch + (flip ^ 1)) & 7) ^ (row0 & 7)) * 16;
       int tile = 0, seg = 0;
       bool dead = false;
       const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -287,27 +293,21 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           constexpr int kR = F8 ? C::RSlots : 1;
           const int rs = tile % kR, vs = tile % C::VSlots;
           if (!wait(r_full + rs, (uint32_t)(tile / kR & 1))) break;
-          const uint8_t* from = raws + rs * C::RSlot;
+          const uint8_t* from = raws + rs * C::RSlot + from_at;
           uint8_t* to = values + vs * C::VSlot;
           const int pos0 = (g.tile0 + t) * kTile;
           const bool tail = pos0 + kTile > g.seq.prefix;
-          constexpr int CPR = D / 16, kChunks = kTile * CPR;  // 16-byte chunks of a row, of the tile
-          constexpr int kBlockChunks = C::KBlock / 16;        // of a swizzled row
-          constexpr int kMine = (kChunks + kConvertThreads - 1) / kConvertThreads;
+          constexpr int CPR = D / 16, kMine = kTile * CPR / kConvertThreads;  // 16-byte chunks of a row, of this thread
+          constexpr int kRowsApart = kConvertThreads / CPR;
+          static_assert(kRowsApart % 8 == 0 && kTile % kRowsApart == 0, "a thread's chunks");
           uint4 u[kMine];
 #pragma unroll
-          for (int k = 0; k < kMine; ++k) {
-            const int idx = k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
-            const int sw = C::KBlock == 128 ? row & 7 : row >> 1 & 3;
-            u[k] = make_uint4(0, 0, 0, 0);
-            if (idx < kChunks)
-              u[k] = *reinterpret_cast<const uint4*>(from + c / kBlockChunks * (kTile * C::KBlock) + row * C::KBlock + ((c % kBlockChunks) ^ sw) * 16);
-          }
+          for (int k = 0; k < kMine; ++k) u[k] = *reinterpret_cast<const uint4*>(from + k * (kRowsApart * C::KBlock));
           if (tail) {
             // rows past the end, and numbers of drafts that are none (the only ones e4m3 has), become zeros
 #pragma unroll
             for (int k = 0; k < kMine; ++k) {
-              const int row = (k * kConvertThreads + tid) / CPR;
+              const int row = row0 + k * kRowsApart;
               if (pos0 + row >= len) u[k] = make_uint4(0, 0, 0, 0);
               else if (pos0 + row >= g.seq.prefix) {
                 uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, odd = 0;
@@ -327,16 +327,11 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           if (tile >= C::VSlots && !wait(v_empty + vs, (uint32_t)(tile / C::VSlots & 1) ^ 1u)) break;
 #pragma unroll
           for (int k = 0; k < kMine; ++k) {
-            const int idx = k * kConvertThreads + tid, row = idx / CPR, c = idx % CPR;
-            if (idx >= kChunks) break;
-            uint4 h[2];
-            h[0] = make_uint4(e4m3x2_to_f16x2(u[k].x), e4m3x2_to_f16x2(u[k].x >> 16), e4m3x2_to_f16x2(u[k].y), e4m3x2_to_f16x2(u[k].y >> 16));
-            h[1] = make_uint4(e4m3x2_to_f16x2(u[k].z), e4m3x2_to_f16x2(u[k].z >> 16), e4m3x2_to_f16x2(u[k].w), e4m3x2_to_f16x2(u[k].w >> 16));
-            // eight lanes write eight different places of the banks: half of them their second chunk first
-            const int flip = c >> 2 & 1;
-            uint8_t* at = to + (c >> 2) * (kTile * 128) + row * 128;
-            *reinterpret_cast<uint4*>(at + (((2 * c + flip) & 7) ^ (row & 7)) * 16) = flip ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(at + (((2 * c + (flip ^ 1)) & 7) ^ (row & 7)) * 16) = flip ? h[0] : h[1];
+            const uint32_t w[4] = {flip ? u[k].z : u[k].x, flip ? u[k].w : u[k].y, flip ? u[k].x : u[k].z, flip ? u[k].y : u[k].w};
+            *reinterpret_cast<uint4*>(to + to_first + k * (kRowsApart * 128)) =
+                make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]), e4m3x2_to_f16x2(w[1] >> 16));
+            *reinterpret_cast<uint4*>(to + to_second + k * (kRowsApart * 128)) =
+                make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]), e4m3x2_to_f16x2(w[3] >> 16));
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
