@@ -29,7 +29,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerSM = 4;          // blocks of an SM at a time
-constexpr int kList = 768;         // numbers that may reach the threshold
+constexpr int kList = 1024;        // numbers that may reach a threshold; kMaxTop * kMaxTop at least (see the join)
 constexpr int kBatch = 4;          // 16-byte loads of a thread in flight
 constexpr int kMaxSplits = 64;
 constexpr int kCounters = 4096;    // rows that may be split
@@ -434,16 +434,32 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
                          __shfl_xor_sync(0xFFFFFFFFu, a.t, o)}, p.c);
       if (lane == 0) sh.part[0] = a;
     }
+    // The parts' alternatives, each list in descending order.  Of the keys at depth d the m-th largest is reached by m lists
+    // with d + 1 keys each, so with m (d + 1) >= top_k nothing below it counts.  Keys are distinct: no more than m lists reach it at
+    // depth d, and others have at most d keys above it, which is m top_k + (splits - m) d <= kList in all (d is 0 where there
+    // are as many lists as alternatives; all keys are no more than kList where there are fewer).  A part has more than
+    // kMaxTop numbers, so none of its keys is missing.
     const int total = p.splits * p.top_k;
-    for (int base = 0; base < total; base += kList - kMaxTop) {  // as many as fit beside the best so far
-      const int held = sh.count;
-      if (tid < held) sh.list[tid] = sh.best[tid];
+    if (total) {
+      const int d = (p.top_k + p.splits - 1) / p.splits - 1, m = (p.top_k + d) / (d + 1);
+      constexpr int kMine = kMaxSplits * kMaxTop / kThreads;
+      unsigned long long key[kMine];
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) key[k] = tid + k * kThreads < total ? __ldcg(p.keys + row * total + tid + k * kThreads) : 0ull;
+      if (tid < p.splits) sh.list[tid] = __ldcg(p.keys + (row * p.splits + tid) * p.top_k + d);
       __syncthreads();
-      const int n = total - base < kList - kMaxTop ? total - base : kList - kMaxTop;
-      for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = __ldcg(p.keys + row * total + base + i);
-        if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
+      if (tid < p.splits) {
+        const unsigned long long mine = sh.list[tid];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < p.splits; ++j) rank += sh.list[j] > mine;
+        if (rank == m - 1) sh.red[0] = mine;
       }
+      __syncthreads();
+      const unsigned long long from = sh.red[0];
+#pragma unroll
+      for (int k = 0; k < kMine; ++k)
+        if (key[k] >= from && key[k]) sh.list[atomicAdd(&sh.count, 1)] = key[k];
       __syncthreads();
       cut_back(sh, p.top_k);
     }
