@@ -5,15 +5,23 @@
 // computed in one pass over the keys with m, l and o carried along (o and l are scaled by 2^(m_old - m_new) when the
 // maximum moves), and joined over disjoint sets of keys by the same rule.
 //
-// The rows of one key/value head -- its group of query heads times the drafts -- share every key, so a block takes ROWS of them
-// (16, 32 or 64) and its warps split the rows by 16 and the keys of a tile between them: scores and outputs
+// Three kernels do so; all divide the work as tree_sched.cuh says and leave parts of shared items to tree_join.cu:
+//   this one                 heads of 64 and 128, up to 16 rows of a key/value head (its group of query heads times the drafts)
+//   tree_attention_tc.cu     bf16 heads of 64 and 128, more rows:   tcgen05, 256 rows a block
+//   tree_attention_tc1.cu    e4m3 of those, and heads of 256:      tcgen05, 128 rows a block
+// Measured on both sides (us, this one / the other; 32/8 heads of 128 unless said otherwise): 16 rows, 4096 keys 11.2 / 12.8, 300 keys
+// 8.1 / 14.3, ragged batch of 32 to 2000 37 / 37; 32 rows, 131072 keys 126 / 86, ragged batch to 2048 46 / 35, e4m3 45 / 37.
+// Heads of 256 (e4m3, 16/2 heads): 8 rows, 4096 keys 18.1 / 13.7, 60000 keys 33.5 / 26.4, 300 keys 9.8 / 10.8.
+//
+// Here a block takes all rows, padded to 16, and its four warps split the keys of a tile between them: scores and outputs
 // are warp-level matrix products (m16n8k16) whose accumulators, maxima and sums stay in the registers of one warp
 // until the segment ends.  Keys and values arrive as 64-key tiles by tensor copies (TMA, 128-byte swizzle, one box
-// per page) issued by a warp of its own, several tiles ahead.  An e4m3 cache stays 8 bits in shared memory and becomes fp16 in registers;
-// its queries are fp16 too, each row scaled by a power of two.  How the work is divided: tree_sched.cuh.
+// per page) issued by a warp of its own, up to eight tiles ahead.  An e4m3 cache stays 8 bits in shared memory and becomes fp16 in
+// registers; its queries are fp16 too, each row scaled by a power of two.
 //
-// Bound: HBM (the cache is read once per 64 rows; other row blocks of the head find it in L2), down to the latency of
-// a launch and a join for short contexts.
+// Bound: HBM (1 x 131072 keys, 32/8 heads of 128, one token: 86 us, 6.2 TB/s), with e4m3 the latency of the conversions in four
+// warps (71 us, 3.8 TB/s; a second group of four warps that takes every other tile: 62, but 61 us for 55 on a ragged batch of
+// 64), and for short contexts that of two launches and a segment's start and end (1 x 4096 keys, 40/8 heads: 10.6 us).
 #include <cstring>
 #include <cuda.h>
 
@@ -257,8 +265,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       }
       const uint32_t sq32 = tc::smem_u32(sq);
       constexpr int KS = D / 16;
-      constexpr bool kHold = D <= 128;  // query fragments stay in registers
-      uint32_t qa[kHold ? KS : 1][4];
+      uint32_t qa[KS][4];  // query fragments stay in registers
       const auto load_q = [&](uint32_t (&a)[4], int ks) {
         if constexpr (F8) {
           // the order of the 16 numbers of a step is the one the 8-bit keys have in registers: lane column c4 has 4 c4 .. 4 c4 + 3
@@ -275,7 +282,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           ldsm4(a, sq32 + r * (D * 2) + ((chunk ^ (r & 7)) << 4));
         }
       };
-      if constexpr (kHold)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) load_q(qa[ks], ks);
 
@@ -309,11 +315,6 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         if constexpr (F8) {
 #pragma unroll
           for (int ks = 0; ks < KS; ks += 2) {
-            uint32_t qb[2][4];
-            if constexpr (!kHold) {
-              load_q(qb[0], ks);
-              load_q(qb[1], ks + 1);
-            }
 #pragma unroll
             for (int kb = 0; kb < C::KW / 16; ++kb) {
               uint32_t r[4];
@@ -322,22 +323,20 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {  // r[0], r[1]: keys 0..7, 8..15 of step ks;  r[2], r[3]: of step ks + 1
                 const uint32_t b0 = e4m3x2_to_f16x2(r[j]), b1 = e4m3x2_to_f16x2(r[j] >> 16);
-                mma16816<true>(x[kb * 2 + (j & 1)], kHold ? qa[kHold ? ks + (j >> 1) : 0] : qb[j >> 1], b0, b1);
+                mma16816<true>(x[kb * 2 + (j & 1)], qa[ks + (j >> 1)], b0, b1);
               }
             }
           }
         } else {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
-            uint32_t qb[4];
-            if constexpr (!kHold) load_q(qb, ks);
 #pragma unroll
             for (int kb = 0; kb < C::KW / 16; ++kb) {
               uint32_t r[4];
               const int row = key0 + kb * 16 + (lane & 7) + ((lane >> 4) << 3);
               ldsm4(r, sk + tile_at<C>(row, 2 * ks + ((lane >> 3) & 1)));
-              mma16816<false>(x[kb * 2], kHold ? qa[kHold ? ks : 0] : qb, r[0], r[1]);
-              mma16816<false>(x[kb * 2 + 1], kHold ? qa[kHold ? ks : 0] : qb, r[2], r[3]);
+              mma16816<false>(x[kb * 2], qa[ks], r[0], r[1]);
+              mma16816<false>(x[kb * 2 + 1], qa[ks], r[2], r[3]);
             }
           }
         }
@@ -641,14 +640,8 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
   p.pool = reinterpret_cast<const uint16_t*>(pool);
   if (tc) return launch_tree_tc(map, p, c, tree_ctas(), st);
   if (tc1) return launch_tree_tc1(map, p, c, tree_ctas(), st);
-  if (f8) {
-    if (c.head_dim == 64) return launch_d<64, true>(map, p, st);
-    if (c.head_dim == 128) return launch_d<128, true>(map, p, st);
-    return launch_d<256, true>(map, p, st);
-  }
-  if (c.head_dim == 64) return launch_d<64, false>(map, p, st);
-  if (c.head_dim == 128) return launch_d<128, false>(map, p, st);
-  return launch_d<256, false>(map, p, st);
+  if (f8) return c.head_dim == 64 ? launch_d<64, true>(map, p, st) : launch_d<128, true>(map, p, st);
+  return c.head_dim == 64 ? launch_d<64, false>(map, p, st) : launch_d<128, false>(map, p, st);
 }
 
 }  // namespace trellis

@@ -688,7 +688,8 @@ cudaError_t launch_one(const CUtensorMap& map, const TreeParams& p, int ctas, cu
 
 }  // namespace
 
-bool tree_tc1_fits(const trellis_cache_t& c, int rows) { return rows > 16 && (c.dtype == TRELLIS_E4M3 || c.head_dim == 256); }
+// heads of 256, which no other kernel takes, and an e4m3 cache from 17 rows on (measured at tree_attention.cu)
+bool tree_tc1_fits(const trellis_cache_t& c, int rows) { return c.head_dim == 256 || (c.dtype == TRELLIS_E4M3 && rows > 16); }
 
 int tree_tc1_rows() { return kRows; }
 

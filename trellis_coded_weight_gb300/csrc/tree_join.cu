@@ -163,11 +163,13 @@ __global__ void __launch_bounds__(kThreads, kPerSM) join_kernel(const TreeParams
 
 template <int D>
 static cudaError_t launch_one(const TreeParams& p, int rows, float lift, int ctas, cudaStream_t st) {
-  const int most = p.max_tokens * p.group;
-  // Few rows are a few units per item, found without counting: 4 x 1 tokens, 1000 keys, 32/8 heads of 128: 12.2 us for the whole
-  // call, 13.5 with the count; 64 drafts, 131072 keys: 119 and 112.
-  if (rows <= 16)
-    return launch_pdl(join_kernel<D, true>, dim3((unsigned)ctas, (most + kRows - 1) / kRows * 4u), dim3(kThreads), 0, st, p, rows, ctas, lift);
+  // Few rows of items with a few parts each (as many as if all items were as long) are a few units per item, found without
+  // counting: 4 x 1 tokens, 1000 keys, 32/8 heads of 128: 12.2 us for the whole call, 13.5 with the count.  Rows or parts that make
+  // more units than four want blocks of their own: 64 drafts, 131072 keys: 119 and 112; 1 x 4096 keys, 16/2 heads of 256: 18.5, 13.7.
+  const int most = p.max_tokens * p.group, row_units = (most + kRows - 1) / kRows;
+  const int col_units = D / 4 * kRows * (1 << tree_parts_shared(ctas / (p.hkv * p.batch) + 1)) / kThreads;
+  if (most <= 16 && col_units <= 4)
+    return launch_pdl(join_kernel<D, true>, dim3((unsigned)ctas, row_units * 4u), dim3(kThreads), 0, st, p, rows, ctas, lift);
   // no more blocks than there can be units: of a head's rows an eighth and one per sequence, times shares of the columns
   const int64_t units = (int64_t)p.hkv * (p.n * p.group / kRows + p.n) * (D / 16), fit = (int64_t)kPerSM * device_sm_count();
   return launch_pdl(join_kernel<D, false>, dim3((unsigned)(units < fit ? units : fit)), dim3(kThreads), 0, st, p, rows, ctas, lift);

@@ -212,11 +212,11 @@ struct TreePages {
   }
 };
 
+__host__ __device__ __forceinline__ int tree_parts_shared(int parts) { return parts <= 8 ? 0 : parts <= 16 ? 1 : parts <= 32 ? 2 : 3; }
 // An item for the joining kernel, of parts from block `first` to `last`: its sequence's first draft, head, first row; packed,
 // the last block, rows, and (log2) how many share its parts.  Packed 0: no item.
 __device__ __forceinline__ int4 tree_item(const TreeSegment& g, int row0, int rows, int first, int last) {
-  const int parts = last - first + 1, shared = parts <= 8 ? 0 : parts <= 16 ? 1 : parts <= 32 ? 2 : 3;
-  return make_int4(g.seq.start, g.head, row0, shared << 24 | rows << 12 | last);
+  return make_int4(g.seq.start, g.head, row0, tree_parts_shared(last - first + 1) << 24 | rows << 12 | last);
 }
 __device__ __forceinline__ int tree_item_last(int w) { return w & 0xFFF; }
 __device__ __forceinline__ int tree_item_rows(int w) { return w >> 12 & 0xFFF; }
