@@ -341,8 +341,8 @@ typedef struct trellis_norm_rope {
  *   c and s from row positions[token] of `rope`
  * q_out gets the queries as bf16.  Keys, and the values as they are, go to
  * row slots[token] % page_size of page slots[token] / page_size of `layer`:
- * as bf16, or as e4m3 of the number divided by its scale, clamped to +-448
- * (nearest, ties to even; NaN stays NaN).
+ * as bf16, or as e4m3 of the number times the (fp32) reciprocal of its
+ * scale, clamped to +-448 (nearest, ties to even; NaN stays NaN).
  *   q [n][q_heads][head_dim]   k, v [n][kv_heads][head_dim] bf16; the strides
  *   are those from token to token, in elements, multiples of 8.  q_out may be
  *   q (with the same stride).
@@ -382,11 +382,11 @@ typedef struct trellis_drafts {
  * the values; one rounding to bf16 at the end.  A token that sees nothing (or
  * only scores of minus infinity) gets zeros and an lse of minus infinity.
  * What a token does not see (masked drafts, rows past a sequence's end) does
- * not reach its result, whatever its bits are.
+ * not reach its result, whatever its bits are.  The results of a query with a
+ * number that is not finite are undefined; no others are touched.
  *   q, out [n][q_heads][head_dim] bf16, strides from token to token in
  *   elements, multiples of 8;  lse [n][q_heads] fp32 or NULL
- *   workspace: as for trellis_matvec_axis0, of at least
- *   trellis_tree_workspace_bytes bytes.
+ *   workspace: at least trellis_tree_workspace_bytes bytes, no initial state.
  * q_heads must be a multiple of cache->heads.  Lengths are device data and
  * clamped: prefix to the table's width, drafts to max_tokens and n, table
  * entries to the pool (entries that a length does not reach are not read).

@@ -616,7 +616,7 @@ def _workspace(nbytes: int, device, what: str) -> torch.Tensor:
 
 
 def new_tree_workspace(cache: PagedCache, batch: DraftBatch, q_heads: int) -> torch.Tensor:
-    """A zero-filled workspace for tree_attention (reusable for calls of these sizes, one at a time)."""
+    """A workspace for tree_attention (reusable for calls of these sizes, one at a time)."""
     with _on(cache.pool):
         return _workspace(int(_serving_lib().trellis_tree_workspace_bytes(cache._ref, max(1, batch.batch), batch.max_tokens,
                                                                           q_heads)), cache.device, "tree_attention")

@@ -2,7 +2,7 @@
 // tree_attention.cu handles at the rate of HBM.
 //
 // The mathematics is that of tree_attention.cu.  A block takes up to 256 rows of one key/value head and 128 keys per
-// step; both products are 128 x N tcgen05 MMAs of one issuing thread with accumulators in tensor memory:
+// step; both products are 128 x N tcgen05 MMAs of one issuing warp with accumulators in tensor memory:
 //   S = Q K^T    Q and K in shared memory (128-byte swizzle, along the head dim)
 //   O += P V     P in tensor memory over the scores it was made of, V in shared memory (swizzled, along the head dim too)
 // Two softmax warpgroups, one thread per row, each own a stream of steps with its own S, O, maximum and sum:
@@ -11,6 +11,9 @@
 // so that one stream's products run while the other's softmax does.  A stream's maximum is only moved when it has grown by
 // more than 2^8: the weights then stay below 2^8, well inside bf16 and fp32, and O is rarely rescaled.
 // Keys and values arrive by TMA in a ring of tiles in the order of their use.
+// Bound: HBM up to 64 or so rows (16 drafts, 131072 keys, 32/8 heads of 128: 87 us, 6.2 TB/s).  With 256 rows the chain of
+// scores, weights and products (a step of both streams 3200 cycles, of which its MMAs take 2150): 64 drafts, 131072 keys 112 us
+// (1.2 PFLOP/s); 4 x 64 drafts, 16384 keys, 40/8 heads, where 64 of 320 rows read the cache once more: 115 us (0.75 PFLOP/s).
 #include <cstring>
 #include <cuda.h>
 

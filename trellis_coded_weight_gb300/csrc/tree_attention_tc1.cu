@@ -1,9 +1,9 @@
 // tree_attention_tc1.cu -- tree attention with the 5th-generation tensor cores for e4m3 caches (any head dim) and heads of
 // 256, where tree_attention_tc.cu's two accumulators do not fit.
 //
-// As there, S = Q K^T and O += P V are tcgen05 MMAs of one issuing thread, P lies in tensor memory over its scores (here Q
-// does too, which spares shared memory a read of it per step), and two
-// softmax warpgroups alternate between the tiles, a thread per row.  Here a block has 128 rows and one accumulator O, so the
+// As there, S = Q K^T and O += P V are tcgen05 MMAs of one issuing warp, P lies in tensor memory over its scores (and Q lies
+// there too: that leaves shared memory to the rings of tiles), and two softmax warpgroups alternate between the tiles, a
+// thread per row.  Here a block has 128 rows and one accumulator O, so the
 // maximum in use is one per row: the warp that has tile i hands its rows' maxima to the warp that has tile i + 1 (an mbarrier
 // per warp), before it makes its weights; the groups' sums of weights stay apart until the end.
 //
@@ -11,7 +11,10 @@
 // two e4m3 numbers of 4 (each row scaled by a power of two first), S = Qhi K^T + Qlo K^T at twice the 16-bit rate.  The
 // values become fp16 in shared memory, by a warpgroup of its own (exact), since weights of 4 bits would not do; P is fp16
 // then.  That group also clears what must not reach a product.
-// Bound: HBM for a cache of 16-bit numbers; with e4m3 the conversion of the values comes near it.
+// Bound: the chain of a tile's scores, weights, conversion and products, 2000 cycles per tile of 64 keys where HBM would take
+// 1400: 32 x 4 drafts, ragged to 8200 e4m3 keys, 16/2 heads of 256: 40 us (3.0 TB/s); 1 x 4 drafts, 131072 keys 40 us, bf16 52
+// (5.2 TB/s).  Repeating few rows in the lanes that idle, each copy with its part of a tile's keys, made the weights of a tile
+// four times as fast and the whole no faster (43 and 49 us): the join of the copies costs more than the chain gains.
 #include <cstring>
 #include <cuda.h>
 
