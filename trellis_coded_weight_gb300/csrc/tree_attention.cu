@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   if (warp == 0) tree_cumulate<kRows, kTile, false, kExtra>(p, seqs);
   __syncthreads();
   const int total = seqs.cum[p.batch];
-  const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
+  const int ctas = tree_ctas_used<kRows, false>(p, total, (int)gridDim.x);
   const int cta = blockIdx.x;
   if (cta >= ctas) {  // fewer steps than blocks
     if (threadIdx.x == 0) p.items[cta] = make_int4(0, 0, 0, 0);

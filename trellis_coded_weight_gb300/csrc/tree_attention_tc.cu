@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
-  const int ctas = tree_ctas_used<true>(total, (int)gridDim.x);
+  const int ctas = tree_ctas_used<kRows, true>(p, total, (int)gridDim.x);
   TreeWalk<kRows, kTile, true> walk(total, ctas, cta);
   TreeSegment g;
   const auto rows_of = [&](const TreeSegment& x) { return min(kRows, x.seq.count * p.group - x.row_block * kRows); };

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
   const uint32_t tmem = uniform(*tmem_slot);
   const int total = seqs.cum[p.batch];
   const int cta = blockIdx.x;
-  const int ctas = tree_ctas_used<false>(total, (int)gridDim.x);
+  const int ctas = tree_ctas_used<kRows, false>(p, total, (int)gridDim.x);
   TreeWalk<kRows, kTile, false> walk(total, ctas, cta);
   TreeSegment g;
 

@@ -120,10 +120,10 @@ __device__ __forceinline__ void tree_cumulate(const TreeParams& p, TreeMap& map)
 
 // The blocks' ranges: block c of `ctas` takes [c * total / ctas, (c + 1) * total / ctas); the block that holds `at`:
 __device__ __forceinline__ int tree_cta_of(int64_t at, int64_t total, int ctas) { return (int)(((at + 1) * ctas - 1) / total); }
-// Blocks in use: none is left without a step.
-template <bool HALVES>
-__device__ __forceinline__ int tree_ctas_used(int total, int grid) {
-  const int most = HALVES ? (total + 1) / 2 : total;
+// Blocks in use: no part of an item is left without a step, so ranges are as long as the longest step.
+template <int ROWS, bool HALVES>
+__device__ __forceinline__ int tree_ctas_used(const TreeParams& p, int total, int grid) {
+  const int most = HALVES && p.max_tokens * p.group > ROWS / 2 ? (total + 1) / 2 : total;
   return most < grid ? most : grid;
 }
 
