@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   __shared__ int s_copies;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) s_copies = 0;
+  // loads that depend on nothing come first: the planning is a chain of trips to memory
+  int32_t r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = tid * 4 + j < p.pages ? p.refs[tid * 4 + j] : 1;
 
   // 1. what each pair asks for: one warp per pair
   for (int i = warp; i < p.pairs; i += kPlanThreads / 32) {
@@ -175,16 +179,19 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
     if (ch < 0 || ch >= p.rows || par < -1 || par >= p.rows) kind = kBad;
     int held = 0, len = 0, full = 0, need = 0;
     if (kind != kBad) {
+      const int32_t first_len = kind != kFree ? p.lens[par] : 0;
+      const int32_t first_child = lane < p.width ? p.table[(int64_t)ch * p.width + lane] : -1;
+      const int32_t first_parent = kind == kFork && lane < p.width ? p.table[(int64_t)par * p.width + lane] : 0;
       bool more = true;
       for (int e = 0; more && e < p.width; e += 32) {  // leading entries >= 0
-        const bool has = e + lane < p.width && p.table[(int64_t)ch * p.width + e + lane] >= 0;
+        const bool has = e + lane < p.width && (e ? p.table[(int64_t)ch * p.width + e + lane] : first_child) >= 0;
         const unsigned b = __ballot_sync(0xFFFFFFFFu, has);
         const int lead = b == 0xFFFFFFFFu ? 32 : __ffs(~b) - 1;
         held += lead;
         more = lead == 32;
       }
       if (kind != kFree) {
-        len = p.lens[par];
+        len = first_len;
         const int64_t most = (int64_t)p.width << p.page_shift;
         if (len < 0 || len > most) kind = kBad;
         else {
@@ -196,11 +203,11 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
       }
       // every page that is shared, copied or given up has to be one of the pool
       bool bad = false;
-      for (int e = lane; e < held; e += 32) bad |= p.table[(int64_t)ch * p.width + e] >= p.pages;
+      for (int e = lane; e < held; e += 32) bad |= (e < 32 ? first_child : p.table[(int64_t)ch * p.width + e]) >= p.pages;
       if (kind == kFork) {
         const int used = (len + (1 << p.page_shift) - 1) >> p.page_shift;
         for (int e = lane; e < used; e += 32) {
-          const int32_t page = p.table[(int64_t)par * p.width + e];
+          const int32_t page = e < 32 ? first_parent : p.table[(int64_t)par * p.width + e];
           bad |= page < 0 || page >= p.pages;
         }
       }
@@ -225,9 +232,9 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParam
   int found = 0;
   for (int64_t base = 0; base < p.pages && found < asked; base += kPlanThreads * 4) {
     const int64_t e = base + tid * 4;
-    int32_t r[4];
+    if (base > 0)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = e + j < p.pages ? p.refs[e + j] : 1;
+      for (int j = 0; j < 4; ++j) r[j] = e + j < p.pages ? p.refs[e + j] : 1;
     const int mine = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
     int total;
     int at = found + block_scan(mine, scratch, &total) - mine;
