@@ -4,9 +4,10 @@
 // Fork and compact are two launches each.  A planning kernel of one thread block works on the integers (page table,
 // reference counts): a running count over the pages gives the k-th lowest free page, so the result does not depend
 // on any order of execution.  It leaves a list of page copies in the workspace.  The copying kernel then moves them in all layers, in
-// units of 16 KB spread evenly over the GPU.  The copies are bound by HBM (a compaction that moves 133 MB: 40 us of copying, 6.7 TB/s
-// read and written; a fork of 159 MB 53 us, 6 TB/s), the planning by latency (6 us for a compaction, 10 for a fork: a handful of
-// dependent trips to memory).  Commit is one launch of 12 us for 25 MB: it has to know where a row goes before it can move it.
+// units of 16 KB spread evenly over the GPU.  The copies are bound by HBM: a compaction that moves 133 MB copies for 40 us, 6.7 TB/s
+// read and written; a fork of 159 MB from few sources writes for 50 us, 3.2 TB/s, where a fill of such a size reaches 3.7.  (One load
+// of a place for all of its copies changed nothing, and cost small forks 2 us.)  The planning is bound by latency: 6 us for a
+// compaction, 10 for a fork, a handful of dependent trips to memory.  Commit is one launch of 12 us for 25 MB: it has to know where a row goes before it can move it.
 #include "common.cuh"
 #include "launch.h"
 #include "pdl.cuh"
