@@ -660,10 +660,13 @@ def new_cache_workspace(cache: PagedCache, table, pairs: int = 0) -> torch.Tenso
 
 def cache_copy(cache: PagedCache, src, dst):
     """Copies pages src[i] to dst[i] (int32) in every layer."""
-    n = src.shape[0]
-    sp, dp = _req_rows(src, "src", torch.int32, (n,)), _req_rows(dst, "dst", torch.int32, (n,))
-    _same_device(cache.device, src=src, dst=dst)
-    _call("trellis_cache_copy", cache.index, cache._ref, sp, dp, n)
+    n, index = src.shape[0], cache.index
+    if not (src.dtype is _I32 and dst.dtype is _I32 and src.shape == dst.shape == (n,) and src.is_contiguous() and
+            dst.is_contiguous() and src.get_device() == dst.get_device() == index):
+        _req_rows(src, "src", _I32, (n,))
+        _req_rows(dst, "dst", _I32, (n,))
+        _same_device(cache.device, src=src, dst=dst)
+    _call("trellis_cache_copy", index, cache._ref, src.data_ptr(), dst.data_ptr(), n)
 
 
 def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, workspace, room: int = 0):
@@ -672,14 +675,22 @@ def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, work
     positions; parent[i] = child[i] only adds the room, parent[i] = -1 frees the row.  status[i]: 0 done, 1 no room,
     2 out of range."""
     rows, width = table.shape
-    pairs = parent.shape[0]
-    args = (_req_rows(table, "table", torch.int32, (rows, width)), _req_rows(lens, "lens", torch.int32, (rows,)),
-            _req_rows(refs, "refs", torch.int32, (cache.pages,)), _req_rows(parent, "parent", torch.int32, (pairs,)),
-            _req_rows(child, "child", torch.int32, (pairs,)), _req_rows(status, "status", torch.int32, (pairs,)))
-    wp, wn = _req_workspace(workspace)
-    _same_device(cache.device, table=table, lens=lens, refs=refs, parent=parent, child=child, status=status,
-                 workspace=workspace)
-    _call("trellis_cache_fork", cache.index, cache._ref, *args, pairs, rows, width, room, wp, wn)
+    pairs, index = parent.shape[0], cache.index
+    if not (table.dtype is _I32 and lens.dtype is _I32 and refs.dtype is _I32 and parent.dtype is _I32 and child.dtype is _I32 and
+            status.dtype is _I32 and lens.shape == (rows,) and refs.shape == (cache.pages,) and
+            parent.shape == child.shape == status.shape == (pairs,) and table.is_contiguous() and lens.is_contiguous() and
+            refs.is_contiguous() and parent.is_contiguous() and child.is_contiguous() and status.is_contiguous() and
+            workspace.is_contiguous() and table.get_device() == lens.get_device() == refs.get_device() ==
+            parent.get_device() == child.get_device() == status.get_device() == workspace.get_device() == index):
+        for t, name, shape in ((table, "table", (rows, width)), (lens, "lens", (rows,)), (refs, "refs", (cache.pages,)),
+                               (parent, "parent", (pairs,)), (child, "child", (pairs,)), (status, "status", (pairs,))):
+            _req_rows(t, name, _I32, shape)
+        _req_workspace(workspace)
+        _same_device(cache.device, table=table, lens=lens, refs=refs, parent=parent, child=child, status=status,
+                     workspace=workspace)
+    _call("trellis_cache_fork", index, cache._ref, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), parent.data_ptr(),
+          child.data_ptr(), status.data_ptr(), pairs, rows, width, room, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return status
 
 
@@ -689,12 +700,19 @@ def cache_compact(cache: PagedCache, table, refs, workspace, out_table=None, out
     rows, width = table.shape
     out_table = table if out_table is None else out_table
     out_refs = refs if out_refs is None else out_refs
-    args = (_req_rows(table, "table", torch.int32, (rows, width)), _req_rows(refs, "refs", torch.int32, (cache.pages,)),
-            _req_rows(out_table, "out_table", torch.int32, (rows, width)),
-            _req_rows(out_refs, "out_refs", torch.int32, (cache.pages,)))
-    wp, wn = _req_workspace(workspace)
-    _same_device(cache.device, table=table, refs=refs, out_table=out_table, out_refs=out_refs, workspace=workspace)
-    _call("trellis_cache_compact", cache.index, cache._ref, *args, rows, width, wp, wn)
+    index, held = cache.index, (cache.pages,)
+    if not (table.dtype is _I32 and refs.dtype is _I32 and out_table.dtype is _I32 and out_refs.dtype is _I32 and
+            refs.shape == held and out_table.shape == (rows, width) and out_refs.shape == held and table.is_contiguous() and
+            refs.is_contiguous() and out_table.is_contiguous() and out_refs.is_contiguous() and workspace.is_contiguous() and
+            table.get_device() == refs.get_device() == out_table.get_device() == out_refs.get_device() ==
+            workspace.get_device() == index):
+        for t, name, shape in ((table, "table", (rows, width)), (refs, "refs", held), (out_table, "out_table", (rows, width)),
+                               (out_refs, "out_refs", held)):
+            _req_rows(t, name, _I32, shape)
+        _req_workspace(workspace)
+        _same_device(cache.device, table=table, refs=refs, out_table=out_table, out_refs=out_refs, workspace=workspace)
+    _call("trellis_cache_compact", index, cache._ref, table.data_ptr(), refs.data_ptr(), out_table.data_ptr(),
+          out_refs.data_ptr(), rows, width, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out_table, out_refs
 
 
@@ -706,11 +724,18 @@ def cache_commit(cache: PagedCache, table, prefix, path, accepted, out_lens=None
     tokens = path.shape[1]
     if out_lens is None:
         out_lens = torch.empty_like(prefix)
-    args = (_req_rows(table, "table", torch.int32, (batch, width)), _req_rows(prefix, "prefix", torch.int32, (batch,)),
-            _req_rows(path, "path", torch.int32, (batch, tokens)),
-            _req_rows(accepted, "accepted", torch.int32, (batch,)), _req_rows(out_lens, "out_lens", torch.int32, (batch,)))
-    _same_device(cache.device, table=table, prefix=prefix, path=path, accepted=accepted, out_lens=out_lens)
-    _call("trellis_cache_commit", cache.index, cache._ref, *args, batch, width, tokens)
+    index, row = cache.index, (batch,)
+    if not (table.dtype is _I32 and prefix.dtype is _I32 and path.dtype is _I32 and accepted.dtype is _I32 and
+            out_lens.dtype is _I32 and prefix.shape == accepted.shape == out_lens.shape == row and path.shape == (batch, tokens) and
+            table.is_contiguous() and prefix.is_contiguous() and path.is_contiguous() and accepted.is_contiguous() and
+            out_lens.is_contiguous() and table.get_device() == prefix.get_device() == path.get_device() ==
+            accepted.get_device() == out_lens.get_device() == index):
+        for t, name, shape in ((table, "table", (batch, width)), (prefix, "prefix", row), (path, "path", (batch, tokens)),
+                               (accepted, "accepted", row), (out_lens, "out_lens", row)):
+            _req_rows(t, name, _I32, shape)
+        _same_device(cache.device, table=table, prefix=prefix, path=path, accepted=accepted, out_lens=out_lens)
+    _call("trellis_cache_commit", index, cache._ref, table.data_ptr(), prefix.data_ptr(), path.data_ptr(),
+          accepted.data_ptr(), out_lens.data_ptr(), batch, width, tokens)
     return out_lens
 
 
