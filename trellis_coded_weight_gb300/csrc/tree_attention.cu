@@ -9,8 +9,10 @@
 //   this one                 heads of 64 and 128, up to 16 rows of a key/value head (its group of query heads times the drafts)
 //   tree_attention_tc.cu     bf16 heads of 64 and 128, more rows:   tcgen05, 256 rows a block
 //   tree_attention_tc1.cu    e4m3 of those, and heads of 256:      tcgen05, 128 rows a block
-// Measured on both sides (us, this one / the other; 32/8 heads of 128 unless said otherwise): 16 rows, 4096 keys 11.2 / 12.3, 300 keys
-// 8.2 / 9.5, ragged batch of 32 to 2000 37 / 35, 60000 keys 46 / 45; 16 rows of heads of 64, 300 keys 6.9 / 8.7; 32 rows, 131072 keys 126 / 86, ragged batch to 2048 46 / 35, e4m3 45 / 37.
+// Measured on both sides (us, this one / the other; 32/8 heads of 128 unless said otherwise):
+//   16 rows: 300 keys 8.2 / 9.5, 4096 keys 11.2 / 12.3, ragged batch of 32 to 2000 37 / 35, 60000 keys 46 / 45;
+//            heads of 64, 300 keys 6.9 / 8.7, 60000 keys 29 / 31
+//   32 rows: 4096 keys 13.0 / 12.8, ragged batch of 32 to 2048 46 / 35 (e4m3 45 / 37), 131072 keys 126 / 86
 // Heads of 256 (e4m3, 16/2 heads): 8 rows, 4096 keys 18.1 / 13.7, 60000 keys 33.5 / 26.4, 300 keys 9.8 / 10.8.
 //
 // Here a block takes all rows, padded to 16, and its four warps split the keys of a tile between them: scores and outputs
