@@ -17,8 +17,8 @@
 // between the threads take the next key each.
 //
 // A row is split over blocks where there are few rows; the last block to arrive joins the parts in their order, so
-// results do not depend on timing.  Bound: latency for a row (1 x 50257 bf16, 5 alternatives: 7.5 us); for many rows the issue of the
-// exponentials and sums, and the tail of alternatives that every block has: 61 x 128256 fp32 13.1 us (2.4 TB/s),
+// results do not depend on timing.  Bound: latency for a row (1 x 50257 bf16, 5 alternatives: 7.7 us); for many rows the issue of the
+// exponentials and sums, and the tail of alternatives that every block has: 61 x 128256 fp32 13.0 us (2.4 TB/s),
 // 256 x 151936 bf16 with 20 alternatives 28 us (2.8 TB/s).
 #include "common.cuh"
 #include "launch.h"
@@ -319,24 +319,27 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
     if (!(acc.r < th) && first + tid < last) sh.holders[atomicAdd(&sh.n_holders, 1)] = tid;
     __syncthreads();
     const int holders = sh.n_holders;
-    // lists what passes: numbers from the threshold up, or (strict) above it
+    // Lists what passes: numbers from the threshold up, or (strict) above it.  The holders' vectors are shared out over all threads
+    // (a warp per holder, most of whose lanes have none where parts are short: 174 x 34577, 25 alternatives 14.1 us, 12.3 so).
+    const int per = (last - first + kThreads - 1) / kThreads, again = holders * per;  // vectors of a holder, of all
     const auto collect = [&](bool strict) {
-      for (int h = warp; h < holders; h += kWarps)
-        for (int v = first + sh.holders[h] + lane * kThreads; v < last; v += 32 * kThreads) {
-          const uint4 u = x.load(v);
-          const float m = Vec<T>::max(u);
-          if (strict ? m <= th : m < th) continue;
-          const int c = x.col(v);
+      for (int k = tid; k < again; k += kThreads) {
+        const int h = k / per, v = first + sh.holders[h] + (k - h * per) * kThreads;
+        if (v >= last) continue;
+        const uint4 u = x.load(v);
+        const float m = Vec<T>::max(u);
+        if (strict ? m <= th : m < th) continue;
+        const int c = x.col(v);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float2 q = Vec<T>::pair(u, i >> 1);
-            const float e = i & 1 ? q.y : q.x;
-            if (!(strict ? e <= th : e < th) && c + i >= 0 && c + i < p.vocab) {
-              const int at = atomicAdd(&sh.count, 1);
-              if (at < kList) sh.list[at] = key_of(e, c + i);
-            }
+        for (int i = 0; i < N; ++i) {
+          const float2 q = Vec<T>::pair(u, i >> 1);
+          const float e = i & 1 ? q.y : q.x;
+          if (!(strict ? e <= th : e < th) && c + i >= 0 && c + i < p.vocab) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kList) sh.list[at] = key_of(e, c + i);
           }
         }
+      }
       __syncthreads();
     };
     collect(false);
