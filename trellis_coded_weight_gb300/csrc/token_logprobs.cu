@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
       __syncthreads();
       collect(true);
       const int above = sh.count;
+      __syncthreads();  // read by all before anyone adds to it: the branch and the loop's end have to be the block's
       listed = above <= kList - 2 * kThreads;
       if (listed) {
         const int end = min(x.col(last), p.vocab);
