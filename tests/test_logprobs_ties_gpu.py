@@ -50,3 +50,15 @@ def test_numbers_above_a_threshold_that_many_equal(top, bf16):
     for _ in range(30):
         got = tb.token_logprobs(x, tokens, top, ws)
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("n,vocab", [(1, 9001), (1, 151936), (700, 2500)])
+def test_rows_of_nan_alone(n, vocab, bf16):
+    # every number orders before all others and is equal to the rest: the first columns, column 0 too
+    x = torch.full((n, vocab), float("nan"), dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")
+    x[n // 2, vocab - 1] = 1.0
+    tokens = torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+    got = tb.token_logprobs(x, tokens, 20, tb.new_logprobs_workspace(n, vocab, 20, "cuda"))
+    assert got.top_ids.tolist() == [list(range(20))] * n
+    assert all(t.isnan().all() for t in (got.logprobs, got.lse, got.entropy, got.top_logprobs))

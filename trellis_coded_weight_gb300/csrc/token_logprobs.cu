@@ -205,9 +205,10 @@ __device__ __forceinline__ float find_threshold(Shared& sh, float thread_max, in
   return sh.threshold;
 }
 
-// The largest key below `below` among the vectors first + of, first + of + kThreads, .. of thread `of`, by a warp.
+// The largest key up to `most` among the vectors first + of, first + of + kThreads, .. of thread `of`, by a warp.  (A NaN in
+// column 0 has the largest key there is.)
 template <typename T>
-__device__ __forceinline__ unsigned long long next_key(const Row<T>& row, int of, int first, int last, unsigned long long below) {
+__device__ __forceinline__ unsigned long long next_key(const Row<T>& row, int of, int first, int last, unsigned long long most) {
   constexpr int N = Vec<T>::N;
   unsigned long long best = 0;
   for (int v = first + of + (threadIdx.x & 31) * kThreads; v < last; v += 32 * kThreads) {
@@ -216,7 +217,7 @@ __device__ __forceinline__ unsigned long long next_key(const Row<T>& row, int of
     for (int i = 0; i < N; ++i)
       if (c + i >= 0 && c + i < row.vocab) {
         const unsigned long long key = key_of(Vec<T>::one(row.x + c + i), c + i);
-        if (key < below && key > best) best = key;
+        if (key <= most && key > best) best = key;
       }
   }
 #pragma unroll
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) logprobs_kernel(const Params
         if (tid == 0) sh.best[k] = b;
         if (warp_best == b) {  // this warp's thread holds it: keys are distinct (more than top_k numbers, so none is 0)
           const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, mine == b)) - 1;
-          const unsigned long long next = next_key(x, warp * 32 + owner, first, last, b);
+          const unsigned long long next = next_key(x, warp * 32 + owner, first, last, b - 1);
           if (lane == owner) mine = next;
         }
         __syncthreads();
