@@ -591,7 +591,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       named_sync(1, 256);
       // the last tile's warp has left the final maxima: both groups bring their sums to them
       const float m = active ? row_max[r] : -INFINITY;
-      const float mine = used == -INFINITY ? 0.f : l * ex2(used - m);
+      // (l is 0 without a maximum, or NaN where all of the row's scores were: it stays)
+      const float mine = used == -INFINITY ? l : l * ex2(used - m);
       row_sum[s * kRows + r] = mine;
       named_sync(1, 256);
       l = mine + row_sum[(1 - s) * kRows + r];
