@@ -63,3 +63,24 @@ def test_rows_that_do_not_see_such_keys_keep_their_results(hq, hkv, d, f8, toks)
     put(s, 1, [71], 0, 0)
     want, want_lse = s.run()
     assert torch.equal(out[~sees], want[~sees]) and torch.equal(lse[~sees], want_lse[~sees])
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", [k for k in KERNELS if k[3]])
+@pytest.mark.parametrize("largest,scale", [((126, 127), 2e-38), ((-126, -128), 2e38)])
+def test_e4m3_queries_at_the_ends_of_their_range(largest, scale, hq, hkv, d, f8, toks):
+    # rows whose largest number has the largest two exponents of bf16, or its smallest normal one and a subnormal one
+    s = Step([70], [toks], hq, hkv, d, 64, f8, seed=d + toks)
+    s.scales *= 0.1
+    q = s.q.float()
+    q /= q.abs().amax(-1, keepdim=True)
+    of = torch.where(torch.arange(toks, device="cuda") % 2 == 0, 1.5 * 2.0 ** largest[0], 1.5 * 2.0 ** largest[1]).float()
+    s.q, s.scale = (q * of[:, None, None]).bfloat16(), scale
+    assert s.q.isfinite().all() and (s.q != 0).any(-1).all()
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", KERNELS)
+def test_zero_queries_weigh_all_alike(hq, hkv, d, f8, toks):
+    s = Step([70], [toks], hq, hkv, d, 64, f8, seed=d + toks)
+    s.q = torch.zeros_like(s.q)
+    s.check(*s.run())

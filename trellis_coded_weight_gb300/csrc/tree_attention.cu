@@ -241,9 +241,10 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             constexpr unsigned kLanes = LPR == 32 ? 0xFFFFFFFFu : (1u << LPR) - 1;
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kLanes << (lane / LPR * LPR), m, o));
-            // the row's largest exponent to 0: fp16 then keeps every bf16 number within 2^-14 of the largest exactly
+            // the row's largest exponent to 0: fp16 then keeps every bf16 number within 2^-14 of the largest exactly.  At the
+            // ends (zero and subnormal rows; the largest exponent) as near as the factor and its reciprocal stay normal numbers.
             uint32_t e = __float_as_uint(m) >> 23;
-            if (e < 2 || e > 252) e = 127;  // zero, subnormal, infinite or NaN rows as they are
+            e = e == 255 ? 127u : min(max(e, 1u), 253u);  // infinite or NaN rows as they are
             fac = __uint_as_float(e << 23);
             const float inv = __uint_as_float((254u - e) << 23);
             u = make_uint4(pack_f16x2(x[0] * inv, x[1] * inv), pack_f16x2(x[2] * inv, x[3] * inv),

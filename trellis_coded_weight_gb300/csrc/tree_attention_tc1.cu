@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       const int row0 = g.row_block * kRows, rows = min(kRows, g.seq.count * p.group - row0), n = g.tiles;
       const int len = g.seq.prefix + g.seq.count;
       const float k_scale = F8 && p.scales ? __ldg(p.scales + g.head) : 1.f;
-      const uint32_t flip = p.scale_log2 * k_scale < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
+      const uint32_t flip = (p.scale_log2 < 0.f) != (k_scale < 0.f) ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
       const bool valid = r < rows, active = w4 * 32 < rows;  // warps without a row only keep the count
       const int draft = tree_draft(p, row0 + r), qhead = g.head * p.group + row0 + r - draft * p.group;
       // ---- queries, 32 rows at a time: loaded along the rows, staged, and put into tensor memory by the warps that own the rows,
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
               // the largest and within 2^-17 of it below
               uint32_t e = max(m2 & 0xFFFFu, m2 >> 16) >> 7;
               const bool none = e == 255;     // infinite or NaN: so are the row's results
-              if (e < 10 || none) e = 134;    // zero, or too small to matter: as they are
+              e = none ? 134u : max(e, 8u);   // below 2^-119 the factor is its smallest, 2^-126
               const float inv = __uint_as_float((261u - e) << 23);
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               uint32_t hi[4], lo[4];
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_ready);
-      // a scale of 0 too leaves minus infinity where it is
-      const float c = fmaxf(fabsf(p.scale_log2 * k_scale) * fac, 1e-37f);
+      // (the row's factor first: a small scale is that of large queries.)  A scale of 0 too leaves minus infinity where it is.
+      const float c = fmaxf(fabsf(p.scale_log2) * fac * fabsf(k_scale), 1e-37f);
       float used = -INFINITY, l = 0.f;        // the maximum that l is relative to
       for (int i = s; i < n; i += 2) {
         wait(s_full + s, ns++);
