@@ -84,3 +84,30 @@ def test_zero_queries_weigh_all_alike(hq, hkv, d, f8, toks):
     s = Step([70], [toks], hq, hkv, d, 64, f8, seed=d + toks)
     s.q = torch.zeros_like(s.q)
     s.check(*s.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", KERNELS)
+def test_small_scales_of_large_queries(hq, hkv, d, f8, toks):
+    # scores of about one from queries of 1e36 (their products with the keys stay below the largest number of fp32)
+    s = Step([300, 5], [toks, toks], hq, hkv, d, 64, f8, seed=d + toks, std=1e36)
+    s.scale = 4e-38
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", KERNELS)
+def test_a_scale_of_zero_weighs_all_alike(hq, hkv, d, f8, toks):
+    s = Step([300, 5], [toks, toks], hq, hkv, d, 64, f8, seed=d + toks, masks="random")
+    s.scale = 0.0
+    s.check(*s.run())
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", [k for k in KERNELS if k[3]])
+def test_a_cache_scale_that_is_no_number(hq, hkv, d, f8, toks):
+    # keys of the first head: its queries' results are NaN, the other heads' are what they were
+    s = Step([70], [toks], hq, hkv, d, 64, f8, seed=d + toks)
+    want, want_lse = s.run()
+    s.scales[0, 0, 0] = float("nan")
+    out, lse = s.run()
+    mine = hq // hkv
+    assert out[:, :mine].isnan().all() and lse[:, :mine].isnan().all()
+    assert torch.equal(out[:, mine:], want[:, mine:]) and torch.equal(lse[:, mine:], want_lse[:, mine:])

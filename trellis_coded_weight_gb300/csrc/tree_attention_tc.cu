@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2, lrow = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + C::S(s) + lanes, t_o = tmem + C::O(s) + lanes;
-    const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // a scale of 0 too leaves minus infinity where it is
+    const float c = score_factor(fabsf(p.scale_log2));
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
     int t0 = 0, seg = 0, ns = 0, no = 0;
     int4 shared_item = make_int4(0, 0, 0, 0);  // the item that starts here and ends in a later block

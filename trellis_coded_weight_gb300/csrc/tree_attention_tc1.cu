@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(q_ready);
-      // (the row's factor first: a small scale is that of large queries.)  A scale of 0 too leaves minus infinity where it is.
-      const float c = fmaxf(fabsf(p.scale_log2) * fac * fabsf(k_scale), 1e-37f);
+      // the row's factor first: a small scale is that of large queries
+      const float c = score_factor(fabsf(p.scale_log2) * fac * fabsf(k_scale));
       float used = -INFINITY, l = 0.f;        // the maximum that l is relative to
       for (int i = s; i < n; i += 2) {
         wait(s_full + s, ns++);

@@ -47,6 +47,10 @@ __device__ __forceinline__ void mma_done(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar))
       : "memory");
 }
+// The factor of a row's scores, from its absolute value: a scale of 0 becomes the smallest number instead, times which every
+// score that is finite vanishes in a sum, and minus infinity stays what it is.
+__device__ __forceinline__ float score_factor(float c) { return c == 0.f ? __uint_as_float(1u) : c; }
+
 // A number that is the same in all lanes, to the compiler too.
 template <typename T>
 __device__ __forceinline__ T uniform(T v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
