@@ -379,7 +379,9 @@ typedef struct trellis_drafts {
  *   out = sum_p softmax_p(scale * q.k_p) v_p      lse = log sum_p exp(scale * q.k_p)
  * Scores, softmax statistics and sums are fp32; the softmax weights are
  * rounded to 16 bits (bf16, or fp16 with an e4m3 cache) for the products with
- * the values; one rounding to bf16 at the end.  A token that sees nothing (or
+ * the values; one rounding to bf16 at the end.  Queries are taken as they are;
+ * over an e4m3 cache numbers below 2^-13 of their row's largest are rounded, to
+ * within 2^-21 of the largest.  A token that sees nothing (or
  * only scores of minus infinity) gets zeros and an lse of minus infinity.
  * What a token does not see (masked drafts, rows past a sequence's end) does
  * not reach its result, whatever its bits are.  The results of a query with a

@@ -111,3 +111,15 @@ def test_a_cache_scale_that_is_no_number(hq, hkv, d, f8, toks):
     mine = hq // hkv
     assert out[:, :mine].isnan().all() and lse[:, :mine].isnan().all()
     assert torch.equal(out[:, mine:], want[:, mine:]) and torch.equal(lse[:, mine:], want_lse[:, mine:])
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,toks", KERNELS)
+@pytest.mark.parametrize("times", [2.0 ** 6, 2.0 ** 10, 2.0 ** 14])
+def test_query_rows_with_one_channel_far_above_the_others(times, hq, hkv, d, f8, toks):
+    # in every row another one; the others' part of a score is what separates the keys for which the large one's is alike
+    s = Step([600, 30], [toks, toks], hq, hkv, d, 64, f8, seed=d + toks)
+    q = s.q.float()
+    row = torch.arange(s.n * hq, device="cuda").view(s.n, hq, 1)
+    q.scatter_(2, row * 7 % d, torch.where(row % 2 == 0, times, -times))
+    s.q = q.bfloat16()
+    s.check(*s.run())

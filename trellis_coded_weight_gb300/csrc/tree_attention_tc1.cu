@@ -7,9 +7,12 @@
 // maximum in use is one per row: the warp that has tile i hands its rows' maxima to the warp that has tile i + 1 (an mbarrier
 // per warp), before it makes its weights; the groups' sums of weights stay apart until the end.
 //
-// An e4m3 cache is copied as it is.  The scores' MMAs read its keys as they are: Q's 8 significant bits are split exactly into
-// two e4m3 numbers of 4 (each row scaled by a power of two first), S = Qhi K^T + Qlo K^T at twice the 16-bit rate.  The
-// values become fp16 in shared memory, by a warpgroup of its own (exact), since weights of 4 bits would not do; P is fp16
+// An e4m3 cache is copied as it is.  The scores' MMAs read its keys as they are: Q is split into two 8-bit numbers (each row
+// scaled by a power of two first), S = Qhi K^T + Qlo K^T at twice the 16-bit rate.  Qhi is e4m3, with 4 of Q's 8 significant
+// bits; what it leaves is a whole number of at most 8 in Q's last place, which e5m2's 3 significant bits hold exactly, and e5m2
+// reaches 2^7 further down.  The split is exact down to 2^-13 of the row's largest number, and within 2^-21 of it below, where
+// Qhi has fewer bits.  (With e4m3 for Qlo too, 2^-9 and 2^-17: the lse of a row of 256 with one number 2^14 times the others
+// was off by 0.13.)  The values become fp16 in shared memory, by a warpgroup of its own (exact), since weights of 4 bits would not do; P is fp16
 // then.  That group also clears what must not reach a product.
 // Bound: the chain of a tile's scores, weights, conversion and products, 2000 cycles per tile of 64 keys where HBM would take
 // 1400: 32 x 4 drafts, ragged to 8200 e4m3 keys, 16/2 heads of 256: 40 us (3.0 TB/s); 1 x 4 drafts, 131072 keys 40 us, bf16 52
@@ -62,7 +65,7 @@ struct Cfg {
   static constexpr int RSlot = F8 ? Tile * D : 0;           // as the cache has them
   static constexpr int Threads = F8 ? 448 : 384;
   static constexpr int KSlots = 3, VSlots = 3, RSlots = F8 ? 3 : 0;
-  static constexpr int Stage = 32 * D * 2;                  // 32 rows of queries: bf16, or two e4m3 numbers
+  static constexpr int Stage = 32 * D * 2;                  // 32 rows of queries: bf16, or two 8-bit numbers
   static_assert(VSlots + 1 < kOdd, "the converting warps are at most the values' slots and a tile ahead");
   static constexpr int Fixed = Stage + 32 * 4 + kRows * 4 * 3 + (int)sizeof(TreeMap) + 1024;
   static constexpr int Smem = 1024 + KSlots * KSlot + VSlots * VSlot + RSlots * RSlot + Fixed;
@@ -78,6 +81,11 @@ struct Cfg {
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 
@@ -215,7 +223,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
         }
         return !dead;
       };
-      // type fields: bf16 1, fp16 0 of kind::f16; e4m3 0 of kind::f8f6f4
+      // type fields: bf16 1, fp16 0 of kind::f16; e4m3 0, e5m2 1 of kind::f8f6f4 (of A from bit 7, of B from bit 10)
       constexpr uint32_t kType = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;
       const uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kType, id_o = (tc::idesc_bf16_f32(128, D) & kType) | kBMnMajor;
       const uint64_t k_desc = tc::desc_kmajor(tc::smem_u32(keys), 8 * C::KBlock, C::KSwizzle),
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             constexpr int kPer = C::KBlock / 32;
             const uint32_t qa = tmem + C::Q + h * (D / 4) + 8 * k;
             const uint64_t ka = b + (uint32_t)((k / kPer * (kTile * C::KBlock) + k % kPer * 32) >> 4);
-            if constexpr (F8) mma_ts_e4m3(tmem + C::S(s), qa, ka, id_s, h > 0 || k > 0);
+            if constexpr (F8) mma_ts_f8(tmem + C::S(s), qa, ka, h == 0 ? id_s : id_s | 1u << 7, h > 0 || k > 0);
             else mma_ts(tmem + C::S(s), qa, ka, id_s, k > 0);
           }
         mma_done(s_full + s);
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
       const bool valid = r < rows, active = w4 * 32 < rows;  // warps without a row only keep the count
       const int draft = tree_draft(p, row0 + r), qhead = g.head * p.group + row0 + r - draft * p.group;
       // ---- queries, 32 rows at a time: loaded along the rows, staged, and put into tensor memory by the warps that own the rows,
-      // each of the two with half of what is there (bf16: half of the row; e4m3: one number of each pair)
+      // each of the two with half of what is there (bf16: half of the row; e4m3: Qhi, Qlo)
       float fac = 1.f;
       {
         constexpr int LPR = D / 8, kStep = 256 / LPR, kMost = 32 / kStep;  // lanes of a row, rows at a time, loads of a thread
@@ -390,8 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
               uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 #pragma unroll
               for (int o = LPR / 2; o; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
-              // the row's largest number to [2^7, 2^8): a number is then the sum of two e4m3 ones, exactly down to 2^-9 of
-              // the largest and within 2^-17 of it below
+              // the row's largest number to [2^7, 2^8)
               uint32_t e = max(m2 & 0xFFFFu, m2 >> 16) >> 7;
               const bool none = e == 255;     // infinite or NaN: so are the row's results
               e = none ? 134u : max(e, 8u);   // below 2^-119 the factor is its smallest, 2^-126
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
                 const float a = bf16lo_to_f32(w[i]) * inv, b = bf16hi_to_f32(w[i]) * inv;
                 hi[i] = none ? 0x7F7Fu : e4m3x2(a, b);
                 const uint32_t back = e4m3x2_to_f16x2(hi[i]);
-                lo[i] = e4m3x2(a - f16_to_f32((uint16_t)back), b - f16_to_f32((uint16_t)(back >> 16)));
+                lo[i] = e5m2x2(a - f16_to_f32((uint16_t)back), b - f16_to_f32((uint16_t)(back >> 16)));
               }
               if (l == 0) row_fac[q] = __uint_as_float((e - 7u) << 23);
               const int ch = l >> 1, at = (l & 1) * 8;

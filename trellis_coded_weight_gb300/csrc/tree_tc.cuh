@@ -37,7 +37,7 @@ __device__ __forceinline__ void named_sync(int id, int count) { asm volatile("ba
   }
 TRELLIS_TREE_MMA(mma_ss, "f16", uint64_t, "%1", "l")           // 16-bit inputs, both bf16 or both fp16 as the descriptor says
 TRELLIS_TREE_MMA(mma_ts, "f16", uint32_t, "[%1]", "r")
-TRELLIS_TREE_MMA(mma_ts_e4m3, "f8f6f4", uint32_t, "[%1]", "r")  // e4m3 inputs
+TRELLIS_TREE_MMA(mma_ts_f8, "f8f6f4", uint32_t, "[%1]", "r")  // 8-bit inputs, each of the kind that the descriptor says
 #undef TRELLIS_TREE_MMA
 // The mbarrier receives one arrival once the products issued so far have completed.
 __device__ __forceinline__ void mma_done(uint64_t* bar) {
