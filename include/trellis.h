@@ -485,7 +485,7 @@ int trellis_cache_commit(const trellis_cache_t *cache, const int32_t *table, con
  *   workspace: as for trellis_matvec_axis0, of at least
  *   trellis_logprobs_workspace_bytes bytes.
  * 1 <= vocab <= 2^24, 0 <= cands <= 64, 0 <= top_k <= min(32, vocab),
- * temperature > 0, n <= 2^20.
+ * temperature > 0 (and log2(e) / temperature finite in fp32), n <= 2^20.
  */
 int trellis_token_logprobs(const void *logits, int dtype, int64_t row_stride, const int32_t *tokens, int n, int vocab,
                            int cands, int top_k, float temperature, float *logprobs, float *lse, float *entropy,

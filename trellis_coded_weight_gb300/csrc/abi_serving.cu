@@ -190,7 +190,7 @@ int trellis_token_logprobs(const void* logits, int dtype, int64_t row_stride, co
   if (dtype != TRELLIS_BF16 && dtype != TRELLIS_F32) return TRELLIS_ESHAPE;
   if (vocab < 1 || vocab > (1 << 24) || cands < 0 || cands > trellis::kMaxCands || top_k < 0 ||
       top_k > trellis::kMaxTop || top_k > vocab || !(temperature > 0.f) || !std::isfinite(temperature) ||
-      !std::isfinite(1.f / temperature))
+      !std::isfinite(trellis::kLog2e / temperature))  // the exponentials' factor
     return TRELLIS_ESHAPE;
   if (n > 1 && (row_stride < vocab || row_stride > (int64_t)1 << 40)) return TRELLIS_ESHAPE;
   if (n == 0) return TRELLIS_OK;

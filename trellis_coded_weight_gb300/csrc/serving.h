@@ -55,5 +55,6 @@ constexpr int kTreeMaxBatch = 1024;
 constexpr int kForkMaxPairs = 1024;
 constexpr int kMaxCands = 64;
 constexpr int kMaxTop = 32;
+constexpr float kLog2e = 1.44269504088896341f;
 
 }  // namespace trellis

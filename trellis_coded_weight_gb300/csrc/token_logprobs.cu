@@ -37,7 +37,6 @@ constexpr int kMaxSplits = 64;
 constexpr int kCounters = 4096;    // rows that may be split
 constexpr int kGroupThreads = 4;   // threads of one of the 64 maxima
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kFar = -16384.f;  // 2^kFar is 0: stands in for minus infinity where it would be multiplied
 
 struct Params {

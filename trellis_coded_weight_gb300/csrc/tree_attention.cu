@@ -46,7 +46,6 @@ constexpr int kTile = 64;  // keys per step
 // an item's start and end, in steps (64 x 1 token, ragged to 2048 keys, 32/8 heads of 128: 97 us without, 56, 57 with 12)
 constexpr int kExtra = 6;
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
