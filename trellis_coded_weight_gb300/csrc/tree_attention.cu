@@ -109,6 +109,7 @@ struct Cfg {
   static constexpr int Fixed = QBytes + Join + kRows * 8 + kRows * 4 + (int)sizeof(TreeMap) + 256;
   static constexpr int Fit = (227 * 1024 - 1024 - Fixed) / Stage;
   static constexpr int Stages = Fit > 8 ? 8 : Fit;
+  static_assert(D <= 128, "heads of 256 are those of tree_attention_tc1.cu");
   static_assert(Stages >= 2, "two tiles in flight at least");
   static constexpr int Smem = 1024 + Stages * Stage + Fixed;
 };
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-            constexpr unsigned kLanes = LPR == 32 ? 0xFFFFFFFFu : (1u << LPR) - 1;
+            constexpr unsigned kLanes = (1u << LPR) - 1;
 #pragma unroll
             for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kLanes << (lane / LPR * LPR), m, o));
             // the row's largest exponent to 0: fp16 then keeps every bf16 number within 2^-14 of the largest exactly.  At the
@@ -639,7 +640,7 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
          copy.bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  p.pool = reinterpret_cast<const uint16_t*>(pool);
+  p.pool = pool;
   if (tc) return launch_tree_tc(map, p, c, tree_ctas(), st);
   if (tc1) return launch_tree_tc1(map, p, c, tree_ctas(), st);
   if (f8) return c.head_dim == 64 ? launch_d<64, true>(map, p, st) : launch_d<128, true>(map, p, st);

@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(seen >> j & 1) || at < 0 || at >= n * kTile) continue;
             int page = __ldg(p.table + (int64_t)g.b * p.width + (pos >> p.page_shift));
             page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
-            const uint16_t* vr = p.pool + (((int64_t)((page * 2 + 1) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
+            const uint16_t* vr = static_cast<const uint16_t*>(p.pool) + (((int64_t)((page * 2 + 1) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               const uint16_t b = vr[k];

@@ -621,9 +621,9 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               if constexpr (F8) {
-                if ((reinterpret_cast<const uint8_t*>(p.pool)[first + k] & 0x7Fu) == 0x7Fu) v[k] = __int_as_float(0x7FC00000);
+                if ((static_cast<const uint8_t*>(p.pool)[first + k] & 0x7Fu) == 0x7Fu) v[k] = __int_as_float(0x7FC00000);
               } else {
-                const uint16_t b = p.pool[first + k];
+                const uint16_t b = static_cast<const uint16_t*>(p.pool)[first + k];
                 if ((b & 0x7F80u) == 0x7F80u) v[k] += bf16_to_f32(b);
               }
             }

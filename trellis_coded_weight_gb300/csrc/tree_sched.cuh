@@ -27,7 +27,7 @@ struct TreeParams {
   const int32_t *table, *prefix, *q_start;
   const uint64_t* mask;
   const float* scales;  // [2][hkv] of the layer, or null
-  const uint16_t* pool; // the layer's pages (bf16 ones)
+  const void* pool;     // the layer's pages, bf16 or e4m3
   int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (tree_item), or none
   float* part;          // two slots per thread block
   int64_t q_stride, out_stride;
