@@ -426,7 +426,10 @@ int trellis_cache_copy(const trellis_cache_t *cache, const int32_t *src, const i
  * that was free before the call.
  *   status [pairs] int32: 0 done; 1 no room (not enough free pages, or more
  *   pages than the row's width: c is left empty, or as it was if it is its own
- *   parent); 2 a row, length or page out of range (nothing done).
+ *   parent); 2 a row, length or page out of range (nothing done).  Free pages
+ *   are claimed in the order of the pairs: once one finds too few, no later
+ *   pair of the call gets fresh pages, also if fewer would do for it.  (Pairs
+ *   that need more than the row's width claim none.)
  *   table [rows][width], lens [rows], refs [pages] int32, updated in place
  *   workspace: at least trellis_cache_workspace_bytes bytes, no initial state.
  * pairs <= 1024; no row may be a child twice.
@@ -456,7 +459,7 @@ size_t trellis_cache_workspace_bytes(const trellis_cache_t *cache, int pairs, in
  * every layer, and lens[b] = prefix[b] + accepted[b].
  *   table [batch][width], prefix, accepted, lens [batch], path [batch][max_tokens] int32
  *   path[b] lists the accepted drafts in ascending order, so path[b][i] >= i;
- *   an entry that does not, or whose pages are out of range, is skipped.
+ *   an entry out of order, or whose pages are out of range, is skipped.
  *   accepted is clamped to [0, max_tokens].  lens may be prefix.
  * max_tokens <= 64.
  */

@@ -672,8 +672,8 @@ def cache_copy(cache: PagedCache, src, dst):
 def cache_fork(cache: PagedCache, table, lens, refs, parent, child, status, workspace, room: int = 0):
     """Forks, grows and frees rows of the page table in place (all int32): row child[i] becomes a copy of row
     parent[i], sharing the pages its length fills and copying the partly filled one, with room for `room` more
-    positions; parent[i] = child[i] only adds the room, parent[i] = -1 frees the row.  status[i]: 0 done, 1 no room,
-    2 out of range."""
+    positions; parent[i] = child[i] only adds the room, parent[i] = -1 frees the row.  status[i]: 0 done, 1 no room (and
+    none for later pairs of the call that need fresh pages), 2 out of range."""
     rows, width = table.shape
     pairs, index = parent.shape[0], cache.index
     if not (table.dtype is _I32 and lens.dtype is _I32 and refs.dtype is _I32 and parent.dtype is _I32 and child.dtype is _I32 and

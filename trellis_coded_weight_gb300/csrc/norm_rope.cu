@@ -9,8 +9,9 @@
 // those lanes, a pair that spans half a rotation is one shuffle away, an interleaved pair is in one lane.  Nothing is
 // staged.  A group of lanes has a share of one token's heads -- queries, then keys, then values, each in a loop of its own
 // with its weights in registers -- and keeps the cosines and sines of its lanes.
-// Bound: launch latency for a few tokens (one of 56 heads of 128: 2.1 us); beyond, HBM and the issue of instructions are close:
-// 4099 tokens of 20 heads of 256 into e4m3 take 21 us, 3.9 TB/s (a general loop over all kinds of heads took three times the
+// Bound: launch latency for a few tokens (one of 56 heads of 128: 2.2 us); beyond, the latency of loads: 4099 tokens of 20 heads of
+// 256 into e4m3 take 21 us, 3.9 TB/s, instructions issue in 42 % of the cycles, and two thirds of the warps' time is spent waiting
+// for numbers from memory, two heads of which are in flight (a general loop over all kinds of heads took three times the
 // instructions, and 25 us).
 #include "common.cuh"
 #include "launch.h"
@@ -185,7 +186,9 @@ cudaError_t launch_d(Params p, int interleaved, cudaStream_t st) {
   constexpr int GROUPS = kThreads / (D / 8);
   const int heads = p.hq + 2 * p.hkv;
   // A token's heads go to as many groups of lanes as fill the GPU once over all tokens: several heads each for many
-  // tokens, one for a few.  (Rounding up instead, into a second wave, measured 35 us against 28.)
+  // tokens, one for a few.  (Rounding up instead, into a second wave, measured 35 us against 28.)  Rounded down, groups idle just
+  // past a whole number of shares, and past one group for each token a second wave begins: 20 heads of 256 into e4m3, 2432 tokens
+  // 13.2 us, 2433 19.7, 4864 23.3, 4865 33.8; 56 heads of 128, 4864 tokens 29.9, 4865 45.3.
   const int64_t groups = (int64_t)kPerSM * device_sm_count() * GROUPS;
   const int64_t split = groups / p.t.n;
   p.split = (int)(split < 1 ? 1 : split > heads ? heads : split);

@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         any = true;
-        // ---- weights, over the scores
+        // ---- weights, over the scores; 16 bits as in tree_attention.cu: bf16, the type of the values they are multiplied with
         const float ms = m == -INFINITY ? 0.f : -m;
         float2 sum = make_float2(0.f, 0.f);
         const auto weigh = [&](const uint32_t (&v)[32], int w) {

@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
             l *= ex2(used - m);
             used = m;
           }
-          // ---- weights, over the scores
+          // ---- weights, over the scores; 16 bits as in tree_attention.cu, of the type that the values have here
           const float ms = m == -INFINITY ? C::Lift : C::Lift - m;
           float2 sum = make_float2(0.f, 0.f);
           const auto weigh = [&](const uint32_t (&v)[32], int w) {

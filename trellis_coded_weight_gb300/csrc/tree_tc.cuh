@@ -1,5 +1,9 @@
 // tree_tc.cuh -- what the tree attention kernels on the 5th-generation tensor cores share (tree_attention_tc.cu,
 // tree_attention_tc1.cu): the forms of the tensor-memory instructions that only they use, and the order of their copies.
+//
+// The softmax in one pass with a running maximum is that of Milakov and Gimelshein, "Online normalizer calculation for softmax"
+// (2018).  Weights that lie in tensor memory over their scores, and a maximum that is moved only when it has grown far, are
+// published too, for attention on this hardware.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
