@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(kThreads, kPerSM) norm_rope_kernel(const Param
   if (tok >= (uint32_t)p.t.n) return;
   int h = (int)(gid - tok * (uint32_t)split);
 
-  const int pos = __ldg(p.t.positions + tok);
-  const int64_t slot = __ldg(p.t.slots + tok);
+  const int pos = p.t.positions[tok];
+  const int64_t slot = p.t.slots[tok];
   const uint16_t* const qb = p.t.q + tok * p.t.q_stride + 8 * l;
   const uint16_t* const kb = p.t.k + tok * p.t.k_stride + 8 * l;
   const uint16_t* const vb = p.t.v + tok * p.t.v_stride + 8 * l;

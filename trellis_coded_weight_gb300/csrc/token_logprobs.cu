@@ -143,7 +143,7 @@ struct Row {
   __device__ __forceinline__ int col(int v) const { return v * Vec<T>::N - skew; }
   __device__ __forceinline__ uint4 load(int v) const {
     const int c = col(v);
-    if (c >= 0 && c + Vec<T>::N <= vocab) return __ldg(reinterpret_cast<const uint4*>(x + c));
+    if (c >= 0 && c + Vec<T>::N <= vocab) return *reinterpret_cast<const uint4*>(x + c);
     return Vec<T>::edge(x, c, vocab);
   }
 };

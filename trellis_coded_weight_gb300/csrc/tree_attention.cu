@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
           uint4 u = make_uint4(0, 0, 0, 0);
           if (r < rows)
-            u = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
-                                                     (int64_t)(g.head * p.group + hh) * D + 8 * l));
+            u = *reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride +
+                                                (int64_t)(g.head * p.group + hh) * D + 8 * l);
           float fac = 1.f;
           if constexpr (F8) {
             float x[8] = {bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y),
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           *reinterpret_cast<uint4*>(sq + r * (D * 2) + ((l ^ (r & 7)) << 4)) = u;
           if (l == 0) {
             row_fac[r] = fac;
-            row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
+            row_mask[r] = r >= rows ? 0ull : p.mask ? p.mask[g.seq.start + d] : d >= 63 ? ~0ull : (2ull << d) - 1;
           }
         }
       }

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kMost; ++k) {
             const int r = r0 + k * kStep, d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
             u[k] = make_uint4(0, 0, 0, 0);
-            if (r < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
+            if (r < rows) u[k] = *reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l);
           }
 #pragma unroll
           for (int k = 0; k < kMost; ++k) {
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (threadIdx.x < qrows) {
           const int r = threadIdx.x, d = tree_draft(p, row0 + r);
-          row_mask[r] = r >= rows ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + d) : d >= 63 ? ~0ull : (2ull << d) - 1;
+          row_mask[r] = r >= rows ? 0ull : p.mask ? p.mask[g.seq.start + d] : d >= 63 ? ~0ull : (2ull << d) - 1;
         }
         tc::fence_proxy_async_smem();
         named_sync(1, 256);  // masks
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < g.seq.count; ++j) {
             const int pos = g.seq.prefix + j, at = pos - g.tile0 * kTile;
             if (!(seen >> j & 1) || at < 0 || at >= n * kTile) continue;
-            int page = __ldg(p.table + (int64_t)g.b * p.width + (pos >> p.page_shift));
+            int page = p.table[(int64_t)g.b * p.width + (pos >> p.page_shift)];
             page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
             const uint16_t* vr = static_cast<const uint16_t*>(p.pool) + (((int64_t)((page * 2 + 1) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
 #pragma unroll

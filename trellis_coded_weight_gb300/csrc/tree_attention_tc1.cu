@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           for (int k = 0; k < kMost; ++k) {
             const int q = rb + k * kStep + threadIdx.x / LPR, d = tree_draft(p, row0 + q), hh = row0 + q - d * p.group;
             u[k] = make_uint4(0, 0, 0, 0);
-            if (q < rows) u[k] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l));
+            if (q < rows) u[k] = *reinterpret_cast<const uint4*>(p.q + (g.seq.start + d) * p.q_stride + (int64_t)(g.head * p.group + hh) * D + 8 * l);
           }
           if (rb > 0) named_sync(1, 256);  // the rows before have been taken
 #pragma unroll
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           }
         }
       }
-      const uint64_t seen = !valid ? 0ull : p.mask ? __ldg(p.mask + g.seq.start + draft) : draft >= 63 ? ~0ull : (2ull << draft) - 1;
+      const uint64_t seen = !valid ? 0ull : p.mask ? p.mask[g.seq.start + draft] : draft >= 63 ? ~0ull : (2ull << draft) - 1;
       // this thread is past the segment before, and so is all that it read of it
       tc::fence_before_sync();
       __syncwarp();
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<D, F8>::Threads, 1)
           for (int j = 0; j < g.seq.count; ++j) {
             const int pos = g.seq.prefix + j, at = pos - g.tile0 * kTile;
             if (!(seen >> j & 1) || at < 0 || at >= n * kTile) continue;
-            int page = __ldg(p.table + (int64_t)g.b * p.width + (pos >> p.page_shift));
+            int page = p.table[(int64_t)g.b * p.width + (pos >> p.page_shift)];
             page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
             const int64_t first = (((int64_t)((page * 2 + 1) * p.hkv + g.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
 #pragma unroll

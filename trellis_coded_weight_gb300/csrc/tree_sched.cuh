@@ -44,14 +44,14 @@ struct TreeSeq {
 };
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   TreeSeq s;
-  int a = __ldg(p.q_start + b), z = __ldg(p.q_start + b + 1);
+  int a = __ldcg(p.q_start + b), z = __ldcg(p.q_start + b + 1);
   a = a < 0 ? 0 : a > p.n ? p.n : a;
   z = z < a ? a : z > p.n ? p.n : z;
   const int room = p.width << p.page_shift;
   int c = z - a;
   c = c > p.max_tokens ? p.max_tokens : c;
   c = c > room ? room : c;
-  int pre = __ldg(p.prefix + b);
+  int pre = __ldcg(p.prefix + b);
   pre = pre < 0 ? 0 : pre > room - c ? room - c : pre;
   s.start = a;
   s.count = c;
@@ -197,7 +197,7 @@ struct TreePages {
   }
   __device__ __forceinline__ int load(int w) const {
     const int pos = first + (32 * w + lane) * box;
-    return pos < len ? __ldg(row + (pos >> shift)) : 0;
+    return pos < len ? row[pos >> shift] : 0;
   }
   // Page of this lane's box of tile t (lanes below `per`).  Tiles come in order, or up to two behind the last one.
   __device__ __forceinline__ int at(int t) {
