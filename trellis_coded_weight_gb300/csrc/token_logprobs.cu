@@ -18,7 +18,7 @@
 //
 // A row is split over blocks where there are few rows; the last block to arrive joins the parts in their order, so
 // results do not depend on timing.  Bound: latency for a row (1 x 50257 bf16, 5 alternatives: 7.7 us); for many rows the issue of the
-// exponentials and sums, and the tail of alternatives that every block has: 61 x 128256 fp32 13.0 us (2.4 TB/s),
+// exponentials and sums, and the tail of alternatives that every block has: 61 x 128256 fp32 12.9 us (2.4 TB/s),
 // 256 x 151936 bf16 with 20 alternatives 28 us (2.8 TB/s).
 #include "common.cuh"
 #include "launch.h"

@@ -22,7 +22,7 @@
 // registers; its queries are fp16 too, each row scaled by a power of two.
 //
 // Bound: HBM (1 x 131072 keys, 32/8 heads of 128, one token: 86 us, 6.2 TB/s), with e4m3 the latency of the conversions in four
-// warps (71 us, 3.8 TB/s; a second group of four warps that takes every other tile: 62, but 61 us for 55 on a ragged batch of
+// warps (72 us, 3.7 TB/s; a second group of four warps that takes every other tile: 62, but 61 us for 55 on a ragged batch of
 // 64), and for short contexts that of two launches and a segment's start and end (1 x 4096 keys, 40/8 heads: 10.6 us).
 #include <cstring>
 #include <cuda.h>
