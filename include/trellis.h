@@ -78,7 +78,7 @@ enum trellis_status {
   TRELLIS_ESHAPE = -9      /* unsupported or inconsistent sizes, strides or types of a serving call */
 };
 
-/* Version of this interface (major*100 + minor): 102. */
+/* Version of this interface (major*100 + minor): 103. */
 int trellis_abi_version(void);
 
 /* Static description of a status code; never NULL. */
@@ -403,6 +403,35 @@ int trellis_tree_attention(const uint16_t *q, int64_t q_stride, const trellis_ca
 size_t trellis_tree_workspace_bytes(const trellis_cache_t *cache, int batch, int max_tokens, int q_heads);
 
 /*
+ * trellis_prompt_attention -- causal attention of the new tokens of whole
+ * prompts, or of their next chunks, over their cached prefixes and over
+ * themselves.  Takes what trellis_tree_attention takes, without a mask and
+ * with up to 2^20 tokens a sequence: token j of sequence b is at position
+ * prefix[b] + j of the cache (written there before) and sees positions
+ * 0 .. prefix[b] + j.  Sequences of any lengths, single tokens among them,
+ * are packed one behind the other.  For token i and query head h:
+ *   out = sum_p softmax_p(scale * q.k_p) v_p      lse = log sum_p exp(scale * q.k_p)
+ * Scores, softmax statistics and sums are fp32; the softmax weights are
+ * rounded to bf16 for the products with the values (their sum is not); one
+ * rounding to bf16 at the end.  Numbers of an e4m3 cache are taken exactly.
+ * A token whose scores are all minus infinity gets zeros and an lse of minus
+ * infinity.  What a token does not see (later tokens, rows past a sequence's
+ * end) does not reach its result, whatever its bits are; a query with a
+ * number that is not finite has an undefined result and touches no other.
+ *   d->mask must be NULL; 1 <= d->max_tokens <= 2^20.  The other arguments,
+ *   the clamping of lengths and the errors are those of trellis_tree_attention
+ *   (out may not overlap q).
+ *   workspace: at least trellis_prompt_workspace_bytes bytes, no initial state.
+ */
+int trellis_prompt_attention(const uint16_t *q, int64_t q_stride, const trellis_cache_t *cache, int layer,
+                             const trellis_drafts_t *d, int q_heads, float scale, uint16_t *out, int64_t out_stride,
+                             float *lse, void *workspace, size_t workspace_bytes, trellis_stream_t stream);
+
+/* Bytes of workspace trellis_prompt_attention needs for (cache, q_heads) on
+ * the current device, whatever the batch; 0 if they are unsupported. */
+size_t trellis_prompt_workspace_bytes(const trellis_cache_t *cache, int q_heads);
+
+/*
  * trellis_cache_copy -- copies pages src[i] to dst[i] in every layer.
  *   src, dst [n] int32; a pair with an index outside the pool is skipped.  No
  *   page may be both a source and a destination, or a destination twice.
@@ -466,6 +495,57 @@ size_t trellis_cache_workspace_bytes(const trellis_cache_t *cache, int pairs, in
 int trellis_cache_commit(const trellis_cache_t *cache, const int32_t *table, const int32_t *prefix,
                          const int32_t *path, const int32_t *accepted, int32_t *lens, int batch, int width,
                          int max_tokens, trellis_stream_t stream);
+
+/*
+ * Low-rank adapters of one projection: adapter i adds
+ *   scales[i] * B_i (A_i x)
+ * to the projection's output, with A_i the first ranks[i] rows of a[i] and B_i
+ * the first ranks[i] columns of b[i]; the others are not part of it, whatever
+ * their bits.
+ */
+typedef struct trellis_adapters {
+  const uint16_t *a;    /* [count][max_rank][in] bf16 */
+  const uint16_t *b;    /* [count][out][max_rank] bf16 */
+  const int32_t *ranks; /* [count], clamped to 0 .. max_rank; NULL: all max_rank */
+  const float *scales;  /* [count]; NULL: all 1 */
+  int64_t in, out;      /* multiples of 8, 8 .. 2^20 */
+  int32_t count;        /* 1 .. 2^16 */
+  int32_t max_rank;     /* a multiple of 8, 8 .. 128 */
+} trellis_adapters_t;
+
+/*
+ * trellis_adapter_plan -- groups a step's tokens by adapter, for
+ * trellis_adapter_add.  Made once for a step, on the device, it serves every
+ * projection of every layer.
+ *   adapter [batch] int32: the adapter of each sequence, negative for none
+ *   q_start [batch + 1] int32: sequence b's tokens are q_start[b] ..
+ *   q_start[b+1]-1 (clamped to [0, n]; a start below an earlier one counts as
+ *   that one)
+ *   plan: at least trellis_adapter_plan_bytes(batch, n) bytes, no initial state.
+ * batch <= 1024, n <= 2^20.
+ */
+int trellis_adapter_plan(const int32_t *adapter, const int32_t *q_start, int batch, int n, void *plan,
+                         size_t plan_bytes, trellis_stream_t stream);
+
+/* Bytes of a plan; 0 if batch or n is unsupported (or 0). */
+size_t trellis_adapter_plan_bytes(int batch, int n);
+
+/*
+ * trellis_adapter_add -- adds the tokens' adapters to a projection's output:
+ *   out[t] = bf16( y[t] + scales[i] * B_i (A_i x[t]) ),  i = token t's adapter
+ * A_i x[t] is accumulated in fp32 and enters the second product as the sum of
+ * two bf16 numbers (to within 2^-16 of its size); sums are fp32, with one
+ * rounding at the end.
+ * Tokens without an adapter (none, an index outside the adapters, or of rank
+ * 0) get y[t] as it is; tokens of no sequence are left as they are.
+ * Results do not depend on the other tokens' adapters or numbers.
+ *   x [n][in], y and out [n][out] bf16, strides from token to token in
+ *   elements, multiples of 8; out may be y (with the same stride).
+ *   plan: as left by trellis_adapter_plan with the same batch and n.
+ */
+int trellis_adapter_add(const uint16_t *x, int64_t x_stride, const uint16_t *y, int64_t y_stride, uint16_t *out,
+                        int64_t out_stride, const trellis_adapters_t *adapters, const void *plan, size_t plan_bytes,
+                        int batch, int n, trellis_stream_t stream);
 
 /*
  * trellis_token_logprobs -- log probabilities of given tokens, with the

@@ -35,7 +35,8 @@ EXPORTS = ("trellis_abi_version", "trellis_status_string", "trellis_check_geom",
            "trellis_set_wait_limit", "trellis_matvec_axis1_host", "trellis_check_cache", "trellis_qk_norm_rope_append",
            "trellis_tree_attention", "trellis_tree_workspace_bytes", "trellis_cache_copy", "trellis_cache_fork",
            "trellis_cache_compact", "trellis_cache_workspace_bytes", "trellis_cache_commit", "trellis_token_logprobs",
-           "trellis_logprobs_workspace_bytes")
+           "trellis_logprobs_workspace_bytes", "trellis_prompt_attention", "trellis_prompt_workspace_bytes",
+           "trellis_adapter_plan", "trellis_adapter_plan_bytes", "trellis_adapter_add")
 
 
 class TrellisGeom(ctypes.Structure):
@@ -379,7 +380,7 @@ class MlpDecodeGraph:
         return self.out
 
 
-# ---- The rest of a decoding step: paged cache, norms with rotation, tree attention, token log probabilities ----
+# ---- The rest of a step: paged cache, norms with rotation, attention of trees and prompts, adapters, token log probabilities ----
 
 TRELLIS_BF16, TRELLIS_E4M3, TRELLIS_F32 = 0, 1, 2
 
@@ -404,6 +405,12 @@ class TrellisDrafts(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
                 ("mask", ctypes.c_void_p), ("batch", ctypes.c_int32), ("width", ctypes.c_int32), ("n", ctypes.c_int32),
                 ("max_tokens", ctypes.c_int32)]
+
+
+class TrellisAdapters(ctypes.Structure):
+    """Mirror of trellis_adapters_t."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("in_", ctypes.c_int64), ("out", ctypes.c_int64), ("count", ctypes.c_int32), ("max_rank", ctypes.c_int32)]
 
 
 _BF16, _I32, _I64, _FP32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
@@ -486,6 +493,13 @@ def _serving_lib():
                 ("trellis_tree_attention", i32, [vp, i64, cache, i32, ctypes.POINTER(TrellisDrafts), i32, f32, vp, i64,
                                                  vp, vp, sz, vp]),
                 ("trellis_tree_workspace_bytes", sz, [cache, i32, i32, i32]),
+                ("trellis_prompt_attention", i32, [vp, i64, cache, i32, ctypes.POINTER(TrellisDrafts), i32, f32, vp, i64,
+                                                   vp, vp, sz, vp]),
+                ("trellis_prompt_workspace_bytes", sz, [cache, i32]),
+                ("trellis_adapter_plan", i32, [vp, vp, i32, i32, vp, sz, vp]),
+                ("trellis_adapter_plan_bytes", sz, [i32, i32]),
+                ("trellis_adapter_add", i32, [vp, i64, vp, i64, vp, i64, ctypes.POINTER(TrellisAdapters), vp, sz, i32, i32,
+                                              vp]),
                 ("trellis_cache_copy", i32, [cache, vp, vp, i32, vp]),
                 ("trellis_cache_fork", i32, [cache, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]),
                 ("trellis_cache_compact", i32, [cache, vp, vp, vp, vp, i32, i32, vp, sz, vp]),
@@ -586,7 +600,7 @@ class DraftBatch:
     """One step's sequences and drafted tokens (trellis_drafts_t), shared by the step's layers.
 
     table [batch, width] int32 pages;  prefix [batch] int32 positions before the drafts;  q_start [batch + 1] int32
-    (sequence b's drafts are tokens q_start[b] .. q_start[b+1] - 1);  max_tokens: most drafts of a sequence (<= 64);
+    (sequence b's drafts are tokens q_start[b] .. q_start[b+1] - 1);  max_tokens: most drafts of a sequence (<= 64; new tokens of a prompt: <= 2^20);
     mask [n] int64: bit j set where the token sees draft j of its sequence (None: drafts 0 .. itself, then n is
     needed).  Keeps the tensors; their contents are read by each call."""
 
@@ -626,6 +640,26 @@ def tree_attention(q, cache: PagedCache, layer: int, batch: DraftBatch, workspac
     """Attention of the drafted tokens q [n, q_heads, head_dim] over their sequences' cached prefixes and the drafts
     their masks name (written to the cache before).  scale defaults to head_dim ** -0.5.  Returns (out, lse), lse
     [n, q_heads] fp32 being the log of each softmax sum; lse=False leaves it out."""
+    return _attention("trellis_tree_attention", q, cache, layer, batch, workspace, scale, out, lse)
+
+
+def new_prompt_workspace(cache: PagedCache, batch: DraftBatch, q_heads: int) -> torch.Tensor:
+    """A workspace for prompt_attention (reusable for calls of any batch with this cache's and q_heads' sizes, one at a time)."""
+    with _on(cache.pool):
+        return _workspace(int(_serving_lib().trellis_prompt_workspace_bytes(cache._ref, q_heads)), cache.device,
+                          "prompt_attention")
+
+
+def prompt_attention(q, cache: PagedCache, layer: int, batch: DraftBatch, workspace, scale: float = None, out=None, lse=None):
+    """Causal attention of the new tokens q [n, q_heads, head_dim] of whole prompts, or of their next chunks, over their
+    sequences' cached prefixes and the new tokens up to their own (written to the cache before).  The batch has no mask
+    and up to 2^20 tokens a sequence.  scale, out, lse and the result as for tree_attention; out may not overlap q."""
+    if batch.mask is not None:
+        raise ValueError("prompt_attention takes a batch without a mask")
+    return _attention("trellis_prompt_attention", q, cache, layer, batch, workspace, scale, out, lse)
+
+
+def _attention(fn, q, cache, layer, batch, workspace, scale, out, lse):
     n, heads, dim = shape = q.shape
     index = cache.index
     if out is None:
@@ -646,7 +680,7 @@ def tree_attention(q, cache: PagedCache, layer: int, batch: DraftBatch, workspac
             _same_device(cache.device, lse=lse)
         _req_workspace(workspace)
         _same_device(cache.device, q=q, out=out, workspace=workspace, batch=batch)
-    _call("trellis_tree_attention", index, q.data_ptr(), qs[0], cache._ref, layer, batch._ref, heads,
+    _call(fn, index, q.data_ptr(), qs[0], cache._ref, layer, batch._ref, heads,
           dim ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], None if lse is False else lse.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, (None if lse is False else lse)
@@ -737,6 +771,84 @@ def cache_commit(cache: PagedCache, table, prefix, path, accepted, out_lens=None
     _call("trellis_cache_commit", index, cache._ref, table.data_ptr(), prefix.data_ptr(), path.data_ptr(),
           accepted.data_ptr(), out_lens.data_ptr(), batch, width, tokens)
     return out_lens
+
+
+class Adapters:
+    """Low-rank adapters of one projection (trellis_adapters_t): a [count, max_rank, in] and b [count, out, max_rank] bf16,
+    ranks [count] int32 (None: all max_rank), scales [count] fp32 (None: all 1).  Keeps the tensors."""
+
+    def __init__(self, a, b, ranks=None, scales=None):
+        if a.dim() != 3 or b.dim() != 3:
+            raise ValueError("a must be [count, max_rank, in] and b [count, out, max_rank]")
+        (count, rank, in_), out = a.shape, b.shape[1]
+        _req_rows(a, "a", _BF16, (count, rank, in_))
+        _req_rows(b, "b", _BF16, (count, out, rank))
+        kept = dict(b=b)
+        if ranks is not None:
+            _req_rows(ranks, "ranks", _I32, (count,))
+            kept["ranks"] = ranks
+        if scales is not None:
+            _req_rows(scales, "scales", _FP32, (count,))
+            kept["scales"] = scales
+        _same_device(a.device, **kept)
+        self.count, self.max_rank, self.in_features, self.out_features = count, rank, in_, out
+        self.device, self.index, self._kept = a.device, a.get_device(), (a, b, ranks, scales)
+        self._c = TrellisAdapters(a.data_ptr(), b.data_ptr(), ranks.data_ptr() if ranks is not None else None,
+                                  scales.data_ptr() if scales is not None else None, in_, out, count, rank)
+        self._ref = ctypes.byref(self._c)
+
+
+class AdapterPlan:
+    """The tokens of one step by adapter, shared by the step's projections and layers: adapter [batch] int32 (negative:
+    none) and q_start [batch + 1] int32 of its sequences, n tokens in all.  Keeps the tensors; adapter_plan reads their
+    contents."""
+
+    def __init__(self, adapter, q_start, n: int):
+        batch = adapter.shape[0]
+        _req_rows(adapter, "adapter", _I32, (batch,))
+        _req_rows(q_start, "q_start", _I32, (batch + 1,))
+        _same_device(adapter.device, q_start=q_start)
+        self.adapter, self.q_start, self.batch, self.n = adapter, q_start, batch, n
+        self.device, self.index = adapter.device, adapter.get_device()
+        if batch and n:
+            self.plan = _workspace(int(_serving_lib().trellis_adapter_plan_bytes(batch, n)), adapter.device, "adapter_plan")
+        else:
+            self.plan = torch.zeros(4, dtype=_I32, device=adapter.device)
+        self._bytes = self.plan.numel() * 4
+
+
+def adapter_plan(plan: AdapterPlan) -> AdapterPlan:
+    """Groups the step's tokens by adapter; call it again when the contents of adapter or q_start have changed."""
+    _call("trellis_adapter_plan", plan.index, plan.adapter.data_ptr(), plan.q_start.data_ptr(), plan.batch, plan.n,
+          plan.plan.data_ptr(), plan._bytes)
+    return plan
+
+
+def adapter_add(x, y, adapters: Adapters, plan: AdapterPlan, out=None):
+    """out = y + scale * B (A x) per token, with the token's adapter by the plan (made by adapter_plan before): x [n, in] the
+    projection's input, y [n, out] its output, rows may be apart.  out defaults to y, in place.  Tokens without an adapter
+    get y; tokens of no sequence are left as they are.  Returns out."""
+    if out is None:
+        out = y
+    n, index = plan.n, plan.index
+    wide, narrow = (n, adapters.out_features), (n, adapters.in_features)
+    xs, ys, os_ = x.stride(), y.stride(), out.stride()
+    if not (x.dtype is _BF16 and y.dtype is _BF16 and out.dtype is _BF16 and x.shape == narrow and y.shape == wide and
+            out.shape == wide and xs[1] == 1 and ys[1] == 1 and os_[1] == 1 and
+            x.get_device() == y.get_device() == out.get_device() == adapters.index == index):
+        for t, name, shape in ((x, "x", narrow), (y, "y", wide), (out, "out", wide)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype != _BF16:
+                raise ValueError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+            if t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+            if t.stride(1) != 1:
+                raise ValueError(f"{name}: the numbers of a token must be contiguous")
+        _same_device(plan.device, x=x, y=y, out=out, adapters=adapters)
+    _call("trellis_adapter_add", index, x.data_ptr(), xs[0], y.data_ptr(), ys[0], out.data_ptr(), os_[0], adapters._ref,
+          plan.plan.data_ptr(), plan._bytes, plan.batch, n)
+    return out
 
 
 class TokenLogprobs(NamedTuple):

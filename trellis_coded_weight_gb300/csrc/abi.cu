@@ -20,7 +20,7 @@ using trellis::device_ok;
 
 namespace {
 
-constexpr int kAbiVersion = 102;
+constexpr int kAbiVersion = 103;
 
 int geom_ok(const trellis_geom_t* g) {
   if (!g) return TRELLIS_ENULL;

@@ -105,6 +105,78 @@ int trellis_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_ca
                                                     lse, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t trellis_prompt_workspace_bytes(const trellis_cache_t* cache, int q_heads) {
+  if (cache_ok(cache) != TRELLIS_OK || q_heads < 1 || q_heads > 1024 || q_heads % cache->heads != 0) return 0;
+  return trellis::prompt_workspace_bytes(*cache, q_heads);
+}
+
+int trellis_prompt_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t* cache, int layer,
+                             const trellis_drafts_t* d, int q_heads, float scale, uint16_t* out, int64_t out_stride,
+                             float* lse, void* workspace, size_t workspace_bytes, trellis_stream_t stream) {
+  int st = cache_ok(cache);
+  if (st) return st;
+  if (!d) return TRELLIS_ENULL;
+  if (d->batch < 0 || d->batch > trellis::kTreeMaxBatch || d->n < 0 || d->n > (1 << 20)) return TRELLIS_EM;
+  if (d->mask) return TRELLIS_ESHAPE;
+  if (d->batch == 0 || d->n == 0) return TRELLIS_OK;
+  if (d->max_tokens < 1 || d->max_tokens > trellis::kPromptMaxTokens) return TRELLIS_EM;
+  if (layer < 0 || layer >= cache->layers || q_heads < 1 || q_heads > 1024 || q_heads % cache->heads != 0 ||
+      d->width < 1 || (int64_t)d->width * cache->page_size > (1 << 30) || !std::isfinite(scale))
+    return TRELLIS_ESHAPE;
+  const int64_t w = (int64_t)q_heads * cache->head_dim;
+  if (d->n > 1 && (!stride_ok(q_stride, w) || !stride_ok(out_stride, w))) return TRELLIS_ESHAPE;
+  if (!q || !out || !d->table || !d->prefix || !d->q_start) return TRELLIS_ENULL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(d->table) || !aligned16(d->prefix) ||
+      !aligned16(d->q_start))
+    return TRELLIS_EALIGN;
+  if ((st = device_ok())) return st;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < trellis::prompt_workspace_bytes(*cache, q_heads))
+    return TRELLIS_EWORKSPACE;
+  return cuda_status(trellis::launch_prompt_attention(q, q_stride, *cache, layer, *d, q_heads, scale, out, out_stride,
+                                                      lse, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+size_t trellis_adapter_plan_bytes(int batch, int n) {
+  if (batch < 1 || batch > trellis::kAdapterMaxBatch || n < 1 || n > (1 << 20)) return 0;
+  return trellis::adapter_plan_bytes(batch, n);
+}
+
+int trellis_adapter_plan(const int32_t* adapter, const int32_t* q_start, int batch, int n, void* plan,
+                         size_t plan_bytes, trellis_stream_t stream) {
+  if (batch < 0 || batch > trellis::kAdapterMaxBatch || n < 0 || n > (1 << 20)) return TRELLIS_EM;
+  if (batch == 0 || n == 0) return TRELLIS_OK;
+  if (!adapter || !q_start) return TRELLIS_ENULL;
+  if (!aligned16(adapter) || !aligned16(q_start)) return TRELLIS_EALIGN;
+  if (!plan || !aligned16(plan) || plan_bytes < trellis::adapter_plan_bytes(batch, n)) return TRELLIS_EWORKSPACE;
+  const int st = device_ok();
+  if (st) return st;
+  return cuda_status(trellis::launch_adapter_plan(adapter, q_start, batch, n, plan, static_cast<cudaStream_t>(stream)));
+}
+
+int trellis_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, int64_t y_stride, uint16_t* out,
+                        int64_t out_stride, const trellis_adapters_t* ad, const void* plan, size_t plan_bytes,
+                        int batch, int n, trellis_stream_t stream) {
+  if (!ad) return TRELLIS_ENULL;
+  if (batch < 0 || batch > trellis::kAdapterMaxBatch || n < 0 || n > (1 << 20)) return TRELLIS_EM;
+  if (ad->in < 8 || ad->in > (1 << 20) || ad->in % 8 != 0 || ad->out < 8 || ad->out > (1 << 20) || ad->out % 8 != 0 ||
+      ad->count < 1 || ad->count > (1 << 16) || ad->max_rank < 8 || ad->max_rank > trellis::kAdapterMaxRank ||
+      ad->max_rank % 8 != 0)
+    return TRELLIS_ESHAPE;
+  if (n > 1 && (!stride_ok(x_stride, ad->in) || !stride_ok(y_stride, ad->out) || !stride_ok(out_stride, ad->out)))
+    return TRELLIS_ESHAPE;
+  if (n > 1 && out == y && out_stride != y_stride) return TRELLIS_ESHAPE;
+  if (batch == 0 || n == 0) return TRELLIS_OK;
+  if (!x || !y || !out || !ad->a || !ad->b) return TRELLIS_ENULL;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(out) || !aligned16(ad->a) || !aligned16(ad->b) ||
+      !aligned16(ad->ranks) || !aligned16(ad->scales))
+    return TRELLIS_EALIGN;
+  if (!plan || !aligned16(plan) || plan_bytes < trellis::adapter_plan_bytes(batch, n)) return TRELLIS_EWORKSPACE;
+  const int st = device_ok();
+  if (st) return st;
+  return cuda_status(trellis::launch_adapter_add(x, x_stride, y, y_stride, out, out_stride, *ad, plan, batch, n,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
 int trellis_cache_copy(const trellis_cache_t* cache, const int32_t* src, const int32_t* dst, int n,
                        trellis_stream_t stream) {
   int st = cache_ok(cache);

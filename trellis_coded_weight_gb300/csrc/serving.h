@@ -1,5 +1,5 @@
 // serving.h -- internal host-side launchers of the calls around a decoding step's projections (norms with
-// rotation and cache write, tree attention, cache pages, token log probabilities).  Arguments are validated by
+// rotation and cache write, attention of trees and of prompts, adapters, cache pages, token log probabilities).  Arguments are validated by
 // abi_serving.cu before these are called.
 //
 // Their kernels are launched as dependents (pdl.cuh): they may have begun before the call ahead has written what they read, so such
@@ -36,6 +36,18 @@ cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const tre
                                   int64_t out_stride, float* lse, void* workspace, cudaStream_t st);
 size_t tree_workspace_bytes(const trellis_cache_t& c, int batch, int max_tokens, int q_heads);
 
+cudaError_t launch_prompt_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,
+                                    const trellis_drafts_t& d, int q_heads, float scale, uint16_t* out,
+                                    int64_t out_stride, float* lse, void* workspace, cudaStream_t st);
+size_t prompt_workspace_bytes(const trellis_cache_t& c, int q_heads);
+
+cudaError_t launch_adapter_plan(const int32_t* adapter, const int32_t* q_start, int batch, int n, void* plan,
+                                cudaStream_t st);
+size_t adapter_plan_bytes(int batch, int n);
+cudaError_t launch_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, int64_t y_stride, uint16_t* out,
+                               int64_t out_stride, const trellis_adapters_t& ad, const void* plan, int batch, int n,
+                               cudaStream_t st);
+
 cudaError_t launch_cache_copy(const trellis_cache_t& c, const int32_t* src, const int32_t* dst, int n, cudaStream_t st);
 cudaError_t launch_cache_fork(const trellis_cache_t& c, int32_t* table, int32_t* lens, int32_t* refs,
                               const int32_t* parent, const int32_t* child, int32_t* status, int pairs, int rows,
@@ -56,6 +68,9 @@ size_t logprobs_workspace_bytes(int n, int vocab, int top_k);
 
 constexpr int kTreeMaxTokens = 64;  // a draft mask is one 64-bit word
 constexpr int kTreeMaxBatch = 1024;
+constexpr int kPromptMaxTokens = 1 << 20;
+constexpr int kAdapterMaxBatch = 1024;
+constexpr int kAdapterMaxRank = 128;
 constexpr int kForkMaxPairs = 1024;
 constexpr int kMaxCands = 64;
 constexpr int kMaxTop = 32;
