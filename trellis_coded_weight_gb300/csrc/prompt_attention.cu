@@ -1,102 +1,761 @@
-// prompt_attention.cu -- causal attention of whole prompts over the paged cache.
+// prompt_attention.cu -- causal attention of whole prompts over the paged cache, on the 5th-generation tensor cores.
 //
-// A warp per query row goes over the keys that its token sees once, with a running maximum and sum:
-//   m' = max(m, s),  l' = l 2^(m - m') + 2^(s - m'),  o' = o 2^(m - m') + 2^(s - m') v
+// A thread block takes a block of query rows of one key/value head and 128 keys per step; both products are 128-row tcgen05
+// MMAs of one issuing warp with accumulators in tensor memory:
+//   S = Q K^T    Q and K in shared memory (128-byte swizzle, along the head dim)
+//   O += P V     P in tensor memory over the scores it was made of, V in shared memory (swizzled, along the head dim too)
+// The softmax is in one pass with a running maximum (tree_tc.cuh).  Heads of 64 and 128: 256 rows, two streams of 128 with an S
+// and an O each, so that one's products run while the other's softmax does.  Heads of 256, whose O takes half of tensor memory:
+// 128 rows, one stream whose tiles alternate between two S.
+// Rows see keys up to their own position: only the last tiles of an item are masked, and streams end where their rows do.
+// Keys and values arrive by TMA in a ring of slots in the order of their use.  An e4m3 cache is copied into the upper half of a
+// slot and widened in place to bf16 (exact).  Values that a product must not meet (rows past the end, numbers that are not finite
+// where not every row sees them) are cleared on the way, the latter added back for the rows that see them (rare).
+// The warps: two softmax warpgroups (a thread per row, a tile's scores in registers); the warp that plans and copies, the one
+// that issues, two that bring the queries; a warpgroup that widens and clears.
+#include <cstring>
+#include <cuda.h>
+
 #include "common.cuh"
+#include "devcache.h"
 #include "launch.h"
 #include "pdl.cuh"
+#include "prompt_sched.cuh"
 #include "serving.h"
+#include "tc_ptx.cuh"
 #include "tree_sched.cuh"
+#include "tree_tc.cuh"
 
 namespace trellis {
 namespace {
 
-constexpr int kThreads = 256;
+using namespace tree;
+using prompt::kTile;
+using prompt::Work;
 
-__device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
-  uint32_t h;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h) : "r"((uint32_t)v));
-  return f16_to_f32((uint16_t)h);
+__device__ int g_prompt_error = 0;  // set when a bounded wait gives up (trellis_device_error)
+
+constexpr int kThreads = 512;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kWidenWarp = 12;
+constexpr int kSoftmaxRegs = 192, kIssueRegs = 56, kWidenRegs = 72;
+static_assert(2 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 65536 / 128, "what the block was launched with");
+constexpr int kWorks = 2;  // items that the copying warp has announced
+constexpr int kOdd = 8;    // items whose odd values are known at a time: the widening warps are a few ahead of the softmax at the most
+
+template <int D>
+struct Cfg {
+  static constexpr int Streams = D == 256 ? 1 : 2;
+  static constexpr int Rows = 128 * Streams;
+  static constexpr int Keys = D == 256 ? 64 : 128;  // of a slot
+  static constexpr int Parts = kTile / Keys;        // slots of a tile's keys, or values
+  static constexpr int Slot = Keys * D * 2;
+  static constexpr int Slots = D == 64 ? 8 : 4;
+  static constexpr int Blocks = D / 64;             // 128-byte blocks of a row
+  static constexpr int QTile = 128 * D * 2;
+  static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 1024;
+  static constexpr int Smem = 1024 + Slots * Slot + Streams * QTile + Fixed;
+  static_assert(Smem <= 227 * 1024, "fits");
+  // tensor memory columns
+  static constexpr int S(int s) { return s * 128; }
+  static constexpr int O(int s) { return 256 + s * D; }
+};
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Two e4m3 numbers (the low bytes' pair of w by sel) as bf16, exactly: exponent and fraction moved to bf16's places, times
+// 2^120.  NaN comes out as +-480.
+__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t sel) {
+  const uint32_t u = __byte_perm(w, 0, sel);
+  const uint32_t v = ((u >> 4) & 0x07F007F0u) | (u & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
+  return r;
+}
+// Whether any of four e4m3 numbers is NaN: bit 7 of its byte of the result.
+__device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
+
+// The order in which an item's tiles of keys and values are copied and used: place of tile t's keys or values among 2n.
+template <int Streams>
+__device__ __forceinline__ int place_of(int t, bool value, int n) {
+  if (Streams == 2) return 2 * t + (value ? 1 : 0);
+  return value ? (t == n - 1 ? 2 * n - 1 : 2 * t + 2) : (t == 0 ? 0 : 2 * t - 1);  // keys of the next tile before a tile's values
+}
+template <int Streams>
+__device__ __forceinline__ int tile_at(int place, int n, bool* value) {
+  if (Streams == 2) {
+    *value = place & 1;
+    return place >> 1;
+  }
+  if (place < 2 && place < n) { *value = false; return place; }
+  if (place == 2 * n - 1) { *value = true; return n - 1; }
+  *value = !(place & 1);
+  return place & 1 ? (place + 1) / 2 : (place - 2) / 2;
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const TreeParams p) {
-  pdl_enter();
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float kLn2 = 0.693147180559945309f;
-  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    const TreeSeq s = tree_seq(p, b);
-    const int64_t rows = (int64_t)s.count * p.hq;
-    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + warp; r < rows; r += (int64_t)gridDim.x * (kThreads / 32)) {
-      const int tok = (int)(r / p.hq), h = (int)(r % p.hq), kvh = h / p.group;
-      const uint16_t* q = p.q + (int64_t)(s.start + tok) * p.q_stride + (int64_t)h * D;
-      const float ks = p.scales ? p.scales[kvh] : 1.f, vs = p.scales ? p.scales[p.hkv + kvh] : 1.f;
-      float x[E], o[E] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = bf16_to_f32(q[lane + 32 * e]);
-      for (int pos = 0; pos <= s.prefix + tok; ++pos) {
-        int page = p.table[(int64_t)b * p.width + (pos >> p.page_shift)];
-        page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
-        const int64_t krow = (((int64_t)(page * 2) * p.hkv + kvh) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-        const int64_t vrow = krow + ((int64_t)p.hkv << p.page_shift);
-        const auto at = [&](int64_t row, int e) {
-          const int64_t i = row * D + lane + 32 * e;
-          return F8 ? e4m3_to_f32(static_cast<const uint8_t*>(p.pool)[i]) : bf16_to_f32(static_cast<const uint16_t*>(p.pool)[i]);
-        };
-        float sc = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sc = fmaf(x[e], at(krow, e), sc);
-#pragma unroll
-        for (int w = 16; w; w >>= 1) sc += __shfl_xor_sync(0xFFFFFFFFu, sc, w);
-        sc *= p.scale_log2 * ks;
-        if (sc == -INFINITY) continue;
-        const float to = fmaxf(m, sc), a = m == -INFINITY ? 0.f : exp2f(m - to), w = exp2f(sc - to);
-        l = l * a + w;
-        m = to;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, at(vrow, e), o[e] * a);
-      }
-      const float f = l == 0.f ? 0.f : vs / l;
-      uint16_t* out = p.out + (int64_t)(s.start + tok) * p.out_stride + (int64_t)h * D;
-#pragma unroll
-      for (int e = 0; e < E; ++e) out[lane + 32 * e] = f32_to_bf16_rn(o[e] * f);
-      if (p.lse && lane == 0) p.lse[(int64_t)(s.start + tok) * p.hq + h] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* ring = base;
+  uint8_t* sq = ring + C::Slots * C::Slot;
+  prompt::Map& plan = *reinterpret_cast<prompt::Map*>(sq + C::Streams * C::QTile);
+  Work* works = reinterpret_cast<Work*>(&plan + 1);
+  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(works + kWorks) + 7) & ~(uintptr_t)7);
+  uint64_t* tail_full = full + C::Slots;  // bf16: of values that are cleared first.  A thread that waits for a phase has to have seen
+  uint64_t* empty = tail_full + C::Slots;  // the one before, and the clearing warps see no others
+  uint64_t* ready = empty + C::Slots;   // widened, or clear
+  uint64_t* q_full = ready + C::Slots;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;       // [2] scores there
+  uint64_t* p_ready = s_full + 2;       // [2] weights written
+  uint64_t* o_full = p_ready + 2;       // [2] the stretch's last product complete
+  uint64_t* o_done = o_full + 2;        // one stream: each product with the values
+  uint64_t* w_full = o_done + 1;        // [kWorks] a stretch announced
+  uint64_t* w_empty = w_full + kWorks;
+  uint64_t* drained = w_empty + kWorks;
+  volatile int* flags = reinterpret_cast<volatile int*>(drained + 1);  // [0] a wait gave up
+  volatile int* odd_of = flags + 4;     // [stretch % kOdd] the stretch, if it has odd values
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(flags) + 4 + kOdd);
+
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::prefetch_tmap(&map);
+    for (int i = 0; i < C::Slots; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(tail_full + i, 1);
+      tc::mbar_init(empty + i, 1);
+      tc::mbar_init(ready + i, 4);
     }
+    tc::mbar_init(q_full, 2);
+    tc::mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(s_full + s, 1);
+      tc::mbar_init(p_ready + s, 4);
+      tc::mbar_init(o_full + s, 1);
+    }
+    tc::mbar_init(o_done, 1);
+    for (int i = 0; i < kWorks; ++i) {
+      tc::mbar_init(w_full + i, 1);
+      tc::mbar_init(w_empty + i, 7 + 4 * C::Streams);
+    }
+    tc::mbar_init(drained, 1);
+    flags[0] = 0;
+    for (int i = 0; i < kOdd; ++i) odd_of[i] = -1;
+    tc::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  pdl_enter();
+  prompt::plan<C::Rows>(p, plan, (int)gridDim.x, reinterpret_cast<int*>(sq));
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = uniform(*tmem_slot);
+  bool dead = false;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {  // of a converged warp
+    const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
+    if (__any_sync(0xFFFFFFFFu, !ok)) {
+      dead = true;
+      if (lane == 0) flags[0] = 1;
+    }
+    return !dead;
+  };
+  // The k-th stretch, for the warps that are told; false where there is none.
+  const auto told = [&](int k, Work& w) {
+    const int s = k % kWorks;
+    if (!wait(w_full + s, (uint32_t)(k / kWorks & 1))) return false;
+    w = works[s];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(w_empty + s);
+    return w.more != 0;
+  };
+
+  if (warp >= kWidenWarp) {
+    // ---- widening and clearing
+    regs_down<kWidenRegs>();
+    const int tid = threadIdx.x & 127;
+    Work w;
+    int e0 = 0;
+    uint32_t f_phase = 0;  // per slot
+    // the group's warps meet at barriers, so they leave together
+    for (int k = 0; tc::bar_and(told(k, w), 2, 128); ++k) {
+      const int n = w.tiles;
+      const int shared_to = w.prefix + w.first + 1;  // keys that every row sees
+      for (int e = 0; e < 2 * n && !dead; ++e) {
+        bool value;
+        const int t = tile_at<C::Streams>(e, n, &value);
+        const bool tail = value && (w.tile0 + t + 1) * kTile > shared_to;
+        if (!F8 && !tail) continue;
+        for (int part = 0; part < C::Parts; ++part) {
+          const int at = e0 + e * C::Parts + part, slot = at % C::Slots;
+          const int pos0 = (w.tile0 + t) * kTile + part * C::Keys;
+          wait((F8 ? full : tail_full) + slot, f_phase >> slot & 1u);
+          f_phase ^= 1u << slot;
+          uint8_t* tile = ring + slot * C::Slot;
+          if constexpr (F8) {
+            constexpr int Chunks = D / 16, Each = C::Keys * Chunks / 128;  // 16 numbers; of a row, of a thread
+            uint4 v[Each];
+#pragma unroll
+            for (int i = 0; i < Each; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + (i * 128 + tid) * 16);
+            if (!tc::bar_and(!dead, 2, 128)) {  // all of it is in registers
+              dead = true;
+              break;
+            }
+#pragma unroll
+            for (int i = 0; i < Each; ++i) {
+              const int c = i * 128 + tid, row = c / Chunks, ch = c % Chunks * 2;
+              uint32_t o[8];
+              const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              uint32_t bad = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                bad |= nan4(in[j]);
+                o[2 * j] = widen2(in[j], 0x1404);
+                o[2 * j + 1] = widen2(in[j], 0x3424);
+              }
+              if (bad & 0x80808080u) {
+                const bool clear = tail && pos0 + row >= shared_to;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const uint32_t b = nan4(in[j >> 1]) >> (j & 1 ? 16 : 0);
+                  if (b & 0x80u) o[j] = (o[j] & 0xFFFF0000u) | (clear ? 0u : 0x7FFFu);
+                  if (b & 0x8000u) o[j] = (o[j] & 0xFFFFu) | (clear ? 0u : 0x7FFF0000u);
+                }
+                if (clear && pos0 + row < w.len) {
+                  odd_of[k % kOdd] = k;
+                  __threadfence_block();
+                }
+              }
+              if (tail && pos0 + row >= w.len)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = 0;
+              uint8_t* to = tile + (ch >> 3) * (C::Keys * 128) + row * 128;
+              *reinterpret_cast<uint4*>(to + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(to + ((((ch & 7) + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          } else {
+            if (dead) break;
+            constexpr int Chunks = D / 8;
+            const int from = max(shared_to - pos0, 0);
+            for (int c = from * Chunks + tid; c < C::Keys * Chunks; c += 128) {
+              const int row = c / Chunks, ch = c % Chunks;
+              uint4* to = reinterpret_cast<uint4*>(tile + (ch >> 3) * (C::Keys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+              if (pos0 + row >= w.len) {
+                *to = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint4 v = *to;
+              bool odd = false;
+              const auto clean = [&](uint32_t& x) {
+                if ((x & 0x7F80u) == 0x7F80u) { x &= 0xFFFF0000u; odd = true; }
+                if ((x >> 16 & 0x7F80u) == 0x7F80u) { x &= 0xFFFFu; odd = true; }
+              };
+              clean(v.x); clean(v.y); clean(v.z); clean(v.w);
+              if (odd) {
+                odd_of[k % kOdd] = k;
+                __threadfence_block();
+                *to = v;
+              }
+            }
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(ready + slot);
+        }
+      }
+      e0 += 2 * n * C::Parts;
+    }
+  } else if (warp >= 8) {
+    regs_down<kIssueRegs>();
+    if (warp == kCopyWarp) {
+      // ---- the warp that plans and copies
+      const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+      const int box = min(1 << p.page_shift, C::Keys);  // rows of one copy
+      int at = 0, end = 0, item = cta, fetched = 0;
+      if (plan.split && cta < plan.ctas) {
+        at = (int)((int64_t)cta * plan.total / plan.ctas);
+        end = (int)((int64_t)(cta + 1) * plan.total / plan.ctas);
+      }
+      int e0 = 0, copied = 0;
+      uint32_t f_phase = 0, t_phase = 0, is_tail = 0;  // per slot: copies into it, of tail values; what the last one was
+      for (int k = 0;; ++k) {
+        Work w = plan.split ? prompt::next_stretch<C::Rows>(p, plan, at, end) : prompt::whole_item<C::Rows>(p, plan, item);
+        if (!plan.split && w.more && lane == 0) fetched = atomicAdd(p.counter, 1);  // the one after it
+        const int s = k % kWorks;
+        if (k >= kWorks && !wait(w_empty + s, (uint32_t)(k / kWorks & 1) ^ 1u)) break;
+        if (lane == 0) {
+          works[s] = w;
+          tc::mbar_arrive(w_full + s);
+        }
+        __syncwarp();
+        if (!w.more) break;
+        const int n = w.tiles;
+        TreeSegment g;
+        g.seq = TreeSeq{w.start, w.len - w.prefix, w.prefix};
+        g.b = w.b;
+        g.tile0 = w.tile0 * C::Parts;
+        TreePages<C::Keys> pages(p, g, lane);
+        const int shared_to = w.prefix + w.first + 1;
+        for (int e = 0; e < 2 * n && !dead; ++e) {
+          bool value;
+          const int t = tile_at<C::Streams>(e, n, &value);
+          for (int part = 0; part < C::Parts; ++part) {
+            const int i = e0 + e * C::Parts + part, slot = i % C::Slots, use = i / C::Slots;
+            const int pos = (w.tile0 + t) * kTile + part * C::Keys + lane * box;  // lane i copies box i of the slot, none past the end
+            const bool mine = lane * box < C::Keys && pos < w.len;
+            int y = 0, page = pages.at(t * C::Parts + part);
+            if (mine) {
+              page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+              y = (((page * 2 + (value ? 1 : 0)) * p.hkv + w.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+            }
+            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+            if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) break;
+            const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
+            uint64_t* bar = (tail ? tail_full : full) + slot;
+            (tail ? t_phase : f_phase) ^= 1u << slot;
+            is_tail = (is_tail & ~(1u << slot)) | (uint32_t)tail << slot;
+            if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * D * (F8 ? 1 : 2)));
+            __syncwarp();
+            copied = i + 1;
+            if (mine) {
+              if constexpr (F8) {
+                tc::tma_load_2d(ring + slot * C::Slot + C::Slot / 2 + lane * box * D, &map, bar, 0, y);
+              } else {
+#pragma unroll
+                for (int blk = 0; blk < C::Blocks; ++blk)
+                  tc::tma_load_2d(ring + slot * C::Slot + blk * (C::Keys * 128) + lane * box * 128, &map, bar, blk * 64, y);
+              }
+            }
+          }
+        }
+        e0 += 2 * n * C::Parts;
+        if (!plan.split) item = grid + __shfl_sync(0xFFFFFFFFu, fetched, 0);
+        if (dead) break;
+      }
+      // no copy may land in a block that has left
+      for (int i = max(0, copied - C::Slots); i < copied; ++i) {
+        const int slot = i % C::Slots;
+        const bool tail = is_tail >> slot & 1u;
+        tc::mbar_wait((tail ? tail_full : full) + slot, ((tail ? t_phase : f_phase) >> slot & 1u) ^ 1u, kDrainNs);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---- the warp that issues the products
+      bool issued = false;
+      Work w;
+      int e0 = 0;
+      uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
+      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, C::Keys), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
+      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
+                     v_desc = desc_mnmajor(tc::smem_u32(ring), C::Keys * 128);
+      for (int k = 0; told(k, w); ++k) {
+        const int n = uniform(w.tiles), shared_to = w.prefix + w.first + 1;
+        const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
+        const auto entry = [&](int t, bool value, int part) { return e0 + place_of<C::Streams>(t, value, n) * C::Parts + part; };
+        const auto take = [&](int t, bool value) {
+          const bool tail = value && (w.tile0 + t + 1) * kTile > shared_to;
+          for (int part = 0; part < C::Parts; ++part) {
+            const int i = entry(t, value, part), slot = i % C::Slots;
+            if (tail && !F8) {
+              if (!wait(tail_full + slot, t_phase >> slot & 1u) || !wait(ready + slot, t_phase >> slot & 1u)) return false;
+              t_phase ^= 1u << slot;
+            } else {
+              if (!wait((F8 ? ready : full) + slot, f_phase >> slot & 1u)) return false;
+              f_phase ^= 1u << slot;
+            }
+          }
+          tc::fence_after_sync();
+          return true;
+        };
+        const auto give = [&](int t, bool value) {
+          for (int part = 0; part < C::Parts; ++part) mma_done(empty + entry(t, value, part) % C::Slots);
+        };
+        const auto scores = [&](int s, int qtile, int t) {
+          const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4));
+#pragma unroll
+          for (int part = 0; part < C::Parts; ++part) {
+            const uint64_t b = k_desc + (uint32_t)(entry(t, false, part) % C::Slots * (C::Slot >> 4));
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              mma_ss(tmem + C::S(s) + part * C::Keys, a + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4),
+                     b + (((x >> 2) * (C::Keys * 128) + (x & 3) * 32) >> 4), id_s, x > 0);
+          }
+          mma_done(s_full + s);
+          issued = true;
+        };
+        const auto outputs = [&](int s, int o, int t, bool fresh) {
+#pragma unroll
+          for (int part = 0; part < C::Parts; ++part) {
+            const uint64_t b = v_desc + (uint32_t)(entry(t, true, part) % C::Slots * (C::Slot >> 4));
+#pragma unroll
+            for (int x = 0; x < C::Keys / 16; ++x)
+              mma_ts(tmem + C::O(o), tmem + C::S(s) + 8 * (part * (C::Keys / 16) + x), b + ((x * 16 * 128) >> 4), id_o,
+                     !(fresh && part == 0 && x == 0));
+          }
+        };
+        const auto weights = [&](int s) {  // waits for the stream's
+          if (!wait(p_ready + s, p_phase >> s & 1u)) return false;
+          p_phase ^= 1u << s;
+          tc::fence_after_sync();
+          return true;
+        };
+        if (!wait(q_full, (uint32_t)(k & 1))) break;
+        tc::fence_after_sync();
+        if constexpr (C::Streams == 1) {
+          for (int t = 0; t < 2 && t < n; ++t) {
+            if (!take(t, false)) break;
+            scores(t, 0, t);
+            give(t, false);
+          }
+          if (n <= 2) mma_done(q_empty);
+          for (int t = 0; t < n && !dead; ++t) {
+            if (!take(t, true) || !weights(t & 1)) break;
+            outputs(t & 1, 0, t, t == 0);
+            give(t, true);
+            mma_done(o_done);
+            if (t + 2 < n) {
+              if (!take(t + 2, false)) break;
+              scores(t & 1, 0, t + 2);
+              give(t + 2, false);
+              if (t + 3 == n) mma_done(q_empty);
+            } else if (t + 1 == n) {
+              mma_done(o_full);
+            }
+          }
+        } else {
+          if (!take(0, false)) break;
+          if (n0 > 0) scores(0, 0, 0);
+          if (n1 > 0) scores(1, 1, 0);
+          give(0, false);
+          if (n == 1) mma_done(q_empty);
+          for (int t = 0; t < n; ++t) {
+            const bool more = t + 1 < n;
+            if (!take(t, true)) break;
+            if (t < n0) {
+              if (!weights(0)) break;
+              outputs(0, 0, t, t == 0);
+              if (t + 1 == n0) mma_done(o_full);
+            }
+            if (more && !take(t + 1, false)) break;
+            if (t + 1 < n0) scores(0, 0, t + 1);
+            if (t < n1) {
+              if (!weights(1)) break;
+              outputs(1, 1, t, t == 0);
+              if (t + 1 == n1) mma_done(o_full + 1);
+            }
+            give(t, true);
+            if (t + 1 < n1) scores(1, 1, t + 1);
+            if (more) {
+              give(t + 1, false);
+              if (t + 2 == n) mma_done(q_empty);
+            }
+          }
+        }
+        if (dead) break;
+        e0 += 2 * n * C::Parts;
+      }
+      // tensor memory is given back once every product issued has completed, also where a wait gave up
+      if (issued) {
+        mma_done(drained);
+        tc::mbar_wait(drained, 0, kDrainNs);
+      }
+    } else {
+      // ---- the warps that bring the queries
+      const int tid = threadIdx.x - kQueryWarp * 32;
+      Work w;
+      for (int k = 0; told(k, w); ++k) {
+        if (k > 0 && !wait(q_empty, (uint32_t)(k & 1) ^ 1u)) break;
+        const float ks = p.scales ? __ldg(p.scales + w.head) : 1.f;
+        constexpr int LPR = D / 8;
+        const int ch = tid % LPR;
+        const uint32_t to = tc::smem_u32(sq) + (ch >> 3) * (128 * 128);
+        for (int r = tid / LPR; r < w.rows; r += 64 / LPR) {
+          const int d = tree_draft(p, w.g0 + r), hh = w.g0 + r - d * p.group;
+          const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
+          cp_async16(to + (r >> 7) * C::QTile + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4), src);
+        }
+        cp_async_wait();
+        if (p.scale_log2 * ks < 0.f)  // a negative scale goes into the queries' signs
+          for (int r = tid / LPR; r < w.rows; r += 64 / LPR) {
+            uint4* at = reinterpret_cast<uint4*>(sq + (ch >> 3) * (128 * 128) + (r >> 7) * C::QTile + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+            uint4 v = *at;
+            v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
+            *at = v;
+          }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(q_full);
+      }
+    }
+  } else {
+    // ---- softmax: stream s, one thread per row; warp i of a group reaches tensor memory lanes 32 i ..
+    regs_up<kSoftmaxRegs>();
+    const int s = warp >> 2, r = threadIdx.x;  // row of the block
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int cta = (int)blockIdx.x;
+    Work w;
+    uint32_t s_phase = 0, o_phase = 0;  // s_phase: per S
+    int products = 0;                   // one stream: tiles of the stretches before
+    int4 shared_item = make_int4(0, 0, 0, 0);  // the item that starts here and ends in a later block
+    if (s < C::Streams)
+      for (int k = 0; told(k, w); ++k) {
+        const bool valid = r < w.rows;
+        const int n = prompt::tiles_of(p, w, s * 128, s * 128 + 128);
+        const int seen = valid ? prompt::seen_by(p, w, r) : 0;
+        const int masked_from = s * 128 < w.rows ? prompt::seen_by(p, w, s * 128) : 0;  // keys that every row of the stream sees
+        const float c = score_factor(fabsf(p.scale_log2 * (p.scales ? __ldg(p.scales + w.head) : 1.f)));
+        const uint32_t t_o = tmem + C::O(s) + lanes;
+        float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
+        for (int i = 0; i < n; ++i) {
+          const int buf = C::Streams == 1 ? i & 1 : s;
+          const uint32_t t_s = tmem + C::S(buf) + lanes;
+          if (!wait(s_full + buf, s_phase >> buf & 1u)) break;
+          s_phase ^= 1u << buf;
+          tc::fence_after_sync();
+          const int pos0 = (w.tile0 + i) * kTile;
+          uint32_t x[4][32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc::tmem_ld_32x32b_x32(t_s + 32 * j, x[j]);
+          tc::tmem_ld_wait();
+          if (pos0 + kTile > masked_from) {  // scores that the row does not see
+            const int upto = seen - pos0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < 32; ++q) x[j][q] = 32 * j + q < upto ? x[j][q] : 0xFF800000u;
+          }
+          float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int q = 0; q < 32; q += 4) {
+              a = fmaxf(fmaxf(a, __uint_as_float(x[j][q])), __uint_as_float(x[j][q + 1]));
+              b = fmaxf(fmaxf(b, __uint_as_float(x[j][q + 2])), __uint_as_float(x[j][q + 3]));
+            }
+          const float mx = fmaxf(a, b) * c;
+          const bool move = mx > m + kMove || (m == -INFINITY && mx > -INFINITY);
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            const float to = move ? mx : m, f = m == to ? 1.f : ex2(m - to);
+            l *= f;
+            m = to;
+            if (i > 0) {
+              if (C::Streams == 1) {  // the product of the tile before it
+                if (!wait(o_done, (uint32_t)(products + i - 1) & 1u)) break;
+                tc::fence_after_sync();
+              }
+#pragma unroll 1
+              for (int col = 0; col < D; col += 16) {
+                uint32_t y[16];
+                tmem_ld_x16(t_o + col, y);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 16; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
+                tmem_st_x16(t_o + col, y);
+              }
+            }
+          }
+          // ---- weights, over the scores: bf16, the type of the values they are multiplied with
+          const float ms = m == -INFINITY ? 0.f : -m;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t e[16];
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j][q]), __uint_as_float(x[j][q + 1])), make_float2(c, c), make_float2(ms, ms));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum = __fadd2_rn(sum, y);
+              e[q >> 1] = pack_bf16x2(y.x, y.y);
+            }
+            tmem_st_x16(t_s + 16 * j, e);
+          }
+          l += sum.x + sum.y;
+          tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(p_ready + buf);
+        }
+        if (dead) break;
+        products += n;
+        // ---- the stretch's end
+        if (n > 0) {
+          if (!wait(o_full + s, o_phase)) break;
+          o_phase ^= 1u;
+          tc::fence_after_sync();
+        }
+        const bool whole = w.tile0 == 0 && w.tiles == w.last + 1;
+        const bool odd = odd_of[k % kOdd] == k;
+        const int d = valid ? tree_draft(p, w.g0 + r) : 0, hh = w.g0 + r - d * p.group;
+        const int64_t token = w.start + w.first + d;
+        const int head = w.head * p.group + hh;
+        const auto fetch = [&](int col, float (&v)[32]) {  // 32 columns of the row
+          uint32_t y[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) y[q] = 0;
+          if (n > 0) {
+            tc::tmem_ld_32x32b_x32(t_o + col, y);
+            tc::tmem_ld_wait();
+          }
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(y[q]);
+          if (odd && valid)
+            for (int pos = max(w.prefix + w.first + 1, w.tile0 * kTile); pos < min(seen, (w.tile0 + w.tiles) * kTile); ++pos) {
+              int page = p.table[(int64_t)w.b * p.width + (pos >> p.page_shift)];
+              page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+              const int64_t at = ((((int64_t)page * 2 + 1) * p.hkv + w.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
+#pragma unroll
+              for (int q = 0; q < 32; ++q) {
+                if constexpr (F8) {
+                  if ((static_cast<const uint8_t*>(p.pool)[at + q] & 0x7F) == 0x7F) v[q] = __uint_as_float(0x7FFFFFFFu);
+                } else {
+                  const uint16_t x = static_cast<const uint16_t*>(p.pool)[at + q];
+                  if ((x & 0x7F80u) == 0x7F80u) v[q] += bf16_to_f32(x);
+                }
+              }
+            }
+        };
+        if (whole) {
+          const float vs = p.scales ? __ldg(p.scales + p.hkv + w.head) : 1.f, f = l == 0.f ? 0.f : vs / l;
+          uint16_t* out = p.out + token * p.out_stride + (int64_t)head * D;
+#pragma unroll 1
+          for (int col = 0; col < D; col += 32) {
+            float v[32];
+            fetch(col, v);
+            if (valid)
+#pragma unroll
+              for (int q = 0; q < 32; q += 8)
+                *reinterpret_cast<uint4*>(out + col + q) =
+                    make_uint4(pack_bf16x2(v[q] * f, v[q + 1] * f), pack_bf16x2(v[q + 2] * f, v[q + 3] * f),
+                               pack_bf16x2(v[q + 4] * f, v[q + 5] * f), pack_bf16x2(v[q + 6] * f, v[q + 7] * f));
+          }
+          if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        } else {  // a part, for the joining kernel
+          float* part = p.part + (int64_t)tree_slot(cta, w.tile0 == 0) * tree_part_floats(C::Rows, D);
+#pragma unroll 1
+          for (int col = 0; col < D; col += 32) {
+            float v[32];
+            fetch(col, v);
+            if (valid)
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4*>(part + ((int64_t)(col + q) / 4 * C::Rows + r) * 4) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+          }
+          if (valid) {
+            part[(int64_t)C::Rows * D + r] = m;
+            part[(int64_t)C::Rows * D + C::Rows + r] = l;
+          }
+          if (w.tile0 == 0 && r == 0)
+            shared_item = make_int4(w.start + w.first, w.head, w.g0, tree_parts_shared(w.until - cta + 1) << 24 | w.rows << 12 | w.until);
+        }
+        tc::fence_before_sync();  // the accumulator is read before the next stretch's weights are announced
+      }
+    if (threadIdx.x == 0) p.items[cta] = shared_item;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && flags[0]) atomicCAS(&g_prompt_error, 0, 4);
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D>
-cudaError_t launch_d(const TreeParams& p, bool f8, cudaStream_t st) {
-  const dim3 grid(152 * 4, p.batch < 64 ? p.batch : 64);
-  return f8 ? launch_pdl(prompt_kernel<D, true>, grid, dim3(kThreads), 0, st, p)
-            : launch_pdl(prompt_kernel<D, false>, grid, dim3(kThreads), 0, st, p);
+template <int D, bool F8>
+cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cudaStream_t st) {
+  auto kern = prompt_kernel<D, F8>;
+  static PerDevice<cudaError_t> attr_of;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  const cudaError_t e = attr_of.get(dev, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Smem);
+  }, cudaErrorInvalidDevice);
+  if (e != cudaSuccess) return e;
+  const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
+  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, Cfg<D>::Rows, 0.f, ctas, st);
 }
+
+int prompt_ctas() { return device_sm_count() < kTreeMaxCtas ? device_sm_count() : kTreeMaxCtas; }
+
+constexpr size_t kItemBytes = kTreeMaxCtas * sizeof(int4);
 
 }  // namespace
 
 size_t prompt_workspace_bytes(const trellis_cache_t& c, int q_heads) {
-  (void)c; (void)q_heads;
-  return 1024;
+  (void)q_heads;  // parts belong to thread blocks, whatever the heads
+  const int rows = c.head_dim == 256 ? Cfg<256>::Rows : Cfg<128>::Rows;
+  return kItemBytes + 16 + (size_t)tree_part_floats(rows, c.head_dim) * 4 * 2 * prompt_ctas();
+}
+
+int read_prompt_error(int reset) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prompt_error, sizeof(int)) != cudaSuccess) return -1;
+  if (reset && v) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_prompt_error, &zero, sizeof(int)) != cudaSuccess) return -1;
+  }
+  return v;
 }
 
 cudaError_t launch_prompt_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,
                                     const trellis_drafts_t& d, int q_heads, float scale, uint16_t* out,
                                     int64_t out_stride, float* lse, void* workspace, cudaStream_t st) {
-  (void)workspace;
   TreeParams p{};
   p.q = q; p.out = out; p.lse = lse;
   p.table = d.table; p.prefix = d.prefix; p.q_start = d.q_start;
   p.scales = c.scales ? c.scales + (int64_t)layer * 2 * c.heads : nullptr;
   p.q_stride = q_stride; p.out_stride = out_stride;
   p.pages = c.pages;
+  p.wait_ns = wait_limit_ns();
   p.batch = d.batch; p.width = d.width; p.n = d.n; p.max_tokens = d.max_tokens;
   p.hq = q_heads; p.hkv = c.heads; p.group = q_heads / c.heads;
+  p.group_inv = (((uint64_t)1 << 32) + p.group - 1) / p.group;
   p.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   p.scale_log2 = scale * kLog2e;
-  p.pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
+  p.items = static_cast<int4*>(workspace);
+  p.counter = reinterpret_cast<int*>(static_cast<char*>(workspace) + kItemBytes);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kItemBytes + 16);
+
+  const auto fn = tensor_map_encoder();
+  if (!fn) return cudaErrorNotSupported;
   const bool f8 = c.dtype == TRELLIS_E4M3;
-  return c.head_dim == 64 ? launch_d<64>(p, f8, st) : c.head_dim == 128 ? launch_d<128>(p, f8, st) : launch_d<256>(p, f8, st);
+  const int row_bytes = c.head_dim * (int)cache_elem_bytes(c), keys = c.head_dim == 256 ? Cfg<256>::Keys : Cfg<128>::Keys;
+  uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
+  CUtensorMap map;
+  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.pages * 2 * c.heads * c.page_size)};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  // e4m3 as it lies in the cache, bf16 in 128-byte blocks of a row, swizzled
+  const cuuint32_t box[2] = {(cuuint32_t)(f8 ? c.head_dim : 64), (cuuint32_t)(c.page_size < keys ? c.page_size : keys)};
+  const cuuint32_t estr[2] = {1, 1};
+  if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  p.pool = pool;
+  const int ctas = prompt_ctas();
+  if (f8)
+    return c.head_dim == 64 ? launch_d<64, true>(map, p, ctas, st) : c.head_dim == 128 ? launch_d<128, true>(map, p, ctas, st)
+                                                                                     : launch_d<256, true>(map, p, ctas, st);
+  return c.head_dim == 64 ? launch_d<64, false>(map, p, ctas, st) : c.head_dim == 128 ? launch_d<128, false>(map, p, ctas, st)
+                                                                                    : launch_d<256, false>(map, p, ctas, st);
 }
 
 }  // namespace trellis

@@ -603,8 +603,8 @@ int read_tree_error(int reset) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_tree_error, &zero, sizeof(int)) != cudaSuccess) return -1;
   }
-  const int w = read_tree_tc_error(reset), x = read_tree_tc1_error(reset);
-  return v ? v : w ? w : x;
+  const int w = read_tree_tc_error(reset), x = read_tree_tc1_error(reset), y = read_prompt_error(reset);
+  return v ? v : w ? w : x ? x : y;
 }
 
 cudaError_t launch_tree_attention(const uint16_t* q, int64_t q_stride, const trellis_cache_t& c, int layer,

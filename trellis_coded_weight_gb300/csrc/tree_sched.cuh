@@ -30,6 +30,7 @@ struct TreeParams {
   const void* pool;     // the layer's pages, bf16 or e4m3
   int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (tree_item), or none
   float* part;          // two slots per thread block
+  int* counter;         // prompts: the next item, which the joining kernel clears; null for trees
   int64_t q_stride, out_stride;
   int64_t pages;
   uint64_t wait_ns;
@@ -247,5 +248,6 @@ int tree_tc1_rows();
 void tree_tc1_box(const trellis_cache_t& c, TreeBox* b);
 cudaError_t launch_tree_tc1(const CUtensorMap& map, const TreeParams& p, const trellis_cache_t& c, int ctas, cudaStream_t st);
 int read_tree_tc1_error(int reset);
+int read_prompt_error(int reset);  // prompt_attention.cu
 
 }  // namespace trellis
