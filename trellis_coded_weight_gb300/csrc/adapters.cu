@@ -1,17 +1,36 @@
 // adapters.cu -- adds low-rank adapters to a projection's output (plan: adapter_plan.cuh).
 //
 //   h = A x  (fp32),  out = bf16(y + scale B h)
-// A warp per row of A, then a thread per output.
+// A cluster of thread blocks takes a tile: up to 64 tokens of one adapter.  Each of its blocks multiplies its part of the inputs
+// with A; the parts of h are added up through distributed shared memory, in the order of the blocks, and each block then makes its
+// part of the outputs.  x, y and out are touched once, A and B once per tile.  Both products are warp-level bf16 MMAs on operands
+// that go from global memory straight into the fragments: a lane loads 16 (or 8) contiguous bytes of a row, and the reduction
+// index is permuted alike on both sides so that these are what its fragments hold; likewise the outputs of four tiles of 8, so that
+// a lane has 8 contiguous ones.  h enters the second product as the sum of two bf16 numbers.
+// Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and
+// makes a share of the outputs.
+// Bound: bytes of x, y and out for prompts, of A and B for single tokens.
 #include "adapter_plan.cuh"
 #include "common.cuh"
+#include "devcache.h"
 #include "launch.h"
 #include "pdl.cuh"
 #include "serving.h"
+#include "tc_ptx.cuh"
 
 namespace trellis {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kGroup = 32;             // rows of A that a warp multiplies with
+constexpr int kCopyLd = kGroup + 4;    // floats from token to token of a warp's products
+constexpr int kPartLd = kAdapterMaxRank + 8;
+constexpr int kCopyBytes = kWarps * kAdapterTile * kCopyLd * 4;
+constexpr int kPartBytes = kAdapterTile * kPartLd * 4;
+constexpr int kSmem = kCopyBytes + kPartBytes + kAdapterTile * 4;
+static_assert(kAdapterTile * kAdapterMaxRank * 4 <= kCopyBytes, "the fragments of h take the products' place");
+static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
 
 struct AddParams {
   const uint16_t *x, *y;
@@ -22,54 +41,308 @@ struct AddParams {
   int batch, n;
 };
 
-__global__ void __launch_bounds__(kThreads) add_kernel(const AddParams p) {
-  pdl_enter();
-  __shared__ float h[kAdapterMaxRank];
-  const AdapterPlanHeader* head = static_cast<const AdapterPlanHeader*>(p.plan);
-  const int32_t* order = adapter_order(p.plan, p.batch, p.n);
-  const int tiles = head->tiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int4 tile = adapter_tiles(p.plan)[t];
-    const bool has = tile.x >= 0 && tile.x < p.ad.count;
-    int rank = has ? p.ad.ranks ? p.ad.ranks[tile.x] : p.ad.max_rank : 0;
-    rank = rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
-    const float scale = has && p.ad.scales ? p.ad.scales[tile.x] : 1.f;
-    for (int i = blockIdx.y; i < tile.z; i += gridDim.y) {
-      const int64_t token = order[tile.y + i];
-      const uint16_t *x = p.x + token * p.x_stride, *y = p.y + token * p.y_stride;
-      uint16_t* out = p.out + token * p.out_stride;
-      for (int r = warp; r < rank; r += kThreads / 32) {
-        const uint16_t* a = p.ad.a + ((int64_t)tile.x * p.ad.max_rank + r) * p.ad.in;
-        float s = 0.f;
-        for (int k = lane; k < p.ad.in; k += 32) s = fmaf(bf16_to_f32(a[k]), bf16_to_f32(x[k]), s);
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float2 ld_cluster(const float* p, uint32_t rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(p, rank)) : "memory");
+  return v;
+}
+// The first `n` of the two bf16 numbers of w, the others zero.
+__device__ __forceinline__ uint32_t first_of(uint32_t w, int n) { return n >= 2 ? w : n == 1 ? w & 0xFFFFu : 0u; }
+
+// h of the block's part of the inputs, for 16 MT tokens: into part[token][rank].
+template <int MT>
+__device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, int rank, int count, const int* tokens, int rank_of_block,
+                                       float* copies, float* part) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int groups = rank <= kGroup ? 1 : rank <= 2 * kGroup ? 2 : 4, splits = kWarps / groups;  // of rows of A; of the inputs
+  const int group = warp % groups, split = warp / groups;
+  const int blocks = (int)((p.ad.in + 31) / 32);
+  const int k0 = (int)((int64_t)rank_of_block * blocks / kCluster), k1 = (int)((int64_t)(rank_of_block + 1) * blocks / kCluster);
+  const uint16_t *x[2 * MT], *w[4];
+  bool has_x[2 * MT], has_w[4];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        if (lane == 0) h[r] = s;
+  for (int i = 0; i < 2 * MT; ++i) {
+    const int t = 8 * i + g;
+    has_x[i] = t < count;
+    x[i] = p.x + (int64_t)tokens[has_x[i] ? t : 0] * p.x_stride + 8 * q;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = group * kGroup + 8 * j + g;
+    has_w[j] = r < rank;
+    w[j] = a + (int64_t)(has_w[j] ? r : 0) * p.ad.in + 8 * q;
+  }
+  const int tiles = min(4, (rank - group * kGroup + 7) / 8);  // of 8 rows of A; may be none
+  float acc[MT][4][4];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
+  if (tiles > 0)
+    for (int k = k0 + split; k < k1; k += splits) {
+      const bool in = 32 * k + 8 * q < p.ad.in;
+      uint4 u[2 * MT], v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (in && has_w[j]) v[j] = __ldg(reinterpret_cast<const uint4*>(w[j] + 32 * k));
       }
-      __syncthreads();
-      for (int c = threadIdx.x; c < p.ad.out; c += kThreads) {
-        if (rank == 0) {
-          out[c] = y[c];
-          continue;
-        }
-        const uint16_t* b = p.ad.b + ((int64_t)tile.x * p.ad.out + c) * p.ad.max_rank;
-        float s = 0.f;
-        for (int r = 0; r < rank; ++r) s = fmaf(bf16_to_f32(b[r]), h[r], s);
-        out[c] = f32_to_bf16_rn(fmaf(scale, s, bf16_to_f32(y[c])));
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (in && has_x[i]) u[i] = *reinterpret_cast<const uint4*>(x[i] + 32 * k);
       }
-      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < tiles)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            mma(acc[i][j], u[2 * i].x, u[2 * i + 1].x, u[2 * i].y, u[2 * i + 1].y, v[j].x, v[j].y);
+            mma(acc[i][j], u[2 * i].z, u[2 * i + 1].z, u[2 * i].w, u[2 * i + 1].w, v[j].z, v[j].w);
+          }
     }
+  float* mine = copies + warp * (kAdapterTile * kCopyLd);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *reinterpret_cast<float2*>(mine + (16 * i + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][0], acc[i][j][1]);
+      *reinterpret_cast<float2*>(mine + (16 * i + 8 + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][2], acc[i][j][3]);
+    }
+  __syncthreads();
+  const int wide = groups * kGroup;  // ranks come out padded with zeros
+  for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
+    const int t = e / wide, r = e - t * wide;
+    float s = 0.f;
+    for (int c = 0; c < splits; ++c) s += copies[((r / kGroup) + c * groups) * (kAdapterTile * kCopyLd) + t * kCopyLd + r % kGroup];
+    part[t * kPartLd + r] = s;
+  }
+}
+
+// The sums over the cluster, as fragments: word of (token tile, block of 32 (NARROW: 16) ranks, high or low part, lane).
+template <bool NARROW>
+__device__ __forceinline__ uint32_t* fragment(uint32_t* h, int mt, int blocks, int kb, int step, int low) {
+  return NARROW ? h + (mt * 2 + low) * 128 : h + ((mt * blocks + kb) * 4 + step * 2 + low) * 128;
+}
+template <int MT, bool NARROW>
+__device__ __forceinline__ void gather(const float* part, int blocks, uint32_t* h) {
+  const int wide = blocks * (NARROW ? 16 : 32) / 2;  // pairs of ranks
+  for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
+    const int t = e / wide, r = (e - t * wide) * 2;
+    float2 s = make_float2(0.f, 0.f);
+    float2 v[kCluster];
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(part + t * kPartLd + r, c);
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      s.x += v[c].x;
+      s.y += v[c].y;
+    }
+    // cut off to bf16 (which never overflows) and what that leaves
+    const uint32_t x = __float_as_uint(s.x) & 0xFFFF0000u, y = __float_as_uint(s.y) & 0xFFFF0000u;
+    const float lx = (x & 0x7F800000u) == 0x7F800000u ? 0.f : s.x - __uint_as_float(x);
+    const float ly = (y & 0x7F800000u) == 0x7F800000u ? 0.f : s.y - __uint_as_float(y);
+    const int row = t & 15, kb = NARROW ? 0 : r >> 5;
+    const int q = NARROW ? r >> 2 : (r & 31) >> 3, step = NARROW ? 0 : (r & 7) >> 2, pair = (r & 3) >> 1;
+    const int word = ((row & 7) * 4 + q) * 4 + (row >> 3) + 2 * pair;
+    fragment<NARROW>(h, t >> 4, blocks, kb, step, 0)[word] = (x >> 16) | y;
+    fragment<NARROW>(h, t >> 4, blocks, kb, step, 1)[word] = pack_bf16x2(lx, ly);
+  }
+}
+
+// The outputs of blocks o0 + warp, + kWarps, .. < o1 of 32, for 16 MT tokens.
+template <int MT, bool NARROW, int NB>
+__device__ __forceinline__ void expand(const AddParams& p, const uint16_t* b, int rank, float scale, int count, const int* tokens,
+                                       uint32_t* h, int o0, int o1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const uint4* hl = reinterpret_cast<const uint4*>(h) + lane;
+  const int left = rank - (NARROW ? 4 : 8) * q;  // ranks from this lane's first on
+  const bool ragged = rank % (NARROW ? 4 : 8) != 0;
+#pragma unroll 1
+  for (int o = o0 + warp; o < o1; o += kWarps) {
+    uint4 v[4][NB];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t row = 32 * (int64_t)o + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb) {
+        v[j][kb] = make_uint4(0, 0, 0, 0);
+        if (row < p.ad.out && left > 32 * kb) {
+          const uint16_t* at = b + row * p.ad.max_rank + (NARROW ? 4 : 8) * q + 32 * kb;
+          if (NARROW) {
+            const uint2 two = __ldg(reinterpret_cast<const uint2*>(at));
+            v[j][kb].x = two.x;
+            v[j][kb].y = two.y;
+          } else {
+            v[j][kb] = __ldg(reinterpret_cast<const uint4*>(at));
+          }
+        }
+      }
+    }
+    const int col = 32 * o + 8 * q;
+    const bool in = col < p.ad.out;
+    uint4 u[2 * MT];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) {
+      const int t = 8 * i + g;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (in && t < count) u[i] = *reinterpret_cast<const uint4*>(p.y + (int64_t)tokens[t] * p.y_stride + col);
+    }
+    if (ragged)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+          const int n = left - 32 * kb;
+          v[j][kb] = make_uint4(first_of(v[j][kb].x, n), first_of(v[j][kb].y, n - 2), first_of(v[j][kb].z, n - 4), first_of(v[j][kb].w, n - 6));
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if (16 * i >= count) break;
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+        for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
+          const uint4 a = hl[(NARROW ? i * 2 + f : (i * NB + kb) * 4 + f) * 32];
+          const bool second = !NARROW && f >= 2;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
+        }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int t = 16 * i + 8 * half + g;
+        if (!in || t >= count) continue;
+        const uint4 y = u[2 * i + half];
+        const auto add = [&](uint32_t w, int j) {
+          return pack_bf16x2(fmaf(scale, acc[j][2 * half], bf16lo_to_f32(w)), fmaf(scale, acc[j][2 * half + 1], bf16hi_to_f32(w)));
+        };
+        *reinterpret_cast<uint4*>(p.out + (int64_t)tokens[t] * p.out_stride + col) = make_uint4(add(y.x, 0), add(y.y, 1), add(y.z, 2), add(y.w, 3));
+      }
+    }
+  }
+}
+
+template <int MT>
+__device__ __forceinline__ void tile_of(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
+                                        float* copies, float* part) {
+  const uint16_t *a = p.ad.a + (int64_t)tile.x * p.ad.max_rank * p.ad.in, *b = p.ad.b + (int64_t)tile.x * p.ad.out * p.ad.max_rank;
+  uint32_t* h = reinterpret_cast<uint32_t*>(copies);
+  shrink<MT>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), copies, part);
+  cluster_arrive();
+  cluster_wait();
+  if (rank <= 16) gather<MT, true>(part, 1, h);
+  else gather<MT, false>(part, rank <= 32 ? 1 : rank <= 64 ? 2 : 4, h);
+  cluster_arrive();  // this block has read the others' parts
+  __syncthreads();
+  if (rank <= 16) expand<MT, true, 1>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
+  else if (rank <= 32) expand<MT, false, 1>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
+  else if (rank <= 64) expand<MT, false, 2>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
+  else expand<MT, false, 4>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
+  cluster_wait();
+}
+
+__global__ void __launch_bounds__(kThreads, 2) add_kernel(const __grid_constant__ AddParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  float* copies = reinterpret_cast<float*>(raw);
+  float* part = reinterpret_cast<float*>(raw + kCopyBytes);
+  int* tokens = reinterpret_cast<int*>(raw + kCopyBytes + kPartBytes);
+  pdl_enter();
+  const int4 head = __ldcg(static_cast<const int4*>(p.plan));
+  const int tiles = p.out == p.y ? head.y : head.x;  // in place there is nothing to do for tokens without an adapter
+  const int32_t* order = adapter_order(p.plan, p.batch, p.n);
+  const int cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster, rank_of_block = (int)tc::cluster_ctarank();
+  const int blocks = (int)((p.ad.out + 31) / 32);
+  for (int t0 = 0; t0 < tiles; t0 += clusters) {
+    // the round's tiles; where they are few, as many clusters for each as have a block of outputs per warp
+    const int now = min(tiles - t0, clusters);
+    const int shares = max(1, min(clusters / now, blocks / (kCluster * kWarps)));
+    if (cluster >= now * shares) break;
+    const int4 tile = __ldcg(adapter_tiles(p.plan) + t0 + cluster % now);
+    const int share = (cluster / now) * kCluster + rank_of_block, all = shares * kCluster;
+    const int o0 = (int)((int64_t)share * blocks / all), o1 = (int)((int64_t)(share + 1) * blocks / all);
+    const bool has = tile.x >= 0 && tile.x < p.ad.count;
+    int rank = has ? p.ad.ranks ? __ldg(p.ad.ranks + tile.x) : p.ad.max_rank : 0;
+    rank = rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
+    __syncthreads();
+    if (threadIdx.x < tile.z) tokens[threadIdx.x] = __ldcg(order + tile.y + threadIdx.x);
+    __syncthreads();
+    if (rank == 0) {
+      if (p.out == p.y) continue;
+      const int chunks = (min(32 * o1, (int)p.ad.out) - 32 * o0) / 8;
+      for (int e = threadIdx.x; e < tile.z * chunks; e += kThreads) {
+        const int64_t token = tokens[e / chunks], col = 32 * o0 + 8 * (e % chunks);
+        *reinterpret_cast<uint4*>(p.out + token * p.out_stride + col) = *reinterpret_cast<const uint4*>(p.y + token * p.y_stride + col);
+      }
+      continue;
+    }
+    const float scale = p.ad.scales ? __ldg(p.ad.scales + tile.x) : 1.f;
+    if (tile.z <= 16) tile_of<1>(p, tile, rank, scale, tokens, o0, o1, copies, part);
+    else tile_of<4>(p, tile, rank, scale, tokens, o0, o1, copies, part);
   }
 }
 
 }  // namespace
 
+// Clusters that the device runs at once.
+int adapter_clusters() {
+  static PerDevice<int> of;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  return of.get(dev, [] {
+    if (cudaFuncSetAttribute(add_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, add_kernel, &cfg) != cudaSuccess) return 0;
+    return n;
+  }, 0);
+}
+
 cudaError_t launch_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, int64_t y_stride, uint16_t* out,
                                int64_t out_stride, const trellis_adapters_t& ad, const void* plan, int batch, int n,
                                cudaStream_t st) {
+  const int fit = adapter_clusters();
+  if (fit < 1) return cudaErrorInvalidConfiguration;
+  // no more clusters than there can be shares of tiles
+  const int64_t shares = (ad.out + 31) / 32 / (kCluster * kWarps), most = adapter_max_tiles(batch, n) * (shares < 1 ? 1 : shares);
   const AddParams p{x, y, out, x_stride, y_stride, out_stride, ad, plan, batch, n};
-  const int64_t tiles = adapter_max_tiles(batch, n);
-  return launch_pdl(add_kernel, dim3((unsigned)(tiles < 1024 ? tiles : 1024), kAdapterTile), dim3(kThreads), 0, st, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(most < fit ? most : fit) * kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, add_kernel, p);
 }
 
 }  // namespace trellis
