@@ -33,6 +33,14 @@ __device__ __forceinline__ int scan(int v, int* warps) {
   return Max ? max(v, before) : v + before;
 }
 
+__device__ __forceinline__ int total(int v, int* warps) {
+  v = __reduce_add_sync(0xFFFFFFFFu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xFFFFFFFFu, warps[threadIdx.x & 31]);
+}
+
 // The last of at[0 .. n) (ascending, at[0] = 0) that is at most x.
 __device__ __forceinline__ int last_upto(const int* at, int n, int x) {
   int lo = 0, hi = n;
@@ -45,7 +53,7 @@ __device__ __forceinline__ int last_upto(const int* at, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(const int32_t* __restrict__ adapter, const int32_t* __restrict__ q_start,
-                                                        int batch, int n, void* plan) {
+                                                        int batch, int n, int clusters, void* plan) {
   pdl_enter();
   __shared__ int warps[kThreads / 32];
   __shared__ int ids[kThreads];                      // by sequence
@@ -98,7 +106,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const int32_t* __restric
   __syncthreads();
   const int groups = groups_of_all, tokens = place[batch];
   const int size = t < groups ? group_first[t + 1] - group_first[t] : 0;
-  const int tiles = (size + kAdapterTile - 1) / kAdapterTile;
+  // The longest tile that needs no more rounds than tiles of 64 do: they are taken by `clusters` at a time, and a last round of few
+  // tiles would take as long as a full one.
+  int tile = kAdapterTile;
+  {
+    const auto count_of = [&](int most) { return total((size + most - 1) / most, warps); };
+    const int full = count_of(kAdapterTile), rounds = (full + clusters - 1) / clusters;
+    if (full >= clusters) {
+      int lo = kAdapterLeast, hi = kAdapterTile;  // hi fits
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (count_of(mid) <= rounds * clusters) hi = mid;
+        else lo = mid + 1;
+      }
+      tile = hi;
+    }
+  }
+  const int tiles = (size + tile - 1) / tile;
   const int tiles_upto = scan<false>(tiles, warps);
   if (t < groups) group_tiles[t] = tiles_upto - tiles;
   if (t == groups - 1) group_tiles[groups] = tiles_upto;
@@ -136,9 +160,9 @@ size_t adapter_plan_bytes(int batch, int n) {
 
 cudaError_t launch_adapter_plan(const int32_t* adapter, const int32_t* q_start, int batch, int n, void* plan, cudaStream_t st) {
   const int blocks = (n + kPerBlock - 1) / kPerBlock;
-  const int most = device_sm_count();
+  const int most = device_sm_count(), fit = adapter_clusters(), clusters = fit < 1 ? 1 : fit < kAdapterMaxClusters ? fit : kAdapterMaxClusters;
   return launch_pdl(plan_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, st, adapter, q_start, batch, n,
-                    plan);
+                    clusters, plan);
 }
 
 }  // namespace trellis

@@ -14,10 +14,14 @@ struct AdapterPlanHeader {
   int tiles, with_adapter;  // tiles in all, and of tokens that have an adapter
   int reserved[2];
 };
+constexpr int kAdapterLeast = kAdapterTile / 2;  // tiles are not cut shorter than this to fill a round
+constexpr int kAdapterMaxClusters = 256;
 __host__ __device__ constexpr int64_t adapter_max_tiles(int batch, int n) {
-  // every group of tokens has at most one tile that is not full; a group needs a sequence and a token
-  return n / kAdapterTile + (batch < n ? batch : n);
+  // every group of tokens has at most one tile that is not full, a group needs a sequence and a token, and a round that is
+  // filled up has no more tiles than clusters
+  return n / kAdapterTile + (batch < n ? batch : n) + (n >= kAdapterLeast ? kAdapterMaxClusters : 0);
 }
+int adapter_clusters();  // that add to a projection's output at once on the current device (adapters.cu); 0: none
 __host__ __device__ __forceinline__ const int4* adapter_tiles(const void* plan) {
   return reinterpret_cast<const int4*>(static_cast<const char*>(plan) + sizeof(AdapterPlanHeader));
 }

@@ -23,13 +23,18 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kGroup = 32;             // rows of A that a warp multiplies with
-constexpr int kCopyLd = kGroup + 4;    // floats from token to token of a warp's products
-constexpr int kPartLd = kAdapterMaxRank + 8;
-constexpr int kCopyBytes = kWarps * kAdapterTile * kCopyLd * 4;
-constexpr int kPartBytes = kAdapterTile * kPartLd * 4;
-constexpr int kSmem = kCopyBytes + kPartBytes + kAdapterTile * 4;
-static_assert(kAdapterTile * kAdapterMaxRank * 4 <= kCopyBytes, "the fragments of h take the products' place");
+constexpr int kGroup = 32;                 // rows of A that a warp multiplies with
+constexpr int kUnit = 32;                  // tokens that a warp multiplies them with, where a tile has more than 16
+constexpr int kCopyLd = kGroup + 4;        // floats from token to token of a warp's products
+constexpr int kCopy = kUnit * kCopyLd;     // floats of a warp's products
+constexpr int kCopyBytes = kWarps * kCopy * 4;
+constexpr int kRing = 64 * 1024;           // copies in flight
+constexpr int kWarpRing = kRing / kWarps;
+constexpr int kSmem = kCopyBytes + kRing + kAdapterTile * 4;
+// With more than 64 ranks every warp's products are part of the sum, and h takes half of the ring.
+constexpr int kWideRing = kRing / 2 / kWarps;
+static_assert(kAdapterTile * kAdapterMaxRank * 4 <= kRing / 2, "h, as fragments");
+static_assert(kAdapterTile * 64 * 4 <= kCopyBytes / 2, "the second half of the warps' products gives way to h");
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
 
 struct AddParams {
@@ -57,20 +62,40 @@ __device__ __forceinline__ float2 ld_cluster(const float* p, uint32_t rank) {
 // The first `n` of the two bf16 numbers of w, the others zero.
 __device__ __forceinline__ uint32_t first_of(uint32_t w, int n) { return n >= 2 ? w : n == 1 ? w & 0xFFFFu : 0u; }
 
-// h of the block's part of the inputs, for 16 MT tokens: into part[token][rank].
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Where the sum over a block's warps of h[token][rank] lies: with the products of the first of them.
+template <int MT>
+__device__ __forceinline__ int part_at(int t, int r, int groups) {
+  constexpr int kSide = MT > 1 ? 2 : 1;  // warps side by side along the tokens
+  return ((t / kUnit) + kSide * (r / kGroup)) * kCopy + (MT > 1 ? t % kUnit : t) * kCopyLd + r % kGroup;
+}
+__device__ __forceinline__ int groups_of(int rank) { return rank <= kGroup ? 1 : rank <= 2 * kGroup ? 2 : 4; }
+
+// h of the block's part of the inputs, for 16 MT tokens.  Warps: along the tokens, the ranks, and what is left along the inputs.
 template <int MT>
 __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, int rank, int count, const int* tokens, int rank_of_block,
-                                       float* copies, float* part) {
+                                       float* copies) {
+  constexpr int kSide = MT > 1 ? 2 : 1, WT = MT > 1 ? 2 : 1;  // warps along the tokens, token tiles of a warp
+  constexpr int kAhead = MT > 1 ? 2 : 3;                     // blocks of 32 inputs whose loads are in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int groups = rank <= kGroup ? 1 : rank <= 2 * kGroup ? 2 : 4, splits = kWarps / groups;  // of rows of A; of the inputs
-  const int group = warp % groups, split = warp / groups;
+  const int groups = groups_of(rank), splits = kWarps / kSide / groups;
+  const int side = warp % kSide, group = warp / kSide % groups, split = warp / kSide / groups;
   const int blocks = (int)((p.ad.in + 31) / 32);
   const int k0 = (int)((int64_t)rank_of_block * blocks / kCluster), k1 = (int)((int64_t)(rank_of_block + 1) * blocks / kCluster);
-  const uint16_t *x[2 * MT], *w[4];
-  bool has_x[2 * MT], has_w[4];
+  const uint16_t *x[2 * WT], *w[4];
+  bool has_x[2 * WT], has_w[4];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i) {
-    const int t = 8 * i + g;
+  for (int i = 0; i < 2 * WT; ++i) {
+    const int t = side * kUnit + 8 * i + g;
     has_x[i] = t < count;
     x[i] = p.x + (int64_t)tokens[has_x[i] ? t : 0] * p.x_stride + 8 * q;
   }
@@ -80,69 +105,77 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
     has_w[j] = r < rank;
     w[j] = a + (int64_t)(has_w[j] ? r : 0) * p.ad.in + 8 * q;
   }
-  const int tiles = min(4, (rank - group * kGroup + 7) / 8);  // of 8 rows of A; may be none
-  float acc[MT][4][4];
+  const int tiles = side * kUnit < count ? min(4, (rank - group * kGroup + 7) / 8) : 0;  // of 8 rows of A; may be none
+  float acc[WT][4][4];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < WT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
   if (tiles > 0)
-    for (int k = k0 + split; k < k1; k += splits) {
-      const bool in = 32 * k + 8 * q < p.ad.in;
-      uint4 u[2 * MT], v[4];
+    for (int k = k0 + split; k < k1; k += splits * kAhead) {
+      uint4 u[kAhead][2 * WT], v[kAhead][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = make_uint4(0, 0, 0, 0);
-        if (in && has_w[j]) v[j] = __ldg(reinterpret_cast<const uint4*>(w[j] + 32 * k));
+      for (int s = 0; s < kAhead; ++s) {
+        const int ks = k + s * splits;
+        const bool in = ks < k1 && 32 * ks + 8 * q < p.ad.in;
+#pragma unroll
+        for (int i = 0; i < 2 * WT; ++i) {
+          u[s][i] = make_uint4(0, 0, 0, 0);
+          if (in && has_x[i]) u[s][i] = *reinterpret_cast<const uint4*>(x[i] + 32 * ks);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[s][j] = make_uint4(0, 0, 0, 0);
+          if (in && has_w[j]) v[s][j] = __ldg(reinterpret_cast<const uint4*>(w[j] + 32 * ks));
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (in && has_x[i]) u[i] = *reinterpret_cast<const uint4*>(x[i] + 32 * k);
-      }
+      for (int s = 0; s < kAhead; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < tiles)
+        for (int j = 0; j < 4; ++j)
+          if (j < tiles)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            mma(acc[i][j], u[2 * i].x, u[2 * i + 1].x, u[2 * i].y, u[2 * i + 1].y, v[j].x, v[j].y);
-            mma(acc[i][j], u[2 * i].z, u[2 * i + 1].z, u[2 * i].w, u[2 * i + 1].w, v[j].z, v[j].w);
-          }
+            for (int i = 0; i < WT; ++i) {
+              mma(acc[i][j], u[s][2 * i].x, u[s][2 * i + 1].x, u[s][2 * i].y, u[s][2 * i + 1].y, v[s][j].x, v[s][j].y);
+              mma(acc[i][j], u[s][2 * i].z, u[s][2 * i + 1].z, u[s][2 * i].w, u[s][2 * i + 1].w, v[s][j].z, v[s][j].w);
+            }
     }
-  float* mine = copies + warp * (kAdapterTile * kCopyLd);
+  float* mine = copies + warp * kCopy;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < WT; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       *reinterpret_cast<float2*>(mine + (16 * i + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][0], acc[i][j][1]);
       *reinterpret_cast<float2*>(mine + (16 * i + 8 + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][2], acc[i][j][3]);
     }
   __syncthreads();
-  const int wide = groups * kGroup;  // ranks come out padded with zeros
-  for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
-    const int t = e / wide, r = e - t * wide;
-    float s = 0.f;
-    for (int c = 0; c < splits; ++c) s += copies[((r / kGroup) + c * groups) * (kAdapterTile * kCopyLd) + t * kCopyLd + r % kGroup];
-    part[t * kPartLd + r] = s;
+  if (splits > 1) {
+    const int wide = groups * kGroup;  // ranks come out padded with zeros
+    for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
+      const int at = part_at<MT>(e / wide, e % wide, groups);
+      float s = copies[at];
+      for (int c = 1; c < splits; ++c) s += copies[at + c * groups * kSide * kCopy];
+      copies[at] = s;
+    }
   }
 }
 
-// The sums over the cluster, as fragments: word of (token tile, block of 32 (NARROW: 16) ranks, high or low part, lane).
+// The sums over the cluster, as fragments: word of (token tile, block of 32 (NARROW: 16) ranks, step, high or low part, lane).
 template <bool NARROW>
 __device__ __forceinline__ uint32_t* fragment(uint32_t* h, int mt, int blocks, int kb, int step, int low) {
   return NARROW ? h + (mt * 2 + low) * 128 : h + ((mt * blocks + kb) * 4 + step * 2 + low) * 128;
 }
 template <int MT, bool NARROW>
-__device__ __forceinline__ void gather(const float* part, int blocks, uint32_t* h) {
+__device__ __forceinline__ void gather(const float* copies, int blocks, uint32_t* h) {
   const int wide = blocks * (NARROW ? 16 : 32) / 2;  // pairs of ranks
   for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
     const int t = e / wide, r = (e - t * wide) * 2;
     float2 s = make_float2(0.f, 0.f);
     float2 v[kCluster];
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(part + t * kPartLd + r, c);
+    for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(copies + part_at<MT>(t, r, 0), c);
 #pragma unroll
     for (int c = 0; c < kCluster; ++c) {
       s.x += v[c].x;
@@ -160,107 +193,185 @@ __device__ __forceinline__ void gather(const float* part, int blocks, uint32_t* 
   }
 }
 
-// The outputs of blocks o0 + warp, + kWarps, .. < o1 of 32, for 16 MT tokens.
+// The second product: outputs of blocks o0 + warp, + kWarps, .. < o1 of 32, for 16 MT tokens.  What a lane needs of y (few tokens: and
+// of B) it copies itself into its warp's ring, some blocks ahead; the first ones are copied before h is there.
 template <int MT, bool NARROW, int NB>
-__device__ __forceinline__ void expand(const AddParams& p, const uint16_t* b, int rank, float scale, int count, const int* tokens,
-                                       uint32_t* h, int o0, int o1) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const uint4* hl = reinterpret_cast<const uint4*>(h) + lane;
-  const int left = rank - (NARROW ? 4 : 8) * q;  // ranks from this lane's first on
-  const bool ragged = rank % (NARROW ? 4 : 8) != 0;
-#pragma unroll 1
-  for (int o = o0 + warp; o < o1; o += kWarps) {
-    uint4 v[4][NB];
+struct Expand {
+  static constexpr bool kRingB = MT == 1 && NB <= 2;  // B goes through the ring too, else it is loaded one block ahead
+  static constexpr int kY = 2 * MT * 512, kB = kRingB ? 4 * NB * (NARROW ? 256 : 512) : 0, kStage = kY + kB;
+  static constexpr int kStages = (NB == 4 ? kWideRing : kWarpRing) / kStage;
+  static_assert(kStages >= 1, "a block");
+  const AddParams& p;
+  const uint16_t* b;
+  const int* tokens;
+  uint8_t* ring;  // the warp's
+  int rank, count, o, o1, lane, g, q, left, stage;
+
+  __device__ __forceinline__ Expand(const AddParams& p_, const uint16_t* b_, int rank_, int count_, const int* tokens_, uint8_t* rings, int o0,
+                                    int o1_)
+      : p(p_), b(b_), tokens(tokens_), rank(rank_), count(count_), o1(o1_), stage(0) {
+    const int warp = threadIdx.x >> 5;
+    lane = threadIdx.x & 31;
+    g = lane >> 2;
+    q = lane & 3;
+    o = o0 + warp;
+    left = rank - (NARROW ? 4 : 8) * q;
+    ring = rings + warp * (NB == 4 ? kWideRing : kWarpRing);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t row = 32 * (int64_t)o + 8 * (g >> 1) + 2 * j + (g & 1);
+    for (int s = 0; s < kStages; ++s) copy(o + s * kWarps, s);
+  }
+  // This lane's numbers of B for tile j of 8 outputs and a block of ranks, where there are any.
+  __device__ __forceinline__ const uint16_t* weights(int block, int j, int kb) const {
+    const int64_t row = 32 * (int64_t)block + 8 * (g >> 1) + 2 * j + (g & 1);
+    return row < p.ad.out && left > 32 * kb ? b + row * p.ad.max_rank + (NARROW ? 4 : 8) * q + 32 * kb : nullptr;
+  }
+  __device__ __forceinline__ void copy(int block, int s) {
+    if (block < o1) {
+      const int col = 32 * block + 8 * q;
+      uint8_t* to = ring + s * kStage;
+      if (col < p.ad.out)
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+          if (8 * i + g < count) cp_async16(to + (i * 32 + lane) * 16, p.y + (int64_t)tokens[8 * i + g] * p.y_stride + col);
+      if constexpr (kRingB)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb)
+            if (const uint16_t* at = weights(block, j, kb)) {
+              if (NARROW) cp_async8(to + kY + (j * 32 + lane) * 8, at);
+              else cp_async16(to + kY + ((j * NB + kb) * 32 + lane) * 16, at);
+            }
+    }
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void load(int block, uint4 (&v)[4][NB]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int kb = 0; kb < NB; ++kb) {
         v[j][kb] = make_uint4(0, 0, 0, 0);
-        if (row < p.ad.out && left > 32 * kb) {
-          const uint16_t* at = b + row * p.ad.max_rank + (NARROW ? 4 : 8) * q + 32 * kb;
-          if (NARROW) {
-            const uint2 two = __ldg(reinterpret_cast<const uint2*>(at));
-            v[j][kb].x = two.x;
-            v[j][kb].y = two.y;
-          } else {
-            v[j][kb] = __ldg(reinterpret_cast<const uint4*>(at));
-          }
+        const uint16_t* at = block < o1 ? weights(block, j, kb) : nullptr;
+        if (!at) continue;
+        if (NARROW) {
+          const uint2 two = __ldg(reinterpret_cast<const uint2*>(at));
+          v[j][kb].x = two.x;
+          v[j][kb].y = two.y;
+        } else {
+          v[j][kb] = __ldg(reinterpret_cast<const uint4*>(at));
         }
       }
-    }
-    const int col = 32 * o + 8 * q;
-    const bool in = col < p.ad.out;
-    uint4 u[2 * MT];
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      const int t = 8 * i + g;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (in && t < count) u[i] = *reinterpret_cast<const uint4*>(p.y + (int64_t)tokens[t] * p.y_stride + col);
-    }
-    if (ragged)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int kb = 0; kb < NB; ++kb) {
-          const int n = left - 32 * kb;
-          v[j][kb] = make_uint4(first_of(v[j][kb].x, n), first_of(v[j][kb].y, n - 2), first_of(v[j][kb].z, n - 4), first_of(v[j][kb].w, n - 6));
-        }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (16 * i >= count) break;
-      float acc[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < NB; ++kb)
-#pragma unroll
-        for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
-          const uint4 a = hl[(NARROW ? i * 2 + f : (i * NB + kb) * 4 + f) * 32];
-          const bool second = !NARROW && f >= 2;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
-        }
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int t = 16 * i + 8 * half + g;
-        if (!in || t >= count) continue;
-        const uint4 y = u[2 * i + half];
-        const auto add = [&](uint32_t w, int j) {
-          return pack_bf16x2(fmaf(scale, acc[j][2 * half], bf16lo_to_f32(w)), fmaf(scale, acc[j][2 * half + 1], bf16hi_to_f32(w)));
-        };
-        *reinterpret_cast<uint4*>(p.out + (int64_t)tokens[t] * p.out_stride + col) = make_uint4(add(y.x, 0), add(y.y, 1), add(y.z, 2), add(y.w, 3));
-      }
-    }
   }
-}
+  __device__ __forceinline__ void run(const uint32_t* h, float scale) {
+    const uint4* hl = reinterpret_cast<const uint4*>(h) + lane;
+    const bool ragged = rank % (NARROW ? 4 : 8) != 0;
+    uint4 v[4][NB], next[4][NB];
+    if constexpr (!kRingB && NB < 4) load(o, next);
+#pragma unroll 1
+    for (; o < o1; o += kWarps) {
+      cp_async_wait<kStages - 1>();
+      const uint8_t* from = ring + stage * kStage;
+      uint4 u[2 * MT];
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) u[i] = *reinterpret_cast<const uint4*>(from + (i * 32 + lane) * 16);
+      if constexpr (kRingB) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb) {
+            v[j][kb] = make_uint4(0, 0, 0, 0);
+            if (!weights(o, j, kb)) continue;
+            if (NARROW) {
+              const uint2 two = *reinterpret_cast<const uint2*>(from + kY + (j * 32 + lane) * 8);
+              v[j][kb].x = two.x;
+              v[j][kb].y = two.y;
+            } else {
+              v[j][kb] = *reinterpret_cast<const uint4*>(from + kY + ((j * NB + kb) * 32 + lane) * 16);
+            }
+          }
+      } else if constexpr (NB < 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb) v[j][kb] = next[j][kb];
+        load(o + kWarps, next);
+      } else {
+        load(o, v);
+      }
+      copy(o + kStages * kWarps, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (ragged)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb) {
+            const int n = left - 32 * kb;
+            v[j][kb] = make_uint4(first_of(v[j][kb].x, n), first_of(v[j][kb].y, n - 2), first_of(v[j][kb].z, n - 4), first_of(v[j][kb].w, n - 6));
+          }
+      const int col = 32 * o + 8 * q;
+      const bool in = col < p.ad.out;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (16 * i >= count) break;
+        float acc[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+          for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
+            const uint4 a = hl[(NARROW ? i * 2 + f : (i * NB + kb) * 4 + f) * 32];
+            const bool second = !NARROW && f >= 2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
+          }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int t = 16 * i + 8 * half + g;
+          if (!in || t >= count) continue;
+          const uint4 y = u[2 * i + half];
+          const auto add = [&](uint32_t w, int j) {
+            return pack_bf16x2(fmaf(scale, acc[j][2 * half], bf16lo_to_f32(w)), fmaf(scale, acc[j][2 * half + 1], bf16hi_to_f32(w)));
+          };
+          *reinterpret_cast<uint4*>(p.out + (int64_t)tokens[t] * p.out_stride + col) = make_uint4(add(y.x, 0), add(y.y, 1), add(y.z, 2), add(y.w, 3));
+        }
+      }
+    }
+    cp_async_wait<0>();
+  }
+};
 
-template <int MT>
+template <int MT, bool NARROW, int NB>
 __device__ __forceinline__ void tile_of(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
-                                        float* copies, float* part) {
+                                        float* copies, uint8_t* ring) {
   const uint16_t *a = p.ad.a + (int64_t)tile.x * p.ad.max_rank * p.ad.in, *b = p.ad.b + (int64_t)tile.x * p.ad.out * p.ad.max_rank;
-  uint32_t* h = reinterpret_cast<uint32_t*>(copies);
-  shrink<MT>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), copies, part);
+  uint32_t* h = reinterpret_cast<uint32_t*>(NB == 4 ? ring + kRing / 2 : reinterpret_cast<uint8_t*>(copies) + kCopyBytes / 2);
+  Expand<MT, NARROW, NB> second(p, b, rank, tile.z, tokens, ring, o0, o1);
+  shrink<MT>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), copies);
   cluster_arrive();
   cluster_wait();
-  if (rank <= 16) gather<MT, true>(part, 1, h);
-  else gather<MT, false>(part, rank <= 32 ? 1 : rank <= 64 ? 2 : 4, h);
-  cluster_arrive();  // this block has read the others' parts
+  gather<MT, NARROW>(copies, NB, h);
+  cluster_arrive();  // this block has read the others' sums
   __syncthreads();
-  if (rank <= 16) expand<MT, true, 1>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
-  else if (rank <= 32) expand<MT, false, 1>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
-  else if (rank <= 64) expand<MT, false, 2>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
-  else expand<MT, false, 4>(p, b, rank, scale, tile.z, tokens, h, o0, o1);
+  second.run(h, scale);
   cluster_wait();
+}
+template <int MT>
+__device__ __forceinline__ void tile_by_rank(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
+                                             float* copies, uint8_t* ring) {
+  if (rank <= 16) tile_of<MT, true, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  else if (rank <= 32) tile_of<MT, false, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  else if (rank <= 64) tile_of<MT, false, 2>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  else tile_of<MT, false, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
 }
 
 __global__ void __launch_bounds__(kThreads, 2) add_kernel(const __grid_constant__ AddParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   float* copies = reinterpret_cast<float*>(raw);
-  float* part = reinterpret_cast<float*>(raw + kCopyBytes);
-  int* tokens = reinterpret_cast<int*>(raw + kCopyBytes + kPartBytes);
+  uint8_t* ring = raw + kCopyBytes;
+  int* tokens = reinterpret_cast<int*>(raw + kCopyBytes + kRing);
   pdl_enter();
   const int4 head = __ldcg(static_cast<const int4*>(p.plan));
   const int tiles = p.out == p.y ? head.y : head.x;  // in place there is nothing to do for tokens without an adapter
@@ -291,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 2) add_kernel(const __grid_constant_
       continue;
     }
     const float scale = p.ad.scales ? __ldg(p.ad.scales + tile.x) : 1.f;
-    if (tile.z <= 16) tile_of<1>(p, tile, rank, scale, tokens, o0, o1, copies, part);
-    else tile_of<4>(p, tile, rank, scale, tokens, o0, o1, copies, part);
+    if (tile.z <= 16) tile_by_rank<1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+    else tile_by_rank<4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
   }
 }
 
