@@ -22,7 +22,7 @@ namespace trellis {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kCluster = 4;
 constexpr int kGroup = 32;                 // rows of A that a warp multiplies with
 constexpr int kUnit = 32;                  // tokens that a warp multiplies them with, where a tile has more than 16
 constexpr int kCopyLd = kGroup + 4;        // floats from token to token of a warp's products
