@@ -23,18 +23,16 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 4;
-constexpr int kGroup = 32;                 // rows of A that a warp multiplies with
-constexpr int kUnit = 32;                  // tokens that a warp multiplies them with, where a tile has more than 16
-constexpr int kCopyLd = kGroup + 4;        // floats from token to token of a warp's products
-constexpr int kCopy = kUnit * kCopyLd;     // floats of a warp's products
-constexpr int kCopyBytes = kWarps * kCopy * 4;
+constexpr int kCopyLd = 36;                // floats from token to token of a warp's products of 32 ranks: bank conflicts of two
+constexpr int kCopy = 64 * kCopyLd;        // floats of a warp's products: 64 tokens by 32 ranks, or 32 by 64
+constexpr int kCopyBytes = kWarps / 2 * kCopy * 4;
 constexpr int kRing = 64 * 1024;           // copies in flight
 constexpr int kWarpRing = kRing / kWarps;
 constexpr int kSmem = kCopyBytes + kRing + kAdapterTile * 4;
-// With more than 64 ranks every warp's products are part of the sum, and h takes half of the ring.
-constexpr int kWideRing = kRing / 2 / kWarps;
+// With more than 64 ranks h takes half of each warp's ring for the second product.
+constexpr int kWideRing = kWarpRing / 2;
 static_assert(kAdapterTile * kAdapterMaxRank * 4 <= kRing / 2, "h, as fragments");
-static_assert(kAdapterTile * 64 * 4 <= kCopyBytes / 2, "the second half of the warps' products gives way to h");
+static_assert(kAdapterTile * 64 * 4 <= kCopyBytes / 2, "the second half of the products gives way to h");
 static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
 
 struct AddParams {
@@ -72,110 +70,166 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Where the sum over a block's warps of h[token][rank] lies: with the products of the first of them.
-template <int MT>
-__device__ __forceinline__ int part_at(int t, int r, int groups) {
-  constexpr int kSide = MT > 1 ? 2 : 1;  // warps side by side along the tokens
-  return ((t / kUnit) + kSide * (r / kGroup)) * kCopy + (MT > 1 ? t % kUnit : t) * kCopyLd + r % kGroup;
-}
-__device__ __forceinline__ int groups_of(int rank) { return rank <= kGroup ? 1 : rank <= 2 * kGroup ? 2 : 4; }
+// How a block's warps share the first product: each has a part of the inputs and, of the tile's tokens and ranks,
+//   up to 16 tokens  all tokens, 32 ranks
+//   more             64 tokens by 32 ranks, or with more than 32 ranks 32 tokens by 64
+// Where the sum over them of h[token][rank] lies: with the products of the first warp that has it.
+template <int MT, int NB>
+struct Share {
+  static constexpr int Tokens = MT == 1 ? 16 : NB == 1 ? 64 : 32, Ranks = MT > 1 && NB > 1 ? 64 : 32;
+  static constexpr int Sides = 16 * MT / Tokens, Groups = 32 * NB / Ranks, Splits = kWarps / (Sides * Groups);
+  static __device__ __forceinline__ int at(int t, int r) {  // pairs of ranks stay pairs
+    return (t / Tokens + Sides * (r / Ranks)) * kCopy + (Ranks == 64 ? (t % Tokens) * 2 + r / 32 % 2 : t % Tokens) * kCopyLd + r % 32;
+  }
+};
 
-// h of the block's part of the inputs, for 16 MT tokens.  Warps: along the tokens, the ranks, and what is left along the inputs.
-template <int MT>
+// h of the block's part of the inputs, for 16 MT tokens.  Where tokens are many, a lane copies what it needs of x into its warp's ring,
+// some blocks of 32 inputs ahead (x comes from HBM; loads into registers kept half as many bytes in flight); A is loaded one block ahead.
+template <int MT, bool NARROW, int NB>
 __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, int rank, int count, const int* tokens, int rank_of_block,
-                                       float* copies) {
-  constexpr int kSide = MT > 1 ? 2 : 1, WT = MT > 1 ? 2 : 1;  // warps along the tokens, token tiles of a warp
-  constexpr int kAhead = MT > 1 ? 2 : 3;                     // blocks of 32 inputs whose loads are in flight
+                                       uint8_t* rings, float* copies) {
+  using H = Share<MT, NB>;
+  constexpr int WT = H::Tokens / 16, NT = NARROW ? 2 : H::Ranks / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int groups = groups_of(rank), splits = kWarps / kSide / groups;
-  const int side = warp % kSide, group = warp / kSide % groups, split = warp / kSide / groups;
+  const int side = warp % H::Sides, group = warp / H::Sides % H::Groups, split = warp / H::Sides / H::Groups;
   const int blocks = (int)((p.ad.in + 31) / 32);
   const int k0 = (int)((int64_t)rank_of_block * blocks / kCluster), k1 = (int)((int64_t)(rank_of_block + 1) * blocks / kCluster);
-  const uint16_t *x[2 * WT], *w[4];
-  bool has_x[2 * WT], has_w[4];
+  const int t0 = side * H::Tokens, r0 = group * H::Ranks;
+  const uint16_t* w = a + (int64_t)(r0 + g) * p.ad.in + 8 * q;
+  const auto row_of = [&](int i) { return p.x + (int64_t)tokens[t0 + 8 * i + g] * p.x_stride + 8 * q; };
+  const auto load_a = [&](int k, uint4 (&v)[NT]) {
+    const bool in = k < k1 && 32 * k + 8 * q < p.ad.in;
 #pragma unroll
-  for (int i = 0; i < 2 * WT; ++i) {
-    const int t = side * kUnit + 8 * i + g;
-    has_x[i] = t < count;
-    x[i] = p.x + (int64_t)tokens[has_x[i] ? t : 0] * p.x_stride + 8 * q;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = group * kGroup + 8 * j + g;
-    has_w[j] = r < rank;
-    w[j] = a + (int64_t)(has_w[j] ? r : 0) * p.ad.in + 8 * q;
-  }
-  const int tiles = side * kUnit < count ? min(4, (rank - group * kGroup + 7) / 8) : 0;  // of 8 rows of A; may be none
-  float acc[WT][4][4];
+    for (int j = 0; j < NT; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (in && r0 + 8 * j + g < rank) v[j] = __ldg(reinterpret_cast<const uint4*>(w + (int64_t)(8 * j) * p.ad.in + 32 * k));
+    }
+  };
+  float acc[WT][NT][4];
 #pragma unroll
   for (int i = 0; i < WT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-  if (tiles > 0)
-    for (int k = k0 + split; k < k1; k += splits * kAhead) {
-      uint4 u[kAhead][2 * WT], v[kAhead][4];
+  const auto multiply = [&](const uint4 (&u)[2 * WT], const uint4 (&v)[NT]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < WT; ++i) {
+        mma(acc[i][j], u[2 * i].x, u[2 * i + 1].x, u[2 * i].y, u[2 * i + 1].y, v[j].x, v[j].y);
+        mma(acc[i][j], u[2 * i].z, u[2 * i + 1].z, u[2 * i].w, u[2 * i + 1].w, v[j].z, v[j].w);
+      }
+  };
+  if (MT > 1) {
+    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage;
+    uint8_t* ring = rings + warp * kWarpRing;
+    const auto copy = [&](int k, int s) {
+      if (k < k1 && 32 * k + 8 * q < p.ad.in)
+#pragma unroll
+        for (int i = 0; i < 2 * WT; ++i)
+          if (t0 + 8 * i + g < count) cp_async16(ring + s * kStage + (i * 32 + lane) * 16, row_of(i) + 32 * k);
+      cp_async_commit();
+    };
+    int k = k0 + split, stage = 0;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) copy(k + s * H::Splits, s);
+    uint4 v[NT];
+    load_a(k, v);
+#pragma unroll 1
+    for (; k < k1; k += H::Splits) {
+      uint4 next[NT], u[2 * WT];
+      if (NT <= 4) load_a(k + H::Splits, next);
+      cp_async_wait<kStages - 1>();
+      const bool in = 32 * k + 8 * q < p.ad.in;
+#pragma unroll
+      for (int i = 0; i < 2 * WT; ++i) {
+        u[i] = *reinterpret_cast<const uint4*>(ring + stage * kStage + (i * 32 + lane) * 16);
+        if (!in || t0 + 8 * i + g >= count) u[i] = make_uint4(0, 0, 0, 0);
+      }
+      copy(k + kStages * H::Splits, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      multiply(u, v);
+      if (NT <= 4) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) v[j] = next[j];
+      } else {
+        load_a(k + H::Splits, v);
+      }
+    }
+    cp_async_wait<0>();
+  } else {
+    constexpr int kAhead = 3;  // blocks whose loads are in flight
+    for (int k = k0 + split; k < k1; k += H::Splits * kAhead) {
+      uint4 u[kAhead][2 * WT], v[kAhead][NT];
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) {
-        const int ks = k + s * splits;
+        const int ks = k + s * H::Splits;
         const bool in = ks < k1 && 32 * ks + 8 * q < p.ad.in;
 #pragma unroll
         for (int i = 0; i < 2 * WT; ++i) {
           u[s][i] = make_uint4(0, 0, 0, 0);
-          if (in && has_x[i]) u[s][i] = *reinterpret_cast<const uint4*>(x[i] + 32 * ks);
+          if (in && t0 + 8 * i + g < count) u[s][i] = *reinterpret_cast<const uint4*>(row_of(i) + 32 * ks);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[s][j] = make_uint4(0, 0, 0, 0);
-          if (in && has_w[j]) v[s][j] = __ldg(reinterpret_cast<const uint4*>(w[j] + 32 * ks));
-        }
+        load_a(ks, v[s]);
       }
 #pragma unroll
-      for (int s = 0; s < kAhead; ++s)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < tiles)
-#pragma unroll
-            for (int i = 0; i < WT; ++i) {
-              mma(acc[i][j], u[s][2 * i].x, u[s][2 * i + 1].x, u[s][2 * i].y, u[s][2 * i + 1].y, v[s][j].x, v[s][j].y);
-              mma(acc[i][j], u[s][2 * i].z, u[s][2 * i + 1].z, u[s][2 * i].w, u[s][2 * i + 1].w, v[s][j].z, v[s][j].w);
-            }
+      for (int s = 0; s < kAhead; ++s) multiply(u[s], v[s]);
     }
-  float* mine = copies + warp * kCopy;
+  }
+  // The sum over the warps that share tokens and ranks: half of those that are left hand theirs to the others.
+  const auto at = [&](int i, int half, int j) {
+    return (MT > 1 && H::Ranks == 64 ? (16 * i + 8 * half + g) * 2 + j / 4 : 16 * i + 8 * half + g) * kCopyLd + j % 4 * 8 + 2 * q;
+  };
+  const int mine = side + H::Sides * group;
+#pragma unroll 1
+  for (int left = H::Splits; left >= 1; left /= 2) {
+    const int half = left / 2;  // splits half .. left - 1 write, 0 .. half - 1 add; at last split 0 writes the sum
+    float* to = copies + (left == 1 ? mine : mine + H::Sides * H::Groups * (split - half)) * kCopy;
+    if (left == 1 ? split == 0 : split >= half && split < left)
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
+      for (int i = 0; i < WT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<float2*>(mine + (16 * i + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][0], acc[i][j][1]);
-      *reinterpret_cast<float2*>(mine + (16 * i + 8 + g) * kCopyLd + 8 * j + 2 * q) = make_float2(acc[i][j][2], acc[i][j][3]);
+        for (int j = 0; j < NT; ++j) {
+          *reinterpret_cast<float2*>(to + at(i, 0, j)) = make_float2(acc[i][j][0], acc[i][j][1]);
+          *reinterpret_cast<float2*>(to + at(i, 1, j)) = make_float2(acc[i][j][2], acc[i][j][3]);
+        }
+    if (left == 1) break;
+    __syncthreads();
+    if (split < half) {
+      const float* from = copies + (mine + H::Sides * H::Groups * split) * kCopy;
+#pragma unroll
+      for (int i = 0; i < WT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const float2 x = *reinterpret_cast<const float2*>(from + at(i, 0, j)), y = *reinterpret_cast<const float2*>(from + at(i, 1, j));
+          acc[i][j][0] += x.x;
+          acc[i][j][1] += x.y;
+          acc[i][j][2] += y.x;
+          acc[i][j][3] += y.y;
+        }
     }
-  __syncthreads();
-  if (splits > 1) {
-    const int wide = groups * kGroup;  // ranks come out padded with zeros
-    for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
-      const int at = part_at<MT>(e / wide, e % wide, groups);
-      float s = copies[at];
-      for (int c = 1; c < splits; ++c) s += copies[at + c * groups * kSide * kCopy];
-      copies[at] = s;
-    }
+    __syncthreads();
   }
 }
 
-// The sums over the cluster, as fragments: word of (token tile, block of 32 (NARROW: 16) ranks, step, high or low part, lane).
-template <bool NARROW>
-__device__ __forceinline__ uint32_t* fragment(uint32_t* h, int mt, int blocks, int kb, int step, int low) {
-  return NARROW ? h + (mt * 2 + low) * 128 : h + ((mt * blocks + kb) * 4 + step * 2 + low) * 128;
+// The sums over the cluster, as fragments: words of (token tile, block of 32 (NARROW: 16) ranks, step, high or low part), a lane's four
+// together.  Blocks of 512 words lie one behind the other, or with more than 64 ranks two in the second half of each warp's ring.
+template <bool NARROW, int NB>
+__device__ __forceinline__ int fragment(int mt, int kb, int step, int low) {
+  if (NARROW) return (mt * 2 + low) * 128;
+  const int block = mt * NB + kb;
+  return (NB == 4 ? (block >> 1) * (kWarpRing / 4) + kWideRing / 4 + (block & 1) * 512 : block * 512) + (step * 2 + low) * 128;
 }
-template <int MT, bool NARROW>
-__device__ __forceinline__ void gather(const float* copies, int blocks, uint32_t* h) {
-  const int wide = blocks * (NARROW ? 16 : 32) / 2;  // pairs of ranks
+template <int MT, bool NARROW, int NB>
+__device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
+  constexpr int wide = NB * (NARROW ? 16 : 32) / 2;  // pairs of ranks
   for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
     const int t = e / wide, r = (e - t * wide) * 2;
     float2 s = make_float2(0.f, 0.f);
     float2 v[kCluster];
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(copies + part_at<MT>(t, r, 0), c);
+    for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(copies + Share<MT, NB>::at(t, r), c);
 #pragma unroll
     for (int c = 0; c < kCluster; ++c) {
       s.x += v[c].x;
@@ -188,13 +242,13 @@ __device__ __forceinline__ void gather(const float* copies, int blocks, uint32_t
     const int row = t & 15, kb = NARROW ? 0 : r >> 5;
     const int q = NARROW ? r >> 2 : (r & 31) >> 3, step = NARROW ? 0 : (r & 7) >> 2, pair = (r & 3) >> 1;
     const int word = ((row & 7) * 4 + q) * 4 + (row >> 3) + 2 * pair;
-    fragment<NARROW>(h, t >> 4, blocks, kb, step, 0)[word] = (x >> 16) | y;
-    fragment<NARROW>(h, t >> 4, blocks, kb, step, 1)[word] = pack_bf16x2(lx, ly);
+    h[fragment<NARROW, NB>(t >> 4, kb, step, 0) + word] = (x >> 16) | y;
+    h[fragment<NARROW, NB>(t >> 4, kb, step, 1) + word] = pack_bf16x2(lx, ly);
   }
 }
 
 // The second product: outputs of blocks o0 + warp, + kWarps, .. < o1 of 32, for 16 MT tokens.  What a lane needs of y (few tokens: and
-// of B) it copies itself into its warp's ring, some blocks ahead; the first ones are copied before h is there.
+// of B) it copies itself into its warp's ring, some blocks ahead; the first ones before h is there.
 template <int MT, bool NARROW, int NB>
 struct Expand {
   static constexpr bool kRingB = MT == 1 && NB <= 2;  // B goes through the ring too, else it is loaded one block ahead
@@ -216,7 +270,9 @@ struct Expand {
     q = lane & 3;
     o = o0 + warp;
     left = rank - (NARROW ? 4 : 8) * q;
-    ring = rings + warp * (NB == 4 ? kWideRing : kWarpRing);
+    ring = rings + warp * kWarpRing;
+  }
+  __device__ __forceinline__ void start() {
 #pragma unroll
     for (int s = 0; s < kStages; ++s) copy(o + s * kWarps, s);
   }
@@ -263,7 +319,7 @@ struct Expand {
       }
   }
   __device__ __forceinline__ void run(const uint32_t* h, float scale) {
-    const uint4* hl = reinterpret_cast<const uint4*>(h) + lane;
+    const uint32_t* hl = h + 4 * lane;
     const bool ragged = rank % (NARROW ? 4 : 8) != 0;
     uint4 v[4][NB], next[4][NB];
     if constexpr (!kRingB && NB < 4) load(o, next);
@@ -322,8 +378,8 @@ struct Expand {
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
           for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
-            const uint4 a = hl[(NARROW ? i * 2 + f : (i * NB + kb) * 4 + f) * 32];
-            const bool second = !NARROW && f >= 2;
+            const uint4 a = *reinterpret_cast<const uint4*>(hl + fragment<NARROW, NB>(i, kb, f >> 1, f & 1));
+            const bool second = f >= 2;
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
           }
@@ -347,12 +403,14 @@ template <int MT, bool NARROW, int NB>
 __device__ __forceinline__ void tile_of(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
                                         float* copies, uint8_t* ring) {
   const uint16_t *a = p.ad.a + (int64_t)tile.x * p.ad.max_rank * p.ad.in, *b = p.ad.b + (int64_t)tile.x * p.ad.out * p.ad.max_rank;
-  uint32_t* h = reinterpret_cast<uint32_t*>(NB == 4 ? ring + kRing / 2 : reinterpret_cast<uint8_t*>(copies) + kCopyBytes / 2);
+  uint32_t* h = reinterpret_cast<uint32_t*>(NB == 4 ? ring : reinterpret_cast<uint8_t*>(copies) + kCopyBytes / 2);
   Expand<MT, NARROW, NB> second(p, b, rank, tile.z, tokens, ring, o0, o1);
-  shrink<MT>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), copies);
+  if (MT == 1) second.start();
+  shrink<MT, NARROW, NB>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), ring, copies);
+  if (MT > 1) second.start();  // the ring is free
   cluster_arrive();
   cluster_wait();
-  gather<MT, NARROW>(copies, NB, h);
+  gather<MT, NARROW, NB>(copies, h);
   cluster_arrive();  // this block has read the others' sums
   __syncthreads();
   second.run(h, scale);
