@@ -9,7 +9,8 @@
 // 128 rows, one stream whose tiles alternate between two S.
 // Rows see keys up to their own position: only the last tiles of an item are masked, and streams end where their rows do.
 // Keys and values arrive by TMA in a ring of slots in the order of their use.  An e4m3 cache is copied into the upper half of a
-// slot and widened in place to bf16 (exact).  Values that a product must not meet (rows past the end, numbers that are not finite
+// slot and widened in place to fp16 (exact).  The queries are fp16 then, each row at a power of two that brings its largest number
+// to 2^14 .. 2^15: bf16 numbers down to 2^-31 of it are exact, others within 2^-40 of it.  Values that a product must not meet (rows past the end, numbers that are not finite
 // where not every row sees them) are cleared on the way, the latter added back for the rows that see them (rare).
 // The warps: two softmax warpgroups (a thread per row, a tile's scores in registers); the warp that plans and copies, the one
 // that issues, two that bring the queries; a warpgroup that widens and clears.
@@ -52,9 +53,12 @@ struct Cfg {
   static constexpr int Slots = D == 64 ? 8 : 4;
   static constexpr int Blocks = D / 64;             // 128-byte blocks of a row
   static constexpr int QTile = 128 * D * 2;
-  static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 1024;
-  static constexpr int Smem = 1024 + Slots * Slot + Streams * QTile + Fixed;
+  static constexpr int Stage = 32 * 64;             // 32 columns of a warp's rows, on their way out
+  static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 2 * Rows * 4 + 1024;
+  static constexpr int Smem = 1024 + Slots * Slot + Streams * (QTile + 4 * Stage) + Fixed;
   static_assert(Smem <= 227 * 1024, "fits");
+  template <bool F8>
+  static constexpr float Lift = F8 ? 7.f : 0.f;     // log2 of a factor of the weights: with it fp16 ones reach 2^15
   // tensor memory columns
   static constexpr int S(int s) { return s * 128; }
   static constexpr int O(int s) { return 256 + s * D; }
@@ -77,17 +81,39 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Two e4m3 numbers (the low bytes' pair of w by sel) as bf16, exactly: exponent and fraction moved to bf16's places, times
-// 2^120.  NaN comes out as +-480.
-__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t sel) {
-  const uint32_t u = __byte_perm(w, 0, sel);
-  const uint32_t v = ((u >> 4) & 0x07F007F0u) | (u & 0x80008000u);
+// Issued by a converged warp with operands that are the warp's, like the products (tree_tc.cuh): copies from lanes of their own are
+// taken one lane after the other, some 200 cycles each (8192 tokens, heads of 64, pages of 64: 657 us so).
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}"
+      ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+      : "memory");
+}
+
+// Two e4m3 numbers as fp16, exactly.
+__device__ __forceinline__ uint32_t widen2(uint16_t v) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
   return r;
 }
-// Whether any of four e4m3 numbers is NaN: bit 7 of its byte of the result.
-__device__ __forceinline__ uint32_t nan4(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// A wait's first try, of a warp: suspended at most hint_ns.
+__device__ __forceinline__ bool first_try(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  return __all_sync(0xFFFFFFFFu, tc::mbar_try_wait_hint(bar, parity, hint_ns));
+}
 
 // The order in which an item's tiles of keys and values are copied and used: place of tile t's keys or values among 2n.
 template <int Streams>
@@ -115,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = base;
   uint8_t* sq = ring + C::Slots * C::Slot;
-  prompt::Map& plan = *reinterpret_cast<prompt::Map*>(sq + C::Streams * C::QTile);
+  uint8_t* stages = sq + C::Streams * C::QTile;
+  float* row_fac = reinterpret_cast<float*>(stages + C::Streams * 4 * C::Stage);  // e4m3: [stretch % 2][row] of the row's scores
+  prompt::Map& plan = *reinterpret_cast<prompt::Map*>(row_fac + 2 * C::Rows);
   Work* works = reinterpret_cast<Work*>(&plan + 1);
   uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(works + kWorks) + 7) & ~(uintptr_t)7);
   uint64_t* tail_full = full + C::Slots;  // bf16: of values that are cleared first.  A thread that waits for a phase has to have seen
@@ -153,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(o_done, 1);
     for (int i = 0; i < kWorks; ++i) {
       tc::mbar_init(w_full + i, 1);
-      tc::mbar_init(w_empty + i, 7 + 4 * C::Streams);
+      tc::mbar_init(w_empty + i, 7 + 4 * C::Streams + (F8 && C::Streams == 1 ? 4 : 0));
     }
     tc::mbar_init(drained, 1);
     flags[0] = 0;
@@ -171,7 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = uniform(*tmem_slot);
   bool dead = false;
+  const uint32_t hint = p.wait_ns < 1000000 ? (uint32_t)p.wait_ns : 1000000u;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {  // of a converged warp
+    if (first_try(bar, parity, hint)) return !dead;
     const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
     if (__any_sync(0xFFFFFFFFu, !ok)) {
       dead = true;
@@ -189,15 +219,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     return w.more != 0;
   };
 
-  if (warp >= kWidenWarp) {
+  constexpr bool kTwoWiden = F8 && C::Streams == 1;  // the second softmax warpgroup widens too: the odd slots
+  if (warp >= kWidenWarp || (kTwoWiden && warp >= 4 && warp < 8)) {
     // ---- widening and clearing
-    regs_down<kWidenRegs>();
-    const int tid = threadIdx.x & 127;
+    if (warp >= kWidenWarp) regs_down<kWidenRegs>();
+    else regs_up<kSoftmaxRegs>();
+    const int tid = threadIdx.x & 127, group_bar = warp >= kWidenWarp ? 2 : 3;
     Work w;
     int e0 = 0;
     uint32_t f_phase = 0;  // per slot
     // the group's warps meet at barriers, so they leave together
-    for (int k = 0; tc::bar_and(told(k, w), 2, 128); ++k) {
+    for (int k = 0; tc::bar_and(told(k, w), group_bar, 128); ++k) {
       const int n = w.tiles;
       const int shared_to = w.prefix + w.first + 1;  // keys that every row sees
       for (int e = 0; e < 2 * n && !dead; ++e) {
@@ -207,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!F8 && !tail) continue;
         for (int part = 0; part < C::Parts; ++part) {
           const int at = e0 + e * C::Parts + part, slot = at % C::Slots;
+          if (kTwoWiden && (slot & 1) != group_bar - 2) continue;
           const int pos0 = (w.tile0 + t) * kTile + part * C::Keys;
           wait((F8 ? full : tail_full) + slot, f_phase >> slot & 1u);
           f_phase ^= 1u << slot;
@@ -216,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 v[Each];
 #pragma unroll
             for (int i = 0; i < Each; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + (i * 128 + tid) * 16);
-            if (!tc::bar_and(!dead, 2, 128)) {  // all of it is in registers
+            if (!tc::bar_and(!dead, group_bar, 128)) {  // all of it is in registers
               dead = true;
               break;
             }
@@ -225,29 +258,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int c = i * 128 + tid, row = c / Chunks, ch = c % Chunks * 2;
               uint32_t o[8];
               const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              uint32_t bad = 0;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                bad |= nan4(in[j]);
-                o[2 * j] = widen2(in[j], 0x1404);
-                o[2 * j + 1] = widen2(in[j], 0x3424);
+                o[2 * j] = widen2((uint16_t)in[j]);
+                o[2 * j + 1] = widen2((uint16_t)(in[j] >> 16));
               }
-              if (bad & 0x80808080u) {
-                const bool clear = tail && pos0 + row >= shared_to;
+              if (tail && pos0 + row >= shared_to) {
+                const bool past = pos0 + row >= w.len;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  const uint32_t b = nan4(in[j >> 1]) >> (j & 1 ? 16 : 0);
-                  if (b & 0x80u) o[j] = (o[j] & 0xFFFF0000u) | (clear ? 0u : 0x7FFFu);
-                  if (b & 0x8000u) o[j] = (o[j] & 0xFFFFu) | (clear ? 0u : 0x7FFF0000u);
-                }
-                if (clear && pos0 + row < w.len) {
-                  odd_of[k % kOdd] = k;
-                  __threadfence_block();
+                  if (past) {
+                    o[j] = 0;
+                    continue;
+                  }
+                  bool odd = false;
+                  if ((o[j] & 0x7C00u) == 0x7C00u) { o[j] &= 0xFFFF0000u; odd = true; }
+                  if ((o[j] >> 16 & 0x7C00u) == 0x7C00u) { o[j] &= 0xFFFFu; odd = true; }
+                  if (odd) {
+                    odd_of[k % kOdd] = k;
+                    __threadfence_block();
+                  }
                 }
               }
-              if (tail && pos0 + row >= w.len)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = 0;
               uint8_t* to = tile + (ch >> 3) * (C::Keys * 128) + row * 128;
               *reinterpret_cast<uint4*>(to + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
               *reinterpret_cast<uint4*>(to + ((((ch & 7) + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -320,29 +352,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = tile_at<C::Streams>(e, n, &value);
           for (int part = 0; part < C::Parts; ++part) {
             const int i = e0 + e * C::Parts + part, slot = i % C::Slots, use = i / C::Slots;
-            const int pos = (w.tile0 + t) * kTile + part * C::Keys + lane * box;  // lane i copies box i of the slot, none past the end
-            const bool mine = lane * box < C::Keys && pos < w.len;
+            const int pos = (w.tile0 + t) * kTile + part * C::Keys + lane * box;  // lane i knows box i of the slot; none past the end
             int y = 0, page = pages.at(t * C::Parts + part);
-            if (mine) {
-              page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
-              y = (((page * 2 + (value ? 1 : 0)) * p.hkv + w.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-            }
-            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+            page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+            y = (((page * 2 + (value ? 1 : 0)) * p.hkv + w.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, lane * box < C::Keys && pos < w.len));
             if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) break;
             const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
-            uint64_t* bar = (tail ? tail_full : full) + slot;
+            const uint32_t bar = tc::smem_u32((tail ? tail_full : full) + slot);
             (tail ? t_phase : f_phase) ^= 1u << slot;
             is_tail = (is_tail & ~(1u << slot)) | (uint32_t)tail << slot;
-            if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * D * (F8 ? 1 : 2)));
-            __syncwarp();
+            expect_bytes(bar, (uint32_t)(boxes * box * D * (F8 ? 1 : 2)));
             copied = i + 1;
-            if (mine) {
+            const uint32_t to = tc::smem_u32(ring + slot * C::Slot);
+            for (int i_box = 0; i_box < boxes; ++i_box) {
+              const int row = __shfl_sync(0xFFFFFFFFu, y, i_box);
               if constexpr (F8) {
-                tc::tma_load_2d(ring + slot * C::Slot + C::Slot / 2 + lane * box * D, &map, bar, 0, y);
+                tma_load(to + C::Slot / 2 + i_box * box * D, &map, bar, 0, row);
               } else {
 #pragma unroll
                 for (int blk = 0; blk < C::Blocks; ++blk)
-                  tc::tma_load_2d(ring + slot * C::Slot + blk * (C::Keys * 128) + lane * box * 128, &map, bar, blk * 64, y);
+                  tma_load(to + blk * (C::Keys * 128) + i_box * box * 128, &map, bar, blk * 64, row);
               }
             }
           }
@@ -363,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       Work w;
       int e0 = 0;
       uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
-      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, C::Keys), id_o = tc::idesc_bf16_f32(128, D) | kBMnMajor;
+      constexpr uint32_t kF16 = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // both operands fp16 instead
+      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, C::Keys) & kF16, id_o = (tc::idesc_bf16_f32(128, D) & kF16) | kBMnMajor;
       const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
                      v_desc = desc_mnmajor(tc::smem_u32(ring), C::Keys * 128);
       for (int k = 0; told(k, w); ++k) {
@@ -484,22 +515,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; told(k, w); ++k) {
         if (k > 0 && !wait(q_empty, (uint32_t)(k & 1) ^ 1u)) break;
         const float ks = p.scales ? __ldg(p.scales + w.head) : 1.f;
-        constexpr int LPR = D / 8;
-        const int ch = tid % LPR;
-        const uint32_t to = tc::smem_u32(sq) + (ch >> 3) * (128 * 128);
-        for (int r = tid / LPR; r < w.rows; r += 64 / LPR) {
-          const int d = tree_draft(p, w.g0 + r), hh = w.g0 + r - d * p.group;
-          const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
-          cp_async16(to + (r >> 7) * C::QTile + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4), src);
-        }
-        cp_async_wait();
-        if (p.scale_log2 * ks < 0.f)  // a negative scale goes into the queries' signs
-          for (int r = tid / LPR; r < w.rows; r += 64 / LPR) {
-            uint4* at = reinterpret_cast<uint4*>(sq + (ch >> 3) * (128 * 128) + (r >> 7) * C::QTile + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4));
-            uint4 v = *at;
-            v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u;
-            *at = v;
+        const uint32_t flip = p.scale_log2 * ks < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
+        constexpr int LPR = D / 8, kRows = 64 / LPR;  // lanes of a row, rows at a time
+        const int ch = tid % LPR, r0 = tid / LPR;
+        uint8_t* to = sq + (ch >> 3) * (128 * 128) + r0 * 128;
+        // (token, head of the group) of row r0 + kRows i, without a division each
+        int d = tree_draft(p, w.g0 + r0), hh = w.g0 + r0 - d * p.group;
+        const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
+        const int dstep = tree_draft(p, kRows), hstep = kRows - dstep * p.group;
+        const int64_t step = dstep * p.q_stride + hstep * D, wrap = p.q_stride - (int64_t)p.group * D;
+        const auto next = [&] {
+          hh += hstep;
+          src += step;
+          if (hh >= p.group) {
+            hh -= p.group;
+            src += wrap;
           }
+        };
+        const auto place = [&](int r) { return (r >> 7) * C::QTile + ((r & 127) - r0) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+        if constexpr (!F8) {
+#pragma unroll 4
+          for (int r = r0; r < w.rows; r += kRows) {
+            cp_async16(tc::smem_u32(to) + place(r), src);
+            next();
+          }
+          cp_async_wait();
+          if (flip)
+            for (int r = r0; r < w.rows; r += kRows) {
+              uint4* at = reinterpret_cast<uint4*>(to + place(r));
+              uint4 v = *at;
+              *at = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+            }
+        } else {
+          constexpr int kMost = 4;  // rows whose loads are in flight
+#pragma unroll 1
+          for (int r1 = r0; r1 < C::Rows; r1 += kRows * kMost) {
+            uint4 u[kMost];
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+              u[i] = make_uint4(0, 0, 0, 0);
+              if (r1 + i * kRows < w.rows) u[i] = *reinterpret_cast<const uint4*>(src);
+              next();
+            }
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) {
+              const int r = r1 + i * kRows;
+              // the row's largest number: positive bf16 patterns compare like integers, two at a time
+              uint32_t big = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
+#pragma unroll
+              for (int o = 1; o < (LPR < 32 ? LPR : 32); o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+              const uint32_t top = max(big & 0xFFFFu, big >> 16) >> 7;  // its exponent
+              // times 2^(141 - top): exact in two steps, each a power of two that fp32 holds
+              const int up = min(141 - (int)top, 250), half = up / 2;
+              const float f0 = __uint_as_float((uint32_t)(127 + half) << 23), f1 = __uint_as_float((uint32_t)(127 + up - half) << 23);
+              const auto f16 = [&](uint32_t x) {
+                x ^= flip;
+                return pack_f16x2(bf16lo_to_f32(x) * f0 * f1, bf16hi_to_f32(x) * f0 * f1);
+              };
+              if (r < w.rows) {
+                *reinterpret_cast<uint4*>(to + place(r)) = make_uint4(f16(u[i].x), f16(u[i].y), f16(u[i].z), f16(u[i].w));
+                if (ch == 0) row_fac[(k & 1) * C::Rows + r] = (float)up;
+              }
+            }
+          }
+        }
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(q_full);
@@ -521,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = prompt::tiles_of(p, w, s * 128, s * 128 + 128);
         const int seen = valid ? prompt::seen_by(p, w, r) : 0;
         const int masked_from = s * 128 < w.rows ? prompt::seen_by(p, w, s * 128) : 0;  // keys that every row of the stream sees
-        const float c = score_factor(fabsf(p.scale_log2 * (p.scales ? __ldg(p.scales + w.head) : 1.f)));
+        float c = score_factor(fabsf(p.scale_log2 * (p.scales ? __ldg(p.scales + w.head) : 1.f)));
         const uint32_t t_o = tmem + C::O(s) + lanes;
         float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
         for (int i = 0; i < n; ++i) {
@@ -530,6 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(s_full + buf, s_phase >> buf & 1u)) break;
           s_phase ^= 1u << buf;
           tc::fence_after_sync();
+          if (F8 && i == 0) {  // 2^-up of the row's queries
+            const int up = (int)row_fac[(k & 1) * C::Rows + r], half = up / 2;
+            c *= __uint_as_float((uint32_t)(127 - half) << 23);
+            c *= __uint_as_float((uint32_t)(127 - (up - half)) << 23);
+            c = c != c ? c : score_factor(fminf(c, 3.402823466e38f));
+          }
           const int pos0 = (w.tile0 + i) * kTile;
           uint32_t x[4][32];
 #pragma unroll
@@ -572,8 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // ---- weights, over the scores: bf16, the type of the values they are multiplied with
-          const float ms = m == -INFINITY ? 0.f : -m;
+          // ---- weights, over the scores, in the type of the values they are multiplied with
+          const float ms = (m == -INFINITY ? 0.f : -m) + C::template Lift<F8>;
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -584,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum = __fadd2_rn(sum, y);
-              e[q >> 1] = pack_bf16x2(y.x, y.y);
+              e[q >> 1] = F8 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
             }
             tmem_st_x16(t_s + 16 * j, e);
           }
@@ -635,19 +720,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (whole) {
           const float vs = p.scales ? __ldg(p.scales + p.hkv + w.head) : 1.f, f = l == 0.f ? 0.f : vs / l;
-          uint16_t* out = p.out + token * p.out_stride + (int64_t)head * D;
+          // 32 columns at a time through shared memory, so that 64 bytes of a row are stored by four lanes together (a row per lane:
+          // four times as many accesses, the end of an item took 4000 cycles)
+          uint8_t* stage = stages + warp * C::Stage;
+          uint16_t* out[4];
+          bool has[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int q = (warp & 3) * 32 + s * 128 + 8 * i + (lane >> 2), dq = tree_draft(p, w.g0 + q), hq = w.g0 + q - dq * p.group;
+            has[i] = q < w.rows;
+            out[i] = p.out + (int64_t)(w.start + w.first + dq) * p.out_stride + (int64_t)(w.head * p.group + hq) * D + 8 * (lane & 3);
+          }
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             float v[32];
             fetch(col, v);
-            if (valid)
+            __syncwarp();
 #pragma unroll
-              for (int q = 0; q < 32; q += 8)
-                *reinterpret_cast<uint4*>(out + col + q) =
-                    make_uint4(pack_bf16x2(v[q] * f, v[q + 1] * f), pack_bf16x2(v[q + 2] * f, v[q + 3] * f),
-                               pack_bf16x2(v[q + 4] * f, v[q + 5] * f), pack_bf16x2(v[q + 6] * f, v[q + 7] * f));
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * q] * f, v[8 * q + 1] * f), pack_bf16x2(v[8 * q + 2] * f, v[8 * q + 3] * f),
+                             pack_bf16x2(v[8 * q + 4] * f, v[8 * q + 5] * f), pack_bf16x2(v[8 * q + 6] * f, v[8 * q + 7] * f));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q = 8 * i + (lane >> 2);
+              if (has[i]) *reinterpret_cast<uint4*>(out[i] + col) = *reinterpret_cast<const uint4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
+            }
           }
-          if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+          if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::template Lift<F8>));
         } else {  // a part, for the joining kernel
           float* part = p.part + (int64_t)tree_slot(cta, w.tile0 == 0) * tree_part_floats(C::Rows, D);
 #pragma unroll 1
@@ -690,7 +791,7 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cuda
   }, cudaErrorInvalidDevice);
   if (e != cudaSuccess) return e;
   const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
-  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, Cfg<D>::Rows, 0.f, ctas, st);
+  return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, Cfg<D>::Rows, Cfg<D>::template Lift<F8>, ctas, st);
 }
 
 int prompt_ctas() { return device_sm_count() < kTreeMaxCtas ? device_sm_count() : kTreeMaxCtas; }
