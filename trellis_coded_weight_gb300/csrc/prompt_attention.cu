@@ -47,11 +47,17 @@ template <int D>
 struct Cfg {
   static constexpr int Streams = D == 256 ? 1 : 2;
   static constexpr int Rows = 128 * Streams;
-  static constexpr int Keys = D == 256 ? 64 : 128;  // of a slot
-  static constexpr int Parts = kTile / Keys;        // slots of a tile's keys, or values
-  static constexpr int Slot = Keys * D * 2;
+  static constexpr int Cols = D < 128 ? D : 128;    // of a slot, which has them for all keys of a tile
+  static constexpr int Parts = D / Cols;            // slots of a tile's keys, or values
+  static constexpr int Slot = kTile * Cols * 2;
   static constexpr int Slots = D == 64 ? 8 : 4;
-  static constexpr int Blocks = D / 64;             // 128-byte blocks of a row
+  static constexpr int Blocks = Cols / 64;          // 128-byte blocks of a row
+  // In a slot 8 rows of a block lie together (1024 bytes), then the blocks of these rows, then the next 8 rows: one copy brings
+  // whole pages so.
+  static constexpr int Group = Blocks * 1024;
+  static __device__ __forceinline__ int at(int row, int chunk) {  // 8 numbers
+    return (row >> 3) * Group + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+  }
   static constexpr int QTile = 128 * D * 2;
   static constexpr int Stage = 32 * 64;             // 32 columns of a warp's rows, on their way out
   static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 2 * Rows * 4 + 1024;
@@ -83,12 +89,20 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 
 // Issued by a converged warp with operands that are the warp's, like the products (tree_tc.cuh): copies from lanes of their own are
 // taken one lane after the other, some 200 cycles each (8192 tokens, heads of 64, pages of 64: 657 us so).
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xFFFFFFFF;\n\t"
       "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}"
       ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int block, int group) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%5, %5, %3, %4}], [%2];\n\t}"
+      ::"r"(dst), "l"(map), "r"(bar), "r"(block), "r"(group), "r"(0)
       : "memory");
 }
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
@@ -113,6 +127,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
 // A wait's first try, of a warp: suspended at most hint_ns.
 __device__ __forceinline__ bool first_try(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
   return __all_sync(0xFFFFFFFFu, tc::mbar_try_wait_hint(bar, parity, hint_ns));
+}
+
+// As desc_mnmajor (tree_tc.cuh), `sbo` bytes from 8 rows to the next 8.
+__device__ __forceinline__ uint64_t desc_values(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (desc_mnmajor(saddr, lbo) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
 }
 
 // The order in which an item's tiles of keys and values are copied and used: place of tile t's keys or values among 2n.
@@ -240,12 +259,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int part = 0; part < C::Parts; ++part) {
           const int at = e0 + e * C::Parts + part, slot = at % C::Slots;
           if (kTwoWiden && (slot & 1) != group_bar - 2) continue;
-          const int pos0 = (w.tile0 + t) * kTile + part * C::Keys;
+          const int pos0 = (w.tile0 + t) * kTile;
           wait((F8 ? full : tail_full) + slot, f_phase >> slot & 1u);
           f_phase ^= 1u << slot;
           uint8_t* tile = ring + slot * C::Slot;
           if constexpr (F8) {
-            constexpr int Chunks = D / 16, Each = C::Keys * Chunks / 128;  // 16 numbers; of a row, of a thread
+            constexpr int Chunks = C::Cols / 16, Each = Chunks;  // 16 numbers; of a row, of a thread
             uint4 v[Each];
 #pragma unroll
             for (int i = 0; i < Each; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + (i * 128 + tid) * 16);
@@ -280,17 +299,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
               }
-              uint8_t* to = tile + (ch >> 3) * (C::Keys * 128) + row * 128;
-              *reinterpret_cast<uint4*>(to + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(to + ((((ch & 7) + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+              // lanes of odd blocks store their second half first: eight lanes then reach all banks
+              const bool odd_block = ch >> 3 & 1;
+              const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+              *reinterpret_cast<uint4*>(tile + C::at(row, odd_block ? ch + 1 : ch)) = odd_block ? hi : lo;
+              *reinterpret_cast<uint4*>(tile + C::at(row, odd_block ? ch : ch + 1)) = odd_block ? lo : hi;
             }
           } else {
             if (dead) break;
-            constexpr int Chunks = D / 8;
+            constexpr int Chunks = C::Cols / 8;
             const int from = max(shared_to - pos0, 0);
-            for (int c = from * Chunks + tid; c < C::Keys * Chunks; c += 128) {
+            for (int c = from * Chunks + tid; c < kTile * Chunks; c += 128) {
               const int row = c / Chunks, ch = c % Chunks;
-              uint4* to = reinterpret_cast<uint4*>(tile + (ch >> 3) * (C::Keys * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+              uint4* to = reinterpret_cast<uint4*>(tile + C::at(row, ch));
               if (pos0 + row >= w.len) {
                 *to = make_uint4(0, 0, 0, 0);
                 continue;
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {
       // ---- the warp that plans and copies
       const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
-      const int box = min(1 << p.page_shift, C::Keys);  // rows of one copy
+      const int box = 1 << p.page_shift;  // rows of one copy: a page's
       int at = 0, end = 0, item = cta, fetched = 0;
       if (plan.split && cta < plan.ctas) {
         at = (int)((int64_t)cta * plan.total / plan.ctas);
@@ -344,37 +365,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         TreeSegment g;
         g.seq = TreeSeq{w.start, w.len - w.prefix, w.prefix};
         g.b = w.b;
-        g.tile0 = w.tile0 * C::Parts;
-        TreePages<C::Keys> pages(p, g, lane);
-        const int shared_to = w.prefix + w.first + 1;
-        for (int e = 0; e < 2 * n && !dead; ++e) {
-          bool value;
-          const int t = tile_at<C::Streams>(e, n, &value);
+        g.tile0 = w.tile0;
+        TreePages<kTile> pages(p, g, lane);
+        const int shared_to = w.prefix + w.first + 1, to_values = p.hkv << p.page_shift;
+        // lane i knows where box i of a tile's keys lies; none past the end
+        const auto rows_of = [&](int t) {
+          int page = pages.at(t);
+          page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+          return (page * 2 * p.hkv + w.head) << p.page_shift;
+        };
+        const auto copy = [&](int t, bool value, int y, int e) {
+          const int left = w.len - (w.tile0 + t) * kTile, boxes = min(kTile, left + box - 1) >> p.page_shift;
+          const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
+#pragma unroll
           for (int part = 0; part < C::Parts; ++part) {
             const int i = e0 + e * C::Parts + part, slot = i % C::Slots, use = i / C::Slots;
-            const int pos = (w.tile0 + t) * kTile + part * C::Keys + lane * box;  // lane i knows box i of the slot; none past the end
-            int y = 0, page = pages.at(t * C::Parts + part);
-            page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
-            y = (((page * 2 + (value ? 1 : 0)) * p.hkv + w.head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-            const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, lane * box < C::Keys && pos < w.len));
-            if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) break;
-            const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
-            const uint32_t bar = tc::smem_u32((tail ? tail_full : full) + slot);
+            if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) return;
+            const uint32_t bar = tc::smem_u32((tail ? tail_full : full) + slot), to = tc::smem_u32(ring) + slot * C::Slot;
             (tail ? t_phase : f_phase) ^= 1u << slot;
             is_tail = (is_tail & ~(1u << slot)) | (uint32_t)tail << slot;
-            expect_bytes(bar, (uint32_t)(boxes * box * D * (F8 ? 1 : 2)));
+            expect_bytes(bar, (uint32_t)(boxes * box * C::Cols * (F8 ? 1 : 2)));
             copied = i + 1;
-            const uint32_t to = tc::smem_u32(ring + slot * C::Slot);
-            for (int i_box = 0; i_box < boxes; ++i_box) {
-              const int row = __shfl_sync(0xFFFFFFFFu, y, i_box);
-              if constexpr (F8) {
-                tma_load(to + C::Slot / 2 + i_box * box * D, &map, bar, 0, row);
-              } else {
-#pragma unroll
-                for (int blk = 0; blk < C::Blocks; ++blk)
-                  tma_load(to + blk * (C::Keys * 128) + i_box * box * 128, &map, bar, blk * 64, row);
-              }
+            for (int j = 0; j < boxes; ++j) {
+              const int row = __shfl_sync(0xFFFFFFFFu, y, j);
+              if constexpr (F8) tma_load_2d(to + C::Slot / 2 + j * box * C::Cols, &map, bar, part * C::Cols, row);
+              else tma_load_4d(to + (j * box >> 3) * C::Group, &map, bar, part * C::Blocks, row >> 3);
             }
+          }
+        };
+        // in the order of place_of()
+        int y = rows_of(0);
+        copy(0, false, y, 0);
+        if (C::Streams == 1) {
+          for (int t = 0; t < n && !dead; ++t) {
+            const int next = t + 1 < n ? rows_of(t + 1) : 0;
+            if (t + 1 < n) copy(t + 1, false, next, 2 * t + 1);
+            if (!dead) copy(t, true, y + to_values, t + 1 < n ? 2 * t + 2 : 2 * n - 1);
+            y = next;
+          }
+        } else {
+          for (int t = 0; t < n && !dead; ++t) {
+            const int next = t + 1 < n ? rows_of(t + 1) : 0;
+            copy(t, true, y + to_values, 2 * t + 1);
+            y = next;
+            if (t + 1 < n && !dead) copy(t + 1, false, y, 2 * t + 2);
           }
         }
         e0 += 2 * n * C::Parts;
@@ -394,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e0 = 0;
       uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
       constexpr uint32_t kF16 = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // both operands fp16 instead
-      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, C::Keys) & kF16, id_o = (tc::idesc_bf16_f32(128, D) & kF16) | kBMnMajor;
-      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), 1024, 2),
-                     v_desc = desc_mnmajor(tc::smem_u32(ring), C::Keys * 128);
+      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kF16, id_o = (tc::idesc_bf16_f32(128, C::Cols) & kF16) | kBMnMajor;
+      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), C::Group, 2),
+                     v_desc = desc_values(tc::smem_u32(ring), 1024, C::Group);
       for (int k = 0; told(k, w); ++k) {
         const int n = uniform(w.tiles), shared_to = w.prefix + w.first + 1;
         const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
@@ -417,17 +451,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         const auto give = [&](int t, bool value) {
-          for (int part = 0; part < C::Parts; ++part) mma_done(empty + entry(t, value, part) % C::Slots);
+          if (C::Parts == 1) mma_done(empty + entry(t, value, 0) % C::Slots);  // several parts are given back one by one, below
         };
         const auto scores = [&](int s, int qtile, int t) {
-          const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4));
 #pragma unroll
           for (int part = 0; part < C::Parts; ++part) {
-            const uint64_t b = k_desc + (uint32_t)(entry(t, false, part) % C::Slots * (C::Slot >> 4));
+            const int slot = entry(t, false, part) % C::Slots;
+            const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4) + part * (C::Blocks * 128 * 128 >> 4)), b = k_desc + (uint32_t)(slot * (C::Slot >> 4));
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              mma_ss(tmem + C::S(s) + part * C::Keys, a + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4),
-                     b + (((x >> 2) * (C::Keys * 128) + (x & 3) * 32) >> 4), id_s, x > 0);
+            for (int x = 0; x < C::Cols / 16; ++x)
+              mma_ss(tmem + C::S(s), a + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4), b + (((x >> 2) * 1024 + (x & 3) * 32) >> 4), id_s, part > 0 || x > 0);
+            if (C::Parts > 1) mma_done(empty + slot);
           }
           mma_done(s_full + s);
           issued = true;
@@ -435,11 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto outputs = [&](int s, int o, int t, bool fresh) {
 #pragma unroll
           for (int part = 0; part < C::Parts; ++part) {
-            const uint64_t b = v_desc + (uint32_t)(entry(t, true, part) % C::Slots * (C::Slot >> 4));
+            const int slot = entry(t, true, part) % C::Slots;
+            const uint64_t b = v_desc + (uint32_t)(slot * (C::Slot >> 4));
 #pragma unroll
-            for (int x = 0; x < C::Keys / 16; ++x)
-              mma_ts(tmem + C::O(o), tmem + C::S(s) + 8 * (part * (C::Keys / 16) + x), b + ((x * 16 * 128) >> 4), id_o,
-                     !(fresh && part == 0 && x == 0));
+            for (int x = 0; x < kTile / 16; ++x)
+              mma_ts(tmem + C::O(o) + part * C::Cols, tmem + C::S(s) + 8 * x, b + ((x * 2 * C::Group) >> 4), id_o, !(fresh && x == 0));
+            if (C::Parts > 1) mma_done(empty + slot);
           }
         };
         const auto weights = [&](int s) {  // waits for the stream's
@@ -838,18 +873,25 @@ cudaError_t launch_prompt_attention(const uint16_t* q, int64_t q_stride, const t
   const auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const bool f8 = c.dtype == TRELLIS_E4M3;
-  const int row_bytes = c.head_dim * (int)cache_elem_bytes(c), keys = c.head_dim == 256 ? Cfg<256>::Keys : Cfg<128>::Keys;
+  const int row_bytes = c.head_dim * (int)cache_elem_bytes(c), cols = c.head_dim < 128 ? c.head_dim : 128;
   uint8_t* pool = static_cast<uint8_t*>(c.pool) + (int64_t)layer * c.pages * cache_page_bytes(c);
   CUtensorMap map;
-  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.pages * 2 * c.heads * c.page_size)};
-  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
-  // e4m3 as it lies in the cache, bf16 in 128-byte blocks of a row, swizzled
-  const cuuint32_t box[2] = {(cuuint32_t)(f8 ? c.head_dim : 64), (cuuint32_t)(c.page_size < keys ? c.page_size : keys)};
-  const cuuint32_t estr[2] = {1, 1};
-  if (fn(&map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  const cuuint64_t rows = (cuuint64_t)(c.pages * 2 * c.heads * c.page_size);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult made;
+  if (f8) {  // as it lies in the cache
+    const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)c.page_size};
+    made = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {  // (64 numbers, 8 rows, blocks of 64 of a row, groups of 8 rows): what a slot holds, 8 rows of a block swizzled together
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)(c.head_dim / 64), rows / 8},
+                     strides[3] = {(cuuint64_t)row_bytes, 128, (cuuint64_t)row_bytes * 8};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(cols / 64), (cuuint32_t)(c.page_size / 8)};
+    made = fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  if (made != CUDA_SUCCESS) return cudaErrorInvalidValue;
   p.pool = pool;
   const int ctas = prompt_ctas();
   if (f8)
