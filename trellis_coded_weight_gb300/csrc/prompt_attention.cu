@@ -374,41 +374,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
           return (page * 2 * p.hkv + w.head) << p.page_shift;
         };
-        const auto copy = [&](int t, bool value, int y, int e) {
+        int now = 0, before = 0;  // of the last two tiles of keys
+#pragma unroll 1
+        for (int e = 0; e < 2 * n && !dead; ++e) {
+          bool value;
+          const int t = tile_at<C::Streams>(e, n, &value);
+          if (!value) {
+            before = now;
+            now = rows_of(t);
+          }
+          const int y = value ? (C::Streams == 1 && t + 1 < n ? before : now) + to_values : now;
           const int left = w.len - (w.tile0 + t) * kTile, boxes = min(kTile, left + box - 1) >> p.page_shift;
           const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
-#pragma unroll
+#pragma unroll 1
           for (int part = 0; part < C::Parts; ++part) {
             const int i = e0 + e * C::Parts + part, slot = i % C::Slots, use = i / C::Slots;
-            if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) return;
+            if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) break;
             const uint32_t bar = tc::smem_u32((tail ? tail_full : full) + slot), to = tc::smem_u32(ring) + slot * C::Slot;
             (tail ? t_phase : f_phase) ^= 1u << slot;
             is_tail = (is_tail & ~(1u << slot)) | (uint32_t)tail << slot;
             expect_bytes(bar, (uint32_t)(boxes * box * C::Cols * (F8 ? 1 : 2)));
             copied = i + 1;
+#pragma unroll 1
             for (int j = 0; j < boxes; ++j) {
               const int row = __shfl_sync(0xFFFFFFFFu, y, j);
               if constexpr (F8) tma_load_2d(to + C::Slot / 2 + j * box * C::Cols, &map, bar, part * C::Cols, row);
               else tma_load_4d(to + (j * box >> 3) * C::Group, &map, bar, part * C::Blocks, row >> 3);
             }
-          }
-        };
-        // in the order of place_of()
-        int y = rows_of(0);
-        copy(0, false, y, 0);
-        if (C::Streams == 1) {
-          for (int t = 0; t < n && !dead; ++t) {
-            const int next = t + 1 < n ? rows_of(t + 1) : 0;
-            if (t + 1 < n) copy(t + 1, false, next, 2 * t + 1);
-            if (!dead) copy(t, true, y + to_values, t + 1 < n ? 2 * t + 2 : 2 * n - 1);
-            y = next;
-          }
-        } else {
-          for (int t = 0; t < n && !dead; ++t) {
-            const int next = t + 1 < n ? rows_of(t + 1) : 0;
-            copy(t, true, y + to_values, 2 * t + 1);
-            y = next;
-            if (t + 1 < n && !dead) copy(t + 1, false, y, 2 * t + 2);
           }
         }
         e0 += 2 * n * C::Parts;
@@ -507,32 +499,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          if (!take(0, false)) break;
-          if (n0 > 0) scores(0, 0, 0);
-          if (n1 > 0) scores(1, 1, 0);
-          give(0, false);
-          if (n == 1) mma_done(q_empty);
-          for (int t = 0; t < n; ++t) {
-            const bool more = t + 1 < n;
-            if (!take(t, true)) break;
-            if (t < n0) {
-              if (!weights(0)) break;
-              outputs(0, 0, t, t == 0);
-              if (t + 1 == n0) mma_done(o_full);
+          // tile t's outputs and tile t + 1's scores of one stream, then of the other; t = -1: the first scores
+#pragma unroll 1
+          for (int t = -1; t < n; ++t) {
+            if (t >= 0 && !take(t, true)) break;
+            bool got = false;  // the next keys
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              const int nq = q ? n1 : n0;
+              if (t >= 0 && t < nq) {
+                if (!weights(q)) break;
+                outputs(q, q, t, t == 0);
+                if (t + 1 == nq) mma_done(o_full + q);
+              }
+              if (!got && t + 1 < n) {
+                if (!take(t + 1, false)) break;
+                got = true;
+              }
+              if (t + 1 < nq) scores(q, q, t + 1);
             }
-            if (more && !take(t + 1, false)) break;
-            if (t + 1 < n0) scores(0, 0, t + 1);
-            if (t < n1) {
-              if (!weights(1)) break;
-              outputs(1, 1, t, t == 0);
-              if (t + 1 == n1) mma_done(o_full + 1);
-            }
-            give(t, true);
-            if (t + 1 < n1) scores(1, 1, t + 1);
-            if (more) {
-              give(t + 1, false);
-              if (t + 2 == n) mma_done(q_empty);
-            }
+            if (dead) break;
+            if (t >= 0) give(t, true);
+            if (t + 1 < n) give(t + 1, false);
+            if (t + 2 == n) mma_done(q_empty);
           }
         }
         if (dead) break;
@@ -651,26 +640,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             c = c != c ? c : score_factor(fminf(c, 3.402823466e38f));
           }
           const int pos0 = (w.tile0 + i) * kTile;
-          uint32_t x[4][32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tc::tmem_ld_32x32b_x32(t_s + 32 * j, x[j]);
-          tc::tmem_ld_wait();
-          if (pos0 + kTile > masked_from) {  // scores that the row does not see
+          // Passes over the scores are loops over 32 or 64 columns: tensor memory is read again for less than what a tile's 128 held in
+          // registers cost in code, since the warps of all kinds share the instruction caches.
+          if (pos0 + kTile > masked_from) {  // scores that the row does not see become minus infinity, in place
             const int upto = seen - pos0;
+#pragma unroll 1
+            for (int j = 0; j < kTile; j += 32) {
+              const int bits = upto - j;
+              const uint32_t keep = bits >= 32 ? 0xFFFFFFFFu : bits > 0 ? (1u << bits) - 1 : 0u;
+              uint32_t y[32];
+              tc::tmem_ld_32x32b_x32(t_s + j, y);
+              tc::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int q = 0; q < 32; ++q) x[j][q] = 32 * j + q < upto ? x[j][q] : 0xFF800000u;
-          }
-          float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int q = 0; q < 32; q += 4) {
-              a = fmaxf(fmaxf(a, __uint_as_float(x[j][q])), __uint_as_float(x[j][q + 1]));
-              b = fmaxf(fmaxf(b, __uint_as_float(x[j][q + 2])), __uint_as_float(x[j][q + 3]));
+              for (int q = 0; q < 32; ++q) y[q] = keep >> q & 1 ? y[q] : 0xFF800000u;
+              tmem_st_x32(t_s + j, y);
             }
-          const float mx = fmaxf(a, b) * c;
+            tmem_st_wait();
+          }
+          float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int j = 0; j < kTile; j += 64) {
+            uint32_t y[2][32];
+            tc::tmem_ld_32x32b_x32(t_s + j, y[0]);
+            tc::tmem_ld_32x32b_x32(t_s + j + 32, y[1]);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 64; q += 8)
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                a[z] = fmaxf(fmaxf(a[z], __uint_as_float(y[q >> 5][(q & 31) + 2 * z])), __uint_as_float(y[q >> 5][(q & 31) + 2 * z + 1]));
+          }
+          const float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c;
           const bool move = mx > m + kMove || (m == -INFINITY && mx > -INFINITY);
           if (__any_sync(0xFFFFFFFFu, move)) {
             const float to = move ? mx : m, f = m == to ? 1.f : ex2(m - to);
@@ -694,21 +694,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // ---- weights, over the scores, in the type of the values they are multiplied with
           const float ms = (m == -INFINITY ? 0.f : -m) + C::template Lift<F8>;
-          float2 sum = make_float2(0.f, 0.f);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int j = 0; j < kTile; j += 64) {
+            uint32_t x[2][32];
+            tc::tmem_ld_32x32b_x32(t_s + j, x[0]);
+            tc::tmem_ld_32x32b_x32(t_s + j + 32, x[1]);
+            tc::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t e[16];
+            for (int h = 0; h < 2; ++h) {
+              uint32_t e[16];
 #pragma unroll
-            for (int q = 0; q < 32; q += 2) {
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[j][q]), __uint_as_float(x[j][q + 1])), make_float2(c, c), make_float2(ms, ms));
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              sum = __fadd2_rn(sum, y);
-              e[q >> 1] = F8 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
+              for (int q = 0; q < 32; q += 2) {
+                float2 y = __ffma2_rn(make_float2(__uint_as_float(x[h][q]), __uint_as_float(x[h][q + 1])), make_float2(c, c), make_float2(ms, ms));
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                sum[q >> 1 & 1] = __fadd2_rn(sum[q >> 1 & 1], y);
+                e[q >> 1] = F8 ? pack_f16x2(y.x, y.y) : pack_bf16x2(y.x, y.y);
+              }
+              tmem_st_x16(t_s + (j >> 1) + 16 * h, e);
             }
-            tmem_st_x16(t_s + 16 * j, e);
           }
-          l += sum.x + sum.y;
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_st_wait();
           tc::fence_before_sync();
           __syncwarp();
