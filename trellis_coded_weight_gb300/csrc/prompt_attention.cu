@@ -38,7 +38,7 @@ __device__ int g_prompt_error = 0;  // set when a bounded wait gives up (trellis
 
 constexpr int kThreads = 512;
 constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kWidenWarp = 12;
-constexpr int kSoftmaxRegs = 192, kIssueRegs = 56, kWidenRegs = 72;
+constexpr int kSoftmaxRegs = 152, kIssueRegs = 96, kWidenRegs = 112;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 65536 / 128, "what the block was launched with");
 constexpr int kWorks = 2;  // items that the copying warp has announced
 constexpr int kOdd = 8;    // items whose odd values are known at a time: the widening warps are a few ahead of the softmax at the most
@@ -124,9 +124,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-// A wait's first try, of a warp: suspended at most hint_ns.
-__device__ __forceinline__ bool first_try(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  return __all_sync(0xFFFFFFFFu, tc::mbar_try_wait_hint(bar, parity, hint_ns));
+// A wait's first look, of a warp: 16 cycles where the phase is complete, as it mostly is (a try with a time limit takes 70).
+__device__ __forceinline__ bool is_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
 // As desc_mnmajor (tree_tc.cuh), `sbo` bytes from 8 rows to the next 8.
@@ -218,9 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = uniform(*tmem_slot);
   bool dead = false;
-  const uint32_t hint = p.wait_ns < 1000000 ? (uint32_t)p.wait_ns : 1000000u;
   const auto wait = [&](uint64_t* bar, uint32_t parity) {  // of a converged warp
-    if (first_try(bar, parity, hint)) return !dead;
+    if (is_done(bar, parity)) return !dead;
     const bool ok = dead || tc::mbar_wait_short(bar, parity, p.wait_ns);
     if (__any_sync(0xFFFFFFFFu, !ok)) {
       dead = true;
@@ -414,118 +421,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_wait((tail ? tail_full : full) + slot, ((tail ? t_phase : f_phase) >> slot & 1u) ^ 1u, kDrainNs);
       }
     } else if (warp == kMmaWarp) {
-      // ---- the warp that issues the products
+      // ---- the warp that issues the products.  All it does between two products is on the way of both streams, at 5 to 10 cycles an
+      // instruction: so what it needs is carried along, not computed, and there is one copy of the code.
       bool issued = false;
       Work w;
-      int e0 = 0;
-      uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
       constexpr uint32_t kF16 = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // both operands fp16 instead
       constexpr uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kF16, id_o = (tc::idesc_bf16_f32(128, C::Cols) & kF16) | kBMnMajor;
+      constexpr uint32_t kSlot = C::Slot >> 4;
       const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), C::Group, 2),
                      v_desc = desc_values(tc::smem_u32(ring), 1024, C::Group);
+      uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
+      int e0 = 0;                                      // the slot of the stretch's first copy
+      const auto take = [&](int slot, bool tail) {     // waits for a slot's tile
+        if (tail && !F8) {
+          if (!wait(tail_full + slot, t_phase >> slot & 1u) || !wait(ready + slot, t_phase >> slot & 1u)) return false;
+          t_phase ^= 1u << slot;
+          return true;
+        }
+        if (!wait((F8 ? ready : full) + slot, f_phase >> slot & 1u)) return false;
+        f_phase ^= 1u << slot;
+        return true;
+      };
       for (int k = 0; told(k, w); ++k) {
-        const int n = uniform(w.tiles), shared_to = w.prefix + w.first + 1;
+        // Units: a tile of a stream, streams in turn; of one stream every tile.  Unit u has S number u % 2, and its outputs are followed
+        // by the scores of unit u + 2.
+        const int n = uniform(w.tiles), first_tail = uniform((w.prefix + w.first + 1) / kTile - w.tile0);
         const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
-        const auto entry = [&](int t, bool value, int part) { return e0 + place_of<C::Streams>(t, value, n) * C::Parts + part; };
-        const auto take = [&](int t, bool value) {
-          const bool tail = value && (w.tile0 + t + 1) * kTile > shared_to;
-          for (int part = 0; part < C::Parts; ++part) {
-            const int i = entry(t, value, part), slot = i % C::Slots;
-            if (tail && !F8) {
-              if (!wait(tail_full + slot, t_phase >> slot & 1u) || !wait(ready + slot, t_phase >> slot & 1u)) return false;
-              t_phase ^= 1u << slot;
-            } else {
-              if (!wait((F8 ? ready : full) + slot, f_phase >> slot & 1u)) return false;
-              f_phase ^= 1u << slot;
-            }
-          }
-          tc::fence_after_sync();
-          return true;
-        };
-        const auto give = [&](int t, bool value) {
-          if (C::Parts == 1) mma_done(empty + entry(t, value, 0) % C::Slots);  // several parts are given back one by one, below
-        };
-        const auto scores = [&](int s, int qtile, int t) {
-#pragma unroll
-          for (int part = 0; part < C::Parts; ++part) {
-            const int slot = entry(t, false, part) % C::Slots;
-            const uint64_t a = q_desc + (uint32_t)(qtile * (C::QTile >> 4) + part * (C::Blocks * 128 * 128 >> 4)), b = k_desc + (uint32_t)(slot * (C::Slot >> 4));
-#pragma unroll
-            for (int x = 0; x < C::Cols / 16; ++x)
-              mma_ss(tmem + C::S(s), a + (((x >> 2) * (128 * 128) + (x & 3) * 32) >> 4), b + (((x >> 2) * 1024 + (x & 3) * 32) >> 4), id_s, part > 0 || x > 0);
-            if (C::Parts > 1) mma_done(empty + slot);
-          }
-          mma_done(s_full + s);
-          issued = true;
-        };
-        const auto outputs = [&](int s, int o, int t, bool fresh) {
-#pragma unroll
-          for (int part = 0; part < C::Parts; ++part) {
-            const int slot = entry(t, true, part) % C::Slots;
-            const uint64_t b = v_desc + (uint32_t)(slot * (C::Slot >> 4));
-#pragma unroll
-            for (int x = 0; x < kTile / 16; ++x)
-              mma_ts(tmem + C::O(o) + part * C::Cols, tmem + C::S(s) + 8 * x, b + ((x * 2 * C::Group) >> 4), id_o, !(fresh && x == 0));
-            if (C::Parts > 1) mma_done(empty + slot);
-          }
-        };
-        const auto weights = [&](int s) {  // waits for the stream's
-          if (!wait(p_ready + s, p_phase >> s & 1u)) return false;
-          p_phase ^= 1u << s;
-          tc::fence_after_sync();
-          return true;
-        };
         if (!wait(q_full, (uint32_t)(k & 1))) break;
-        tc::fence_after_sync();
-        if constexpr (C::Streams == 1) {
-          for (int t = 0; t < 2 && t < n; ++t) {
-            if (!take(t, false)) break;
-            scores(t, 0, t);
-            give(t, false);
-          }
-          if (n <= 2) mma_done(q_empty);
-          for (int t = 0; t < n && !dead; ++t) {
-            if (!take(t, true) || !weights(t & 1)) break;
-            outputs(t & 1, 0, t, t == 0);
-            give(t, true);
-            mma_done(o_done);
-            if (t + 2 < n) {
-              if (!take(t + 2, false)) break;
-              scores(t & 1, 0, t + 2);
-              give(t + 2, false);
-              if (t + 3 == n) mma_done(q_empty);
-            } else if (t + 1 == n) {
-              mma_done(o_full);
-            }
-          }
-        } else {
-          // tile t's outputs and tile t + 1's scores of one stream, then of the other; t = -1: the first scores
+        int t = C::Streams == 2 ? -1 : -2, b = 0;
 #pragma unroll 1
-          for (int t = -1; t < n; ++t) {
-            if (t >= 0 && !take(t, true)) break;
-            bool got = false;  // the next keys
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              const int nq = q ? n1 : n0;
-              if (t >= 0 && t < nq) {
-                if (!weights(q)) break;
-                outputs(q, q, t, t == 0);
-                if (t + 1 == nq) mma_done(o_full + q);
-              }
-              if (!got && t + 1 < n) {
-                if (!take(t + 1, false)) break;
-                got = true;
-              }
-              if (t + 1 < nq) scores(q, q, t + 1);
+        for (;;) {
+          const int mine = C::Streams == 1 ? n : b ? n1 : n0, next = t + (C::Streams == 2 ? 1 : 2);
+          if (t >= 0 && t < mine) {
+            const int slot = (e0 + place_of<C::Streams>(t, true, n) * C::Parts) % C::Slots;
+            if (C::Streams == 1 || b == 0 || n0 <= t)
+#pragma unroll
+              for (int part = 0; part < C::Parts; ++part)
+                if (!take(slot + part, t >= first_tail)) break;
+            if (!wait(p_ready + b, p_phase >> b & 1u)) break;
+            p_phase ^= 1u << b;
+            tc::fence_after_sync();
+            const uint64_t d = v_desc + slot * kSlot;
+            const uint32_t o = tmem + (C::Streams == 1 ? C::O(0) : C::O(0) + b * D), a = tmem + C::S(0) + b * 128;
+#pragma unroll
+            for (int part = 0; part < C::Parts; ++part) {
+#pragma unroll
+              for (int x = 0; x < kTile / 16; ++x)
+                mma_ts(o + part * C::Cols, a + 8 * x, d + part * kSlot + ((x * 2 * C::Group) >> 4), id_o, x > 0 || t > 0);
+              if (C::Streams == 1 || b == 1 || n1 <= t) mma_done(empty + slot + part);
             }
-            if (dead) break;
-            if (t >= 0) give(t, true);
-            if (t + 1 < n) give(t + 1, false);
-            if (t + 2 == n) mma_done(q_empty);
+            if (C::Streams == 1) mma_done(o_done);
+            if (next - (C::Streams == 2 ? 0 : 1) == mine) mma_done(o_full + (C::Streams == 1 ? 0 : b));
+          }
+          if (next < mine) {
+            const int slot = (e0 + place_of<C::Streams>(next, false, n) * C::Parts) % C::Slots;
+            if (C::Streams == 1 || b == 0 || n0 <= next) {
+#pragma unroll
+              for (int part = 0; part < C::Parts; ++part)
+                if (!take(slot + part, false)) break;
+              tc::fence_after_sync();
+            }
+            const uint64_t a = q_desc + (C::Streams == 1 ? 0 : b * (C::QTile >> 4)), d = k_desc + slot * kSlot;
+            const uint32_t to = tmem + C::S(0) + b * 128;
+#pragma unroll
+            for (int part = 0; part < C::Parts; ++part) {
+#pragma unroll
+              for (int x = 0; x < C::Cols / 16; ++x)
+                mma_ss(to, a + ((part * C::Blocks * 128 * 128 + (x >> 2) * (128 * 128) + (x & 3) * 32) >> 4), d + part * kSlot + (((x >> 2) * 1024 + (x & 3) * 32) >> 4),
+                       id_s, part > 0 || x > 0);
+              if (C::Parts > 1) mma_done(empty + slot + part);
+            }
+            mma_done(s_full + b);
+            if (C::Parts == 1 && (b == 1 || n1 <= next)) mma_done(empty + slot);
+            issued = true;
+            if (next + 1 == n && (C::Streams == 1 || b == 1 || n1 <= next)) mma_done(q_empty);
+          }
+          if (dead) break;
+          if (C::Streams == 2) {
+            t += b;
+            b ^= 1;
+            if (t >= n) break;
+          } else {
+            ++t;
+            b ^= 1;
+            if (t >= n) break;
           }
         }
         if (dead) break;
-        e0 += 2 * n * C::Parts;
+        e0 = (e0 + 2 * n * C::Parts) % C::Slots;
       }
       // tensor memory is given back once every product issued has completed, also where a wait gave up
       if (issued) {
@@ -658,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
           float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
+#pragma unroll
           for (int j = 0; j < kTile; j += 64) {
             uint32_t y[2][32];
             tc::tmem_ld_32x32b_x32(t_s + j, y[0]);
