@@ -37,7 +37,7 @@ using prompt::Work;
 __device__ int g_prompt_error = 0;  // set when a bounded wait gives up (trellis_device_error)
 
 constexpr int kThreads = 512;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kQueryWarp = 10, kWidenWarp = 12;
+constexpr int kCopyWarp = 0, kMmaWarp = 1, kQueryWarp = 2, kSoftmaxWarp = 4, kWidenWarp = 12;
 constexpr int kSoftmaxRegs = 152, kIssueRegs = 96, kWidenRegs = 112;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 65536 / 128, "what the block was launched with");
 constexpr int kWorks = 2;  // items that the copying warp has announced
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   constexpr bool kTwoWiden = F8 && C::Streams == 1;  // the second softmax warpgroup widens too: the odd slots
-  if (warp >= kWidenWarp || (kTwoWiden && warp >= 4 && warp < 8)) {
+  if (warp >= kWidenWarp || (kTwoWiden && warp >= kSoftmaxWarp + 4 && warp < kSoftmaxWarp + 8)) {
     // ---- widening and clearing
     if (warp >= kWidenWarp) regs_down<kWidenRegs>();
     else regs_up<kSoftmaxRegs>();
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       e0 += 2 * n * C::Parts;
     }
-  } else if (warp >= 8) {
+  } else if (warp < kSoftmaxWarp) {
     regs_down<kIssueRegs>();
     if (warp == kCopyWarp) {
       // ---- the warp that plans and copies
@@ -448,17 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = uniform(w.tiles), first_tail = uniform((w.prefix + w.first + 1) / kTile - w.tile0);
         const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
         if (!wait(q_full, (uint32_t)(k & 1))) break;
-        int t = C::Streams == 2 ? -1 : -2, b = 0;
-#pragma unroll 1
-        for (;;) {
+        int t = C::Streams == 2 ? -1 : -2;
+        const auto unit = [&](int b) {
           const int mine = C::Streams == 1 ? n : b ? n1 : n0, next = t + (C::Streams == 2 ? 1 : 2);
           if (t >= 0 && t < mine) {
             const int slot = (e0 + place_of<C::Streams>(t, true, n) * C::Parts) % C::Slots;
             if (C::Streams == 1 || b == 0 || n0 <= t)
 #pragma unroll
               for (int part = 0; part < C::Parts; ++part)
-                if (!take(slot + part, t >= first_tail)) break;
-            if (!wait(p_ready + b, p_phase >> b & 1u)) break;
+                if (!take(slot + part, t >= first_tail)) return;
+            if (!wait(p_ready + b, p_phase >> b & 1u)) return;
             p_phase ^= 1u << b;
             tc::fence_after_sync();
             const uint64_t d = v_desc + slot * kSlot;
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (C::Streams == 1 || b == 0 || n0 <= next) {
 #pragma unroll
               for (int part = 0; part < C::Parts; ++part)
-                if (!take(slot + part, false)) break;
+                if (!take(slot + part, false)) return;
               tc::fence_after_sync();
             }
             const uint64_t a = q_desc + (C::Streams == 1 ? 0 : b * (C::QTile >> 4)), d = k_desc + slot * kSlot;
@@ -496,15 +495,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             issued = true;
             if (next + 1 == n && (C::Streams == 1 || b == 1 || n1 <= next)) mma_done(q_empty);
           }
-          if (dead) break;
-          if (C::Streams == 2) {
-            t += b;
-            b ^= 1;
-            if (t >= n) break;
-          } else {
-            ++t;
-            b ^= 1;
-            if (t >= n) break;
+        };
+        // One copy of it, or two: with heads of 128 in bf16 the products are what bounds, and fewer instructions between them weigh more
+        // than their number (8192 tokens 372 us and 397, e4m3 600 and 565).
+        constexpr bool kTwice = D == 128 && !F8;
+        if (kTwice) {
+#pragma unroll 1
+          for (; t < n && !dead; ++t) {
+            unit(0);
+            if (!dead) unit(1);
+          }
+        } else {
+#pragma unroll 1
+          for (int b = 0; t < n && !dead; b ^= 1) {
+            unit(b);
+            t += C::Streams == 2 ? b : 1;
           }
         }
         if (dead) break;
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---- softmax: stream s, one thread per row; warp i of a group reaches tensor memory lanes 32 i ..
     regs_up<kSoftmaxRegs>();
-    const int s = warp >> 2, r = threadIdx.x;  // row of the block
+    const int s = (warp - kSoftmaxWarp) >> 2, r = threadIdx.x - kSoftmaxWarp * 32;  // row of the block
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const int cta = (int)blockIdx.x;
     Work w;
@@ -747,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float vs = p.scales ? __ldg(p.scales + p.hkv + w.head) : 1.f, f = l == 0.f ? 0.f : vs / l;
           // 32 columns at a time through shared memory, so that 64 bytes of a row are stored by four lanes together (a row per lane:
           // four times as many accesses, the end of an item took 4000 cycles)
-          uint8_t* stage = stages + warp * C::Stage;
+          uint8_t* stage = stages + (warp - kSoftmaxWarp) * C::Stage;
           uint16_t* out[4];
           bool has[4];
 #pragma unroll
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_before_sync();  // the accumulator is read before the next stretch's weights are announced
       }
-    if (threadIdx.x == 0) p.items[cta] = shared_item;
+    if (r == 0) p.items[cta] = shared_item;
   }
   tc::fence_before_sync();
   __syncthreads();
