@@ -8,9 +8,11 @@
 // and an O each, so that one's products run while the other's softmax does.  Heads of 256, whose O takes half of tensor memory:
 // 128 rows, one stream whose tiles alternate between two S.
 // Rows see keys up to their own position: only the last tiles of an item are masked, and streams end where their rows do.
-// Keys and values arrive by TMA in a ring of slots in the order of their use.  An e4m3 cache is copied into the upper half of a
-// slot and widened in place to fp16 (exact).  The queries are fp16 then, each row at a power of two that brings its largest number
-// to 2^14 .. 2^15: bf16 numbers down to 2^-31 of it are exact, others within 2^-40 of it.  Values that a product must not meet (rows past the end, numbers that are not finite
+// Keys and values arrive by TMA in a ring of slots in the order of their use.  Of an e4m3 cache the keys are multiplied as they are, as
+// in tree_attention_tc1.cu: each row of queries is scaled by a power of two and split into an e4m3 and an e5m2 number, exactly down to
+// 2^-13 of the row's largest and within 2^-21 of it below, so S is two 8-bit products at twice the rate.  The values are copied into
+// the upper half of a slot and widened in place to fp16 (exact); P is fp16 then, since weights of 4 bits would not do.  (Keys widened
+// too: 8192 tokens of heads of 256 took 730 us.)  Values that a product must not meet (rows past the end, numbers that are not finite
 // where not every row sees them) are cleared on the way, the latter added back for the rows that see them (rare).
 // The warps: two softmax warpgroups (a thread per row, a tile's scores in registers); the warp that plans and copies, the one
 // that issues, two that bring the queries; a warpgroup that widens and clears.
@@ -58,10 +60,15 @@ struct Cfg {
   static __device__ __forceinline__ int at(int row, int chunk) {  // 8 numbers
     return (row >> 3) * Group + (chunk >> 3) * 1024 + (row & 7) * 128 + (((chunk & 7) ^ (row & 7)) << 4);
   }
-  static constexpr int QTile = 128 * D * 2;
+  static constexpr int QTile = 128 * D * 2;         // bf16, or two 8-bit numbers: the high parts, then the low ones
+  static constexpr int QBuffers = D == 64 ? 2 : 1;  // the next stretch's queries are brought early where there is room
+  // An 8-bit row of a slot (a block): 128 bytes in the 128-byte swizzle, or 64 in the 64-byte one.
+  static __device__ __forceinline__ int at8(int row, int chunk) {  // 16 numbers
+    return row * Cols + ((chunk ^ (Cols == 128 ? row & 7 : row >> 1 & 3)) << 4);
+  }
   static constexpr int Stage = 32 * 64;             // 32 columns of a warp's rows, on their way out
-  static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 2 * Rows * 4 + 1024;
-  static constexpr int Smem = 1024 + Slots * Slot + Streams * (QTile + 4 * Stage) + Fixed;
+  static constexpr int Fixed = (int)sizeof(prompt::Map) + kWorks * (int)sizeof(Work) + 4 * Rows * 4 + 1024;
+  static constexpr int Smem = 1024 + Slots * Slot + Streams * (QBuffers * QTile + 4 * Stage) + Fixed;
   static_assert(Smem <= 227 * 1024, "fits");
   template <bool F8>
   static constexpr float Lift = F8 ? 7.f : 0.f;     // log2 of a factor of the weights: with it fp16 ones reach 2^15
@@ -137,6 +144,26 @@ __device__ __forceinline__ bool is_done(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
+// D[tmem] (+)= A[smem desc] * B[smem desc], 8-bit inputs, each of the kind that the descriptor says, fp32 accumulate.
+__device__ __forceinline__ void mma_ss_f8(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 // As desc_mnmajor (tree_tc.cuh), `sbo` bytes from 8 rows to the next 8.
 __device__ __forceinline__ uint64_t desc_values(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return (desc_mnmajor(saddr, lbo) & ~((uint64_t)0x3FFF << 32)) | (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
@@ -168,17 +195,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* ring = base;
   uint8_t* sq = ring + C::Slots * C::Slot;
-  uint8_t* stages = sq + C::Streams * C::QTile;
-  float* row_fac = reinterpret_cast<float*>(stages + C::Streams * 4 * C::Stage);  // e4m3: [stretch % 2][row] of the row's scores
-  prompt::Map& plan = *reinterpret_cast<prompt::Map*>(row_fac + 2 * C::Rows);
+  uint8_t* stages = sq + C::QBuffers * C::Streams * C::QTile;
+  float* row_up = reinterpret_cast<float*>(stages + C::Streams * 4 * C::Stage);  // e4m3: [stretch % 4][row] log2 of the queries' scale
+  prompt::Map& plan = *reinterpret_cast<prompt::Map*>(row_up + 4 * C::Rows);
   Work* works = reinterpret_cast<Work*>(&plan + 1);
   uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(works + kWorks) + 7) & ~(uintptr_t)7);
-  uint64_t* tail_full = full + C::Slots;  // bf16: of values that are cleared first.  A thread that waits for a phase has to have seen
-  uint64_t* empty = tail_full + C::Slots;  // the one before, and the clearing warps see no others
+  uint64_t* raw_full = full + C::Slots;   // of values that are widened, or cleared, first.  A thread that waits for a phase has to have
+  uint64_t* empty = raw_full + C::Slots;  // seen the one before, and the widening warps see no others
   uint64_t* ready = empty + C::Slots;   // widened, or clear
-  uint64_t* q_full = ready + C::Slots;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* s_full = q_empty + 1;       // [2] scores there
+  uint64_t* q_full = ready + C::Slots;  // [QBuffers]
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;       // [2] scores there
   uint64_t* p_ready = s_full + 2;       // [2] weights written
   uint64_t* o_full = p_ready + 2;       // [2] the stretch's last product complete
   uint64_t* o_done = o_full + 2;        // one stream: each product with the values
@@ -194,12 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::prefetch_tmap(&map);
     for (int i = 0; i < C::Slots; ++i) {
       tc::mbar_init(full + i, 1);
-      tc::mbar_init(tail_full + i, 1);
+      tc::mbar_init(raw_full + i, 1);
       tc::mbar_init(empty + i, 1);
       tc::mbar_init(ready + i, 4);
     }
-    tc::mbar_init(q_full, 2);
-    tc::mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(q_full + i, 2);
+      tc::mbar_init(q_empty + i, 1);
+    }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(s_full + s, 1);
       tc::mbar_init(p_ready + s, 4);
@@ -262,19 +291,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool value;
         const int t = tile_at<C::Streams>(e, n, &value);
         const bool tail = value && (w.tile0 + t + 1) * kTile > shared_to;
-        if (!F8 && !tail) continue;
+        if (!value || (!F8 && !tail)) continue;
         for (int part = 0; part < C::Parts; ++part) {
           const int at = e0 + e * C::Parts + part, slot = at % C::Slots;
           if (kTwoWiden && (slot & 1) != group_bar - 2) continue;
           const int pos0 = (w.tile0 + t) * kTile;
-          wait((F8 ? full : tail_full) + slot, f_phase >> slot & 1u);
+          wait(raw_full + slot, f_phase >> slot & 1u);
           f_phase ^= 1u << slot;
           uint8_t* tile = ring + slot * C::Slot;
           if constexpr (F8) {
             constexpr int Chunks = C::Cols / 16, Each = Chunks;  // 16 numbers; of a row, of a thread
             uint4 v[Each];
 #pragma unroll
-            for (int i = 0; i < Each; ++i) v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + (i * 128 + tid) * 16);
+            for (int i = 0; i < Each; ++i)
+              v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + C::at8((i * 128 + tid) / Chunks, (i * 128 + tid) % Chunks));
             if (!tc::bar_and(!dead, group_bar, 128)) {  // all of it is in registers
               dead = true;
               break;
@@ -356,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         end = (int)((int64_t)(cta + 1) * plan.total / plan.ctas);
       }
       int e0 = 0, copied = 0;
-      uint32_t f_phase = 0, t_phase = 0, is_tail = 0;  // per slot: copies into it, of tail values; what the last one was
+      uint32_t f_phase = 0, r_phase = 0, is_raw = 0;  // per slot: copies into it, those for the widening warps; what the last one was
       for (int k = 0;; ++k) {
         Work w = plan.split ? prompt::next_stretch<C::Rows>(p, plan, at, end) : prompt::whole_item<C::Rows>(p, plan, item);
         if (!plan.split && w.more && lane == 0) fetched = atomicAdd(p.counter, 1);  // the one after it
@@ -392,20 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int y = value ? (C::Streams == 1 && t + 1 < n ? before : now) + to_values : now;
           const int left = w.len - (w.tile0 + t) * kTile, boxes = min(kTile, left + box - 1) >> p.page_shift;
-          const bool tail = !F8 && value && (w.tile0 + t + 1) * kTile > shared_to;
+          const bool through = value && (F8 || (w.tile0 + t + 1) * kTile > shared_to);  // the widening warps
 #pragma unroll 1
           for (int part = 0; part < C::Parts; ++part) {
             const int i = e0 + e * C::Parts + part, slot = i % C::Slots, use = i / C::Slots;
             if (use > 0 && !wait(empty + slot, (uint32_t)(use & 1) ^ 1u)) break;
-            const uint32_t bar = tc::smem_u32((tail ? tail_full : full) + slot), to = tc::smem_u32(ring) + slot * C::Slot;
-            (tail ? t_phase : f_phase) ^= 1u << slot;
-            is_tail = (is_tail & ~(1u << slot)) | (uint32_t)tail << slot;
+            const uint32_t bar = tc::smem_u32((through ? raw_full : full) + slot),
+                           to = tc::smem_u32(ring) + slot * C::Slot + (F8 && value ? C::Slot / 2 : 0);
+            (through ? r_phase : f_phase) ^= 1u << slot;
+            is_raw = (is_raw & ~(1u << slot)) | (uint32_t)through << slot;
             expect_bytes(bar, (uint32_t)(boxes * box * C::Cols * (F8 ? 1 : 2)));
             copied = i + 1;
 #pragma unroll 1
             for (int j = 0; j < boxes; ++j) {
               const int row = __shfl_sync(0xFFFFFFFFu, y, j);
-              if constexpr (F8) tma_load_2d(to + C::Slot / 2 + j * box * C::Cols, &map, bar, part * C::Cols, row);
+              if constexpr (F8) tma_load_2d(to + j * box * C::Cols, &map, bar, part * C::Cols, row);
               else tma_load_4d(to + (j * box >> 3) * C::Group, &map, bar, part * C::Blocks, row >> 3);
             }
           }
@@ -417,28 +448,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // no copy may land in a block that has left
       for (int i = max(0, copied - C::Slots); i < copied; ++i) {
         const int slot = i % C::Slots;
-        const bool tail = is_tail >> slot & 1u;
-        tc::mbar_wait((tail ? tail_full : full) + slot, ((tail ? t_phase : f_phase) >> slot & 1u) ^ 1u, kDrainNs);
+        const bool was_raw = is_raw >> slot & 1u;
+        tc::mbar_wait((was_raw ? raw_full : full) + slot, ((was_raw ? r_phase : f_phase) >> slot & 1u) ^ 1u, kDrainNs);
       }
     } else if (warp == kMmaWarp) {
       // ---- the warp that issues the products.  All it does between two products is on the way of both streams, at 5 to 10 cycles an
       // instruction: so what it needs is carried along, not computed, and there is one copy of the code.
       bool issued = false;
       Work w;
-      constexpr uint32_t kF16 = F8 ? ~((1u << 7) | (1u << 10)) : ~0u;  // both operands fp16 instead
-      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & kF16, id_o = (tc::idesc_bf16_f32(128, C::Cols) & kF16) | kBMnMajor;
+      constexpr uint32_t kNoType = ~((1u << 7) | (1u << 10));  // both operands fp16, or e4m3
+      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, kTile) & (F8 ? kNoType : ~0u),
+                         id_o = (tc::idesc_bf16_f32(128, C::Cols) & (F8 ? kNoType : ~0u)) | kBMnMajor;
       constexpr uint32_t kSlot = C::Slot >> 4;
-      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), 1024, 2), k_desc = tc::desc_kmajor(tc::smem_u32(ring), C::Group, 2),
+      constexpr uint32_t kSwizzle = F8 && C::Cols == 64 ? 4 : 2, kRows8 = F8 ? 8 * C::Cols : 1024;
+      const uint64_t q_desc = tc::desc_kmajor(tc::smem_u32(sq), kRows8, kSwizzle), k_desc = tc::desc_kmajor(tc::smem_u32(ring), F8 ? kRows8 : C::Group, kSwizzle),
                      v_desc = desc_values(tc::smem_u32(ring), 1024, C::Group);
-      uint32_t p_phase = 0, f_phase = 0, t_phase = 0;  // per S; per slot, of all that is not a tail's values, and of those
+      uint32_t p_phase = 0, f_phase = 0, r_phase = 0;  // per S; per slot, of what comes directly, and of the rest
       int e0 = 0;                                      // the slot of the stretch's first copy
-      const auto take = [&](int slot, bool tail) {     // waits for a slot's tile
-        if (tail && !F8) {
-          if (!wait(tail_full + slot, t_phase >> slot & 1u) || !wait(ready + slot, t_phase >> slot & 1u)) return false;
-          t_phase ^= 1u << slot;
+      const auto take = [&](int slot, bool through) {  // waits for a slot's tile
+        if (through) {
+          if (!wait(raw_full + slot, r_phase >> slot & 1u) || !wait(ready + slot, r_phase >> slot & 1u)) return false;
+          r_phase ^= 1u << slot;
           return true;
         }
-        if (!wait((F8 ? ready : full) + slot, f_phase >> slot & 1u)) return false;
+        if (!wait(full + slot, f_phase >> slot & 1u)) return false;
         f_phase ^= 1u << slot;
         return true;
       };
@@ -447,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // by the scores of unit u + 2.
         const int n = uniform(w.tiles), first_tail = uniform((w.prefix + w.first + 1) / kTile - w.tile0);
         const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
-        if (!wait(q_full, (uint32_t)(k & 1))) break;
+        const int qb = k % C::QBuffers;
+        if (!wait(q_full + qb, (uint32_t)(k / C::QBuffers & 1))) break;
+        const uint64_t q_at = q_desc + (uint32_t)(qb * (C::Streams * C::QTile >> 4));
         int t = C::Streams == 2 ? -1 : -2;
         const auto unit = [&](int b) {
           const int mine = C::Streams == 1 ? n : b ? n1 : n0, next = t + (C::Streams == 2 ? 1 : 2);
@@ -456,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (C::Streams == 1 || b == 0 || n0 <= t)
 #pragma unroll
               for (int part = 0; part < C::Parts; ++part)
-                if (!take(slot + part, t >= first_tail)) return;
+                if (!take(slot + part, F8 || t >= first_tail)) return;
             if (!wait(p_ready + b, p_phase >> b & 1u)) return;
             p_phase ^= 1u << b;
             tc::fence_after_sync();
@@ -480,10 +515,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!take(slot + part, false)) return;
               tc::fence_after_sync();
             }
-            const uint64_t a = q_desc + (C::Streams == 1 ? 0 : b * (C::QTile >> 4)), d = k_desc + slot * kSlot;
+            const uint64_t a = q_at + (C::Streams == 1 ? 0 : b * (C::QTile >> 4)), d = k_desc + slot * kSlot;
             const uint32_t to = tmem + C::S(0) + b * 128;
 #pragma unroll
             for (int part = 0; part < C::Parts; ++part) {
+              if constexpr (F8) {  // [high, low part][block of 128 columns][row]
+#pragma unroll
+                for (int low = 0; low < 2; ++low)
+#pragma unroll
+                  for (int x = 0; x < C::Cols / 32; ++x)
+                    mma_ss_f8(to, a + ((low * C::QTile / 2 + part * 128 * C::Cols + x * 32) >> 4), d + part * kSlot + (x * 32 >> 4), id_s | (uint32_t)low << 7,
+                              part > 0 || low > 0 || x > 0);
+              } else
 #pragma unroll
               for (int x = 0; x < C::Cols / 16; ++x)
                 mma_ss(to, a + ((part * C::Blocks * 128 * 128 + (x >> 2) * (128 * 128) + (x & 3) * 32) >> 4), d + part * kSlot + (((x >> 2) * 1024 + (x & 3) * 32) >> 4),
@@ -493,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_done(s_full + b);
             if (C::Parts == 1 && (b == 1 || n1 <= next)) mma_done(empty + slot);
             issued = true;
-            if (next + 1 == n && (C::Streams == 1 || b == 1 || n1 <= next)) mma_done(q_empty);
+            if (next + 1 == n && (C::Streams == 1 || b == 1 || n1 <= next)) mma_done(q_empty + qb);
           }
         };
         // One copy of it, or two: with heads of 128 in bf16 the products are what bounds, and fewer instructions between them weigh more
@@ -525,12 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tid = threadIdx.x - kQueryWarp * 32;
       Work w;
       for (int k = 0; told(k, w); ++k) {
-        if (k > 0 && !wait(q_empty, (uint32_t)(k & 1) ^ 1u)) break;
         const float ks = p.scales ? __ldg(p.scales + w.head) : 1.f;
         const uint32_t flip = p.scale_log2 * ks < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
         constexpr int LPR = D / 8, kRows = 64 / LPR;  // lanes of a row, rows at a time
         const int ch = tid % LPR, r0 = tid / LPR;
-        uint8_t* to = sq + (ch >> 3) * (128 * 128) + r0 * 128;
+        uint8_t* to = sq + k % C::QBuffers * (C::Streams * C::QTile);
         // (token, head of the group) of row r0 + kRows i, without a division each
         int d = tree_draft(p, w.g0 + r0), hh = w.g0 + r0 - d * p.group;
         const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
@@ -544,8 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             src += wrap;
           }
         };
-        const auto place = [&](int r) { return (r >> 7) * C::QTile + ((r & 127) - r0) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+        const auto room = [&] { return k < C::QBuffers || wait(q_empty + k % C::QBuffers, (uint32_t)(k / C::QBuffers & 1) ^ 1u); };
         if constexpr (!F8) {
+          const auto place = [&](int r) { return (r >> 7) * C::QTile + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+          if (!room()) break;
 #pragma unroll 4
           for (int r = r0; r < w.rows; r += kRows) {
             cp_async16(tc::smem_u32(to) + place(r), src);
@@ -559,41 +603,64 @@ __global__ void __launch_bounds__(kThreads, 1)
               *at = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
             }
         } else {
-          constexpr int kMost = 4;  // rows whose loads are in flight
+          constexpr int kMost = 8;  // rows whose loads are in flight
+          const int d0 = d, h0 = hh;
+          const uint16_t* src0 = src;
+          // Twice over the rows: for their scales, before the place is free, then for the numbers.
 #pragma unroll 1
-          for (int r1 = r0; r1 < C::Rows; r1 += kRows * kMost) {
-            uint4 u[kMost];
-#pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-              u[i] = make_uint4(0, 0, 0, 0);
-              if (r1 + i * kRows < w.rows) u[i] = *reinterpret_cast<const uint4*>(src);
-              next();
+          for (int pass = 0; pass < 2; ++pass) {
+            if (pass == 1) {
+              if (!room()) break;
+              d = d0;
+              hh = h0;
+              src = src0;
+              __syncwarp();
             }
+#pragma unroll 1
+            for (int r1 = r0; r1 < C::Rows && r1 - r0 < w.rows; r1 += kRows * kMost) {
+              uint4 u[kMost];
 #pragma unroll
-            for (int i = 0; i < kMost; ++i) {
-              const int r = r1 + i * kRows;
-              // the row's largest number: positive bf16 patterns compare like integers, two at a time
-              uint32_t big = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
+              for (int i = 0; i < kMost; ++i) {
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (r1 + i * kRows < w.rows) u[i] = *reinterpret_cast<const uint4*>(src);
+                next();
+              }
 #pragma unroll
-              for (int o = 1; o < (LPR < 32 ? LPR : 32); o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-              const uint32_t top = max(big & 0xFFFFu, big >> 16) >> 7;  // its exponent
-              // times 2^(141 - top): exact in two steps, each a power of two that fp32 holds
-              const int up = min(141 - (int)top, 250), half = up / 2;
-              const float f0 = __uint_as_float((uint32_t)(127 + half) << 23), f1 = __uint_as_float((uint32_t)(127 + up - half) << 23);
-              const auto f16 = [&](uint32_t x) {
-                x ^= flip;
-                return pack_f16x2(bf16lo_to_f32(x) * f0 * f1, bf16hi_to_f32(x) * f0 * f1);
-              };
-              if (r < w.rows) {
-                *reinterpret_cast<uint4*>(to + place(r)) = make_uint4(f16(u[i].x), f16(u[i].y), f16(u[i].z), f16(u[i].w));
-                if (ch == 0) row_fac[(k & 1) * C::Rows + r] = (float)up;
+              for (int i = 0; i < kMost; ++i) {
+                const int r = r1 + i * kRows;
+                if (pass == 0) {
+                  // the row's largest number: positive bf16 patterns compare like integers, two at a time
+                  uint32_t big = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
+#pragma unroll
+                  for (int o = 1; o < LPR; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+                  const uint32_t top = max(big & 0xFFFFu, big >> 16) >> 7;  // its exponent: comes to 2^7 .. 2^8
+                  if (r < w.rows && ch == 0) row_up[(k & 3) * C::Rows + r] = (float)min(134 - (int)top, 127);
+                  continue;
+                }
+                if (r >= w.rows) continue;
+                const float f = __uint_as_float((uint32_t)(127 + (int)row_up[(k & 3) * C::Rows + r]) << 23);
+                uint32_t hi[4], lo[4];
+                const uint32_t x[4] = {u[i].x ^ flip, u[i].y ^ flip, u[i].z ^ flip, u[i].w ^ flip};
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const float a = bf16lo_to_f32(x[z]) * f, b = bf16hi_to_f32(x[z]) * f;
+                  hi[z] = e4m3x2(a, b);
+                  const uint32_t back = widen2((uint16_t)hi[z]);
+                  lo[z] = e5m2x2(a - f16_to_f32((uint16_t)back), b - f16_to_f32((uint16_t)(back >> 16)));
+                }
+                // 8 numbers: half of a chunk of 16
+                const int half_chunk = ch % (C::Cols / 8);
+                uint8_t* at = to + (r >> 7) * C::QTile + ch / (C::Cols / 8) * (128 * C::Cols) + C::at8(r & 127, half_chunk >> 1) + (half_chunk & 1) * 8;
+                *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2*>(at + C::QTile / 2) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
               }
             }
           }
+          if (dead) break;
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(q_full);
+        if (lane == 0) tc::mbar_arrive(q_full + k % C::QBuffers);
       }
     }
   } else {
@@ -622,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_phase ^= 1u << buf;
           tc::fence_after_sync();
           if (F8 && i == 0) {  // 2^-up of the row's queries
-            const int up = (int)row_fac[(k & 1) * C::Rows + r], half = up / 2;
+            const int up = (int)row_up[(k & 3) * C::Rows + r], half = up / 2;
             c *= __uint_as_float((uint32_t)(127 - half) << 23);
             c *= __uint_as_float((uint32_t)(127 - (up - half)) << 23);
             c = c != c ? c : score_factor(fminf(c, 3.402823466e38f));
@@ -874,11 +941,12 @@ cudaError_t launch_prompt_attention(const uint16_t* q, int64_t q_stride, const t
   const cuuint64_t rows = (cuuint64_t)(c.pages * 2 * c.heads * c.page_size);
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult made;
-  if (f8) {  // as it lies in the cache
+  if (f8) {  // 128 bytes (or 64) of each row, swizzled
     const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, rows}, strides[1] = {(cuuint64_t)row_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)c.page_size};
     made = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+              cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   } else {  // (64 numbers, 8 rows, blocks of 64 of a row, groups of 8 rows): what a slot holds, 8 rows of a block swizzled together
     const cuuint64_t dims[4] = {64, 8, (cuuint64_t)(c.head_dim / 64), rows / 8},
                      strides[3] = {(cuuint64_t)row_bytes, 128, (cuuint64_t)row_bytes * 8};
