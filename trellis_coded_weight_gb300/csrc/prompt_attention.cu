@@ -42,7 +42,7 @@ constexpr int kThreads = 512;
 constexpr int kCopyWarp = 0, kMmaWarp = 1, kQueryWarp = 2, kSoftmaxWarp = 4, kWidenWarp = 12;
 constexpr int kSoftmaxRegs = 152, kIssueRegs = 96, kWidenRegs = 112;
 static_assert(2 * kSoftmaxRegs + kIssueRegs + kWidenRegs <= 65536 / 128, "what the block was launched with");
-constexpr int kWorks = 2;  // items that the copying warp has announced
+constexpr int kWorks = 4;  // stretches that the copying warp has announced
 constexpr int kOdd = 8;    // items whose odd values are known at a time: the widening warps are a few ahead of the softmax at the most
 
 template <int D>
@@ -378,26 +378,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down<kIssueRegs>();
     if (warp == kCopyWarp) {
       // ---- the warp that plans and copies
-      const int grid = (int)gridDim.x, cta = (int)blockIdx.x;
+      const int cta = (int)blockIdx.x;
       const int box = 1 << p.page_shift;  // rows of one copy: a page's
-      int at = 0, end = 0, item = cta, fetched = 0;
+      int at = 0, end = 0, item = cta;
       if (plan.split && cta < plan.ctas) {
         at = (int)((int64_t)cta * plan.total / plan.ctas);
         end = (int)((int64_t)(cta + 1) * plan.total / plan.ctas);
       }
       int e0 = 0, copied = 0;
       uint32_t f_phase = 0, r_phase = 0, is_raw = 0;  // per slot: copies into it, those for the widening warps; what the last one was
-      for (int k = 0;; ++k) {
-        Work w = plan.split ? prompt::next_stretch<C::Rows>(p, plan, at, end) : prompt::whole_item<C::Rows>(p, plan, item);
-        if (!plan.split && w.more && lane == 0) fetched = atomicAdd(p.counter, 1);  // the one after it
+      // The next stretch is planned and announced before the tiles of this one are copied, so that its queries are brought meanwhile.
+      const auto announce = [&](int k, Work& w) {
+        if (plan.split) {
+          w = prompt::next_stretch<C::Rows>(p, plan, at, end);
+        } else {
+          if (k > 0) {
+            if (lane == 0) item = (int)gridDim.x + atomicAdd(p.counter, 1);
+            item = __shfl_sync(0xFFFFFFFFu, item, 0);
+          }
+          w = prompt::whole_item<C::Rows>(p, plan, item);
+        }
         const int s = k % kWorks;
-        if (k >= kWorks && !wait(w_empty + s, (uint32_t)(k / kWorks & 1) ^ 1u)) break;
+        if (k >= kWorks && !wait(w_empty + s, (uint32_t)(k / kWorks & 1) ^ 1u)) return false;
         if (lane == 0) {
           works[s] = w;
           tc::mbar_arrive(w_full + s);
         }
         __syncwarp();
-        if (!w.more) break;
+        return true;
+      };
+      Work w, following;
+      announce(0, w);
+      for (int k = 0; w.more; ++k, w = following) {
+        if (!announce(k + 1, following)) break;
         const int n = w.tiles;
         TreeSegment g;
         g.seq = TreeSeq{w.start, w.len - w.prefix, w.prefix};
@@ -442,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         e0 += 2 * n * C::Parts;
-        if (!plan.split) item = grid + __shfl_sync(0xFFFFFFFFu, fetched, 0);
         if (dead) break;
       }
       // no copy may land in a block that has left
