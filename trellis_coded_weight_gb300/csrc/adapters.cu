@@ -26,14 +26,20 @@ constexpr int kCluster = 4;
 constexpr int kCopyLd = 36;                // floats from token to token of a warp's products of 32 ranks: bank conflicts of two
 constexpr int kCopy = 64 * kCopyLd;        // floats of a warp's products: 64 tokens by 32 ranks, or 32 by 64
 constexpr int kCopyBytes = kWarps / 2 * kCopy * 4;
-constexpr int kRing = 64 * 1024;           // copies in flight
-constexpr int kWarpRing = kRing / kWarps;
-constexpr int kSmem = kCopyBytes + kRing + kAdapterTile * 4;
-// With more than 64 ranks h takes half of each warp's ring for the second product.
-constexpr int kWideRing = kWarpRing / 2;
-static_assert(kAdapterTile * kAdapterMaxRank * 4 <= kRing / 2, "h, as fragments");
+// A kernel for each bound on the rank: with ranks up to 32 two blocks of 128 registers a thread share an SM, with more one of 255 has
+// it (two: 4096 tokens of rank 64, 17408 inputs: 108 us for 97, spilling), which also leaves room for more copies in flight.
+template <int RMAX>
+struct Size {
+  static constexpr int Blocks = RMAX <= 32 ? 2 : 1;    // of an SM
+  static constexpr int Ring = (RMAX <= 32 ? 64 : 128) * 1024;  // copies in flight
+  static constexpr int WarpRing = Ring / kWarps;
+  // With more than 64 ranks h takes half of each warp's ring for the second product.
+  static constexpr int WideRing = WarpRing / 2;
+  static constexpr int Smem = kCopyBytes + Ring + kAdapterTile * 4;
+  static_assert(kAdapterTile * kAdapterMaxRank * 4 <= Ring / 2, "h, as fragments");
+  static_assert(Blocks * (Smem + 1024) <= 228 * 1024, "fits");
+};
 static_assert(kAdapterTile * 64 * 4 <= kCopyBytes / 2, "the second half of the products gives way to h");
-static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two blocks an SM");
 
 struct AddParams {
   const uint16_t *x, *y;
@@ -85,10 +91,12 @@ struct Share {
 
 // h of the block's part of the inputs, for 16 MT tokens.  Where tokens are many, a lane copies what it needs of x into its warp's ring,
 // some blocks of 32 inputs ahead (x comes from HBM; loads into registers kept half as many bytes in flight); A is loaded one block ahead.
-template <int MT, bool NARROW, int NB>
+template <int RMAX, int MT, bool NARROW, int NB>
 __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, int rank, int count, const int* tokens, int rank_of_block,
                                        uint8_t* rings, float* copies) {
   using H = Share<MT, NB>;
+  constexpr int kWarpRing = Size<RMAX>::WarpRing;
+  constexpr bool kRoom = RMAX > 32;  // for registers
   constexpr int WT = H::Tokens / 16, NT = NARROW ? 2 : H::Ranks / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int side = warp % H::Sides, group = warp / H::Sides % H::Groups, split = warp / H::Sides / H::Groups;
@@ -122,7 +130,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
       }
   };
   if (MT > 1) {
-    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage;
+    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage < 8 ? kWarpRing / kStage : 8;
     uint8_t* ring = rings + warp * kWarpRing;
     const auto copy = [&](int k, int s) {
       if (k < k1 && 32 * k + 8 * q < p.ad.in)
@@ -139,7 +147,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
 #pragma unroll 1
     for (; k < k1; k += H::Splits) {
       uint4 next[NT], u[2 * WT];
-      if (NT <= 4) load_a(k + H::Splits, next);
+      if (NT <= 4 || kRoom) load_a(k + H::Splits, next);
       cp_async_wait<kStages - 1>();
       const bool in = 32 * k + 8 * q < p.ad.in;
 #pragma unroll
@@ -150,7 +158,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
       copy(k + kStages * H::Splits, stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
       multiply(u, v);
-      if (NT <= 4) {
+      if (NT <= 4 || kRoom) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] = next[j];
       } else {
@@ -159,7 +167,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
     }
     cp_async_wait<0>();
   } else {
-    constexpr int kAhead = 3;  // blocks whose loads are in flight
+    constexpr int kAhead = kRoom ? 6 : 3;  // blocks whose loads are in flight
     for (int k = k0 + split; k < k1; k += H::Splits * kAhead) {
       uint4 u[kAhead][2 * WT], v[kAhead][NT];
 #pragma unroll
@@ -215,13 +223,14 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
 
 // The sums over the cluster, as fragments: words of (token tile, block of 32 (NARROW: 16) ranks, step, high or low part), a lane's four
 // together.  Blocks of 512 words lie one behind the other, or with more than 64 ranks two in the second half of each warp's ring.
-template <bool NARROW, int NB>
+template <int RMAX, bool NARROW, int NB>
 __device__ __forceinline__ int fragment(int mt, int kb, int step, int low) {
+  constexpr int kWarpRing = Size<RMAX>::WarpRing, kPerWarp = 16 / kWarps;
   if (NARROW) return (mt * 2 + low) * 128;
   const int block = mt * NB + kb;
-  return (NB == 4 ? (block >> 1) * (kWarpRing / 4) + kWideRing / 4 + (block & 1) * 512 : block * 512) + (step * 2 + low) * 128;
+  return (NB == 4 ? block / kPerWarp * (kWarpRing / 4) + kWarpRing / 8 + block % kPerWarp * 512 : block * 512) + (step * 2 + low) * 128;
 }
-template <int MT, bool NARROW, int NB>
+template <int RMAX, int MT, bool NARROW, int NB>
 __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
   constexpr int wide = NB * (NARROW ? 16 : 32) / 2;  // pairs of ranks
   for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
@@ -242,18 +251,20 @@ __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
     const int row = t & 15, kb = NARROW ? 0 : r >> 5;
     const int q = NARROW ? r >> 2 : (r & 31) >> 3, step = NARROW ? 0 : (r & 7) >> 2, pair = (r & 3) >> 1;
     const int word = ((row & 7) * 4 + q) * 4 + (row >> 3) + 2 * pair;
-    h[fragment<NARROW, NB>(t >> 4, kb, step, 0) + word] = (x >> 16) | y;
-    h[fragment<NARROW, NB>(t >> 4, kb, step, 1) + word] = pack_bf16x2(lx, ly);
+    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 0) + word] = (x >> 16) | y;
+    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 1) + word] = pack_bf16x2(lx, ly);
   }
 }
 
 // The second product: outputs of blocks o0 + warp, + kWarps, .. < o1 of 32, for 16 MT tokens.  What a lane needs of y (few tokens: and
 // of B) it copies itself into its warp's ring, some blocks ahead; the first ones before h is there.
-template <int MT, bool NARROW, int NB>
+template <int RMAX, int MT, bool NARROW, int NB>
 struct Expand {
+  static constexpr int kWarpRing = Size<RMAX>::WarpRing, kWideRing = Size<RMAX>::WideRing;
+  static constexpr bool kRoom = RMAX > 32;  // for registers
   static constexpr bool kRingB = MT == 1 && NB <= 2;  // B goes through the ring too, else it is loaded one block ahead
   static constexpr int kY = 2 * MT * 512, kB = kRingB ? 4 * NB * (NARROW ? 256 : 512) : 0, kStage = kY + kB;
-  static constexpr int kStages = (NB == 4 ? kWideRing : kWarpRing) / kStage;
+  static constexpr int kFit = (NB == 4 ? kWideRing : kWarpRing) / kStage, kStages = kFit < 4 ? kFit : 4;
   static_assert(kStages >= 1, "a block");
   const AddParams& p;
   const uint16_t* b;
@@ -322,7 +333,7 @@ struct Expand {
     const uint32_t* hl = h + 4 * lane;
     const bool ragged = rank % (NARROW ? 4 : 8) != 0;
     uint4 v[4][NB], next[4][NB];
-    if constexpr (!kRingB && NB < 4) load(o, next);
+    if constexpr (!kRingB && (NB < 4 || kRoom)) load(o, next);
 #pragma unroll 1
     for (; o < o1; o += kWarps) {
       cp_async_wait<kStages - 1>();
@@ -345,7 +356,7 @@ struct Expand {
               v[j][kb] = *reinterpret_cast<const uint4*>(from + kY + ((j * NB + kb) * 32 + lane) * 16);
             }
           }
-      } else if constexpr (NB < 4) {
+      } else if constexpr (NB < 4 || kRoom) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -378,7 +389,7 @@ struct Expand {
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
           for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
-            const uint4 a = *reinterpret_cast<const uint4*>(hl + fragment<NARROW, NB>(i, kb, f >> 1, f & 1));
+            const uint4 a = *reinterpret_cast<const uint4*>(hl + fragment<RMAX, NARROW, NB>(i, kb, f >> 1, f & 1));
             const bool second = f >= 2;
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
@@ -399,37 +410,40 @@ struct Expand {
   }
 };
 
-template <int MT, bool NARROW, int NB>
+template <int RMAX, int MT, bool NARROW, int NB>
 __device__ __forceinline__ void tile_of(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
                                         float* copies, uint8_t* ring) {
   const uint16_t *a = p.ad.a + (int64_t)tile.x * p.ad.max_rank * p.ad.in, *b = p.ad.b + (int64_t)tile.x * p.ad.out * p.ad.max_rank;
   uint32_t* h = reinterpret_cast<uint32_t*>(NB == 4 ? ring : reinterpret_cast<uint8_t*>(copies) + kCopyBytes / 2);
-  Expand<MT, NARROW, NB> second(p, b, rank, tile.z, tokens, ring, o0, o1);
+  Expand<RMAX, MT, NARROW, NB> second(p, b, rank, tile.z, tokens, ring, o0, o1);
   if (MT == 1) second.start();
-  shrink<MT, NARROW, NB>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), ring, copies);
+  shrink<RMAX, MT, NARROW, NB>(p, a, rank, tile.z, tokens, (int)tc::cluster_ctarank(), ring, copies);
   if (MT > 1) second.start();  // the ring is free
   cluster_arrive();
   cluster_wait();
-  gather<MT, NARROW, NB>(copies, h);
+  gather<RMAX, MT, NARROW, NB>(copies, h);
   cluster_arrive();  // this block has read the others' sums
   __syncthreads();
   second.run(h, scale);
   cluster_wait();
 }
-template <int MT>
+template <int RMAX, int MT>
 __device__ __forceinline__ void tile_by_rank(const AddParams& p, const int4& tile, int rank, float scale, const int* tokens, int o0, int o1,
                                              float* copies, uint8_t* ring) {
-  if (rank <= 16) tile_of<MT, true, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
-  else if (rank <= 32) tile_of<MT, false, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
-  else if (rank <= 64) tile_of<MT, false, 2>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
-  else tile_of<MT, false, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  if (rank <= 16) return tile_of<RMAX, MT, true, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  if constexpr (RMAX > 16)
+    if (rank <= 32) return tile_of<RMAX, MT, false, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  if constexpr (RMAX > 32)
+    if (rank <= 64) return tile_of<RMAX, MT, false, 2>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+  if constexpr (RMAX > 64) tile_of<RMAX, MT, false, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) add_kernel(const __grid_constant__ AddParams p) {
+template <int RMAX>
+__global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const __grid_constant__ AddParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   float* copies = reinterpret_cast<float*>(raw);
   uint8_t* ring = raw + kCopyBytes;
-  int* tokens = reinterpret_cast<int*>(raw + kCopyBytes + kRing);
+  int* tokens = reinterpret_cast<int*>(raw + kCopyBytes + Size<RMAX>::Ring);
   pdl_enter();
   const int4 head = __ldcg(static_cast<const int4*>(p.plan));
   const int tiles = p.out == p.y ? head.y : head.x;  // in place there is nothing to do for tokens without an adapter
@@ -460,24 +474,25 @@ __global__ void __launch_bounds__(kThreads, 2) add_kernel(const __grid_constant_
       continue;
     }
     const float scale = p.ad.scales ? __ldg(p.ad.scales + tile.x) : 1.f;
-    if (tile.z <= 16) tile_by_rank<1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
-    else tile_by_rank<4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+    if (tile.z <= 16) tile_by_rank<RMAX, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+    else tile_by_rank<RMAX, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
   }
 }
 
 }  // namespace
 
-// Clusters that the device runs at once.
-int adapter_clusters() {
+namespace {
+
+template <int RMAX>
+int clusters_of(int dev) {
   static PerDevice<int> of;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   return of.get(dev, [] {
-    if (cudaFuncSetAttribute(add_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return 0;
+    const auto kern = add_kernel<RMAX>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Size<RMAX>::Smem) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = Size<RMAX>::Smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCluster;
@@ -485,23 +500,23 @@ int adapter_clusters() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, add_kernel, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
     return n;
   }, 0);
 }
 
-cudaError_t launch_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, int64_t y_stride, uint16_t* out,
-                               int64_t out_stride, const trellis_adapters_t& ad, const void* plan, int batch, int n,
-                               cudaStream_t st) {
-  const int fit = adapter_clusters();
+template <int RMAX>
+cudaError_t launch_rank(const AddParams& p, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  const int fit = clusters_of<RMAX>(dev);
   if (fit < 1) return cudaErrorInvalidConfiguration;
   // no more clusters than there can be shares of tiles
-  const int64_t shares = (ad.out + 31) / 32 / (kCluster * kWarps), most = adapter_max_tiles(batch, n) * (shares < 1 ? 1 : shares);
-  const AddParams p{x, y, out, x_stride, y_stride, out_stride, ad, plan, batch, n};
+  const int64_t shares = (p.ad.out + 31) / 32 / (kCluster * kWarps), most = adapter_max_tiles(p.batch, p.n) * (shares < 1 ? 1 : shares);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(most < fit ? most : fit) * kCluster);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Size<RMAX>::Smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -511,7 +526,23 @@ cudaError_t launch_adapter_add(const uint16_t* x, int64_t x_stride, const uint16
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, add_kernel, p);
+  return cudaLaunchKernelEx(&cfg, add_kernel<RMAX>, p);
+}
+
+}  // namespace
+
+// Clusters that the device runs at once, where two blocks share an SM; half as many where one has it.
+int adapter_clusters() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? clusters_of<16>(dev) : 0;
+}
+
+cudaError_t launch_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, int64_t y_stride, uint16_t* out,
+                               int64_t out_stride, const trellis_adapters_t& ad, const void* plan, int batch, int n,
+                               cudaStream_t st) {
+  const AddParams p{x, y, out, x_stride, y_stride, out_stride, ad, plan, batch, n};
+  return ad.max_rank <= 16 ? launch_rank<16>(p, st) : ad.max_rank <= 32 ? launch_rank<32>(p, st)
+       : ad.max_rank <= 64 ? launch_rank<64>(p, st) : launch_rank<128>(p, st);
 }
 
 }  // namespace trellis
