@@ -96,7 +96,6 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
                                        uint8_t* rings, float* copies) {
   using H = Share<MT, NB>;
   constexpr int kWarpRing = Size<RMAX>::WarpRing;
-  constexpr bool kRoom = RMAX > 32;  // for registers
   constexpr int WT = H::Tokens / 16, NT = NARROW ? 2 : H::Ranks / 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int side = warp % H::Sides, group = warp / H::Sides % H::Groups, split = warp / H::Sides / H::Groups;
@@ -130,7 +129,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
       }
   };
   if (MT > 1) {
-    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage < 8 ? kWarpRing / kStage : 8;
+    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage < 4 ? kWarpRing / kStage : 4;
     uint8_t* ring = rings + warp * kWarpRing;
     const auto copy = [&](int k, int s) {
       if (k < k1 && 32 * k + 8 * q < p.ad.in)
@@ -147,7 +146,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
 #pragma unroll 1
     for (; k < k1; k += H::Splits) {
       uint4 next[NT], u[2 * WT];
-      if (NT <= 4 || kRoom) load_a(k + H::Splits, next);
+      if (NT <= 4) load_a(k + H::Splits, next);
       cp_async_wait<kStages - 1>();
       const bool in = 32 * k + 8 * q < p.ad.in;
 #pragma unroll
@@ -158,7 +157,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
       copy(k + kStages * H::Splits, stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
       multiply(u, v);
-      if (NT <= 4 || kRoom) {
+      if (NT <= 4) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] = next[j];
       } else {
@@ -167,7 +166,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
     }
     cp_async_wait<0>();
   } else {
-    constexpr int kAhead = kRoom ? 6 : 3;  // blocks whose loads are in flight
+    constexpr int kAhead = 3;  // blocks whose loads are in flight
     for (int k = k0 + split; k < k1; k += H::Splits * kAhead) {
       uint4 u[kAhead][2 * WT], v[kAhead][NT];
 #pragma unroll
@@ -261,7 +260,6 @@ __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
 template <int RMAX, int MT, bool NARROW, int NB>
 struct Expand {
   static constexpr int kWarpRing = Size<RMAX>::WarpRing, kWideRing = Size<RMAX>::WideRing;
-  static constexpr bool kRoom = RMAX > 32;  // for registers
   static constexpr bool kRingB = MT == 1 && NB <= 2;  // B goes through the ring too, else it is loaded one block ahead
   static constexpr int kY = 2 * MT * 512, kB = kRingB ? 4 * NB * (NARROW ? 256 : 512) : 0, kStage = kY + kB;
   static constexpr int kFit = (NB == 4 ? kWideRing : kWarpRing) / kStage, kStages = kFit < 4 ? kFit : 4;
@@ -333,7 +331,7 @@ struct Expand {
     const uint32_t* hl = h + 4 * lane;
     const bool ragged = rank % (NARROW ? 4 : 8) != 0;
     uint4 v[4][NB], next[4][NB];
-    if constexpr (!kRingB && (NB < 4 || kRoom)) load(o, next);
+    if constexpr (!kRingB && NB < 4) load(o, next);
 #pragma unroll 1
     for (; o < o1; o += kWarps) {
       cp_async_wait<kStages - 1>();
@@ -356,7 +354,7 @@ struct Expand {
               v[j][kb] = *reinterpret_cast<const uint4*>(from + kY + ((j * NB + kb) * 32 + lane) * 16);
             }
           }
-      } else if constexpr (NB < 4 || kRoom) {
+      } else if constexpr (NB < 4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the group's warps meet at barriers, so they leave together
     for (int k = 0; tc::bar_and(told(k, w), group_bar, 128); ++k) {
       const int n = w.tiles;
-      const int shared_to = w.prefix + w.first + 1;  // keys that every row sees
+      const int shared_to = w.shared0;  // keys that every row sees
       for (int e = 0; e < 2 * n && !dead; ++e) {
         bool value;
         const int t = tile_at<C::Streams>(e, n, &value);
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         g.b = w.b;
         g.tile0 = w.tile0;
         TreePages<kTile> pages(p, g, lane);
-        const int shared_to = w.prefix + w.first + 1, to_values = p.hkv << p.page_shift;
+        const int shared_to = w.shared0, to_values = p.hkv << p.page_shift;
         // lane i knows where box i of a tile's keys lies; none past the end
         const auto rows_of = [&](int t) {
           int page = pages.at(t);
@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; told(k, w); ++k) {
         // Units: a tile of a stream, streams in turn; of one stream every tile.  Unit u has S number u % 2, and its outputs are followed
         // by the scores of unit u + 2.
-        const int n = uniform(w.tiles), first_tail = uniform((w.prefix + w.first + 1) / kTile - w.tile0);
-        const int n0 = uniform(prompt::tiles_of(p, w, 0, 128)), n1 = C::Streams == 2 ? uniform(prompt::tiles_of(p, w, 128, 256)) : 0;
+        const int n = uniform(w.tiles), first_tail = uniform(w.shared0 / kTile - w.tile0);
+        const int n0 = uniform(w.n0), n1 = C::Streams == 2 ? uniform(w.n1) : 0;
         const int qb = k % C::QBuffers;
         if (!wait(q_full + qb, (uint32_t)(k / C::QBuffers & 1))) break;
         const uint64_t q_at = q_desc + (uint32_t)(qb * (C::Streams * C::QTile >> 4));
@@ -586,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ch = tid % LPR, r0 = tid / LPR;
         uint8_t* to = sq + k % C::QBuffers * (C::Streams * C::QTile);
         // (token, head of the group) of row r0 + kRows i, without a division each
-        int d = tree_draft(p, w.g0 + r0), hh = w.g0 + r0 - d * p.group;
+        int d = prompt::draft(p, w.g0 + r0), hh = w.g0 + r0 - d * p.group;
         const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
-        const int dstep = tree_draft(p, kRows), hstep = kRows - dstep * p.group;
+        const int dstep = prompt::draft(p, kRows), hstep = kRows - dstep * p.group;
         const int64_t step = dstep * p.q_stride + hstep * D, wrap = p.q_stride - (int64_t)p.group * D;
         const auto next = [&] {
           hh += hstep;
@@ -688,9 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (s < C::Streams)
       for (int k = 0; told(k, w); ++k) {
         const bool valid = r < w.rows;
-        const int n = prompt::tiles_of(p, w, s * 128, s * 128 + 128);
-        const int seen = valid ? prompt::seen_by(p, w, r) : 0;
-        const int masked_from = s * 128 < w.rows ? prompt::seen_by(p, w, s * 128) : 0;  // keys that every row of the stream sees
+        const int n = s ? w.n1 : w.n0;
+        const int d = valid ? prompt::draft(p, w.g0 + r) : 0, hh = w.g0 + r - d * p.group;
+        const int seen = valid ? w.prefix + w.first + d + 1 : 0;
+        const int masked_from = s ? w.shared1 : w.shared0;  // keys that every row of the stream sees
         float c = score_factor(fabsf(p.scale_log2 * (p.scales ? __ldg(p.scales + w.head) : 1.f)));
         const uint32_t t_o = tmem + C::O(s) + lanes;
         float m = -INFINITY, l = 0.f;  // the maximum in use, the sum
@@ -798,7 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool whole = w.tile0 == 0 && w.tiles == w.last + 1;
         const bool odd = odd_of[k % kOdd] == k;
-        const int d = valid ? tree_draft(p, w.g0 + r) : 0, hh = w.g0 + r - d * p.group;
         const int64_t token = w.start + w.first + d;
         const int head = w.head * p.group + hh;
         const auto fetch = [&](int col, float (&v)[32]) {  // 32 columns of the row
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(y[q]);
           if (odd && valid)
-            for (int pos = max(w.prefix + w.first + 1, w.tile0 * kTile); pos < min(seen, (w.tile0 + w.tiles) * kTile); ++pos) {
+            for (int pos = max(w.shared0, w.tile0 * kTile); pos < min(seen, (w.tile0 + w.tiles) * kTile); ++pos) {
               int page = p.table[(int64_t)w.b * p.width + (pos >> p.page_shift)];
               page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
               const int64_t at = ((((int64_t)page * 2 + 1) * p.hkv + w.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
@@ -832,13 +832,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 32 columns at a time through shared memory, so that 64 bytes of a row are stored by four lanes together (a row per lane:
           // four times as many accesses, the end of an item took 4000 cycles)
           uint8_t* stage = stages + (warp - kSoftmaxWarp) * C::Stage;
+          // rows (lane / 4) + 8 i of the warp's 32
           uint16_t* out[4];
-          bool has[4];
+          const int q0 = (warp & 3) * 32 + s * 128 + (lane >> 2);
+          int dq = prompt::draft(p, w.g0 + q0), hq = w.g0 + q0 - dq * p.group;
+          out[0] = p.out + (int64_t)(w.start + w.first + dq) * p.out_stride + (int64_t)(w.head * p.group + hq) * D + 8 * (lane & 3);
+          const int dstep = prompt::draft(p, 8), hstep = 8 - dstep * p.group;
+          const int64_t step = dstep * p.out_stride + hstep * D, wrap = p.out_stride - (int64_t)p.group * D;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int q = (warp & 3) * 32 + s * 128 + 8 * i + (lane >> 2), dq = tree_draft(p, w.g0 + q), hq = w.g0 + q - dq * p.group;
-            has[i] = q < w.rows;
-            out[i] = p.out + (int64_t)(w.start + w.first + dq) * p.out_stride + (int64_t)(w.head * p.group + hq) * D + 8 * (lane & 3);
+          for (int i = 1; i < 4; ++i) {
+            hq += hstep;
+            out[i] = out[i - 1] + step;
+            if (hq >= p.group) {
+              hq -= p.group;
+              out[i] += wrap;
+            }
           }
 #pragma unroll 1
           for (int col = 0; col < D; col += 32) {
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int q = 8 * i + (lane >> 2);
-              if (has[i]) *reinterpret_cast<uint4*>(out[i] + col) = *reinterpret_cast<const uint4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
+              if (q0 + 8 * i < w.rows) *reinterpret_cast<uint4*>(out[i] + col) = *reinterpret_cast<const uint4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
             }
           }
           if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::template Lift<F8>));

@@ -40,11 +40,14 @@ struct Work {
   int prefix, len;       // the sequence's
   int tile0, tiles, last;  // of the item's tiles 0 .. last these
   int until;             // the item's last thread block, where it is split
+  int n0, n1;            // tiles that rows 0 .. 127, and 128 .. 255, take part in
+  int shared0, shared1;  // keys that all of these rows see
   int more;              // 0: nothing is left
 };
 
 // Rows 0 .. r of a block: the last one's token, and the keys that it sees.
-__device__ __forceinline__ int token_of(const TreeParams& p, const Work& w, int r) { return w.first + tree_draft(p, w.g0 + r); }
+__device__ __forceinline__ int draft(const TreeParams& p, int x) { return p.group == 1 ? x : (int)__umulhi((uint32_t)x, (uint32_t)p.group_inv); }  // x / group
+__device__ __forceinline__ int token_of(const TreeParams& p, const Work& w, int r) { return w.first + draft(p, w.g0 + r); }
 __device__ __forceinline__ int seen_by(const TreeParams& p, const Work& w, int r) { return w.prefix + token_of(p, w, r) + 1; }
 // Tiles of the stretch that rows r0 .. r1 - 1 (of a stream) take part in.
 __device__ __forceinline__ int tiles_of(const TreeParams& p, const Work& w, int r0, int r1) {
@@ -144,6 +147,15 @@ __device__ void plan(const TreeParams& p, Map& m, int grid, int* keys) {
   __syncthreads();
 }
 
+// Fills in what follows from the stretch.
+template <int ROWS>
+__device__ __forceinline__ void finish(const TreeParams& p, Work& w) {
+  w.n0 = tiles_of(p, w, 0, 128);
+  w.n1 = ROWS > 128 ? tiles_of(p, w, 128, 256) : 0;
+  w.shared0 = seen_by(p, w, 0);
+  w.shared1 = w.rows > 128 ? seen_by(p, w, 128) : 0;
+}
+
 // Fills the rest of a work from its sequence and block of rows.
 template <int ROWS>
 __device__ __forceinline__ void describe(const TreeParams& p, Work& w, const TreeSeq& s, int rb) {
@@ -175,6 +187,7 @@ __device__ __forceinline__ Work whole_item(const TreeParams& p, const Map& m, in
   describe<ROWS>(p, w, tree_seq(p, w.b), m.cum[lo + 1] - 1 - block);  // from the last block to the first
   w.tile0 = 0;
   w.tiles = w.last + 1;
+  finish<ROWS>(p, w);
   return w;
 }
 
@@ -204,7 +217,10 @@ __device__ __forceinline__ Work next_stretch(const TreeParams& p, const Map& m, 
     w.tiles = max(stop - kExtra, 0) - w.tile0;
     w.until = tree_cta_of(at - off + length - 1, m.total, m.ctas);
     at += stop - off;
-    if (w.tiles > 0) return w;
+    if (w.tiles > 0) {
+      finish<ROWS>(p, w);
+      return w;
+    }
   }
   return Work{};
 }
