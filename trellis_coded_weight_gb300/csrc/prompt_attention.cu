@@ -715,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < kTile; j += 32) {
               const int bits = upto - j;
+              if (__all_sync(0xFFFFFFFFu, bits >= 32)) continue;
               const uint32_t keep = bits >= 32 ? 0xFFFFFFFFu : bits > 0 ? (1u << bits) - 1 : 0u;
               uint32_t y[32];
               tc::tmem_ld_32x32b_x32(t_s + j, y);
@@ -852,12 +853,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int col = 0; col < D; col += 32) {
             float v[32];
             fetch(col, v);
+            uint32_t e[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float2 y = __fmul2_rn(make_float2(v[2 * q], v[2 * q + 1]), make_float2(f, f));
+              e[q] = pack_bf16x2(y.x, y.y);
+            }
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
-                  make_uint4(pack_bf16x2(v[8 * q] * f, v[8 * q + 1] * f), pack_bf16x2(v[8 * q + 2] * f, v[8 * q + 3] * f),
-                             pack_bf16x2(v[8 * q + 4] * f, v[8 * q + 5] * f), pack_bf16x2(v[8 * q + 6] * f, v[8 * q + 7] * f));
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = make_uint4(e[4 * q], e[4 * q + 1], e[4 * q + 2], e[4 * q + 3]);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

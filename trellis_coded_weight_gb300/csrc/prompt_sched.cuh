@@ -19,18 +19,26 @@ namespace prompt {
 
 constexpr int kTile = 128;     // keys of a step
 constexpr int kExtra = 2;      // an item's start and end, in steps
-constexpr int kJoin = 6;       // what parts and their joining cost, in steps
+constexpr int kJoin = 12;      // what parts and their joining cost, in steps
 constexpr int kLeast = 4;      // steps of a range at the least
 constexpr int kEntries = 512;  // blocks of rows (of all sequences) that can be split
 constexpr int kMaxSeqs = kTreeMaxBatch;
 
 struct Map {
+  static constexpr int kCached = 256;
+  int4 seq[kCached];            // the first sequences: start, count, prefix
   int cum[kMaxSeqs + 1];        // blocks of rows before the i-th sequence of the order
   uint16_t order[kMaxSeqs];     // sequences by falling length
   int cost[kEntries + 1];       // split: steps before entry e (of all heads)
   int entries, items, total, ctas;
   bool split;
 };
+
+__device__ __forceinline__ TreeSeq seq_of(const TreeParams& p, const Map& m, int b) {
+  if (b >= Map::kCached) return tree_seq(p, b);
+  const int4 v = m.seq[b];
+  return TreeSeq{v.x, v.y, v.z};
+}
 
 // What a thread block does next: a stretch of one item's steps.
 struct Work {
@@ -58,13 +66,12 @@ __device__ __forceinline__ int tiles_of(const TreeParams& p, const Work& w, int 
 }
 
 template <int ROWS>
-__device__ __forceinline__ int blocks_of(const TreeParams& p, const TreeSeq& s) { return (int)(((int64_t)s.count * p.group + ROWS - 1) / ROWS); }
+__device__ __forceinline__ int blocks_of(const TreeParams& p, const TreeSeq& s) { return (s.count * p.group + ROWS - 1) / ROWS; }  // at most 2^30 rows
 // Tiles of block rb of a sequence.
 template <int ROWS>
 __device__ __forceinline__ int item_tiles(const TreeParams& p, const TreeSeq& s, int rb) {
-  const int64_t z = ((int64_t)rb + 1) * ROWS, all = (int64_t)s.count * p.group;
-  const int last = (int)(((z < all ? z : all) - 1) / p.group);
-  return (s.prefix + last) / kTile + 1;
+  const uint32_t z = (uint32_t)(rb + 1) * ROWS, all = (uint32_t)(s.count * p.group);
+  return (s.prefix + (int)(((z < all ? z : all) - 1) / (uint32_t)p.group)) / kTile + 1;
 }
 
 // Fills the map; by all threads of the block.
@@ -75,6 +82,7 @@ __device__ void plan(const TreeParams& p, Map& m, int grid, int* keys) {
   for (int b = tid; b < kMaxSeqs; b += threads) {
     const TreeSeq s = b < n ? tree_seq(p, b) : TreeSeq{0, 0, 0};
     keys[b] = s.count ? s.prefix + s.count : 0;
+    if (b < Map::kCached) m.seq[b] = make_int4(s.start, s.count, s.prefix, 0);
   }
   __syncthreads();
   for (int b = tid; b < n; b += threads) {
@@ -92,7 +100,7 @@ __device__ void plan(const TreeParams& p, Map& m, int grid, int* keys) {
     int before = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
       int v = 0;
-      if (i0 + lane < n) v = blocks_of<ROWS>(p, tree_seq(p, m.order[i0 + lane]));
+      if (i0 + lane < n) v = blocks_of<ROWS>(p, seq_of(p, m, m.order[i0 + lane]));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -122,7 +130,7 @@ __device__ void plan(const TreeParams& p, Map& m, int grid, int* keys) {
             if (m.cum[mid] <= e0 + lane) lo = mid;
             else hi = mid;
           }
-          v = item_tiles<ROWS>(p, tree_seq(p, m.order[lo]), e0 + lane - m.cum[lo]) + kExtra;
+          v = item_tiles<ROWS>(p, seq_of(p, m, m.order[lo]), e0 + lane - m.cum[lo]) + kExtra;
         }
         most = max(most, __reduce_max_sync(0xFFFFFFFFu, v));
         far = far || (int64_t)sum + (int64_t)most * 32 * p.hkv > (1 << 30);
@@ -159,11 +167,11 @@ __device__ __forceinline__ void finish(const TreeParams& p, Work& w) {
 // Fills the rest of a work from its sequence and block of rows.
 template <int ROWS>
 __device__ __forceinline__ void describe(const TreeParams& p, Work& w, const TreeSeq& s, int rb) {
-  const int64_t row0 = (int64_t)rb * ROWS, rows = (int64_t)s.count * p.group - row0;
+  const int row0 = rb * ROWS, rows = s.count * p.group - row0;
   w.start = s.start;
-  w.first = (int)(row0 / p.group);
-  w.g0 = (int)(row0 - (int64_t)w.first * p.group);
-  w.rows = rows < ROWS ? (int)rows : ROWS;
+  w.first = (int)((uint32_t)row0 / (uint32_t)p.group);
+  w.g0 = row0 - w.first * p.group;
+  w.rows = rows < ROWS ? rows : ROWS;
   w.prefix = s.prefix;
   w.len = s.prefix + s.count;
   w.last = item_tiles<ROWS>(p, s, rb) - 1;
@@ -184,7 +192,7 @@ __device__ __forceinline__ Work whole_item(const TreeParams& p, const Map& m, in
     else hi = mid;
   }
   w.b = m.order[lo];
-  describe<ROWS>(p, w, tree_seq(p, w.b), m.cum[lo + 1] - 1 - block);  // from the last block to the first
+  describe<ROWS>(p, w, seq_of(p, m, w.b), m.cum[lo + 1] - 1 - block);  // from the last block to the first
   w.tile0 = 0;
   w.tiles = w.last + 1;
   finish<ROWS>(p, w);
@@ -212,7 +220,7 @@ __device__ __forceinline__ Work next_stretch(const TreeParams& p, const Map& m, 
       else z = mid;
     }
     w.b = m.order[s];
-    describe<ROWS>(p, w, tree_seq(p, w.b), lo - m.cum[s]);
+    describe<ROWS>(p, w, seq_of(p, m, w.b), lo - m.cum[s]);
     w.tile0 = max(off - kExtra, 0);
     w.tiles = max(stop - kExtra, 0) - w.tile0;
     w.until = tree_cta_of(at - off + length - 1, m.total, m.ctas);
