@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           w = prompt::next_stretch<C::Rows>(p, plan, at, end);
         } else {
           if (k > 0) {
-            if (lane == 0) item = (int)gridDim.x + atomicAdd(p.counter, 1);
+            if (lane == 0) item = (int)gridDim.x + (p.counter ? atomicAdd(p.counter, 1) : item);
             item = __shfl_sync(0xFFFFFFFFu, item, 0);
           }
           w = prompt::whole_item<C::Rows>(p, plan, item);
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool F8>
-cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cudaStream_t st) {
+cudaError_t launch_d(const CUtensorMap& map, TreeParams p, int ctas, cudaStream_t st) {
   auto kern = prompt_kernel<D, F8>;
   static PerDevice<cudaError_t> attr_of;
   int dev = 0;
@@ -912,7 +912,14 @@ cudaError_t launch_d(const CUtensorMap& map, const TreeParams& p, int ctas, cuda
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::Smem);
   }, cudaErrorInvalidDevice);
   if (e != cudaSuccess) return e;
+  // Where there is at most an item for each block and none is longer than its parts and their joining would cost, none is split and
+  // nobody asks for a second one: no joining kernel, then (100 tokens: 12.3 us with it).
+  const int64_t items = (int64_t)p.hkv * ((int64_t)p.n * p.group / Cfg<D>::Rows + p.batch);
+  const int64_t most = (((int64_t)p.width << p.page_shift) + kTile - 1) / kTile + prompt::kExtra;
+  const bool alone = items <= ctas && most <= prompt::kJoin;
+  if (alone) p.counter = nullptr;
   const cudaError_t e2 = launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), Cfg<D>::Smem, st, map, p);
+  if (alone) return e2;
   return e2 != cudaSuccess ? e2 : launch_tree_join(p, D, Cfg<D>::Rows, Cfg<D>::template Lift<F8>, ctas, st);
 }
 
