@@ -276,3 +276,32 @@ def test_refusals_of_the_binding():
         tb.AdapterPlan(i32([0]), i32([0, 1, 2]), 2)
     with pytest.raises(ValueError):
         tb.AdapterPlan(i32([0] * 1025), i32([0] * 1026), 2)
+
+
+def test_counts_of_zero():
+    s = Step([4, 3], [0, 1], [8, 8], 8, 256, 512)
+    s.run()
+    none = tb.adapter_plan(tb.AdapterPlan(i32([]), i32([0]), 0))
+    assert tb.adapter_add(s.x[:0], s.y[:0], s.adapters, none).numel() == 0
+    empty = tb.adapter_plan(tb.AdapterPlan(i32([0, 1]), i32([0, 0, 0]), 7))
+    s.out.fill_(7.5)
+    assert bool((tb.adapter_add(s.x, s.y, s.adapters, empty, out=s.out) == 7.5).all())
+
+
+def test_a_plan_not_made_yet_does_nothing():
+    s = Step([4, 3], [0, 1], [8, 8], 8, 256, 512)
+    s.run()
+    s.out.fill_(7.5)
+    fresh = tb.AdapterPlan(i32([0, 1]), i32([0, 4, 7]), 7)
+    assert bool((tb.adapter_add(s.x, s.y, s.adapters, fresh, out=s.out) == 7.5).all())
+
+
+@pytest.mark.parametrize("rank,count", [(16, 90), (40, 90), (16, 300), (128, 50)])
+def test_rounds_of_many_adapters(rank, count):
+    """More tiles than clusters: whole rounds and a last one that clusters share."""
+    rng = np.random.default_rng(count)
+    toks = rng.integers(1, 40, count).tolist()
+    s = Step(toks, list(range(count)), [int(r) for r in rng.integers(1, rank + 1, count)], rank, 264, 2056, seed=count)
+    first = s.run().clone()
+    s.check(first)
+    assert torch.equal(s.run(), first)

@@ -392,3 +392,103 @@ def test_refusals_of_the_binding():
             tb.prompt_attention(**{**ok, **bad})
     with pytest.raises(tb.TrellisError):  # three heads over two
         tb.prompt_attention(p.q[:, :3].contiguous(), p.cache, 0, p.batch, p.ws)
+
+
+@pytest.mark.parametrize("f8,d", [(False, 128), (True, 128), (False, 256), (True, 256), (False, 64), (True, 64)])
+def test_bounded_waits_run_out_and_the_next_call_is_right(f8, d):
+    p = Prompts([30000, 0], [300, 700], 16, 8, d, 64, f8, seed=21)
+    want = [t.clone() for t in p.run()]
+    assert tb.device_error(reset=True) == 0
+    tb.set_wait_limit(200)
+    try:
+        p.run(p.ws)
+        torch.cuda.synchronize()
+        assert tb.device_error(reset=True) != 0
+    finally:
+        tb.set_wait_limit(0)
+    got = p.run(p.ws)
+    assert tb.device_error(reset=True) == 0 and all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8", [(32, 8, 128, False), (7, 1, 64, False), (16, 2, 256, True), (40, 8, 128, True), (16, 2, 64, True), (6, 6, 256, False)])
+def test_many_items_per_block_in_repeated_calls(hq, hkv, d, f8):
+    """Rings of tiles and queries that go through many items, of one and of two streams' rows."""
+    rng = np.random.default_rng(d + hq)
+    lens = [int(x) for x in rng.integers(0, 700, 120)]
+    toks = [int(x) for x in rng.integers(1, 300, 120)]
+    p = Prompts(lens, toks, hq, hkv, d, 64, f8, seed=22)
+    first = [t.clone() for t in p.run()]
+    p.check(*first, sequences=range(0, 120, 7))
+    for _ in range(20):
+        got = p.run(p.ws)
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    assert tb.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_over_an_e4m3_cache_of_the_whole_range(d):
+    """Rows of very different sizes in one block; keys are small enough for scores of a few units at the most."""
+    p = Prompts([40], [200], 4, 2, d, 16, True, seed=23, scale=1.0)
+    size = torch.exp2(torch.randint(-100, 60, (200, 4, 1), device="cuda").float())
+    p.q.copy_((p.q.float() * size).bfloat16())
+    p.scales[:, 0] = 2.0 ** -65
+    out, lse = p.run()
+    p.check(out, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_channel_far_above_the_others_over_an_e4m3_cache(d):
+    """A query's numbers below 2^-13 of its row's largest are rounded to within 2^-21 of the largest, so a score is off by at most
+    2^-21 max|q| sum|k| besides the rest: e in the exponent, and twice e A on the outputs."""
+    p = Prompts([40], [200], 4, 2, d, 16, True, seed=23)
+    p.q[:, :, 3] *= 2.0 ** 16
+    p.pool.view(torch.uint8)[0, :, 0, :, :, 3] = 0  # keys do not see it
+    out, lse = p.run()
+    kv = p.keys_values(0)
+    for h in range(4):
+        q, k, v = p.q[:, h].double(), kv[0, h // 2], kv[1, h // 2]
+        unseen = torch.arange(240, device="cuda")[None] > 40 + torch.arange(200, device="cuda")[:, None]
+        x = (q @ k.T * p.scale).masked_fill(unseen, -torch.inf)
+        lw = torch.logsumexp(x, 1)
+        w = torch.exp(x - lw[:, None])
+        size = (q.abs() @ k.abs().T).masked_fill(unseen, 0).amax(1) * p.scale
+        e = 2.0 ** -21 * q.abs().amax(1) * k.abs().sum(1).amax() * p.scale
+        tol = 1.1 * (2.0 ** -8 * (w @ v).abs() + (2.0 ** -8 + 2.0 ** -17 * size + 2 * e)[:, None] * (w @ v.abs())) + 1e-30
+        assert bool(((out[:, h].double() - w @ v).abs() <= tol).all())
+        assert bool(((lse[:, h].double() - lw).abs() <= 2.0 ** -18 * size + e + 1e-5).all())
+
+
+def test_one_workspace_in_two_graphs():
+    """Two graphs that share a workspace, replayed one after the other in both orders."""
+    a, b = Prompts([5, 9000], [300, 100], 8, 2, 128, 64, seed=24), Prompts([0] * 3, [700, 65, 900], 8, 2, 128, 64, seed=25)
+    want = [x.clone() for x in (*a.run(), *b.run())]
+    graphs = []
+    for p in (a, b):
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            p.run(a.ws)
+        torch.cuda.current_stream().wait_stream(st)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tb.prompt_attention(p.q, p.cache, p.layer, p.batch, a.ws, p.scale, out=p.out, lse=p.lse)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (1, 1), (0, 0)):
+        for x in (a.out, a.lse, b.out, b.lse):
+            x.fill_(1)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in order:
+            assert torch.equal((a, b)[i].out, want[2 * i]) and torch.equal((a, b)[i].lse, want[2 * i + 1])
+
+
+def test_counts_of_zero():
+    p = Prompts([0], [70], 4, 2, 64, 16)
+    p.run()
+    none = tb.DraftBatch(p.batch.table[:0], p.batch.prefix[:0], p.batch.q_start[:1].contiguous(), 70, None, 0)
+    assert tb.prompt_attention(p.q[:0], p.cache, 0, none, p.ws)[0].numel() == 0
+    nothing = tb.DraftBatch(p.batch.table, p.batch.prefix, torch.zeros_like(p.batch.q_start), 70, None, 70)
+    out, lse = p.out.fill_(7.5), p.lse.fill_(7.5)
+    tb.prompt_attention(p.q, p.cache, 0, nothing, p.ws, out=out, lse=lse)
+    assert bool((out == 7.5).all()) and bool((lse == 7.5).all())
