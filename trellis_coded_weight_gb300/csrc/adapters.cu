@@ -90,7 +90,8 @@ struct Share {
 };
 
 // h of the block's part of the inputs, for 16 MT tokens.  Where tokens are many, a lane copies what it needs of x into its warp's ring,
-// some blocks of 32 inputs ahead (x comes from HBM; loads into registers kept half as many bytes in flight); A is loaded one block ahead.
+// some blocks of 32 inputs ahead (x comes from HBM; loads into registers kept half as many bytes in flight), and of A above 32 ranks;
+// else A is loaded one block ahead.
 template <int RMAX, int MT, bool NARROW, int NB>
 __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, int rank, int count, const int* tokens, int rank_of_block,
                                        uint8_t* rings, float* copies) {
@@ -129,24 +130,29 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
       }
   };
   if (MT > 1) {
-    constexpr int kStage = 2 * WT * 512, kStages = kWarpRing / kStage < 4 ? kWarpRing / kStage : 4;
+    constexpr bool kRingA = NT == 8;  // two sets of so many numbers of A do not fit in registers
+    constexpr int kX = 2 * WT * 512, kStage = kX + (kRingA ? NT * 512 : 0), kStages = kWarpRing / kStage < 4 ? kWarpRing / kStage : 4;
     uint8_t* ring = rings + warp * kWarpRing;
     const auto copy = [&](int k, int s) {
       if (k < k1 && 32 * k + 8 * q < p.ad.in)
 #pragma unroll
         for (int i = 0; i < 2 * WT; ++i)
           if (t0 + 8 * i + g < count) cp_async16(ring + s * kStage + (i * 32 + lane) * 16, row_of(i) + 32 * k);
+      if (kRingA && k < k1 && 32 * k + 8 * q < p.ad.in)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (r0 + 8 * j + g < rank) cp_async16(ring + s * kStage + kX + (j * 32 + lane) * 16, w + (int64_t)(8 * j) * p.ad.in + 32 * k);
       cp_async_commit();
     };
     int k = k0 + split, stage = 0;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) copy(k + s * H::Splits, s);
     uint4 v[NT];
-    load_a(k, v);
+    if (!kRingA) load_a(k, v);
 #pragma unroll 1
     for (; k < k1; k += H::Splits) {
       uint4 next[NT], u[2 * WT];
-      if (NT <= 4) load_a(k + H::Splits, next);
+      if (!kRingA) load_a(k + H::Splits, next);
       cp_async_wait<kStages - 1>();
       const bool in = 32 * k + 8 * q < p.ad.in;
 #pragma unroll
@@ -154,15 +160,18 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
         u[i] = *reinterpret_cast<const uint4*>(ring + stage * kStage + (i * 32 + lane) * 16);
         if (!in || t0 + 8 * i + g >= count) u[i] = make_uint4(0, 0, 0, 0);
       }
+      if (kRingA)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          v[j] = *reinterpret_cast<const uint4*>(ring + stage * kStage + kX + (j * 32 + lane) * 16);
+          if (!in || r0 + 8 * j + g >= rank) v[j] = make_uint4(0, 0, 0, 0);
+        }
       copy(k + kStages * H::Splits, stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
       multiply(u, v);
-      if (NT <= 4) {
+      if (!kRingA)
 #pragma unroll
         for (int j = 0; j < NT; ++j) v[j] = next[j];
-      } else {
-        load_a(k + H::Splits, v);
-      }
     }
     cp_async_wait<0>();
   } else {
