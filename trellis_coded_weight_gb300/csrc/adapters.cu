@@ -445,6 +445,26 @@ __device__ __forceinline__ void tile_by_rank(const AddParams& p, const int4& til
   if constexpr (RMAX > 64) tile_of<RMAX, MT, false, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
 }
 
+__device__ __forceinline__ int rank_of(const AddParams& p, int adapter) {
+  const bool has = adapter >= 0 && adapter < p.ad.count;
+  const int rank = has ? p.ad.ranks ? __ldg(p.ad.ranks + adapter) : p.ad.max_rank : 0;
+  return rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
+}
+
+// The tiles by falling rank, where there are more of them than clusters: each cluster then takes one from the front of a round and
+// one from the back of the next.
+constexpr int kSorted = kThreads;
+__device__ __noinline__ void sort_tiles(const AddParams& p, int tiles, int* ranks, uint16_t* order) {
+  const int t = threadIdx.x;
+  ranks[t] = t < tiles ? rank_of(p, __ldcg(adapter_tiles(p.plan) + t).x) : -1;
+  __syncthreads();
+  const int mine = ranks[t];
+  int place = 0;
+  for (int i = 0; i < tiles; ++i) place += ranks[i] > mine || (ranks[i] == mine && i < t);
+  if (t < tiles) order[place] = (uint16_t)t;
+  __syncthreads();
+}
+
 template <int RMAX>
 __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const __grid_constant__ AddParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -457,17 +477,21 @@ __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const
   const int32_t* order = adapter_order(p.plan, p.batch, p.n);
   const int cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster, rank_of_block = (int)tc::cluster_ctarank();
   const int blocks = (int)((p.ad.out + 31) / 32);
-  for (int t0 = 0; t0 < tiles; t0 += clusters) {
+  constexpr bool kSort = RMAX > 32;  // below that tiles cost about the same
+  __shared__ uint16_t order_of[kSort ? kSorted : 1];
+  const bool sorted = kSort && p.ad.ranks && tiles > clusters && tiles <= kSorted;
+  if (kSort && sorted) sort_tiles(p, tiles, reinterpret_cast<int*>(raw), order_of);
+  bool back = false;
+  for (int t0 = 0; t0 < tiles; t0 += clusters, back = !back) {
     // the round's tiles; where they are few, as many clusters for each as have a block of outputs per warp
     const int now = min(tiles - t0, clusters);
     const int shares = max(1, min(clusters / now, blocks / (kCluster * kWarps)));
     if (cluster >= now * shares) break;
-    const int4 tile = __ldcg(adapter_tiles(p.plan) + t0 + cluster % now);
+    const int at = t0 + (kSort && back && now == clusters ? clusters - 1 - cluster : cluster % now);
+    const int4 tile = __ldcg(adapter_tiles(p.plan) + (kSort && sorted ? order_of[at] : at));
     const int share = (cluster / now) * kCluster + rank_of_block, all = shares * kCluster;
     const int o0 = (int)((int64_t)share * blocks / all), o1 = (int)((int64_t)(share + 1) * blocks / all);
-    const bool has = tile.x >= 0 && tile.x < p.ad.count;
-    int rank = has ? p.ad.ranks ? __ldg(p.ad.ranks + tile.x) : p.ad.max_rank : 0;
-    rank = rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
+    const int rank = rank_of(p, tile.x);
     __syncthreads();
     if (threadIdx.x < tile.z) tokens[threadIdx.x] = __ldcg(order + tile.y + threadIdx.x);
     __syncthreads();
