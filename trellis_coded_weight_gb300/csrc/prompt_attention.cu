@@ -187,6 +187,30 @@ __device__ __forceinline__ int tile_at(int place, int n, bool* value) {
   return place & 1 ? (place + 1) / 2 : (place - 2) / 2;
 }
 
+// Adds the values that were cleared since they are not finite, times f, to the numbers of a row that sees them (bf16 ones, or floats
+// four columns apart by `stride`).  Rare, and out of the way: its code would be in all rows' way else.
+template <int D, bool F8>
+__device__ __noinline__ void add_odd(const TreeParams& p, int b, int head, int from, int to, float f, uint16_t* out, float* part, int stride) {
+  for (int pos = from; pos < to; ++pos) {
+    int page = p.table[(int64_t)b * p.width + (pos >> p.page_shift)];
+    page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
+    const int64_t at = (((((int64_t)page * 2 + 1) * p.hkv + head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D;
+    for (int q = 0; q < D; ++q) {
+      float x;
+      if (F8) {
+        if ((static_cast<const uint8_t*>(p.pool)[at + q] & 0x7F) != 0x7F) continue;
+        x = __uint_as_float(0x7FFFFFFFu);
+      } else {
+        const uint16_t v = static_cast<const uint16_t*>(p.pool)[at + q];
+        if ((v & 0x7F80u) != 0x7F80u) continue;
+        x = bf16_to_f32(v);
+      }
+      if (out) out[q] = f32_to_bf16_rn(bf16_to_f32(out[q]) + x * f);
+      else part[(int64_t)(q >> 2) * stride + (q & 3)] += x;
+    }
+  }
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ TreeParams p) {
@@ -300,18 +324,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           f_phase ^= 1u << slot;
           uint8_t* tile = ring + slot * C::Slot;
           if constexpr (F8) {
-            constexpr int Chunks = C::Cols / 16, Each = Chunks;  // 16 numbers; of a row, of a thread
+            // 64 rows at a time: the first ones go below the copied numbers, the others over them, once all are in registers
+            constexpr int Chunks = C::Cols / 16, Each = Chunks / 2;  // 16 numbers; of a row, of a thread
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
             uint4 v[Each];
 #pragma unroll
             for (int i = 0; i < Each; ++i)
-              v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + C::at8((i * 128 + tid) / Chunks, (i * 128 + tid) % Chunks));
-            if (!tc::bar_and(!dead, group_bar, 128)) {  // all of it is in registers
+              v[i] = *reinterpret_cast<const uint4*>(tile + C::Slot / 2 + C::at8(half * 64 + (i * 128 + tid) / Chunks, (i * 128 + tid) % Chunks));
+            if (half == 1 && !tc::bar_and(!dead, group_bar, 128)) {
               dead = true;
               break;
             }
 #pragma unroll
             for (int i = 0; i < Each; ++i) {
-              const int c = i * 128 + tid, row = c / Chunks, ch = c % Chunks * 2;
+              const int c = i * 128 + tid, row = half * 64 + c / Chunks, ch = c % Chunks * 2;
               uint32_t o[8];
               const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
@@ -342,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(tile + C::at(row, odd_block ? ch + 1 : ch)) = odd_block ? hi : lo;
               *reinterpret_cast<uint4*>(tile + C::at(row, odd_block ? ch : ch + 1)) = odd_block ? lo : hi;
             }
+            }
+            if (dead) break;
           } else {
             if (dead) break;
             constexpr int Chunks = C::Cols / 8;
@@ -764,14 +793,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           // ---- weights, over the scores, in the type of the values they are multiplied with
           const float ms = (m == -INFINITY ? 0.f : -m) + C::template Lift<F8>;
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          constexpr int kHalves = F8 ? 1 : 2;  // e4m3: less code for more warps (chunk 557 us with 64 columns at a time, 503)
 #pragma unroll 1
-          for (int j = 0; j < kTile; j += 64) {
-            uint32_t x[2][32];
-            tc::tmem_ld_32x32b_x32(t_s + j, x[0]);
-            tc::tmem_ld_32x32b_x32(t_s + j + 32, x[1]);
+          for (int j = 0; j < kTile; j += 32 * kHalves) {
+            uint32_t x[kHalves][32];
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) tc::tmem_ld_32x32b_x32(t_s + j + 32 * h, x[h]);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < kHalves; ++h) {
               uint32_t e[16];
 #pragma unroll
               for (int q = 0; q < 32; q += 2) {
@@ -800,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool whole = w.tile0 == 0 && w.tiles == w.last + 1;
         const bool odd = odd_of[k % kOdd] == k;
+        const int odd_from = max(w.shared0, w.tile0 * kTile), odd_to = min(seen, (w.tile0 + w.tiles) * kTile);
         const int64_t token = w.start + w.first + d;
         const int head = w.head * p.group + hh;
         const auto fetch = [&](int col, float (&v)[32]) {  // 32 columns of the row
@@ -812,21 +843,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(y[q]);
-          if (odd && valid)
-            for (int pos = max(w.shared0, w.tile0 * kTile); pos < min(seen, (w.tile0 + w.tiles) * kTile); ++pos) {
-              int page = p.table[(int64_t)w.b * p.width + (pos >> p.page_shift)];
-              page = page < 0 ? 0 : page >= p.pages ? (int)p.pages - 1 : page;
-              const int64_t at = ((((int64_t)page * 2 + 1) * p.hkv + w.head << p.page_shift) + (pos & ((1 << p.page_shift) - 1))) * D + col;
-#pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                if constexpr (F8) {
-                  if ((static_cast<const uint8_t*>(p.pool)[at + q] & 0x7F) == 0x7F) v[q] = __uint_as_float(0x7FFFFFFFu);
-                } else {
-                  const uint16_t x = static_cast<const uint16_t*>(p.pool)[at + q];
-                  if ((x & 0x7F80u) == 0x7F80u) v[q] += bf16_to_f32(x);
-                }
-              }
-            }
         };
         if (whole) {
           const float vs = p.scales ? __ldg(p.scales + p.hkv + w.head) : 1.f, f = l == 0.f ? 0.f : vs / l;
@@ -870,6 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (q0 + 8 * i < w.rows) *reinterpret_cast<uint4*>(out[i] + col) = *reinterpret_cast<const uint4*>(stage + q * 64 + (((lane & 3) ^ (q >> 1 & 3)) << 4));
             }
           }
+          if (odd) {
+            __syncwarp();  // the row was stored by other lanes
+            if (valid) add_odd<D, F8>(p, w.b, w.head, odd_from, odd_to, f, p.out + token * p.out_stride + (int64_t)head * D, nullptr, 0);
+          }
           if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::template Lift<F8>));
         } else {  // a part, for the joining kernel
           float* part = p.part + (int64_t)tree_slot(cta, w.tile0 == 0) * tree_part_floats(C::Rows, D);
@@ -882,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int q = 0; q < 32; q += 4)
                 *reinterpret_cast<float4*>(part + ((int64_t)(col + q) / 4 * C::Rows + r) * 4) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
           }
+          if (odd && valid) add_odd<D, F8>(p, w.b, w.head, odd_from, odd_to, 1.f, nullptr, part + r * 4, C::Rows * 4);
           if (valid) {
             part[(int64_t)C::Rows * D + r] = m;
             part[(int64_t)C::Rows * D + C::Rows + r] = l;
