@@ -627,9 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; told(k, w); ++k) {
         const float ks = p.scales ? __ldg(p.scales + w.head) : 1.f;
         const uint32_t flip = p.scale_log2 * ks < 0.f ? 0x80008000u : 0u;  // a negative scale goes into the queries' signs
+        uint8_t* to = sq + k % C::QBuffers * (C::Streams * C::QTile);
+        const auto room = [&] { return k < C::QBuffers || wait(q_empty + k % C::QBuffers, (uint32_t)(k / C::QBuffers & 1) ^ 1u); };
+        if constexpr (!F8) {
         constexpr int LPR = D / 8, kRows = 64 / LPR;  // lanes of a row, rows at a time
         const int ch = tid % LPR, r0 = tid / LPR;
-        uint8_t* to = sq + k % C::QBuffers * (C::Streams * C::QTile);
         // (token, head of the group) of row r0 + kRows i, without a division each
         int d = prompt::draft(p, w.g0 + r0), hh = w.g0 + r0 - d * p.group;
         const uint16_t* src = p.q + (int64_t)(w.start + w.first + d) * p.q_stride + (int64_t)(w.head * p.group + hh) * D + 8 * ch;
@@ -643,8 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             src += wrap;
           }
         };
-        const auto room = [&] { return k < C::QBuffers || wait(q_empty + k % C::QBuffers, (uint32_t)(k / C::QBuffers & 1) ^ 1u); };
-        if constexpr (!F8) {
           const auto place = [&](int r) { return (r >> 7) * C::QTile + (ch >> 3) * (128 * 128) + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4); };
           if (!room()) break;
 #pragma unroll 4
@@ -659,82 +659,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint4 v = *at;
               *at = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
             }
-        } else if constexpr (D == 64) {
-          // A thread per row, all of it in registers: with lanes side by side along a row, its largest number took most of the time (8 x
-          // 2000 tokens, 64/8 heads: 542 us).
+        } else {
+          // A thread per row, 64 numbers at a time: with lanes side by side along a row, its largest number took most of the time (8 x
+          // 2000 tokens, 64/8 heads of 64: 542 us for 447).  Larger heads: the scales of all rows first, before there is room.
+          const auto row_of = [&](int r) {
+            const int dr = prompt::draft(p, w.g0 + r), hr = w.g0 + r - dr * p.group;
+            return p.q + (int64_t)(w.start + w.first + dr) * p.q_stride + (int64_t)(w.head * p.group + hr) * D;
+          };
+          const auto load = [&](const uint16_t* row, uint4 (&u)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = *reinterpret_cast<const uint4*>(row + 8 * i);
+          };
+          const auto largest = [&](const uint4 (&u)[8], uint32_t big) {  // positive bf16 patterns compare like integers, two at a time
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              big = __vmaxu2(big, __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu)));
+            return big;
+          };
+          const auto scale_up = [&](uint32_t big) { return min(134 - (int)(max(big & 0xFFFFu, big >> 16) >> 7), 127); };  // largest to 2^7 .. 2^8
+          float* ups = row_up + (k & 3) * C::Rows;
+          if (D > 64)
+#pragma unroll 1
+            for (int r = tid; r < w.rows; r += 64) {
+              const uint16_t* row = row_of(r);
+              uint32_t big = 0;
+#pragma unroll 1
+              for (int col = 0; col < D; col += 64) {
+                uint4 u[8];
+                load(row + col, u);
+                big = largest(u, big);
+              }
+              ups[r] = (float)scale_up(big);
+            }
           if (!room()) break;
 #pragma unroll 1
           for (int r = tid; r < w.rows; r += 64) {
-            const int dr = prompt::draft(p, w.g0 + r), hr = w.g0 + r - dr * p.group;
-            const uint16_t* row = p.q + (int64_t)(w.start + w.first + dr) * p.q_stride + (int64_t)(w.head * p.group + hr) * D;
-            uint4 u[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) u[i] = *reinterpret_cast<const uint4*>(row + 8 * i);
-            uint32_t big = 0;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              big = __vmaxu2(big, __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu)));
-            const int up = min(134 - (int)(max(big & 0xFFFFu, big >> 16) >> 7), 127);
-            row_up[(k & 3) * C::Rows + r] = (float)up;
-            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-            uint8_t* at = to + (r >> 7) * C::QTile;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t hi[4], lo[4];
-              split8(u[2 * i], flip, f, hi[0], hi[1], lo[0], lo[1]);
-              split8(u[2 * i + 1], flip, f, hi[2], hi[3], lo[2], lo[3]);
-              *reinterpret_cast<uint4*>(at + C::at8(r & 127, i)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(at + C::QTile / 2 + C::at8(r & 127, i)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-          }
-        } else {
-          constexpr int kMost = 8;  // rows whose loads are in flight
-          const int d0 = d, h0 = hh;
-          const uint16_t* src0 = src;
-          // Twice over the rows: for their scales, before the place is free, then for the numbers.
+            const uint16_t* row = row_of(r);
 #pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
-            if (pass == 1) {
-              if (!room()) break;
-              d = d0;
-              hh = h0;
-              src = src0;
-              __syncwarp();
-            }
-#pragma unroll 1
-            for (int r1 = r0; r1 < C::Rows && r1 - r0 < w.rows; r1 += kRows * kMost) {
-              uint4 u[kMost];
+            for (int col = 0; col < D; col += 64) {
+              uint4 u[8];
+              load(row + col, u);
+              if (D == 64) ups[r] = (float)scale_up(largest(u, 0));
+              const float f = __uint_as_float((uint32_t)(127 + (int)ups[r]) << 23);
+              uint8_t* at = to + (r >> 7) * C::QTile + col / C::Cols * (128 * C::Cols);
 #pragma unroll
-              for (int i = 0; i < kMost; ++i) {
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (r1 + i * kRows < w.rows) u[i] = *reinterpret_cast<const uint4*>(src);
-                next();
-              }
-#pragma unroll
-              for (int i = 0; i < kMost; ++i) {
-                const int r = r1 + i * kRows;
-                if (pass == 0) {
-                  // the row's largest number: positive bf16 patterns compare like integers, two at a time
-                  uint32_t big = __vmaxu2(__vmaxu2(u[i].x & 0x7FFF7FFFu, u[i].y & 0x7FFF7FFFu), __vmaxu2(u[i].z & 0x7FFF7FFFu, u[i].w & 0x7FFF7FFFu));
-#pragma unroll
-                  for (int o = 1; o < LPR; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-                  const uint32_t top = max(big & 0xFFFFu, big >> 16) >> 7;  // its exponent: comes to 2^7 .. 2^8
-                  if (r < w.rows && ch == 0) row_up[(k & 3) * C::Rows + r] = (float)min(134 - (int)top, 127);
-                  continue;
-                }
-                if (r >= w.rows) continue;
-                const float f = __uint_as_float((uint32_t)(127 + (int)row_up[(k & 3) * C::Rows + r]) << 23);
-                uint2 hi, lo;
-                split8(u[i], flip, f, hi.x, hi.y, lo.x, lo.y);
-                // 8 numbers: half of a chunk of 16
-                const int half_chunk = ch % (C::Cols / 8);
-                uint8_t* at = to + (r >> 7) * C::QTile + ch / (C::Cols / 8) * (128 * C::Cols) + C::at8(r & 127, half_chunk >> 1) + (half_chunk & 1) * 8;
-                *reinterpret_cast<uint2*>(at) = hi;
-                *reinterpret_cast<uint2*>(at + C::QTile / 2) = lo;
+              for (int i = 0; i < 4; ++i) {
+                uint32_t hi[4], lo[4];
+                split8(u[2 * i], flip, f, hi[0], hi[1], lo[0], lo[1]);
+                split8(u[2 * i + 1], flip, f, hi[2], hi[3], lo[2], lo[3]);
+                const int place = C::at8(r & 127, col % C::Cols / 16 + i);
+                *reinterpret_cast<uint4*>(at + place) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(at + C::QTile / 2 + place) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
               }
             }
           }
-          if (dead) break;
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
