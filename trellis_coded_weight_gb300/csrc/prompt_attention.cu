@@ -390,26 +390,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             if (dead) break;
             constexpr int Chunks = C::Cols / 8;
-            const int from = max(shared_to - pos0, 0);
-            for (int c = from * Chunks + tid; c < kTile * Chunks; c += 128) {
-              const int row = c / Chunks, ch = c % Chunks;
-              uint4* to = reinterpret_cast<uint4*>(tile + C::at(row, ch));
-              if (pos0 + row >= w.len) {
-                *to = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint4 v = *to;
-              bool odd = false;
-              const auto clean = [&](uint32_t& x) {
-                if ((x & 0x7F80u) == 0x7F80u) { x &= 0xFFFF0000u; odd = true; }
-                if ((x >> 16 & 0x7F80u) == 0x7F80u) { x &= 0xFFFFu; odd = true; }
+            const int from = max(shared_to - pos0, 0), to = min(w.len - pos0, kTile);  // rows that some do not see; their end
+            for (int c = max(to, 0) * Chunks + tid; c < kTile * Chunks; c += 128) *reinterpret_cast<uint4*>(tile + C::at(c / Chunks, c % Chunks)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (int c = from * Chunks + tid; c < to * Chunks; c += 128) {
+              uint4* at = reinterpret_cast<uint4*>(tile + C::at(c / Chunks, c % Chunks));
+              const uint4 v = *at;
+              // an exponent of ones carries into bit 15
+              const auto carry = [](uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; };
+              if (((carry(v.x) | carry(v.y) | carry(v.z) | carry(v.w)) & 0x80008000u) == 0) continue;
+              const auto clean = [&](uint32_t x) {
+                if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+                if ((x >> 16 & 0x7F80u) == 0x7F80u) x &= 0xFFFFu;
+                return x;
               };
-              clean(v.x); clean(v.y); clean(v.z); clean(v.w);
-              if (odd) {
-                odd_of[k % kOdd] = k;
-                __threadfence_block();
-                *to = v;
-              }
+              *at = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+              odd_of[k % kOdd] = k;
+              __threadfence_block();
             }
           }
           tc::fence_proxy_async_smem();
@@ -433,29 +430,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e0 = 0, copied = 0;
       uint32_t f_phase = 0, r_phase = 0, is_raw = 0;  // per slot: copies into it, those for the widening warps; what the last one was
       // The next stretch is planned and announced before the tiles of this one are copied, so that its queries are brought meanwhile.
-      const auto announce = [&](int k, Work& w) {
+      Work w{}, following;
+      for (int k = 0;; ++k) {
         if (plan.split) {
-          w = prompt::next_stretch<C::Rows>(p, plan, at, end);
+          following = prompt::next_stretch<C::Rows>(p, plan, at, end);
         } else {
           if (k > 0) {
             if (lane == 0) item = (int)gridDim.x + (p.counter ? atomicAdd(p.counter, 1) : item);
             item = __shfl_sync(0xFFFFFFFFu, item, 0);
           }
-          w = prompt::whole_item<C::Rows>(p, plan, item);
+          following = prompt::whole_item<C::Rows>(p, plan, item);
         }
-        const int s = k % kWorks;
-        if (k >= kWorks && !wait(w_empty + s, (uint32_t)(k / kWorks & 1) ^ 1u)) return false;
+        const int told_at = k % kWorks;
+        if (k >= kWorks && !wait(w_empty + told_at, (uint32_t)(k / kWorks & 1) ^ 1u)) break;
         if (lane == 0) {
-          works[s] = w;
-          tc::mbar_arrive(w_full + s);
+          works[told_at] = following;
+          tc::mbar_arrive(w_full + told_at);
         }
         __syncwarp();
-        return true;
-      };
-      Work w, following;
-      announce(0, w);
-      for (int k = 0; w.more; ++k, w = following) {
-        if (!announce(k + 1, following)) break;
+        if (k == 0) {
+          w = following;
+          if (!w.more) break;
+          continue;
+        }
         const int n = w.tiles;
         TreeSegment g;
         g.seq = TreeSeq{w.start, w.len - w.prefix, w.prefix};
@@ -500,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         e0 += 2 * n * C::Parts;
-        if (dead) break;
+        w = following;
+        if (dead || !w.more) break;
       }
       // no copy may land in a block that has left
       for (int i = max(0, copied - C::Slots); i < copied; ++i) {
