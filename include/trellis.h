@@ -412,8 +412,10 @@ size_t trellis_tree_workspace_bytes(const trellis_cache_t *cache, int batch, int
  * are packed one behind the other.  For token i and query head h:
  *   out = sum_p softmax_p(scale * q.k_p) v_p      lse = log sum_p exp(scale * q.k_p)
  * Scores, softmax statistics and sums are fp32; the softmax weights are
- * rounded to bf16 for the products with the values (their sum is not); one
- * rounding to bf16 at the end.  Numbers of an e4m3 cache are taken exactly.
+ * rounded to 16 bits (bf16, or fp16 with an e4m3 cache) for the products with
+ * the values (their sum is not); one rounding to bf16 at the end.  Queries are
+ * taken as they are; over an e4m3 cache numbers below 2^-13 of their row's
+ * largest are rounded, to within 2^-21 of the largest.
  * A token whose scores are all minus infinity gets zeros and an lse of minus
  * infinity.  What a token does not see (later tokens, rows past a sequence's
  * end) does not reach its result, whatever its bits are; a query with a
@@ -541,7 +543,8 @@ size_t trellis_adapter_plan_bytes(int batch, int n);
  * 0) get y[t] as it is; tokens of no sequence are left as they are.
  * Results do not depend on the other tokens' adapters or numbers.
  *   x [n][in], y and out [n][out] bf16, strides from token to token in
- *   elements, multiples of 8; out may be y (with the same stride).
+ *   elements, multiples of 8; out may be y (with the same stride), but may not
+ *   overlap x.
  *   plan: as left by trellis_adapter_plan with the same batch and n.
  */
 int trellis_adapter_add(const uint16_t *x, int64_t x_stride, const uint16_t *y, int64_t y_stride, uint16_t *out,
@@ -629,7 +632,7 @@ int trellis_prefill_plan(int M, const trellis_geom_t *g, int sms, int *tokens_pe
 
 /*
  * trellis_device_error -- diagnostic of the kernels that wait on mbarriers.  Every
- * such wait inside trellis_gemm_prefill and trellis_tree_attention is bounded (2 s); a wait that gives
+ * such wait inside trellis_gemm_prefill, trellis_tree_attention and trellis_prompt_attention is bounded (2 s); a wait that gives
  * up records a non-zero code in a device word instead of hanging the GPU.
  * Returns that code (0 = none), reading it synchronously from the current
  * device; reset != 0 clears it.  Negative values are trellis_status errors.
@@ -639,7 +642,7 @@ int trellis_device_error(int reset);
 /*
  * trellis_set_wait_limit -- diagnostic with no counterpart in the pages:
  * sets the limit of each bounded wait in the tensor-core kernels
- * (trellis_gemm_prefill, trellis_tree_attention) for launches issued after the call, in
+ * (trellis_gemm_prefill, trellis_tree_attention, trellis_prompt_attention) for launches issued after the call, in
  * nanoseconds of the GPU's global timer; 0 restores the default (2 s).
  * It exists so that tests can make the waits run out on an ordinary
  * problem and check the error path: the kernel then records a non-zero

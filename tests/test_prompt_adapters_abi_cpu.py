@@ -69,6 +69,7 @@ def test_adapter_add_errors_before_launch(lib):
     for strides in ((248, 512, 512), (256, 504, 512), (256, 512, 504), (260, 512, 512), (256, 516, 512), (256, 512, 516)):
         assert add(lib, strides=strides) == ESHAPE, strides
     assert add(lib, strides=(256, 512, 520), out=A) == ESHAPE  # in place with another stride
+    assert add(lib, ad=adapters(in_=512), strides=(512, 512, 512), x=2 * A) == ESHAPE  # out over x
     for name in ("x", "y", "out"):
         assert add(lib, **{name: None}) == ENULL
         assert add(lib, **{name: A + 4}) == EALIGN

@@ -166,6 +166,7 @@ int trellis_adapter_add(const uint16_t* x, int64_t x_stride, const uint16_t* y, 
     return TRELLIS_ESHAPE;
   if (n > 1 && out == y && out_stride != y_stride) return TRELLIS_ESHAPE;
   if (batch == 0 || n == 0) return TRELLIS_OK;
+  if (x && x == out) return TRELLIS_ESHAPE;
   if (!x || !y || !out || !ad->a || !ad->b) return TRELLIS_ENULL;
   if (!aligned16(x) || !aligned16(y) || !aligned16(out) || !aligned16(ad->a) || !aligned16(ad->b) ||
       !aligned16(ad->ranks) || !aligned16(ad->scales))

@@ -9,7 +9,11 @@
 // a lane has 8 contiguous ones.  h enters the second product as the sum of two bf16 numbers.
 // Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and
 // makes a share of the outputs.
-// Bound: bytes of x, y and out for prompts, of A and B for single tokens.
+// Bound: 4096 tokens of rank 16, 5120 to 17408: bytes of x, y and out (60 us, 5.4 TB/s).  Higher ranks: the first product of a tile, at
+// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 80 us, 128 133).  64 tokens of 40 adapters to rank 64: 32 us
+// (1.6 TB/s): a tile of rank 64 takes 20 whatever the others take, of which 8 are the launch of full blocks, and there are no more
+// clusters than SMs / 4.  1 token: 5.3 us of latency (launch, plan, tokens, x and A, two cluster barriers, B).
+// Clusters of 8: 115 us where 4 take 70, since each block reads as many parts of h as there are; of 2: 81.
 #include "adapter_plan.cuh"
 #include "common.cuh"
 #include "devcache.h"

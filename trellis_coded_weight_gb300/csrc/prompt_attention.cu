@@ -14,8 +14,14 @@
 // the upper half of a slot and widened in place to fp16 (exact); P is fp16 then, since weights of 4 bits would not do.  (Keys widened
 // too: 8192 tokens of heads of 256 took 730 us.)  Values that a product must not meet (rows past the end, numbers that are not finite
 // where not every row sees them) are cleared on the way, the latter added back for the rows that see them (rare).
-// The warps: two softmax warpgroups (a thread per row, a tile's scores in registers); the warp that plans and copies, the one
-// that issues, two that bring the queries; a warpgroup that widens and clears.
+// The warps: one that plans and copies, one that issues, two that bring the queries; two softmax warpgroups (a thread per row); a
+// warpgroup that widens and clears (two with e4m3 and heads of 256, whose second softmax warpgroup has nothing else to do).
+// Bound: the products, and what lies between them.  A tile of a stream is 1024 cycles of products with heads of 128 (512 with 64,
+// 2048 with 256) and takes 1480: S at N = 128 needs all of shared memory's bandwidth, which the copies also want, and a commit before
+// a wait costs the issuing warp 70 cycles.  16384 tokens, 32/8 heads of 128: 1.43 ms (1.54 PFLOP/s); 8192 tokens, 16/2 of 256: 379 us
+// (1.45); with e4m3 537 (1.02), where a tile's widening shares shared memory and issue slots with the rest.  Heads of 64: weights are
+// the longer part (two warps of an SM's quarter share 1024 cycles of exponentials per tile): 8192 tokens, 64/8 659 us (0.83).
+// Short items pay 5000 cycles each for their end and the first weights of the next: 16 sequences to 2000 tokens 334 us (1.14).
 #include <cstring>
 #include <cuda.h>
 
