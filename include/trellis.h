@@ -544,7 +544,7 @@ size_t trellis_adapter_plan_bytes(int batch, int n);
  * Results do not depend on the other tokens' adapters or numbers.
  *   x [n][in], y and out [n][out] bf16, strides from token to token in
  *   elements, multiples of 8; out may be y (with the same stride), but may not
- *   overlap x.
+ *   overlap it otherwise, nor x.
  *   plan: as left by trellis_adapter_plan with the same batch and n.
  */
 int trellis_adapter_add(const uint16_t *x, int64_t x_stride, const uint16_t *y, int64_t y_stride, uint16_t *out,

@@ -19,7 +19,7 @@ def prompts(**kw):
 
 
 def attention(lib, c=None, d=None, layer=0, hq=16, scale=0.1, stride=2048, ws=A, ws_bytes=1 << 40, **kw):
-    a = dict(q=A, out=A, lse=A)
+    a = dict(q=A, out=2 * A, lse=A)
     a.update(kw)
     return lib.trellis_prompt_attention(a["q"], stride, ctypes.byref(c or cache()), layer, ctypes.byref(d or prompts()), hq, scale,
                                         a["out"], stride, a["lse"], ws, ws_bytes, None)
@@ -40,6 +40,7 @@ def test_prompt_attention_errors_before_launch(lib):
     for kw in (dict(table=A + 4), dict(prefix=A + 4), dict(q_start=A + 8)):
         assert attention(lib, d=prompts(**kw)) == EALIGN
     assert attention(lib, q=None) == ENULL and attention(lib, out=None) == ENULL
+    assert attention(lib, out=A) == ESHAPE  # out over q
     assert attention(lib, q=A + 2) == EALIGN and attention(lib, out=A + 4) == EALIGN and attention(lib, lse=A + 4) == EALIGN
     assert attention(lib, c=cache(head_dim=96)) == ESHAPE and attention(lib, c=cache(pool=None)) == ENULL
     size = lambda c, hq: lib.trellis_prompt_workspace_bytes(ctypes.byref(c), hq)  # noqa: E731

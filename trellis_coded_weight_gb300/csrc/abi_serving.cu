@@ -126,6 +126,7 @@ int trellis_prompt_attention(const uint16_t* q, int64_t q_stride, const trellis_
   const int64_t w = (int64_t)q_heads * cache->head_dim;
   if (d->n > 1 && (!stride_ok(q_stride, w) || !stride_ok(out_stride, w))) return TRELLIS_ESHAPE;
   if (!q || !out || !d->table || !d->prefix || !d->q_start) return TRELLIS_ENULL;
+  if (q == out) return TRELLIS_ESHAPE;
   if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(d->table) || !aligned16(d->prefix) ||
       !aligned16(d->q_start))
     return TRELLIS_EALIGN;
