@@ -10,9 +10,10 @@
 // Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and
 // makes a share of the outputs.
 // Bound: 4096 tokens of rank 16, 5120 to 17408: bytes of x, y and out (60 us, 5.4 TB/s).  Higher ranks: the first product of a tile, at
-// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 80 us, 128 133).  64 tokens of 40 adapters to rank 64: 32 us
-// (1.6 TB/s): a tile of rank 64 takes 20 whatever the others take, of which 8 are the launch of full blocks, and there are no more
-// clusters than SMs / 4.  1 token: 5.3 us of latency (launch, plan, tokens, x and A, two cluster barriers, B).
+// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 80 us, 128 133).  64 tokens of 40 adapters to rank 64: 26 us
+// (1.9 TB/s): a tile of rank 64 takes its cluster 19 whatever the others take, 9 of them before the second product, whose blocks of
+// outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token:
+// 5.1 us of latency (launch, plan, tokens, x and A, two cluster barriers, B).
 // Clusters of 8: 115 us where 4 take 70, since each block reads as many parts of h as there are; of 2: 81.
 #include "adapter_plan.cuh"
 #include "common.cuh"
@@ -73,8 +74,12 @@ __device__ __forceinline__ uint32_t first_of(uint32_t w, int n) { return n >= 2 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+// The first `bytes` of them, the others zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -281,6 +286,8 @@ struct Expand {
   const uint16_t* b;
   const int* tokens;
   uint8_t* ring;  // the warp's
+  const uint16_t* y_row[kRingB ? 2 : 1];  // kRingB: tokens g and 8 + g
+  const uint16_t* next_b;  // kRingB: this lane's numbers of the next block to copy, for tile 0 and ranks 0 ..
   int rank, count, o, o1, lane, g, q, left, stage;
 
   __device__ __forceinline__ Expand(const AddParams& p_, const uint16_t* b_, int rank_, int count_, const int* tokens_, uint8_t* rings, int o0,
@@ -293,6 +300,10 @@ struct Expand {
     o = o0 + warp;
     left = rank - (NARROW ? 4 : 8) * q;
     ring = rings + warp * kWarpRing;
+    if constexpr (kRingB)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) y_row[i] = p.y + (8 * i + g < count ? (int64_t)tokens[8 * i + g] * p.y_stride : 0) + 8 * q;
+    next_b = b + (32 * (int64_t)o + 8 * (g >> 1) + (g & 1)) * p.ad.max_rank + (left > 0 ? (NARROW ? 4 : 8) * q : 0);
   }
   __device__ __forceinline__ void start() {
 #pragma unroll
@@ -310,16 +321,25 @@ struct Expand {
       if (col < p.ad.out)
 #pragma unroll
         for (int i = 0; i < 2 * MT; ++i)
-          if (8 * i + g < count) cp_async16(to + (i * 32 + lane) * 16, p.y + (int64_t)tokens[8 * i + g] * p.y_stride + col);
-      if constexpr (kRingB)
+          if (8 * i + g < count)
+            cp_async16(to + (i * 32 + lane) * 16, kRingB ? y_row[kRingB ? i : 0] + 32 * block : p.y + (int64_t)tokens[8 * i + g] * p.y_stride + col);
+      // Ranks that the adapter has not become zeros (the address is one of its own all the same).  Outputs past the end have whatever
+      // the ring holds; their results are not stored.
+      if constexpr (kRingB) {
+        const uint16_t* from = next_b;
+        const uint32_t at = tc::smem_u32(to) + kY + lane * (NARROW ? 8 : 16);
+        const int rows = (int)p.ad.out - 32 * block - 8 * (g >> 1) - (g & 1);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j, from += 2 * p.ad.max_rank) {
+          if (2 * j >= rows) break;
 #pragma unroll
-          for (int kb = 0; kb < NB; ++kb)
-            if (const uint16_t* at = weights(block, j, kb)) {
-              if (NARROW) cp_async8(to + kY + (j * 32 + lane) * 8, at);
-              else cp_async16(to + kY + ((j * NB + kb) * 32 + lane) * 16, at);
-            }
+          for (int kb = 0; kb < NB; ++kb) {
+            if (NARROW) cp_async8(at + j * 256, from, 2 * max(0, min(left, 4)));
+            else cp_async16(at + (j * NB + kb) * 512, from + (left > 32 * kb ? 32 * kb : 0), 2 * max(0, min(left - 32 * kb, 8)));
+          }
+        }
+        next_b += (int64_t)kWarps * 32 * p.ad.max_rank;
+      }
     }
     cp_async_commit();
   }
@@ -345,24 +365,31 @@ struct Expand {
     const bool ragged = rank % (NARROW ? 4 : 8) != 0;
     uint4 v[4][NB], next[4][NB];
     if constexpr (!kRingB && NB < 4) load(o, next);
+    // Few tokens: h stays in registers, since reading it again with every block takes as much of shared memory's bandwidth as B does
+    // (64 adapters of rank 16: 19 us so, 16).
+    constexpr int kSteps = NARROW ? 2 : 4;  // high and low parts of each step
+    uint4 held[kRingB ? NB : 1][kSteps];
+    if constexpr (kRingB)
+#pragma unroll
+      for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+        for (int f = 0; f < kSteps; ++f) held[kb][f] = *reinterpret_cast<const uint4*>(hl + fragment<RMAX, NARROW, NB>(0, kb, f >> 1, f & 1));
 #pragma unroll 1
     for (; o < o1; o += kWarps) {
       cp_async_wait<kStages - 1>();
       const uint8_t* from = ring + stage * kStage;
       uint4 u[2 * MT];
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) u[i] = *reinterpret_cast<const uint4*>(from + (i * 32 + lane) * 16);
+      for (int i = 0; i < 2 * MT; ++i)
+        u[i] = *reinterpret_cast<const uint4*>(from + (i * 32 + lane) * 16);
       if constexpr (kRingB) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb) {
-            v[j][kb] = make_uint4(0, 0, 0, 0);
-            if (!weights(o, j, kb)) continue;
             if (NARROW) {
               const uint2 two = *reinterpret_cast<const uint2*>(from + kY + (j * 32 + lane) * 8);
-              v[j][kb].x = two.x;
-              v[j][kb].y = two.y;
+              v[j][kb] = make_uint4(two.x, two.y, 0, 0);
             } else {
               v[j][kb] = *reinterpret_cast<const uint4*>(from + kY + ((j * NB + kb) * 32 + lane) * 16);
             }
@@ -378,7 +405,7 @@ struct Expand {
       }
       copy(o + kStages * kWarps, stage);
       stage = stage + 1 == kStages ? 0 : stage + 1;
-      if (ragged)
+      if (!kRingB && ragged)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -399,8 +426,10 @@ struct Expand {
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-          for (int f = 0; f < (NARROW ? 2 : 4); ++f) {  // high and low parts of each step
-            const uint4 a = *reinterpret_cast<const uint4*>(hl + fragment<RMAX, NARROW, NB>(i, kb, f >> 1, f & 1));
+          for (int f = 0; f < kSteps; ++f) {
+            uint4 a;
+            if constexpr (kRingB) a = held[kb][f];
+            else a = *reinterpret_cast<const uint4*>(hl + fragment<RMAX, NARROW, NB>(i, kb, f >> 1, f & 1));
             const bool second = f >= 2;
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma(acc[j], a.x, a.y, a.z, a.w, second ? v[j][kb].z : v[j][kb].x, second ? v[j][kb].w : v[j][kb].y);
@@ -455,8 +484,7 @@ __device__ __forceinline__ int rank_of(const AddParams& p, int adapter) {
   return rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
 }
 
-// The tiles by falling rank, where there are more of them than clusters: each cluster then takes one from the front of a round and
-// one from the back of the next.
+// The tiles by falling rank, where there are more of them than clusters.
 constexpr int kSorted = kThreads;
 __device__ __noinline__ void sort_tiles(const AddParams& p, int tiles, int* ranks, uint16_t* order) {
   const int t = threadIdx.x;
@@ -485,15 +513,17 @@ __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const
   __shared__ uint16_t order_of[kSort ? kSorted : 1];
   const bool sorted = kSort && p.ad.ranks && tiles > clusters && tiles <= kSorted;
   if (kSort && sorted) sort_tiles(p, tiles, reinterpret_cast<int*>(raw), order_of);
-  bool back = false;
-  for (int t0 = 0; t0 < tiles; t0 += clusters, back = !back) {
-    // the round's tiles; where they are few, as many clusters for each as have a block of outputs per warp
+  bool back = false;  // every other round of the sorted ones
+  for (int t0 = 0; t0 < tiles; t0 += clusters, back = sorted && !back) {
+    // The round's tiles; where they are few, as many clusters for each as have a block of outputs per warp.  Back: the clusters whose
+    // last tile was least take the first ones, and few tiles are shared by two thirds of the clusters (by all: 31 us for 27).
     const int now = min(tiles - t0, clusters);
-    const int shares = max(1, min(clusters / now, blocks / (kCluster * kWarps)));
-    if (cluster >= now * shares) break;
-    const int at = t0 + (kSort && back && now == clusters ? clusters - 1 - cluster : cluster % now);
+    const int shares = max(1, min((kSort && back ? clusters * 2 / 3 : clusters) / now, blocks / (kCluster * kWarps)));
+    const int me = kSort && back ? clusters - 1 - cluster : cluster;
+    if (me >= now * shares) break;
+    const int at = t0 + me % now;
     const int4 tile = __ldcg(adapter_tiles(p.plan) + (kSort && sorted ? order_of[at] : at));
-    const int share = (cluster / now) * kCluster + rank_of_block, all = shares * kCluster;
+    const int share = (me / now) * kCluster + rank_of_block, all = shares * kCluster;
     const int o0 = (int)((int64_t)share * blocks / all), o1 = (int)((int64_t)(share + 1) * blocks / all);
     const int rank = rank_of(p, tile.x);
     __syncthreads();
@@ -509,8 +539,9 @@ __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const
       continue;
     }
     const float scale = p.ad.scales ? __ldg(p.ad.scales + tile.x) : 1.f;
-    if (tile.z <= 16) tile_by_rank<RMAX, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
-    else tile_by_rank<RMAX, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+    // in this order: ragged prompts 82 us, and 92 with the code of few tokens in front
+    if (tile.z > 16) tile_by_rank<RMAX, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
+    else tile_by_rank<RMAX, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
   }
 }
 
