@@ -10,7 +10,7 @@
 // Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and
 // makes a share of the outputs.
 // Bound: 4096 tokens of rank 16, 5120 to 17408: bytes of x, y and out (60 us, 5.4 TB/s).  Higher ranks: the first product of a tile, at
-// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 80 us, 128 133).  64 tokens of 40 adapters to rank 64: 26 us
+// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 84 us, 128 142).  64 tokens of 40 adapters to rank 64: 26 us
 // (1.9 TB/s): a tile of rank 64 takes its cluster 19 whatever the others take, 9 of them before the second product, whose blocks of
 // outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token:
 // 5.1 us of latency (launch, plan, tokens, x and A, two cluster barriers, B).
