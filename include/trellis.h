@@ -537,8 +537,8 @@ size_t trellis_adapter_plan_bytes(int batch, int n);
  * trellis_adapter_add -- adds the tokens' adapters to a projection's output:
  *   out[t] = bf16( y[t] + scales[i] * B_i (A_i x[t]) ),  i = token t's adapter
  * A_i x[t] is accumulated in fp32 and enters the second product as the sum of
- * two bf16 numbers (to within 2^-16 of its size); sums are fp32, with one
- * rounding at the end.
+ * two bf16 numbers (to within 2^-16 of its size, or 2^-132); sums are fp32,
+ * with one rounding at the end.
  * Tokens without an adapter (none, an index outside the adapters, or of rank
  * 0) get y[t] as it is; tokens of no sequence are left as they are.
  * Results do not depend on the other tokens' adapters or numbers.

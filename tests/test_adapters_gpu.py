@@ -305,3 +305,36 @@ def test_rounds_of_many_adapters(rank, count):
     first = s.run().clone()
     s.check(first)
     assert torch.equal(s.run(), first)
+
+
+def check_any_numbers(s, out):
+    """Every number against the definition, infinities and NaN in their places.  The finite ones are to the tolerance above."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        for b, (t, a) in enumerate(zip(s.toks, s.which)):
+            rows, r = slice(int(s.starts[b]), int(s.starts[b + 1])), s.ranks[a]
+            x, A, B, y = (v.double().cpu().numpy() for v in (s.x[rows], s.a[a, :r], s.b[a, :, :r], s.y[rows]))
+            # one product after the other: a library's matrix product may pad with zeros
+            h, T = (x[:, None] * A[None]).sum(-1), (np.abs(x)[:, None] * np.abs(A)[None]).sum(-1)
+            low, S, big = (sum(g[:, i, None] * w[None, :, i] for i in range(r)) for g, w in ((h, B), (np.abs(h), np.abs(B)), (T, np.abs(B))))
+            want, got = y + low, out[rows].double().cpu().numpy()
+            fine = np.isfinite(want)
+            assert np.array_equal(np.isnan(got), np.isnan(want)), (b, r, np.argwhere(np.isnan(got) != np.isnan(want))[:4].tolist())
+            assert np.array_equal(got[~fine & ~np.isnan(want)], want[~fine & ~np.isnan(want)]), (b, r)
+            tol = 1.1 * (2.0 ** -8 * np.abs(want) + s.k * 2.0 ** -24 * big + 2.0 ** -16 * S + (r + 3) * 2.0 ** -24 * (S + np.abs(y)))
+            assert np.all(np.abs(got - want)[fine] <= tol[fine]), (b, r)
+
+
+RANKS_OF_ALL_KERNELS = [(8, 1), (8, 5), (8, 8), (16, 16), (24, 17), (32, 32), (40, 3), (64, 40), (64, 64), (128, 9), (128, 100), (128, 128)]
+
+
+@pytest.mark.parametrize("max_rank,rank", RANKS_OF_ALL_KERNELS)
+def test_infinite_numbers_in_b(max_rank, rank):
+    """B's infinities are infinite in the outputs, also where the low-rank product is a bf16 number (its low part is zero)."""
+    s = Step([3, 70], [0, 1], [rank, rank], max_rank, 264, 520, seed=30 + rank, scales=False)
+    s.x[:, :] = 0
+    for t in range(s.tokens):  # h is a column of A (exact), twice it, or with a second one what takes more than 8 bits
+        s.x[t, (37 * t) % 264] = 1.0 + t % 2
+        if t % 3 == 2:
+            s.x[t, (37 * t + 5) % 264] = 1.0
+    s.b[0, 9, 0], s.b[0, 10, rank - 1], s.b[1, 500, rank // 2] = float("inf"), -float("inf"), -float("inf")
+    check_any_numbers(s, s.run())

@@ -247,6 +247,18 @@ __device__ __forceinline__ int fragment(int mt, int kb, int step, int low) {
   const int block = mt * NB + kb;
   return (NB == 4 ? block / kPerWarp * (kWarpRing / 4) + kWarpRing / 8 + block % kPerWarp * 512 : block * 512) + (step * 2 + low) * 128;
 }
+// The two bf16 numbers (in the upper halves of floats) whose sum h is: cut off (which never overflows), and what that leaves, of the same
+// sign.  Neither is zero
+// unless h is: the least bf16 number (2^-133) stands in for it, since zero times an infinite number of B would be NaN where h is not zero.
+__device__ __forceinline__ uint2 split(float h) {
+  constexpr uint32_t kLeast = 0x00010000u;
+  const uint32_t bits = __float_as_uint(h), sign = bits & 0x80000000u;
+  if ((bits << 1) == 0) return make_uint2(bits, bits);
+  uint32_t high = bits & 0xFFFF0000u;
+  if ((high << 1) == 0) high |= kLeast;
+  const float low = (high & 0x7F800000u) == 0x7F800000u ? 0.f : h - __uint_as_float(high);
+  return make_uint2(high, fabsf(low) < __uint_as_float(kLeast) ? sign | kLeast : __float_as_uint(low));
+}
 template <int RMAX, int MT, bool NARROW, int NB>
 __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
   constexpr int wide = NB * (NARROW ? 16 : 32) / 2;  // pairs of ranks
@@ -261,15 +273,12 @@ __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
       s.x += v[c].x;
       s.y += v[c].y;
     }
-    // cut off to bf16 (which never overflows) and what that leaves
-    const uint32_t x = __float_as_uint(s.x) & 0xFFFF0000u, y = __float_as_uint(s.y) & 0xFFFF0000u;
-    const float lx = (x & 0x7F800000u) == 0x7F800000u ? 0.f : s.x - __uint_as_float(x);
-    const float ly = (y & 0x7F800000u) == 0x7F800000u ? 0.f : s.y - __uint_as_float(y);
+    const uint2 x = split(s.x), y = split(s.y);
     const int row = t & 15, kb = NARROW ? 0 : r >> 5;
     const int q = NARROW ? r >> 2 : (r & 31) >> 3, step = NARROW ? 0 : (r & 7) >> 2, pair = (r & 3) >> 1;
     const int word = ((row & 7) * 4 + q) * 4 + (row >> 3) + 2 * pair;
-    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 0) + word] = (x >> 16) | y;
-    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 1) + word] = pack_bf16x2(lx, ly);
+    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 0) + word] = (x.x >> 16) | y.x;
+    h[fragment<RMAX, NARROW, NB>(t >> 4, kb, step, 1) + word] = pack_bf16x2(__uint_as_float(x.y), __uint_as_float(y.y));
   }
 }
 
