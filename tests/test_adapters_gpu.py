@@ -338,3 +338,15 @@ def test_infinite_numbers_in_b(max_rank, rank):
             s.x[t, (37 * t + 5) % 264] = 1.0
     s.b[0, 9, 0], s.b[0, 10, rank - 1], s.b[1, 500, rank // 2] = float("inf"), -float("inf"), -float("inf")
     check_any_numbers(s, s.run())
+
+
+@pytest.mark.parametrize("max_rank,rank", RANKS_OF_ALL_KERNELS)
+def test_infinite_numbers_in_x_and_a(max_rank, rank):
+    """Ranks that an adapter does not have take no part, also where a token's numbers are infinite."""
+    s = Step([3, 70, 2, 40], [0, 1, 2, 3], [rank] * 4, max_rank, 264, 520, seed=50 + rank, scales=False)
+    for i in (0, 1):  # one sign: sums of infinities are infinite
+        s.a[i, :rank], s.b[i, :, :rank] = s.a[i, :rank].abs() + 0.01, s.b[i, :, :rank].abs() + 0.01
+    s.x[1, 100], s.x[3 + 40, 7], s.x[3 + 69, 263], s.x[75 + 20, 9] = float("inf"), -float("inf"), float("inf"), float("inf")
+    s.a[2, 0, 0], s.a[3, rank - 1, 11] = float("inf"), -float("inf")
+    s.x[75 + 30, 11] = 0  # times infinity: NaN
+    check_any_numbers(s, s.run())

@@ -248,19 +248,17 @@ __device__ __forceinline__ int fragment(int mt, int kb, int step, int low) {
   return (NB == 4 ? block / kPerWarp * (kWarpRing / 4) + kWarpRing / 8 + block % kPerWarp * 512 : block * 512) + (step * 2 + low) * 128;
 }
 // The two bf16 numbers (in the upper halves of floats) whose sum h is: cut off (which never overflows), and what that leaves, of the same
-// sign.  Neither is zero
-// unless h is: the least bf16 number (2^-133) stands in for it, since zero times an infinite number of B would be NaN where h is not zero.
+// sign.  Neither is zero unless h is: the least bf16 number (2^-133) stands in for it, since zero times an infinite number of B would be
+// NaN where h times it is infinite.
 __device__ __forceinline__ uint2 split(float h) {
   constexpr uint32_t kLeast = 0x00010000u;
-  const uint32_t bits = __float_as_uint(h), sign = bits & 0x80000000u;
-  if ((bits << 1) == 0) return make_uint2(bits, bits);
-  uint32_t high = bits & 0xFFFF0000u;
-  if ((high << 1) == 0) high |= kLeast;
-  const float low = (high & 0x7F800000u) == 0x7F800000u ? 0.f : h - __uint_as_float(high);
-  return make_uint2(high, fabsf(low) < __uint_as_float(kLeast) ? sign | kLeast : __float_as_uint(low));
+  const uint32_t sign = __float_as_uint(h) & 0x80000000u, size = __float_as_uint(h) & 0x7FFFFFFFu;
+  const uint32_t least = size ? kLeast : 0u, high = max(size & 0x7FFF0000u, least);
+  const float low = __uint_as_float(size) - __uint_as_float(high);  // NaN where h is infinite
+  return make_uint2(sign | high, sign | (low >= __uint_as_float(kLeast) ? __float_as_uint(low) : least));
 }
 template <int RMAX, int MT, bool NARROW, int NB>
-__device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
+__device__ __forceinline__ void gather(const float* copies, int rank, uint32_t* h) {
   constexpr int wide = NB * (NARROW ? 16 : 32) / 2;  // pairs of ranks
   for (int e = threadIdx.x; e < 16 * MT * wide; e += kThreads) {
     const int t = e / wide, r = (e - t * wide) * 2;
@@ -273,6 +271,9 @@ __device__ __forceinline__ void gather(const float* copies, uint32_t* h) {
       s.x += v[c].x;
       s.y += v[c].y;
     }
+    // ranks that the adapter does not have: zeros, since those of A times an infinite number of x are NaN
+    if (r >= rank) s.x = 0.f;
+    if (r + 1 >= rank) s.y = 0.f;
     const uint2 x = split(s.x), y = split(s.y);
     const int row = t & 15, kb = NARROW ? 0 : r >> 5;
     const int q = NARROW ? r >> 2 : (r & 31) >> 3, step = NARROW ? 0 : (r & 7) >> 2, pair = (r & 3) >> 1;
@@ -470,7 +471,7 @@ __device__ __forceinline__ void tile_of(const AddParams& p, const int4& tile, in
   if (MT > 1) second.start();  // the ring is free
   cluster_arrive();
   cluster_wait();
-  gather<RMAX, MT, NARROW, NB>(copies, h);
+  gather<RMAX, MT, NARROW, NB>(copies, rank, h);
   cluster_arrive();  // this block has read the others' sums
   __syncthreads();
   second.run(h, scale);
