@@ -81,14 +81,19 @@ def generate(model, prompts, which, length, chunk=10 ** 6):
     """Continues the prompts together, each by its most likely tokens; `chunk`: most tokens of a prompt in one step."""
     seqs = base.Sequences(model.cache)
     rows = list(range(len(prompts)))
+    first = [None] * len(prompts)  # what follows a prompt: the results of the step that took its last chunk
     for at in range(0, max(len(p) for p in prompts), chunk):
         here = [r for r in rows if at < len(prompts[r])]
         got = step(model, seqs, here, [prompts[r][at:at + chunk] for r in here], [which[r] for r in here])
+        for i, r in enumerate(here):
+            first[r] = (got.top_ids[i], got.top_logprobs[i])
+    ids, lp = (torch.stack(t) for t in zip(*first))
     tokens, logprobs = [], []
     for _ in range(length):
-        tokens.append(got.top_ids[:, 0].tolist())
-        logprobs.append(got.top_logprobs.clone())
+        tokens.append(ids[:, 0].tolist())
+        logprobs.append(lp)
         got = step(model, seqs, rows, [[t] for t in tokens[-1]], which)
+        ids, lp = got.top_ids, got.top_logprobs
     return tokens, torch.stack(logprobs)
 
 

@@ -40,3 +40,19 @@ def test_requests_together_are_what_they_are_alone(example, dtype):
     _, changed = r["others"]
     assert (changed[0, 0] - lp[0, 0]).abs().max() > 0.1 and (changed[0, 2] - lp[0, 2]).abs().max() > 0.1
     assert (changed[0, 1] - lp[0, 1]).abs().max() < 0.1
+
+
+def test_prompts_in_chunks_together_are_what_they_are_whole(example):
+    """Prompts of different lengths end in different chunks' steps; each is continued from its own last token's results."""
+    model = example.Model()
+    g = torch.Generator().manual_seed(6)
+    prompts = [torch.randint(0, example.VOCAB, (n,), generator=g).tolist() for n in (150, 67, 211)]
+    tokens, lp = example.generate(model, prompts, [1, -1, 2], 4)
+    parts, parts_lp = example.generate(model, prompts, [1, -1, 2], 4, chunk=64)
+    assert lp.shape == parts_lp.shape
+    for i in range(len(prompts)):
+        for s in range(len(tokens)):
+            assert (lp[s, i] - parts_lp[s, i]).abs().max() < 0.1, (i, s)
+            if tokens[s][i] != parts[s][i]:
+                assert lp[s, i, 0] - lp[s, i, 1] < 0.1
+                break
