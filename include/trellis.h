@@ -423,8 +423,8 @@ size_t trellis_tree_workspace_bytes(const trellis_cache_t *cache, int batch, int
  *   d->mask must be NULL; 1 <= d->max_tokens <= 2^20.  The other arguments,
  *   the clamping of lengths and the errors are those of trellis_tree_attention
  *   (out may not overlap q).
- *   workspace: as for trellis_matvec_axis0 (zero-filled before its first use),
- *   of at least trellis_prompt_workspace_bytes bytes.
+ *   workspace: at least trellis_prompt_workspace_bytes bytes, no initial state;
+ *   calls that share one must not overlap in time.
  */
 int trellis_prompt_attention(const uint16_t *q, int64_t q_stride, const trellis_cache_t *cache, int layer,
                              const trellis_drafts_t *d, int q_heads, float scale, uint16_t *out, int64_t out_stride,

@@ -492,3 +492,40 @@ def test_counts_of_zero():
     out, lse = p.out.fill_(7.5), p.lse.fill_(7.5)
     tb.prompt_attention(p.q, p.cache, 0, nothing, p.ws, out=out, lse=lse)
     assert bool((out == 7.5).all()) and bool((lse == 7.5).all())
+
+
+@pytest.mark.parametrize("hq,hkv,d,f8,lens,toks", [
+    (40, 8, 128, False, [0, 300, 0, 17] * 4, [1300, 900, 500, 1] * 4),  # items of whole blocks, more than there are thread blocks
+    (16, 2, 256, True, [0] * 12, [700] * 12),
+    (16, 4, 64, True, [0] * 20, [900] * 20),
+    (8, 2, 128, False, [9000], [300]),                                  # split ranges, joined
+    (8, 2, 128, False, [0], [100])])                                    # an item for each block at most
+@pytest.mark.parametrize("fill", [0, 5, 1 << 20, -1, -1000, 0x7FFFFFFF, "floats"])
+def test_a_workspace_of_any_contents(hq, hkv, d, f8, lens, toks, fill):
+    """A program's scratch memory that other calls have used: the workspace needs no initial state."""
+    p = Prompts(lens, toks, hq, hkv, d, 64, f8, seed=26)
+    want = [t.clone() for t in p.run()]
+    words = p.ws.view(torch.int32)
+    if fill == "floats":
+        g = torch.Generator(device="cuda").manual_seed(3)
+        p.ws.view(torch.float32).copy_(torch.randn(words.shape, generator=g, device="cuda"))
+    else:
+        words.fill_(fill)
+    p.out.fill_(7.5), p.lse.fill_(7.5)
+    out, lse = p.run(p.ws)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_one_scratch_buffer_for_tree_and_prompt_attention():
+    p = Prompts([500, 0, 100, 40] * 5, [64, 3, 20, 1] * 5, 8, 2, 128, 16, seed=27)
+    big = Prompts([0] * 12, [1200, 900, 1, 700] * 3, 40, 8, 128, 64, seed=28)
+    want, want_l = [t.clone() for t in big.run()]
+    tree = tb.DraftBatch(i32(p.table), i32(p.lens), i32(p.q_start), 64, None, p.n)
+    p.run()
+    need = max(tb.new_tree_workspace(p.cache, tree, 8).numel(), big.ws.numel())
+    scratch = torch.zeros(need, dtype=big.ws.dtype, device="cuda")
+    for _ in range(3):
+        tb.tree_attention(p.q, p.cache, 0, tree, scratch, p.scale)
+        big.out.fill_(7.5), big.lse.fill_(7.5)
+        big.run(scratch)
+        assert torch.equal(big.out, want) and torch.equal(big.lse, want_l)

@@ -47,7 +47,6 @@ __global__ void __launch_bounds__(kThreads, kPerSM) join_kernel(const TreeParams
   __shared__ int4 s_item;
   __shared__ int2 s_at;
   constexpr int LPR = D / 4;  // fours of columns of a row
-  if (p.counter && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.counter = 0;
   const int64_t part_floats = tree_part_floats(prows, D);
   const int tid = threadIdx.x, lane = tid & 31;
   // of a unit's threads as many share a column's parts as the item says, and two at least where a row has fewer columns than

@@ -30,7 +30,7 @@ struct TreeParams {
   const void* pool;     // the layer's pages, bf16 or e4m3
   int4* items;          // [kTreeMaxCtas]: the item that block c is the first to share (tree_item), or none
   float* part;          // two slots per thread block
-  int* counter;         // prompts: the next item, which the joining kernel clears; null for trees
+  int* counter;         // prompts: items taken, besides each block's first; null for trees
   int64_t q_stride, out_stride;
   int64_t pages;
   uint64_t wait_ns;
