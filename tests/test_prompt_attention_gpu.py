@@ -529,3 +529,19 @@ def test_one_scratch_buffer_for_tree_and_prompt_attention():
         big.out.fill_(7.5), big.lse.fill_(7.5)
         big.run(scratch)
         assert torch.equal(big.out, want) and torch.equal(big.lse, want_l)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["inf", "nan"])
+def test_scores_of_minus_infinity_give_zeros_whatever_the_values(d, kind):
+    """Tokens whose scores are all minus infinity, over values that are not finite: in whole tiles, at the end of what they see,
+    and where an item is split."""
+    for lens, toks in (([0], [300]), ([6000], [200])):
+        p = Prompts(lens, toks, 2, 1, d, 16, seed=13)
+        p.q[:, :, 0] = 1.0
+        p.pool[..., 0, :, :, 0] = -float("inf")  # every key's first number
+        end = lens[0] + toks[0]
+        for pos in (3, lens[0] + 1, lens[0] + 150, end - 1):
+            p.row(0, pos)[1, 0, 5] = float(kind)
+        out, lse = p.run()
+        assert bool((out == 0).all()) and bool((lse == -torch.inf).all())

@@ -888,6 +888,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int col = 0; col < D; col += 32) {
             float v[32];
             fetch(col, v);
+            if (__any_sync(0xFFFFFFFFu, l == 0.f))  // zeros, also over values that are not finite
+#pragma unroll
+              for (int q = 0; q < 32; ++q) v[q] = l == 0.f ? 0.f : v[q];
             uint32_t e[16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
@@ -907,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (odd) {
             __syncwarp();  // the row was stored by other lanes
-            if (valid) add_odd<D, F8>(p, w.b, w.head, odd_from, odd_to, f, p.out + token * p.out_stride + (int64_t)head * D, nullptr, 0);
+            if (valid && l != 0.f) add_odd<D, F8>(p, w.b, w.head, odd_from, odd_to, f, p.out + token * p.out_stride + (int64_t)head * D, nullptr, 0);
           }
           if (valid && p.lse) p.lse[token * p.hq + head] = l == 0.f ? -INFINITY : kLn2 * (m + (log2f(l) - C::template Lift<F8>));
         } else {  // a part, for the joining kernel

@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, kPerSM) join_kernel(const TreeParams
     }
     if (r < rows && mine == 0) {
       const float f = s.l == 0.f ? 0.f : vs / s.l;
+      if (s.l == 0.f) s.o = make_float4(0.f, 0.f, 0.f, 0.f);  // also over values that are not finite
       const int d = tree_draft(p, row0 + r), hh = row0 + r - d * p.group;
       *reinterpret_cast<uint2*>(p.out + (item.x + d) * p.out_stride + (int64_t)(head * p.group + hh) * D + col) =
           make_uint2(pack_bf16x2(s.o.x * f, s.o.y * f), pack_bf16x2(s.o.z * f, s.o.w * f));
