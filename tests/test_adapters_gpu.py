@@ -350,3 +350,24 @@ def test_infinite_numbers_in_x_and_a(max_rank, rank):
     s.a[2, 0, 0], s.a[3, rank - 1, 11] = float("inf"), -float("inf")
     s.x[75 + 30, 11] = 0  # times infinity: NaN
     check_any_numbers(s, s.run())
+
+
+@pytest.mark.parametrize("rank", [8, 32, 64, 128])
+@pytest.mark.parametrize("n", [264, 4104])
+def test_a_token_does_not_depend_on_who_shares_its_adapter(rank, n):
+    """The same token alone, among few and many tokens of its adapter, and beside other adapters: equal bits."""
+    k = 1544
+    s = Step([64], [0], [rank - 3] + [rank] * 60, rank, k, n, seed=rank + n)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    more = [torch.randn((200, m), generator=g, device="cuda").bfloat16() for m in (k, n)]
+    s.run()
+    want = None
+    for toks, which in (([1], [0]), ([2], [0]), ([16], [0]), ([17], [0]), ([33], [0]), ([64], [0]), ([1, 3], [0, 1]), ([16, 130], [0, 1]),
+                        ([64, 100, 1], [0, 1, 2]), ([64, 100], [0, 0]), ([1] + [2] * 60, [0] + list(range(1, 61))), ([1, 40, 64], [0, -1, 0])):
+        total = sum(toks)
+        x, y = torch.cat([s.x, more[0]])[:total], torch.cat([s.y, more[1]])[:total]
+        plan = tb.adapter_plan(tb.AdapterPlan(i32(which), i32(np.concatenate([[0], np.cumsum(toks)])), total))
+        got = tb.adapter_add(x, y, s.adapters, plan, out=torch.empty_like(y))
+        want = got[0] if want is None else want
+        assert torch.equal(got[0], want), (toks, which)
+        assert not torch.equal(got[0], y[0])

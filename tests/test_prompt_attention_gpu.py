@@ -545,3 +545,68 @@ def test_scores_of_minus_infinity_give_zeros_whatever_the_values(d, kind):
             p.row(0, pos)[1, 0, 5] = float(kind)
         out, lse = p.run()
         assert bool((out == 0).all()) and bool((lse == -torch.inf).all())
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_clamped_lengths_and_pages_give_what_the_clamped_ones_give(d, f8):
+    """Prefixes past the table's width or below zero, starts outside n, more tokens than max_tokens, pages outside the pool."""
+    p = Prompts([0, 30 * 16 - 50], [100, 50], 4, 2, d, 16, f8, seed=14)
+    assert p.table.shape[1] == 30
+    p.run()
+
+    def call(table, prefix, starts, most):
+        p.out.fill_(7.5), p.lse.fill_(7.5)
+        batch = tb.DraftBatch(i32(table), i32(prefix), i32(starts), most, None, p.n)
+        return tb.prompt_attention(p.q, p.cache, 0, batch, p.ws, p.scale, out=p.out, lse=p.lse)
+
+    for prefix, starts in (([0, 10 ** 9], [0, 100, 2 ** 30]), ([-5, 30 * 16], [-7, 100, 151]), ([0, 30 * 16 - 49], [0, 100, 150])):
+        p.check(*call(p.table, prefix, starts, 100))
+    out, lse = call(p.table, [0, 30 * 16 - 50], [0, 100, 150], 40)
+    assert bool((out[40:100] == 7.5).all()) and bool((lse[40:100] == 7.5).all()) and bool((out[140:] == 7.5).all())
+    short = Prompts.__new__(Prompts)
+    short.__dict__.update(p.__dict__, toks=[40, 40])
+    short.check(out, lse)
+    # pages outside the pool are its first or its last one
+    last = p.pool.shape[1] - 1
+    p.pool.view(torch.uint8)[:, [0, last]] = p.pool.view(torch.uint8)[:, p.table[1, [2, 3]]]  # finite
+    wild, kept = p.table.copy(), p.table.copy()
+    wild[1, 1], wild[1, 7], wild[0, 2] = 10 ** 9, -5, last + 1
+    kept[1, 1], kept[1, 7], kept[0, 2] = last, 0, last
+    want = [t.clone() for t in call(kept, p.lens, p.q_start, 100)]
+    got = call(wild, p.lens, p.q_start, 100)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    p.table = kept
+    p.check(*got)
+    assert tb.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_that_are_not_finite_touch_no_other_over_an_e4m3_cache(d):
+    p = Prompts([20, 0], [300, 130], 4, 2, d, 16, True, seed=10)
+    out, lse = p.run()
+    want, want_l = out.clone(), lse.clone()
+    p.q[57, 1, 5] = float("nan")
+    p.q[301, 3, 0] = float("inf")
+    p.run()
+    keep = torch.ones((p.n, 4), dtype=torch.bool, device="cuda")
+    keep[57, 1] = keep[301, 3] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_l[keep])
+
+
+@pytest.mark.parametrize("f8,d", [(False, 128), (True, 128), (False, 256), (True, 64)])
+def test_a_sequence_does_not_depend_on_the_others_numbers(f8, d):
+    p = Prompts([500, 0, 9000], [300, 1200, 64], 8, 2, d, 64, f8, seed=16)
+    first, first_l = (t.clone() for t in p.run())
+    bits = p.pool.view(torch.uint8)
+    for b in (0, 2):  # other queries, and other pages with other numbers
+        p.q[p.q_start[b]:p.q_start[b + 1]] *= -3
+        held = p.table[b, :-(-(p.lens[b] + p.toks[b]) // 64)].tolist()
+        bits[:, held] = bits[:, held[::-1]].clone()
+        p.table[b, :len(held)] = held[::-1]
+    p.table[0, [0, 1]] = p.table[0, [1, 0]]
+    out, lse = p.run()
+    mine = slice(300, 1500)
+    assert torch.equal(out[mine], first[mine]) and torch.equal(lse[mine], first_l[mine])
+    assert not torch.equal(out[:300], first[:300]) and not torch.equal(out[1500:], first[1500:])
+    p.check(out, lse)
