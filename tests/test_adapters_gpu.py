@@ -371,3 +371,12 @@ def test_a_token_does_not_depend_on_who_shares_its_adapter(rank, n):
         want = got[0] if want is None else want
         assert torch.equal(got[0], want), (toks, which)
         assert not torch.equal(got[0], y[0])
+
+
+@pytest.mark.parametrize("count", [50, 90, 250, 300])
+@pytest.mark.parametrize("ranks", ["equal", "mixed"])
+def test_rounds_of_adapters_of_equal_and_of_mixed_ranks(count, ranks):
+    """More tiles than clusters, each of a token or two, with the same rank or with several."""
+    rank = [64] * count if ranks == "equal" else [(i * 11) % 64 + 1 for i in range(count)]
+    s = Step([1 + b % 2 for b in range(count)], list(range(count)), rank, 64, 264, 4104, seed=count)
+    s.check(s.run())

@@ -494,9 +494,9 @@ __device__ __forceinline__ int rank_of(const AddParams& p, int adapter) {
   return rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
 }
 
-// The tiles by falling rank, where there are more of them than clusters.
+// The tiles by falling rank, where there are more of them than clusters.  Whether those of the first round differ in rank.
 constexpr int kSorted = kThreads;
-__device__ __noinline__ void sort_tiles(const AddParams& p, int tiles, int* ranks, uint16_t* order) {
+__device__ __noinline__ bool sort_tiles(const AddParams& p, int tiles, int clusters, int* ranks, uint16_t* order) {
   const int t = threadIdx.x;
   ranks[t] = t < tiles ? rank_of(p, __ldcg(adapter_tiles(p.plan) + t).x) : -1;
   __syncthreads();
@@ -505,6 +505,9 @@ __device__ __noinline__ void sort_tiles(const AddParams& p, int tiles, int* rank
   for (int i = 0; i < tiles; ++i) place += ranks[i] > mine || (ranks[i] == mine && i < t);
   if (t < tiles) order[place] = (uint16_t)t;
   __syncthreads();
+  const bool differ = ranks[order[0]] != ranks[order[clusters - 1]];
+  __syncthreads();  // the ranks' place is used again
+  return differ;
 }
 
 template <int RMAX>
@@ -522,11 +525,13 @@ __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const
   constexpr bool kSort = RMAX > 32;  // below that tiles cost about the same
   __shared__ uint16_t order_of[kSort ? kSorted : 1];
   const bool sorted = kSort && p.ad.ranks && tiles > clusters && tiles <= kSorted;
-  if (kSort && sorted) sort_tiles(p, tiles, reinterpret_cast<int*>(raw), order_of);
-  bool back = false;  // every other round of the sorted ones
-  for (int t0 = 0; t0 < tiles; t0 += clusters, back = sorted && !back) {
+  const bool turns = kSort && sorted && sort_tiles(p, tiles, clusters, reinterpret_cast<int*>(raw), order_of);
+  bool back = false;  // every other round where ranks differ
+  for (int t0 = 0; t0 < tiles; t0 += clusters, back = turns && !back) {
     // The round's tiles; where they are few, as many clusters for each as have a block of outputs per warp.  Back: the clusters whose
-    // last tile was least take the first ones, and few tiles are shared by two thirds of the clusters (by all: 31 us for 27).
+    // last tile was least take the first ones, and few tiles are shared by two thirds of the clusters, those that are free first (by
+    // all: 31 us for 27, 64 tokens of 40 adapters to rank 64).  With equal ranks all are free at once (50 adapters of rank 64: 40 us,
+    // 45 shared by two thirds).
     const int now = min(tiles - t0, clusters);
     const int shares = max(1, min((kSort && back ? clusters * 2 / 3 : clusters) / now, blocks / (kCluster * kWarps)));
     const int me = kSort && back ? clusters - 1 - cluster : cluster;
