@@ -3,7 +3,8 @@
 // Sequences are ranked by (adapter, index): rank = number of sequences that come before, counted directly (at most 1024 of them).
 // Sums over the ranked sequences then give each its place in the order, and each group of equal adapters its tiles; the tokens'
 // places and the tiles are found by binary search.  Every block counts for itself and writes its share of the tokens and tiles.
-// Bound: latency of a few dependent rounds; once a step.
+// Bound: latency of a few dependent rounds; once a step.  1 token 4.4 us, 64 sequences 5.8, 9 of 4493 tokens 7.3, 1024 sequences 35 (each
+// thread's count of the 1024, and the scans); with one adapter_add behind it 9.5, 32, 92.
 #include "adapter_plan.cuh"
 #include "launch.h"
 #include "pdl.cuh"

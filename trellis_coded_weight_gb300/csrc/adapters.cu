@@ -1,19 +1,20 @@
 // adapters.cu -- adds low-rank adapters to a projection's output (plan: adapter_plan.cuh).
 //
 //   h = A x  (fp32),  out = bf16(y + scale B h)
-// A cluster of thread blocks takes a tile: up to 64 tokens of one adapter.  Each of its blocks multiplies its part of the inputs
-// with A; the parts of h are added up through distributed shared memory, in the order of the blocks, and each block then makes its
-// part of the outputs.  x, y and out are touched once, A and B once per tile.  Both products are warp-level bf16 MMAs on operands
-// that go from global memory straight into the fragments: a lane loads 16 (or 8) contiguous bytes of a row, and the reduction
-// index is permuted alike on both sides so that these are what its fragments hold; likewise the outputs of four tiles of 8, so that
-// a lane has 8 contiguous ones.  h enters the second product as the sum of two bf16 numbers.
-// Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and
-// makes a share of the outputs.
+// A cluster of thread blocks takes a tile: up to 64 tokens of one adapter.  Each of its blocks multiplies its part of the inputs with A;
+// the parts of h are added up through distributed shared memory, in the order of the blocks, and each block then makes its part of the
+// outputs.  x, y and out are touched once, A and B once per tile (where clusters share a tile, x and A by each).  Both products are
+// warp-level bf16 MMAs on operands that go from global memory straight into the fragments: a lane loads 16 (or 8) contiguous bytes of a
+// row, and the reduction index is permuted alike on both sides so that these are what its fragments hold; likewise the outputs of four
+// tiles of 8, so that a lane has 8 contiguous ones.  h enters the second product as the sum of two bf16 numbers.
+// Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and makes a
+// share of the outputs.
 // Bound: 4096 tokens of rank 16, 5120 to 17408: bytes of x, y and out (60 us, 5.4 TB/s).  Higher ranks: the first product of a tile, at
-// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 84 us, 128 142).  64 tokens of 40 adapters to rank 64: 26 us
-// (1.9 TB/s): a tile of rank 64 takes its cluster 19 whatever the others take, 9 of them before the second product, whose blocks of
-// outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token:
-// 5.1 us of latency (launch, plan, tokens, x and A, two cluster barriers, B).
+// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 86 us, 128 142; A comes again with each tile).  Ranks 17 to 32:
+// 4096 tokens, 5120 to 17408, 78 us (4.2 TB/s), in a kernel that spills 36 numbers a thread for two blocks an SM.  64 tokens of 40
+// adapters to rank 64: 26 us (1.9 TB/s): a tile of rank 64 takes its cluster 19 whatever the others take, 9 of them before the second
+// product, whose blocks of outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token: 5.1 us
+// of latency (launch, plan, tokens, x and A, two cluster barriers, B).
 // Clusters of 8: 115 us where 4 take 70, since each block reads as many parts of h as there are; of 2: 81.
 #include "adapter_plan.cuh"
 #include "common.cuh"
@@ -31,8 +32,9 @@ constexpr int kCluster = 4;
 constexpr int kCopyLd = 36;                // floats from token to token of a warp's products of 32 ranks: bank conflicts of two
 constexpr int kCopy = 64 * kCopyLd;        // floats of a warp's products: 64 tokens by 32 ranks, or 32 by 64
 constexpr int kCopyBytes = kWarps / 2 * kCopy * 4;
-// A kernel for each bound on the rank: with ranks up to 32 two blocks of 128 registers a thread share an SM, with more one of 255 has
-// it (two: 4096 tokens of rank 64, 17408 inputs: 108 us for 97, spilling), which also leaves room for more copies in flight.
+// A kernel for each bound on the rank: with ranks up to 32 two blocks of 128 registers a thread share an SM, with more one has it (204
+// and 210 registers are used; two blocks: 4096 tokens of rank 64, 17408 inputs: 108 us for 97, spilling), which also leaves room for
+// more copies in flight.
 template <int RMAX>
 struct Size {
   static constexpr int Blocks = RMAX <= 32 ? 2 : 1;    // of an SM

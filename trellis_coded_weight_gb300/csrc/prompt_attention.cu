@@ -16,12 +16,16 @@
 // where not every row sees them) are cleared on the way, the latter added back for the rows that see them (rare).
 // The warps: one that plans and copies, one that issues, two that bring the queries; two softmax warpgroups (a thread per row); a
 // warpgroup that widens and clears (two with e4m3 and heads of 256, whose second softmax warpgroup has nothing else to do).
+// Weights are rounded to 16 bits for the product with the values, in their type: an MMA's operands are both bf16 or both fp16.  (Error
+// against 64 bits: 0.0021 of the outputs' size with a bf16 cache, 0.0016 from their own rounding alone.)  Their sum is not rounded.
 // Bound: the products, and what lies between them.  A tile of a stream is 1024 cycles of products with heads of 128 (512 with 64,
 // 2048 with 256) and takes 1480: S at N = 128 needs all of shared memory's bandwidth, which the copies also want, and a commit before
-// a wait costs the issuing warp 70 cycles.  16384 tokens, 32/8 heads of 128: 1.43 ms (1.54 PFLOP/s); 8192 tokens, 16/2 of 256: 379 us
-// (1.45); with e4m3 537 (1.02), where a tile's widening shares shared memory and issue slots with the rest.  Heads of 64: weights are
-// the longer part (two warps of an SM's quarter share 1024 cycles of exponentials per tile): 8192 tokens, 64/8 659 us (0.83).
-// Short items pay 5000 cycles each for their end and the first weights of the next: 16 sequences to 2000 tokens 334 us (1.14).
+// a wait costs the issuing warp 70 cycles.  16384 tokens, 32/8 heads of 128: 1.43 ms (1.54 PFLOP/s); 8192 tokens, 16/2 of 256: 385 us
+// (1.43).  With e4m3 545 (1.01; 4 x 4096 tokens, 32/8 of 128: 525): each block widens the values for its own rows, and tensor pipe, shared
+// memory and issue slots are each busy for 40 to 50 % of the time.  Heads of 64: tensor pipe and exponentials are busy for 35 % each; a
+// pair of tiles takes 2920 cycles, 1024 in each of them, since a stream has one S and its scores, maximum, weights and product follow one
+// another: 8192 tokens, 64/8 661 us (0.83).  Short items pay 5000 cycles each for their end and the first weights of the next: 16 sequences to 2000
+// tokens 330 us (1.15).
 #include <cstring>
 #include <cuda.h>
 
