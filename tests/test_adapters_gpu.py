@@ -380,3 +380,42 @@ def test_rounds_of_adapters_of_equal_and_of_mixed_ranks(count, ranks):
     rank = [64] * count if ranks == "equal" else [(i * 11) % 64 + 1 for i in range(count)]
     s = Step([1 + b % 2 for b in range(count)], list(range(count)), rank, 64, 264, 4104, seed=count)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("toks,rank", [([1], 16), ([1] * 40, 64), ([300, 2, 70], 16), ([300, 2, 70], 32), ([500], 128)])
+def test_adapters_written_directly_before_a_call(toks, rank):
+    """Requests bring their adapters: what a call reads of them may have been written by the launch ahead, captured or not."""
+    count = 3
+    steps = [Step(toks, [b % count for b in range(len(toks))], [rank, max(1, rank - 5 * i), rank], rank, 1544, 1288, seed=60 + i, nan=False) for i in range(4)]
+    want = []
+    for t in steps:
+        t.x, t.y = steps[0].x, steps[0].y
+        want.append(t.run().clone())
+        torch.cuda.synchronize()
+    a, b, ranks, scales = (v.clone() for v in (steps[0].a, steps[0].b, i32(steps[0].ranks), steps[0].scales))
+    kept = [i32(t.ranks) for t in steps]
+    adapters = tb.Adapters(a, b, ranks, scales)
+    outs = [torch.empty_like(w) for w in want]
+
+    def calls():
+        for t, r, out in zip(steps, kept, outs):
+            for to, of in ((ranks, r), (scales, t.scales), (a, t.a), (b, t.b)):
+                to.mul_(0).add_(of)
+            tb.adapter_add(steps[0].x, steps[0].y, adapters, steps[0].plan, out=out)
+
+    for _ in range(10):
+        calls()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        calls()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(10):
+        for o in outs:
+            o.fill_(1)
+        graph.replay()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))

@@ -10,10 +10,10 @@
 // Where tiles are fewer than clusters (single tokens), and in the last round, several clusters share a tile: each computes h and makes a
 // share of the outputs.
 // Bound: 4096 tokens of rank 16, 5120 to 17408: bytes of x, y and out (60 us, 5.4 TB/s).  Higher ranks: the first product of a tile, at
-// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 86 us, 128 142; A comes again with each tile).  Ranks 17 to 32:
-// 4096 tokens, 5120 to 17408, 78 us (4.2 TB/s), in a kernel that spills 36 numbers a thread for two blocks an SM.  64 tokens of 40
+// a few blocks of inputs in flight (4096 tokens, 17408 to 5120, rank 64 84 us, 128 137; A comes again with each tile).  Ranks 17 to 32:
+// 4096 tokens, 5120 to 17408, 77 us (4.3 TB/s), in a kernel that spills 35 numbers a thread for two blocks an SM.  64 tokens of 40
 // adapters to rank 64: 26 us (1.9 TB/s): a tile of rank 64 takes its cluster 19 whatever the others take, 9 of them before the second
-// product, whose blocks of outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token: 5.1 us
+// product, whose blocks of outputs then follow one another in each warp; and there are no more clusters than SMs / 4.  1 token: 5.2 us
 // of latency (launch, plan, tokens, x and A, two cluster barriers, B).
 // Clusters of 8: 115 us where 4 take 70, since each block reads as many parts of h as there are; of 2: 81.
 #include "adapter_plan.cuh"
@@ -121,7 +121,7 @@ __device__ __forceinline__ void shrink(const AddParams& p, const uint16_t* a, in
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       v[j] = make_uint4(0, 0, 0, 0);
-      if (in && r0 + 8 * j + g < rank) v[j] = __ldg(reinterpret_cast<const uint4*>(w + (int64_t)(8 * j) * p.ad.in + 32 * k));
+      if (in && r0 + 8 * j + g < rank) v[j] = *reinterpret_cast<const uint4*>(w + (int64_t)(8 * j) * p.ad.in + 32 * k);
     }
   };
   float acc[WT][NT][4];
@@ -364,11 +364,11 @@ struct Expand {
         const uint16_t* at = block < o1 ? weights(block, j, kb) : nullptr;
         if (!at) continue;
         if (NARROW) {
-          const uint2 two = __ldg(reinterpret_cast<const uint2*>(at));
+          const uint2 two = *reinterpret_cast<const uint2*>(at);
           v[j][kb].x = two.x;
           v[j][kb].y = two.y;
         } else {
-          v[j][kb] = __ldg(reinterpret_cast<const uint4*>(at));
+          v[j][kb] = *reinterpret_cast<const uint4*>(at);
         }
       }
   }
@@ -492,7 +492,7 @@ __device__ __forceinline__ void tile_by_rank(const AddParams& p, const int4& til
 
 __device__ __forceinline__ int rank_of(const AddParams& p, int adapter) {
   const bool has = adapter >= 0 && adapter < p.ad.count;
-  const int rank = has ? p.ad.ranks ? __ldg(p.ad.ranks + adapter) : p.ad.max_rank : 0;
+  const int rank = has ? p.ad.ranks ? p.ad.ranks[adapter] : p.ad.max_rank : 0;
   return rank < 0 ? 0 : rank > p.ad.max_rank ? p.ad.max_rank : rank;
 }
 
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, Size<RMAX>::Blocks) add_kernel(const
       }
       continue;
     }
-    const float scale = p.ad.scales ? __ldg(p.ad.scales + tile.x) : 1.f;
+    const float scale = p.ad.scales ? p.ad.scales[tile.x] : 1.f;
     // in this order: ragged prompts 82 us, and 92 with the code of few tokens in front
     if (tile.z > 16) tile_by_rank<RMAX, 4>(p, tile, rank, scale, tokens, o0, o1, copies, ring);
     else tile_by_rank<RMAX, 1>(p, tile, rank, scale, tokens, o0, o1, copies, ring);

@@ -3,7 +3,7 @@
 // abi_serving.cu before these are called.
 //
 // Their kernels are launched as dependents (pdl.cuh): they may have begun before the call ahead has written what they read, so such
-// data (lengths, tables, masks, queries, logits, positions) is not read-only while they run.  It is loaded by plain loads or from
+// data (lengths, tables, masks, queries, logits, positions, adapters) is not read-only while they run.  It is loaded by plain loads or from
 // L2, never by the read-only path; that is for the model's constants (norm weights, rotation tables, scales).
 #pragma once
 #include <cstddef>
